@@ -17,6 +17,7 @@
  *                     and, with a sliding window W, t > len_b - N + i - W
  *     K[t]  = k_pool[block_tables[b][t / BS]][kv][t % BS][:]
  *     affine pages: K[t][d] = scale[t][d/64] * code[t][d] + bias[t][d/64]
+ *     e4m3 pages:   K[t][d] = scale[block of t][kv] * code[t][d]
  *     out[b][h][i] = softmax_t(scale * <q, K[t]>) . V[t]       rounded to bf16
  *
  * The work is split along the sequence into partitions; each partition keeps an
@@ -37,6 +38,13 @@
  *                 (affine pages only; NULL for bf16 pages). Dim d uses group d/64.
  *                 These are the layouts of the pages' BlockPool
  *                 (state/paged/cache.ts): every plane [numBlocks, H, blockSize, width].
+ *   e4m3 pages    (bits = 8, group_size = PKV_GROUP_BLOCK) k_pool, v_pool: one byte per
+ *                 value, an e4m3 code (4 exponent and 3 fraction bits, bias 7, largest
+ *                 448, no infinities) [num_blocks, num_kv_heads, block_size, W];
+ *                 k_scales, v_scales: f32 [num_blocks, num_kv_heads], >= 0 and finite, one
+ *                 for the block's rows of a KV head; k_biases, v_biases unused (NULL).
+ *                 A row at or past seq_len may hold any byte. No page of the reference
+ *                 has this format; it is the 8-bit float cache of other servers.
  *   block_tables  int32 [num_seqs, max_blocks_per_seq]: logical page -> physical block.
  *   seq_lens      int32 [num_seqs]: cached rows per sequence, including the n_query
  *                 new ones.
@@ -94,24 +102,29 @@ extern "C" {
                                     default, see pkv_set_wait_limit_ns); the outputs of that call
                                     are then unspecified */
 
+/* pkv_pool_layout.group_size of e4m3 pages (with bits = 8): one f32 scale per block and KV head. */
+#define PKV_GROUP_BLOCK (-1)
+
 /* Pool layout descriptor (the pages' PagedAttentionStorage: blockSize, headDim,
  * vHeadDim, quantization {bits, groupSize}).
  * Head dims with a kernel (key/value; the host rejects the rest), each with up to 64
  * query rows per KV head ((num_q_heads / num_kv_heads) * n_query, the pages' limit for
  * the few-query kernel, kernels/attention/multi-query.ts):
  *   equal dims: 64, 128, 256 (bf16) and 128, 256 (affine);
- *   bf16 192/128, 256/128 and 128/256; affine 256/128 and 128/256. */
+ *   bf16 192/128, 256/128 and 128/256; affine 256/128 and 128/256;
+ *   e4m3 pages: every pair of the bf16 ones. */
 typedef struct pkv_pool_layout {
   int32_t num_blocks;   /* blocks in the pool, > 0 */
   int32_t num_kv_heads; /* HK, > 0 */
   int32_t block_size;   /* BS: rows per block; a multiple of the chunk the kernels stage (16 rows
-                           bf16, 32 affine), or 8 (bf16) / 8 or 16 (affine) rows, a chunk then
+                           bf16, 32 affine and e4m3), or 8 (bf16) / 8 or 16 (others) rows, a chunk then
                            spanning several blocks: such pools run partitions (not the balanced
                            schedule), and neither the CUDA-core contraction nor the fused
                            append-and-attend call takes them (PKV_ERR_UNSUPPORTED_SHAPE) */
   int32_t head_dim;     /* D: key (and query) head dim */
-  int32_t bits;         /* 16 = bf16 pages; 4 or 8 = affine codes */
-  int32_t group_size;   /* affine group; must be 64 (ignored for bf16) */
+  int32_t bits;         /* 16 = bf16 pages; 4 or 8 = affine codes; 8 = e4m3 codes with group_size -1 */
+  int32_t group_size;   /* affine group: 64; PKV_GROUP_BLOCK (-1) with bits = 8: e4m3 pages
+                           (ignored for bf16) */
   int32_t v_head_dim;   /* Dv: value (and output) head dim; 0 = head_dim */
 } pkv_pool_layout;
 
@@ -343,6 +356,16 @@ int pkv_paged_decode_attention_no_alloc(const pkv_pool_layout* layout, const pkv
  * codes packed lowest bits first. Bad block ids skip their row and set
  * PKV_DEVERR_BAD_BLOCK; seq_lens[b] + n_new above max_blocks_per_seq*block_size
  * sets PKV_DEVERR_BAD_SEQ_LEN and writes nothing for that sequence.
+ * e4m3 pages: per touched block, KV head and plane, with a the largest magnitude of the
+ * block's new rows and s its scale (0 when the block holds no earlier row, whatever the
+ * scale plane says there),
+ *     s' = max(s, 2^e), e the smallest integer >= -126 with a <= 448 * 2^e (0 if a = 0),
+ *     new rows:     code = e4m3(x / s')             nearest even (0 when s' = 0)
+ *     earlier rows: code = e4m3(code * (s / s'))    when s' > s
+ * and s' is stored. Between powers of two the second line is exact but for values that
+ * fall below the type's normal range, so growing a scale costs the earlier rows nothing
+ * more. A block that receives rows must belong to one sequence only. Values must be
+ * finite.
  * Layouts: every (bits, head dims) pair the decode has a kernel for.
  * Asynchronous on `stream`. */
 int pkv_paged_append(const pkv_pool_layout* layout, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t n_new,
@@ -368,7 +391,9 @@ int pkv_paged_append(const pkv_pool_layout* layout, int32_t num_seqs, int32_t ma
  * partition, so no second launch and no re-read of the rows from another CTA is
  * needed. Blocks shared by several sequences must not receive new rows (the
  * caller copies them first). A row whose block id is bad is neither written nor
- * read and sets PKV_DEVERR_BAD_BLOCK. */
+ * read and sets PKV_DEVERR_BAD_BLOCK.
+ * e4m3 pages are refused (PKV_ERR_UNSUPPORTED_SHAPE): a new row may rescale its whole
+ * block, which other CTAs read. Call pkv_paged_append, then the decode. */
 int pkv_paged_decode_append_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
                                       const void* q, const void* k_new, const void* v_new, void* k_pool,
                                       void* v_pool, void* k_scales, void* k_biases, void* v_scales,

@@ -4,6 +4,7 @@ with a thin ctypes binding."""
 
 from .binding import (  # noqa: F401
     EXPORTS,
+    PKV_GROUP_BLOCK,
     LibraryNotBuilt,
     PkvError,
     DecodeParams,

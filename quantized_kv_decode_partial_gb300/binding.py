@@ -47,6 +47,8 @@ PKV_ERR_CUDA = -7
 PKV_ERR_SCRATCH_TOO_SMALL = -8
 PKV_STATIC_SCRATCH_BYTES = 16 << 20
 
+PKV_GROUP_BLOCK = -1  # PoolLayout.group_size of e4m3 pages (bits=8): one f32 scale per block and KV head
+
 PKV_CONTRACTION_AUTO = 0
 PKV_CONTRACTION_TENSOR = 1
 PKV_CONTRACTION_CUDA_CORE = 2
@@ -162,9 +164,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def v_head_dim_of(v_pool: torch.Tensor, bits: int) -> int:
-    """Value head dim of a V pool: its row width, in values (bf16) or codes (affine words)."""
-    w = v_pool.shape[-1]
-    return w if bits == 16 else w * 32 // bits
+    """Value head dim of a V pool: its row's bits (bf16 values, affine words, e4m3 codes) over the stored bits."""
+    return v_pool.shape[-1] * v_pool.element_size() * 8 // bits
 
 
 def layout_for(k_pool: torch.Tensor, head_dim: int, bits: int, group_size: int = 64,
@@ -229,7 +230,9 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     """Decode attention over a paged cache (see include/pkv_decode.h).
 
     q bf16 [B, HQ, N, D]; pools bf16 [NB, HK, BS, D] (bits=16) or int32 code
-    words [NB, HK, BS, D*bits/32] with bf16 scale/bias planes [NB, HK, BS, D/64];
+    words [NB, HK, BS, D*bits/32] with bf16 scale/bias planes [NB, HK, BS, D/64],
+    or float8_e4m3fn (or uint8) codes [NB, HK, BS, D] with f32 scale planes [NB, HK]
+    (bits=8, group_size=PKV_GROUP_BLOCK, no biases);
     block_tables int32 [B, max_blocks]; seq_lens int32 [B]. Runs on the current
     CUDA stream of q's device and returns bf16 [B, HQ, N, D].
     """
@@ -435,7 +438,7 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
                  k_scales=None, k_biases=None, v_scales=None, v_biases=None,
                  error_flag: Optional[torch.Tensor] = None) -> None:
     """Writes k_new/v_new bf16 [B, HK, n_new, D] at positions seq_lens[b].. of each
-    sequence (quantising affine pages); see include/pkv_decode.h."""
+    sequence (quantising affine and e4m3 pages); see include/pkv_decode.h."""
     lib = load_library()
     B, HK, n_new, D = k_new.shape
     layout = layout_for(k_pool, D, bits, group_size, v_pool)

@@ -25,6 +25,7 @@ SOURCES = [
     "pkv_api.cu",
     "pkv_merge_gather.cu",
     "pkv_append.cu",
+    "pkv_append_blocks.cu",
     "pkv_partial_bf16.cu",
     "pkv_partial_bf16_cc.cu",
     "pkv_partial_u4.cu",
@@ -35,6 +36,9 @@ SOURCES = [
     "pkv_partial_bf16_pc.cu",
     "pkv_partial_u4_pc.cu",
     "pkv_partial_u8_pc.cu",
+    "pkv_partial_e4m3.cu",
+    "pkv_partial_e4m3_bal.cu",
+    "pkv_partial_e4m3_pc.cu",
 ]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -28,20 +28,28 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
+// Pages of e4m3 codes with one f32 scale per block and KV head.
+bool block_scaled(const pkv_pool_layout* L) { return L->bits == 8 && L->group_size == PKV_GROUP_BLOCK; }
+
+// Page format of a layout, as the kernels' BITS argument: 16, 4, 8 or kFmtE4m3.
+int format_of(const pkv_pool_layout* L) { return block_scaled(L) ? pkv::kFmtE4m3 : L->bits; }
+
 // cc: the CUDA-core contraction (bf16 pages only), else the tensor-core one; bal: the
 // balanced-schedule instantiation (tensor cores, several CTAs per SM).
-PartialInfo partial_info(int bits, int dk, int dv, int nq, bool solo = false, bool cc = false, bool bal = false) {
-  if (cc) return bits == 16 ? pkv::partial_info_bf16_cc(dk, dv, nq, solo) : PartialInfo{};
+PartialInfo partial_info(int fmt, int dk, int dv, int nq, bool solo = false, bool cc = false, bool bal = false) {
+  if (cc) return fmt == 16 ? pkv::partial_info_bf16_cc(dk, dv, nq, solo) : PartialInfo{};
   if (bal) {
     if (solo) return PartialInfo{};
-    if (bits == 16) return pkv::partial_info_bf16_bal(dk, dv, nq);
-    if (bits == 4) return pkv::partial_info_u4_bal(dk, dv, nq);
-    if (bits == 8) return pkv::partial_info_u8_bal(dk, dv, nq);
+    if (fmt == 16) return pkv::partial_info_bf16_bal(dk, dv, nq);
+    if (fmt == 4) return pkv::partial_info_u4_bal(dk, dv, nq);
+    if (fmt == 8) return pkv::partial_info_u8_bal(dk, dv, nq);
+    if (fmt == pkv::kFmtE4m3) return pkv::partial_info_e4m3_bal(dk, dv, nq);
     return PartialInfo{};
   }
-  if (bits == 16) return pkv::partial_info_bf16(dk, dv, nq, solo);
-  if (bits == 4) return pkv::partial_info_u4(dk, dv, nq, solo);
-  if (bits == 8) return pkv::partial_info_u8(dk, dv, nq, solo);
+  if (fmt == 16) return pkv::partial_info_bf16(dk, dv, nq, solo);
+  if (fmt == 4) return pkv::partial_info_u4(dk, dv, nq, solo);
+  if (fmt == 8) return pkv::partial_info_u8(dk, dv, nq, solo);
+  if (fmt == pkv::kFmtE4m3) return pkv::partial_info_e4m3(dk, dv, nq, solo);
   return PartialInfo{};
 }
 
@@ -72,8 +80,10 @@ BalancedWorkspace balanced_workspace(long long runs, long long units, long long 
   return w;
 }
 
-// Stored bytes of one row of head dim `d`: bf16 values, or codes plus bf16 scale and bias.
+// Stored bytes of one row of head dim `d`: bf16 values, or codes plus bf16 scale and bias
+// (a block's one scale is not counted).
 long long stored_row_bytes(const pkv_pool_layout* L, int d) {
+  if (block_scaled(L)) return d;
   return L->bits == 16 ? 2ll * d : static_cast<long long>(d) * L->bits / 8 + d / 64 * 4;
 }
 
@@ -83,7 +93,7 @@ int check_layout(const pkv_pool_layout* L) {
   if (!L) return PKV_ERR_NULL_POINTER;
   if (L->num_blocks <= 0 || L->num_kv_heads <= 0 || L->block_size <= 0) return PKV_ERR_BAD_LAYOUT;
   if (L->bits != 16 && L->bits != 4 && L->bits != 8) return PKV_ERR_BAD_LAYOUT;
-  if (L->bits == 16) {
+  if (L->bits == 16 || block_scaled(L)) {
     if (L->head_dim != 64 && L->head_dim != 128 && L->head_dim != 192 && L->head_dim != 256) return PKV_ERR_BAD_LAYOUT;
     if (v_dim(L) != 64 && v_dim(L) != 128 && v_dim(L) != 256) return PKV_ERR_BAD_LAYOUT;
   } else {
@@ -115,9 +125,24 @@ int check_params(const pkv_pool_layout* L, const pkv_decode_params* P) {
   const long long nq = static_cast<long long>(P->num_q_heads / L->num_kv_heads) * P->n_query;
   if (nq > 64) return PKV_ERR_UNSUPPORTED_SHAPE;
   const bool cc = P->contraction == PKV_CONTRACTION_CUDA_CORE;
-  if (!partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq), false, cc).exists)
+  if (!partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), false, cc).exists)
     return PKV_ERR_UNSUPPORTED_SHAPE;
   return PKV_OK;
+}
+
+// The scale and bias planes a layout needs: four bf16 planes (affine, aligned to
+// `affine_align`), two f32 planes (e4m3), none (bf16).
+bool scale_planes_given(const pkv_pool_layout* L, const void* k_scales, const void* k_biases, const void* v_scales,
+                        const void* v_biases) {
+  if (L->bits == 16) return true;
+  return k_scales && v_scales && (block_scaled(L) || (k_biases && v_biases));
+}
+bool scale_planes_aligned(const pkv_pool_layout* L, const void* k_scales, const void* k_biases, const void* v_scales,
+                          const void* v_biases, uintptr_t affine_align) {
+  if (L->bits == 16) return true;
+  if (block_scaled(L)) return aligned(k_scales, 4) && aligned(v_scales, 4);
+  return aligned(k_scales, affine_align) && aligned(k_biases, affine_align) && aligned(v_scales, affine_align) &&
+         aligned(v_biases, affine_align);
 }
 
 // Whether a call runs the CUDA-core contraction: when the caller asks for it, or, left to
@@ -184,7 +209,7 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
     // first, below): the partitions then merge inside their clusters, with no
     // workspace and no second launch.
     const long long nq_rows = static_cast<long long>(P->num_q_heads / L->num_kv_heads) * P->n_query;
-    const PartialInfo two = partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq_rows), false,
+    const PartialInfo two = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq_rows), false,
                                          P->contraction == PKV_CONTRACTION_CUDA_CORE);
     const long long default_ctas = units * ((span + part - 1) / part);
     if (P->window > 0 && default_ctas <= 2 * slots && two.exists && two.smem_bytes <= 114 * 1024) {
@@ -197,7 +222,7 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
       // 6% less on 8 sequences. With CTAs of under 1 MB (2 sequences: 928 rows) the
       // per-CTA start and merge showed, and 496 short CTAs through the workspace were
       // 14% faster.
-      const PartialInfo one = partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq_rows), true,
+      const PartialInfo one = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq_rows), true,
                                            P->contraction == PKV_CONTRACTION_CUDA_CORE);
       const long long sms = sm_count > 0 ? sm_count : 1;
       bool placed = false;
@@ -233,13 +258,13 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
   // instantiations for such pools (no CTA-alone variant, no balanced schedule, no
   // CUDA-core contraction).
   const bool pieces =
-      L->block_size < partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq), false, false).chunk_rows;
+      L->block_size < partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), false, false).chunk_rows;
   if (pieces && P->contraction == PKV_CONTRACTION_CUDA_CORE) return PKV_ERR_UNSUPPORTED_SHAPE;
   const bool cc = use_cuda_cores(L, P, ctas, sm_count);
   const bool use_solo = !pieces && ctas <= sms &&
-                        partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq), true, cc).exists;
+                        partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), true, cc).exists;
   if (solo) *solo = use_solo;
-  const PartialInfo info = partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq), use_solo, cc);
+  const PartialInfo info = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), use_solo, cc);
   out->contraction = cc ? PKV_CONTRACTION_CUDA_CORE : PKV_CONTRACTION_TENSOR;
   out->partition_tokens = static_cast<int32_t>(part);
   out->max_partitions = max_parts;
@@ -276,7 +301,7 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
   if (P->partition_tokens == 0 && P->schedule != PKV_SCHEDULE_PARTITIONS && !cc && !pieces &&
       P->num_seqs <= pkv::kMaxBalancedSeqs &&
       (P->schedule == PKV_SCHEDULE_BALANCED || (L->bits == 4 && max_parts > 1 && !out->merge_in_cluster))) {
-    const PartialInfo bi = partial_info(L->bits, L->head_dim, v_dim(L), static_cast<int>(nq), false, false, true);
+    const PartialInfo bi = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), false, false, true);
     const long long unit_chunks = (window_rows(P, max_len) + bi.chunk_rows - 1) / std::max(bi.chunk_rows, 1);
     const long long units = static_cast<long long>(P->num_seqs) * L->num_kv_heads;
     if (bi.exists && units * unit_chunks < (1ll << 31)) {
@@ -468,7 +493,7 @@ struct PreparedDecode {
   pkv::MergeParams m;
   CUtensorMap tk, tv;
   dim3 grid;
-  int bits, dk, dv, nq, device;
+  int fmt, dk, dv, nq, device;
   bool solo, cc, bal, pc, partial, merge;
 };
 
@@ -483,16 +508,15 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   if (rc) return rc;
   rc = check_params(layout, params);
   if (rc) return rc;
-  const bool quant = layout->bits != 16;
   const bool partial = passes & kPassPartial;
   if (!seq_lens || !out) return PKV_ERR_NULL_POINTER;
   if (partial && (!q || !k_pool || !v_pool || !block_tables)) return PKV_ERR_NULL_POINTER;
-  if (partial && quant && (!k_scales || !k_biases || !v_scales || !v_biases)) return PKV_ERR_NULL_POINTER;
+  if (partial && !scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(error_flag, 4) || !aligned(workspace, 16))
     return PKV_ERR_MISALIGNED;
-  if (quant && (!aligned(k_scales, 16) || !aligned(k_biases, 16) || !aligned(v_scales, 16) || !aligned(v_biases, 16)))
-    return PKV_ERR_MISALIGNED;
+  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 16)) return PKV_ERR_MISALIGNED;
+  if (k_new && block_scaled(layout)) return PKV_ERR_UNSUPPORTED_SHAPE;  // a new row may rescale its whole block
   if ((k_new == nullptr) != (v_new == nullptr)) return PKV_ERR_NULL_POINTER;
   if (!aligned(k_new, 16) || !aligned(v_new, 16)) return PKV_ERR_MISALIGNED;
 
@@ -515,7 +539,7 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   const int D = layout->head_dim, DV = v_dim(layout), HK = layout->num_kv_heads;
   const int nq = (params->num_q_heads / HK) * params->n_query;
   const bool cc = plan.contraction == PKV_CONTRACTION_CUDA_CORE;
-  const PartialInfo info = partial_info(layout->bits, D, DV, nq, solo, cc, bal);
+  const PartialInfo info = partial_info(format_of(layout), D, DV, nq, solo, cc, bal);
   // Blocks smaller than the instantiation's chunk: a chunk spans 2^piece_log2 blocks. The
   // fused call writes a chunk's new rows into one block, so it needs whole chunks.
   int piece_log2 = 0;
@@ -526,16 +550,19 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   // allows (within the bound the plan sized the workspace for).
   int bal_ctas = 0;
   if (bal) {
-    const int occ = layout->bits == 16  ? pkv::partial_bal_ctas_per_sm_bf16(D, DV, nq, dev)
-                    : layout->bits == 4 ? pkv::partial_bal_ctas_per_sm_u4(D, DV, nq, dev)
-                                        : pkv::partial_bal_ctas_per_sm_u8(D, DV, nq, dev);
+    const int fmt = format_of(layout);
+    const int occ = fmt == 16  ? pkv::partial_bal_ctas_per_sm_bf16(D, DV, nq, dev)
+                    : fmt == 4 ? pkv::partial_bal_ctas_per_sm_u4(D, DV, nq, dev)
+                    : fmt == 8 ? pkv::partial_bal_ctas_per_sm_u8(D, DV, nq, dev)
+                               : pkv::partial_bal_ctas_per_sm_e4m3(D, DV, nq, dev);
     if (occ <= 0) return cuda_fail("occupancy of the balanced partial kernel", cudaGetLastError());
     bal_ctas = sms * static_cast<int>(std::min<long long>(occ, bal_ctas_per_sm_bound(info)));
   }
   const long long rows = static_cast<long long>(layout->num_blocks) * HK * layout->block_size;
   const int elem = info.tensor_elem_bytes;
-  const long long row_elems_k = quant ? static_cast<long long>(D) * layout->bits / 8 : D;
-  const long long row_elems_v = quant ? static_cast<long long>(DV) * layout->bits / 8 : DV;
+  const bool codes = layout->bits != 16;
+  const long long row_elems_k = codes ? static_cast<long long>(D) * layout->bits / 8 : D;
+  const long long row_elems_v = codes ? static_cast<long long>(DV) * layout->bits / 8 : DV;
 
   *pd = PreparedDecode{};
   if (partial) {
@@ -549,10 +576,15 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
-  p.k_scales = static_cast<const __nv_bfloat16*>(k_scales);
-  p.k_biases = static_cast<const __nv_bfloat16*>(k_biases);
-  p.v_scales = static_cast<const __nv_bfloat16*>(v_scales);
-  p.v_biases = static_cast<const __nv_bfloat16*>(v_biases);
+  if (block_scaled(layout)) {
+    p.k_block_scales = static_cast<const float*>(k_scales);
+    p.v_block_scales = static_cast<const float*>(v_scales);
+  } else {
+    p.k_scales = static_cast<const __nv_bfloat16*>(k_scales);
+    p.k_biases = static_cast<const __nv_bfloat16*>(k_biases);
+    p.v_scales = static_cast<const __nv_bfloat16*>(v_scales);
+    p.v_biases = static_cast<const __nv_bfloat16*>(v_biases);
+  }
   p.out = static_cast<__nv_bfloat16*>(out);
   const size_t slots = static_cast<size_t>(params->num_seqs) * params->num_q_heads * params->n_query * plan.max_partitions;
   const size_t o_bytes = bal ? balanced_workspace(static_cast<long long>(bal_ctas) * info.page_groups,
@@ -581,12 +613,12 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   if (k_new) {  // the pools are the caller's writable planes (the fused entry takes them non-const)
     p.k_new = static_cast<const __nv_bfloat16*>(k_new);
     p.v_new = static_cast<const __nv_bfloat16*>(v_new);
-    p.app = append_target(quant, const_cast<void*>(k_pool), const_cast<void*>(v_pool), const_cast<void*>(k_scales),
+    p.app = append_target(codes, const_cast<void*>(k_pool), const_cast<void*>(v_pool), const_cast<void*>(k_scales),
                           const_cast<void*>(k_biases), const_cast<void*>(v_scales), const_cast<void*>(v_biases));
   }
 
   pd->grid = bal ? dim3(bal_ctas) : dim3(plan.max_partitions, HK, params->num_seqs);
-  pd->bits = layout->bits;
+  pd->fmt = format_of(layout);
   pd->dk = D;
   pd->dv = DV;
   pd->nq = nq;
@@ -634,21 +666,25 @@ int launch_prepared(const PreparedDecode& pd, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (pd.partial) {
     if (pd.pc)
-      e = pd.bits == 16  ? pkv::launch_partial_bf16_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
-          : pd.bits == 4 ? pkv::launch_partial_u4_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
-                         : pkv::launch_partial_u8_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
+      e = pd.fmt == 16  ? pkv::launch_partial_bf16_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+          : pd.fmt == 4 ? pkv::launch_partial_u4_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+          : pd.fmt == 8 ? pkv::launch_partial_u8_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+                        : pkv::launch_partial_e4m3_pc(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
     else if (pd.bal)
-      e = pd.bits == 16  ? pkv::launch_partial_bf16_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
-          : pd.bits == 4 ? pkv::launch_partial_u4_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
-                         : pkv::launch_partial_u8_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
+      e = pd.fmt == 16  ? pkv::launch_partial_bf16_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+          : pd.fmt == 4 ? pkv::launch_partial_u4_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+          : pd.fmt == 8 ? pkv::launch_partial_u8_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device)
+                        : pkv::launch_partial_e4m3_bal(pd.dk, pd.dv, pd.nq, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
     else if (pd.cc)
       e = pkv::launch_partial_bf16_cc(pd.dk, pd.dv, pd.nq, pd.solo, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
-    else if (pd.bits == 16)
+    else if (pd.fmt == 16)
       e = pkv::launch_partial_bf16(pd.dk, pd.dv, pd.nq, pd.solo, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
-    else if (pd.bits == 4)
+    else if (pd.fmt == 4)
       e = pkv::launch_partial_u4(pd.dk, pd.dv, pd.nq, pd.solo, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
-    else
+    else if (pd.fmt == 8)
       e = pkv::launch_partial_u8(pd.dk, pd.dv, pd.nq, pd.solo, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
+    else
+      e = pkv::launch_partial_e4m3(pd.dk, pd.dv, pd.nq, pd.solo, pd.p, pd.tk, pd.tv, pd.grid, st, pd.device);
     if (e != cudaSuccess) return cuda_fail("partial kernel launch", e);
   }
   if (pd.merge) {
@@ -847,18 +883,40 @@ int pkv_paged_append(const pkv_pool_layout* layout, int32_t num_seqs, int32_t ma
                      int32_t* error_flag, void* stream) {
   int rc = check_layout(layout);
   if (rc) return rc;
-  if (!pkv::append_supported(layout->bits, layout->head_dim, v_dim(layout))) return PKV_ERR_BAD_LAYOUT;
+  if (!pkv::append_supported(format_of(layout), layout->head_dim, v_dim(layout))) return PKV_ERR_BAD_LAYOUT;
   if (num_seqs <= 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || n_new < 0 || n_new > 65535)
     return PKV_ERR_BAD_PARAMS;
   if (static_cast<long long>(max_blocks_per_seq) * layout->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
-  const bool quant = layout->bits != 16;
   if (!k_new || !v_new || !block_tables || !seq_lens || !k_pool || !v_pool) return PKV_ERR_NULL_POINTER;
-  if (quant && (!k_scales || !k_biases || !v_scales || !v_biases)) return PKV_ERR_NULL_POINTER;
+  if (!scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(error_flag, 4))
     return PKV_ERR_MISALIGNED;
-  if (quant && (!aligned(k_scales, 4) || !aligned(k_biases, 4) || !aligned(v_scales, 4) || !aligned(v_biases, 4)))
-    return PKV_ERR_MISALIGNED;
+  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 4)) return PKV_ERR_MISALIGNED;
+  if (block_scaled(layout)) {
+    pkv::AppendBlockParams a{};
+    a.src[0] = static_cast<const __nv_bfloat16*>(k_new);
+    a.src[1] = static_cast<const __nv_bfloat16*>(v_new);
+    a.pool[0] = static_cast<uint8_t*>(k_pool);
+    a.pool[1] = static_cast<uint8_t*>(v_pool);
+    a.scales[0] = static_cast<float*>(k_scales);
+    a.scales[1] = static_cast<float*>(v_scales);
+    a.dim[0] = layout->head_dim;
+    a.dim[1] = v_dim(layout);
+    a.block_tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.error_flag = error_flag;
+    a.num_blocks = layout->num_blocks;
+    a.num_kv_heads = layout->num_kv_heads;
+    a.block_size = layout->block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.n_new = n_new;
+    (void)cudaGetLastError();
+    cudaError_t e = pkv::launch_append_blocks(a, num_seqs, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("append kernel launch", e);
+    return PKV_OK;
+  }
+  const bool quant = layout->bits != 16;
   pkv::AppendParams a{};
   a.k_new = static_cast<const __nv_bfloat16*>(k_new);
   a.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -985,14 +1043,12 @@ int pkv_paged_decode_attention_no_alloc(const pkv_pool_layout* layout, const pkv
   if (rc) return rc;
   rc = check_params(layout, params);
   if (rc) return rc;
-  const bool quant = layout->bits != 16;
   if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out) return PKV_ERR_NULL_POINTER;
-  if (quant && (!k_scales || !k_biases || !v_scales || !v_biases)) return PKV_ERR_NULL_POINTER;
+  if (!scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(error_flag, 4))
     return PKV_ERR_MISALIGNED;
-  if (quant && (!aligned(k_scales, 16) || !aligned(k_biases, 16) || !aligned(v_scales, 16) || !aligned(v_biases, 16)))
-    return PKV_ERR_MISALIGNED;
+  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 16)) return PKV_ERR_MISALIGNED;
 
   int sms = 0;
   rc = device_sm_count(&sms);

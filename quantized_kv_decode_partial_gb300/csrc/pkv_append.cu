@@ -52,6 +52,8 @@ cudaError_t launch_append_of(const AppendParams& p, int num_seqs, cudaStream_t s
 }  // namespace
 
 bool append_supported(int bits, int head_dim, int v_head_dim) {
+  // e4m3 pages: the pairs of the bf16 ones (pkv_append_blocks.cu takes any multiple of 16)
+  if (bits == kFmtE4m3) return append_supported(16, head_dim, v_head_dim);
 #define X(B_, DK_, DV_) \
   if (bits == B_ && head_dim == DK_ && v_head_dim == DV_) return true;
   PKV_APPEND_SHAPES(X)

@@ -11,6 +11,10 @@
 
 namespace pkv {
 
+// Page formats by their stored bits (the BITS template argument): 16 (bf16), 4 and 8
+// (affine codes); e4m3 codes with one f32 scale per block and KV head take this tag.
+constexpr int kFmtE4m3 = 9;
+
 constexpr int kDevErrBadBlock = 1;
 constexpr int kDevErrBadSeqLen = 2;
 constexpr int kDevErrTimeout = 4;
@@ -41,6 +45,8 @@ struct PartialParams {
   const __nv_bfloat16* k_biases;
   const __nv_bfloat16* v_scales;
   const __nv_bfloat16* v_biases;
+  const float* k_block_scales;  // [NB, HK]   (e4m3 pages)
+  const float* v_block_scales;
   __nv_bfloat16* out;   // [B, HQ, N, DV], written directly with one partition or a cluster merge
   __nv_bfloat16* out_mirror;  // optional second destination of those writes (mapped host memory)
   float* ws_o;          // [B*HQ*N, max_partitions, D]
@@ -105,6 +111,18 @@ struct AppendParams {
   const int32_t* seq_lens;     // rows before the append
   AppendTarget dst;
   int32_t* error_flag;
+  int num_blocks, num_kv_heads, block_size, max_blocks, n_new;
+};
+
+// Append into e4m3 pages with one scale per (block, KV head): K at index 0, V at index 1.
+struct AppendBlockParams {
+  const __nv_bfloat16* src[2];  // [B, HK, n_new, dim]
+  uint8_t* pool[2];             // [NB, HK, BS, dim]
+  float* scales[2];             // [NB, HK]
+  const int32_t* block_tables;
+  const int32_t* seq_lens;      // rows before the append
+  int32_t* error_flag;
+  int dim[2];
   int num_blocks, num_kv_heads, block_size, max_blocks, n_new;
 };
 
@@ -252,6 +270,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint6
                : "memory");
 }
 
+// 4-byte copy global -> shared through the load/store path.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Makes the current phase of the mbarrier also wait for this thread's earlier cp.async
 // copies: its pending count is raised by one now and lowered when they have landed.
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
@@ -262,6 +285,26 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The four e4m3 codes of a word as two fp16 pairs (exact): bytes 0, 1 and bytes 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {

@@ -27,6 +27,7 @@ struct PartialInfo {
 PartialInfo partial_info_bf16(int dk, int dv, int nq, bool solo);
 PartialInfo partial_info_u4(int dk, int dv, int nq, bool solo);
 PartialInfo partial_info_u8(int dk, int dv, int nq, bool solo);
+PartialInfo partial_info_e4m3(int dk, int dv, int nq, bool solo);
 // bf16 pages with the CUDA-core contraction (up to 4 query rows per KV head, equal head dims)
 PartialInfo partial_info_bf16_cc(int dk, int dv, int nq, bool solo);
 
@@ -36,6 +37,8 @@ cudaError_t launch_partial_u4(int dk, int dv, int nq, bool solo, const PartialPa
                               const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 cudaError_t launch_partial_u8(int dk, int dv, int nq, bool solo, const PartialParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
+cudaError_t launch_partial_e4m3(int dk, int dv, int nq, bool solo, const PartialParams& p, const CUtensorMap& tk,
+                                const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 cudaError_t launch_partial_bf16_cc(int dk, int dv, int nq, bool solo, const PartialParams& p, const CUtensorMap& tk,
                                    const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 
@@ -44,15 +47,19 @@ cudaError_t launch_partial_bf16_cc(int dk, int dv, int nq, bool solo, const Part
 PartialInfo partial_info_bf16_bal(int dk, int dv, int nq);
 PartialInfo partial_info_u4_bal(int dk, int dv, int nq);
 PartialInfo partial_info_u8_bal(int dk, int dv, int nq);
+PartialInfo partial_info_e4m3_bal(int dk, int dv, int nq);
 int partial_bal_ctas_per_sm_bf16(int dk, int dv, int nq, int device);
 int partial_bal_ctas_per_sm_u4(int dk, int dv, int nq, int device);
 int partial_bal_ctas_per_sm_u8(int dk, int dv, int nq, int device);
+int partial_bal_ctas_per_sm_e4m3(int dk, int dv, int nq, int device);
 cudaError_t launch_partial_bf16_bal(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
                                     const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 cudaError_t launch_partial_u4_bal(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 cudaError_t launch_partial_u8_bal(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
+cudaError_t launch_partial_e4m3_bal(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 
 // Instantiations for pools of blocks smaller than a chunk (PartialParams.piece_log2 > 0) of
 // the same shapes' grids of several CTAs per SM; their PartialInfo is that of those grids.
@@ -62,6 +69,8 @@ cudaError_t launch_partial_u4_pc(int dk, int dv, int nq, const PartialParams& p,
                                  const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 cudaError_t launch_partial_u8_pc(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
                                  const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
+cudaError_t launch_partial_e4m3_pc(int dk, int dv, int nq, const PartialParams& p, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, dim3 grid, cudaStream_t stream, int device);
 
 int merge_groups(int head_dim, int max_partitions);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
@@ -70,5 +79,6 @@ cudaError_t launch_gather(const GatherParams& p, int num_seqs, cudaStream_t stre
 bool append_supported(int bits, int head_dim, int v_head_dim);
 cudaError_t launch_append(const AppendParams& p, int bits, int head_dim, int v_head_dim, int num_seqs,
                           cudaStream_t stream);
+cudaError_t launch_append_blocks(const AppendBlockParams& p, int num_seqs, cudaStream_t stream);
 
 }  // namespace pkv

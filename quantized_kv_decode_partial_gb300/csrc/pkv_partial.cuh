@@ -49,6 +49,12 @@
 //        o_d = sum_t P'_g(t) c_td + sum_t p(t) b_g(t).
 //    The scale terms cost a few FMAs per key and group instead of two per
 //    element; the bias terms of the scores run as one extra bf16 MMA per tile.
+//  * e4m3 pages (one f32 scale per block and KV head) take the 8-bit byte layout. Both
+//    products run as fp16 MMAs on the codes' own values (every e4m3 value is an fp16
+//    value; one conversion per pair). The key scale of a block multiplies its scores;
+//    the value scale cannot ride on the fp16 weights (its range is f32's), so each
+//    chunk's V^T P^T goes to fresh accumulators and enters O^T by one f32 FMA with the
+//    chunk's scale, 4 FMAs per 4 MMAs of a 32-row chunk. The kernel stays bound by HBM.
 //  * Rows at or past seq_len in the last page are masked before they can reach
 //    an accumulator (scores set to -inf by select; their V operand or V scale
 //    zeroed), so stale storage may hold anything, NaN included.
@@ -72,17 +78,20 @@ namespace pkv {
 // with up to that many query rows per KV head (NT = WQ = 1).
 template <int BITS, int D, int DV, int NT, int WQ, bool SOLO, int CCQ = 0, bool BAL = false>
 struct PartialCfg {
-  static constexpr bool kQuant = BITS != 16;
-  static constexpr int kElemBytes = kQuant ? 1 : 2;                    // tensor-map element size
-  static constexpr int kRowBytes = kQuant ? D * BITS / 8 : 2 * D;      // stored bytes of one K row
-  static constexpr int kRowBytesV = kQuant ? DV * BITS / 8 : 2 * DV;   // ... and of one V row
+  static constexpr bool kQuant = BITS == 4 || BITS == 8;  // affine codes
+  static constexpr bool kBlk = BITS == kFmtE4m3;          // e4m3 codes, one scale per block and KV head
+  static constexpr int kCodeBits = kBlk ? 8 : BITS;       // stored bits of one value
+  static constexpr int kElemBytes = BITS == 16 ? 2 : 1;   // tensor-map element size
+  static constexpr int kRowBytes = D * kCodeBits / 8;     // stored bytes of one K row
+  static constexpr int kRowBytesV = DV * kCodeBits / 8;   // ... and of one V row
   static constexpr int kGroups = D / 64;
   static constexpr int kGroupsV = DV / 64;
-  // Rows per stage: 32 for affine pages when a stage stays within ~9.5 KB, else 16.
+  // Rows per stage: 32 for affine and e4m3 pages when a stage stays within ~9.5 KB, else 16.
   static constexpr int kCh =
-      (kQuant && 32 * (kRowBytes + kRowBytesV) + 2 * 32 * (kGroups + kGroupsV) * 2 <= 9728) ? 32 : 16;
-  static constexpr int kRB = kRowBytes >= 128 ? 128 : kRowBytes;      // bytes of one box row
-  static constexpr int kRBV = kRowBytesV >= 128 ? 128 : kRowBytesV;
+      (BITS != 16 && 32 * (kRowBytes + kRowBytesV) + (kQuant ? 2 * 32 * (kGroups + kGroupsV) * 2 : 32) <= 9728) ? 32
+                                                                                                                : 16;
+  static constexpr int kRB = kRowBytes % 128 == 0 ? 128 : 64;  // bytes of one box row
+  static constexpr int kRBV = kRowBytesV % 128 == 0 ? 128 : 64;
   static constexpr int kBoxes = kRowBytes / kRB;
   static constexpr int kBoxesV = kRowBytesV / kRBV;
   static constexpr int kBoxBytes = kCh * kRB;
@@ -91,13 +100,15 @@ struct PartialCfg {
   static constexpr int kPlaneBytesV = kBoxesV * kBoxBytesV;
   static constexpr int kSbBytes = kQuant ? kCh * kGroups * 2 : 0;     // one K scale or bias plane
   static constexpr int kSbBytesV = kQuant ? kCh * kGroupsV * 2 : 0;   // one V scale or bias plane
-  // stage layout: K rows, V rows, K scales, K biases, V scales, V biases
+  // stage layout: K rows, V rows, K scales, K biases, V scales, V biases (affine); e4m3
+  // pages: K rows, V rows, then the f32 scales of the chunk's up to four blocks, K and V
   static constexpr int kOffV = kPlaneBytes;
   static constexpr int kOffKs = kPlaneBytes + kPlaneBytesV;
   static constexpr int kOffKb = kOffKs + kSbBytes;
   static constexpr int kOffVs = kOffKb + kSbBytes;
   static constexpr int kOffVb = kOffVs + kSbBytesV;
-  static constexpr int kTxBytes = kOffVb + kSbBytesV;
+  static constexpr int kOffVScale = kOffKs + 16;  // e4m3: V scales (K scales at kOffKs)
+  static constexpr int kTxBytes = kOffVb + kSbBytesV + (kBlk ? 32 : 0);
   static constexpr int kTmaBytes = kPlaneBytes + kPlaneBytesV;  // the part the TMA copies bring
   static constexpr int kSbCopies = (2 * kSbBytes + 2 * kSbBytesV) / 16;  // 16-byte copies of scales and biases
   static constexpr int kStageBytes = (kTxBytes + 1023) / 1024 * 1024;
@@ -187,7 +198,7 @@ struct PartialCfg {
   static_assert((kRB == 128 || kRB == 64) && (kRBV == 128 || kRBV == 64), "box rows of 64 or 128 bytes");
   static_assert(kRowBytes % kRB == 0 && kRowBytesV % kRBV == 0, "whole boxes per row");
   static_assert(kWarps * kStagesPerWarp * 12 + 4 <= kBarrierBytes, "barrier area");
-  static_assert(!kQuant || (D % 64 == 0 && DV % 64 == 0), "affine head dims are whole 64-dim groups");
+  static_assert(BITS == 16 || (D % 64 == 0 && DV % 64 == 0), "head dims of codes are whole 64-dim groups");
   static_assert(DV % 64 == 0, "value head dims are whole 4-m-tile groups");
   static_assert(WQ == 1 || WQ == 2 || WQ == 4 || WQ == 8, "query groups of 1, 2, 4 or 8 warps");
   static_assert(kWarps % WQ == 0, "whole query groups");
@@ -226,18 +237,21 @@ __device__ __forceinline__ void q_dims(int kk, int reg, int t, int& d_lo, int& d
     const int base = 64 * grp + 32 * cc + 8 * t + s + 2 * reg;
     d_lo = base;
     d_hi = base + 4;
-  } else {
+  } else if constexpr (BITS == 8) {
     const int grp = kk >> 2, c = kk & 3;
     const int base = 64 * grp + 16 * c + 4 * t + reg;
     d_lo = base;
     d_hi = base + 2;
+  } else {  // e4m3: the low or the high byte pair of a word
+    d_lo = 16 * kk + 4 * t + 2 * reg;
+    d_hi = d_lo + 1;
   }
 }
 
 // Loads the query values one lane needs from row `qrow` (D bf16 values) as 2 * D/16
 // words of bf16 pairs, with vector loads of the contiguous runs q_dims addresses
 // (zeros when !valid): bf16 pages take a word per (k-step, register); 4-bit pages 16
-// bytes per 32-dim half group; 8-bit pages 8 bytes per 16-dim quarter group.
+// bytes per 32-dim half group; 8-bit and e4m3 pages 8 bytes per 16-dim quarter group.
 template <int BITS, int D>
 __device__ __forceinline__ void q_load_words(const __nv_bfloat16* qrow, int t, bool valid, uint32_t (&w)[D / 8]) {
   if constexpr (BITS == 16) {
@@ -267,8 +281,8 @@ __device__ __forceinline__ void q_load_words(const __nv_bfloat16* qrow, int t, b
 // The bf16 pair (dims d_lo, d_hi of q_dims(kk, reg)) from the words of q_load_words.
 template <int BITS, int W>
 __device__ __forceinline__ uint32_t q_pair(const uint32_t (&w)[W], int kk, int reg) {
-  if constexpr (BITS == 16) {
-    return w[2 * kk + reg];
+  if constexpr (BITS == 16 || BITS == kFmtE4m3) {
+    return w[2 * kk + reg];  // e4m3: 8-byte run kk holds dims base..base+3, pairs in order
   } else if constexpr (BITS == 4) {
     // 16-byte run c = kk/2 holds dims base..base+7 as words of pairs; the lane needs
     // elements j = (kk & 1) + 2 reg and j + 4
@@ -508,6 +522,7 @@ __global__ void __maxnreg__(255)
     // piece q mod nb of local chunk q / nb); with blocks of a chunk or more, piece q is
     // chunk q.
     const int nbl = PC ? p.piece_log2 : 0, nb = 1 << nbl, pb = C::kCh >> nbl;  // PC: instantiations for such pools
+    const int piece_shift = (C::kCh == 32 ? 5 : 4) - nbl;                       // log2 of pb
     auto piece_row = [&](int q) { return chunk_row(q >> nbl) + (q & (nb - 1)) * pb; };  // its first cache row
     // TMA row coordinate of local piece q in physical block ph (the block's rows of this
     // KV head plus the piece's offset in the block), -1 for a bad block id, or -2 for a
@@ -591,6 +606,9 @@ __global__ void __maxnreg__(255)
       }
     }
 
+    // e4m3 pages: lane j < nb copies the K scale of the chunk's piece j, lane 4 + j its V scale.
+    const float* const bs_src = C::kBlk ? (lane < 4 ? p.k_block_scales : p.v_block_scales) : nullptr;
+
     // Issues the next chunk into stage `is` (the one just consumed: with one stage per
     // chunk in flight, chunk i always lands in stage i mod kStagesPerGroup).
     auto issue_next = [&](int is) {  // the leader warp, warp-uniform
@@ -614,7 +632,7 @@ __global__ void __maxnreg__(255)
         if (!__all_sync(0xffffffffu, mine >= 0 || mine == -2)) row = -1;
         pieces_in = __popc(__ballot_sync(0xffffffffu, lane < nb && mine >= 0));
       }
-      if (!BAL && p.k_new != nullptr) {
+      if (!C::kBlk && !BAL && p.k_new != nullptr) {
         // Fused append: the step's new rows len-N .. len-1 that fall in this chunk are
         // written into its page first (the warp writes, fences its generic-proxy stores
         // against the async proxy, then lane 0 copies the chunk). Chunks lie inside one
@@ -624,8 +642,9 @@ __global__ void __maxnreg__(255)
         if (a0 < a1 && row >= 0) {
           for (int tr = a0; tr < a1; ++tr) {
             const size_t src = (static_cast<size_t>(b) * p.num_kv_heads + hk) * N + (tr - (len - N));
-            append_row<BITS, D, DV>(p.k_new + src * D, p.v_new + src * DV, p.app, static_cast<size_t>(row) + (tr - cr),
-                                    lane);
+            if constexpr (!C::kBlk)
+              append_row<BITS, D, DV>(p.k_new + src * D, p.v_new + src * DV, p.app,
+                                      static_cast<size_t>(row) + (tr - cr), lane);
           }
           fence_proxy_async_global();
           __syncwarp();
@@ -645,6 +664,24 @@ __global__ void __maxnreg__(255)
             if (32 * j + lane < C::kSbCopies && prow >= 0)
               cp_async_16(st + (PC ? sb_dst[j] & 0xFFFF : sb_dst[j]), sb_src[j] + static_cast<size_t>(prow) * sb_pitch[j],
                           policy);
+          }
+          cp_async_mbar_arrive(fb);
+        }
+        __syncwarp();
+      }
+      if constexpr (C::kBlk) {
+        // The blocks' scales: a 4-byte copy per piece and plane. A piece past the length has
+        // none; its slot is zeroed, since its (masked) keys still meet it.
+        if (row >= 0) {
+          const int j = lane & 3;
+          const int prow = nbl > 0 ? __shfl_sync(0xffffffffu, crd_cur, (ip + j) & 31) : row;
+          if (lane < 8 && j < nb) {
+            const uint32_t dst = st + (lane < 4 ? C::kOffKs : C::kOffVScale) + 4 * j;
+            if (prow >= 0) {
+              cp_async_4(dst, bs_src + static_cast<unsigned>(prow) / static_cast<unsigned>(p.block_size));
+            } else {
+              st_shared_u32(dst, 0u);
+            }
           }
           cp_async_mbar_arrive(fb);
         }
@@ -745,7 +782,7 @@ __global__ void __maxnreg__(255)
 #pragma unroll
           for (int reg = 0; reg < 2; ++reg)
             bf16x2_to_f32(q_pair<BITS>(qw[nt], kk, reg), qv[kk][nt][2 * reg], qv[kk][nt][2 * reg + 1]);
-      if constexpr (!C::kQuant) {
+      if constexpr (BITS == 16) {
 #pragma unroll
         for (int kk = 0; kk < C::kKs; ++kk)
 #pragma unroll
@@ -755,7 +792,7 @@ __global__ void __maxnreg__(255)
               qf[kk][nt][reg] = pack_bf16x2(qv[kk][nt][2 * reg], qv[kk][nt][2 * reg + 1]);  // exact
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) colscale[nt][0] = colscale[nt][1] = p.score_scale;
-      } else {
+      } else {  // codes: fp16, after the row's prescale
         int kexp[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -777,11 +814,13 @@ __global__ void __maxnreg__(255)
             for (int reg = 0; reg < 2; ++reg)
               fr[reg] = pack_f16x2(qv[kk][nt][2 * reg] * up, qv[kk][nt][2 * reg + 1] * up);
             // Per-group sums of the prescaled q (columns 2t, 2t+1), through the MMA path.
-            mma_f16(acc, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, fr[0], fr[1]);
-            if ((kk & 3) == 3) {
-              qsum[kk >> 2][nt][0] = acc[0] * C::kCodeUnit;
-              qsum[kk >> 2][nt][1] = acc[1] * C::kCodeUnit;
-              acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+            if constexpr (C::kQuant) {
+              mma_f16(acc, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, fr[0], fr[1]);
+              if ((kk & 3) == 3) {
+                qsum[kk >> 2][nt][0] = acc[0] * C::kCodeUnit;
+                qsum[kk >> 2][nt][1] = acc[1] * C::kCodeUnit;
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+              }
             }
             const float f = q_over16<BITS>(kk) ? up * (1.f / 16.f) : up;
 #pragma unroll
@@ -790,14 +829,17 @@ __global__ void __maxnreg__(255)
           }
         }
         // Column c = 2t + e2 of n-tile nt is query row 8 nt + 2t + e2, prescaled by the
-        // lanes whose g equals 2t + e2. Codes are counted in units of 2^-24.
+        // lanes whose g equals 2t + e2. Affine codes are counted in units of 2^-24; e4m3
+        // codes enter as their own values.
+        constexpr int kUnitLog2 = C::kQuant ? 24 : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e2 = 0; e2 < 2; ++e2) {
             const int k = __shfl_sync(0xffffffffu, kexp[nt], (2 * t + e2) * 4);
-            colscale[nt][e2] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23);
+            colscale[nt][e2] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 + kUnitLog2 - k) << 23);
           }
+        if constexpr (C::kQuant) {
         // The bias part of the scores, sum_g b_g * sum_{d in g} q_d, runs as one bf16 MMA per
         // 16-key tile: A holds each key's G biases twice (k slots 0..G-1 and G..2G-1), B
         // holds query column g's group sums split into bf16 high parts (slots 0..G-1) and
@@ -825,6 +867,7 @@ __global__ void __maxnreg__(255)
           }
           qsb[nt] = pack_bf16x2(slot_val[0], slot_val[1]);  // exact: both are bf16 values
         }
+        }  // affine
       }
     }
 
@@ -903,6 +946,37 @@ __global__ void __maxnreg__(255)
 #pragma unroll
               for (int e = 0; e < 4; ++e) sacc[nt][e] += sacc2[nt][e];
           }
+        } else if constexpr (C::kBlk) {
+          // A CTA alone on its SM takes two accumulators, as above.
+          constexpr int kChains = SOLO ? 2 : 1;
+          float sacc2[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc2[nt][e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < C::kKs / 2; ++i) {  // 32 bytes of each row: two k-steps
+            uint32_t xk[4];
+            ldsm_x4(swizzled<C::kRB>(kpl + (32 * i / C::kRB) * C::kBoxBytes, lrow, (2 * i) % (C::kRB / 16) + lch_n), xk);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const int kk = 2 * i + cc;
+              uint32_t a0, a1, a2, a3;  // dims 4t..4t+3 of rows g and g + 8
+              e4m3x4_to_f16x2(xk[2 * cc], a0, a2);
+              e4m3x4_to_f16x2(xk[2 * cc + 1], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16((kChains == 2 && cc) ? sacc2[nt] : sacc[nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
+            }
+          }
+          const uint32_t ksc = kpl + C::kOffKs;
+          const float ks0 = ld_shared_f32(ksc + (PC ? 4 * ((tile * 16 + g) >> piece_shift) : 0));
+          const float ks1 = PC ? ld_shared_f32(ksc + 4 * ((tile * 16 + g + 8) >> piece_shift)) : ks0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sacc[nt][e] = (kChains == 2 ? sacc[nt][e] + sacc2[nt][e] : sacc[nt][e]) * (e < 2 ? ks0 : ks1);
         } else {
           // scales of keys g and g + 8 of this tile, all groups
           float ks0[C::kGroups], ks1[C::kGroups];
@@ -1075,6 +1149,68 @@ __global__ void __maxnreg__(255)
     };
     auto value_chunk = [&](uint32_t kpl, uint32_t vpl, int kbase, bool stale, const float (&pr)[C::kTiles][NT][4]) {
       // ---- O^T += V^T P^T
+      if constexpr (C::kBlk) {
+        // Weights of the whole chunk as B fragments; with several blocks in the chunk, each
+        // key's weight times its block's scale over the chunk's largest (at most 1). The
+        // chunk's product then takes that largest scale on its way into O^T.
+        uint32_t pb2[C::kTiles][NT][2];
+        const uint32_t vsc = kpl + C::kOffVScale;
+        float vmax = ld_shared_f32(vsc);
+        if constexpr (PC)
+          for (int j = 1; j < nb; ++j) vmax = fmaxf(vmax, ld_shared_f32(vsc + 4 * j));
+        const float vinv = PC && vmax > 0.f ? 1.f / vmax : 0.f;
+#pragma unroll
+        for (int tile = 0; tile < C::kTiles; ++tile) {
+          const float ra = PC ? ld_shared_f32(vsc + 4 * ((tile * 16 + g) >> piece_shift)) * vinv : 1.f;
+          const float rb = PC ? ld_shared_f32(vsc + 4 * ((tile * 16 + g + 8) >> piece_shift)) * vinv : 1.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb2[tile][nt][0] = movmatrix_trans(pack_f16x2(pr[tile][nt][0] * ra, pr[tile][nt][1] * ra));
+            pb2[tile][nt][1] = movmatrix_trans(pack_f16x2(pr[tile][nt][2] * rb, pr[tile][nt][3] * rb));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C::kMt / 2; ++i) {  // 32 bytes of each row: m-tiles 2 i, 2 i + 1
+          float acc[2][NT][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
+#pragma unroll
+          for (int tile = 0; tile < C::kTiles; ++tile) {
+            uint32_t y[4];
+            ldsm_x4_t(swizzled<C::kRBV>(vpl + (32 * i / C::kRBV) * C::kBoxBytesV, tile * 16 + lrow_t,
+                                        (2 * i) % (C::kRBV / 16) + lch_t),
+                      y);
+            if (stale) {  // codes at or past len may be NaN
+              const int k0 = kbase + tile * 16 + 2 * t;
+              const uint32_t m01 = (k0 < len ? 0x0000ffffu : 0u) | (k0 + 1 < len ? 0xffff0000u : 0u);
+              const uint32_t m23 = (k0 + 8 < len ? 0x0000ffffu : 0u) | (k0 + 9 < len ? 0xffff0000u : 0u);
+              y[0] &= m01;
+              y[1] &= m01;
+              y[2] &= m23;
+              y[3] &= m23;
+            }
+            // y: dims 2g, 2g + 1 of key 2t (low half) and of key 2t + 1; a pair of keys per register
+            uint32_t a[4], b[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) e4m3x4_to_f16x2(__byte_perm(y[r], 0u, 0x3120), a[r], b[r]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[0][nt], a[0], a[1], a[2], a[3], pb2[tile][nt][0], pb2[tile][nt][1]);
+              mma_f16(acc[1][nt], b[0], b[1], b[2], b[3], pb2[tile][nt][0], pb2[tile][nt][1]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[2 * i + j][nt][e] = fmaf(vmax, acc[j][nt][e], o[2 * i + j][nt][e]);
+        }
+      } else {
 #pragma unroll
       for (int tile = 0; tile < C::kTiles; ++tile) {
         const int lrow = tile * 16 + lrow_t;
@@ -1199,6 +1335,7 @@ __global__ void __maxnreg__(255)
           }  // unpaired groups
         }
       }
+      }  // bf16 and affine pages
     };
 
     for (; done < seg_end; ++done, cs_parity ^= (cs == C::kStagesPerGroup - 1), cs = cs == C::kStagesPerGroup - 1 ? 0 : cs + 1) {
@@ -1324,9 +1461,9 @@ __global__ void __maxnreg__(255)
         }
         break;
       }
-      // o: four (4-bit pages) or two (8-bit) consecutive head dims per store where the
+      // o: four (4-bit pages) or two (8-bit, e4m3) consecutive head dims per store where the
       // accumulator layout puts them in one thread, as in the combine below
-      constexpr int kRun = BITS == 4 ? 4 : BITS == 8 ? 2 : 1;
+      constexpr int kRun = BITS == 4 ? 4 : BITS == 16 ? 1 : 2;
 #pragma unroll
       for (int mt = 0; mt < C::kMt; mt += kRun)
 #pragma unroll
@@ -1399,10 +1536,10 @@ __global__ void __maxnreg__(255)
           cl[rbase + r] = l_run[nt][e2];
         }
     }
-    // o values, four (4-bit pages) or two (8-bit) consecutive head dims per store where
+    // o values, four (4-bit pages) or two (8-bit, e4m3) consecutive head dims per store where
     // the accumulator layout puts them in one thread; padding rows of the last n-tile
     // are never read
-    constexpr int kRun = BITS == 4 ? 4 : BITS == 8 ? 2 : 1;
+    constexpr int kRun = BITS == 4 ? 4 : BITS == 16 ? 1 : 2;
 #pragma unroll
     for (int mt = 0; mt < C::kMt; mt += kRun)
 #pragma unroll

@@ -1,0 +1,74 @@
+"""CPU checks of the C ABI for e4m3 pages: which layouts are planned, what is refused."""
+
+import ctypes
+
+import pytest
+
+from quantized_kv_decode_partial_gb300 import binding as B
+from quantized_kv_decode_partial_gb300 import build as pkv_build
+
+FAKE = 1 << 20  # aligned, never dereferenced: checks come before any CUDA call
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pkv_build.build()
+    return B.load_library()
+
+
+def plan_rc(lib, lay, par):
+    return lib.pkv_make_plan(ctypes.byref(lay), ctypes.byref(par), 152, ctypes.byref(B.Plan()))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 256), (192, 128), (256, 128), (128, 256)])
+@pytest.mark.parametrize("bs", [8, 16, 32, 96])
+def test_layouts_and_query_rows(lib, dk, dv, bs):
+    for nq in (1, 8, 9, 33, 64, 65):
+        lay = B.PoolLayout(100, 2, bs, dk, 8, B.PKV_GROUP_BLOCK, dv)
+        rc = plan_rc(lib, lay, B.DecodeParams(3, 2 * nq, 1, 8))
+        assert rc == (B.PKV_OK if nq <= 64 else B.PKV_ERR_UNSUPPORTED_SHAPE)
+
+
+@pytest.mark.parametrize("lay,code", [
+    (B.PoolLayout(100, 2, 32, 128, 4, B.PKV_GROUP_BLOCK), B.PKV_ERR_BAD_LAYOUT),  # 4-bit codes are affine
+    (B.PoolLayout(100, 2, 32, 96, 8, B.PKV_GROUP_BLOCK), B.PKV_ERR_BAD_LAYOUT),
+    (B.PoolLayout(100, 2, 4, 128, 8, B.PKV_GROUP_BLOCK), B.PKV_ERR_BAD_LAYOUT),
+    (B.PoolLayout(100, 2, 48, 128, 8, B.PKV_GROUP_BLOCK), B.PKV_ERR_BAD_LAYOUT),
+    (B.PoolLayout(100, 2, 32, 128, 8, -2), B.PKV_ERR_BAD_LAYOUT),
+    (B.PoolLayout(100, 2, 32, 128, 8, 0), B.PKV_ERR_BAD_LAYOUT),
+    (B.PoolLayout(100, 2, 32, 64, 8, 64), B.PKV_ERR_BAD_LAYOUT),  # affine pages have no 64-dim heads
+    (B.PoolLayout(100, 2, 32, 64, 8, B.PKV_GROUP_BLOCK, 128), B.PKV_ERR_UNSUPPORTED_SHAPE),
+])
+def test_layouts_that_are_refused(lib, lay, code):
+    assert plan_rc(lib, lay, B.DecodeParams(1, 4, 1, 4)) == code
+
+
+def test_the_cuda_core_contraction_is_refused(lib):
+    lay = B.PoolLayout(100, 2, 32, 128, 8, B.PKV_GROUP_BLOCK)
+    assert plan_rc(lib, lay, B.DecodeParams(1, 4, 1, 4, 0, 0, B.PKV_CONTRACTION_CUDA_CORE)) == B.PKV_ERR_UNSUPPORTED_SHAPE
+
+
+def test_scale_planes_are_required_and_biases_are_not(lib):
+    lay, par = B.PoolLayout(100, 2, 32, 128, 8, B.PKV_GROUP_BLOCK), B.DecodeParams(1, 4, 1, 4)
+
+    def attend(ks, vs, k=FAKE):
+        return lib.pkv_paged_decode_attention(ctypes.byref(lay), ctypes.byref(par), FAKE, k, FAKE, ks, None, vs, None,
+                                              FAKE, FAKE, 0.1, FAKE, FAKE, 1 << 30, None, None)
+
+    assert attend(None, FAKE) == B.PKV_ERR_NULL_POINTER and attend(FAKE, None) == B.PKV_ERR_NULL_POINTER
+    assert attend(FAKE + 2, FAKE) == B.PKV_ERR_MISALIGNED and attend(FAKE, FAKE + 1) == B.PKV_ERR_MISALIGNED
+    assert attend(FAKE, FAKE, FAKE + 8) == B.PKV_ERR_MISALIGNED
+
+    def append(ks, vs, n=1):
+        return lib.pkv_paged_append(ctypes.byref(lay), 1, 4, n, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ks, None, vs, None,
+                                    None, None)
+
+    assert append(None, FAKE) == B.PKV_ERR_NULL_POINTER and append(FAKE, FAKE + 2) == B.PKV_ERR_MISALIGNED
+    assert append(FAKE, FAKE, -1) == B.PKV_ERR_BAD_PARAMS
+
+
+def test_the_fused_call_is_refused(lib):
+    lay, par = B.PoolLayout(100, 2, 32, 128, 8, B.PKV_GROUP_BLOCK), B.DecodeParams(1, 4, 1, 4)
+    rc = lib.pkv_paged_decode_append_attention(ctypes.byref(lay), ctypes.byref(par), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                               None, FAKE, None, FAKE, FAKE, 0.1, FAKE, FAKE, 1 << 30, None, None)
+    assert rc == B.PKV_ERR_UNSUPPORTED_SHAPE
