@@ -401,6 +401,100 @@ int pkv_paged_decode_append_attention(const pkv_pool_layout* layout, const pkv_d
                                       float scale, void* out, void* workspace, size_t workspace_bytes,
                                       int32_t* error_flag, void* stream);
 
+/* Sparse decode attention: each (sequence, KV head) attends over top_k blocks of its cache,
+ * chosen for the step's queries by a score that reads 4 * head_dim bytes per block instead
+ * of the block. The reference has no counterpart of it.
+ *
+ * Block bounds. k_bounds, bf16 [num_blocks, num_kv_heads, 2, head_dim], 16-byte aligned,
+ * holds for each block and KV head the elementwise smallest (row 0) and largest (row 1) of
+ * its stored keys, rounded outward to bf16. The caller owns the plane; it needs no initial
+ * values, and pkv_update_block_bounds keeps it after each append.
+ *
+ * Score of block j for the query rows r of a KV head (its REP heads times n_query):
+ *     score_j = max_r sum_d max(q_rd * lo_jd, q_rd * hi_jd),
+ * the largest product any key of the block could have with any of the rows.
+ *
+ * Choice. With nb = ceil(len / block_size) blocks held: all of them when nb <= top_k, else
+ * the first_blocks first, the last_blocks last and, of those between, the best-scored, in
+ * all top_k. Blocks are compared as by exact sums, ties going to the lower block: f32 sums
+ * decide where their error cannot matter, f64 sums of exact products elsewhere, so the
+ * choice does not depend on the order of a sum. A NaN score counts as the lowest.
+ *
+ * The softmax then runs over the chosen rows alone, the causal rule among the n_query newest
+ * rows included. window must be 0 and num_seqs * num_kv_heads at most 65535; the layouts and
+ * query-row limits are those of the decode. last_blocks must cover the n_query newest rows
+ * however full the last block is: (last_blocks - 1) * block_size >= n_query - 1. */
+typedef struct pkv_sparse_params {
+  int32_t top_k;        /* blocks per (sequence, KV head), > 0 */
+  int32_t first_blocks; /* taken at the start of the sequence, >= 0 */
+  int32_t last_blocks;  /* taken at its end, >= 1; first_blocks + last_blocks <= top_k */
+} pkv_sparse_params;
+
+typedef struct pkv_sparse_plan {
+  pkv_plan attention;     /* of the decode over chosen blocks: num_seqs * num_kv_heads sequences of
+                             one KV head; its workspace_bytes are what
+                             pkv_selected_decode_attention needs */
+  size_t select_bytes;    /* workspace of pkv_select_blocks (0 when the table holds no more than top_k blocks) */
+  size_t workspace_bytes; /* workspace of pkv_sparse_decode_attention */
+} pkv_sparse_plan;
+
+/* Plans as pkv_make_plan and pkv_plan_for_current_device do. */
+int pkv_make_sparse_plan(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                         const pkv_sparse_params* sparse, int32_t sm_count, pkv_sparse_plan* plan);
+int pkv_sparse_plan_for_current_device(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                       const pkv_sparse_params* sparse, pkv_sparse_plan* plan);
+
+/* Brings the bounds of each sequence's blocks up to date after an append.
+ *   seq_lens  rows held, the new ones included
+ *   n_new     the last n_new rows of each sequence are new (all of them where it holds
+ *             fewer): blocks whose rows are all new get fresh bounds, a block that held
+ *             rows before has its bounds widened by the new ones. e4m3 pages, whose earlier
+ *             rows an append may have rescaled, have every touched block read whole.
+ * A call with n_new of at least every length rebuilds all bounds. k_scales and k_biases as
+ * for the decode. Keys must be finite. Bounds of other blocks stay as they were. Bad block
+ * ids and lengths (outside [0, max_blocks_per_seq*block_size]) are skipped and flagged as
+ * by pkv_paged_append. Blocks that receive rows must belong to one sequence only.
+ * Asynchronous on `stream`. */
+int pkv_update_block_bounds(const pkv_pool_layout* layout, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t n_new,
+                            const void* k_pool, const void* k_scales, const void* k_biases,
+                            const int32_t* block_tables, const int32_t* seq_lens, void* k_bounds,
+                            int32_t* error_flag, void* stream);
+
+/* The choice alone.
+ *   blocks         int32 [num_seqs, num_kv_heads, top_k]: the chosen blocks' places in the
+ *                  sequence, ascending, -1 past the last (NULL: not wanted)
+ *   chosen_tables  int32 [num_seqs, num_kv_heads, top_k]: block_tables entry * num_kv_heads +
+ *                  KV head of each, the block's number in the pool seen as num_blocks *
+ *                  num_kv_heads blocks of one head (-1 past the last, and for a bad block id)
+ *   chosen_lens    int32 [num_seqs, num_kv_heads]: rows of the chosen blocks (0 for a bad length)
+ *   workspace      plan.select_bytes
+ * A seq_len below n_query or above the table flags PKV_DEVERR_BAD_SEQ_LEN. A bad block id
+ * scores lowest and is flagged. */
+int pkv_select_blocks(const pkv_pool_layout* layout, const pkv_decode_params* params, const pkv_sparse_params* sparse,
+                      const void* q, const void* k_bounds, const int32_t* block_tables, const int32_t* seq_lens,
+                      int32_t* blocks, int32_t* chosen_tables, int32_t* chosen_lens, void* workspace,
+                      size_t workspace_bytes, int32_t* error_flag, void* stream);
+
+/* The attention alone, over a choice made by pkv_select_blocks (or one of the caller's own
+ * in the same form: any blocks, the last chosen_lens rows of which end at the sequence's
+ * newest). Workspace: plan.attention.workspace_bytes. Other arguments and errors as
+ * pkv_paged_decode_attention. */
+int pkv_selected_decode_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                  const pkv_sparse_params* sparse, const void* q, const void* k_pool,
+                                  const void* v_pool, const void* k_scales, const void* k_biases,
+                                  const void* v_scales, const void* v_biases, const int32_t* chosen_tables,
+                                  const int32_t* chosen_lens, float scale, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* error_flag, void* stream);
+
+/* Choice and attention. `blocks` as pkv_select_blocks (may be NULL). Workspace:
+ * plan.workspace_bytes; calls that overlap on the GPU need one each. */
+int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                const pkv_sparse_params* sparse, const void* q, const void* k_pool,
+                                const void* v_pool, const void* k_scales, const void* k_biases, const void* v_scales,
+                                const void* v_biases, const void* k_bounds, const int32_t* block_tables,
+                                const int32_t* seq_lens, float scale, int32_t* blocks, void* out, void* workspace,
+                                size_t workspace_bytes, int32_t* error_flag, void* stream);
+
 /* Bit-exact gather of one pool plane into contiguous per-sequence rows, the
  * fetch copy of the pages' BlockPool.gather / pickBlocks (state/paged/cache.ts):
  *   out[b][h][t][:] = pool[block_tables[b][t / block_size]][h][t % block_size][:]

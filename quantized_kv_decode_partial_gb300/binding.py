@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -29,6 +29,12 @@ EXPORTS = (
     "pkv_step_destroy",
     "pkv_paged_decode_append_attention",
     "pkv_paged_append",
+    "pkv_make_sparse_plan",
+    "pkv_sparse_plan_for_current_device",
+    "pkv_update_block_bounds",
+    "pkv_select_blocks",
+    "pkv_selected_decode_attention",
+    "pkv_sparse_decode_attention",
     "pkv_paged_gather",
     "pkv_strerror",
     "pkv_last_cuda_error",
@@ -90,6 +96,14 @@ class Plan(ctypes.Structure):
                                                                       ("balanced", ctypes.c_int32)]
 
 
+class SparseParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("top_k", "first_blocks", "last_blocks")]
+
+
+class SparsePlan(ctypes.Structure):
+    _fields_ = [("attention", Plan), ("select_bytes", ctypes.c_size_t), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -138,6 +152,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pkv_paged_append.restype = ctypes.c_int
     lib.pkv_paged_gather.argtypes = [P, I32, I32, I32, I32, P, P, I32, I32, I32, P, P, P]
     lib.pkv_paged_gather.restype = ctypes.c_int
+    LPS = [ctypes.POINTER(PoolLayout), ctypes.POINTER(DecodeParams), ctypes.POINTER(SparseParams)]
+    lib.pkv_make_sparse_plan.argtypes = LPS + [I32, ctypes.POINTER(SparsePlan)]
+    lib.pkv_make_sparse_plan.restype = ctypes.c_int
+    lib.pkv_sparse_plan_for_current_device.argtypes = LPS + [ctypes.POINTER(SparsePlan)]
+    lib.pkv_sparse_plan_for_current_device.restype = ctypes.c_int
+    lib.pkv_update_block_bounds.argtypes = [ctypes.POINTER(PoolLayout), I32, I32, I32, P, P, P, P, P, P, P, P]
+    lib.pkv_update_block_bounds.restype = ctypes.c_int
+    lib.pkv_select_blocks.argtypes = LPS + [P, P, P, P, P, P, P, P, SZ, P, P]
+    lib.pkv_select_blocks.restype = ctypes.c_int
+    lib.pkv_selected_decode_attention.argtypes = LPS + [P, P, P, P, P, P, P, P, P, F, P, P, SZ, P, P]
+    lib.pkv_selected_decode_attention.restype = ctypes.c_int
+    lib.pkv_sparse_decode_attention.argtypes = LPS + [P, P, P, P, P, P, P, P, P, P, F, P, P, P, SZ, P, P]
+    lib.pkv_sparse_decode_attention.restype = ctypes.c_int
     lib.pkv_strerror.argtypes = [ctypes.c_int]
     lib.pkv_strerror.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error.argtypes = []
@@ -448,6 +475,155 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
                                   _ptr(block_tables), _ptr(seq_lens), _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
                                   _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(error_flag), stream)
     _check(rc, lib)
+
+
+def make_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparseParams,
+                     sm_count: Optional[int] = None) -> SparsePlan:
+    """The library's plan of a sparse step (workspace bytes, the attention's own plan)."""
+    lib = load_library()
+    plan = SparsePlan()
+    args = (ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse))
+    if sm_count is None:
+        rc = lib.pkv_sparse_plan_for_current_device(*args, ctypes.byref(plan))
+    else:
+        rc = lib.pkv_make_sparse_plan(*args, sm_count, ctypes.byref(plan))
+    _check(rc, lib)
+    return plan
+
+
+def _cached_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparseParams) -> SparsePlan:
+    key = _plan_key(layout, params) + (sparse.top_k, sparse.first_blocks, sparse.last_blocks)
+    plan = _plan_cache.get(key)
+    if plan is None:
+        plan = make_sparse_plan(layout, params, sparse)
+        if len(_plan_cache) > 1024:
+            _plan_cache.clear()
+        _plan_cache[key] = plan
+    return plan
+
+
+def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                        k_bounds: torch.Tensor, *, n_new: int, bits: int = 16, group_size: int = 64,
+                        k_scales: Optional[torch.Tensor] = None, k_biases: Optional[torch.Tensor] = None,
+                        error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Brings k_bounds bf16 [NB, HK, 2, D] (each block's smallest and largest key, elementwise)
+    up to date after the last n_new rows of every sequence were appended (seq_lens counts
+    them); see include/pkv_decode.h. Returns k_bounds."""
+    lib = load_library()
+    layout = layout_for(k_pool, k_bounds.shape[-1], bits, group_size)
+    if layout.head_dim == 192:  # the values are not looked at; no pages have 192-dim ones
+        layout.v_head_dim = 128
+    B, max_blocks = block_tables.shape
+    with _on_device(k_pool.device):
+        stream = torch.cuda.current_stream(k_pool.device).cuda_stream
+        rc = lib.pkv_update_block_bounds(ctypes.byref(layout), B, max_blocks, n_new, _ptr(k_pool), _ptr(k_scales),
+                                         _ptr(k_biases), _ptr(block_tables), _ptr(seq_lens), _ptr(k_bounds),
+                                         _ptr(error_flag), stream)
+    _check(rc, lib)
+    return k_bounds
+
+
+class BlockSelection(NamedTuple):
+    """Blocks chosen for a step (pkv_select_blocks): ``blocks`` int32 [B, HK, top_k], their places
+    in the sequence; ``tables`` and ``lens``, the form the attention over them reads."""
+
+    blocks: torch.Tensor
+    tables: torch.Tensor
+    lens: torch.Tensor
+
+
+def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, *,
+                  block_size: int, top_k: int, first_blocks: int = 1, last_blocks: int = 1,
+                  out: Optional[BlockSelection] = None, workspace: Optional[torch.Tensor] = None,
+                  error_flag: Optional[torch.Tensor] = None) -> BlockSelection:
+    """Chooses top_k blocks for each (sequence, KV head) of queries q bf16 [B, HQ, N, D] by their
+    bounds (pkv_select_blocks). Depends on the bounds alone, whatever the pages' format."""
+    lib = load_library()
+    B, HQ, N, D = q.shape
+    nb, hk = k_bounds.shape[:2]
+    layout = PoolLayout(nb, hk, block_size, D, 16, 64, 64 if D == 64 else 128)
+    params = DecodeParams(B, HQ, N, block_tables.shape[1])
+    sparse = SparseParams(top_k, first_blocks, last_blocks)
+    with _on_device(q.device):
+        plan = _cached_sparse_plan(layout, params, sparse)
+        if out is None:
+            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=q.device)
+            out = BlockSelection(new(B, hk, top_k), new(B, hk, top_k), new(B, hk))
+        if workspace is None and plan.select_bytes:
+            workspace = torch.empty(plan.select_bytes, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        stream = torch.cuda.current_stream(q.device).cuda_stream
+        rc = lib.pkv_select_blocks(ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q),
+                                   _ptr(k_bounds), _ptr(block_tables), _ptr(seq_lens), _ptr(out.blocks),
+                                   _ptr(out.tables), _ptr(out.lens), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
+    _check(rc, lib)
+    return out
+
+
+def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, selection: BlockSelection,
+                              scale: float, *, bits: int = 16, group_size: int = 64,
+                              k_scales: Optional[torch.Tensor] = None, k_biases: Optional[torch.Tensor] = None,
+                              v_scales: Optional[torch.Tensor] = None, v_biases: Optional[torch.Tensor] = None,
+                              partition_tokens: int = 0, out: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None,
+                              contraction: int = 0, schedule: int = 0) -> torch.Tensor:
+    """Decode attention over chosen blocks (pkv_selected_decode_attention); otherwise as
+    ``paged_decode_attention``."""
+    lib = load_library()
+    B, HQ, N, D = q.shape
+    layout = layout_for(k_pool, D, bits, group_size, v_pool)
+    top_k = selection.tables.shape[-1]
+    params = DecodeParams(B, HQ, N, top_k, partition_tokens, 0, contraction, schedule)
+    last = min(top_k, 1 + -(-(N - 1) // layout.block_size))  # which blocks were taken is settled: any valid numbers
+    sparse = SparseParams(top_k, 0, last)
+    with _on_device(q.device):
+        plan = _cached_sparse_plan(layout, params, sparse)
+        if out is None:
+            out = _out_like(q, layout)
+        if workspace is None and plan.attention.workspace_bytes:
+            workspace = torch.empty(plan.attention.workspace_bytes, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        stream = torch.cuda.current_stream(q.device).cuda_stream
+        rc = lib.pkv_selected_decode_attention(
+            ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q), _ptr(k_pool), _ptr(v_pool),
+            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(selection.tables),
+            _ptr(selection.lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
+    _check(rc, lib)
+    return out
+
+
+def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, k_bounds: torch.Tensor,
+                            block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, *, top_k: int,
+                            first_blocks: int = 1, last_blocks: int = 1, bits: int = 16, group_size: int = 64,
+                            k_scales: Optional[torch.Tensor] = None, k_biases: Optional[torch.Tensor] = None,
+                            v_scales: Optional[torch.Tensor] = None, v_biases: Optional[torch.Tensor] = None,
+                            blocks: Optional[torch.Tensor] = None, partition_tokens: int = 0,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            error_flag: Optional[torch.Tensor] = None, contraction: int = 0,
+                            schedule: int = 0) -> torch.Tensor:
+    """Decode attention over the top_k blocks of each (sequence, KV head) that the bounds k_bounds
+    bf16 [NB, HK, 2, D] score highest for the queries, the first_blocks first and last_blocks
+    last always among them (pkv_sparse_decode_attention). ``blocks`` int32 [B, HK, top_k]
+    receives the choice. Otherwise as ``paged_decode_attention``."""
+    lib = load_library()
+    B, HQ, N, D = q.shape
+    layout = layout_for(k_pool, D, bits, group_size, v_pool)
+    params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, 0, contraction, schedule)
+    sparse = SparseParams(top_k, first_blocks, last_blocks)
+    with _on_device(q.device):
+        plan = _cached_sparse_plan(layout, params, sparse)
+        if out is None:
+            out = _out_like(q, layout)
+        if workspace is None:
+            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+        ws_bytes = workspace.numel() * workspace.element_size()
+        stream = torch.cuda.current_stream(q.device).cuda_stream
+        rc = lib.pkv_sparse_decode_attention(
+            ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q), _ptr(k_pool), _ptr(v_pool),
+            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(k_bounds), _ptr(block_tables),
+            _ptr(seq_lens), float(scale), _ptr(blocks), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
+    _check(rc, lib)
+    return out
 
 
 def paged_gather(pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_len: int,

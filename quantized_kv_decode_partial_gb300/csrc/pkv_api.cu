@@ -967,6 +967,253 @@ int pkv_paged_gather(const void* pool, int32_t num_blocks, int32_t num_kv_heads,
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Sparse decode attention over chosen blocks (pkv_sparse.cu)
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_sparse(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S) {
+  int rc = check_layout(L);
+  if (rc) return rc;
+  rc = check_params(L, P);
+  if (rc) return rc;
+  if (!S) return PKV_ERR_NULL_POINTER;
+  if (P->window != 0) return PKV_ERR_BAD_PARAMS;
+  if (S->top_k < 1 || S->first_blocks < 0 || S->last_blocks < 1 ||
+      static_cast<long long>(S->first_blocks) + S->last_blocks > S->top_k ||
+      static_cast<long long>(S->top_k) * L->block_size >= (1ll << 31))
+    return PKV_ERR_BAD_PARAMS;
+  // the n_query newest rows lie in the last blocks, however full the last one is
+  if (static_cast<long long>(S->last_blocks - 1) * L->block_size < P->n_query - 1) return PKV_ERR_BAD_PARAMS;
+  if (static_cast<long long>(P->num_seqs) * L->num_kv_heads > 65535) return PKV_ERR_BAD_PARAMS;
+  return PKV_OK;
+}
+
+// The decode over chosen blocks: the pool as NB * HK blocks of one KV head, every (sequence,
+// KV head) a sequence of at most top_k of them.
+void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S,
+                 pkv_pool_layout* vl, pkv_decode_params* vp) {
+  *vl = *L;
+  vl->num_blocks = L->num_blocks * L->num_kv_heads;
+  vl->num_kv_heads = 1;
+  *vp = *P;
+  vp->num_seqs = P->num_seqs * L->num_kv_heads;
+  vp->num_q_heads = P->num_q_heads / L->num_kv_heads;
+  vp->max_blocks_per_seq = S->top_k;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Offsets into the workspace of the choice (scores, tile magnitudes, f64 keys) and, after
+// it, of a whole sparse step (chosen tables and lengths, then the attention's workspace).
+struct SparseWorkspace {
+  size_t tile_abs, keys64, select_bytes, tables, lens, attention;
+};
+SparseWorkspace sparse_workspace(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S) {
+  const size_t units = static_cast<size_t>(P->num_seqs) * L->num_kv_heads;
+  const size_t cells = P->max_blocks_per_seq > S->top_k ? units * P->max_blocks_per_seq : 0;
+  SparseWorkspace w;
+  w.tile_abs = round256(cells * sizeof(float));
+  w.keys64 = w.tile_abs + (cells ? round256(units * pkv::select_tiles(P->max_blocks_per_seq) * sizeof(float)) : 0);
+  w.select_bytes = w.keys64 + round256(cells * sizeof(unsigned long long));
+  w.tables = w.select_bytes;
+  w.lens = w.tables + round256(units * S->top_k * sizeof(int32_t));
+  w.attention = w.lens + round256(units * sizeof(int32_t));
+  return w;
+}
+
+int sparse_plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S, int sm_count,
+                     pkv_sparse_plan* out) {
+  pkv_pool_layout vl;
+  pkv_decode_params vp;
+  chosen_view(L, P, S, &vl, &vp);
+  int rc = check_params(&vl, &vp);
+  if (rc) return rc;
+  rc = plan_impl(&vl, &vp, sm_count, &out->attention);
+  if (rc) return rc;
+  const SparseWorkspace w = sparse_workspace(L, P, S);
+  out->select_bytes = w.select_bytes;
+  out->workspace_bytes = w.attention + out->attention.workspace_bytes;
+  return PKV_OK;
+}
+
+// Fills the parameters of the choice; its workspace is `workspace` (select_bytes).
+pkv::SelectParams select_params(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S,
+                                const void* q, const void* k_bounds, const int32_t* block_tables,
+                                const int32_t* seq_lens, int32_t* blocks, int32_t* tables, int32_t* lens,
+                                void* workspace, int32_t* error_flag) {
+  const SparseWorkspace w = sparse_workspace(L, P, S);
+  char* const ws = static_cast<char*>(workspace);
+  pkv::SelectParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_bounds = static_cast<const __nv_bfloat16*>(k_bounds);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.scores = reinterpret_cast<float*>(ws);
+  p.tile_abs = reinterpret_cast<float*>(ws + w.tile_abs);
+  p.keys64 = reinterpret_cast<unsigned long long*>(ws + w.keys64);
+  p.out_blocks = blocks;
+  p.out_tables = tables;
+  p.out_lens = lens;
+  p.error_flag = error_flag;
+  p.num_blocks = L->num_blocks;
+  p.num_kv_heads = L->num_kv_heads;
+  p.block_size = L->block_size;
+  p.max_blocks = P->max_blocks_per_seq;
+  p.n_query = P->n_query;
+  p.nq = P->num_q_heads / L->num_kv_heads * P->n_query;
+  p.head_dim = L->head_dim;
+  p.top_k = S->top_k;
+  p.first = S->first_blocks;
+  p.last = S->last_blocks;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_make_sparse_plan(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                         const pkv_sparse_params* sparse, int32_t sm_count, pkv_sparse_plan* plan) {
+  if (!plan) return PKV_ERR_NULL_POINTER;
+  int rc = check_sparse(layout, params, sparse);
+  if (rc) return rc;
+  if (sm_count <= 0) return PKV_ERR_BAD_PARAMS;
+  return sparse_plan_impl(layout, params, sparse, sm_count, plan);
+}
+
+int pkv_sparse_plan_for_current_device(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                       const pkv_sparse_params* sparse, pkv_sparse_plan* plan) {
+  if (!plan) return PKV_ERR_NULL_POINTER;
+  int rc = check_sparse(layout, params, sparse);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  return sparse_plan_impl(layout, params, sparse, sms, plan);
+}
+
+int pkv_update_block_bounds(const pkv_pool_layout* layout, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t n_new,
+                            const void* k_pool, const void* k_scales, const void* k_biases,
+                            const int32_t* block_tables, const int32_t* seq_lens, void* k_bounds,
+                            int32_t* error_flag, void* stream) {
+  int rc = check_layout(layout);
+  if (rc) return rc;
+  if (num_seqs <= 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || n_new < 0) return PKV_ERR_BAD_PARAMS;
+  const long long max_len = static_cast<long long>(max_blocks_per_seq) * layout->block_size;
+  if (max_len >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  if (!k_pool || !block_tables || !seq_lens || !k_bounds) return PKV_ERR_NULL_POINTER;
+  const void* const biases = block_scaled(layout) ? nullptr : k_biases;
+  if (!scale_planes_given(layout, k_scales, biases, k_scales, biases)) return PKV_ERR_NULL_POINTER;
+  if (!aligned(k_pool, 16) || !aligned(k_bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(error_flag, 4) || !scale_planes_aligned(layout, k_scales, biases, k_scales, biases, 4))
+    return PKV_ERR_MISALIGNED;
+  if (n_new == 0) return PKV_OK;
+  pkv::BoundsParams p{};
+  p.k_pool = k_pool;
+  if (block_scaled(layout)) {
+    p.k_block_scales = static_cast<const float*>(k_scales);
+  } else {
+    p.k_scales = static_cast<const __nv_bfloat16*>(k_scales);
+    p.k_biases = static_cast<const __nv_bfloat16*>(k_biases);
+  }
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.k_bounds = static_cast<__nv_bfloat16*>(k_bounds);
+  p.error_flag = error_flag;
+  p.num_blocks = layout->num_blocks;
+  p.num_kv_heads = layout->num_kv_heads;
+  p.block_size = layout->block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.n_new = static_cast<int>(std::min<long long>(n_new, max_len));
+  p.blocks = std::min((layout->block_size - 2 + p.n_new) / layout->block_size + 1, max_blocks_per_seq);
+  if (static_cast<long long>(p.blocks) * layout->num_kv_heads >= (1ll << 31) - 4) return PKV_ERR_BAD_PARAMS;
+  (void)cudaGetLastError();
+  cudaError_t e = pkv::launch_bounds(p, format_of(layout), layout->head_dim, num_seqs,
+                                     static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("bounds kernel launch", e);
+  return PKV_OK;
+}
+
+int pkv_select_blocks(const pkv_pool_layout* layout, const pkv_decode_params* params, const pkv_sparse_params* sparse,
+                      const void* q, const void* k_bounds, const int32_t* block_tables, const int32_t* seq_lens,
+                      int32_t* blocks, int32_t* chosen_tables, int32_t* chosen_lens, void* workspace,
+                      size_t workspace_bytes, int32_t* error_flag, void* stream) {
+  int rc = check_sparse(layout, params, sparse);
+  if (rc) return rc;
+  if (!q || !k_bounds || !block_tables || !seq_lens || !chosen_tables || !chosen_lens) return PKV_ERR_NULL_POINTER;
+  if (!aligned(q, 16) || !aligned(k_bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(blocks, 4) || !aligned(chosen_tables, 4) || !aligned(chosen_lens, 4) || !aligned(workspace, 16) ||
+      !aligned(error_flag, 4))
+    return PKV_ERR_MISALIGNED;
+  const size_t need = sparse_workspace(layout, params, sparse).select_bytes;
+  if (need && (!workspace || workspace_bytes < need)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  (void)cudaGetLastError();
+  cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
+                                                   chosen_tables, chosen_lens, workspace, error_flag),
+                                     params->num_seqs, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("block choice launch", e);
+  return PKV_OK;
+}
+
+int pkv_selected_decode_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                  const pkv_sparse_params* sparse, const void* q, const void* k_pool,
+                                  const void* v_pool, const void* k_scales, const void* k_biases,
+                                  const void* v_scales, const void* v_biases, const int32_t* chosen_tables,
+                                  const int32_t* chosen_lens, float scale, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* error_flag, void* stream) {
+  int rc = check_sparse(layout, params, sparse);
+  if (rc) return rc;
+  pkv_pool_layout vl;
+  pkv_decode_params vp;
+  chosen_view(layout, params, sparse, &vl, &vp);
+  return enqueue_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, chosen_tables,
+                        chosen_lens, scale, out, workspace, workspace_bytes, error_flag, stream,
+                        kPassPartial | kPassMerge);
+}
+
+int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
+                                const pkv_sparse_params* sparse, const void* q, const void* k_pool,
+                                const void* v_pool, const void* k_scales, const void* k_biases, const void* v_scales,
+                                const void* v_biases, const void* k_bounds, const int32_t* block_tables,
+                                const int32_t* seq_lens, float scale, int32_t* blocks, void* out, void* workspace,
+                                size_t workspace_bytes, int32_t* error_flag, void* stream) {
+  int rc = check_sparse(layout, params, sparse);
+  if (rc) return rc;
+  if (!k_bounds || !block_tables || !seq_lens) return PKV_ERR_NULL_POINTER;
+  if (!aligned(k_bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(blocks, 4))
+    return PKV_ERR_MISALIGNED;
+  const SparseWorkspace w = sparse_workspace(layout, params, sparse);
+  if (!workspace || workspace_bytes < w.attention) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 16)) return PKV_ERR_MISALIGNED;
+  char* const ws = static_cast<char*>(workspace);
+  int32_t* const tables = reinterpret_cast<int32_t*>(ws + w.tables);
+  int32_t* const lens = reinterpret_cast<int32_t*>(ws + w.lens);
+  pkv_pool_layout vl;
+  pkv_decode_params vp;
+  chosen_view(layout, params, sparse, &vl, &vp);
+  PreparedDecode pd;  // every argument is checked before the first launch
+  rc = prepare_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, tables, lens, scale, out,
+                      ws + w.attention, workspace_bytes - w.attention, error_flag, kPassPartial | kPassMerge, nullptr,
+                      nullptr, &pd);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
+                                                   tables, lens, workspace, error_flag),
+                                     params->num_seqs, sms, st);
+  if (e != cudaSuccess) return cuda_fail("block choice launch", e);
+  return launch_prepared(pd, st);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // The entry point that allocates nothing (pkv_paged_decode_attention_no_alloc)
 // ---------------------------------------------------------------------------
 namespace {
@@ -1105,6 +1352,6 @@ uint64_t pkv_set_wait_limit_ns(uint64_t ns) {
   return g_wait_limit_ns.exchange(ns == 0 ? pkv::kWaitLimitNs : ns, std::memory_order_relaxed);
 }
 
-int pkv_version(void) { return 200; }
+int pkv_version(void) { return 300; }
 
 }  // extern "C"

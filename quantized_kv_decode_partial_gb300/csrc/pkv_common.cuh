@@ -126,6 +126,38 @@ struct AppendBlockParams {
   int num_blocks, num_kv_heads, block_size, max_blocks, n_new;
 };
 
+// Upkeep of the block bounds (pkv_sparse.cu).
+struct BoundsParams {
+  const void* k_pool;
+  const __nv_bfloat16* k_scales;  // affine pages
+  const __nv_bfloat16* k_biases;
+  const float* k_block_scales;    // e4m3 pages
+  const int32_t* block_tables;
+  const int32_t* seq_lens;        // rows held, the n_new new ones included
+  __nv_bfloat16* k_bounds;        // [NB, HK, 2, D]
+  int32_t* error_flag;
+  int num_blocks, num_kv_heads, block_size, max_blocks, n_new;
+  int blocks;                     // blocks the last n_new rows of a sequence can touch
+};
+
+// Scores and choice of blocks (pkv_sparse.cu); a unit is a (sequence, KV head).
+struct SelectParams {
+  const __nv_bfloat16* q;         // [units, nq, D]
+  const __nv_bfloat16* k_bounds;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  float* scores;                  // [units, max_blocks]
+  float* tile_abs;                // [units, tiles]: largest magnitude of 16 blocks' bounds
+  unsigned long long* keys64;     // [units, max_blocks]: f64 scores of ambiguous blocks, as ordered integers
+  int32_t* out_blocks;            // [units, top_k], optional
+  int32_t* out_tables;            // [units, top_k]
+  int32_t* out_lens;              // [units]
+  int32_t* error_flag;
+  int num_blocks, num_kv_heads, block_size, max_blocks;
+  int n_query, nq, head_dim, top_k, first, last;
+  int tiles, tiles_per_warp;      // set by launch_select
+};
+
 struct GatherParams {
   const uint8_t* pool;
   const int32_t* block_tables;

@@ -1,0 +1,707 @@
+// Sparse decode attention over a paged cache: which blocks of each (sequence, KV head) a
+// step reads.
+//
+// Each (block, KV head) carries the bounds of its stored keys, k_bounds [NB, HK, 2, D]: the
+// elementwise smallest (row 0) and largest (row 1) value, rounded outward to bf16. For a
+// query row q no key of block j scores above
+//     u_j(q) = sum_d max(q_d lo_jd, q_d hi_jd) = <max(q, 0), hi_j> + <min(q, 0), lo_j>
+// and the block's score for a KV head is the largest u_j over its query rows. The step then
+// attends over `first` blocks at the start, `last` at the end and the best-scored others,
+// top_k in all, through the decode kernels: the pool seen as NB * HK blocks of one head, and
+// every (sequence, KV head) as a sequence of its chosen blocks in order.
+//
+// Three kernels: the bounds' upkeep after an append, the scores, and the choice.
+#include "pkv_launch.h"
+
+namespace pkv {
+
+namespace {
+
+// ------------------------------------------------------------------------------ bounds' upkeep
+// One warp per (sequence, touched block, KV head). A lane holds the same 16 bytes of every
+// kRowsPerPass-th row, so each pass is one coalesced 16-byte load per lane, and keeps the
+// running bounds of its dims in registers. Bound by HBM for bf16 and e4m3 pages (packed
+// min/max, 2 values per instruction); affine codes cost an FMA, a minimum and a maximum per
+// value, which 4-bit pages are bound by.
+template <int FMT, int D>
+struct BoundsCfg {
+  static constexpr int kBits = FMT == kFmtE4m3 ? 8 : FMT;
+  static constexpr int kRowBytes = D * kBits / 8;
+  static constexpr int kLanes = kRowBytes / 16;        // lanes per row
+  static constexpr int kRowsPerPass = 32 / kLanes;     // rows per warp-wide load
+  static constexpr int kVals = 128 / kBits;            // values per lane
+  static constexpr bool kAffine = FMT == 4 || FMT == 8;
+  static constexpr int kUnroll = kAffine ? 4 : 8;      // loads in flight per lane
+};
+
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(128) pkv_bounds_kernel(const __grid_constant__ BoundsParams p) {
+  using C = BoundsCfg<FMT, D>;
+  wait_for_prerequisite_grids();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const int unit = blockIdx.x * 4 + warp;
+  if (unit >= p.blocks * p.num_kv_heads) return;
+  const int t = unit / p.num_kv_heads, h = unit - t * p.num_kv_heads;
+  const int len = p.seq_lens[b];
+  if (len < 0 || static_cast<long long>(len) > static_cast<long long>(p.max_blocks) * p.block_size) {
+    if (lane == 0 && unit == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadSeqLen);
+    return;
+  }
+  const int begin = len > p.n_new ? len - p.n_new : 0;
+  const int blk = begin / p.block_size + t;
+  const long long row0 = static_cast<long long>(blk) * p.block_size;
+  if (row0 >= len) return;
+  const int phys = p.block_tables[static_cast<size_t>(b) * p.max_blocks + blk];
+  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+    if (lane == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+    return;
+  }
+  // rows [r0, r1) of the block are new; earlier ones are in the stored bounds already, but
+  // for e4m3 pages, whose scale may have grown with the new rows: those are taken whole
+  const int r1 = static_cast<int>(min(len - row0, static_cast<long long>(p.block_size)));
+  const bool held = row0 < begin && FMT != kFmtE4m3;
+  const int r0 = held ? static_cast<int>(begin - row0) : 0;
+  const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + h;
+  const int sub = lane / C::kLanes, col = lane % C::kLanes;  // row within a pass, 16-byte column
+  const bool on = sub < C::kRowsPerPass;
+  const char* base = static_cast<const char*>(p.k_pool) + (cell * p.block_size) * C::kRowBytes + col * 16;
+
+  // this lane's dims: [col * kVals, col * kVals + kVals)
+  constexpr int kWords = C::kAffine ? C::kVals : C::kVals / 2;  // f32 values, or 16-bit pairs
+  uint32_t lo[kWords], hi[kWords];
+  constexpr uint32_t kInf = C::kAffine ? 0x7F800000u : FMT == 16 ? 0x7F807F80u : 0x7C007C00u;
+  constexpr uint32_t kNegInf = C::kAffine ? 0xFF800000u : FMT == 16 ? 0xFF80FF80u : 0xFC00FC00u;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    lo[i] = kInf;
+    hi[i] = kNegInf;
+  }
+  for (int r = r0; r < r1; r += C::kRowsPerPass * C::kUnroll) {
+    uint4 v[C::kUnroll];
+    float sc[C::kUnroll], bi[C::kUnroll];
+#pragma unroll
+    for (int u = 0; u < C::kUnroll; ++u) {
+      const int row = r + u * C::kRowsPerPass + sub;
+      const bool in = on && row < r1;
+      // a row past the end repeats the first one, which changes no bound
+      const int rr = in ? row : r0;
+      v[u] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(rr) * C::kRowBytes);
+      if constexpr (C::kAffine) {
+        const size_t g = (cell * p.block_size + rr) * (D / 64) + col * C::kVals / 64;
+        sc[u] = __bfloat162float(p.k_scales[g]);
+        bi[u] = __bfloat162float(p.k_biases[g]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < C::kUnroll; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (FMT == 16) {
+          lo[k] = min_bf16x2(lo[k], w[k]);
+          hi[k] = max_bf16x2(hi[k], w[k]);
+        } else if constexpr (FMT == kFmtE4m3) {
+          uint32_t a, c;
+          e4m3x4_to_f16x2(w[k], a, c);
+          lo[2 * k] = min_f16x2(lo[2 * k], a);
+          hi[2 * k] = max_f16x2(hi[2 * k], a);
+          lo[2 * k + 1] = min_f16x2(lo[2 * k + 1], c);
+          hi[2 * k + 1] = max_f16x2(hi[2 * k + 1], c);
+        } else {
+          constexpr int kPer = 32 / FMT;  // codes per word
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            // scale * code is exact in f32 (8 by 8 bits), so this rounds once
+            const float x = fmaf(sc[u], static_cast<float>((w[k] >> (FMT * j)) & ((1u << FMT) - 1u)), bi[u]);
+            const int i = k * kPer + j;
+            lo[i] = __float_as_uint(fminf(__uint_as_float(lo[i]), x));
+            hi[i] = __float_as_uint(fmaxf(__uint_as_float(hi[i]), x));
+          }
+        }
+      }
+    }
+  }
+  // the row groups of the pass, into the first
+  auto merge = [&](int i, uint32_t l, uint32_t m) {
+    if constexpr (FMT == 16) {
+      lo[i] = min_bf16x2(lo[i], l);
+      hi[i] = max_bf16x2(hi[i], m);
+    } else if constexpr (FMT == kFmtE4m3) {
+      lo[i] = min_f16x2(lo[i], l);
+      hi[i] = max_f16x2(hi[i], m);
+    } else {
+      lo[i] = __float_as_uint(fminf(__uint_as_float(lo[i]), __uint_as_float(l)));
+      hi[i] = __float_as_uint(fmaxf(__uint_as_float(hi[i]), __uint_as_float(m)));
+    }
+  };
+  if constexpr ((C::kLanes & (C::kLanes - 1)) == 0) {
+#pragma unroll
+    for (int d = C::kLanes; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        merge(i, __shfl_xor_sync(0xffffffffu, lo[i], d), __shfl_xor_sync(0xffffffffu, hi[i], d));
+  } else {
+#pragma unroll
+    for (int s = 1; s < C::kRowsPerPass; ++s)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        merge(i, __shfl_down_sync(0xffffffffu, lo[i], s * C::kLanes), __shfl_down_sync(0xffffffffu, hi[i], s * C::kLanes));
+  }
+  if (lane >= C::kLanes) return;
+  // 2 rows of D bf16: the lane's kVals values of each
+  uint32_t* const out_lo = reinterpret_cast<uint32_t*>(p.k_bounds + cell * 2 * D + col * C::kVals);
+  uint32_t* const out_hi = out_lo + D / 2;
+  const float scale = FMT == kFmtE4m3 ? p.k_block_scales[cell] : 1.f;
+#pragma unroll
+  for (int q = 0; q < C::kVals / 8; ++q) {  // 8 values, one 16-byte store, at a time
+    uint32_t l4[4], h4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (FMT == 16) {
+        l4[i] = lo[4 * q + i];
+        h4[i] = hi[4 * q + i];
+      } else {
+        float2 a, c;
+        if constexpr (FMT == kFmtE4m3) {
+          a = __half22float2(*reinterpret_cast<__half2*>(&lo[4 * q + i]));
+          c = __half22float2(*reinterpret_cast<__half2*>(&hi[4 * q + i]));
+          a = make_float2(a.x * scale, a.y * scale);
+          c = make_float2(c.x * scale, c.y * scale);
+        } else {
+          a = make_float2(__uint_as_float(lo[8 * q + 2 * i]), __uint_as_float(lo[8 * q + 2 * i + 1]));
+          c = make_float2(__uint_as_float(hi[8 * q + 2 * i]), __uint_as_float(hi[8 * q + 2 * i + 1]));
+        }
+        const __nv_bfloat162 l = __halves2bfloat162(__float2bfloat16_rd(a.x), __float2bfloat16_rd(a.y));
+        const __nv_bfloat162 m = __halves2bfloat162(__float2bfloat16_ru(c.x), __float2bfloat16_ru(c.y));
+        l4[i] = *reinterpret_cast<const uint32_t*>(&l);
+        h4[i] = *reinterpret_cast<const uint32_t*>(&m);
+      }
+    }
+    if (held) {
+      const uint4 l = reinterpret_cast<const uint4*>(out_lo)[q], m = reinterpret_cast<const uint4*>(out_hi)[q];
+      const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, mw[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        l4[i] = min_bf16x2(l4[i], lw[i]);
+        h4[i] = max_bf16x2(h4[i], mw[i]);
+      }
+    }
+    reinterpret_cast<uint4*>(out_lo)[q] = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+    reinterpret_cast<uint4*>(out_hi)[q] = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+  }
+}
+
+template <int FMT, int D>
+cudaError_t launch_bounds_of(const BoundsParams& p, int num_seqs, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((p.blocks * p.num_kv_heads + 3) / 4, num_seqs);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pkv_bounds_kernel<FMT, D>, p);
+}
+
+// -------------------------------------------------------------------------------------- scores
+// A warp scores 16 blocks at a time against all query rows of its KV head (up to 64) with
+// m16n8k16 MMAs: blocks on M, query rows on N, and the products of the two bounds summed
+// over 2 D. The order of the dims within the contraction is free, so the A fragments are the
+// 16-byte loads themselves (each lane 8 dims of two blocks per load, four lanes a 64-byte
+// run) and no bound passes through shared memory; the B fragment of the same dims is 16
+// bytes of a query row. Bound by HBM: 4 D bytes per (block, KV head).
+constexpr int kScoreWarps = 4;
+constexpr int kScoreTile = 16;  // blocks per warp and step
+
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kSteps = D / 32;           // 16-byte loads per bound row and lane
+  constexpr int kStride = D * 2 + 64;      // bytes of a staged query row, padded: rows g, g + 1 meet in no bank
+  extern __shared__ __align__(16) uint8_t sq[];
+  wait_for_prerequisite_grids();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const size_t unit = static_cast<size_t>(b) * p.num_kv_heads + h;
+  const int len = p.seq_lens[b];
+  if (len < p.n_query || len > p.max_blocks * p.block_size) return;  // the choice flags it
+  const int n = (len + p.block_size - 1) / p.block_size;
+  const int cta_tile = blockIdx.x * kScoreWarps * p.tiles_per_warp;
+  if (n <= p.top_k || cta_tile * kScoreTile >= n) return;  // every block is taken, or none is here
+  const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  const int ntiles = (p.nq + 7) / 8;  // tiles of 8 query rows
+
+  for (int it = 0; it < p.tiles_per_warp; ++it) {
+    const int tile = cta_tile + it * kScoreWarps + warp;  // warp-uniform
+    const int j0 = tile * kScoreTile;
+    const bool live = j0 < n;
+    uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
+    int ph0 = -1, ph1 = -1;
+    if (live) {
+      const bool in = lane < kScoreTile && j0 + lane < n;
+      const int ph = in ? table[j0 + lane] : -1;
+      const bool ok = static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks);
+      if (in && !ok && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+      ph0 = __shfl_sync(0xffffffffu, ok ? ph : -1, g);
+      ph1 = __shfl_sync(0xffffffffu, ok ? ph : -1, g + 8);
+      const __nv_bfloat16* r0 = p.k_bounds + (static_cast<size_t>(ph0 < 0 ? 0 : ph0) * p.num_kv_heads + h) * 2 * D + 8 * t;
+      const __nv_bfloat16* r1 = p.k_bounds + (static_cast<size_t>(ph1 < 0 ? 0 : ph1) * p.num_kv_heads + h) * 2 * D + 8 * t;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        lo0[i] = ph0 >= 0 ? ld_nc_keep_v4(r0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        hi0[i] = ph0 >= 0 ? ld_nc_keep_v4(r0 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        lo1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        hi1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    if (it == 0) {  // the query rows, staged while the first bounds are in flight
+      const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
+      for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += kScoreWarps * 32) {
+        const int r = i / (D / 8), c = i - r * (D / 8);
+        *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncthreads();
+    }
+    if (!live) continue;
+    // the largest magnitude of the tile's bounds: what the choice's error bound needs
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const uint4 w[4] = {lo0[i], hi0[i], lo1[i], hi1[i]};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m = max_bf16x2(m, w[k].x & 0x7FFF7FFFu);
+        m = max_bf16x2(m, w[k].y & 0x7FFF7FFFu);
+        m = max_bf16x2(m, w[k].z & 0x7FFF7FFFu);
+        m = max_bf16x2(m, w[k].w & 0x7FFF7FFFu);
+      }
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0) p.tile_abs[unit * p.tiles + tile] = __uint_as_float(m << 16);
+
+    float best0 = -INFINITY, best1 = -INFINITY;  // blocks j0 + g and j0 + g + 8
+    for (int nt = 0; nt < ntiles; ++nt) {
+      float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(sq + (8 * nt + g) * kStride + (32 * i + 8 * t) * 2);
+        mma_bf16(up, hi0[i].x, hi1[i].x, hi0[i].y, hi1[i].y, max_bf16x2(q.x, 0u), max_bf16x2(q.y, 0u));
+        mma_bf16(dn, lo0[i].x, lo1[i].x, lo0[i].y, lo1[i].y, min_bf16x2(q.x, 0u), min_bf16x2(q.y, 0u));
+        mma_bf16(up, hi0[i].z, hi1[i].z, hi0[i].w, hi1[i].w, max_bf16x2(q.z, 0u), max_bf16x2(q.w, 0u));
+        mma_bf16(dn, lo0[i].z, lo1[i].z, lo0[i].w, lo1[i].w, min_bf16x2(q.z, 0u), min_bf16x2(q.w, 0u));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (8 * nt + 2 * t + e < p.nq) {
+          best0 = fmaxf(best0, up[e] + dn[e]);
+          best1 = fmaxf(best1, up[e + 2] + dn[e + 2]);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, d));
+      best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, d));
+    }
+    if (t == 0) {
+      float* s = p.scores + unit * p.max_blocks + j0;
+      if (j0 + g < n) s[g] = ph0 >= 0 ? best0 : -INFINITY;
+      if (j0 + g + 8 < n) s[g + 8] = ph1 >= 0 ? best1 : -INFINITY;
+    }
+  }
+  allow_dependent_launch();
+}
+
+// -------------------------------------------------------------------------------------- choice
+// One CTA per (sequence, KV head). The blocks taken are those that exact sums would take,
+// ties to the lower block: f32 scores decide all but the few within their error bound E of
+// the last place, and those are summed again in f64 (products of bf16 values are exact
+// there, and so is nearly every sum of up to 256 of them).
+//
+// With T the k-th largest of the candidates' f32 scores and |f32 - exact| <= E: a score
+// above T + 2E is in (at most k - 1 scores lie above T, and a block below T cannot overtake
+// it), one below T - 2E is out, the rest is ambiguous. E = D 2^-23 |q|_1 max|bound|: at most
+// D / 8 MMA steps and a final sum per score, each off by under 2^-20 of the sum of the
+// products' magnitudes.
+//
+// T comes from histograms of 2048 equal bins over [lowest, highest] key, narrowed to the bin
+// that holds the k-th until it is one value (two rounds as a rule): spread scores meet few
+// bank conflicts, which radix digits of nearby floats would.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectBins = 2048;
+constexpr int kSelectKeys = 8192;  // scores kept in shared memory; more are read again from L2
+
+__device__ __forceinline__ uint32_t order_key(float s) {  // NaN lowest, then by value
+  if (!(s == s)) return 0u;
+  const uint32_t u = __float_as_uint(s + 0.f);  // -0 as 0
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t k) {
+  if (k == 0u) return -INFINITY;
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ unsigned long long order_key(double s) {
+  if (!(s == s)) return 0ull;
+  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s + 0.0));
+  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+
+struct SelectShared {
+  uint32_t keys[kSelectKeys];
+  alignas(8) int hist[kSelectBins];
+  unsigned long long red[kSelectThreads / 32];
+  unsigned long long found;
+  int bin, above, in_bin;
+};
+
+// Sum over the block of a pair of counts packed as two 32-bit halves; every thread gets it.
+__device__ __forceinline__ unsigned long long block_sum(SelectShared& sh, unsigned long long v) {
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();  // red is free
+  if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  unsigned long long s = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w) s += sh.red[w];
+  return s;
+}
+
+// Exclusive prefix over the block, in thread order, of such a pair.
+__device__ __forceinline__ unsigned long long block_prefix(SelectShared& sh, unsigned long long v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  __syncthreads();  // red is free
+  if (lane == 31) sh.red[warp] = incl;
+  __syncthreads();
+  unsigned long long s = incl - v;
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w)
+    if (w < warp) s += sh.red[w];
+  return s;
+}
+
+// The need-th largest (need >= 1) of the keys in [lo, hi] that key_of(i, &key) yields for i
+// in [0, n); `need` becomes its rank among the keys equal to it. Every thread gets it.
+template <typename Key, typename F>
+__device__ __forceinline__ Key nth_largest(SelectShared& sh, F key_of, int n, int& need, Key lo, Key hi) {
+  for (;;) {
+    const Key span = hi - lo;
+    const int width = sizeof(Key) == 8 ? 64 - __clzll(static_cast<long long>(span)) : 32 - __clz(static_cast<int>(span));
+    const int shift = width > 11 ? width - 11 : 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) sh.hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+      Key k;
+      if (key_of(i, k) && k >= lo && k <= hi) atomicAdd(&sh.hist[static_cast<int>((k - lo) >> shift)], 1);
+    }
+    __syncthreads();
+    // bins from the top, four per thread
+    constexpr int kPer = kSelectBins / kSelectThreads;
+    const int top = kSelectBins - 1 - kPer * threadIdx.x;
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sum += sh.hist[top - j];
+    int above = static_cast<int>(block_prefix(sh, static_cast<unsigned long long>(sum)));
+    if (above < need && above + sum >= need) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int c = sh.hist[top - j];
+        if (above < need && above + c >= need) {
+          sh.bin = top - j;
+          sh.above = above;
+          sh.in_bin = c;
+        }
+        above += c;
+      }
+    }
+    __syncthreads();
+    need -= sh.above;
+    lo += static_cast<Key>(sh.bin) << shift;
+    if (shift == 0) return lo;
+    const Key end = lo + ((static_cast<Key>(1) << shift) - 1);
+    hi = end < hi ? end : hi;
+    if (sh.in_bin == 1) {  // alone in its bin
+      for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+        Key k;
+        if (key_of(i, k) && k >= lo && k <= hi) sh.found = static_cast<unsigned long long>(k);
+      }
+      __syncthreads();
+      return static_cast<Key>(sh.found);
+    }
+  }
+}
+
+// A block's score in f64: the largest u_j over the query rows, by one warp.
+__device__ __forceinline__ double exact_score(const __nv_bfloat16* q, int nq, const __nv_bfloat16* bounds, int D,
+                                              int lane) {
+  double best = -INFINITY;
+  for (int r = 0; r < nq; ++r) {
+    double s = 0.0;
+    for (int d = lane; d < D; d += 32) {
+      const double x = __bfloat162float(q[static_cast<size_t>(r) * D + d]);
+      s += fmax(x * __bfloat162float(bounds[d]), x * __bfloat162float(bounds[D + d]));
+    }
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    best = s > best || !(s == s) ? s : best;
+  }
+  return best;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelectShared sh;
+  wait_for_prerequisite_grids();
+  const int unit = blockIdx.x, b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = p.seq_lens[b];
+  int32_t* const out_blocks = p.out_blocks ? p.out_blocks + static_cast<size_t>(unit) * p.top_k : nullptr;
+  int32_t* const out_table = p.out_tables + static_cast<size_t>(unit) * p.top_k;
+  const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  const bool bad = len < p.n_query || len > p.max_blocks * p.block_size;
+  const int n = bad ? 0 : (len + p.block_size - 1) / p.block_size;
+  const int taken = n < p.top_k ? n : p.top_k;
+  if (threadIdx.x == 0) {
+    p.out_lens[unit] = bad ? 0 : (taken - 1) * p.block_size + (len - (n - 1) * p.block_size);
+    if (bad && p.error_flag) atomicOr(p.error_flag, kDevErrBadSeqLen);
+  }
+  auto put = [&](int pos, int j) {  // block j at place pos of the choice
+    const int ph = j < 0 ? -1 : table[j];
+    const bool ok = static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks);
+    if (out_blocks) out_blocks[pos] = j;
+    out_table[pos] = ok ? ph * p.num_kv_heads + h : -1;
+    if (j >= 0 && !ok && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+  };
+  for (int i = taken + threadIdx.x; i < p.top_k; i += kSelectThreads) put(i, -1);
+  if (n <= p.top_k) {
+    for (int j = threadIdx.x; j < n; j += kSelectThreads) put(j, j);
+    return;
+  }
+  // candidates: blocks c0 .. c0 + count - 1, k of which are taken
+  const int c0 = p.first, count = n - p.first - p.last, k = p.top_k - p.first - p.last;
+  const float* scores = p.scores + static_cast<size_t>(unit) * p.max_blocks + c0;
+  unsigned long long* const keys64 = p.keys64 + static_cast<size_t>(unit) * p.max_blocks + c0;
+  const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
+  const bool staged = count <= kSelectKeys;
+
+  // keys and their range; the query's largest 1-norm and the bounds' largest magnitude
+  uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+  for (int i = threadIdx.x; i < count; i += kSelectThreads) {
+    const uint32_t key = order_key(scores[i]);
+    if (staged) sh.keys[i] = key;
+    kmin = min(kmin, key);
+    kmax = max(kmax, key);
+  }
+  float mag = 0.f;
+  for (int i = threadIdx.x; i < (n + kScoreTile - 1) / kScoreTile; i += kSelectThreads)
+    mag = fmaxf(mag, p.tile_abs[static_cast<size_t>(unit) * p.tiles + i]);
+  float q1 = 0.f;
+  for (int r = warp; r < p.nq; r += kSelectThreads / 32) {
+    float s = 0.f;
+    for (int d = lane; d < p.head_dim; d += 32) s += fabsf(__bfloat162float(q[static_cast<size_t>(r) * p.head_dim + d]));
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    q1 = fmaxf(q1, s);
+  }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  const uint32_t mag_u = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
+  {
+    uint32_t* const w = reinterpret_cast<uint32_t*>(sh.hist);
+    if (lane == 0) {
+      w[4 * warp] = kmin;
+      w[4 * warp + 1] = kmax;
+      w[4 * warp + 2] = mag_u;
+      w[4 * warp + 3] = __float_as_uint(q1);
+    }
+    __syncthreads();
+    uint32_t m = 0u, q1u = 0u;
+#pragma unroll
+    for (int i = 0; i < kSelectThreads / 32; ++i) {
+      kmin = min(kmin, w[4 * i]);
+      kmax = max(kmax, w[4 * i + 1]);
+      m = max(m, w[4 * i + 2]);
+      q1u = max(q1u, w[4 * i + 3]);
+    }
+    mag = __uint_as_float(m);
+    q1 = __uint_as_float(q1u);
+  }
+  const float err = static_cast<float>(p.head_dim) * 1.1920929e-7f * q1 * mag;  // E
+
+  auto key_at = [&](int i) { return staged ? sh.keys[i] : order_key(scores[i]); };
+  float above = INFINITY, below = INFINITY;  // scores beyond `above` are in, under `below` out
+  int ties = 0;                              // how many ambiguous blocks are taken
+  bool exact = false;                        // whether f64 keys decide them
+  unsigned long long t64 = 0ull;
+  if (k > 0) {
+    int rank = k;
+    const float T = key_score(nth_largest<uint32_t>(
+        sh, [&](int i, uint32_t& key) { key = key_at(i); return true; }, count, rank, kmin, kmax));
+    above = T + 2.f * err;
+    below = T - 2.f * err;
+    unsigned long long c = 0;
+    for (int i = threadIdx.x; i < count; i += kSelectThreads) {
+      const float s = key_score(key_at(i));
+      c += s > above ? (1ull << 32) : s < below ? 0ull : 1ull;
+    }
+    c = block_sum(sh, c);
+    const int ambiguous = static_cast<int>(c & 0xFFFFFFFFull);
+    ties = k - static_cast<int>(c >> 32);
+    exact = ambiguous > ties && err != 0.f;  // err = 0: every product is 0, the scores are exact
+    if (exact) {
+      unsigned long long lo64 = ~0ull, hi64 = 0ull;  // range of this warp's keys
+      for (int i0 = warp * 32; i0 < count; i0 += kSelectThreads) {
+        const int i = i0 + lane;
+        bool amb = false;
+        if (i < count) {
+          const float s = key_score(key_at(i));
+          amb = !(s > above) && !(s < below);
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, amb);
+        while (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int ph = table[c0 + i0 + src];
+          double s = -INFINITY;
+          if (static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks))
+            s = exact_score(q, p.nq, p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * p.head_dim,
+                            p.head_dim, lane);
+          const unsigned long long key = order_key(s);
+          if (lane == 0) keys64[i0 + src] = key;
+          lo64 = key < lo64 ? key : lo64;
+          hi64 = key > hi64 ? key : hi64;
+        }
+      }
+      __syncthreads();  // the keys are written, the histogram's space is free
+      {
+        unsigned long long* const w = reinterpret_cast<unsigned long long*>(sh.hist);
+        if (lane == 0) {
+          w[2 * warp] = lo64;
+          w[2 * warp + 1] = hi64;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSelectThreads / 32; ++i) {
+          lo64 = w[2 * i] < lo64 ? w[2 * i] : lo64;
+          hi64 = w[2 * i + 1] > hi64 ? w[2 * i + 1] : hi64;
+        }
+      }
+      t64 = nth_largest<unsigned long long>(
+          sh,
+          [&](int i, unsigned long long& key) {
+            const float s = key_score(key_at(i));
+            if (s > above || s < below) return false;
+            key = keys64[i];
+            return true;
+          },
+          count, ties, lo64, hi64);
+    }
+  }
+  // 2: taken; 1: taken while `ties` last, in order; 0: not
+  auto status = [&](int j) {
+    const int i = j - c0;
+    if (i < 0 || i >= count) return 2;
+    if (k == 0) return 0;
+    const float s = key_score(key_at(i));
+    if (s > above) return 2;
+    if (s < below) return 0;
+    if (!exact) return 1;
+    const unsigned long long key = keys64[i];
+    return key > t64 ? 2 : key == t64 ? 1 : 0;
+  };
+  // each thread a run of blocks; the places by a prefix over (taken, tied) counts
+  const int per = (n + kSelectThreads - 1) / kSelectThreads;
+  const int j0 = min(n, static_cast<int>(threadIdx.x) * per), j1 = min(n, j0 + per);
+  unsigned long long c = 0;
+  for (int j = j0; j < j1; ++j) {
+    const int s = status(j);
+    c += s == 2 ? (1ull << 32) : static_cast<unsigned long long>(s);
+  }
+  c = block_prefix(sh, c);
+  int sure = static_cast<int>(c >> 32), tied = static_cast<int>(c & 0xFFFFFFFFull);
+  for (int j = j0; j < j1; ++j) {
+    const int s = status(j);
+    if (s == 2 || (s == 1 && tied < ties)) put(sure + min(tied, ties), j);
+    sure += s == 2;
+    tied += s == 1;
+  }
+}
+
+template <int D>
+cudaError_t launch_score_of(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  const int per_cta = kScoreWarps * p.tiles_per_warp;
+  cfg.gridDim = dim3((p.tiles + per_cta - 1) / per_cta, p.num_kv_heads, num_seqs);
+  cfg.blockDim = dim3(kScoreWarps * 32);
+  cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * (D * 2 + 64);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pkv_score_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_seqs, cudaStream_t stream) {
+#define X(F_, D_) \
+  if (fmt == F_ && head_dim == D_) return launch_bounds_of<F_, D_>(p, num_seqs, stream);
+  X(16, 64) X(16, 128) X(16, 192) X(16, 256) X(8, 128) X(8, 256) X(4, 128) X(4, 256)
+  X(kFmtE4m3, 64) X(kFmtE4m3, 128) X(kFmtE4m3, 192) X(kFmtE4m3, 256)
+#undef X
+  return cudaErrorInvalidValue;
+}
+
+int select_tiles(int max_blocks) { return (max_blocks + kScoreTile - 1) / kScoreTile; }
+
+cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, cudaStream_t stream) {
+  p.tiles = select_tiles(p.max_blocks);
+  if (p.max_blocks > p.top_k) {  // else every block is taken
+    // A warp takes one tile while that fills the GPU about four times over, then up to 8, so
+    // that the query rows are staged for more of them.
+    const long long tiles = static_cast<long long>(p.tiles) * p.num_kv_heads * num_seqs;
+    const long long fill = 4ll * 16 * (sm_count > 0 ? sm_count : 1);
+    const long long per = tiles / fill;
+    p.tiles_per_warp = static_cast<int>(per < 1 ? 1 : per > 8 ? 8 : per);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (p.head_dim == 64) e = launch_score_of<64>(p, num_seqs, stream);
+    if (p.head_dim == 128) e = launch_score_of<128>(p, num_seqs, stream);
+    if (p.head_dim == 192) e = launch_score_of<192>(p, num_seqs, stream);
+    if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, stream);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * p.num_kv_heads);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pkv_select_kernel, p);
+}
+
+}  // namespace pkv
