@@ -245,6 +245,64 @@ def make_plan(layout: PoolLayout, params: DecodeParams, sm_count: Optional[int] 
     return plan
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the current stream's handle without building a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+class _Call:
+    """What a call's shapes settle: the argument structures and the plan."""
+
+    __slots__ = ("layout", "params", "layout_ref", "params_ref", "sparse", "sparse_ref", "workspace_bytes", "out_shape")
+
+    def __init__(self, layout, params, q, sparse=None):
+        if q.get_device() < 0:
+            raise ValueError("expected CUDA tensors")
+        self.layout, self.params, self.sparse = layout, params, sparse
+        self.layout_ref, self.params_ref = ctypes.byref(layout), ctypes.byref(params)
+        self.sparse_ref = None if sparse is None else ctypes.byref(sparse)
+        dv = layout.v_head_dim or layout.head_dim
+        self.out_shape = tuple(q.shape[:-1]) + (dv,)
+
+    def new_out(self, q):
+        return torch.empty(self.out_shape, dtype=q.dtype, device=q.device)
+
+
+_calls = {}
+
+
+def _remember(key, call):
+    if len(_calls) > 1024:
+        _calls.clear()
+    _calls[key] = call
+    return call
+
+
+def _check_block_scales(bits: int, group_size: int, *scales) -> None:
+    if bits == 8 and group_size == PKV_GROUP_BLOCK:
+        for s in scales:
+            if s is not None and s.dtype is not torch.float32:
+                raise TypeError(f"scales of e4m3 pages are float32 [num_blocks, num_kv_heads], not {s.dtype}")
+
+
+def _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
+                 schedule) -> _Call:
+    """Cached by what settles the call; runs with q's device current."""
+    key = (q.get_device(), q.shape, k_pool.shape, v_pool.shape, v_pool.dtype, block_tables.shape, bits, group_size,
+           partition_tokens, window, contraction, schedule)
+    call = _calls.get(key)
+    if call is None:
+        B, HQ, N, D = q.shape
+        call = _Call(layout_for(k_pool, D, bits, group_size, v_pool),
+                     DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule), q)
+        call.workspace_bytes = _cached_plan(call.layout, call.params).workspace_bytes
+        _remember(key, call)
+    return call
+
+
 def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                            block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, *,
                            bits: int = 16, group_size: int = 64,
@@ -264,22 +322,22 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     CUDA stream of q's device and returns bf16 [B, HQ, N, D].
     """
     lib = load_library()
-    B, HQ, N, D = q.shape
-    layout = layout_for(k_pool, D, bits, group_size, v_pool)
-    params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule)
+    _check_block_scales(bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
-        plan = _cached_plan(layout, params)
+        call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
+                            schedule)
         if out is None:
-            out = _out_like(q, layout)
-        if workspace is None and plan.workspace_bytes:
-            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+            out = call.new_out(q)
+        if workspace is None and call.workspace_bytes:
+            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        stream = torch.cuda.current_stream(q.device).cuda_stream
         rc = lib.pkv_paged_decode_attention(
-            ctypes.byref(layout), ctypes.byref(params), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(block_tables),
-            _ptr(seq_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
-    _check(rc, lib)
+            call.layout_ref, call.params_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), block_tables.data_ptr(),
+            seq_lens.data_ptr(), float(scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag),
+            _raw_stream(q.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return out
 
 
@@ -296,22 +354,21 @@ def paged_decode_append_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: t
     k_new/v_new bf16 [B, HK, N, D] at cache positions seq_lens[b]-N .. seq_lens[b]-1
     (seq_lens counts the new rows), then attends as ``paged_decode_attention``."""
     lib = load_library()
-    B, HQ, N, D = q.shape
-    layout = layout_for(k_pool, D, bits, group_size, v_pool)
-    params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule)
     with _on_device(q.device):
-        plan = _cached_plan(layout, params)
+        call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
+                            schedule)
         if out is None:
-            out = _out_like(q, layout)
-        if workspace is None and plan.workspace_bytes:
-            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+            out = call.new_out(q)
+        if workspace is None and call.workspace_bytes:
+            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        stream = torch.cuda.current_stream(q.device).cuda_stream
         rc = lib.pkv_paged_decode_append_attention(
-            ctypes.byref(layout), ctypes.byref(params), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool),
-            _ptr(v_pool), _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(block_tables),
-            _ptr(seq_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
-    _check(rc, lib)
+            call.layout_ref, call.params_ref, q.data_ptr(), _ptr(k_new), _ptr(v_new), k_pool.data_ptr(),
+            v_pool.data_ptr(), _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), block_tables.data_ptr(),
+            seq_lens.data_ptr(), float(scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag),
+            _raw_stream(q.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return out
 
 
@@ -411,13 +468,15 @@ class HostDecodeStep:
 class _on_device:
     """Makes `device` current for the call (a no-op when it already is)."""
 
+    __slots__ = ("index", "prev")
+
     def __init__(self, device: torch.device):
-        self.index = device.index if device.index is not None else torch.cuda.current_device()
+        self.index = device.index
         self.prev = None
 
     def __enter__(self):
         cur = torch.cuda.current_device()
-        if cur != self.index:
+        if self.index is not None and cur != self.index:
             self.prev = cur
             torch.cuda.set_device(self.index)
         return self
@@ -467,14 +526,36 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
     """Writes k_new/v_new bf16 [B, HK, n_new, D] at positions seq_lens[b].. of each
     sequence (quantising affine and e4m3 pages); see include/pkv_decode.h."""
     lib = load_library()
+    _check_block_scales(bits, group_size, k_scales, v_scales)
     B, HK, n_new, D = k_new.shape
-    layout = layout_for(k_pool, D, bits, group_size, v_pool)
+    key = ("append", k_new.get_device(), k_pool.shape, v_pool.shape, v_pool.dtype, D, bits, group_size)
+    call = _calls.get(key)
+    if call is None:
+        call = _remember(key, _Call(layout_for(k_pool, D, bits, group_size, v_pool), DecodeParams(), k_new))
     with _on_device(k_new.device):
-        stream = torch.cuda.current_stream(k_new.device).cuda_stream
-        rc = lib.pkv_paged_append(ctypes.byref(layout), B, block_tables.shape[1], n_new, _ptr(k_new), _ptr(v_new),
-                                  _ptr(block_tables), _ptr(seq_lens), _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
-                                  _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(error_flag), stream)
+        rc = lib.pkv_paged_append(call.layout_ref, B, block_tables.shape[1], n_new, k_new.data_ptr(), v_new.data_ptr(),
+                                  block_tables.data_ptr(), seq_lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                  _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(error_flag),
+                                  _raw_stream(k_new.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
+
+
+def paged_gather(pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
+                 out: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Bit-exact gather of one pool plane [NB, HK, BS, W] into [B, HK, max_len, W]."""
+    lib = load_library()
+    nb, hk, bs = pool.shape[:3]
+    row_bytes = pool[0, 0, 0].numel() * pool.element_size()
+    B = block_tables.shape[0]
+    if out is None:
+        out = torch.zeros((B, hk, max_len) + tuple(pool.shape[3:]), dtype=pool.dtype, device=pool.device)
+    with _on_device(pool.device):
+        stream = torch.cuda.current_stream(pool.device).cuda_stream
+        rc = lib.pkv_paged_gather(_ptr(pool), nb, hk, bs, row_bytes, _ptr(block_tables), _ptr(seq_lens), B,
+                                  block_tables.shape[1], max_len, _ptr(out), _ptr(error_flag), stream)
     _check(rc, lib)
+    return out
 
 
 def make_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparseParams,
@@ -491,15 +572,21 @@ def make_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparsePar
     return plan
 
 
-def _cached_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparseParams) -> SparsePlan:
-    key = _plan_key(layout, params) + (sparse.top_k, sparse.first_blocks, sparse.last_blocks)
-    plan = _plan_cache.get(key)
-    if plan is None:
-        plan = make_sparse_plan(layout, params, sparse)
-        if len(_plan_cache) > 1024:
-            _plan_cache.clear()
-        _plan_cache[key] = plan
-    return plan
+def _require(dtype: torch.dtype, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _require_contiguous(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)}, not {list(t.shape)}")
 
 
 def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
@@ -510,22 +597,36 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
     up to date after the last n_new rows of every sequence were appended (seq_lens counts
     them); see include/pkv_decode.h. Returns k_bounds."""
     lib = load_library()
-    layout = layout_for(k_pool, k_bounds.shape[-1], bits, group_size)
-    if layout.head_dim == 192:  # the values are not looked at; no pages have 192-dim ones
-        layout.v_head_dim = 128
+    _check_block_scales(bits, group_size, k_scales)
+    key = ("bounds", k_bounds.get_device(), k_pool.shape, k_pool.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
+           block_tables.dtype, seq_lens.shape, seq_lens.dtype, bits, group_size)
+    call = _calls.get(key)
+    if call is None:
+        _require(torch.bfloat16, k_bounds=k_bounds)
+        _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+        D = k_pool.shape[-1] * k_pool.element_size() * 8 // bits
+        _require_shape("k_bounds", k_bounds, k_pool.shape[0], k_pool.shape[1], 2, D)
+        _require_shape("seq_lens", seq_lens, block_tables.shape[0])
+        layout = layout_for(k_pool, D, bits, group_size)
+        if D == 192:  # the values are not looked at; no pages have 192-dim ones
+            layout.v_head_dim = 128
+        call = _remember(key, _Call(layout, DecodeParams(), k_bounds))
+    _require_contiguous(k_pool=k_pool, block_tables=block_tables, seq_lens=seq_lens, k_bounds=k_bounds,
+                        k_scales=k_scales, k_biases=k_biases)
     B, max_blocks = block_tables.shape
     with _on_device(k_pool.device):
-        stream = torch.cuda.current_stream(k_pool.device).cuda_stream
-        rc = lib.pkv_update_block_bounds(ctypes.byref(layout), B, max_blocks, n_new, _ptr(k_pool), _ptr(k_scales),
-                                         _ptr(k_biases), _ptr(block_tables), _ptr(seq_lens), _ptr(k_bounds),
-                                         _ptr(error_flag), stream)
-    _check(rc, lib)
+        rc = lib.pkv_update_block_bounds(call.layout_ref, B, max_blocks, n_new, k_pool.data_ptr(), _ptr(k_scales),
+                                         _ptr(k_biases), block_tables.data_ptr(), seq_lens.data_ptr(),
+                                         k_bounds.data_ptr(), _ptr(error_flag), _raw_stream(k_pool.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return k_bounds
 
 
 class BlockSelection(NamedTuple):
     """Blocks chosen for a step (pkv_select_blocks): ``blocks`` int32 [B, HK, top_k], their places
-    in the sequence; ``tables`` and ``lens``, the form the attention over them reads."""
+    in the sequence; ``tables`` [B, HK, top_k] and ``lens`` [B, HK], the form the attention over
+    them reads."""
 
     blocks: torch.Tensor
     tables: torch.Tensor
@@ -539,24 +640,43 @@ def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.T
     """Chooses top_k blocks for each (sequence, KV head) of queries q bf16 [B, HQ, N, D] by their
     bounds (pkv_select_blocks). Depends on the bounds alone, whatever the pages' format."""
     lib = load_library()
-    B, HQ, N, D = q.shape
-    nb, hk = k_bounds.shape[:2]
-    layout = PoolLayout(nb, hk, block_size, D, 16, 64, 64 if D == 64 else 128)
-    params = DecodeParams(B, HQ, N, block_tables.shape[1])
-    sparse = SparseParams(top_k, first_blocks, last_blocks)
     with _on_device(q.device):
-        plan = _cached_sparse_plan(layout, params, sparse)
+        key = ("select", q.get_device(), q.shape, q.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
+               block_tables.dtype, seq_lens.shape, seq_lens.dtype, block_size, top_k, first_blocks, last_blocks)
+        call = _calls.get(key)
+        if call is None:
+            B, HQ, N, D = q.shape
+            _require(torch.bfloat16, q=q, k_bounds=k_bounds)
+            _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+            nb, hk = k_bounds.shape[:2]
+            _require_shape("k_bounds", k_bounds, nb, hk, 2, D)
+            _require_shape("block_tables", block_tables, B, block_tables.shape[1])
+            _require_shape("seq_lens", seq_lens, B)
+            call = _Call(PoolLayout(nb, hk, block_size, D, 16, 64, 64 if D == 64 else 128),
+                         DecodeParams(B, HQ, N, block_tables.shape[1]), q,
+                         SparseParams(top_k, first_blocks, last_blocks))
+            call.workspace_bytes = make_sparse_plan(call.layout, call.params, call.sparse).select_bytes
+            _remember(key, call)
+        B, hk = q.shape[0], k_bounds.shape[1]
         if out is None:
             new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=q.device)
             out = BlockSelection(new(B, hk, top_k), new(B, hk, top_k), new(B, hk))
-        if workspace is None and plan.select_bytes:
-            workspace = torch.empty(plan.select_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            _require(torch.int32, blocks=out.blocks, tables=out.tables, lens=out.lens)
+            _require_shape("out.blocks", out.blocks, B, hk, top_k)
+            _require_shape("out.tables", out.tables, B, hk, top_k)
+            _require_shape("out.lens", out.lens, B, hk)
+        _require_contiguous(q=q, k_bounds=k_bounds, block_tables=block_tables, seq_lens=seq_lens, blocks=out.blocks,
+                            tables=out.tables, lens=out.lens)
+        if workspace is None and call.workspace_bytes:
+            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        stream = torch.cuda.current_stream(q.device).cuda_stream
-        rc = lib.pkv_select_blocks(ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q),
-                                   _ptr(k_bounds), _ptr(block_tables), _ptr(seq_lens), _ptr(out.blocks),
-                                   _ptr(out.tables), _ptr(out.lens), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
-    _check(rc, lib)
+        rc = lib.pkv_select_blocks(call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(),
+                                   k_bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                                   _ptr(out.blocks), out.tables.data_ptr(), out.lens.data_ptr(), _ptr(workspace),
+                                   ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return out
 
 
@@ -570,25 +690,38 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     """Decode attention over chosen blocks (pkv_selected_decode_attention); otherwise as
     ``paged_decode_attention``."""
     lib = load_library()
-    B, HQ, N, D = q.shape
-    layout = layout_for(k_pool, D, bits, group_size, v_pool)
-    top_k = selection.tables.shape[-1]
-    params = DecodeParams(B, HQ, N, top_k, partition_tokens, 0, contraction, schedule)
-    last = min(top_k, 1 + -(-(N - 1) // layout.block_size))  # which blocks were taken is settled: any valid numbers
-    sparse = SparseParams(top_k, 0, last)
+    _check_block_scales(bits, group_size, k_scales, v_scales)
+    tables, lens = selection.tables, selection.lens
     with _on_device(q.device):
-        plan = _cached_sparse_plan(layout, params, sparse)
+        key = ("selected", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, tables.shape,
+               tables.dtype, lens.shape, lens.dtype, bits, group_size, partition_tokens, contraction, schedule)
+        call = _calls.get(key)
+        if call is None:
+            B, HQ, N, D = q.shape
+            layout = layout_for(k_pool, D, bits, group_size, v_pool)
+            top_k = tables.shape[-1]
+            _require(torch.bfloat16, q=q)
+            _require(torch.int32, tables=tables, lens=lens)
+            _require_shape("selection.tables", tables, B, layout.num_kv_heads, top_k)
+            _require_shape("selection.lens", lens, B, layout.num_kv_heads)
+            # which blocks were taken is settled: any numbers that hold the new rows
+            sparse = SparseParams(top_k, 0, 1 + -(-(N - 1) // layout.block_size))
+            call = _Call(layout, DecodeParams(B, HQ, N, top_k, partition_tokens, 0, contraction, schedule), q, sparse)
+            call.workspace_bytes = make_sparse_plan(layout, call.params, sparse).attention.workspace_bytes
+            _remember(key, call)
+        _require_contiguous(q=q, k_pool=k_pool, v_pool=v_pool, tables=tables, lens=lens, k_scales=k_scales,
+                            k_biases=k_biases, v_scales=v_scales, v_biases=v_biases, out=out)
         if out is None:
-            out = _out_like(q, layout)
-        if workspace is None and plan.attention.workspace_bytes:
-            workspace = torch.empty(plan.attention.workspace_bytes, dtype=torch.uint8, device=q.device)
+            out = call.new_out(q)
+        if workspace is None and call.workspace_bytes:
+            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        stream = torch.cuda.current_stream(q.device).cuda_stream
         rc = lib.pkv_selected_decode_attention(
-            ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(selection.tables),
-            _ptr(selection.lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
-    _check(rc, lib)
+            call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), tables.data_ptr(), lens.data_ptr(), float(scale),
+            out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return out
 
 
@@ -606,38 +739,39 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     last always among them (pkv_sparse_decode_attention). ``blocks`` int32 [B, HK, top_k]
     receives the choice. Otherwise as ``paged_decode_attention``."""
     lib = load_library()
-    B, HQ, N, D = q.shape
-    layout = layout_for(k_pool, D, bits, group_size, v_pool)
-    params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, 0, contraction, schedule)
-    sparse = SparseParams(top_k, first_blocks, last_blocks)
+    _check_block_scales(bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
-        plan = _cached_sparse_plan(layout, params, sparse)
+        key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, k_bounds.shape,
+               k_bounds.dtype, block_tables.shape, block_tables.dtype, seq_lens.shape, seq_lens.dtype,
+               None if blocks is None else (blocks.shape, blocks.dtype), bits, group_size, partition_tokens,
+               contraction, schedule, top_k, first_blocks, last_blocks)
+        call = _calls.get(key)
+        if call is None:
+            B, HQ, N, D = q.shape
+            layout = layout_for(k_pool, D, bits, group_size, v_pool)
+            _require(torch.bfloat16, q=q, k_bounds=k_bounds)
+            _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens, blocks=blocks)
+            _require_shape("k_bounds", k_bounds, layout.num_blocks, layout.num_kv_heads, 2, D)
+            _require_shape("block_tables", block_tables, B, block_tables.shape[1])
+            _require_shape("seq_lens", seq_lens, B)
+            _require_shape("blocks", blocks, B, layout.num_kv_heads, top_k)
+            call = _Call(layout, DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, 0, contraction, schedule),
+                         q, SparseParams(top_k, first_blocks, last_blocks))
+            call.workspace_bytes = make_sparse_plan(layout, call.params, call.sparse).workspace_bytes
+            _remember(key, call)
+        _require_contiguous(q=q, k_pool=k_pool, v_pool=v_pool, k_bounds=k_bounds, block_tables=block_tables,
+                            seq_lens=seq_lens, blocks=blocks, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
+                            v_biases=v_biases, out=out)
         if out is None:
-            out = _out_like(q, layout)
+            out = call.new_out(q)
         if workspace is None:
-            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
         ws_bytes = workspace.numel() * workspace.element_size()
-        stream = torch.cuda.current_stream(q.device).cuda_stream
         rc = lib.pkv_sparse_decode_attention(
-            ctypes.byref(layout), ctypes.byref(params), ctypes.byref(sparse), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(k_bounds), _ptr(block_tables),
-            _ptr(seq_lens), float(scale), _ptr(blocks), _ptr(out), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
-    _check(rc, lib)
-    return out
-
-
-def paged_gather(pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
-                 out: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Bit-exact gather of one pool plane [NB, HK, BS, W] into [B, HK, max_len, W]."""
-    lib = load_library()
-    nb, hk, bs = pool.shape[:3]
-    row_bytes = pool[0, 0, 0].numel() * pool.element_size()
-    B = block_tables.shape[0]
-    if out is None:
-        out = torch.zeros((B, hk, max_len) + tuple(pool.shape[3:]), dtype=pool.dtype, device=pool.device)
-    with _on_device(pool.device):
-        stream = torch.cuda.current_stream(pool.device).cuda_stream
-        rc = lib.pkv_paged_gather(_ptr(pool), nb, hk, bs, row_bytes, _ptr(block_tables), _ptr(seq_lens), B,
-                                  block_tables.shape[1], max_len, _ptr(out), _ptr(error_flag), stream)
-    _check(rc, lib)
+            call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), k_bounds.data_ptr(),
+            block_tables.data_ptr(), seq_lens.data_ptr(), float(scale), _ptr(blocks), out.data_ptr(), workspace.data_ptr(),
+            ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+    if rc != PKV_OK:
+        _check(rc, lib)
     return out
