@@ -81,18 +81,10 @@ __global__ void __launch_bounds__(128) pkv_append_blocks_kernel(const __grid_con
   const int r0 = first < len ? static_cast<int>(len - first) : 0;       // its first new row
   const int r1 = static_cast<int>(min(end - first, static_cast<long long>(p.block_size)));
   const int phys = p.block_tables[static_cast<size_t>(b) * p.max_blocks + blk];
-  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-    if (threadIdx.x == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
-    return;
-  }
   const int D = p.dim[plane];
-  const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + h;
   const uint4* src = reinterpret_cast<const uint4*>(
       p.src[plane] +
       ((static_cast<size_t>(b) * p.num_kv_heads + h) * p.n_new + static_cast<size_t>(first + r0 - len)) * D);
-  uint8_t* block = p.pool[plane] + cell * p.block_size * D;
-  uint2* dst = reinterpret_cast<uint2*>(block + static_cast<size_t>(r0) * D);
-  const float old = r0 > 0 ? p.scales[plane][cell] : 0.f;
   const int n8 = (r1 - r0) * (D / 8);
   const int T = blockDim.x;
 
@@ -101,8 +93,17 @@ __global__ void __launch_bounds__(128) pkv_append_blocks_kernel(const __grid_con
 #pragma unroll
   for (int k = 0; k < kHold; ++k) {
     const int i = threadIdx.x + k * T;
-    v[k] = i < n8 ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+    v[k] = i < n8 ? ld_nc_keep_v4(src + i) : make_uint4(0u, 0u, 0u, 0u);
   }
+  // the rows are in flight while the table's answer arrives
+  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+    if (threadIdx.x == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+    return;
+  }
+  const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + h;
+  uint8_t* block = p.pool[plane] + cell * p.block_size * D;
+  uint2* dst = reinterpret_cast<uint2*>(block + static_cast<size_t>(r0) * D);
+  const float old = r0 > 0 ? p.scales[plane][cell] : 0.f;
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
     m = max_u16x2(m, max_u16x2(max_u16x2(abs_bf16x2(v[k].x), abs_bf16x2(v[k].y)),

@@ -239,16 +239,23 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
   extern __shared__ __align__(16) uint8_t sq[];
   wait_for_prerequisite_grids();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z;
+  // the KV heads of a run of blocks are neighbours in the grid, as their bounds are in memory
+  const int chunk = blockIdx.x / p.num_kv_heads, h = blockIdx.x - chunk * p.num_kv_heads, b = blockIdx.y;
   const size_t unit = static_cast<size_t>(b) * p.num_kv_heads + h;
   const int len = p.seq_lens[b];
   if (len < p.n_query || len > p.max_blocks * p.block_size) return;  // the choice flags it
   const int n = (len + p.block_size - 1) / p.block_size;
-  const int cta_tile = blockIdx.x * kScoreWarps * p.tiles_per_warp;
+  const int cta_tile = chunk * kScoreWarps * p.tiles_per_warp;
   if (n <= p.top_k || cta_tile * kScoreTile >= n) return;  // every block is taken, or none is here
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   const int ntiles = (p.nq + 7) / 8;  // tiles of 8 query rows
 
+  // a tile's block ids, one per lane of the first 16; -1 past the last block
+  auto ids_of = [&](int tile) {
+    const int j = tile * kScoreTile + lane;
+    return lane < kScoreTile && j < n ? table[j] : -1;
+  };
+  int ids = ids_of(cta_tile + warp);
   for (int it = 0; it < p.tiles_per_warp; ++it) {
     const int tile = cta_tile + it * kScoreWarps + warp;  // warp-uniform
     const int j0 = tile * kScoreTile;
@@ -256,12 +263,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
     uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
     int ph0 = -1, ph1 = -1;
     if (live) {
-      const bool in = lane < kScoreTile && j0 + lane < n;
-      const int ph = in ? table[j0 + lane] : -1;
-      const bool ok = static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks);
-      if (in && !ok && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
-      ph0 = __shfl_sync(0xffffffffu, ok ? ph : -1, g);
-      ph1 = __shfl_sync(0xffffffffu, ok ? ph : -1, g + 8);
+      const bool ok = static_cast<unsigned>(ids) < static_cast<unsigned>(p.num_blocks);
+      if (!ok && lane < kScoreTile && j0 + lane < n && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+      ph0 = __shfl_sync(0xffffffffu, ok ? ids : -1, g);
+      ph1 = __shfl_sync(0xffffffffu, ok ? ids : -1, g + 8);
       const __nv_bfloat16* r0 = p.k_bounds + (static_cast<size_t>(ph0 < 0 ? 0 : ph0) * p.num_kv_heads + h) * 2 * D + 8 * t;
       const __nv_bfloat16* r1 = p.k_bounds + (static_cast<size_t>(ph1 < 0 ? 0 : ph1) * p.num_kv_heads + h) * 2 * D + 8 * t;
 #pragma unroll
@@ -272,6 +277,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
         hi1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    if (it + 1 < p.tiles_per_warp) ids = ids_of(tile + kScoreWarps);
     if (it == 0) {  // the query rows, staged while the first bounds are in flight
       const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
       for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += kScoreWarps * 32) {
@@ -332,8 +338,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 // -------------------------------------------------------------------------------------- choice
 // One CTA per (sequence, KV head). The blocks taken are those that exact sums would take,
 // ties to the lower block: f32 scores decide all but the few within their error bound E of
-// the last place, and those are summed again in f64 (products of bf16 values are exact
-// there, and so is nearly every sum of up to 256 of them).
+// the last place, and those are summed again in pairs of f32 (48 bits; the products of bf16
+// values are exact, and so is nearly every sum of up to 256 of them).
 //
 // With T the k-th largest of the candidates' f32 scores and |f32 - exact| <= E: a score
 // above T + 2E is in (at most k - 1 scores lie above T, and a block below T cannot overtake
@@ -346,7 +352,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 // bank conflicts, which radix digits of nearby floats would.
 constexpr int kSelectThreads = 512;
 constexpr int kSelectBins = 2048;
-constexpr int kSelectKeys = 8192;  // scores kept in shared memory; more are read again from L2
+constexpr int kSelectKeys = 7680;  // scores kept in shared memory; more are read again from L2
+constexpr int kSelectAmbiguous = 256;  // ambiguous blocks ranked in shared memory; more by way of the workspace
 
 __device__ __forceinline__ uint32_t order_key(float s) {  // NaN lowest, then by value
   if (!(s == s)) return 0u;
@@ -357,17 +364,15 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   if (k == 0u) return -INFINITY;
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-__device__ __forceinline__ unsigned long long order_key(double s) {
-  if (!(s == s)) return 0ull;
-  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s + 0.0));
-  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
-}
-
 struct SelectShared {
   uint32_t keys[kSelectKeys];
   alignas(8) int hist[kSelectBins];
   unsigned long long red[kSelectThreads / 32];
   unsigned long long found;
+  unsigned long long amb_key[kSelectAmbiguous];  // ambiguous candidates: the exact score's key,
+  int amb[kSelectAmbiguous];                     // the candidate's number
+  int amb_rank[kSelectAmbiguous];                // and its rank among them
+  int amb_count;
   int bin, above, in_bin;
 };
 
@@ -454,20 +459,41 @@ __device__ __forceinline__ Key nth_largest(SelectShared& sh, F key_of, int n, in
   }
 }
 
-// A block's score in f64: the largest u_j over the query rows, by one warp.
-__device__ __forceinline__ double exact_score(const __nv_bfloat16* q, int nq, const __nv_bfloat16* bounds, int D,
-                                              int lane) {
-  double best = -INFINITY;
-  for (int r = 0; r < nq; ++r) {
-    double s = 0.0;
-    for (int d = lane; d < D; d += 32) {
-      const double x = __bfloat162float(q[static_cast<size_t>(r) * D + d]);
-      s += fmax(x * __bfloat162float(bounds[d]), x * __bfloat162float(bounds[D + d]));
-    }
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    best = s > best || !(s == s) ? s : best;
+// A sum kept as an unevaluated pair of f32 (hi + lo, |lo| at most half a step of hi): the
+// rounding error of each addition is itself an f32 and joins lo, so the pair carries about
+// 48 bits. The f64 unit is far slower on this GPU (2 lanes per clock and SM).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const float s = __fadd_rn(a.hi, b.hi), v = __fsub_rn(s, a.hi);
+  if (!(fabsf(s) < INFINITY)) return Pair{s, 0.f};  // infinite or NaN: no error term
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));  // s + e = a.hi + b.hi exactly
+  const float l = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+  const float h = __fadd_rn(s, l);
+  return Pair{h, __fsub_rn(l, __fsub_rn(h, s))};
+}
+
+constexpr unsigned long long kLowestKey = 1ull;  // of a NaN score and of a bad block
+
+// u_j of one query row as an ordered integer, by one warp: the products of bf16 values are
+// exact in f32. Pairs order by hi, then by lo.
+__device__ __forceinline__ unsigned long long exact_key(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int D,
+                                                        int lane) {
+  Pair s{0.f, 0.f};
+  for (int d = 2 * lane; d < D; d += 64) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(q + d);
+    const __nv_bfloat162 l = *reinterpret_cast<const __nv_bfloat162*>(bounds + d);
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(bounds + D + d);
+    const float x0 = __low2float(x), x1 = __high2float(x);
+    s = pair_add(s, Pair{fmaxf(x0 * __low2float(l), x0 * __low2float(h)), 0.f});
+    s = pair_add(s, Pair{fmaxf(x1 * __high2float(l), x1 * __high2float(h)), 0.f});
   }
-  return best;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1)
+    s = pair_add(s, Pair{__shfl_xor_sync(0xffffffffu, s.hi, k), __shfl_xor_sync(0xffffffffu, s.lo, k)});
+  const uint32_t hi = order_key(s.hi);
+  return hi == 0u ? kLowestKey : (static_cast<unsigned long long>(hi) << 32) | order_key(s.lo);
 }
 
 __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid_constant__ SelectParams p) {
@@ -551,7 +577,8 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
   auto key_at = [&](int i) { return staged ? sh.keys[i] : order_key(scores[i]); };
   float above = INFINITY, below = INFINITY;  // scores beyond `above` are in, under `below` out
   int ties = 0;                              // how many ambiguous blocks are taken
-  bool exact = false;                        // whether f64 keys decide them
+  int ambiguous = 0;
+  bool exact = false;                        // whether exact sums decide which
   unsigned long long t64 = 0ull;
   if (k > 0) {
     int rank = k;
@@ -559,16 +586,47 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
         sh, [&](int i, uint32_t& key) { key = key_at(i); return true; }, count, rank, kmin, kmax));
     above = T + 2.f * err;
     below = T - 2.f * err;
-    unsigned long long c = 0;
+    if (threadIdx.x == 0) sh.amb_count = 0;
+    __syncthreads();
+    int sure = 0;
     for (int i = threadIdx.x; i < count; i += kSelectThreads) {
       const float s = key_score(key_at(i));
-      c += s > above ? (1ull << 32) : s < below ? 0ull : 1ull;
+      if (s > above) {
+        ++sure;
+      } else if (!(s < below)) {
+        const int at = atomicAdd(&sh.amb_count, 1);
+        if (at < kSelectAmbiguous) sh.amb[at] = i;
+      }
     }
-    c = block_sum(sh, c);
-    const int ambiguous = static_cast<int>(c & 0xFFFFFFFFull);
-    ties = k - static_cast<int>(c >> 32);
+    ties = k - static_cast<int>(block_sum(sh, static_cast<unsigned long long>(sure)));
+    ambiguous = sh.amb_count;
     exact = ambiguous > ties && err != 0.f;  // err = 0: every product is 0, the scores are exact
-    if (exact) {
+    auto bounds_of = [&](int i) -> const __nv_bfloat16* {  // nullptr for a bad block
+      const int ph = table[c0 + i];
+      if (static_cast<unsigned>(ph) >= static_cast<unsigned>(p.num_blocks)) return nullptr;
+      return p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * p.head_dim;
+    };
+    if (exact && ambiguous <= kSelectAmbiguous) {
+      // few, as a rule: a warp per (block, query row), then a rank by counting
+      for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) sh.amb_key[i] = 0ull;
+      __syncthreads();
+      for (int w = warp; w < ambiguous * p.nq; w += kSelectThreads / 32) {
+        const int at = w / p.nq, r = w - at * p.nq;
+        const __nv_bfloat16* bd = bounds_of(sh.amb[at]);
+        const unsigned long long key =
+            bd ? exact_key(q + static_cast<size_t>(r) * p.head_dim, bd, p.head_dim, lane) : kLowestKey;
+        if (lane == 0) atomicMax(&sh.amb_key[at], key);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
+        const unsigned long long key = sh.amb_key[i];
+        const int at = sh.amb[i];
+        int rank = 0;
+        for (int j = 0; j < ambiguous; ++j) rank += sh.amb_key[j] > key || (sh.amb_key[j] == key && sh.amb[j] < at);
+        sh.amb_rank[i] = rank;
+      }
+      __syncthreads();
+    } else if (exact) {
       unsigned long long lo64 = ~0ull, hi64 = 0ull;  // range of this warp's keys
       for (int i0 = warp * 32; i0 < count; i0 += kSelectThreads) {
         const int i = i0 + lane;
@@ -581,12 +639,12 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
         while (todo) {
           const int src = __ffs(todo) - 1;
           todo &= todo - 1;
-          const int ph = table[c0 + i0 + src];
-          double s = -INFINITY;
-          if (static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks))
-            s = exact_score(q, p.nq, p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * p.head_dim,
-                            p.head_dim, lane);
-          const unsigned long long key = order_key(s);
+          const __nv_bfloat16* bd = bounds_of(i0 + src);
+          unsigned long long key = kLowestKey;
+          for (int r = 0; bd && r < p.nq; ++r) {
+            const unsigned long long of = exact_key(q + static_cast<size_t>(r) * p.head_dim, bd, p.head_dim, lane);
+            key = of > key ? of : key;
+          }
           if (lane == 0) keys64[i0 + src] = key;
           lo64 = key < lo64 ? key : lo64;
           hi64 = key > hi64 ? key : hi64;
@@ -617,6 +675,7 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
           count, ties, lo64, hi64);
     }
   }
+  const int ties_all = ties;
   // 2: taken; 1: taken while `ties` last, in order; 0: not
   auto status = [&](int j) {
     const int i = j - c0;
@@ -626,6 +685,10 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
     if (s > above) return 2;
     if (s < below) return 0;
     if (!exact) return 1;
+    if (ambiguous <= kSelectAmbiguous) {
+      for (int at = 0; at < ambiguous; ++at)
+        if (sh.amb[at] == i) return sh.amb_rank[at] < ties_all ? 2 : 0;
+    }
     const unsigned long long key = keys64[i];
     return key > t64 ? 2 : key == t64 ? 1 : 0;
   };
@@ -651,7 +714,9 @@ template <int D>
 cudaError_t launch_score_of(const SelectParams& p, int num_seqs, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   const int per_cta = kScoreWarps * p.tiles_per_warp;
-  cfg.gridDim = dim3((p.tiles + per_cta - 1) / per_cta, p.num_kv_heads, num_seqs);
+  const long long ctas = static_cast<long long>((p.tiles + per_cta - 1) / per_cta) * p.num_kv_heads;
+  if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), num_seqs);
   cfg.blockDim = dim3(kScoreWarps * 32);
   cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * (D * 2 + 64);
   cfg.stream = stream;
