@@ -201,6 +201,15 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
       if (half < rich_rows && ctas >= slots) break;
       part = half;
     }
+    // e4m3 pages: a grid of at most one CTA per SM with more partitions than a cluster
+    // holds takes 16 of them instead, while a CTA still reads no more than 256 KB: the
+    // merge then needs no second launch and no workspace (1 x 8192 rows of 256-dim heads,
+    // 32 -> 16 partitions: 9.1 -> 9.7 us on the GPU, 17.9 -> 13.0 us per call from the host).
+    if (block_scaled(L) && P->window == 0) {
+      const long long parts = (span + part - 1) / part;
+      const long long wide = round_up((span + pkv::kMaxClusterParts - 1) / pkv::kMaxClusterParts, ch);
+      if (parts > pkv::kMaxClusterParts && units * parts <= sm_count && wide * kv_row <= (256ll << 10)) part = wide;
+    }
     // With a window, every sequence longer than it reads the same span, so the
     // (sequence, KV head) units carry even work. When the grid above is at most two
     // waves (a short step, where the merge launch shows) and 2..16 partitions per unit
@@ -497,6 +506,21 @@ struct PreparedDecode {
   bool solo, cc, bal, pc, partial, merge;
 };
 
+// The pointers of a decode call (of its partial pass, or of the merge pass alone).
+int check_decode_pointers(const pkv_pool_layout* layout, bool partial, const void* q, const void* k_pool,
+                          const void* v_pool, const void* k_scales, const void* k_biases, const void* v_scales,
+                          const void* v_biases, const int32_t* block_tables, const int32_t* seq_lens, const void* out,
+                          const void* workspace, const int32_t* error_flag) {
+  if (!seq_lens || !out) return PKV_ERR_NULL_POINTER;
+  if (partial && (!q || !k_pool || !v_pool || !block_tables)) return PKV_ERR_NULL_POINTER;
+  if (partial && !scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(error_flag, 4) || !aligned(workspace, 16))
+    return PKV_ERR_MISALIGNED;
+  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 16)) return PKV_ERR_MISALIGNED;
+  return PKV_OK;
+}
+
 // Checks the arguments of a decode call (the passes in `passes`) and prepares its
 // launches; no CUDA work is enqueued.
 int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* params, const void* q,
@@ -509,13 +533,9 @@ int prepare_decode(const pkv_pool_layout* layout, const pkv_decode_params* param
   rc = check_params(layout, params);
   if (rc) return rc;
   const bool partial = passes & kPassPartial;
-  if (!seq_lens || !out) return PKV_ERR_NULL_POINTER;
-  if (partial && (!q || !k_pool || !v_pool || !block_tables)) return PKV_ERR_NULL_POINTER;
-  if (partial && !scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
-  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
-      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(error_flag, 4) || !aligned(workspace, 16))
-    return PKV_ERR_MISALIGNED;
-  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 16)) return PKV_ERR_MISALIGNED;
+  rc = check_decode_pointers(layout, partial, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, block_tables,
+                             seq_lens, out, workspace, error_flag);
+  if (rc) return rc;
   if (k_new && block_scaled(layout)) return PKV_ERR_UNSUPPORTED_SHAPE;  // a new row may rescale its whole block
   if ((k_new == nullptr) != (v_new == nullptr)) return PKV_ERR_NULL_POINTER;
   if (!aligned(k_new, 16) || !aligned(v_new, 16)) return PKV_ERR_MISALIGNED;
@@ -988,9 +1008,32 @@ int check_sparse(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
   return PKV_OK;
 }
 
+// Rows per partition of the decode over `blocks` chosen blocks per unit (0: the library's
+// choice, for grids of more than one wave). The units read the same number of rows, as a
+// rule, so the partitions are as many as one wave holds, of 256 rows or more, and merge in
+// clusters: of the grids of one and of two CTAs per SM the one that fills more of its wave,
+// the former where they tie. 64 units of 4096 bf16 rows (D=128, 16 query rows): 2 partitions
+// 26.9 us, the library's choice (8, through the workspace) 32.0 us; 64 units of 1536 4-bit
+// rows (D=256): 2 partitions 12.6 us, the library's choice (balanced) 21.5 us.
+int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int blocks, int sm_count) {
+  const long long units = vp->num_seqs, rows = static_cast<long long>(blocks) * vl->block_size, sms = sm_count;
+  const int nq = vp->num_q_heads * vp->n_query;
+  const bool cc = vp->contraction == PKV_CONTRACTION_CUDA_CORE;
+  const PartialInfo one = partial_info(format_of(vl), vl->head_dim, v_dim(vl), nq, true, cc);
+  const PartialInfo two = partial_info(format_of(vl), vl->head_dim, v_dim(vl), nq, false, cc);
+  const long long per_sm = two.smem_bytes <= 114 * 1024 ? 2 : 1;
+  const long long most = std::max(1ll, rows / 256);
+  const long long p1 = one.exists && vl->block_size >= two.chunk_rows
+                           ? std::min(std::min<long long>(pkv::kMaxClusterParts, sms / units), most)
+                           : 0;
+  const long long p2 = std::min(std::min(per_sm == 2 ? 16ll : 8ll, per_sm * sms / units), most);
+  const long long parts = units * p1 * per_sm >= units * p2 ? p1 : p2;
+  return parts > 0 ? static_cast<int>(round_up((rows + parts - 1) / parts, chunk_rows_of(vl->bits))) : 0;
+}
+
 // The decode over chosen blocks: the pool as NB * HK blocks of one KV head, every (sequence,
 // KV head) a sequence of at most top_k of them.
-void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S,
+void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S, int sm_count,
                  pkv_pool_layout* vl, pkv_decode_params* vp) {
   *vl = *L;
   vl->num_blocks = L->num_blocks * L->num_kv_heads;
@@ -999,7 +1042,12 @@ void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
   vp->num_seqs = P->num_seqs * L->num_kv_heads;
   vp->num_q_heads = P->num_q_heads / L->num_kv_heads;
   vp->max_blocks_per_seq = S->top_k;
+  if (vp->partition_tokens == 0 && vp->schedule != PKV_SCHEDULE_BALANCED)
+    vp->partition_tokens = chosen_partition(vl, vp, std::min(S->top_k, P->max_blocks_per_seq), sm_count);
 }
+
+// Scores of a unit in the workspace: rows of 16-byte groups.
+size_t score_stride(const pkv_decode_params* P) { return (static_cast<size_t>(P->max_blocks_per_seq) + 3) / 4 * 4; }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1012,7 +1060,7 @@ SparseWorkspace sparse_workspace(const pkv_pool_layout* L, const pkv_decode_para
   const size_t units = static_cast<size_t>(P->num_seqs) * L->num_kv_heads;
   const size_t cells = P->max_blocks_per_seq > S->top_k ? units * P->max_blocks_per_seq : 0;
   SparseWorkspace w;
-  w.tile_abs = round256(cells * sizeof(float));
+  w.tile_abs = cells ? round256(units * score_stride(P) * sizeof(uint32_t)) : 0;
   w.keys64 = w.tile_abs + (cells ? round256(units * pkv::select_tiles(P->max_blocks_per_seq) * sizeof(float)) : 0);
   w.select_bytes = w.keys64 + round256(cells * sizeof(unsigned long long));
   w.tables = w.select_bytes;
@@ -1025,7 +1073,7 @@ int sparse_plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, const
                      pkv_sparse_plan* out) {
   pkv_pool_layout vl;
   pkv_decode_params vp;
-  chosen_view(L, P, S, &vl, &vp);
+  chosen_view(L, P, S, sm_count, &vl, &vp);
   int rc = check_params(&vl, &vp);
   if (rc) return rc;
   rc = plan_impl(&vl, &vp, sm_count, &out->attention);
@@ -1048,7 +1096,8 @@ pkv::SelectParams select_params(const pkv_pool_layout* L, const pkv_decode_param
   p.k_bounds = static_cast<const __nv_bfloat16*>(k_bounds);
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
-  p.scores = reinterpret_cast<float*>(ws);
+  p.scores = reinterpret_cast<uint32_t*>(ws);
+  p.score_stride = static_cast<int>(score_stride(P));
   p.tile_abs = reinterpret_cast<float*>(ws + w.tile_abs);
   p.keys64 = reinterpret_cast<unsigned long long*>(ws + w.keys64);
   p.out_blocks = blocks;
@@ -1166,9 +1215,15 @@ int pkv_selected_decode_attention(const pkv_pool_layout* layout, const pkv_decod
                                   size_t workspace_bytes, int32_t* error_flag, void* stream) {
   int rc = check_sparse(layout, params, sparse);
   if (rc) return rc;
+  rc = check_decode_pointers(layout, true, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, chosen_tables,
+                             chosen_lens, out, workspace, error_flag);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
   pkv_pool_layout vl;
   pkv_decode_params vp;
-  chosen_view(layout, params, sparse, &vl, &vp);
+  chosen_view(layout, params, sparse, sms, &vl, &vp);
   return enqueue_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, chosen_tables,
                         chosen_lens, scale, out, workspace, workspace_bytes, error_flag, stream,
                         kPassPartial | kPassMerge);
@@ -1182,25 +1237,26 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
                                 size_t workspace_bytes, int32_t* error_flag, void* stream) {
   int rc = check_sparse(layout, params, sparse);
   if (rc) return rc;
-  if (!k_bounds || !block_tables || !seq_lens) return PKV_ERR_NULL_POINTER;
-  if (!aligned(k_bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(blocks, 4))
-    return PKV_ERR_MISALIGNED;
+  if (!k_bounds) return PKV_ERR_NULL_POINTER;
+  rc = check_decode_pointers(layout, true, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, block_tables,
+                             seq_lens, out, workspace, error_flag);
+  if (rc) return rc;
+  if (!aligned(k_bounds, 16) || !aligned(blocks, 4)) return PKV_ERR_MISALIGNED;
   const SparseWorkspace w = sparse_workspace(layout, params, sparse);
   if (!workspace || workspace_bytes < w.attention) return PKV_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned(workspace, 16)) return PKV_ERR_MISALIGNED;
   char* const ws = static_cast<char*>(workspace);
   int32_t* const tables = reinterpret_cast<int32_t*>(ws + w.tables);
   int32_t* const lens = reinterpret_cast<int32_t*>(ws + w.lens);
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
   pkv_pool_layout vl;
   pkv_decode_params vp;
-  chosen_view(layout, params, sparse, &vl, &vp);
+  chosen_view(layout, params, sparse, sms, &vl, &vp);
   PreparedDecode pd;  // every argument is checked before the first launch
   rc = prepare_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, tables, lens, scale, out,
                       ws + w.attention, workspace_bytes - w.attention, error_flag, kPassPartial | kPassMerge, nullptr,
                       nullptr, &pd);
-  if (rc) return rc;
-  int sms = 0;
-  rc = device_sm_count(&sms);
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();

@@ -12,6 +12,8 @@
 //
 // A block's new rows are contiguous in k_new/v_new and in the pool, so a unit is one run of
 // 16-byte loads and 8-byte stores: bound by HBM, 2 bytes read and 1 written per value.
+#include <type_traits>
+
 #include "pkv_launch.h"
 
 namespace pkv {
@@ -20,10 +22,14 @@ namespace {
 
 constexpr int kHold = 8;  // 16-byte loads a thread keeps in registers between the two uses of the values
 
-__device__ __forceinline__ uint32_t abs_bf16x2(uint32_t w) { return w & 0x7FFF7FFFu; }
-
-// Elementwise maximum of non-negative bf16 pairs, which order as unsigned integers do.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+// Elementwise maximum of the magnitudes of bf16 pairs (the values are finite).
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, const uint4& v) {
+  return max_abs(max_abs(max_abs(max_abs(m, v.x), v.y), v.z), v.w);
+}
 
 // The smallest power of two s (at least 2^-126) with a <= 448 s, for a > 0; 0 for a = 0.
 __device__ __forceinline__ float pow2_scale(float a) {
@@ -40,17 +46,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Codes of 8 bf16 values over s (s > 0): by its exact reciprocal `inv` when s is a power of
-// two (as the append makes it), else by division (a scale the caller chose).
-__device__ __forceinline__ uint2 quantize8(const uint4& v, float s, float inv, bool exact) {
+// Codes of 8 bf16 values over s (s > 0): times its exact reciprocal when s is a power of
+// two (EXACT, as the append makes it), else by division (a scale the caller chose).
+template <bool EXACT>
+__device__ __forceinline__ uint2 quantize8(const uint4& v, float s, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-    c[i] = exact ? e4m3x2(lo * inv, hi * inv) : e4m3x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+    c[i] = EXACT ? e4m3x2(lo * inv, hi * inv) : e4m3x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // The four codes of a word times `ratio`, as codes.
@@ -105,14 +112,8 @@ __global__ void __launch_bounds__(128) pkv_append_blocks_kernel(const __grid_con
   uint2* dst = reinterpret_cast<uint2*>(block + static_cast<size_t>(r0) * D);
   const float old = r0 > 0 ? p.scales[plane][cell] : 0.f;
 #pragma unroll
-  for (int k = 0; k < kHold; ++k)
-    m = max_u16x2(m, max_u16x2(max_u16x2(abs_bf16x2(v[k].x), abs_bf16x2(v[k].y)),
-                               max_u16x2(abs_bf16x2(v[k].z), abs_bf16x2(v[k].w))));
-  for (int i = threadIdx.x + kHold * T; i < n8; i += T) {
-    const uint4 w = src[i];
-    m = max_u16x2(m, max_u16x2(max_u16x2(abs_bf16x2(w.x), abs_bf16x2(w.y)),
-                               max_u16x2(abs_bf16x2(w.z), abs_bf16x2(w.w))));
-  }
+  for (int k = 0; k < kHold; ++k) m = max_abs(m, v[k]);
+  for (int i = threadIdx.x + kHold * T; i < n8; i += T) m = max_abs(m, src[i]);
   m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
   if (T > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -134,15 +135,21 @@ __global__ void __launch_bounds__(128) pkv_append_blocks_kernel(const __grid_con
       row[i] = w;
     }
   }
-  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
   const float inv = s > 0.f ? 1.f / s : 0.f;  // s = 0: every value is 0, and so is every code
   const float by = s > 0.f ? s : 1.f;
+  auto write = [&](auto exact) {
 #pragma unroll
-  for (int k = 0; k < kHold; ++k) {
-    const int i = threadIdx.x + k * T;
-    if (i < n8) dst[i] = quantize8(v[k], by, inv, exact);
+    for (int k = 0; k < kHold; ++k) {
+      const int i = threadIdx.x + k * T;
+      if (i < n8) dst[i] = quantize8<decltype(exact)::value>(v[k], by, inv);
+    }
+    for (int i = threadIdx.x + kHold * T; i < n8; i += T) dst[i] = quantize8<decltype(exact)::value>(src[i], by, inv);
+  };
+  if ((__float_as_uint(s) & 0x7FFFFFu) == 0u) {
+    write(std::true_type{});
+  } else {
+    write(std::false_type{});
   }
-  for (int i = threadIdx.x + kHold * T; i < n8; i += T) dst[i] = quantize8(src[i], by, inv, exact);
 }
 
 }  // namespace

@@ -146,7 +146,7 @@ struct SelectParams {
   const __nv_bfloat16* k_bounds;
   const int32_t* block_tables;
   const int32_t* seq_lens;
-  float* scores;                  // [units, max_blocks]
+  uint32_t* scores;               // [units, score_stride]: f32 scores as integers of the same order
   float* tile_abs;                // [units, tiles]: largest magnitude of 16 blocks' bounds
   unsigned long long* keys64;     // [units, max_blocks]: f64 scores of ambiguous blocks, as ordered integers
   int32_t* out_blocks;            // [units, top_k], optional
@@ -154,6 +154,7 @@ struct SelectParams {
   int32_t* out_lens;              // [units]
   int32_t* error_flag;
   int num_blocks, num_kv_heads, block_size, max_blocks;
+  int score_stride;               // max_blocks rounded up to 4
   int n_query, nq, head_dim, top_k, first, last;
   int tiles, tiles_per_warp;      // set by launch_select
 };
@@ -279,6 +280,11 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
 // Starts fetching the 128-byte line holding `ptr` into L1 (and L2).
 __device__ __forceinline__ void prefetch_l1(const void* ptr) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(ptr));
+}
+
+// Starts bringing `bytes` (a multiple of 16) from `ptr` (16-byte aligned) into L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void* ptr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {

@@ -228,7 +228,20 @@ cudaError_t launch_bounds_of(const BoundsParams& p, int num_seqs, cudaStream_t s
 // over 2 D. The order of the dims within the contraction is free, so the A fragments are the
 // 16-byte loads themselves (each lane 8 dims of two blocks per load, four lanes a 64-byte
 // run) and no bound passes through shared memory; the B fragment of the same dims is 16
-// bytes of a query row. Bound by HBM: 4 D bytes per (block, KV head).
+// bytes of a query row. Bound by HBM: 4 D bytes per (block, KV head). While a warp works on a
+// tile, its next tile's bounds are on their way into L2, which keeps enough bytes in flight
+// with the 16 warps that the fragments' registers leave room for.
+//
+// Scores are stored as integers of the same order, NaN lowest.
+__device__ __forceinline__ uint32_t order_key(float s) {  // NaN lowest, then by value
+  if (!(s == s)) return 0u;
+  const uint32_t u = __float_as_uint(s + 0.f);  // -0 as 0
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t k) {
+  if (k == 0u) return -INFINITY;
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTile = 16;  // blocks per warp and step
 
@@ -238,6 +251,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
   constexpr int kStride = D * 2 + 64;      // bytes of a staged query row, padded: rows g, g + 1 meet in no bank
   extern __shared__ __align__(16) uint8_t sq[];
   wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the choice may take its place on the SMs; it waits for this grid's end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the KV heads of a run of blocks are neighbours in the grid, as their bounds are in memory
   const int chunk = blockIdx.x / p.num_kv_heads, h = blockIdx.x - chunk * p.num_kv_heads, b = blockIdx.y;
@@ -251,11 +265,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
   const int ntiles = (p.nq + 7) / 8;  // tiles of 8 query rows
 
   // a tile's block ids, one per lane of the first 16; -1 past the last block
-  auto ids_of = [&](int tile) {
-    const int j = tile * kScoreTile + lane;
-    return lane < kScoreTile && j < n ? table[j] : -1;
+  auto ids_of = [&](int it) {
+    const int j = (cta_tile + it * kScoreWarps + warp) * kScoreTile + lane;
+    return it < p.tiles_per_warp && lane < kScoreTile && j < n ? table[j] : -1;
   };
-  int ids = ids_of(cta_tile + warp);
+  auto good = [&](int ph) { return static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks); };
+  int ids = ids_of(0), ids_next = ids_of(1);
   for (int it = 0; it < p.tiles_per_warp; ++it) {
     const int tile = cta_tile + it * kScoreWarps + warp;  // warp-uniform
     const int j0 = tile * kScoreTile;
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
     uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
     int ph0 = -1, ph1 = -1;
     if (live) {
-      const bool ok = static_cast<unsigned>(ids) < static_cast<unsigned>(p.num_blocks);
+      const bool ok = good(ids);
       if (!ok && lane < kScoreTile && j0 + lane < n && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
       ph0 = __shfl_sync(0xffffffffu, ok ? ids : -1, g);
       ph1 = __shfl_sync(0xffffffffu, ok ? ids : -1, g + 8);
@@ -277,7 +292,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
         hi1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    if (it + 1 < p.tiles_per_warp) ids = ids_of(tile + kScoreWarps);
+    if (good(ids_next))
+      prefetch_l2_bulk(p.k_bounds + (static_cast<size_t>(ids_next) * p.num_kv_heads + h) * 2 * D, 4 * D);
+    ids = ids_next;
+    ids_next = ids_of(it + 2);
     if (it == 0) {  // the query rows, staged while the first bounds are in flight
       const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
       for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += kScoreWarps * 32) {
@@ -327,12 +345,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
       best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, d));
     }
     if (t == 0) {
-      float* s = p.scores + unit * p.max_blocks + j0;
-      if (j0 + g < n) s[g] = ph0 >= 0 ? best0 : -INFINITY;
-      if (j0 + g + 8 < n) s[g + 8] = ph1 >= 0 ? best1 : -INFINITY;
+      uint32_t* s = p.scores + unit * p.score_stride + j0;
+      if (j0 + g < n) s[g] = order_key(ph0 >= 0 ? best0 : -INFINITY);
+      if (j0 + g + 8 < n) s[g + 8] = order_key(ph1 >= 0 ? best1 : -INFINITY);
     }
   }
-  allow_dependent_launch();
 }
 
 // -------------------------------------------------------------------------------------- choice
@@ -349,47 +366,36 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 //
 // T comes from histograms of 2048 equal bins over [lowest, highest] key, narrowed to the bin
 // that holds the k-th until it is one value (two rounds as a rule): spread scores meet few
-// bank conflicts, which radix digits of nearby floats would.
+// bank conflicts, which radix digits of nearby floats would. The marks of 32 blocks at a time
+// (ballots) and a prefix over their counts then give each taken block its place.
 constexpr int kSelectThreads = 512;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectKeys = 7680;  // scores kept in shared memory; more are read again from L2
 constexpr int kSelectAmbiguous = 256;  // ambiguous blocks ranked in shared memory; more by way of the workspace
 
-__device__ __forceinline__ uint32_t order_key(float s) {  // NaN lowest, then by value
-  if (!(s == s)) return 0u;
-  const uint32_t u = __float_as_uint(s + 0.f);  // -0 as 0
-  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
-__device__ __forceinline__ float key_score(uint32_t k) {
-  if (k == 0u) return -INFINITY;
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
+constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is always taken; no score has it
+constexpr int kSegment = 32 * kSelectThreads;  // blocks whose marks fit shared memory at once, a word per thread
+
 struct SelectShared {
-  uint32_t keys[kSelectKeys];
-  alignas(8) int hist[kSelectBins];
+  uint32_t keys[kSelectKeys];  // later the chosen blocks
+  union {
+    int hist[kSelectBins];
+    unsigned long long pairs[kSelectThreads / 32][2];
+    struct {
+      uint32_t sure[kSelectThreads], amb[kSelectThreads];  // marks of 32 blocks: taken, ambiguous
+    } marks;
+  };
   unsigned long long red[kSelectThreads / 32];
   unsigned long long found;
-  unsigned long long amb_key[kSelectAmbiguous];  // ambiguous candidates: the exact score's key,
-  int amb[kSelectAmbiguous];                     // the candidate's number
-  int amb_rank[kSelectAmbiguous];                // and its rank among them
-  int amb_count;
+  unsigned long long amb_key[kSelectAmbiguous];  // ambiguous blocks: the exact score's key
+  int amb[kSelectAmbiguous];                     // and the block
   int bin, above, in_bin;
 };
 
-// Sum over the block of a pair of counts packed as two 32-bit halves; every thread gets it.
-__device__ __forceinline__ unsigned long long block_sum(SelectShared& sh, unsigned long long v) {
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  __syncthreads();  // red is free
-  if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  unsigned long long s = 0;
-#pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) s += sh.red[w];
-  return s;
-}
-
-// Exclusive prefix over the block, in thread order, of such a pair.
-__device__ __forceinline__ unsigned long long block_prefix(SelectShared& sh, unsigned long long v) {
+// Exclusive prefix over the block, in thread order, of a pair of counts packed as two 32-bit
+// halves, and their total.
+__device__ __forceinline__ unsigned long long block_prefix(SelectShared& sh, unsigned long long v,
+                                                           unsigned long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long incl = v;
 #pragma unroll
@@ -400,11 +406,15 @@ __device__ __forceinline__ unsigned long long block_prefix(SelectShared& sh, uns
   __syncthreads();  // red is free
   if (lane == 31) sh.red[warp] = incl;
   __syncthreads();
-  unsigned long long s = incl - v;
+  unsigned long long before = incl - v;
+  total = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w)
-    if (w < warp) s += sh.red[w];
-  return s;
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    const unsigned long long r = sh.red[w];
+    if (w < warp) before += r;
+    total += r;
+  }
+  return before;
 }
 
 // The need-th largest (need >= 1) of the keys in [lo, hi] that key_of(i, &key) yields for i
@@ -423,13 +433,14 @@ __device__ __forceinline__ Key nth_largest(SelectShared& sh, F key_of, int n, in
       if (key_of(i, k) && k >= lo && k <= hi) atomicAdd(&sh.hist[static_cast<int>((k - lo) >> shift)], 1);
     }
     __syncthreads();
-    // bins from the top, four per thread
+    // bins from the top, a few per thread
     constexpr int kPer = kSelectBins / kSelectThreads;
     const int top = kSelectBins - 1 - kPer * threadIdx.x;
     int sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sum += sh.hist[top - j];
-    int above = static_cast<int>(block_prefix(sh, static_cast<unsigned long long>(sum)));
+    unsigned long long all;
+    int above = static_cast<int>(block_prefix(sh, static_cast<unsigned long long>(sum), all));
     if (above < need && above + sum >= need) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -499,6 +510,7 @@ __device__ __forceinline__ unsigned long long exact_key(const __nv_bfloat16* q, 
 __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ SelectShared sh;
   wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
   const int unit = blockIdx.x, b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = p.seq_lens[b];
@@ -524,90 +536,136 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
     for (int j = threadIdx.x; j < n; j += kSelectThreads) put(j, j);
     return;
   }
-  // candidates: blocks c0 .. c0 + count - 1, k of which are taken
-  const int c0 = p.first, count = n - p.first - p.last, k = p.top_k - p.first - p.last;
-  const float* scores = p.scores + static_cast<size_t>(unit) * p.max_blocks + c0;
-  unsigned long long* const keys64 = p.keys64 + static_cast<size_t>(unit) * p.max_blocks + c0;
+  const uint32_t* scores = p.scores + static_cast<size_t>(unit) * p.score_stride;  // 16-byte aligned
+  unsigned long long* const keys64 = p.keys64 + static_cast<size_t>(unit) * p.max_blocks;
   const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
-  const bool staged = count <= kSelectKeys;
+  const bool staged = n <= kSelectKeys;
+  auto forced = [&](int j) { return j < p.first || j >= n - p.last; };
+  auto key_at = [&](int j) { return staged ? sh.keys[j] : forced(j) ? kForced : __ldcg(scores + j); };
 
-  // keys and their range; the query's largest 1-norm and the bounds' largest magnitude
+  // keys and the candidates' range; the bounds' largest magnitude; the query's largest 1-norm
   uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-  for (int i = threadIdx.x; i < count; i += kSelectThreads) {
-    const uint32_t key = order_key(scores[i]);
-    if (staged) sh.keys[i] = key;
-    kmin = min(kmin, key);
-    kmax = max(kmax, key);
+  constexpr int kBatch = 4;
+  for (int j0 = 4 * threadIdx.x; j0 < n; j0 += 4 * kSelectThreads * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + 4 * kSelectThreads * u;
+      v[u] = j < n ? __ldcg(reinterpret_cast<const uint4*>(scores + j)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + 4 * kSelectThreads * u;
+      uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e >= n) continue;
+        if (forced(j + e)) {
+          w[e] = kForced;
+        } else {
+          kmin = min(kmin, w[e]);
+          kmax = max(kmax, w[e]);
+        }
+        if (staged) sh.keys[j + e] = w[e];
+      }
+    }
   }
   float mag = 0.f;
   for (int i = threadIdx.x; i < (n + kScoreTile - 1) / kScoreTile; i += kSelectThreads)
     mag = fmaxf(mag, p.tile_abs[static_cast<size_t>(unit) * p.tiles + i]);
   float q1 = 0.f;
-  for (int r = warp; r < p.nq; r += kSelectThreads / 32) {
+  for (int r = warp; r < p.nq; r += kSelectThreads / 32) {  // a row's D / 8 <= 32 lanes of 8 values
     float s = 0.f;
-    for (int d = lane; d < p.head_dim; d += 32) s += fabsf(__bfloat162float(q[static_cast<size_t>(r) * p.head_dim + d]));
+    if (lane < p.head_dim / 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(r) * p.head_dim + 8 * lane);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s += fabsf(__uint_as_float(w[e] << 16)) + fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
+    }
+#pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     q1 = fmaxf(q1, s);
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   const uint32_t mag_u = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
-  {
-    uint32_t* const w = reinterpret_cast<uint32_t*>(sh.hist);
-    if (lane == 0) {
-      w[4 * warp] = kmin;
-      w[4 * warp + 1] = kmax;
-      w[4 * warp + 2] = mag_u;
-      w[4 * warp + 3] = __float_as_uint(q1);
-    }
-    __syncthreads();
-    uint32_t m = 0u, q1u = 0u;
-#pragma unroll
-    for (int i = 0; i < kSelectThreads / 32; ++i) {
-      kmin = min(kmin, w[4 * i]);
-      kmax = max(kmax, w[4 * i + 1]);
-      m = max(m, w[4 * i + 2]);
-      q1u = max(q1u, w[4 * i + 3]);
-    }
-    mag = __uint_as_float(m);
-    q1 = __uint_as_float(q1u);
+  if (lane == 0) {
+    sh.pairs[warp][0] = (static_cast<unsigned long long>(kmin) << 32) | kmax;
+    sh.pairs[warp][1] = (static_cast<unsigned long long>(mag_u) << 32) | __float_as_uint(q1);
   }
-  const float err = static_cast<float>(p.head_dim) * 1.1920929e-7f * q1 * mag;  // E
+  __syncthreads();
+  uint32_t mu = 0u, qu = 0u;
+#pragma unroll
+  for (int i = 0; i < kSelectThreads / 32; ++i) {
+    kmin = min(kmin, static_cast<uint32_t>(sh.pairs[i][0] >> 32));
+    kmax = max(kmax, static_cast<uint32_t>(sh.pairs[i][0]));
+    mu = max(mu, static_cast<uint32_t>(sh.pairs[i][1] >> 32));
+    qu = max(qu, static_cast<uint32_t>(sh.pairs[i][1]));
+  }
+  const float err = static_cast<float>(p.head_dim) * 1.1920929e-7f * __uint_as_float(qu) * __uint_as_float(mu);  // E
 
-  auto key_at = [&](int i) { return staged ? sh.keys[i] : order_key(scores[i]); };
   float above = INFINITY, below = INFINITY;  // scores beyond `above` are in, under `below` out
-  int ties = 0;                              // how many ambiguous blocks are taken
-  int ambiguous = 0;
-  bool exact = false;                        // whether exact sums decide which
-  unsigned long long t64 = 0ull;
+  const int k = p.top_k - p.first - p.last;
   if (k > 0) {
     int rank = k;
     const float T = key_score(nth_largest<uint32_t>(
-        sh, [&](int i, uint32_t& key) { key = key_at(i); return true; }, count, rank, kmin, kmax));
+        sh, [&](int j, uint32_t& key) { key = key_at(j); return key != kForced; }, n, rank, kmin, kmax));
     above = T + 2.f * err;
     below = T - 2.f * err;
-    if (threadIdx.x == 0) sh.amb_count = 0;
+  }
+  // marks of the 32 blocks of each word of a segment: taken, ambiguous
+  auto is_amb = [&](uint32_t key) {
+    const float s = key_score(key);
+    return key != kForced && k > 0 && !(s > above) && !(s < below);
+  };
+  auto mark = [&](int seg) {
     __syncthreads();
-    int sure = 0;
-    for (int i = threadIdx.x; i < count; i += kSelectThreads) {
-      const float s = key_score(key_at(i));
-      if (s > above) {
-        ++sure;
-      } else if (!(s < below)) {
-        const int at = atomicAdd(&sh.amb_count, 1);
-        if (at < kSelectAmbiguous) sh.amb[at] = i;
+    for (int w = warp; w < kSelectThreads && seg + 32 * w < n; w += kSelectThreads / 32) {
+      const int j = seg + 32 * w + lane;
+      const uint32_t key = j < n ? key_at(j) : 0u;
+      const bool sure = j < n && (key == kForced || key_score(key) > above);
+      const bool amb = j < n && is_amb(key);
+      const uint32_t ms = __ballot_sync(0xffffffffu, sure), ma = __ballot_sync(0xffffffffu, amb);
+      if (lane == 0) {
+        sh.marks.sure[w] = ms;
+        sh.marks.amb[w] = ma;
       }
     }
-    ties = k - static_cast<int>(block_sum(sh, static_cast<unsigned long long>(sure)));
-    ambiguous = sh.amb_count;
-    exact = ambiguous > ties && err != 0.f;  // err = 0: every product is 0, the scores are exact
-    auto bounds_of = [&](int i) -> const __nv_bfloat16* {  // nullptr for a bad block
-      const int ph = table[c0 + i];
+    __syncthreads();
+  };
+  // this thread's word of a segment, and the counts before it
+  uint32_t my_sure = 0u, my_amb = 0u;
+  auto count = [&](int seg, unsigned long long& total) {
+    const bool on = seg + 32 * static_cast<int>(threadIdx.x) < n;
+    my_sure = on ? sh.marks.sure[threadIdx.x] : 0u;
+    my_amb = on ? sh.marks.amb[threadIdx.x] : 0u;
+    return block_prefix(sh, (static_cast<unsigned long long>(__popc(my_sure)) << 32) | __popc(my_amb), total);
+  };
+  int sure = 0, ambiguous = 0;
+  unsigned long long before = 0;
+  for (int seg = 0; seg < n; seg += kSegment) {
+    unsigned long long total;
+    mark(seg);
+    before = count(seg, total);
+    int at = ambiguous + static_cast<int>(before & 0xFFFFFFFFull);
+    for (uint32_t m = my_amb; m && at < kSelectAmbiguous; m &= m - 1)
+      sh.amb[at++] = seg + 32 * threadIdx.x + __ffs(m) - 1;
+    sure += static_cast<int>(total >> 32);
+    ambiguous += static_cast<int>(total & 0xFFFFFFFFull);
+  }
+  int ties = p.top_k - sure;  // how many ambiguous blocks are taken, in order where exact sums tie
+  bool remark = n > kSegment;
+  unsigned long long t64 = 0ull;
+  const bool exact = ambiguous > ties && err != 0.f;  // err = 0: every product is 0, the scores are exact
+  const bool few = ambiguous <= kSelectAmbiguous;
+  if (exact) {
+    auto bounds_of = [&](int j) -> const __nv_bfloat16* {  // nullptr for a bad block
+      const int ph = table[j];
       if (static_cast<unsigned>(ph) >= static_cast<unsigned>(p.num_blocks)) return nullptr;
       return p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * p.head_dim;
     };
-    if (exact && ambiguous <= kSelectAmbiguous) {
-      // few, as a rule: a warp per (block, query row), then a rank by counting
+    if (few) {  // as a rule: a warp per (block, query row), then a rank by counting
       for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) sh.amb_key[i] = 0ull;
       __syncthreads();
       for (int w = warp; w < ambiguous * p.nq; w += kSelectThreads / 32) {
@@ -618,96 +676,110 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
         if (lane == 0) atomicMax(&sh.amb_key[at], key);
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
-        const unsigned long long key = sh.amb_key[i];
-        const int at = sh.amb[i];
-        int rank = 0;
-        for (int j = 0; j < ambiguous; ++j) rank += sh.amb_key[j] > key || (sh.amb_key[j] == key && sh.amb[j] < at);
-        sh.amb_rank[i] = rank;
-      }
-      __syncthreads();
-    } else if (exact) {
-      unsigned long long lo64 = ~0ull, hi64 = 0ull;  // range of this warp's keys
-      for (int i0 = warp * 32; i0 < count; i0 += kSelectThreads) {
-        const int i = i0 + lane;
-        bool amb = false;
-        if (i < count) {
-          const float s = key_score(key_at(i));
-          amb = !(s > above) && !(s < below);
+      if (!remark) {  // unmark those that are not taken
+        for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
+          int rank = 0;  // the list is in block order
+          for (int o = 0; o < ambiguous; ++o)
+            rank += sh.amb_key[o] > sh.amb_key[i] || (sh.amb_key[o] == sh.amb_key[i] && o < i);
+          if (rank >= ties) atomicAnd(&sh.marks.amb[sh.amb[i] / 32], ~(1u << (sh.amb[i] & 31)));
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, amb);
+        __syncthreads();
+      }
+    } else {
+      unsigned long long lo64 = ~0ull, hi64 = 0ull;  // range of this warp's keys
+      for (int i0 = warp * 32; i0 < n; i0 += kSelectThreads) {
+        uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < n && is_amb(key_at(min(i0 + lane, n - 1))));
         while (todo) {
-          const int src = __ffs(todo) - 1;
+          const int j = i0 + __ffs(todo) - 1;
           todo &= todo - 1;
-          const __nv_bfloat16* bd = bounds_of(i0 + src);
+          const __nv_bfloat16* bd = bounds_of(j);
           unsigned long long key = kLowestKey;
           for (int r = 0; bd && r < p.nq; ++r) {
             const unsigned long long of = exact_key(q + static_cast<size_t>(r) * p.head_dim, bd, p.head_dim, lane);
             key = of > key ? of : key;
           }
-          if (lane == 0) keys64[i0 + src] = key;
+          if (lane == 0) keys64[j] = key;
           lo64 = key < lo64 ? key : lo64;
           hi64 = key > hi64 ? key : hi64;
         }
       }
-      __syncthreads();  // the keys are written, the histogram's space is free
-      {
-        unsigned long long* const w = reinterpret_cast<unsigned long long*>(sh.hist);
-        if (lane == 0) {
-          w[2 * warp] = lo64;
-          w[2 * warp + 1] = hi64;
-        }
-        __syncthreads();
+      __syncthreads();  // the keys are written, the marks' space is free
+      if (lane == 0) {
+        sh.pairs[warp][0] = lo64;
+        sh.pairs[warp][1] = hi64;
+      }
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSelectThreads / 32; ++i) {
-          lo64 = w[2 * i] < lo64 ? w[2 * i] : lo64;
-          hi64 = w[2 * i + 1] > hi64 ? w[2 * i + 1] : hi64;
-        }
+      for (int i = 0; i < kSelectThreads / 32; ++i) {
+        lo64 = sh.pairs[i][0] < lo64 ? sh.pairs[i][0] : lo64;
+        hi64 = sh.pairs[i][1] > hi64 ? sh.pairs[i][1] : hi64;
       }
       t64 = nth_largest<unsigned long long>(
           sh,
-          [&](int i, unsigned long long& key) {
-            const float s = key_score(key_at(i));
-            if (s > above || s < below) return false;
-            key = keys64[i];
+          [&](int j, unsigned long long& key) {
+            if (!is_amb(key_at(j))) return false;
+            key = keys64[j];
             return true;
           },
-          count, ties, lo64, hi64);
+          n, ties, lo64, hi64);
+      remark = true;
     }
   }
-  const int ties_all = ties;
-  // 2: taken; 1: taken while `ties` last, in order; 0: not
-  auto status = [&](int j) {
-    const int i = j - c0;
-    if (i < 0 || i >= count) return 2;
-    if (k == 0) return 0;
-    const float s = key_score(key_at(i));
-    if (s > above) return 2;
-    if (s < below) return 0;
-    if (!exact) return 1;
-    if (ambiguous <= kSelectAmbiguous) {
-      for (int at = 0; at < ambiguous; ++at)
-        if (sh.amb[at] == i) return sh.amb_rank[at] < ties_all ? 2 : 0;
+  // Places: each thread its word of a segment. The chosen go to a list first where it fits,
+  // so that their table entries are read all at once.
+  const bool listed = p.top_k <= kSelectKeys;
+  int* const list = reinterpret_cast<int*>(sh.keys);
+  int base = 0, tied = 0;  // blocks placed, ambiguous ones met so far
+  for (int seg = 0; seg < n; seg += kSegment) {
+    if (remark) {
+      mark(seg);
+      if (exact && few) {  // several segments: unmark this one's
+        for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
+          const int j = sh.amb[i] - seg;
+          if (j < 0 || j >= kSegment) continue;
+          int rank = 0;
+          for (int o = 0; o < ambiguous; ++o)
+            rank += sh.amb_key[o] > sh.amb_key[i] || (sh.amb_key[o] == sh.amb_key[i] && o < i);
+          if (rank >= ties) atomicAnd(&sh.marks.amb[j / 32], ~(1u << (j & 31)));
+        }
+      } else if (exact) {  // above the threshold: sure; at it: in order; below: out
+        for (int w = threadIdx.x; w < kSelectThreads && seg + 32 * w < n; w += kSelectThreads) {
+          for (uint32_t m = sh.marks.amb[w]; m; m &= m - 1) {
+            const uint32_t bit = m & (0u - m);
+            const unsigned long long key = keys64[seg + 32 * w + __ffs(m) - 1];
+            if (key > t64) sh.marks.sure[w] |= bit;
+            if (key != t64) sh.marks.amb[w] &= ~bit;
+          }
+        }
+      }
+      __syncthreads();
     }
-    const unsigned long long key = keys64[i];
-    return key > t64 ? 2 : key == t64 ? 1 : 0;
-  };
-  // each thread a run of blocks; the places by a prefix over (taken, tied) counts
-  const int per = (n + kSelectThreads - 1) / kSelectThreads;
-  const int j0 = min(n, static_cast<int>(threadIdx.x) * per), j1 = min(n, j0 + per);
-  unsigned long long c = 0;
-  for (int j = j0; j < j1; ++j) {
-    const int s = status(j);
-    c += s == 2 ? (1ull << 32) : static_cast<unsigned long long>(s);
+    unsigned long long total;
+    before = count(seg, total);
+    int s = static_cast<int>(before >> 32), a = tied + static_cast<int>(before & 0xFFFFFFFFull);
+    const int placed = base;  // sure ones of earlier segments
+    for (uint32_t m = my_sure | my_amb; m; m &= m - 1) {
+      const uint32_t bit = m & (0u - m);
+      const int j = seg + 32 * threadIdx.x + __ffs(m) - 1;
+      const bool is_sure = (my_sure & bit) != 0u;
+      if (is_sure || a < ties) {
+        const int pos = placed + s + min(a, ties);
+        if (listed) {
+          list[pos] = j;
+        } else {
+          put(pos, j);
+        }
+      }
+      s += is_sure;
+      a += !is_sure;
+    }
+    base += static_cast<int>(total >> 32);
+    tied += static_cast<int>(total & 0xFFFFFFFFull);
+    if (seg + kSegment < n) __syncthreads();
   }
-  c = block_prefix(sh, c);
-  int sure = static_cast<int>(c >> 32), tied = static_cast<int>(c & 0xFFFFFFFFull);
-  for (int j = j0; j < j1; ++j) {
-    const int s = status(j);
-    if (s == 2 || (s == 1 && tied < ties)) put(sure + min(tied, ties), j);
-    sure += s == 2;
-    tied += s == 1;
-  }
+  if (!listed) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.top_k; i += kSelectThreads) put(i, list[i]);
 }
 
 template <int D>
