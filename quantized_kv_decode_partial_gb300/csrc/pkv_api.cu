@@ -1196,13 +1196,13 @@ int pkv_select_blocks(const pkv_pool_layout* layout, const pkv_decode_params* pa
     return PKV_ERR_MISALIGNED;
   const size_t need = sparse_workspace(layout, params, sparse).select_bytes;
   if (need && (!workspace || workspace_bytes < need)) return PKV_ERR_WORKSPACE_TOO_SMALL;
-  int sms = 0;
-  rc = device_sm_count(&sms);
+  int sms = 0, dev = 0;
+  rc = device_sm_count(&sms, &dev);
   if (rc) return rc;
   (void)cudaGetLastError();
   cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
                                                    chosen_tables, chosen_lens, workspace, error_flag),
-                                     params->num_seqs, sms, static_cast<cudaStream_t>(stream));
+                                     params->num_seqs, sms, dev, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("block choice launch", e);
   return PKV_OK;
 }
@@ -1247,8 +1247,8 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
   char* const ws = static_cast<char*>(workspace);
   int32_t* const tables = reinterpret_cast<int32_t*>(ws + w.tables);
   int32_t* const lens = reinterpret_cast<int32_t*>(ws + w.lens);
-  int sms = 0;
-  rc = device_sm_count(&sms);
+  int sms = 0, dev = 0;
+  rc = device_sm_count(&sms, &dev);
   if (rc) return rc;
   pkv_pool_layout vl;
   pkv_decode_params vp;
@@ -1262,7 +1262,7 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
   (void)cudaGetLastError();
   cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
                                                    tables, lens, workspace, error_flag),
-                                     params->num_seqs, sms, st);
+                                     params->num_seqs, sms, dev, st);
   if (e != cudaSuccess) return cuda_fail("block choice launch", e);
   return launch_prepared(pd, st);
 }

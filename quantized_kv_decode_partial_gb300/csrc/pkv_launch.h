@@ -83,6 +83,6 @@ cudaError_t launch_append_blocks(const AppendBlockParams& p, int num_seqs, cudaS
 
 cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_seqs, cudaStream_t stream);
 int select_tiles(int max_blocks);  // tiles of SelectParams for a table of this width
-cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, cudaStream_t stream);
+cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device, cudaStream_t stream);
 
 }  // namespace pkv

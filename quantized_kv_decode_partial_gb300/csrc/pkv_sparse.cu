@@ -11,6 +11,9 @@
 // every (sequence, KV head) as a sequence of its chosen blocks in order.
 //
 // Three kernels: the bounds' upkeep after an append, the scores, and the choice.
+#include <algorithm>
+#include <atomic>
+
 #include "pkv_launch.h"
 
 namespace pkv {
@@ -232,16 +235,17 @@ cudaError_t launch_bounds_of(const BoundsParams& p, int num_seqs, cudaStream_t s
 // tile, its next tile's bounds are on their way into L2, which keeps enough bytes in flight
 // with the 16 warps that the fragments' registers leave room for.
 //
-// Scores are stored as integers of the same order, NaN lowest.
-__device__ __forceinline__ uint32_t order_key(float s) {  // NaN lowest, then by value
-  if (!(s == s)) return 0u;
+// Scores are stored as integers of the same order, NaN as -infinity.
+constexpr uint32_t kLowestScore = 0x007FFFFFu;  // of -infinity, and of NaN
+__device__ __forceinline__ uint32_t order_key(float s) {
+  if (!(s == s)) return kLowestScore;
   const uint32_t u = __float_as_uint(s + 0.f);  // -0 as 0
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float key_score(uint32_t k) {
-  if (k == 0u) return -INFINITY;
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTile = 16;  // blocks per warp and step
 
@@ -368,79 +372,79 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 // that holds the k-th until it is one value (two rounds as a rule): spread scores meet few
 // bank conflicts, which radix digits of nearby floats would. The marks of 32 blocks at a time
 // (ballots) and a prefix over their counts then give each taken block its place.
-constexpr int kSelectThreads = 512;
+//
+// The CTA's time is a chain of dependent steps (loads, barriers, prefixes), so it takes as
+// few warps as its blocks need: 8 for tables of up to 2048 blocks, 32 above.
 constexpr int kSelectBins = 2048;
-constexpr int kSelectKeys = 7680;  // scores kept in shared memory; more are read again from L2
-constexpr int kSelectAmbiguous = 256;  // ambiguous blocks ranked in shared memory; more by way of the workspace
-
+constexpr int kSelectMostKeys = 24576;  // scores kept in shared memory; more are read again from L2
+constexpr int kSelectAmbiguous = 256;   // ambiguous blocks ranked in shared memory; more by way of the workspace
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is always taken; no score has it
-constexpr int kSegment = 32 * kSelectThreads;  // blocks whose marks fit shared memory at once, a word per thread
 
+template <int T>
 struct SelectShared {
-  uint32_t keys[kSelectKeys];  // later the chosen blocks
+  static constexpr int kSegment = 32 * T;  // blocks whose marks fit at once, a word per thread
   union {
     int hist[kSelectBins];
-    unsigned long long pairs[kSelectThreads / 32][2];
+    unsigned long long pairs[T / 32][2];
     struct {
-      uint32_t sure[kSelectThreads], amb[kSelectThreads];  // marks of 32 blocks: taken, ambiguous
+      uint32_t sure[T], amb[T];  // marks of 32 blocks: taken, ambiguous
     } marks;
   };
-  unsigned long long red[kSelectThreads / 32];
+  uint32_t red[32];
   unsigned long long found;
   unsigned long long amb_key[kSelectAmbiguous];  // ambiguous blocks: the exact score's key
   int amb[kSelectAmbiguous];                     // and the block
   int bin, above, in_bin;
 };
 
-// Exclusive prefix over the block, in thread order, of a pair of counts packed as two 32-bit
-// halves, and their total.
-__device__ __forceinline__ unsigned long long block_prefix(SelectShared& sh, unsigned long long v,
-                                                           unsigned long long& total) {
+// Exclusive prefix over the block, in thread order, and the total.
+template <int T>
+__device__ __forceinline__ uint32_t block_prefix(SelectShared<T>& sh, uint32_t v, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
   }
   __syncthreads();  // red is free
   if (lane == 31) sh.red[warp] = incl;
   __syncthreads();
-  unsigned long long before = incl - v;
-  total = 0;
+  uint32_t w = lane < T / 32 ? sh.red[lane] : 0u;  // every warp scans the warps' sums
+  const uint32_t own = w;
 #pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    const unsigned long long r = sh.red[w];
-    if (w < warp) before += r;
-    total += r;
+  for (int d = 1; d < T / 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += o;
   }
-  return before;
+  total = __shfl_sync(0xffffffffu, w, T / 32 - 1);
+  return __shfl_sync(0xffffffffu, w - own, warp) + incl - v;
 }
 
 // The need-th largest (need >= 1) of the keys in [lo, hi] that key_of(i, &key) yields for i
 // in [0, n); `need` becomes its rank among the keys equal to it. Every thread gets it.
-template <typename Key, typename F>
-__device__ __forceinline__ Key nth_largest(SelectShared& sh, F key_of, int n, int& need, Key lo, Key hi) {
+template <int T, typename Key, typename F>
+__device__ __forceinline__ Key nth_largest(SelectShared<T>& sh, F key_of, int n, int& need, Key lo, Key hi) {
   for (;;) {
     const Key span = hi - lo;
     const int width = sizeof(Key) == 8 ? 64 - __clzll(static_cast<long long>(span)) : 32 - __clz(static_cast<int>(span));
     const int shift = width > 11 ? width - 11 : 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) sh.hist[i] = 0;
+    for (int i = threadIdx.x; i < kSelectBins; i += T) sh.hist[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
       Key k;
       if (key_of(i, k) && k >= lo && k <= hi) atomicAdd(&sh.hist[static_cast<int>((k - lo) >> shift)], 1);
     }
     __syncthreads();
     // bins from the top, a few per thread
-    constexpr int kPer = kSelectBins / kSelectThreads;
+    constexpr int kPer = kSelectBins / T;
     const int top = kSelectBins - 1 - kPer * threadIdx.x;
     int sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sum += sh.hist[top - j];
-    unsigned long long all;
-    int above = static_cast<int>(block_prefix(sh, static_cast<unsigned long long>(sum), all));
+    uint32_t all;
+    int above = static_cast<int>(block_prefix(sh, static_cast<uint32_t>(sum), all));
     if (above < need && above + sum >= need) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -460,7 +464,7 @@ __device__ __forceinline__ Key nth_largest(SelectShared& sh, F key_of, int n, in
     const Key end = lo + ((static_cast<Key>(1) << shift) - 1);
     hi = end < hi ? end : hi;
     if (sh.in_bin == 1) {  // alone in its bin
-      for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+      for (int i = threadIdx.x; i < n; i += T) {
         Key k;
         if (key_of(i, k) && k >= lo && k <= hi) sh.found = static_cast<unsigned long long>(k);
       }
@@ -485,35 +489,72 @@ __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   return Pair{h, __fsub_rn(l, __fsub_rn(h, s))};
 }
 
-constexpr unsigned long long kLowestKey = 1ull;  // of a NaN score and of a bad block
+// of a NaN score and of a bad block
+constexpr unsigned long long kLowestKey = static_cast<unsigned long long>(kLowestScore) << 32;
+constexpr int kExactRows = 4;  // query rows summed side by side, so that their chains of additions overlap
 
-// u_j of one query row as an ordered integer, by one warp: the products of bf16 values are
-// exact in f32. Pairs order by hi, then by lo.
-__device__ __forceinline__ unsigned long long exact_key(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int D,
-                                                        int lane) {
-  Pair s{0.f, 0.f};
+// The largest u_j of query rows r0 .. r0 + kExactRows - 1 (within nq) as an ordered integer,
+// by one warp: the products of bf16 values are exact in f32 (above 2^-134). Pairs order by
+// hi, then by lo.
+__device__ __forceinline__ unsigned long long exact_key(const __nv_bfloat16* q, int r0, int nq,
+                                                        const __nv_bfloat16* bounds, int D, int lane) {
+  Pair s[kExactRows];
+#pragma unroll
+  for (int r = 0; r < kExactRows; ++r) s[r] = Pair{0.f, 0.f};
   for (int d = 2 * lane; d < D; d += 64) {
-    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(q + d);
     const __nv_bfloat162 l = *reinterpret_cast<const __nv_bfloat162*>(bounds + d);
     const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(bounds + D + d);
-    const float x0 = __low2float(x), x1 = __high2float(x);
-    s = pair_add(s, Pair{fmaxf(x0 * __low2float(l), x0 * __low2float(h)), 0.f});
-    s = pair_add(s, Pair{fmaxf(x1 * __high2float(l), x1 * __high2float(h)), 0.f});
+#pragma unroll
+    for (int r = 0; r < kExactRows; ++r) {
+      const int row = r0 + r < nq ? r0 + r : nq - 1;
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(q + static_cast<size_t>(row) * D + d);
+      const float x0 = __low2float(x), x1 = __high2float(x);
+      s[r] = pair_add(s[r], Pair{fmaxf(x0 * __low2float(l), x0 * __low2float(h)), 0.f});
+      s[r] = pair_add(s[r], Pair{fmaxf(x1 * __high2float(l), x1 * __high2float(h)), 0.f});
+    }
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1)
-    s = pair_add(s, Pair{__shfl_xor_sync(0xffffffffu, s.hi, k), __shfl_xor_sync(0xffffffffu, s.lo, k)});
-  const uint32_t hi = order_key(s.hi);
-  return hi == 0u ? kLowestKey : (static_cast<unsigned long long>(hi) << 32) | order_key(s.lo);
+#pragma unroll
+    for (int r = 0; r < kExactRows; ++r)
+      s[r] = pair_add(s[r], Pair{__shfl_xor_sync(0xffffffffu, s[r].hi, k), __shfl_xor_sync(0xffffffffu, s[r].lo, k)});
+  unsigned long long best = kLowestKey;
+#pragma unroll
+  for (int r = 0; r < kExactRows; ++r) {
+    const uint32_t hi = order_key(s[r].hi);
+    const unsigned long long key =
+        hi == kLowestScore ? kLowestKey : (static_cast<unsigned long long>(hi) << 32) | order_key(s[r].lo);
+    best = key > best ? key : best;
+  }
+  return best;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ SelectShared sh;
+template <int T>
+__global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelectShared<T> sh;
+  extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: the scores, later the chosen blocks
+  constexpr int kSegment = SelectShared<T>::kSegment;
   wait_for_prerequisite_grids();
   allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
   const int unit = blockIdx.x, b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = p.seq_lens[b];
+  const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
+  // the query's largest 1-norm, while the length arrives: a row's D / 8 <= 32 lanes hold 8 values each
+  float q1 = 0.f;
+  for (int r = warp; r < p.nq; r += T / 32) {
+    float s = 0.f;
+    if (lane < p.head_dim / 8) {
+      const uint4 v = ld_nc_keep_v4(q + static_cast<size_t>(r) * p.head_dim + 8 * lane);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s += fabsf(__uint_as_float(w[e] << 16)) + fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    q1 = fmaxf(q1, s);
+  }
   int32_t* const out_blocks = p.out_blocks ? p.out_blocks + static_cast<size_t>(unit) * p.top_k : nullptr;
   int32_t* const out_table = p.out_tables + static_cast<size_t>(unit) * p.top_k;
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
@@ -531,31 +572,34 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
     out_table[pos] = ok ? ph * p.num_kv_heads + h : -1;
     if (j >= 0 && !ok && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
   };
-  for (int i = taken + threadIdx.x; i < p.top_k; i += kSelectThreads) put(i, -1);
+  for (int i = taken + threadIdx.x; i < p.top_k; i += T) put(i, -1);
   if (n <= p.top_k) {
-    for (int j = threadIdx.x; j < n; j += kSelectThreads) put(j, j);
+    for (int j = threadIdx.x; j < n; j += T) put(j, j);
     return;
   }
   const uint32_t* scores = p.scores + static_cast<size_t>(unit) * p.score_stride;  // 16-byte aligned
   unsigned long long* const keys64 = p.keys64 + static_cast<size_t>(unit) * p.max_blocks;
-  const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
-  const bool staged = n <= kSelectKeys;
+  const bool staged = n <= p.key_space;
   auto forced = [&](int j) { return j < p.first || j >= n - p.last; };
-  auto key_at = [&](int j) { return staged ? sh.keys[j] : forced(j) ? kForced : __ldcg(scores + j); };
+  auto key_at = [&](int j) { return staged ? sh_keys[j] : forced(j) ? kForced : __ldcg(scores + j); };
 
-  // keys and the candidates' range; the bounds' largest magnitude; the query's largest 1-norm
+  // keys and the candidates' range; the bounds' largest magnitude
   uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-  constexpr int kBatch = 4;
-  for (int j0 = 4 * threadIdx.x; j0 < n; j0 += 4 * kSelectThreads * kBatch) {
+  float mag = 0.f;
+  const int tiles = (n + kScoreTile - 1) / kScoreTile;
+  constexpr int kBatch = 2;
+  for (int j0 = 4 * threadIdx.x, t0 = threadIdx.x; j0 < n; j0 += 4 * T * kBatch) {
     uint4 v[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int j = j0 + 4 * kSelectThreads * u;
+      const int j = j0 + 4 * T * u;
       v[u] = j < n ? __ldcg(reinterpret_cast<const uint4*>(scores + j)) : make_uint4(0u, 0u, 0u, 0u);
     }
+    for (; t0 < tiles && t0 < j0 + 4 * T * kBatch; t0 += T)
+      mag = fmaxf(mag, __ldcg(p.tile_abs + static_cast<size_t>(unit) * p.tiles + t0));
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int j = j0 + 4 * kSelectThreads * u;
+      const int j = j0 + 4 * T * u;
       uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -566,26 +610,9 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
           kmin = min(kmin, w[e]);
           kmax = max(kmax, w[e]);
         }
-        if (staged) sh.keys[j + e] = w[e];
+        if (staged) sh_keys[j + e] = w[e];
       }
     }
-  }
-  float mag = 0.f;
-  for (int i = threadIdx.x; i < (n + kScoreTile - 1) / kScoreTile; i += kSelectThreads)
-    mag = fmaxf(mag, p.tile_abs[static_cast<size_t>(unit) * p.tiles + i]);
-  float q1 = 0.f;
-  for (int r = warp; r < p.nq; r += kSelectThreads / 32) {  // a row's D / 8 <= 32 lanes of 8 values
-    float s = 0.f;
-    if (lane < p.head_dim / 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(r) * p.head_dim + 8 * lane);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s += fabsf(__uint_as_float(w[e] << 16)) + fabsf(__uint_as_float(w[e] & 0xFFFF0000u));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    q1 = fmaxf(q1, s);
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
@@ -596,37 +623,39 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
   }
   __syncthreads();
   uint32_t mu = 0u, qu = 0u;
-#pragma unroll
-  for (int i = 0; i < kSelectThreads / 32; ++i) {
-    kmin = min(kmin, static_cast<uint32_t>(sh.pairs[i][0] >> 32));
-    kmax = max(kmax, static_cast<uint32_t>(sh.pairs[i][0]));
-    mu = max(mu, static_cast<uint32_t>(sh.pairs[i][1] >> 32));
-    qu = max(qu, static_cast<uint32_t>(sh.pairs[i][1]));
+  if (lane < T / 32) {
+    const unsigned long long x = sh.pairs[lane][0], y = sh.pairs[lane][1];
+    kmin = static_cast<uint32_t>(x >> 32);
+    kmax = static_cast<uint32_t>(x);
+    mu = static_cast<uint32_t>(y >> 32);
+    qu = static_cast<uint32_t>(y);
   }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  mu = __reduce_max_sync(0xffffffffu, mu);
+  qu = __reduce_max_sync(0xffffffffu, qu);
   const float err = static_cast<float>(p.head_dim) * 1.1920929e-7f * __uint_as_float(qu) * __uint_as_float(mu);  // E
 
-  float above = INFINITY, below = INFINITY;  // scores beyond `above` are in, under `below` out
+  // keys over `above` are taken, under `below` not; the ones between are ambiguous
+  uint32_t above = kForced - 1u, below = kForced;
   const int k = p.top_k - p.first - p.last;
   if (k > 0) {
     int rank = k;
-    const float T = key_score(nth_largest<uint32_t>(
+    const float s = key_score(nth_largest<T, uint32_t>(
         sh, [&](int j, uint32_t& key) { key = key_at(j); return key != kForced; }, n, rank, kmin, kmax));
-    above = T + 2.f * err;
-    below = T - 2.f * err;
+    const float hi = s + 2.f * err, lo = s - 2.f * err;  // NaN past infinity: then every score is ambiguous
+    above = hi == hi ? order_key(hi) : kForced - 1u;
+    below = lo == lo ? order_key(lo) : 0u;
   }
+  auto is_amb = [&](uint32_t key) { return key <= above && key >= below; };
   // marks of the 32 blocks of each word of a segment: taken, ambiguous
-  auto is_amb = [&](uint32_t key) {
-    const float s = key_score(key);
-    return key != kForced && k > 0 && !(s > above) && !(s < below);
-  };
   auto mark = [&](int seg) {
     __syncthreads();
-    for (int w = warp; w < kSelectThreads && seg + 32 * w < n; w += kSelectThreads / 32) {
+    for (int w = warp; w < T && seg + 32 * w < n; w += T / 32) {
       const int j = seg + 32 * w + lane;
       const uint32_t key = j < n ? key_at(j) : 0u;
-      const bool sure = j < n && (key == kForced || key_score(key) > above);
-      const bool amb = j < n && is_amb(key);
-      const uint32_t ms = __ballot_sync(0xffffffffu, sure), ma = __ballot_sync(0xffffffffu, amb);
+      const uint32_t ms = __ballot_sync(0xffffffffu, j < n && key > above);
+      const uint32_t ma = __ballot_sync(0xffffffffu, j < n && is_amb(key));
       if (lane == 0) {
         sh.marks.sure[w] = ms;
         sh.marks.amb[w] = ma;
@@ -634,68 +663,71 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
     }
     __syncthreads();
   };
-  // this thread's word of a segment, and the counts before it
+  // this thread's word of a segment, and the counts before it: taken in the high half,
+  // ambiguous in the low half (a segment holds at most 2^15 blocks)
   uint32_t my_sure = 0u, my_amb = 0u;
-  auto count = [&](int seg, unsigned long long& total) {
+  auto count = [&](int seg, uint32_t& total) {
     const bool on = seg + 32 * static_cast<int>(threadIdx.x) < n;
     my_sure = on ? sh.marks.sure[threadIdx.x] : 0u;
     my_amb = on ? sh.marks.amb[threadIdx.x] : 0u;
-    return block_prefix(sh, (static_cast<unsigned long long>(__popc(my_sure)) << 32) | __popc(my_amb), total);
+    return block_prefix(sh, (static_cast<uint32_t>(__popc(my_sure)) << 16) | __popc(my_amb), total);
   };
   int sure = 0, ambiguous = 0;
-  unsigned long long before = 0;
+  uint32_t before = 0u, total = 0u;
   for (int seg = 0; seg < n; seg += kSegment) {
-    unsigned long long total;
     mark(seg);
     before = count(seg, total);
-    int at = ambiguous + static_cast<int>(before & 0xFFFFFFFFull);
+    int at = ambiguous + static_cast<int>(before & 0xFFFFu);
     for (uint32_t m = my_amb; m && at < kSelectAmbiguous; m &= m - 1)
       sh.amb[at++] = seg + 32 * threadIdx.x + __ffs(m) - 1;
-    sure += static_cast<int>(total >> 32);
-    ambiguous += static_cast<int>(total & 0xFFFFFFFFull);
+    sure += static_cast<int>(total >> 16);
+    ambiguous += static_cast<int>(total & 0xFFFFu);
   }
   int ties = p.top_k - sure;  // how many ambiguous blocks are taken, in order where exact sums tie
-  bool remark = n > kSegment;
   unsigned long long t64 = 0ull;
   const bool exact = ambiguous > ties && err != 0.f;  // err = 0: every product is 0, the scores are exact
   const bool few = ambiguous <= kSelectAmbiguous;
+  bool remark = n > kSegment, recount = remark || exact;
+  const int row_groups = (p.nq + kExactRows - 1) / kExactRows;
+  // rank of ambiguous block i among them; the list is in block order
+  auto rank_of = [&](int i) {
+    int rank = 0;
+    for (int o = 0; o < ambiguous; ++o)
+      rank += sh.amb_key[o] > sh.amb_key[i] || (sh.amb_key[o] == sh.amb_key[i] && o < i);
+    return rank;
+  };
   if (exact) {
     auto bounds_of = [&](int j) -> const __nv_bfloat16* {  // nullptr for a bad block
       const int ph = table[j];
       if (static_cast<unsigned>(ph) >= static_cast<unsigned>(p.num_blocks)) return nullptr;
       return p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * p.head_dim;
     };
-    if (few) {  // as a rule: a warp per (block, query row), then a rank by counting
-      for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) sh.amb_key[i] = 0ull;
+    if (few) {  // as a rule: a warp per (block, query rows), then a rank by counting
+      for (int i = threadIdx.x; i < ambiguous; i += T) sh.amb_key[i] = 0ull;
       __syncthreads();
-      for (int w = warp; w < ambiguous * p.nq; w += kSelectThreads / 32) {
-        const int at = w / p.nq, r = w - at * p.nq;
+      for (int w = warp; w < ambiguous * row_groups; w += T / 32) {
+        const int at = w / row_groups, r = w - at * row_groups;
         const __nv_bfloat16* bd = bounds_of(sh.amb[at]);
-        const unsigned long long key =
-            bd ? exact_key(q + static_cast<size_t>(r) * p.head_dim, bd, p.head_dim, lane) : kLowestKey;
+        const unsigned long long key = bd ? exact_key(q, r * kExactRows, p.nq, bd, p.head_dim, lane) : kLowestKey;
         if (lane == 0) atomicMax(&sh.amb_key[at], key);
       }
       __syncthreads();
       if (!remark) {  // unmark those that are not taken
-        for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
-          int rank = 0;  // the list is in block order
-          for (int o = 0; o < ambiguous; ++o)
-            rank += sh.amb_key[o] > sh.amb_key[i] || (sh.amb_key[o] == sh.amb_key[i] && o < i);
-          if (rank >= ties) atomicAnd(&sh.marks.amb[sh.amb[i] / 32], ~(1u << (sh.amb[i] & 31)));
-        }
+        for (int i = threadIdx.x; i < ambiguous; i += T)
+          if (rank_of(i) >= ties) atomicAnd(&sh.marks.amb[sh.amb[i] / 32], ~(1u << (sh.amb[i] & 31)));
         __syncthreads();
       }
     } else {
       unsigned long long lo64 = ~0ull, hi64 = 0ull;  // range of this warp's keys
-      for (int i0 = warp * 32; i0 < n; i0 += kSelectThreads) {
+      for (int i0 = warp * 32; i0 < n; i0 += T) {
         uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < n && is_amb(key_at(min(i0 + lane, n - 1))));
         while (todo) {
           const int j = i0 + __ffs(todo) - 1;
           todo &= todo - 1;
           const __nv_bfloat16* bd = bounds_of(j);
           unsigned long long key = kLowestKey;
-          for (int r = 0; bd && r < p.nq; ++r) {
-            const unsigned long long of = exact_key(q + static_cast<size_t>(r) * p.head_dim, bd, p.head_dim, lane);
+          for (int r = 0; bd && r < p.nq; r += kExactRows) {
+            const unsigned long long of = exact_key(q, r, p.nq, bd, p.head_dim, lane);
             key = of > key ? of : key;
           }
           if (lane == 0) keys64[j] = key;
@@ -709,12 +741,11 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
         sh.pairs[warp][1] = hi64;
       }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kSelectThreads / 32; ++i) {
+      for (int i = 0; i < T / 32; ++i) {
         lo64 = sh.pairs[i][0] < lo64 ? sh.pairs[i][0] : lo64;
         hi64 = sh.pairs[i][1] > hi64 ? sh.pairs[i][1] : hi64;
       }
-      t64 = nth_largest<unsigned long long>(
+      t64 = nth_largest<T, unsigned long long>(
           sh,
           [&](int j, unsigned long long& key) {
             if (!is_amb(key_at(j))) return false;
@@ -727,23 +758,19 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
   }
   // Places: each thread its word of a segment. The chosen go to a list first where it fits,
   // so that their table entries are read all at once.
-  const bool listed = p.top_k <= kSelectKeys;
-  int* const list = reinterpret_cast<int*>(sh.keys);
-  int base = 0, tied = 0;  // blocks placed, ambiguous ones met so far
+  const bool listed = p.top_k <= p.key_space;
+  int* const list = reinterpret_cast<int*>(sh_keys);
+  int placed = 0, tied = 0;  // taken and ambiguous blocks of earlier segments
   for (int seg = 0; seg < n; seg += kSegment) {
     if (remark) {
       mark(seg);
       if (exact && few) {  // several segments: unmark this one's
-        for (int i = threadIdx.x; i < ambiguous; i += kSelectThreads) {
+        for (int i = threadIdx.x; i < ambiguous; i += T) {
           const int j = sh.amb[i] - seg;
-          if (j < 0 || j >= kSegment) continue;
-          int rank = 0;
-          for (int o = 0; o < ambiguous; ++o)
-            rank += sh.amb_key[o] > sh.amb_key[i] || (sh.amb_key[o] == sh.amb_key[i] && o < i);
-          if (rank >= ties) atomicAnd(&sh.marks.amb[j / 32], ~(1u << (j & 31)));
+          if (j >= 0 && j < kSegment && rank_of(i) >= ties) atomicAnd(&sh.marks.amb[j / 32], ~(1u << (j & 31)));
         }
-      } else if (exact) {  // above the threshold: sure; at it: in order; below: out
-        for (int w = threadIdx.x; w < kSelectThreads && seg + 32 * w < n; w += kSelectThreads) {
+      } else if (exact) {  // above the threshold: taken; at it: in order; below: not
+        for (int w = threadIdx.x; w < T && seg + 32 * w < n; w += T) {
           for (uint32_t m = sh.marks.amb[w]; m; m &= m - 1) {
             const uint32_t bit = m & (0u - m);
             const unsigned long long key = keys64[seg + 32 * w + __ffs(m) - 1];
@@ -754,16 +781,18 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
       }
       __syncthreads();
     }
-    unsigned long long total;
-    before = count(seg, total);
-    int s = static_cast<int>(before >> 32), a = tied + static_cast<int>(before & 0xFFFFFFFFull);
-    const int placed = base;  // sure ones of earlier segments
+    if (recount) {
+      before = count(seg, total);
+    } else {
+      __syncthreads();  // the keys' last reader is done: the list takes their place
+    }
+    int s = placed + static_cast<int>(before >> 16), a = tied + static_cast<int>(before & 0xFFFFu);
     for (uint32_t m = my_sure | my_amb; m; m &= m - 1) {
       const uint32_t bit = m & (0u - m);
       const int j = seg + 32 * threadIdx.x + __ffs(m) - 1;
       const bool is_sure = (my_sure & bit) != 0u;
       if (is_sure || a < ties) {
-        const int pos = placed + s + min(a, ties);
+        const int pos = s + min(a, ties);
         if (listed) {
           list[pos] = j;
         } else {
@@ -773,13 +802,35 @@ __global__ void __launch_bounds__(kSelectThreads) pkv_select_kernel(const __grid
       s += is_sure;
       a += !is_sure;
     }
-    base += static_cast<int>(total >> 32);
-    tied += static_cast<int>(total & 0xFFFFFFFFull);
-    if (seg + kSegment < n) __syncthreads();
+    placed += static_cast<int>(total >> 16);
+    tied += static_cast<int>(total & 0xFFFFu);
   }
   if (!listed) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.top_k; i += kSelectThreads) put(i, list[i]);
+  for (int i = threadIdx.x; i < p.top_k; i += T) put(i, list[i]);
+}
+
+template <int T>
+cudaError_t launch_select_of(const SelectParams& p, int num_seqs, int device, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};  // devices whose function attribute is set (bit per device < 64)
+  const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0ull;
+  if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(pkv_select_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSelectMostKeys * sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * p.num_kv_heads);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = p.key_space * sizeof(uint32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pkv_select_kernel<T>, p);
 }
 
 template <int D>
@@ -813,7 +864,7 @@ cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_
 
 int select_tiles(int max_blocks) { return (max_blocks + kScoreTile - 1) / kScoreTile; }
 
-cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, cudaStream_t stream) {
+cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device, cudaStream_t stream) {
   p.tiles = select_tiles(p.max_blocks);
   if (p.max_blocks > p.top_k) {  // else every block is taken
     // A warp takes one tile while that fills the GPU about four times over, then up to 8, so
@@ -829,16 +880,9 @@ cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, cudaStream
     if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, stream);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * p.num_kv_heads);
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_select_kernel, p);
+  p.key_space = std::min(std::max(p.max_blocks, 1), kSelectMostKeys);
+  return p.max_blocks <= 2048 ? launch_select_of<256>(p, num_seqs, device, stream)
+                              : launch_select_of<1024>(p, num_seqs, device, stream);
 }
 
 }  // namespace pkv
