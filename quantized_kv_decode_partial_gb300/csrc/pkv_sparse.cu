@@ -45,6 +45,10 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {  // m, |w|
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -252,7 +256,7 @@ constexpr int kScoreTile = 16;  // blocks per warp and step
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kSteps = D / 32;           // 16-byte loads per bound row and lane
-  constexpr int kStride = D * 2 + 64;      // bytes of a staged query row, padded: rows g, g + 1 meet in no bank
+  constexpr int kStride = D * 4 + 64;      // bytes of a staged query row, padded: rows g, g + 1 meet in no bank
   extern __shared__ __align__(16) uint8_t sq[];
   wait_for_prerequisite_grids();
   allow_dependent_launch();  // the choice may take its place on the SMs; it waits for this grid's end
@@ -300,11 +304,15 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
       prefetch_l2_bulk(p.k_bounds + (static_cast<size_t>(ids_next) * p.num_kv_heads + h) * 2 * D, 4 * D);
     ids = ids_next;
     ids_next = ids_of(it + 2);
-    if (it == 0) {  // the query rows, staged while the first bounds are in flight
+    if (it == 0) {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
       const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
       for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += kScoreWarps * 32) {
         const int r = i / (D / 8), c = i - r * (D / 8);
-        *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) =
+            make_uint4(max_bf16x2(v.x, 0u), max_bf16x2(v.y, 0u), max_bf16x2(v.z, 0u), max_bf16x2(v.w, 0u));
+        *reinterpret_cast<uint4*>(sq + r * kStride + D * 2 + c * 16) =
+            make_uint4(min_bf16x2(v.x, 0u), min_bf16x2(v.y, 0u), min_bf16x2(v.z, 0u), min_bf16x2(v.w, 0u));
       }
       __syncthreads();
     }
@@ -316,10 +324,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
       const uint4 w[4] = {lo0[i], hi0[i], lo1[i], hi1[i]};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m = max_bf16x2(m, w[k].x & 0x7FFF7FFFu);
-        m = max_bf16x2(m, w[k].y & 0x7FFF7FFFu);
-        m = max_bf16x2(m, w[k].z & 0x7FFF7FFFu);
-        m = max_bf16x2(m, w[k].w & 0x7FFF7FFFu);
+        m = max_abs_bf16x2(m, w[k].x);
+        m = max_abs_bf16x2(m, w[k].y);
+        m = max_abs_bf16x2(m, w[k].z);
+        m = max_abs_bf16x2(m, w[k].w);
       }
     }
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
@@ -330,11 +338,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
       float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4*>(sq + (8 * nt + g) * kStride + (32 * i + 8 * t) * 2);
-        mma_bf16(up, hi0[i].x, hi1[i].x, hi0[i].y, hi1[i].y, max_bf16x2(q.x, 0u), max_bf16x2(q.y, 0u));
-        mma_bf16(dn, lo0[i].x, lo1[i].x, lo0[i].y, lo1[i].y, min_bf16x2(q.x, 0u), min_bf16x2(q.y, 0u));
-        mma_bf16(up, hi0[i].z, hi1[i].z, hi0[i].w, hi1[i].w, max_bf16x2(q.z, 0u), max_bf16x2(q.w, 0u));
-        mma_bf16(dn, lo0[i].z, lo1[i].z, lo0[i].w, lo1[i].w, min_bf16x2(q.z, 0u), min_bf16x2(q.w, 0u));
+        const uint8_t* const at = sq + (8 * nt + g) * kStride + (32 * i + 8 * t) * 2;
+        const uint4 pos = *reinterpret_cast<const uint4*>(at), neg = *reinterpret_cast<const uint4*>(at + D * 2);
+        mma_bf16(up, hi0[i].x, hi1[i].x, hi0[i].y, hi1[i].y, pos.x, pos.y);
+        mma_bf16(dn, lo0[i].x, lo1[i].x, lo0[i].y, lo1[i].y, neg.x, neg.y);
+        mma_bf16(up, hi0[i].z, hi1[i].z, hi0[i].w, hi1[i].w, pos.z, pos.w);
+        mma_bf16(dn, lo0[i].z, lo1[i].z, lo0[i].w, lo1[i].w, neg.z, neg.w);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -364,9 +373,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 //
 // With T the k-th largest of the candidates' f32 scores and |f32 - exact| <= E: a score
 // above T + 2E is in (at most k - 1 scores lie above T, and a block below T cannot overtake
-// it), one below T - 2E is out, the rest is ambiguous. E = D 2^-23 |q|_1 max|bound|: at most
-// D / 8 MMA steps and a final sum per score, each off by under 2^-20 of the sum of the
-// products' magnitudes.
+// it), one below T - 2E is out, the rest is ambiguous. E = D 2^-25 |q|_1 max|bound|: D / 8
+// MMA steps and a final sum per score, each off by at most 2^-22 of the products' magnitudes
+// summed (16 exact products join an f32 accumulator per step; the largest error seen, over
+// sums with and without cancellation, is under a tenth of E).
 //
 // T comes from histograms of 2048 equal bins over [lowest, highest] key, narrowed to the bin
 // that holds the k-th until it is one value (two rounds as a rule): spread scores meet few
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ S
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   mu = __reduce_max_sync(0xffffffffu, mu);
   qu = __reduce_max_sync(0xffffffffu, qu);
-  const float err = static_cast<float>(p.head_dim) * 1.1920929e-7f * __uint_as_float(qu) * __uint_as_float(mu);  // E
+  const float err = static_cast<float>(p.head_dim) * 2.98023224e-8f * __uint_as_float(qu) * __uint_as_float(mu);  // E
 
   // keys over `above` are taken, under `below` not; the ones between are ambiguous
   uint32_t above = kForced - 1u, below = kForced;
@@ -810,16 +820,21 @@ __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ S
   for (int i = threadIdx.x; i < p.top_k; i += T) put(i, list[i]);
 }
 
+// Raises a kernel's dynamic shared memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& configured, int device) {
+  const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0ull;  // a bit per device < 64
+  if (bit && (configured.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 template <int T>
 cudaError_t launch_select_of(const SelectParams& p, int num_seqs, int device, cudaStream_t stream) {
-  static std::atomic<unsigned long long> configured{0};  // devices whose function attribute is set (bit per device < 64)
-  const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0ull;
-  if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(pkv_select_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSelectMostKeys * sizeof(uint32_t));
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_acq_rel);
-  }
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_smem(pkv_select_kernel<T>, kSelectMostKeys * sizeof(uint32_t), configured, device);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * p.num_kv_heads);
   cfg.blockDim = dim3(T);
@@ -834,14 +849,17 @@ cudaError_t launch_select_of(const SelectParams& p, int num_seqs, int device, cu
 }
 
 template <int D>
-cudaError_t launch_score_of(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = allow_smem(pkv_score_kernel<D>, 64 * (D * 4 + 64), configured, device);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int per_cta = kScoreWarps * p.tiles_per_warp;
   const long long ctas = static_cast<long long>((p.tiles + per_cta - 1) / per_cta) * p.num_kv_heads;
   if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), num_seqs);
   cfg.blockDim = dim3(kScoreWarps * 32);
-  cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * (D * 2 + 64);
+  cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * (D * 4 + 64);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
@@ -874,10 +892,10 @@ cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device
     const long long per = tiles / fill;
     p.tiles_per_warp = static_cast<int>(per < 1 ? 1 : per > 8 ? 8 : per);
     cudaError_t e = cudaErrorInvalidValue;
-    if (p.head_dim == 64) e = launch_score_of<64>(p, num_seqs, stream);
-    if (p.head_dim == 128) e = launch_score_of<128>(p, num_seqs, stream);
-    if (p.head_dim == 192) e = launch_score_of<192>(p, num_seqs, stream);
-    if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, stream);
+    if (p.head_dim == 64) e = launch_score_of<64>(p, num_seqs, device, stream);
+    if (p.head_dim == 128) e = launch_score_of<128>(p, num_seqs, device, stream);
+    if (p.head_dim == 192) e = launch_score_of<192>(p, num_seqs, device, stream);
+    if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, device, stream);
     if (e != cudaSuccess) return e;
   }
   p.key_space = std::min(std::max(p.max_blocks, 1), kSelectMostKeys);

@@ -384,3 +384,31 @@ def test_a_run_of_steps_over_e4m3_pages():
         diff = np.abs(out.double().cpu().numpy() - ref)
         assert (diff <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * vmax).all(), step
     assert np.array_equal(dev[0].cpu().numpy(), kc) and np.array_equal(dev[3].cpu().numpy(), vs, equal_nan=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("shape", ["normal", "cancelling", "one large", "growing"])
+def test_score_errors_are_far_within_the_bound_the_choice_uses(d, shape):
+    # E = D 2^-25 |q|_1 max|bound|; the f32 scores lie at the start of the choice's workspace,
+    # as integers of the same order
+    rng = np.random.default_rng(d)
+    n, bs, rep = 64, 16, 4
+    bounds, q = rng.normal(size=(n, 1, 2, d)), rng.normal(size=(1, rep, 1, d))
+    if shape == "cancelling":
+        bounds[..., 1::2] = -bounds[..., ::2] * np.sign(q[0, 0, 0, 1::2] * q[0, 0, 0, ::2])
+        q[..., 1::2] = np.abs(q[..., ::2]) * np.sign(q[..., 1::2])
+    elif shape == "one large":
+        bounds[..., 0] *= 300
+    elif shape == "growing":
+        bounds *= 2.0 ** np.linspace(-6, 6, d)
+    bounds = bf16(np.sort(bounds, 2))
+    q = bf16(q)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    B.select_blocks(q.to(DEV), bounds.to(DEV), i32([list(range(n))]), i32([n * bs]), block_size=bs, top_k=8, workspace=ws)
+    keys = ws[:4 * n].cpu().numpy().view(np.uint32)
+    got = np.where(keys >> 31, keys ^ np.uint32(0x80000000), ~keys).astype(np.uint32).view(np.float32).astype(np.float64)
+    bd, qd = bounds.double().numpy(), q.double().numpy()
+    ref = S.block_scores(qd[0, :, 0], bd[:, 0, 0], bd[:, 0, 1])
+    e = d * 2.0 ** -25 * np.abs(qd).sum(-1).max() * np.abs(bd).max()
+    worst = np.abs(got - ref).max() / e
+    assert worst < 0.1, worst
