@@ -306,10 +306,15 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
   // faster SMs more CTAs (balanced: 8-bit layer 718.8 -> 748.1 us, bf16 8 x 128K rows
   // 609.6 -> 642.6 us). The chunk list must index in 32 bits: the longest unit reads at
   // most the table, or with a window W + N - 1 rows plus the alignment of its first chunk.
+  // e4m3 pages are bound by their arithmetic when query rows times head dims exceed 8 x 256
+  // (8 sequences of 20001 to 40003 rows, 8 KV heads, partitions -> balanced; D=128: 8 rows
+  // 88.4 -> 91.5 us, 16 rows 105.5 -> 96.3, 32 rows 200.4 -> 172.2; D=64: 16 rows 60.6 -> 64.2,
+  // 32 rows 130.3 -> 96.8; D=256: 8 rows 169.9 -> 164.6).
+  const bool bal_format = L->bits == 4 || (block_scaled(L) && nq * (L->head_dim + v_dim(L)) > 8 * 256);
   out->balanced = 0;
   if (P->partition_tokens == 0 && P->schedule != PKV_SCHEDULE_PARTITIONS && !cc && !pieces &&
       P->num_seqs <= pkv::kMaxBalancedSeqs &&
-      (P->schedule == PKV_SCHEDULE_BALANCED || (L->bits == 4 && max_parts > 1 && !out->merge_in_cluster))) {
+      (P->schedule == PKV_SCHEDULE_BALANCED || (bal_format && max_parts > 1 && !out->merge_in_cluster))) {
     const PartialInfo bi = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), false, false, true);
     const long long unit_chunks = (window_rows(P, max_len) + bi.chunk_rows - 1) / std::max(bi.chunk_rows, 1);
     const long long units = static_cast<long long>(P->num_seqs) * L->num_kv_heads;

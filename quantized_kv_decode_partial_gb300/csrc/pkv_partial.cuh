@@ -627,7 +627,18 @@ __global__ void __maxnreg__(255)
       // row: the first piece's coordinate, -1 when a stored piece has a bad block id
       int row = __shfl_sync(0xffffffffu, crd_cur, ip & 31);
       int pieces_in = 1;  // pieces copied
-      if (nbl > 0) {
+      int pr[4] = {row, row, row, row};  // e4m3: the pieces' coordinates, in every lane
+      if constexpr (C::kBlk && PC) {
+        pieces_in = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pr[j] = __shfl_sync(0xffffffffu, crd_cur, (ip + j) & 31);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= nb) continue;
+          if (pr[j] == -1) row = -1;
+          pieces_in += pr[j] >= 0;
+        }
+      } else if (nbl > 0) {
         const int mine = __shfl_sync(0xffffffffu, crd_cur, (ip + (lane & (nb - 1))) & 31);
         if (!__all_sync(0xffffffffu, mine >= 0 || mine == -2)) row = -1;
         pieces_in = __popc(__ballot_sync(0xffffffffu, lane < nb && mine >= 0));
@@ -674,7 +685,7 @@ __global__ void __maxnreg__(255)
         // none; its slot is zeroed, since its (masked) keys still meet it.
         if (row >= 0) {
           const int j = lane & 3;
-          const int prow = nbl > 0 ? __shfl_sync(0xffffffffu, crd_cur, (ip + j) & 31) : row;
+          const int prow = j == 0 ? pr[0] : j == 1 ? pr[1] : j == 2 ? pr[2] : pr[3];
           if (lane < 8 && j < nb) {
             const uint32_t dst = st + (lane < 4 ? C::kOffKs : C::kOffVScale) + 4 * j;
             if (prow >= 0) {
@@ -695,7 +706,21 @@ __global__ void __maxnreg__(255)
           fence_proxy_async_smem();
           mbar_arrive_expect_tx(fb, pieces_in * (C::kTmaBytes >> nbl));
         }
-        for (int j = 0; j < nb; ++j) {
+        if constexpr (C::kBlk) {
+          if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j >= nb || pr[j] < 0) continue;
+#pragma unroll
+              for (int sg = 0; sg < C::kBoxes; ++sg)
+                tma_load_3d(st + (sg * C::kCh + j * pb) * C::kRB, &tmap_k, 0, pr[j], sg, fb, policy);
+#pragma unroll
+              for (int sg = 0; sg < C::kBoxesV; ++sg)
+                tma_load_3d(st + C::kOffV + (sg * C::kCh + j * pb) * C::kRBV, &tmap_v, 0, pr[j], sg, fb, policy);
+            }
+          }
+        }
+        for (int j = 0; !C::kBlk && j < nb; ++j) {
           const int prow = __shfl_sync(0xffffffffu, crd_cur, (ip + j) & 31);
           if (lane == 0 && prow >= 0) {
 #pragma unroll
@@ -909,8 +934,26 @@ __global__ void __maxnreg__(255)
     // update of (m_run, l_run), giving the chunk's weights pr and, where a running maximum
     // grew, the factors corr (returns whether any did, warp-uniform). rescale: applies corr
     // to the value accumulators. value_chunk: O^T += V^T P^T over the chunk's value rows.
+    // e4m3 pages: a chunk's scales by key row. Whole blocks: one scale. Small blocks: the 16
+    // keys of a tile lie in one block of 16 rows or in two of 8, rows 0-7 and 8-15; `two`
+    // tells which, so a tile's scales are picked from the chunk's four without an address.
+    const bool two = PC && piece_shift == 3;
+    auto load_scales = [&](uint32_t addr, float (&v)[4]) {
+      if constexpr (PC) {
+        ld_shared_f32x4(addr, v);
+      } else {
+        v[0] = v[1] = v[2] = v[3] = ld_shared_f32(addr);
+      }
+    };
+    auto pick_scales = [&](const float (&v)[4], int tile, float& a, float& b) {
+      a = PC && two ? v[2 * tile] : v[PC ? tile : 0];
+      b = PC && two ? v[2 * tile + 1] : a;
+    };
     auto score_chunk = [&](uint32_t kpl, uint32_t sbq, int kbase, bool full_vis, float (&pr)[C::kTiles][NT][4],
                            float (&corr)[NT][2]) -> bool {
+      float kscale[4];
+      if constexpr (C::kBlk) load_scales(kpl + C::kOffKs, kscale);
+      auto key_scales = [&](int tile, float& a, float& b) { pick_scales(kscale, tile, a, b); };
       // ---- scores x = (K q) * scale * log2(e), keys on rows
       float x[C::kTiles][NT][4];
 #pragma unroll
@@ -969,9 +1012,8 @@ __global__ void __maxnreg__(255)
                 mma_f16((kChains == 2 && cc) ? sacc2[nt] : sacc[nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
             }
           }
-          const uint32_t ksc = kpl + C::kOffKs;
-          const float ks0 = ld_shared_f32(ksc + (PC ? 4 * ((tile * 16 + g) >> piece_shift) : 0));
-          const float ks1 = PC ? ld_shared_f32(ksc + 4 * ((tile * 16 + g + 8) >> piece_shift)) : ks0;
+          float ks0, ks1;  // scales of keys g and g + 8
+          key_scales(tile, ks0, ks1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1154,15 +1196,22 @@ __global__ void __maxnreg__(255)
         // key's weight times its block's scale over the chunk's largest (at most 1). The
         // chunk's product then takes that largest scale on its way into O^T.
         uint32_t pb2[C::kTiles][NT][2];
-        const uint32_t vsc = kpl + C::kOffVScale;
-        float vmax = ld_shared_f32(vsc);
-        if constexpr (PC)
-          for (int j = 1; j < nb; ++j) vmax = fmaxf(vmax, ld_shared_f32(vsc + 4 * j));
-        const float vinv = PC && vmax > 0.f ? 1.f / vmax : 0.f;
+        float vs[4];
+        load_scales(kpl + C::kOffVScale, vs);
+        float vmax = vs[0];
+        if constexpr (PC) {
+          vmax = fmaxf(vmax, vs[1]);
+          if (nb == 4) vmax = fmaxf(vmax, fmaxf(vs[2], vs[3]));
+        }
+        const float vinv = PC && vmax >= 1.1754944e-38f ? fast_rcp(vmax) : 0.f;  // normal numbers
 #pragma unroll
         for (int tile = 0; tile < C::kTiles; ++tile) {
-          const float ra = PC ? ld_shared_f32(vsc + 4 * ((tile * 16 + g) >> piece_shift)) * vinv : 1.f;
-          const float rb = PC ? ld_shared_f32(vsc + 4 * ((tile * 16 + g + 8) >> piece_shift)) * vinv : 1.f;
+          float ra = 1.f, rb = 1.f;
+          if constexpr (PC) {
+            pick_scales(vs, tile, ra, rb);
+            ra *= vinv;
+            rb *= vinv;
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             pb2[tile][nt][0] = movmatrix_trans(pack_f16x2(pr[tile][nt][0] * ra, pr[tile][nt][1] * ra));

@@ -300,8 +300,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
         hi1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    if (good(ids_next))
-      prefetch_l2_bulk(p.k_bounds + (static_cast<size_t>(ids_next) * p.num_kv_heads + h) * 2 * D, 4 * D);
+    {  // the next tile's bounds towards L2, half of each block's lines per half warp
+      const int ph = __shfl_sync(0xffffffffu, ids_next, lane & 15);
+      if (good(ph)) {
+        const __nv_bfloat16* r = p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * D + (lane >> 4) * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) prefetch_l2(r + 64 * i);
+      }
+    }
     ids = ids_next;
     ids_next = ids_of(it + 2);
     if (it == 0) {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
@@ -318,18 +324,19 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
     }
     if (!live) continue;
     // the largest magnitude of the tile's bounds: what the choice's error bound needs
-    uint32_t m = 0u;
+    uint32_t mm[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const uint4 w[4] = {lo0[i], hi0[i], lo1[i], hi1[i]};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m = max_abs_bf16x2(m, w[k].x);
-        m = max_abs_bf16x2(m, w[k].y);
-        m = max_abs_bf16x2(m, w[k].z);
-        m = max_abs_bf16x2(m, w[k].w);
+        mm[0] = max_abs_bf16x2(mm[0], w[k].x);
+        mm[1] = max_abs_bf16x2(mm[1], w[k].y);
+        mm[2] = max_abs_bf16x2(mm[2], w[k].z);
+        mm[3] = max_abs_bf16x2(mm[3], w[k].w);
       }
     }
+    uint32_t m = max_bf16x2(max_bf16x2(mm[0], mm[1]), max_bf16x2(mm[2], mm[3]));
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
     if (lane == 0) p.tile_abs[unit * p.tiles + tile] = __uint_as_float(m << 16);
 
