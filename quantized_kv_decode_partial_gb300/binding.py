@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -253,6 +254,27 @@ def _raw_stream(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
+class _Workspaces(threading.local):
+    """The default stream's workspaces of one host thread, a growing one per device. Calls on
+    that stream run one after the other, and the launches of one thread's call are not mixed
+    with another call's, so they may share it; a call on any other stream (a captured one
+    among them) gets a workspace of its own."""
+
+    def __init__(self):
+        self.held = {}
+
+    def get(self, device: torch.device, index: int, stream: int, nbytes: int) -> torch.Tensor:
+        if stream != 0:
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = self.held.get(index)
+        if ws is None or ws.numel() < nbytes:
+            ws = self.held[index] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws
+
+
+_workspaces = _Workspaces()
+
+
 class _Call:
     """What a call's shapes settle: the argument structures and the plan."""
 
@@ -324,18 +346,19 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     lib = load_library()
     _check_block_scales(bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
+        stream = _raw_stream(q.get_device())
         call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
                             schedule)
         if out is None:
             out = call.new_out(q)
         if workspace is None and call.workspace_bytes:
-            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.pkv_paged_decode_attention(
             call.layout_ref, call.params_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
             _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), block_tables.data_ptr(),
             seq_lens.data_ptr(), float(scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag),
-            _raw_stream(q.get_device()))
+            stream)
     if rc != PKV_OK:
         _check(rc, lib)
     return out
@@ -355,18 +378,19 @@ def paged_decode_append_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: t
     (seq_lens counts the new rows), then attends as ``paged_decode_attention``."""
     lib = load_library()
     with _on_device(q.device):
+        stream = _raw_stream(q.get_device())
         call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
                             schedule)
         if out is None:
             out = call.new_out(q)
         if workspace is None and call.workspace_bytes:
-            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.pkv_paged_decode_append_attention(
             call.layout_ref, call.params_ref, q.data_ptr(), _ptr(k_new), _ptr(v_new), k_pool.data_ptr(),
             v_pool.data_ptr(), _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), block_tables.data_ptr(),
             seq_lens.data_ptr(), float(scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag),
-            _raw_stream(q.get_device()))
+            stream)
     if rc != PKV_OK:
         _check(rc, lib)
     return out
@@ -641,6 +665,7 @@ def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.T
     bounds (pkv_select_blocks). Depends on the bounds alone, whatever the pages' format."""
     lib = load_library()
     with _on_device(q.device):
+        stream = _raw_stream(q.get_device())
         key = ("select", q.get_device(), q.shape, q.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
                block_tables.dtype, seq_lens.shape, seq_lens.dtype, block_size, top_k, first_blocks, last_blocks)
         call = _calls.get(key)
@@ -669,12 +694,12 @@ def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.T
         _require_contiguous(q=q, k_bounds=k_bounds, block_tables=block_tables, seq_lens=seq_lens, blocks=out.blocks,
                             tables=out.tables, lens=out.lens)
         if workspace is None and call.workspace_bytes:
-            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.pkv_select_blocks(call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(),
                                    k_bounds.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
                                    _ptr(out.blocks), out.tables.data_ptr(), out.lens.data_ptr(), _ptr(workspace),
-                                   ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+                                   ws_bytes, _ptr(error_flag), stream)
     if rc != PKV_OK:
         _check(rc, lib)
     return out
@@ -693,6 +718,7 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     _check_block_scales(bits, group_size, k_scales, v_scales)
     tables, lens = selection.tables, selection.lens
     with _on_device(q.device):
+        stream = _raw_stream(q.get_device())
         key = ("selected", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, tables.shape,
                tables.dtype, lens.shape, lens.dtype, bits, group_size, partition_tokens, contraction, schedule)
         call = _calls.get(key)
@@ -714,12 +740,12 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
         if out is None:
             out = call.new_out(q)
         if workspace is None and call.workspace_bytes:
-            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.pkv_selected_decode_attention(
             call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
             _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), tables.data_ptr(), lens.data_ptr(), float(scale),
-            out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+            out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
     if rc != PKV_OK:
         _check(rc, lib)
     return out
@@ -741,6 +767,7 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     lib = load_library()
     _check_block_scales(bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
+        stream = _raw_stream(q.get_device())
         key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, k_bounds.shape,
                k_bounds.dtype, block_tables.shape, block_tables.dtype, seq_lens.shape, seq_lens.dtype,
                None if blocks is None else (blocks.shape, blocks.dtype), bits, group_size, partition_tokens,
@@ -765,13 +792,13 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
         if out is None:
             out = call.new_out(q)
         if workspace is None:
-            workspace = torch.empty(call.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = workspace.numel() * workspace.element_size()
         rc = lib.pkv_sparse_decode_attention(
             call.layout_ref, call.params_ref, call.sparse_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
             _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), k_bounds.data_ptr(),
             block_tables.data_ptr(), seq_lens.data_ptr(), float(scale), _ptr(blocks), out.data_ptr(), workspace.data_ptr(),
-            ws_bytes, _ptr(error_flag), _raw_stream(q.get_device()))
+            ws_bytes, _ptr(error_flag), stream)
     if rc != PKV_OK:
         _check(rc, lib)
     return out

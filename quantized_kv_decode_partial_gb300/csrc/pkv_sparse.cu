@@ -10,7 +10,9 @@
 // top_k in all, through the decode kernels: the pool seen as NB * HK blocks of one head, and
 // every (sequence, KV head) as a sequence of its chosen blocks in order.
 //
-// Three kernels: the bounds' upkeep after an append, the scores, and the choice.
+// The bounds' upkeep after an append is one kernel. Scores and choice are two, or one where
+// a cluster per (sequence, KV head) scores every block in one step and the GPU holds all
+// clusters at once.
 #include <algorithm>
 #include <atomic>
 
@@ -250,37 +252,34 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-constexpr int kScoreWarps = 4;
+constexpr int kScoreWarps = 4;  // of the kernel that scores alone
 constexpr int kScoreTile = 16;  // blocks per warp and step
 
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int kSteps = D / 32;           // 16-byte loads per bound row and lane
-  constexpr int kStride = D * 4 + 64;      // bytes of a staged query row, padded: rows g, g + 1 meet in no bank
-  extern __shared__ __align__(16) uint8_t sq[];
-  wait_for_prerequisite_grids();
-  allow_dependent_launch();  // the choice may take its place on the SMs; it waits for this grid's end
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // the KV heads of a run of blocks are neighbours in the grid, as their bounds are in memory
-  const int chunk = blockIdx.x / p.num_kv_heads, h = blockIdx.x - chunk * p.num_kv_heads, b = blockIdx.y;
-  const size_t unit = static_cast<size_t>(b) * p.num_kv_heads + h;
-  const int len = p.seq_lens[b];
-  if (len < p.n_query || len > p.max_blocks * p.block_size) return;  // the choice flags it
-  const int n = (len + p.block_size - 1) / p.block_size;
-  const int cta_tile = chunk * kScoreWarps * p.tiles_per_warp;
-  if (n <= p.top_k || cta_tile * kScoreTile >= n) return;  // every block is taken, or none is here
-  const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+// Bytes of a staged query row: max(q, 0), min(q, 0), padded so that rows g, g + 1 meet in no bank.
+constexpr __host__ __device__ int query_row_bytes(int D) { return D * 4 + 64; }
+
+// Scores this warp's tiles first_tile, first_tile + step, ... (`count` of them, the same for
+// every warp of the CTA) of unit (b, h) with n blocks; sq: space for the query rows. ready()
+// runs once, in every thread, before the first result; put(j, key) and put_tile(tile, m) take
+// a block's score and the bits of a tile's largest |bound|.
+template <int D, int WARPS, typename Ready, typename Put, typename PutTile>
+__device__ __forceinline__ void score_tiles(const SelectParams& p, size_t unit, int h, const int32_t* table, int n,
+                                            int first_tile, int step, int count, uint8_t* sq, Ready ready, Put put,
+                                            PutTile put_tile) {
+  constexpr int kSteps = D / 32;  // 16-byte loads per bound row and lane
+  constexpr int kStride = query_row_bytes(D);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int ntiles = (p.nq + 7) / 8;  // tiles of 8 query rows
 
   // a tile's block ids, one per lane of the first 16; -1 past the last block
   auto ids_of = [&](int it) {
-    const int j = (cta_tile + it * kScoreWarps + warp) * kScoreTile + lane;
-    return it < p.tiles_per_warp && lane < kScoreTile && j < n ? table[j] : -1;
+    const int j = (first_tile + it * step) * kScoreTile + lane;
+    return it < count && lane < kScoreTile && j < n ? table[j] : -1;
   };
   auto good = [&](int ph) { return static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks); };
   int ids = ids_of(0), ids_next = ids_of(1);
-  for (int it = 0; it < p.tiles_per_warp; ++it) {
-    const int tile = cta_tile + it * kScoreWarps + warp;  // warp-uniform
+  for (int it = 0; it < count; ++it) {
+    const int tile = first_tile + it * step;  // warp-uniform
     const int j0 = tile * kScoreTile;
     const bool live = j0 < n;
     uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
     ids_next = ids_of(it + 2);
     if (it == 0) {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
       const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
-      for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += kScoreWarps * 32) {
+      for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += WARPS * 32) {
         const int r = i / (D / 8), c = i - r * (D / 8);
         const uint4 v = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) =
@@ -321,6 +320,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
             make_uint4(min_bf16x2(v.x, 0u), min_bf16x2(v.y, 0u), min_bf16x2(v.z, 0u), min_bf16x2(v.w, 0u));
       }
       __syncthreads();
+      ready();
     }
     if (!live) continue;
     // the largest magnitude of the tile's bounds: what the choice's error bound needs
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
     }
     uint32_t m = max_bf16x2(max_bf16x2(mm[0], mm[1]), max_bf16x2(mm[2], mm[3]));
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-    if (lane == 0) p.tile_abs[unit * p.tiles + tile] = __uint_as_float(m << 16);
+    put_tile(tile, m << 16);
 
     float best0 = -INFINITY, best1 = -INFINITY;  // blocks j0 + g and j0 + g + 8
     for (int nt = 0; nt < ntiles; ++nt) {
@@ -365,11 +365,33 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
       best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, d));
     }
     if (t == 0) {
-      uint32_t* s = p.scores + unit * p.score_stride + j0;
-      if (j0 + g < n) s[g] = order_key(ph0 >= 0 ? best0 : -INFINITY);
-      if (j0 + g + 8 < n) s[g + 8] = order_key(ph1 >= 0 ? best1 : -INFINITY);
+      if (j0 + g < n) put(j0 + g, order_key(ph0 >= 0 ? best0 : -INFINITY));
+      if (j0 + g + 8 < n) put(j0 + g + 8, order_key(ph1 >= 0 ? best1 : -INFINITY));
     }
   }
+}
+
+// Scores alone, into the workspace.
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) uint8_t sq[];
+  wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the choice may take its place on the SMs; it waits for this grid's end
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the KV heads of a run of blocks are neighbours in the grid, as their bounds are in memory
+  const int chunk = blockIdx.x / p.num_kv_heads, h = blockIdx.x - chunk * p.num_kv_heads, b = blockIdx.y;
+  const size_t unit = static_cast<size_t>(b) * p.num_kv_heads + h;
+  const int len = p.seq_lens[b];
+  if (len < p.n_query || len > p.max_blocks * p.block_size) return;  // the choice flags it
+  const int n = (len + p.block_size - 1) / p.block_size;
+  const int cta_tile = chunk * kScoreWarps * p.tiles_per_warp;
+  if (n <= p.top_k || cta_tile * kScoreTile >= n) return;  // every block is taken, or none is here
+  score_tiles<D, kScoreWarps>(
+      p, unit, h, p.block_tables + static_cast<size_t>(b) * p.max_blocks, n, cta_tile + warp, kScoreWarps,
+      p.tiles_per_warp, sq, [] {}, [&](int j, uint32_t key) { p.scores[unit * p.score_stride + j] = key; },
+      [&](int tile, uint32_t m) {
+        if (lane == 0) p.tile_abs[unit * p.tiles + tile] = __uint_as_float(m);
+      });
 }
 
 // -------------------------------------------------------------------------------------- choice
@@ -546,20 +568,13 @@ __device__ __forceinline__ unsigned long long exact_key(const __nv_bfloat16* q, 
   return best;
 }
 
+// The largest 1-norm of the unit's query rows this warp looks at.
 template <int T>
-__global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ SelectShared<T> sh;
-  extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: the scores, later the chosen blocks
-  constexpr int kSegment = SelectShared<T>::kSegment;
-  wait_for_prerequisite_grids();
-  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
-  const int unit = blockIdx.x, b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = p.seq_lens[b];
+__device__ __forceinline__ float query_norm(const SelectParams& p, int unit) {
   const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
-  // the query's largest 1-norm, while the length arrives: a row's D / 8 <= 32 lanes hold 8 values each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float q1 = 0.f;
-  for (int r = warp; r < p.nq; r += T / 32) {
+  for (int r = warp; r < p.nq; r += T / 32) {  // a row's D / 8 <= 32 lanes hold 8 values each
     float s = 0.f;
     if (lane < p.head_dim / 8) {
       const uint4 v = ld_nc_keep_v4(q + static_cast<size_t>(r) * p.head_dim + 8 * lane);
@@ -572,6 +587,18 @@ __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ S
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     q1 = fmaxf(q1, s);
   }
+  return q1;
+}
+
+// Chooses the blocks of one unit. FUSED: sh_keys holds the scores of its n blocks and
+// `mag_bits` the largest |bound| this thread knows of; else both are read from the workspace.
+template <int T, bool FUSED>
+__device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<T>& sh, uint32_t* sh_keys, int unit,
+                                            int len, float q1, uint32_t mag_bits) {
+  constexpr int kSegment = SelectShared<T>::kSegment;
+  const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
   int32_t* const out_blocks = p.out_blocks ? p.out_blocks + static_cast<size_t>(unit) * p.top_k : nullptr;
   int32_t* const out_table = p.out_tables + static_cast<size_t>(unit) * p.top_k;
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
@@ -596,16 +623,26 @@ __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ S
   }
   const uint32_t* scores = p.scores + static_cast<size_t>(unit) * p.score_stride;  // 16-byte aligned
   unsigned long long* const keys64 = p.keys64 + static_cast<size_t>(unit) * p.max_blocks;
-  const bool staged = n <= p.key_space;
+  const bool staged = FUSED || n <= p.key_space;
   auto forced = [&](int j) { return j < p.first || j >= n - p.last; };
   auto key_at = [&](int j) { return staged ? sh_keys[j] : forced(j) ? kForced : __ldcg(scores + j); };
 
   // keys and the candidates' range; the bounds' largest magnitude
   uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-  float mag = 0.f;
+  if constexpr (FUSED) {
+    for (int j = threadIdx.x; j < n; j += T) {
+      if (forced(j)) {
+        sh_keys[j] = kForced;
+      } else {
+        kmin = min(kmin, sh_keys[j]);
+        kmax = max(kmax, sh_keys[j]);
+      }
+    }
+  }
+  float mag = __uint_as_float(mag_bits);
   const int tiles = (n + kScoreTile - 1) / kScoreTile;
   constexpr int kBatch = 2;
-  for (int j0 = 4 * threadIdx.x, t0 = threadIdx.x; j0 < n; j0 += 4 * T * kBatch) {
+  for (int j0 = 4 * threadIdx.x, t0 = threadIdx.x; !FUSED && j0 < n; j0 += 4 * T * kBatch) {
     uint4 v[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -827,6 +864,63 @@ __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ S
   for (int i = threadIdx.x; i < p.top_k; i += T) put(i, list[i]);
 }
 
+// The choice alone, from the workspace's scores.
+template <int T>
+__global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelectShared<T> sh;
+  extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: the scores, later the chosen blocks
+  wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
+  const int unit = blockIdx.x;
+  const int len = p.seq_lens[unit / p.num_kv_heads];
+  const float q1 = query_norm<T>(p, unit);  // while the length arrives
+  select_unit<T, false>(p, sh, sh_keys, unit, len, q1, 0u);
+}
+
+// Scores and choice of one unit by a cluster of 1 to 8 CTAs: each scores its share of the
+// tiles, one per warp, into the first CTA's shared memory, and that one chooses. One launch
+// less, and no trip of the scores through L2: 8 units of 1024 blocks (D=128, 4 query rows)
+// 11.4 -> 10.9 us on the GPU and 2.7 us less per call from the host. With several tiles per
+// warp or more than one wave of clusters the two kernels were faster (fused -> two: 64 units
+// of 626 blocks, D=256, 17.4 -> 15.7 us; 512 of up to 1024, 43.2 -> 39.8; 64 of 8192,
+// 64.6 -> 61.6).
+constexpr int kFusedThreads = 256;
+constexpr int kFusedCluster = 8;
+constexpr int kFusedBlocks = kFusedCluster * kFusedThreads / 32 * kScoreTile;  // 1024
+
+template <int D>
+__global__ void __launch_bounds__(kFusedThreads)
+    pkv_choose_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelectShared<kFusedThreads> sh;
+  __shared__ uint32_t mags[kFusedCluster * kFusedThreads / 32];  // largest |bound| per warp of the cluster
+  extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: scores, later the chosen blocks; then query rows
+  wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
+  const int rank = blockIdx.x, ctas = gridDim.x, unit = blockIdx.y;
+  const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
+  const int len = p.seq_lens[b];
+  const float q1 = rank == 0 ? query_norm<kFusedThreads>(p, unit) : 0.f;
+  const int n = len < p.n_query || len > p.max_blocks * p.block_size ? 0 : (len + p.block_size - 1) / p.block_size;
+  uint32_t mag = 0u;
+  if (n > p.top_k) {  // the same for the whole cluster
+    constexpr int kWarps = kFusedThreads / 32;
+    const int warp = threadIdx.x >> 5, tiles = (n + kScoreTile - 1) / kScoreTile;
+    cluster_arrive_relaxed();  // tells that this CTA runs; the first CTA's memory is written after all have
+    score_tiles<D, kWarps>(
+        p, unit, h, p.block_tables + static_cast<size_t>(b) * p.max_blocks, n, rank * kWarps + warp, ctas * kWarps,
+        (tiles + ctas * kWarps - 1) / (ctas * kWarps), reinterpret_cast<uint8_t*>(sh_keys + p.key_space),
+        [] { cluster_wait(); }, [&](int j, uint32_t key) { st_cluster_u32(smem_addr(sh_keys + j), 0, key); },
+        [&](int, uint32_t m) { mag = max(mag, m); });
+    if ((threadIdx.x & 31) == 0) st_cluster_u32(smem_addr(mags + rank * kWarps + warp), 0, mag);
+    cluster_sync();
+    if (rank != 0) return;
+    mag = threadIdx.x < ctas * kWarps ? mags[threadIdx.x] : 0u;
+  } else if (rank != 0) {
+    return;
+  }
+  select_unit<kFusedThreads, true>(p, sh, sh_keys, unit, len, q1, mag);
+}
+
 // Raises a kernel's dynamic shared memory limit once per device.
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& configured, int device) {
@@ -858,7 +952,7 @@ cudaError_t launch_select_of(const SelectParams& p, int num_seqs, int device, cu
 template <int D>
 cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  const cudaError_t e = allow_smem(pkv_score_kernel<D>, 64 * (D * 4 + 64), configured, device);
+  const cudaError_t e = allow_smem(pkv_score_kernel<D>, 64 * query_row_bytes(D), configured, device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int per_cta = kScoreWarps * p.tiles_per_warp;
@@ -866,7 +960,7 @@ cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cud
   if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), num_seqs);
   cfg.blockDim = dim3(kScoreWarps * 32);
-  cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * (D * 4 + 64);
+  cfg.dynamicSmemBytes = (p.nq + 7) / 8 * 8 * query_row_bytes(D);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
@@ -874,6 +968,29 @@ cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cud
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, pkv_score_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t launch_choose_of(const SelectParams& p, int units, int cluster, int device, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e =
+      allow_smem(pkv_choose_kernel<D>, kFusedBlocks * 4 + 64 * query_row_bytes(D), configured, device);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(cluster, units);
+  cfg.blockDim = dim3(kFusedThreads);
+  cfg.dynamicSmemBytes = p.key_space * sizeof(uint32_t) + (p.nq + 7) / 8 * 8 * query_row_bytes(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pkv_choose_kernel<D>, p);
 }
 
 }  // namespace
@@ -891,6 +1008,19 @@ int select_tiles(int max_blocks) { return (max_blocks + kScoreTile - 1) / kScore
 
 cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device, cudaStream_t stream) {
   p.tiles = select_tiles(p.max_blocks);
+  if (p.max_blocks <= kFusedBlocks) {
+    const int units = num_seqs * p.num_kv_heads;  // at most 65535
+    int cluster = 1;
+    while (cluster * (kFusedThreads / 32) < p.tiles) cluster *= 2;
+    if (units * cluster <= sm_count) {
+      p.key_space = (p.max_blocks + 3) / 4 * 4;
+      if (p.head_dim == 64) return launch_choose_of<64>(p, units, cluster, device, stream);
+      if (p.head_dim == 128) return launch_choose_of<128>(p, units, cluster, device, stream);
+      if (p.head_dim == 192) return launch_choose_of<192>(p, units, cluster, device, stream);
+      if (p.head_dim == 256) return launch_choose_of<256>(p, units, cluster, device, stream);
+      return cudaErrorInvalidValue;
+    }
+  }
   if (p.max_blocks > p.top_k) {  // else every block is taken
     // A warp takes one tile while that fills the GPU about four times over, then up to 8, so
     // that the query rows are staged for more of them.

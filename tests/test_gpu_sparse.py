@@ -209,6 +209,20 @@ def test_more_blocks_than_shared_memory_holds():
         check_choice(rng, bounds, q, tables, [n * bs - 7], bs, top_k, 1, 1)
 
 
+@pytest.mark.parametrize("n,seqs,hk,width", [(17, 1, 3, 40), (129, 3, 2, 129), (300, 4, 2, 300), (1000, 1, 8, 1000),
+                                             (1024, 1, 1, 1024), (1025, 1, 1, 1025), (257, 3, 2, 9000), (129, 100, 2, 129)])
+def test_one_kernel_and_two(n, seqs, hk, width):
+    # clusters of 1, 2, 4 and 8 CTAs, tables on both sides of 1024 blocks, more clusters than SMs
+    rng = np.random.default_rng(n + seqs + hk)
+    bs, d = 16, 64
+    lens = [max(1, n - 11 * b) * bs - b % bs for b in range(seqs)]
+    tables, nb = make_tables(rng, lens, bs)
+    tables = [t + [-1] * (width - len(t)) for t in tables]
+    bounds = random_bounds(rng, nb, hk, d)
+    q = bf16(rng.normal(size=(seqs, hk, 1, d)))
+    check_choice(rng, bounds, q, tables, lens, bs, 16, 1, 1)
+
+
 def test_infinite_and_nan_bounds_and_bad_blocks():
     rng = np.random.default_rng(11)
     n, d, bs, top_k = 200, 128, 16, 30
@@ -389,10 +403,10 @@ def test_a_run_of_steps_over_e4m3_pages():
 @pytest.mark.parametrize("d", [64, 128, 192, 256])
 @pytest.mark.parametrize("shape", ["normal", "cancelling", "one large", "growing"])
 def test_score_errors_are_far_within_the_bound_the_choice_uses(d, shape):
-    # E = D 2^-25 |q|_1 max|bound|; the f32 scores lie at the start of the choice's workspace,
-    # as integers of the same order
+    # E = D 2^-25 |q|_1 max|bound|; for wide tables the f32 scores lie at the start of the
+    # choice's workspace, as integers of the same order
     rng = np.random.default_rng(d)
-    n, bs, rep = 64, 16, 4
+    n, bs, rep, width = 128, 16, 4, 8193
     bounds, q = rng.normal(size=(n, 1, 2, d)), rng.normal(size=(1, rep, 1, d))
     if shape == "cancelling":
         bounds[..., 1::2] = -bounds[..., ::2] * np.sign(q[0, 0, 0, 1::2] * q[0, 0, 0, ::2])
@@ -403,8 +417,9 @@ def test_score_errors_are_far_within_the_bound_the_choice_uses(d, shape):
         bounds *= 2.0 ** np.linspace(-6, 6, d)
     bounds = bf16(np.sort(bounds, 2))
     q = bf16(q)
-    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
-    B.select_blocks(q.to(DEV), bounds.to(DEV), i32([list(range(n))]), i32([n * bs]), block_size=bs, top_k=8, workspace=ws)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    tables = [list(range(n)) + [-1] * (width - n)]
+    B.select_blocks(q.to(DEV), bounds.to(DEV), i32(tables), i32([n * bs]), block_size=bs, top_k=8, workspace=ws)
     keys = ws[:4 * n].cpu().numpy().view(np.uint32)
     got = np.where(keys >> 31, keys ^ np.uint32(0x80000000), ~keys).astype(np.uint32).view(np.float32).astype(np.float64)
     bd, qd = bounds.double().numpy(), q.double().numpy()
