@@ -187,7 +187,9 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
     // 2% slower halved again.
     const long long slots = 2ll * (sm_count > 0 ? sm_count : 1);
     const long long target = 4 * slots;
-    constexpr long long kMaxCtaBytes = 3ll << 20;
+    // e4m3 pages, whose three CTAs per SM are shorter apart: 768 KB (64 sequences of 1024 to
+    // 32768 rows, 8 KV heads, D=128: 343.5 -> 325.3 us; D=64: 186.7 -> 177.1).
+    const long long kMaxCtaBytes = block_scaled(L) ? 768ll << 10 : 3ll << 20;
     const long long units = static_cast<long long>(P->num_seqs) * L->num_kv_heads;
     const long long kv_row = stored_row_bytes(L, L->head_dim) + stored_row_bytes(L, v_dim(L));  // K + V
     const long long floor_rows = 256;
@@ -1014,7 +1016,7 @@ int check_sparse(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
 }
 
 // Rows per partition of the decode over `blocks` chosen blocks per unit (0: the library's
-// choice, for grids of more than one wave). The units read the same number of rows, as a
+// choice). The units read the same number of rows, as a
 // rule, so the partitions are as many as one wave holds, of 256 rows or more, and merge in
 // clusters: of the grids of one and of two CTAs per SM the one that fills more of its wave,
 // the former where they tie. 64 units of 4096 bf16 rows (D=128, 16 query rows): 2 partitions
@@ -1032,7 +1034,11 @@ int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int
                            ? std::min(std::min<long long>(pkv::kMaxClusterParts, sms / units), most)
                            : 0;
   const long long p2 = std::min(std::min(per_sm == 2 ? 16ll : 8ll, per_sm * sms / units), most);
-  const long long parts = units * p1 * per_sm >= units * p2 ? p1 : p2;
+  long long parts = units * p1 * per_sm >= units * p2 ? p1 : p2;
+  // One to four waves of e4m3 units: four partitions each even out the last wave while a CTA
+  // reads 128 KB or more (512 units of 2048 rows, D=128: 58.4 -> 50.9 us).
+  if (parts == 0 && block_scaled(vl) && units <= 4 * 3 * sms && rows * stored_row_bytes(vl, vl->head_dim) >= (256ll << 10))
+    parts = 4;
   return parts > 0 ? static_cast<int>(round_up((rows + parts - 1) / parts, chunk_rows_of(vl->bits))) : 0;
 }
 

@@ -156,7 +156,7 @@ struct SelectParams {
   int num_blocks, num_kv_heads, block_size, max_blocks;
   int score_stride;               // max_blocks rounded up to 4
   int n_query, nq, head_dim, top_k, first, last;
-  int tiles, tiles_per_warp, key_space;  // set by launch_select
+  int tiles, tiles_per_warp, key_space, after_scores;  // set by launch_select
 };
 
 struct GatherParams {

@@ -163,10 +163,16 @@ struct PartialCfg {
   static constexpr int kWP = kWarps / WQ;
   static constexpr int kSoloStages = (kSeven ? kSoloBase : kSixLone ? kSoloBase - kRecvNeedBytes : kSoloBudget) /
                                      (kWarps * kStageBytes);
+  // e4m3 pages with 64- or 128-dim values and up to 8 query rows: two stages per warp instead
+  // of three let a third CTA on the SM, a fourth for 64-dim heads (as many bytes in flight,
+  // more warps). 8 sequences of 20001 to 40003 rows, D=128, 4 query rows: 87.4 -> 79.1 us, in
+  // blocks of 16 rows 103.5 -> 85.9; 32 sequences of 512 to 16384 rows, D=64: 69.4 -> 54.4.
+  static constexpr bool kThird = kBlk && !SOLO && !BAL && DV <= 128 && NT == 1 && WQ == 1;
   // (a query group of 8 warps shares one ring of 8 or 16 stages, within 144 KB)
   static constexpr int kStagesPerWarp = WQ == 8 ? (8 * 2 * kStageBytes <= 144 * 1024 ? 2 : 1)
                                         : kEightLone ? 1
                                         : SOLO || kSeven || kSixLone ? (kSoloStages < 4 ? kSoloStages : 4)
+                                        : kThird ? 2
                                                 : (kStageBytes <= 9 * 1024 ? 3 : 2);
   static constexpr int kStagesPerGroup = kStagesPerWarp * WQ;  // each page group's private ring
   static constexpr int kMt = DV / 16;       // 16-dim m-tiles of O^T
@@ -188,7 +194,7 @@ struct PartialCfg {
   // The receive area (after the ring) is there when the CTA is alone on its SM, or when it
   // does not cost the second CTA per SM (or the CTA already has its SM to itself).
   static constexpr int kBaseSmem = kWorkBytes + kBarrierBytes + 1024;
-  static constexpr bool kPush = !BAL && !kSeven && (SOLO || kBaseSmem + kRecvNeedBytes <= 114 * 1024 ||
+  static constexpr bool kPush = !BAL && !kSeven && !kThird && (SOLO || kBaseSmem + kRecvNeedBytes <= 114 * 1024 ||
                                          (kBaseSmem > 114 * 1024 && kBaseSmem + kRecvNeedBytes <= 227 * 1024));
   static constexpr int kRecvBytes = kPush ? kRecvNeedBytes : 0;
   static constexpr int kDataBytes = kWorkBytes + kRecvBytes;
@@ -205,6 +211,7 @@ struct PartialCfg {
   static_assert(kStagesPerWarp >= 2 || WQ >= 4, "at least two stages per warp (a ring of 4 or 8 for 4- or 8-warp groups)");
   static_assert(!(WQ == 8 && SOLO), "a query group of 8 warps is its CTA already");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+  static_assert(!kThird || 3 * (kSmemBytes + 1024) <= 228 * 1024, "three CTAs per SM");
   static_assert(CCQ == 0 || (BITS == 16 && D == DV && NT == 1 && WQ == 1 && kCh == 16 && kRB == 128),
                 "CUDA-core contraction: bf16 pages, equal head dims, 128-byte rows, one warp per query group");
   static_assert(!CCQ || kWarps <= 8, "weight buffers of at most 8 warps");

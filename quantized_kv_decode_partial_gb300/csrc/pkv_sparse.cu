@@ -869,11 +869,14 @@ template <int T>
 __global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: the scores, later the chosen blocks
-  wait_for_prerequisite_grids();
-  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
+  // Behind the scores, this grid starts once every CTA of theirs has seen the work before
+  // them complete: the inputs may be read before the scores are waited for.
+  if (!p.after_scores) wait_for_prerequisite_grids();
   const int unit = blockIdx.x;
   const int len = p.seq_lens[unit / p.num_kv_heads];
-  const float q1 = query_norm<T>(p, unit);  // while the length arrives
+  const float q1 = query_norm<T>(p, unit);
+  if (p.after_scores) wait_for_prerequisite_grids();
+  allow_dependent_launch();  // the attention may take its place on the SMs; it waits for this grid's end
   select_unit<T, false>(p, sh, sh_keys, unit, len, q1, 0u);
 }
 
@@ -1034,6 +1037,7 @@ cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device
     if (p.head_dim == 192) e = launch_score_of<192>(p, num_seqs, device, stream);
     if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, device, stream);
     if (e != cudaSuccess) return e;
+    p.after_scores = 1;
   }
   p.key_space = std::min(std::max(p.max_blocks, 1), kSelectMostKeys);
   return p.max_blocks <= 2048 ? launch_select_of<256>(p, num_seqs, device, stream)
