@@ -20,8 +20,6 @@ namespace pkv {
 
 namespace {
 
-constexpr int kHold = 8;  // 16-byte loads a thread keeps in registers between the two uses of the values
-
 // Elementwise maximum of the magnitudes of bf16 pairs (the values are finite).
 __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t w) {
   const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
@@ -69,7 +67,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }
 
-// Grid (touched block x KV head x plane, sequence).
+// Grid (touched block x KV head x plane, sequence). kHold: 16-byte loads a thread keeps in
+// registers between the two uses of the values (rows beyond those are read again).
+template <int kHold>
 __global__ void __launch_bounds__(128) pkv_append_blocks_kernel(const __grid_constant__ AppendBlockParams p) {
   __shared__ uint32_t red[4];
   wait_for_prerequisite_grids();
@@ -161,17 +161,21 @@ cudaError_t launch_append_blocks(const AppendBlockParams& p, int num_seqs, cudaS
   const long long units = static_cast<long long>(blocks) * p.num_kv_heads * 2;
   if (units >= (1ll << 31)) return cudaErrorInvalidValue;
   const int rows = p.n_new < p.block_size ? p.n_new : p.block_size;
+  const int loads = rows * (max(p.dim[0], p.dim[1]) / 8);  // 16-byte loads of a unit
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units), num_seqs);
-  // one warp where it holds a unit's rows in registers (a few tokens), else four
-  cfg.blockDim = dim3(rows * (max(p.dim[0], p.dim[1]) / 8) <= kHold * 32 ? 32 : 128);
+  // One warp where it holds a unit's rows in registers (a few tokens), else four: with 4 loads
+  // per thread while that covers a unit (fewer registers, more units per SM), else with 8.
+  const bool one_warp = loads <= 4 * 32;
+  cfg.blockDim = dim3(one_warp ? 32 : 128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_append_blocks_kernel, p);
+  return loads <= 4 * 128 ? cudaLaunchKernelEx(&cfg, pkv_append_blocks_kernel<4>, p)
+                          : cudaLaunchKernelEx(&cfg, pkv_append_blocks_kernel<8>, p);
 }
 
 }  // namespace pkv
