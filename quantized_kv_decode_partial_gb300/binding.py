@@ -602,10 +602,15 @@ def _require(dtype: torch.dtype, **tensors) -> None:
             raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
-def _require_contiguous(**tensors) -> None:
-    for name, t in tensors.items():
+def _contiguous(*tensors) -> bool:
+    for t in tensors:
         if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+            return False
+    return True
+
+
+def _not_contiguous() -> None:
+    raise ValueError("tensors must be contiguous")
 
 
 def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
@@ -635,8 +640,8 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
         if D == 192:  # the values are not looked at; no pages have 192-dim ones
             layout.v_head_dim = 128
         call = _remember(key, _Call(layout, DecodeParams(), k_bounds))
-    _require_contiguous(k_pool=k_pool, block_tables=block_tables, seq_lens=seq_lens, k_bounds=k_bounds,
-                        k_scales=k_scales, k_biases=k_biases)
+    if not _contiguous(k_pool, block_tables, seq_lens, k_bounds, k_scales, k_biases):
+        _not_contiguous()
     B, max_blocks = block_tables.shape
     with _on_device(k_pool.device):
         rc = lib.pkv_update_block_bounds(call.layout_ref, B, max_blocks, n_new, k_pool.data_ptr(), _ptr(k_scales),
@@ -691,8 +696,8 @@ def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.T
             _require_shape("out.blocks", out.blocks, B, hk, top_k)
             _require_shape("out.tables", out.tables, B, hk, top_k)
             _require_shape("out.lens", out.lens, B, hk)
-        _require_contiguous(q=q, k_bounds=k_bounds, block_tables=block_tables, seq_lens=seq_lens, blocks=out.blocks,
-                            tables=out.tables, lens=out.lens)
+        if not _contiguous(q, k_bounds, block_tables, seq_lens, *out):
+            _not_contiguous()
         if workspace is None and call.workspace_bytes:
             workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -735,8 +740,8 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
             call = _Call(layout, DecodeParams(B, HQ, N, top_k, partition_tokens, 0, contraction, schedule), q, sparse)
             call.workspace_bytes = make_sparse_plan(layout, call.params, sparse).attention.workspace_bytes
             _remember(key, call)
-        _require_contiguous(q=q, k_pool=k_pool, v_pool=v_pool, tables=tables, lens=lens, k_scales=k_scales,
-                            k_biases=k_biases, v_scales=v_scales, v_biases=v_biases, out=out)
+        if not _contiguous(q, k_pool, v_pool, tables, lens, k_scales, k_biases, v_scales, v_biases, out):
+            _not_contiguous()
         if out is None:
             out = call.new_out(q)
         if workspace is None and call.workspace_bytes:
@@ -786,9 +791,9 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
                          q, SparseParams(top_k, first_blocks, last_blocks))
             call.workspace_bytes = make_sparse_plan(layout, call.params, call.sparse).workspace_bytes
             _remember(key, call)
-        _require_contiguous(q=q, k_pool=k_pool, v_pool=v_pool, k_bounds=k_bounds, block_tables=block_tables,
-                            seq_lens=seq_lens, blocks=blocks, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
-                            v_biases=v_biases, out=out)
+        if not _contiguous(q, k_pool, v_pool, k_bounds, block_tables, seq_lens, blocks, out, k_scales, k_biases, v_scales,
+                           v_biases):
+            _not_contiguous()
         if out is None:
             out = call.new_out(q)
         if workspace is None:

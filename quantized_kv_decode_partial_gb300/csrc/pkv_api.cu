@@ -1015,31 +1015,46 @@ int check_sparse(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
   return PKV_OK;
 }
 
-// Rows per partition of the decode over `blocks` chosen blocks per unit (0: the library's
-// choice). The units read the same number of rows, as a
-// rule, so the partitions are as many as one wave holds, of 256 rows or more, and merge in
-// clusters: of the grids of one and of two CTAs per SM the one that fills more of its wave,
-// the former where they tie. 64 units of 4096 bf16 rows (D=128, 16 query rows): 2 partitions
-// 26.9 us, the library's choice (8, through the workspace) 32.0 us; 64 units of 1536 4-bit
-// rows (D=256): 2 partitions 12.6 us, the library's choice (balanced) 21.5 us.
-int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int blocks, int sm_count) {
+// Rows per partition of the decode over `blocks` chosen blocks per unit, of a table of `width`
+// (0: the library's choice). The units read the same number of rows, as a rule, so a grid of
+// one wave whose partitions merge in clusters wastes little, and needs neither a second launch
+// nor the workspace. How many partitions, from whole sparse steps of 8 to 512 units of 512 to
+// 8192 rows (D=128; 4 and 16 query rows; bf16, e4m3 and 4-bit pages):
+//  * Shapes with a variant for one CTA per SM (`one`): 4 per unit up to a wave (32 units of 4096
+//    bf16 rows: 27.8 us; 2: 29.0, 8: 28.0), 2 (64 units: 38.7 us; 4: 39.7, 8: 41.5), else 1.
+//    More than 4 only while they are at most 96 CTAs: clusters of 8 that hold whole SMs do not
+//    all fit the GPCs at once (16 units of 4096 rows: 6 per unit 23.1 us, 8 per unit 26.9).
+//  * Others: up to 8, 256 CTAs at most (64 units of 4096 e4m3 rows, 16 query rows: 4 per unit
+//    37.2 us; 2: 44.1, 8: 41.2).
+//  * Up to two CTAs per SM: 1, or 3 through the workspace for long units and few query rows
+//    (256 units of 4096 4-bit rows: 79.3 -> 67.8 us).
+//  * More units: the library's choice, but for e4m3 up to four waves 4 (512 units of 2048
+//    rows: 58.4 -> 50.9 us).
+//  * Behind scores of many blocks, the library's choice: its CTAs share their SMs with the
+//    kernels before and after (64 units of 4096 rows chosen from 131072: 100.3 -> 93.9 us).
+int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int blocks, int width, int sm_count) {
   const long long units = vp->num_seqs, rows = static_cast<long long>(blocks) * vl->block_size, sms = sm_count;
+  const bool many_scores = units * width * 4 * vl->head_dim >= (64ll << 20);  // 64 MB of bounds or more
   const int nq = vp->num_q_heads * vp->n_query;
   const bool cc = vp->contraction == PKV_CONTRACTION_CUDA_CORE;
   const PartialInfo one = partial_info(format_of(vl), vl->head_dim, v_dim(vl), nq, true, cc);
   const PartialInfo two = partial_info(format_of(vl), vl->head_dim, v_dim(vl), nq, false, cc);
-  const long long per_sm = two.smem_bytes <= 114 * 1024 ? 2 : 1;
-  const long long most = std::max(1ll, rows / 256);
-  const long long p1 = one.exists && vl->block_size >= two.chunk_rows
-                           ? std::min(std::min<long long>(pkv::kMaxClusterParts, sms / units), most)
-                           : 0;
-  const long long p2 = std::min(std::min(per_sm == 2 ? 16ll : 8ll, per_sm * sms / units), most);
-  long long parts = units * p1 * per_sm >= units * p2 ? p1 : p2;
-  // One to four waves of e4m3 units: four partitions each even out the last wave while a CTA
-  // reads 128 KB or more (512 units of 2048 rows, D=128: 58.4 -> 50.9 us).
-  if (parts == 0 && block_scaled(vl) && units <= 4 * 3 * sms && rows * stored_row_bytes(vl, vl->head_dim) >= (256ll << 10))
+  const bool solo = one.exists && vl->block_size >= two.chunk_rows;
+  long long parts = 0;
+  if (many_scores && units <= 2 * sms) {
+    // the library's choice
+  } else if (solo && units <= sms) {
+    parts = std::min(8ll, 96 / units);
+    if (parts < 4) parts = 4 * units <= sms ? 4 : 2 * units <= sms ? 2 : 1;
+  } else if (units <= 2 * sms) {
+    parts = std::min(8ll, std::max(1ll, 256 / units));
+    if (parts == 1 && rows >= 4096 && nq <= 8) parts = 3;
+  } else if (block_scaled(vl) && units <= 4 * 3 * sms && rows * vl->head_dim >= (256ll << 10)) {
     parts = 4;
-  return parts > 0 ? static_cast<int>(round_up((rows + parts - 1) / parts, chunk_rows_of(vl->bits))) : 0;
+  }
+  if (parts == 0) return 0;
+  parts = std::min(parts, std::max(1ll, rows / 128));
+  return static_cast<int>(round_up((rows + parts - 1) / parts, chunk_rows_of(vl->bits)));
 }
 
 // The decode over chosen blocks: the pool as NB * HK blocks of one KV head, every (sequence,
@@ -1054,7 +1069,8 @@ void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
   vp->num_q_heads = P->num_q_heads / L->num_kv_heads;
   vp->max_blocks_per_seq = S->top_k;
   if (vp->partition_tokens == 0 && vp->schedule != PKV_SCHEDULE_BALANCED)
-    vp->partition_tokens = chosen_partition(vl, vp, std::min(S->top_k, P->max_blocks_per_seq), sm_count);
+    vp->partition_tokens = chosen_partition(vl, vp, std::min(S->top_k, P->max_blocks_per_seq), P->max_blocks_per_seq,
+                                            sm_count);
 }
 
 // Scores of a unit in the workspace: rows of 16-byte groups.

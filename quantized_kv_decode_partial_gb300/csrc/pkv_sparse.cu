@@ -262,7 +262,8 @@ constexpr __host__ __device__ int query_row_bytes(int D) { return D * 4 + 64; }
 // every warp of the CTA) of unit (b, h) with n blocks; sq: space for the query rows. ready()
 // runs once, in every thread, before the first result; put(j, key) and put_tile(tile, m) take
 // a block's score and the bits of a tile's largest |bound|.
-template <int D, int WARPS, typename Ready, typename Put, typename PutTile>
+// NT: most tiles of 8 query rows (nq <= 8 NT).
+template <int D, int NT, int WARPS, typename Ready, typename Put, typename PutTile>
 __device__ __forceinline__ void score_tiles(const SelectParams& p, size_t unit, int h, const int32_t* table, int n,
                                             int first_tile, int step, int count, uint8_t* sq, Ready ready, Put put,
                                             PutTile put_tile) {
@@ -277,88 +278,92 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, size_t unit, 
     return it < count && lane < kScoreTile && j < n ? table[j] : -1;
   };
   auto good = [&](int ph) { return static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks); };
-  int ids = ids_of(0), ids_next = ids_of(1);
-  for (int it = 0; it < count; ++it) {
-    const int tile = first_tile + it * step;  // warp-uniform
-    const int j0 = tile * kScoreTile;
-    const bool live = j0 < n;
-    uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
-    int ph0 = -1, ph1 = -1;
-    if (live) {
-      const bool ok = good(ids);
-      if (!ok && lane < kScoreTile && j0 + lane < n && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
-      ph0 = __shfl_sync(0xffffffffu, ok ? ids : -1, g);
-      ph1 = __shfl_sync(0xffffffffu, ok ? ids : -1, g + 8);
-      const __nv_bfloat16* r0 = p.k_bounds + (static_cast<size_t>(ph0 < 0 ? 0 : ph0) * p.num_kv_heads + h) * 2 * D + 8 * t;
-      const __nv_bfloat16* r1 = p.k_bounds + (static_cast<size_t>(ph1 < 0 ? 0 : ph1) * p.num_kv_heads + h) * 2 * D + 8 * t;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        lo0[i] = ph0 >= 0 ? ld_nc_keep_v4(r0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-        hi0[i] = ph0 >= 0 ? ld_nc_keep_v4(r0 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-        lo1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-        hi1[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    {  // the next tile's bounds towards L2, half of each block's lines per half warp
-      const int ph = __shfl_sync(0xffffffffu, ids_next, lane & 15);
-      if (good(ph)) {
-        const __nv_bfloat16* r = p.k_bounds + (static_cast<size_t>(ph) * p.num_kv_heads + h) * 2 * D + (lane >> 4) * D;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) prefetch_l2(r + 64 * i);
-      }
-    }
-    ids = ids_next;
-    ids_next = ids_of(it + 2);
-    if (it == 0) {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
-      const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
-      for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += WARPS * 32) {
-        const int r = i / (D / 8), c = i - r * (D / 8);
-        const uint4 v = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) =
-            make_uint4(max_bf16x2(v.x, 0u), max_bf16x2(v.y, 0u), max_bf16x2(v.z, 0u), max_bf16x2(v.w, 0u));
-        *reinterpret_cast<uint4*>(sq + r * kStride + D * 2 + c * 16) =
-            make_uint4(min_bf16x2(v.x, 0u), min_bf16x2(v.y, 0u), min_bf16x2(v.z, 0u), min_bf16x2(v.w, 0u));
-      }
-      __syncthreads();
-      ready();
-    }
-    if (!live) continue;
-    // the largest magnitude of the tile's bounds: what the choice's error bound needs
-    uint32_t mm[4] = {0u, 0u, 0u, 0u};
+  // one bound (0: lo, 1: hi) of blocks ph0 and ph1, in fragment order; zeros for a bad block
+  auto load = [&](int ph0, int ph1, int bound, uint4 (&a)[kSteps], uint4 (&b)[kSteps]) {
+    const __nv_bfloat16* r0 = p.k_bounds + (static_cast<size_t>(ph0 < 0 ? 0 : ph0) * p.num_kv_heads + h) * 2 * D + 8 * t;
+    const __nv_bfloat16* r1 = p.k_bounds + (static_cast<size_t>(ph1 < 0 ? 0 : ph1) * p.num_kv_heads + h) * 2 * D + 8 * t;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const uint4 w[4] = {lo0[i], hi0[i], lo1[i], hi1[i]};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mm[0] = max_abs_bf16x2(mm[0], w[k].x);
-        mm[1] = max_abs_bf16x2(mm[1], w[k].y);
-        mm[2] = max_abs_bf16x2(mm[2], w[k].z);
-        mm[3] = max_abs_bf16x2(mm[3], w[k].w);
-      }
+      a[i] = ph0 >= 0 ? ld_nc_keep_v4(r0 + bound * D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+      b[i] = ph1 >= 0 ? ld_nc_keep_v4(r1 + bound * D + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     }
-    uint32_t m = max_bf16x2(max_bf16x2(mm[0], mm[1]), max_bf16x2(mm[2], mm[3]));
-    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-    put_tile(tile, m << 16);
+  };
+  // the blocks g and g + 8 of a tile, -1 where there is none
+  auto pick = [&](int ids, int& ph0, int& ph1) {
+    const int ph = good(ids) ? ids : -1;
+    ph0 = __shfl_sync(0xffffffffu, ph, g);
+    ph1 = __shfl_sync(0xffffffffu, ph, g + 8);
+  };
 
-    float best0 = -INFINITY, best1 = -INFINITY;  // blocks j0 + g and j0 + g + 8
-    for (int nt = 0; nt < ntiles; ++nt) {
-      float up[4] = {0.f, 0.f, 0.f, 0.f}, dn[4] = {0.f, 0.f, 0.f, 0.f};
+  int ids = ids_of(0), ids_next = ids_of(1);
+  uint4 lo0[kSteps], hi0[kSteps], lo1[kSteps], hi1[kSteps];
+  int ph0, ph1;
+  pick(ids, ph0, ph1);
+  load(ph0, ph1, 1, hi0, hi1);
+  load(ph0, ph1, 0, lo0, lo1);
+  {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
+    const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
+    for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += WARPS * 32) {
+      const int r = i / (D / 8), c = i - r * (D / 8);
+      const uint4 v = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) =
+          make_uint4(max_bf16x2(v.x, 0u), max_bf16x2(v.y, 0u), max_bf16x2(v.z, 0u), max_bf16x2(v.w, 0u));
+      *reinterpret_cast<uint4*>(sq + r * kStride + D * 2 + c * 16) =
+          make_uint4(min_bf16x2(v.x, 0u), min_bf16x2(v.y, 0u), min_bf16x2(v.z, 0u), min_bf16x2(v.w, 0u));
+    }
+    __syncthreads();
+    ready();
+  }
+  for (int it = 0; it < count; ++it) {
+    const int j0 = (first_tile + it * step) * kScoreTile;  // warp-uniform
+    if (j0 >= n) break;
+    if (!good(ids) && lane < kScoreTile && j0 + lane < n && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+    int next0, next1;
+    pick(ids_next, next0, next1);
+    const int ids_after = ids_of(it + 2);
+    // Each bound's registers take the next tile's as soon as the MMAs have read them, so that
+    // loads are in flight throughout. mm: the tile's largest magnitude, for the choice's E.
+    uint32_t mm[4] = {0u, 0u, 0u, 0u};
+    float acc[NT][2][4];  // <max(q, 0), hi> and <min(q, 0), lo>, apart for the sake of latency
+    auto half = [&](int bound, uint4 (&a)[kSteps], uint4 (&b)[kSteps]) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const uint8_t* const at = sq + (8 * nt + g) * kStride + (32 * i + 8 * t) * 2;
-        const uint4 pos = *reinterpret_cast<const uint4*>(at), neg = *reinterpret_cast<const uint4*>(at + D * 2);
-        mma_bf16(up, hi0[i].x, hi1[i].x, hi0[i].y, hi1[i].y, pos.x, pos.y);
-        mma_bf16(dn, lo0[i].x, lo1[i].x, lo0[i].y, lo1[i].y, neg.x, neg.y);
-        mma_bf16(up, hi0[i].z, hi1[i].z, hi0[i].w, hi1[i].w, pos.z, pos.w);
-        mma_bf16(dn, lo0[i].z, lo1[i].z, lo0[i].w, lo1[i].w, neg.z, neg.w);
+        mm[0] = max_abs_bf16x2(max_abs_bf16x2(mm[0], a[i].x), b[i].x);
+        mm[1] = max_abs_bf16x2(max_abs_bf16x2(mm[1], a[i].y), b[i].y);
+        mm[2] = max_abs_bf16x2(max_abs_bf16x2(mm[2], a[i].z), b[i].z);
+        mm[3] = max_abs_bf16x2(max_abs_bf16x2(mm[3], a[i].w), b[i].w);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float (&c)[4] = acc[nt][bound];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = 0.f;
+        if (nt >= ntiles) continue;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint4 q = *reinterpret_cast<const uint4*>(sq + (8 * nt + g) * kStride + (bound ? 0 : D * 2) +
+                                                          (32 * i + 8 * t) * 2);
+          mma_bf16(c, a[i].x, b[i].x, a[i].y, b[i].y, q.x, q.y);
+          mma_bf16(c, a[i].z, b[i].z, a[i].w, b[i].w, q.z, q.w);
+        }
+      }
+      load(next0, next1, bound, a, b);
+    };
+    half(1, hi0, hi1);
+    half(0, lo0, lo1);
+    uint32_t m = max_bf16x2(max_bf16x2(mm[0], mm[1]), max_bf16x2(mm[2], mm[3]));
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    put_tile(first_tile + it * step, m << 16);
+
+    float best0 = -INFINITY, best1 = -INFINITY;  // blocks j0 + g and j0 + g + 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (8 * nt + 2 * t + e < p.nq) {
-          best0 = fmaxf(best0, up[e] + dn[e]);
-          best1 = fmaxf(best1, up[e + 2] + dn[e + 2]);
+          best0 = fmaxf(best0, acc[nt][0][e] + acc[nt][1][e]);
+          best1 = fmaxf(best1, acc[nt][0][e + 2] + acc[nt][1][e + 2]);
         }
-    }
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
       best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, d));
@@ -368,11 +373,15 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, size_t unit, 
       if (j0 + g < n) put(j0 + g, order_key(ph0 >= 0 ? best0 : -INFINITY));
       if (j0 + g + 8 < n) put(j0 + g + 8, order_key(ph1 >= 0 ? best1 : -INFINITY));
     }
+    ph0 = next0;
+    ph1 = next1;
+    ids = ids_next;
+    ids_next = ids_after;
   }
 }
 
 // Scores alone, into the workspace.
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) uint8_t sq[];
   wait_for_prerequisite_grids();
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
   const int n = (len + p.block_size - 1) / p.block_size;
   const int cta_tile = chunk * kScoreWarps * p.tiles_per_warp;
   if (n <= p.top_k || cta_tile * kScoreTile >= n) return;  // every block is taken, or none is here
-  score_tiles<D, kScoreWarps>(
+  score_tiles<D, NT, kScoreWarps>(
       p, unit, h, p.block_tables + static_cast<size_t>(b) * p.max_blocks, n, cta_tile + warp, kScoreWarps,
       p.tiles_per_warp, sq, [] {}, [&](int j, uint32_t key) { p.scores[unit * p.score_stride + j] = key; },
       [&](int tile, uint32_t m) {
@@ -891,7 +900,7 @@ constexpr int kFusedThreads = 256;
 constexpr int kFusedCluster = 8;
 constexpr int kFusedBlocks = kFusedCluster * kFusedThreads / 32 * kScoreTile;  // 1024
 
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kFusedThreads)
     pkv_choose_kernel(const __grid_constant__ SelectParams p) {
   __shared__ SelectShared<kFusedThreads> sh;
@@ -909,7 +918,7 @@ __global__ void __launch_bounds__(kFusedThreads)
     constexpr int kWarps = kFusedThreads / 32;
     const int warp = threadIdx.x >> 5, tiles = (n + kScoreTile - 1) / kScoreTile;
     cluster_arrive_relaxed();  // tells that this CTA runs; the first CTA's memory is written after all have
-    score_tiles<D, kWarps>(
+    score_tiles<D, NT, kWarps>(
         p, unit, h, p.block_tables + static_cast<size_t>(b) * p.max_blocks, n, rank * kWarps + warp, ctas * kWarps,
         (tiles + ctas * kWarps - 1) / (ctas * kWarps), reinterpret_cast<uint8_t*>(sh_keys + p.key_space),
         [] { cluster_wait(); }, [&](int j, uint32_t key) { st_cluster_u32(smem_addr(sh_keys + j), 0, key); },
@@ -952,10 +961,10 @@ cudaError_t launch_select_of(const SelectParams& p, int num_seqs, int device, cu
   return cudaLaunchKernelEx(&cfg, pkv_select_kernel<T>, p);
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  const cudaError_t e = allow_smem(pkv_score_kernel<D>, 64 * query_row_bytes(D), configured, device);
+  const cudaError_t e = allow_smem(pkv_score_kernel<D, NT>, 64 * query_row_bytes(D), configured, device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int per_cta = kScoreWarps * p.tiles_per_warp;
@@ -970,14 +979,14 @@ cudaError_t launch_score_of(const SelectParams& p, int num_seqs, int device, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_score_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, pkv_score_kernel<D, NT>, p);
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_choose_of(const SelectParams& p, int units, int cluster, int device, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e =
-      allow_smem(pkv_choose_kernel<D>, kFusedBlocks * 4 + 64 * query_row_bytes(D), configured, device);
+      allow_smem(pkv_choose_kernel<D, NT>, kFusedBlocks * 4 + 64 * query_row_bytes(D), configured, device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cluster, units);
@@ -993,7 +1002,7 @@ cudaError_t launch_choose_of(const SelectParams& p, int units, int cluster, int 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pkv_choose_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, pkv_choose_kernel<D, NT>, p);
 }
 
 }  // namespace
@@ -1017,10 +1026,10 @@ cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device
     while (cluster * (kFusedThreads / 32) < p.tiles) cluster *= 2;
     if (units * cluster <= sm_count) {
       p.key_space = (p.max_blocks + 3) / 4 * 4;
-      if (p.head_dim == 64) return launch_choose_of<64>(p, units, cluster, device, stream);
-      if (p.head_dim == 128) return launch_choose_of<128>(p, units, cluster, device, stream);
-      if (p.head_dim == 192) return launch_choose_of<192>(p, units, cluster, device, stream);
-      if (p.head_dim == 256) return launch_choose_of<256>(p, units, cluster, device, stream);
+#define X(D_, NT_) \
+  if (p.head_dim == D_ && p.nq <= 8 * NT_) return launch_choose_of<D_, NT_>(p, units, cluster, device, stream);
+      X(64, 1) X(128, 1) X(192, 1) X(256, 1) X(64, 8) X(128, 8) X(192, 8) X(256, 8)
+#undef X
       return cudaErrorInvalidValue;
     }
   }
@@ -1031,11 +1040,14 @@ cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device
     const long long fill = 4ll * 16 * (sm_count > 0 ? sm_count : 1);
     const long long per = tiles / fill;
     p.tiles_per_warp = static_cast<int>(per < 1 ? 1 : per > 8 ? 8 : per);
-    cudaError_t e = cudaErrorInvalidValue;
-    if (p.head_dim == 64) e = launch_score_of<64>(p, num_seqs, device, stream);
-    if (p.head_dim == 128) e = launch_score_of<128>(p, num_seqs, device, stream);
-    if (p.head_dim == 192) e = launch_score_of<192>(p, num_seqs, device, stream);
-    if (p.head_dim == 256) e = launch_score_of<256>(p, num_seqs, device, stream);
+    auto score = [&]() -> cudaError_t {
+#define X(D_, NT_) \
+  if (p.head_dim == D_ && p.nq <= 8 * NT_) return launch_score_of<D_, NT_>(p, num_seqs, device, stream);
+      X(64, 1) X(128, 1) X(192, 1) X(256, 1) X(64, 2) X(128, 2) X(192, 2) X(256, 2) X(64, 8) X(128, 8) X(192, 8) X(256, 8)
+#undef X
+      return cudaErrorInvalidValue;
+    };
+    const cudaError_t e = score();
     if (e != cudaSuccess) return e;
     p.after_scores = 1;
   }
