@@ -418,7 +418,7 @@ int pkv_paged_decode_append_attention(const pkv_pool_layout* layout, const pkv_d
  * Choice. With nb = ceil(len / block_size) blocks held: all of them when nb <= top_k, else
  * the first_blocks first, the last_blocks last and, of those between, the best-scored, in
  * all top_k. Blocks are compared as by exact sums, ties going to the lower block: f32 sums
- * decide where their error cannot matter, f64 sums of exact products elsewhere, so the
+ * decide where their error cannot matter, sums of 48 bits of exact products elsewhere, so the
  * choice does not depend on the order of a sum. A NaN score counts as the lowest.
  *
  * The softmax then runs over the chosen rows alone, the causal rule among the n_query newest

@@ -1078,7 +1078,7 @@ size_t score_stride(const pkv_decode_params* P) { return (static_cast<size_t>(P-
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Offsets into the workspace of the choice (scores, tile magnitudes, f64 keys) and, after
+// Offsets into the workspace of the choice (scores, tile magnitudes, exact keys) and, after
 // it, of a whole sparse step (chosen tables and lengths, then the attention's workspace).
 struct SparseWorkspace {
   size_t tile_abs, keys64, select_bytes, tables, lens, attention;

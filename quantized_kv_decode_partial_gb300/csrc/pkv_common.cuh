@@ -148,7 +148,7 @@ struct SelectParams {
   const int32_t* seq_lens;
   uint32_t* scores;               // [units, score_stride]: f32 scores as integers of the same order
   float* tile_abs;                // [units, tiles]: largest magnitude of 16 blocks' bounds
-  unsigned long long* keys64;     // [units, max_blocks]: f64 scores of ambiguous blocks, as ordered integers
+  unsigned long long* keys64;     // [units, max_blocks]: exact scores of many ambiguous blocks, as ordered integers
   int32_t* out_blocks;            // [units, top_k], optional
   int32_t* out_tables;            // [units, top_k]
   int32_t* out_lens;              // [units]
@@ -280,11 +280,6 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
 // Starts fetching the 128-byte line holding `ptr` into L1 (and L2).
 __device__ __forceinline__ void prefetch_l1(const void* ptr) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(ptr));
-}
-
-// Starts fetching the 128-byte line holding `ptr` into L2.
-__device__ __forceinline__ void prefetch_l2(const void* ptr) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr));
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {

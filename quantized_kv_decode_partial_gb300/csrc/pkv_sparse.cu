@@ -237,9 +237,11 @@ cudaError_t launch_bounds_of(const BoundsParams& p, int num_seqs, cudaStream_t s
 // over 2 D. The order of the dims within the contraction is free, so the A fragments are the
 // 16-byte loads themselves (each lane 8 dims of two blocks per load, four lanes a 64-byte
 // run) and no bound passes through shared memory; the B fragment of the same dims is 16
-// bytes of a query row. Bound by HBM: 4 D bytes per (block, KV head). While a warp works on a
-// tile, its next tile's bounds are on their way into L2, which keeps enough bytes in flight
-// with the 16 warps that the fragments' registers leave room for.
+// bytes of a query row. Bound by HBM: 4 D bytes per (block, KV head). The registers of each
+// bound take the next tile's values as soon as the MMAs have read them, so that the 16 warps
+// they leave room for keep loads in flight throughout. Bulk copies of a block's two rows (512
+// bytes) into rings in shared memory were slower (64 units of 8192 blocks, D=128, scores and
+// choice: 61.6 -> 70.2 us).
 //
 // Scores are stored as integers of the same order, NaN as -infinity.
 constexpr uint32_t kLowestScore = 0x007FFFFFu;  // of -infinity, and of NaN
@@ -417,8 +419,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 // sums with and without cancellation, is under a tenth of E).
 //
 // T comes from histograms of 2048 equal bins over [lowest, highest] key, narrowed to the bin
-// that holds the k-th until it is one value (two rounds as a rule): spread scores meet few
-// bank conflicts, which radix digits of nearby floats would. The marks of 32 blocks at a time
+// that holds the k-th until that holds at most 32 keys, which every warp then ranks (one round
+// as a rule): spread scores meet few bank conflicts, which radix digits of nearby floats would. The marks of 32 blocks at a time
 // (ballots) and a prefix over their counts then give each taken block its place.
 //
 // The CTA's time is a chain of dependent steps (loads, barriers, prefixes), so it takes as
@@ -439,10 +441,10 @@ struct SelectShared {
     } marks;
   };
   uint32_t red[32];
-  unsigned long long found;
+  unsigned long long few[32];  // keys of the threshold's bin
   unsigned long long amb_key[kSelectAmbiguous];  // ambiguous blocks: the exact score's key
   int amb[kSelectAmbiguous];                     // and the block
-  int bin, above, in_bin;
+  int bin, above, in_bin, few_count;
 };
 
 // Exclusive prefix over the block, in thread order, and the total.
@@ -498,6 +500,7 @@ __device__ __forceinline__ Key nth_largest(SelectShared<T>& sh, F key_of, int n,
       for (int j = 0; j < kPer; ++j) {
         const int c = sh.hist[top - j];
         if (above < need && above + c >= need) {
+          sh.few_count = 0;
           sh.bin = top - j;
           sh.above = above;
           sh.in_bin = c;
@@ -511,13 +514,25 @@ __device__ __forceinline__ Key nth_largest(SelectShared<T>& sh, F key_of, int n,
     if (shift == 0) return lo;
     const Key end = lo + ((static_cast<Key>(1) << shift) - 1);
     hi = end < hi ? end : hi;
-    if (sh.in_bin == 1) {  // alone in its bin
+    const int in_bin = sh.in_bin;
+    if (in_bin <= 32) {  // few in the bin: every warp ranks them, a lane each
       for (int i = threadIdx.x; i < n; i += T) {
         Key k;
-        if (key_of(i, k) && k >= lo && k <= hi) sh.found = static_cast<unsigned long long>(k);
+        if (key_of(i, k) && k >= lo && k <= hi) sh.few[atomicAdd(&sh.few_count, 1) & 31] = static_cast<unsigned long long>(k);
       }
       __syncthreads();
-      return static_cast<Key>(sh.found);
+      const int lane = threadIdx.x & 31;
+      const Key mine = lane < in_bin ? static_cast<Key>(sh.few[lane]) : Key(0);
+      int greater = 0, equal = 0;
+      for (int i = 0; i < in_bin; ++i) {
+        const Key o = __shfl_sync(0xffffffffu, mine, i);
+        greater += o > mine;
+        equal += o == mine;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, lane < in_bin && greater < need && need <= greater + equal);
+      const int at = hit ? __ffs(hit) - 1 : 0;
+      need -= __shfl_sync(0xffffffffu, greater, at);
+      return __shfl_sync(0xffffffffu, mine, at);
     }
   }
 }
@@ -875,7 +890,7 @@ __device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<
 
 // The choice alone, from the workspace's scores.
 template <int T>
-__global__ void __launch_bounds__(T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(T, 1024 / T) pkv_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sh_keys[];  // [key_space]: the scores, later the chosen blocks
   // Behind the scores, this grid starts once every CTA of theirs has seen the work before
