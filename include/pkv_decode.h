@@ -452,7 +452,9 @@ int pkv_sparse_plan_for_current_device(const pkv_pool_layout* layout, const pkv_
  *             rows before has its bounds widened by the new ones. e4m3 pages, whose earlier
  *             rows an append may have rescaled, have every touched block read whole.
  * A call with n_new of at least every length rebuilds all bounds. k_scales and k_biases as
- * for the decode. Keys must be finite. Bounds of other blocks stay as they were. Bad block
+ * for the decode. Keys must be finite. Bounds of other blocks stay as they were. Rows that a
+ * sequence gives up (its length falls back within a block) stay in that block's bounds, which
+ * then bound its keys less tightly, until a rebuild. Bad block
  * ids and lengths (outside [0, max_blocks_per_seq*block_size]) are skipped and flagged as
  * by pkv_paged_append. Blocks that receive rows must belong to one sequence only.
  * Asynchronous on `stream`. */
@@ -477,8 +479,9 @@ int pkv_select_blocks(const pkv_pool_layout* layout, const pkv_decode_params* pa
                       size_t workspace_bytes, int32_t* error_flag, void* stream);
 
 /* The attention alone, over a choice made by pkv_select_blocks (or one of the caller's own
- * in the same form: any blocks, the last chosen_lens rows of which end at the sequence's
- * newest). Workspace: plan.attention.workspace_bytes. Other arguments and errors as
+ * in the same form: any blocks of that KV head, in any order, the same one more than once if
+ * wanted; chosen_lens rows of them are read, and the last n_query of those count as the
+ * sequence's newest). Workspace: plan.attention.workspace_bytes. Other arguments and errors as
  * pkv_paged_decode_attention. */
 int pkv_selected_decode_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
                                   const pkv_sparse_params* sparse, const void* q, const void* k_pool,

@@ -2,7 +2,8 @@
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, and PyTorch allocates the output and
-the workspace. Every step of the computation runs in the library's kernels;
+the workspace (held between calls on the default stream, one per host thread
+and device). Every step of the computation runs in the library's kernels;
 there is no fallback, and a missing library raises ``LibraryNotBuilt``.
 """
 
@@ -198,7 +199,9 @@ def v_head_dim_of(v_pool: torch.Tensor, bits: int) -> int:
 
 def layout_for(k_pool: torch.Tensor, head_dim: int, bits: int, group_size: int = 64,
                v_pool: Optional[torch.Tensor] = None) -> PoolLayout:
-    nb, hk, bs, _ = k_pool.shape
+    nb, hk, bs, width = k_pool.shape
+    if width * k_pool.element_size() * 8 != head_dim * bits:
+        raise ValueError(f"k_pool rows of {width} {k_pool.dtype} are not {head_dim} values of {bits} bits")
     dv = 0 if v_pool is None else v_head_dim_of(v_pool, bits)
     return PoolLayout(nb, hk, bs, head_dim, bits, group_size, 0 if dv == head_dim else dv)
 
@@ -303,17 +306,22 @@ def _remember(key, call):
     return call
 
 
-def _check_block_scales(bits: int, group_size: int, *scales) -> None:
+def _check_block_scales(k_pool, bits: int, group_size: int, *scales) -> None:
     if bits == 8 and group_size == PKV_GROUP_BLOCK:
+        cells = k_pool.shape[:2]
         for s in scales:
-            if s is not None and s.dtype is not torch.float32:
+            if s is None:
+                continue
+            if s.dtype is not torch.float32:
                 raise TypeError(f"scales of e4m3 pages are float32 [num_blocks, num_kv_heads], not {s.dtype}")
+            if s.shape != cells or not s.is_contiguous():
+                raise ValueError("scales of e4m3 pages are contiguous [num_blocks, num_kv_heads] planes")
 
 
 def _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
                  schedule) -> _Call:
     """Cached by what settles the call; runs with q's device current."""
-    key = (q.get_device(), q.shape, k_pool.shape, v_pool.shape, v_pool.dtype, block_tables.shape, bits, group_size,
+    key = (q.get_device(), q.shape, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, block_tables.shape, bits, group_size,
            partition_tokens, window, contraction, schedule)
     call = _calls.get(key)
     if call is None:
@@ -344,7 +352,7 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     CUDA stream of q's device and returns bf16 [B, HQ, N, D].
     """
     lib = load_library()
-    _check_block_scales(bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
         call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
@@ -550,9 +558,9 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
     """Writes k_new/v_new bf16 [B, HK, n_new, D] at positions seq_lens[b].. of each
     sequence (quantising affine and e4m3 pages); see include/pkv_decode.h."""
     lib = load_library()
-    _check_block_scales(bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
     B, HK, n_new, D = k_new.shape
-    key = ("append", k_new.get_device(), k_pool.shape, v_pool.shape, v_pool.dtype, D, bits, group_size)
+    key = ("append", k_new.get_device(), k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, D, bits, group_size)
     call = _calls.get(key)
     if call is None:
         call = _remember(key, _Call(layout_for(k_pool, D, bits, group_size, v_pool), DecodeParams(), k_new))
@@ -602,15 +610,11 @@ def _require(dtype: torch.dtype, **tensors) -> None:
             raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
-def _contiguous(*tensors) -> bool:
+def _check_tensors(index: int, *tensors) -> None:
+    """All contiguous and on device `index`."""
     for t in tensors:
-        if t is not None and not t.is_contiguous():
-            return False
-    return True
-
-
-def _not_contiguous() -> None:
-    raise ValueError("tensors must be contiguous")
+        if t is not None and not (t.is_contiguous() and t.get_device() == index):
+            raise ValueError("tensors must be contiguous and on one device")
 
 
 def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
@@ -626,7 +630,7 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
     up to date after the last n_new rows of every sequence were appended (seq_lens counts
     them); see include/pkv_decode.h. Returns k_bounds."""
     lib = load_library()
-    _check_block_scales(bits, group_size, k_scales)
+    _check_block_scales(k_pool, bits, group_size, k_scales)
     key = ("bounds", k_bounds.get_device(), k_pool.shape, k_pool.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
            block_tables.dtype, seq_lens.shape, seq_lens.dtype, bits, group_size)
     call = _calls.get(key)
@@ -640,8 +644,7 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
         if D == 192:  # the values are not looked at; no pages have 192-dim ones
             layout.v_head_dim = 128
         call = _remember(key, _Call(layout, DecodeParams(), k_bounds))
-    if not _contiguous(k_pool, block_tables, seq_lens, k_bounds, k_scales, k_biases):
-        _not_contiguous()
+    _check_tensors(k_bounds.get_device(), k_pool, block_tables, seq_lens, k_bounds, k_scales, k_biases, error_flag)
     B, max_blocks = block_tables.shape
     with _on_device(k_pool.device):
         rc = lib.pkv_update_block_bounds(call.layout_ref, B, max_blocks, n_new, k_pool.data_ptr(), _ptr(k_scales),
@@ -696,8 +699,7 @@ def select_blocks(q: torch.Tensor, k_bounds: torch.Tensor, block_tables: torch.T
             _require_shape("out.blocks", out.blocks, B, hk, top_k)
             _require_shape("out.tables", out.tables, B, hk, top_k)
             _require_shape("out.lens", out.lens, B, hk)
-        if not _contiguous(q, k_bounds, block_tables, seq_lens, *out):
-            _not_contiguous()
+        _check_tensors(q.get_device(), q, k_bounds, block_tables, seq_lens, *out, workspace, error_flag)
         if workspace is None and call.workspace_bytes:
             workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -720,11 +722,11 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     """Decode attention over chosen blocks (pkv_selected_decode_attention); otherwise as
     ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
     tables, lens = selection.tables, selection.lens
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
-        key = ("selected", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, tables.shape,
+        key = ("selected", q.get_device(), q.shape, q.dtype, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, tables.shape,
                tables.dtype, lens.shape, lens.dtype, bits, group_size, partition_tokens, contraction, schedule)
         call = _calls.get(key)
         if call is None:
@@ -733,6 +735,7 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
             top_k = tables.shape[-1]
             _require(torch.bfloat16, q=q)
             _require(torch.int32, tables=tables, lens=lens)
+            _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
             _require_shape("selection.tables", tables, B, layout.num_kv_heads, top_k)
             _require_shape("selection.lens", lens, B, layout.num_kv_heads)
             # which blocks were taken is settled: any numbers that hold the new rows
@@ -740,10 +743,13 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
             call = _Call(layout, DecodeParams(B, HQ, N, top_k, partition_tokens, 0, contraction, schedule), q, sparse)
             call.workspace_bytes = make_sparse_plan(layout, call.params, sparse).attention.workspace_bytes
             _remember(key, call)
-        if not _contiguous(q, k_pool, v_pool, tables, lens, k_scales, k_biases, v_scales, v_biases, out):
-            _not_contiguous()
+        _check_tensors(q.get_device(), q, k_pool, v_pool, tables, lens, k_scales, k_biases, v_scales, v_biases, out,
+                       workspace, error_flag)
         if out is None:
             out = call.new_out(q)
+        else:
+            _require(torch.bfloat16, out=out)
+            _require_shape("out", out, *call.out_shape)
         if workspace is None and call.workspace_bytes:
             workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -770,10 +776,10 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     last always among them (pkv_sparse_decode_attention). ``blocks`` int32 [B, HK, top_k]
     receives the choice. Otherwise as ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
-        key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, v_pool.shape, v_pool.dtype, k_bounds.shape,
+        key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, k_bounds.shape,
                k_bounds.dtype, block_tables.shape, block_tables.dtype, seq_lens.shape, seq_lens.dtype,
                None if blocks is None else (blocks.shape, blocks.dtype), bits, group_size, partition_tokens,
                contraction, schedule, top_k, first_blocks, last_blocks)
@@ -784,6 +790,7 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
             _require(torch.bfloat16, q=q, k_bounds=k_bounds)
             _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens, blocks=blocks)
             _require_shape("k_bounds", k_bounds, layout.num_blocks, layout.num_kv_heads, 2, D)
+            _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
             _require_shape("block_tables", block_tables, B, block_tables.shape[1])
             _require_shape("seq_lens", seq_lens, B)
             _require_shape("blocks", blocks, B, layout.num_kv_heads, top_k)
@@ -791,11 +798,13 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
                          q, SparseParams(top_k, first_blocks, last_blocks))
             call.workspace_bytes = make_sparse_plan(layout, call.params, call.sparse).workspace_bytes
             _remember(key, call)
-        if not _contiguous(q, k_pool, v_pool, k_bounds, block_tables, seq_lens, blocks, out, k_scales, k_biases, v_scales,
-                           v_biases):
-            _not_contiguous()
+        _check_tensors(q.get_device(), q, k_pool, v_pool, k_bounds, block_tables, seq_lens, blocks, out, k_scales, k_biases,
+                       v_scales, v_biases, workspace, error_flag)
         if out is None:
             out = call.new_out(q)
+        else:
+            _require(torch.bfloat16, out=out)
+            _require_shape("out", out, *call.out_shape)
         if workspace is None:
             workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
         ws_bytes = workspace.numel() * workspace.element_size()

@@ -712,7 +712,9 @@ __device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   mu = __reduce_max_sync(0xffffffffu, mu);
   qu = __reduce_max_sync(0xffffffffu, qu);
-  const float err = static_cast<float>(p.head_dim) * 2.98023224e-8f * __uint_as_float(qu) * __uint_as_float(mu);  // E
+  float err = static_cast<float>(p.head_dim) * 2.98023224e-8f * __uint_as_float(qu) * __uint_as_float(mu);  // E
+  // Where E leaves the normal range so may the products, whose roundings E does not count: exact sums decide.
+  if (qu != 0u && mu != 0u && err < 1.17549435e-38f) err = INFINITY;
 
   // keys over `above` are taken, under `below` not; the ones between are ambiguous
   uint32_t above = kForced - 1u, below = kForced;

@@ -1,0 +1,128 @@
+"""Arguments the binding refuses before a kernel sees them (no GPU needed)."""
+
+import pytest
+import torch
+
+from quantized_kv_decode_partial_gb300 import binding as B
+
+NB, HK, BS, D = 6, 2, 32, 128
+E4M3 = dict(bits=8, group_size=B.PKV_GROUP_BLOCK)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def codes(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def scales(*shape):
+    return torch.ones(shape, dtype=torch.float32)
+
+
+def decode(**kw):
+    a = dict(q=bf16(3, 4, 1, D), k_pool=codes(NB, HK, BS, D), v_pool=codes(NB, HK, BS, D), block_tables=i32(3, 2),
+             seq_lens=i32(3), scale=0.1, k_scales=scales(NB, HK), v_scales=scales(NB, HK), **E4M3)
+    return {**a, **kw}
+
+
+def append(**kw):
+    a = dict(k_new=bf16(3, HK, 1, D), v_new=bf16(3, HK, 1, D), block_tables=i32(3, 2), seq_lens=i32(3),
+             k_pool=codes(NB, HK, BS, D), v_pool=codes(NB, HK, BS, D), k_scales=scales(NB, HK), v_scales=scales(NB, HK),
+             **E4M3)
+    return {**a, **kw}
+
+
+def sparse(**kw):
+    return decode(k_bounds=bf16(NB, HK, 2, D), top_k=2, **kw)
+
+
+def select(**kw):
+    a = dict(q=bf16(3, 4, 1, D), k_bounds=bf16(NB, HK, 2, D), block_tables=i32(3, 4), seq_lens=i32(3), block_size=BS,
+             top_k=2)
+    return {**a, **kw}
+
+
+def selected(**kw):
+    a = decode(selection=B.BlockSelection(i32(3, HK, 2), i32(3, HK, 2), i32(3, HK)))
+    del a["block_tables"], a["seq_lens"]
+    return {**a, **kw}
+
+
+def bounds(**kw):
+    a = dict(k_pool=bf16(NB, HK, BS, D), block_tables=i32(3, 2), seq_lens=i32(3), k_bounds=bf16(NB, HK, 2, D), n_new=1)
+    return {**a, **kw}
+
+
+@pytest.mark.parametrize("scale,error", [(torch.ones(NB, HK, dtype=torch.float16), TypeError),
+                                         (scales(NB, 1), ValueError), (scales(NB * HK), ValueError),
+                                         (scales(NB, 2 * HK)[:, ::2], ValueError)])
+@pytest.mark.parametrize("call,args", [(B.paged_decode_attention, decode), (B.paged_append, append),
+                                       (B.sparse_decode_attention, sparse), (B.selected_decode_attention, selected)])
+def test_scales_of_e4m3_pages(call, args, scale, error):
+    for name in ("k_scales", "v_scales"):
+        with pytest.raises(error, match="e4m3"):
+            call(**args(**{name: scale}))
+
+
+def test_pools_of_another_format():
+    # a pool whose rows hold fewer bytes than the format's would be read past its end
+    with pytest.raises(ValueError, match="k_pool"):
+        B.layout_for(codes(NB, HK, BS, D), D, 16)
+    with pytest.raises(ValueError, match="k_pool"):
+        B.layout_for(torch.zeros(NB, HK, BS, D // 8, dtype=torch.int32), D, 8)
+    assert B.layout_for(torch.zeros(NB, HK, BS, D // 8, dtype=torch.int32), D, 4).head_dim == D
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call,args,wrong,error", [
+    (B.sparse_decode_attention, sparse, dict(q=torch.zeros(3, 4, 1, D)), TypeError),
+    (B.sparse_decode_attention, sparse, dict(seq_lens=torch.zeros(3, dtype=torch.int64)), TypeError),
+    (B.sparse_decode_attention, sparse, dict(seq_lens=i32(2)), ValueError),
+    (B.sparse_decode_attention, sparse, dict(k_bounds=bf16(NB, HK, D, 2)), ValueError),
+    (B.sparse_decode_attention, sparse, dict(v_pool=codes(NB - 1, HK, BS, D)), ValueError),
+    (B.sparse_decode_attention, sparse, dict(blocks=i32(3, HK, 3)), ValueError),
+    (B.sparse_decode_attention, sparse, dict(out=bf16(3, 4, 1, D // 2)), ValueError),
+    (B.sparse_decode_attention, sparse, dict(out=torch.zeros(3, 4, 1, D)), TypeError),
+    (B.sparse_decode_attention, sparse, dict(q=bf16(3, D, 1, 4).transpose(1, 3)), ValueError),
+    (B.select_blocks, select, dict(k_bounds=torch.zeros(NB, HK, 2, D)), TypeError),
+    (B.select_blocks, select, dict(block_tables=i32(2, 4)), ValueError),
+    (B.select_blocks, select, dict(out=B.BlockSelection(i32(3, HK, 2), i32(3, HK, 1), i32(3, HK))), ValueError),
+    (B.selected_decode_attention, selected, dict(selection=B.BlockSelection(i32(3, HK, 2), i32(3, 1, 2), i32(3, HK))),
+     ValueError),
+    (B.selected_decode_attention, selected, dict(v_pool=codes(NB, HK, BS // 2, D)), ValueError),
+    (B.update_block_bounds, bounds, dict(k_bounds=torch.zeros(NB, HK, 2, D)), TypeError),
+    (B.update_block_bounds, bounds, dict(k_bounds=bf16(NB, HK, 2, 2 * D)), ValueError),
+    (B.update_block_bounds, bounds, dict(seq_lens=i32(4)), ValueError),
+])
+def test_types_and_shapes(call, args, wrong, error):
+    def on_gpu(x):
+        if isinstance(x, tuple):
+            return B.BlockSelection(*map(on_gpu, x))
+        return x.cuda() if isinstance(x, torch.Tensor) else x
+
+    right = {k: on_gpu(v) for k, v in args().items()}
+    for _ in range(2):  # the second time with the right call's shapes remembered
+        with pytest.raises(error):
+            call(**{**right, **{k: on_gpu(v) for k, v in wrong.items()}})
+        call(**right)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call,args,name", [(B.sparse_decode_attention, sparse, "seq_lens"),
+                                            (B.sparse_decode_attention, sparse, "k_bounds"),
+                                            (B.select_blocks, select, "block_tables"),
+                                            (B.selected_decode_attention, selected, "v_pool"),
+                                            (B.update_block_bounds, bounds, "seq_lens")])
+def test_tensors_on_the_host(call, args, name):
+    right = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in args().items()}
+    if "selection" in right:
+        right["selection"] = B.BlockSelection(*(t.cuda() for t in right["selection"]))
+    with pytest.raises(ValueError, match="one device"):
+        call(**{**right, name: right[name].cpu()})

@@ -427,3 +427,16 @@ def test_score_errors_are_far_within_the_bound_the_choice_uses(d, shape):
     e = d * 2.0 ** -25 * np.abs(qd).sum(-1).max() * np.abs(bd).max()
     worst = np.abs(got - ref).max() / e
     assert worst < 0.1, worst
+
+
+@pytest.mark.parametrize("width", [400, 1500])
+def test_products_near_the_smallest_normal_number(width):
+    # scores around 2^-118, where the error bound of an f32 score would leave the normal range
+    rng = np.random.default_rng(41)
+    n, bs, d = 400, 16, 128
+    bounds = bf16(random_bounds(rng, n, 2, d).double().numpy() * 2.0 ** -61)
+    q = bf16(rng.normal(size=(1, 8, 1, d)) * 2.0 ** -60)
+    bounds[100:110] = bounds[50]  # equal scores among them
+    tables = [[int(x) for x in rng.permutation(n)] + [-1] * (width - n)]
+    for top_k in (3, 40, 399):
+        check_choice(rng, bounds, q, tables, [n * bs - 3], bs, top_k, 1, 1)
