@@ -308,11 +308,15 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
   // faster SMs more CTAs (balanced: 8-bit layer 718.8 -> 748.1 us, bf16 8 x 128K rows
   // 609.6 -> 642.6 us). The chunk list must index in 32 bits: the longest unit reads at
   // most the table, or with a window W + N - 1 rows plus the alignment of its first chunk.
-  // e4m3 pages are bound by their arithmetic when query rows times head dims exceed 8 x 256
-  // (8 sequences of 20001 to 40003 rows, 8 KV heads, partitions -> balanced; D=128: 8 rows
-  // 88.4 -> 91.5 us, 16 rows 105.5 -> 96.3, 32 rows 200.4 -> 172.2; D=64: 16 rows 60.6 -> 64.2,
-  // 32 rows 130.3 -> 96.8; D=256: 8 rows 169.9 -> 164.6).
-  const bool bal_format = L->bits == 4 || (block_scaled(L) && nq * (L->head_dim + v_dim(L)) > 8 * 256);
+  // e4m3 pages are bound by their arithmetic when more than 8 query rows times head dims exceed
+  // 8 x 256 (8 sequences of 20001 to 40003 rows, 8 KV heads, partitions -> balanced; D=128: 8
+  // rows 80.8 -> 91.5 us, 16 rows 94.4 -> 94.8, 32 rows 176.7 -> 161.4; D=64: 16 rows 60.6 ->
+  // 63.4, 32 rows 131.1 -> 96.9; D=256: 8 rows 165.3 -> 176.8, 16 rows 252.6 -> 239.6; 64
+  // sequences of up to 32768 rows, D=128, 16 rows: 383.0 -> 355.3). Tables of up to 8192 rows
+  // hold too few chunks per run (160 sequences of up to 8192 rows, D=128, 16 rows: 261.4 ->
+  // 268.4; 64 of up to 2000: 44.2 -> 52.1; 100 of up to 16384: 305.0 -> 293.7).
+  const bool bal_format = L->bits == 4 || (block_scaled(L) && nq > 8 && nq * (L->head_dim + v_dim(L)) > 8 * 256 &&
+                                           P->max_blocks_per_seq * static_cast<long long>(L->block_size) > 8192);
   out->balanced = 0;
   if (P->partition_tokens == 0 && P->schedule != PKV_SCHEDULE_PARTITIONS && !cc && !pieces &&
       P->num_seqs <= pkv::kMaxBalancedSeqs &&

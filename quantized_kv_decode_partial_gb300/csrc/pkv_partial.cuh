@@ -100,15 +100,16 @@ struct PartialCfg {
   static constexpr int kPlaneBytesV = kBoxesV * kBoxBytesV;
   static constexpr int kSbBytes = kQuant ? kCh * kGroups * 2 : 0;     // one K scale or bias plane
   static constexpr int kSbBytesV = kQuant ? kCh * kGroupsV * 2 : 0;   // one V scale or bias plane
-  // stage layout: K rows, V rows, K scales, K biases, V scales, V biases (affine); e4m3
-  // pages: K rows, V rows, then the f32 scales of the chunk's up to four blocks, K and V
+  // stage layout: K rows, V rows, K scales, K biases, V scales, V biases (affine). The f32
+  // scales of an e4m3 chunk's up to four blocks, K then V, lie in an area of their own: 32
+  // bytes more per stage would cost it another KB, since boxes start on KB boundaries.
   static constexpr int kOffV = kPlaneBytes;
   static constexpr int kOffKs = kPlaneBytes + kPlaneBytesV;
   static constexpr int kOffKb = kOffKs + kSbBytes;
   static constexpr int kOffVs = kOffKb + kSbBytes;
   static constexpr int kOffVb = kOffVs + kSbBytesV;
-  static constexpr int kOffVScale = kOffKs + 16;  // e4m3: V scales (K scales at kOffKs)
-  static constexpr int kTxBytes = kOffVb + kSbBytesV + (kBlk ? 32 : 0);
+  static constexpr int kTxBytes = kOffVb + kSbBytesV;
+  static constexpr int kSlotBytes = kBlk ? 32 : 0;  // of a stage's block scales
   static constexpr int kTmaBytes = kPlaneBytes + kPlaneBytesV;  // the part the TMA copies bring
   static constexpr int kSbCopies = (2 * kSbBytes + 2 * kSbBytesV) / 16;  // 16-byte copies of scales and biases
   static constexpr int kStageBytes = (kTxBytes + 1023) / 1024 * 1024;
@@ -125,7 +126,7 @@ struct PartialCfg {
   static constexpr int kBalBytes = BAL ? (2 * kMaxBalancedSeqs + 4) * 4 : 0;
   // stage ring of a CTA alone on its SM, with the receive area of the push-form cluster
   // merge (kSoloBudget) or without it (kSoloBase)
-  static constexpr int kSoloBase = 227 * 1024 - kBarrierBytes - 1024 - kPBufBytes - kBalBytes;
+  static constexpr int kSoloBase = 227 * 1024 - kBarrierBytes - 1024 - kPBufBytes - kBalBytes - 32 * kSlotBytes;
   static constexpr int kSoloBudget = kSoloBase - (SOLO ? kRecvNeedBytes : 0);
   // A CTA of a grid of several per SM whose four warps' two stages each already take more
   // than half the SM's shared memory (16 KB stages: bf16 D=256) has its SM to itself anyway.
@@ -163,11 +164,24 @@ struct PartialCfg {
   static constexpr int kWP = kWarps / WQ;
   static constexpr int kSoloStages = (kSeven ? kSoloBase : kSixLone ? kSoloBase - kRecvNeedBytes : kSoloBudget) /
                                      (kWarps * kStageBytes);
-  // e4m3 pages with 64- or 128-dim values and up to 8 query rows: two stages per warp instead
-  // of three let a third CTA on the SM, a fourth for 64-dim heads (as many bytes in flight,
-  // more warps). 8 sequences of 20001 to 40003 rows, D=128, 4 query rows: 87.4 -> 79.1 us, in
-  // blocks of 16 rows 103.5 -> 85.9; 32 sequences of 512 to 16384 rows, D=64: 69.4 -> 54.4.
-  static constexpr bool kThird = kBlk && !SOLO && !BAL && DV <= 128 && NT == 1 && WQ == 1;
+  // Row stride (floats) of the per-page-group outputs in the combine area: padded by 4 so
+  // rows stay 16-byte aligned for vector access and a warp's stores spread over the banks.
+  static constexpr int kCoStride = DV + 4;
+  // per-page-group states (m, l, o) for the in-CTA combine, then the CTA's own state for a cluster merge
+  static constexpr int kGroupStateFloats = kNqAll * (kCoStride + 2);
+  static constexpr int kCtaStateFloats = kNqAll * (DV + 2);
+  static constexpr int kCombineBytes = (kWP * kGroupStateFloats + kCtaStateFloats) * 4;
+  // e4m3 pages: two stages per warp instead of three, and at most 168 registers per thread,
+  // let a third CTA on the SM, a fourth for 64-dim heads with up to 8 query rows (as many
+  // bytes in flight, more warps for chains of dependent instructions). 8 sequences of 20001
+  // to 40003 rows, D=128, 4 query rows: 87.4 -> 79.1 us, in blocks of 16 rows 103.5 -> 85.9, with
+  // 16 query rows 126.1 -> 111.4; D=256, 16 query rows, 267 -> 239; 32 sequences of 512 to 16384
+  // rows, D=64: 69.4 -> 54.4. Four tiles of query rows per warp (64-dim heads with more than
+  // 16) need more registers than that.
+  static constexpr bool kThird = kBlk && !SOLO && kWarps == 4 && NT <= 2 &&
+                                 3 * ((8 * kStageBytes > kCombineBytes ? 8 * kStageBytes : kCombineBytes) + kBarrierBytes +
+                                      kBalBytes + 8 * kSlotBytes + 2048) <= 228 * 1024;
+  static constexpr int kRegs = kThird ? 168 : 255;  // 3 x 128 threads share an SM's 65536
   // (a query group of 8 warps shares one ring of 8 or 16 stages, within 144 KB)
   static constexpr int kStagesPerWarp = WQ == 8 ? (8 * 2 * kStageBytes <= 144 * 1024 ? 2 : 1)
                                         : kEightLone ? 1
@@ -178,13 +192,6 @@ struct PartialCfg {
   static constexpr int kMt = DV / 16;       // 16-dim m-tiles of O^T
   static constexpr int kKs = D / 16;        // k16 steps of Q K^T
   static constexpr int kTiles = kCh / 16;   // 16-key tiles per stage
-  // Row stride (floats) of the per-page-group outputs in the combine area: padded by 4 so
-  // rows stay 16-byte aligned for vector access and a warp's stores spread over the banks.
-  static constexpr int kCoStride = DV + 4;
-  // per-page-group states (m, l, o) for the in-CTA combine, then the CTA's own state for a cluster merge
-  static constexpr int kGroupStateFloats = kNqAll * (kCoStride + 2);
-  static constexpr int kCtaStateFloats = kNqAll * (DV + 2);
-  static constexpr int kCombineBytes = (kWP * kGroupStateFloats + kCtaStateFloats) * 4;
   static constexpr int kRingBytes = kWarps * kStagesPerWarp * kStageBytes;
   static constexpr int kGroupBytes = kStagesPerGroup * kStageBytes;  // one page group's ring
   // When a page group's state (and the CTA's, after the last group's) fits its own ring,
@@ -193,12 +200,13 @@ struct PartialCfg {
   static constexpr int kWorkBytes = kRingBytes > kCombineBytes ? kRingBytes : kCombineBytes;
   // The receive area (after the ring) is there when the CTA is alone on its SM, or when it
   // does not cost the second CTA per SM (or the CTA already has its SM to itself).
-  static constexpr int kBaseSmem = kWorkBytes + kBarrierBytes + 1024;
+  static constexpr int kScaleBytes = kWarps * kStagesPerWarp * kSlotBytes;
+  static constexpr int kBaseSmem = kWorkBytes + kBarrierBytes + kScaleBytes + 1024;
   static constexpr bool kPush = !BAL && !kSeven && !kThird && (SOLO || kBaseSmem + kRecvNeedBytes <= 114 * 1024 ||
                                          (kBaseSmem > 114 * 1024 && kBaseSmem + kRecvNeedBytes <= 227 * 1024));
   static constexpr int kRecvBytes = kPush ? kRecvNeedBytes : 0;
   static constexpr int kDataBytes = kWorkBytes + kRecvBytes;
-  static constexpr int kSmemBytes = kDataBytes + kBarrierBytes + kPBufBytes + kBalBytes + 1024;  // + alignment slack
+  static constexpr int kSmemBytes = kDataBytes + kBarrierBytes + kPBufBytes + kBalBytes + kScaleBytes + 1024;  // + alignment slack
   static constexpr float kCodeUnit = 5.9604644775390625e-8f;  // 2^-24: value of fp16 bit pattern 1
 
   static_assert((kRB == 128 || kRB == 64) && (kRBV == 128 || kRBV == 64), "box rows of 64 or 128 bytes");
@@ -363,7 +371,7 @@ __device__ __forceinline__ void load_group_row(uint32_t addr, float (&v)[G]) {
 // 4-7 by the odd group's; each group's MMAs keep the columns of their own group.
 template <int BITS, int D, int DV, int NT, int WQ, bool SOLO, bool HOSTIN, int CCQ = 0, bool PV = false,
           bool BAL = false, bool PC = false>
-__global__ void __maxnreg__(255)
+__global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kRegs))
     pkv_partial_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v) {
   using C = PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>;
@@ -521,6 +529,8 @@ __global__ void __maxnreg__(255)
     uint64_t* my_full = full_bar + pg * C::kStagesPerGroup;
     int* my_ok = stage_ok + pg * C::kStagesPerGroup;
     uint8_t* my_ring = smem + pg * C::kStagesPerGroup * C::kStageBytes;
+    const uint32_t my_slots = smem_addr(smem + C::kDataBytes + C::kBarrierBytes + C::kPBufBytes + C::kBalBytes) +
+                              pg * C::kStagesPerGroup * C::kSlotBytes;  // e4m3: the stages' block scales
     const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
     const uint64_t policy = l2_evict_first_policy();
     auto chunk_row = [&](int i) { return t_first + (pg + i * C::kWP) * C::kCh; };  // first cache row of local chunk i
@@ -694,7 +704,7 @@ __global__ void __maxnreg__(255)
           const int j = lane & 3;
           const int prow = j == 0 ? pr[0] : j == 1 ? pr[1] : j == 2 ? pr[2] : pr[3];
           if (lane < 8 && j < nb) {
-            const uint32_t dst = st + (lane < 4 ? C::kOffKs : C::kOffVScale) + 4 * j;
+            const uint32_t dst = my_slots + is * C::kSlotBytes + (lane < 4 ? 0 : 16) + 4 * j;
             if (prow >= 0) {
               cp_async_4(dst, bs_src + static_cast<unsigned>(prow) / static_cast<unsigned>(p.block_size));
             } else {
@@ -959,7 +969,7 @@ __global__ void __maxnreg__(255)
     auto score_chunk = [&](uint32_t kpl, uint32_t sbq, int kbase, bool full_vis, float (&pr)[C::kTiles][NT][4],
                            float (&corr)[NT][2]) -> bool {
       float kscale[4];
-      if constexpr (C::kBlk) load_scales(kpl + C::kOffKs, kscale);
+      if constexpr (C::kBlk) load_scales(sbq, kscale);
       auto key_scales = [&](int tile, float& a, float& b) { pick_scales(kscale, tile, a, b); };
       // ---- scores x = (K q) * scale * log2(e), keys on rows
       float x[C::kTiles][NT][4];
@@ -1196,15 +1206,18 @@ __global__ void __maxnreg__(255)
             for (int e2 = 0; e2 < 2; ++e2) corr_v[grp][nt][e2] *= corr[nt][e2];
       }
     };
-    auto value_chunk = [&](uint32_t kpl, uint32_t vpl, int kbase, bool stale, const float (&pr)[C::kTiles][NT][4]) {
+    auto value_chunk = [&](uint32_t kpl, uint32_t vpl, uint32_t sbq, int kbase, bool stale, const float (&pr)[C::kTiles][NT][4]) {
       // ---- O^T += V^T P^T
       if constexpr (C::kBlk) {
         // Weights of the whole chunk as B fragments; with several blocks in the chunk, each
         // key's weight times its block's scale over the chunk's largest (at most 1). The
-        // chunk's product then takes that largest scale on its way into O^T.
+        // chunk's product then takes that largest scale on its way into O^T. A weight below
+        // fp16's normal range is off by at most 2^-25, so a key by 2^-25 of what the chunk's
+        // largest scale can hold: more than 2^-11 of its own value only where that scale is
+        // far above both the key's scale and the values stored under it.
         uint32_t pb2[C::kTiles][NT][2];
         float vs[4];
-        load_scales(kpl + C::kOffVScale, vs);
+        load_scales(sbq + 16, vs);
         float vmax = vs[0];
         if constexpr (PC) {
           vmax = fmaxf(vmax, vs[1]);
@@ -1400,7 +1413,8 @@ __global__ void __maxnreg__(255)
         uint8_t* stage = my_ring + cs * C::kStageBytes;
         const uint32_t kpl = smem_addr(stage);
         const uint32_t vpl = kpl + C::kOffV;
-        const uint32_t sbq = kpl + C::kOffKs;  // scale/bias planes (affine pages)
+        // scale/bias planes (affine pages), block scales (e4m3)
+        const uint32_t sbq = C::kBlk ? my_slots + cs * C::kSlotBytes : kpl + C::kOffKs;
         const int kbase = BAL ? seg_row + (done - seg_start) * C::kCh : chunk_row(done);
         const bool full_vis = kbase + C::kCh <= vis_base && (win == 0 || kbase >= vis_base + N - 1 - win);
         const bool stale = kbase + C::kCh > len;
@@ -1412,7 +1426,7 @@ __global__ void __maxnreg__(255)
         float pr[C::kTiles][NT][4];
         float corr[NT][2];
         if (score_chunk(kpl, sbq, kbase, full_vis, pr, corr)) rescale(corr);
-        value_chunk(kpl, vpl, kbase, stale, pr);
+        value_chunk(kpl, vpl, sbq, kbase, stale, pr);
         }  // tensor-core contraction
       }
       if constexpr (WQ == 1) {
