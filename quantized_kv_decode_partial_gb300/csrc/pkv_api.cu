@@ -1028,10 +1028,13 @@ int check_sparse(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv
 //    bf16 rows: 27.8 us; 2: 29.0, 8: 28.0), 2 (64 units: 38.7 us; 4: 39.7, 8: 41.5), else 1.
 //    More than 4 only while they are at most 96 CTAs: clusters of 8 that hold whole SMs do not
 //    all fit the GPCs at once (16 units of 4096 rows: 6 per unit 23.1 us, 8 per unit 26.9).
-//  * Others: up to 8, 256 CTAs at most (64 units of 4096 e4m3 rows, 16 query rows: 4 per unit
-//    37.2 us; 2: 44.1, 8: 41.2).
-//  * Up to two CTAs per SM: 1, or 3 through the workspace for long units and few query rows
-//    (256 units of 4096 4-bit rows: 79.3 -> 67.8 us).
+//  * Others: up to 8, 256 CTAs at most (64 units of 4096 e4m3 rows, 16 query rows, the
+//    attention alone: 4 per unit 20.8 us; 2: 28.8, 8: 25.2).
+//  * Up to two units per SM: 1, or 3 through the workspace for long units and few query rows
+//    (256 units of 4096 4-bit rows: 79.3 -> 67.8 us). e4m3 pages, which have three CTAs on an SM:
+//    as many as fill them (attention alone, 16 query rows: 128 units of 4096 rows, 3 per unit
+//    32.1 us, 2: 34.8; 192 units, 2 per unit 43.3, 1: 58.5), or 3 where that is 1 and the units
+//    are long (256 units of 4096 rows: 65.5 -> 58.4; of 2048: 35.9 -> 36.6).
 //  * More units: the library's choice, but for e4m3 up to four waves 4 (512 units of 2048
 //    rows: 58.4 -> 50.9 us).
 //  * Behind scores of many blocks, the library's choice: its CTAs share their SMs with the
@@ -1051,8 +1054,10 @@ int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int
     parts = std::min(8ll, 96 / units);
     if (parts < 4) parts = 4 * units <= sms ? 4 : 2 * units <= sms ? 2 : 1;
   } else if (units <= 2 * sms) {
-    parts = std::min(8ll, std::max(1ll, 256 / units));
-    if (parts == 1 && rows >= 4096 && nq <= 8) parts = 3;
+    const bool three = block_scaled(vl) && units > 64;  // CTAs per SM to fill
+    parts = std::min(8ll, std::max(1ll, (three ? 3 * sms : 256) / units));
+    const bool long_units = rows >= 4096 || (three && rows * vl->head_dim >= (512ll << 10));
+    if (parts == 1 && long_units && (three || nq <= 8)) parts = 3;
   } else if (block_scaled(vl) && units <= 4 * 3 * sms && rows * vl->head_dim >= (256ll << 10)) {
     parts = 4;
   }
