@@ -54,7 +54,11 @@
 //    value; one conversion per pair). The key scale of a block multiplies its scores;
 //    the value scale cannot ride on the fp16 weights (its range is f32's), so each
 //    chunk's V^T P^T goes to fresh accumulators and enters O^T by one f32 FMA with the
-//    chunk's scale, 4 FMAs per 4 MMAs of a 32-row chunk. The kernel stays bound by HBM.
+//    chunk's scale, 4 FMAs per 4 MMAs of a 32-row chunk. Up to 8 query rows the kernel is
+//    bound by HBM (64 sequences of 1024 to 32768 rows, D=128: 330 us, 1.03 of a copy's rate);
+//    above, by dependent instructions: 8 sequences of 20001 to 40003 rows, 16 query rows,
+//    94 us (0.80; in blocks of 16 rows 108). Scores by e4m3 MMAs on unconverted keys against q
+//    in two e4m3 parts were slower throughout (330 -> 373 us, 111 -> 166 us).
 //  * Rows at or past seq_len in the last page are masked before they can reach
 //    an accumulator (scores set to -inf by select; their V operand or V scale
 //    zeroed), so stale storage may hold anything, NaN included.
@@ -207,6 +211,11 @@ struct PartialCfg {
   static constexpr int kRecvBytes = kPush ? kRecvNeedBytes : 0;
   static constexpr int kDataBytes = kWorkBytes + kRecvBytes;
   static constexpr int kSmemBytes = kDataBytes + kBarrierBytes + kPBufBytes + kBalBytes + kScaleBytes + 1024;  // + alignment slack
+  // How far (base 2) scores may exceed the running maximum before it follows: weights of up to
+  // 2^kSlack cost f32 sums and fp16 weights no precision, and with 16 query rows nearly every
+  // chunk of a short run would raise some row's maximum and rescale every output (8 sequences
+  // of 20001 to 40003 rows in blocks of 16, D=128, 16 query rows: 111.7 -> 108.2 us).
+  static constexpr float kSlack = 6.f;  // e4m3 pages alone
   static constexpr float kCodeUnit = 5.9604644775390625e-8f;  // 2^-24: value of fp16 bit pattern 1
 
   static_assert((kRB == 128 || kRB == 64) && (kRBV == 128 || kRBV == 64), "box rows of 64 or 128 bytes");
@@ -1143,7 +1152,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
 #pragma unroll
           for (int tile = 0; tile < C::kTiles; ++tile) mx = fmaxf(mx, fmaxf(x[tile][nt][e2], x[tile][nt][e2 + 2]));
           lmx[nt][e2] = mx;
-          below &= mx <= m_run[nt][e2];
+          below &= mx <= (C::kBlk ? m_run[nt][e2] + C::kSlack : m_run[nt][e2]);
         }
       if (__all_sync(0xffffffffu, below)) {
 #pragma unroll
@@ -1169,7 +1178,8 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mnew = fmaxf(m_run[nt][e2], mx);
+            const float mnew =
+                C::kBlk ? (mx > m_run[nt][e2] + C::kSlack ? mx : m_run[nt][e2]) : fmaxf(m_run[nt][e2], mx);
             const float muse = mnew == -INFINITY ? 0.f : mnew;
             const float c = fast_exp2(m_run[nt][e2] - muse);
             m_run[nt][e2] = mnew;

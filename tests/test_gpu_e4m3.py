@@ -114,6 +114,20 @@ def test_scales_far_apart(bs):
     run_attend(np.random.default_rng(bs), [200, 129], 4, 2, 128, 128, 1, bs, spread=40)
 
 
+@pytest.mark.parametrize("rep,d,bs,schedule", [(1, 128, 32, 1), (16, 128, 32, 1), (16, 128, 32, 2), (4, 256, 16, 1),
+                                               (12, 64, 8, 1)])
+@pytest.mark.parametrize("rising", [True, False])
+def test_scores_rising_and_falling_along_the_cache(rep, d, bs, schedule, rising):
+    # the running maximum follows a row's scores in steps, whatever their order
+    def edit(kc, ks, vc, vs, tables):
+        for t in tables:
+            held = [b for b in t if b >= 0]
+            for i, b in enumerate(held if rising else held[::-1]):
+                ks[b] *= 0.02 * 500.0 ** (i / len(held))
+
+    run_attend(np.random.default_rng(rep + d), [2500, 700], 2 * rep, 2, d, d, 1, bs, schedule=schedule, edit=edit)
+
+
 @pytest.mark.parametrize("bs", [8, 32])
 def test_zero_scales(bs):
     def edit(kc, ks, vc, vs, tables):
