@@ -58,7 +58,7 @@
 //    bound by HBM (64 sequences of 1024 to 32768 rows, D=128: 330 us, 1.03 of a copy's rate);
 //    above, by dependent instructions: 8 sequences of 20001 to 40003 rows, 16 query rows,
 //    94 us (0.80; in blocks of 16 rows 108). Scores by e4m3 MMAs on unconverted keys against q
-//    in two e4m3 parts were slower throughout (330 -> 373 us, 111 -> 166 us).
+//    in two e4m3 parts were slower throughout (330 -> 373 us, 126 -> 166 us).
 //  * Rows at or past seq_len in the last page are masked before they can reach
 //    an accumulator (scores set to -inf by select; their V operand or V scale
 //    zeroed), so stale storage may hold anything, NaN included.
