@@ -8,6 +8,7 @@ it, the output's rounding 2^-8 of the value. Bound: 2^-8 |ref| + 2^-8 max|V| + 2
 """
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -440,3 +441,65 @@ def test_products_near_the_smallest_normal_number(width):
     tables = [[int(x) for x in rng.permutation(n)] + [-1] * (width - n)]
     for top_k in (3, 40, 399):
         check_choice(rng, bounds, q, tables, [n * bs - 3], bs, top_k, 1, 1)
+
+
+@pytest.mark.parametrize("fmt", [16, "e4m3"])
+def test_nearly_as_many_units_as_a_call_takes(fmt):
+    # 8191 sequences of 8 KV heads; all blocks chosen is the dense decode, two are the ends
+    g = torch.Generator(device=DEV).manual_seed(5)
+    seqs, hk, hq, d, bs = 8191, 8, 8, 64, 32
+    lens = torch.randint(1, 3 * bs + 1, (seqs,), generator=g, device=DEV, dtype=torch.int32)
+    tables = torch.randperm(3 * seqs, generator=g, device=DEV, dtype=torch.int32).view(seqs, 3)
+    rows = torch.randn((2, 3 * seqs, hk, bs, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    q = torch.randn((seqs, hq, 1, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    kw, sc = {}, {}
+    if fmt == "e4m3":
+        rows = rows.to(torch.float8_e4m3fn)
+        kw = dict(bits=8, group_size=B.PKV_GROUP_BLOCK)
+        sc = dict(k_scales=torch.ones((3 * seqs, hk), device=DEV), v_scales=torch.ones((3 * seqs, hk), device=DEV))
+    k, v = rows[0], rows[1]
+    bounds = torch.empty((3 * seqs, hk, 2, d), dtype=torch.bfloat16, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    B.update_block_bounds(k, tables, lens, bounds, n_new=3 * bs, k_scales=sc.get("k_scales"), error_flag=err, **kw)
+    blocks = torch.empty((seqs, hk, 2), dtype=torch.int32, device=DEV)
+    dense = B.paged_decode_attention(q, k, v, tables, lens, 0.125, error_flag=err, **sc, **kw)
+    every = B.sparse_decode_attention(q, k, v, bounds, tables, lens, 0.125, top_k=3, error_flag=err, **sc, **kw)
+    ends = B.sparse_decode_attention(q, k, v, bounds, tables, lens, 0.125, top_k=2, blocks=blocks, error_flag=err, **sc, **kw)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    # the same sums in another order, then a rounding to bf16 on each side
+    vmax = float(v.float().abs().max())
+    assert ((every.float() - dense.float()).abs() <= 2.0 ** -7 * dense.float().abs() + 2.0 ** -7 * vmax).all()
+    n = (lens + bs - 1) // bs
+    last = torch.where(n > 1, n - 1, -1)
+    assert (blocks[:, :, 0] == 0).all() and (blocks[:, :, 1] == last[:, None]).all()
+    assert ((ends.float() - every.float())[n <= 2].abs() <= 2.0 ** -7 * every.float()[n <= 2].abs() + 2.0 ** -7 * vmax).all()
+
+
+def test_two_threads_on_the_default_stream_and_on_one_side_stream():
+    # each thread holds its own workspace of the default stream; other streams' are each call's own
+    rng = np.random.default_rng(43)
+    cases = [run_sparse(rng, fmt, lens, 8, 2, 128, 128, 1, 16, 12, 1, 1)
+             for fmt, lens in ((16, [9000, 1600]), ("e4m3", [700, 5000, 64]))]
+    lengths = ([9000, 1600], [700, 5000, 64])
+    side = torch.cuda.Stream()
+    wrong, gate = [], threading.Barrier(2)
+
+    def work(case, lens):
+        q, k, v, bounds, tables, want, _ = case
+        qd, dt, dl = q.to(DEV), i32(tables), i32(lens)
+        torch.cuda.synchronize()
+        for stream in (torch.cuda.default_stream(), side):
+            with torch.cuda.stream(stream):
+                gate.wait()
+                got = [B.sparse_decode_attention(qd, k.pool, v.pool, bounds, dt, dl, 1 / math.sqrt(128), top_k=12,
+                                                 k_scales=k.scales, v_scales=v.scales, **k.kw) for _ in range(40)]
+                stream.synchronize()
+                wrong.extend(1 for o in got if not torch.equal(o, want))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, lengths)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
