@@ -381,6 +381,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Two 16x16 matrices of bytes (lanes 0-15 and 16-31 give their rows' addresses, 16 bytes
+// each), transposed: v[0] and v[2] hold columns g of the first and the second, v[1] and v[3]
+// columns g + 8, each rows 4t .. 4t + 3.
+__device__ __forceinline__ void ldsm_bytes_x2_t(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // Transpose an 8x8 matrix of 16-bit elements held one row-pair per thread.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;

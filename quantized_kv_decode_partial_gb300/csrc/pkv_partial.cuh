@@ -51,13 +51,14 @@
 //    element; the bias terms of the scores run as one extra bf16 MMA per tile.
 //  * e4m3 pages (one f32 scale per block and KV head) take the 8-bit byte layout. Both
 //    products run as fp16 MMAs on the codes' own values (every e4m3 value is an fp16
-//    value; one conversion per pair). The key scale of a block multiplies its scores;
+//    value; one conversion per pair, V's bytes transposed by the loads from shared memory).
+//    The key scale of a block multiplies its scores;
 //    the value scale cannot ride on the fp16 weights (its range is f32's), so each
 //    chunk's V^T P^T goes to fresh accumulators and enters O^T by one f32 FMA with the
 //    chunk's scale, 4 FMAs per 4 MMAs of a 32-row chunk. Up to 8 query rows the kernel is
 //    bound by HBM (64 sequences of 1024 to 32768 rows, D=128: 330 us, 1.03 of a copy's rate);
 //    above, by dependent instructions: 8 sequences of 20001 to 40003 rows, 16 query rows,
-//    94 us (0.80; in blocks of 16 rows 108). Scores by e4m3 MMAs on unconverted keys against q
+//    95 us (0.79; in blocks of 16 rows 104). Scores by e4m3 MMAs on unconverted keys against q
 //    in two e4m3 parts were slower throughout (330 -> 373 us, 126 -> 166 us).
 //  * Rows at or past seq_len in the last page are masked before they can reach
 //    an accumulator (scores set to -inf by select; their V operand or V scale
@@ -238,7 +239,7 @@ struct PartialCfg {
 // Physical head dim held by row `half` (0: g, 1: g + 8) of O^T m-tile `mt`.
 template <int BITS>
 __device__ __forceinline__ int out_dim(int mt, int half, int g) {
-  if constexpr (BITS == 16) {
+  if constexpr (BITS == 16 || BITS == kFmtE4m3) {
     return 16 * mt + 8 * half + g;
   } else if constexpr (BITS == 4) {
     return 64 * (mt >> 2) + 32 * half + 4 * g + (mt & 3);
@@ -944,6 +945,18 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
     // ldmatrix row/chunk of this lane: non-transposed (keys on M) and transposed (keys on K).
     const int lrow_n = (lane & 7) + ((lane >> 3) & 1) * 8, lch_n = lane >> 4;
     const int lrow_t = (lane & 7) + (lane >> 4) * 8, lch_t = (lane >> 3) & 1;
+    // e4m3 pages: a lane gets bytes of four consecutive rows of a transposed tile, the keys of
+    // its two B registers. So rows c = 4t + j of V's tile are keys 2t + (j & 1) for j < 2 and 8 +
+    // ((2t) ^ 4) + (j & 1) else, and rows 8 + r of K's are keys 8 + (r ^ 4): with the flip, any 8
+    // rows that a matrix load takes at once differ in the low 3 bits, and meet in no bank. Against
+    // transposed 16-bit loads and a permutation per register, with the offsets below: 8 sequences
+    // of 20001 to 40003 rows, 16 query rows, D=128 in blocks of 16 rows 108.2 -> 104.0 us, D=256
+    // 234.9 -> 215.6; 4 rows, D=256, 160.6 -> 157.4.
+    const int lrow_k = lrow_n ^ ((lrow_n & 8) >> 1);
+    const int lrow_v = (lane & 1) + ((lane >> 1) & 2) + 4 * (((lane >> 1) ^ (lane >> 3)) & 1) + 4 * (lane & 2);
+    // Their offsets in the first tile, at the lane's 16-byte chunk 0 or 1. Boxes start on KB
+    // boundaries, so chunk 2 j on is an XOR away, and a tile or box further an addition.
+    const uint32_t ofs_k = swizzled<C::kRB>(0u, lrow_k, lch_n), ofs_v = swizzled<C::kRBV>(0u, lrow_v, lane >> 4);
     // 4-bit pages: this lane's ldmatrix offsets within the K and V planes of a stage, per
     // 64-dim group, for the first 16-key tile (tile t adds 16 rows: the swizzle pattern
     // repeats every 8 rows), fixed for the whole loop.
@@ -1026,11 +1039,11 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
 #pragma unroll
           for (int i = 0; i < C::kKs / 2; ++i) {  // 32 bytes of each row: two k-steps
             uint32_t xk[4];
-            ldsm_x4(swizzled<C::kRB>(kpl + (32 * i / C::kRB) * C::kBoxBytes, lrow, (2 * i) % (C::kRB / 16) + lch_n), xk);
+            ldsm_x4(((kpl + ofs_k) ^ ((2 * i) % (C::kRB / 16) * 16)) + (32 * i / C::kRB) * C::kBoxBytes + tile * 16 * C::kRB, xk);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
               const int kk = 2 * i + cc;
-              uint32_t a0, a1, a2, a3;  // dims 4t..4t+3 of rows g and g + 8
+              uint32_t a0, a1, a2, a3;  // dims 4t..4t+3 of rows g and g + 8 (key 8 + (g ^ 4))
               e4m3x4_to_f16x2(xk[2 * cc], a0, a2);
               e4m3x4_to_f16x2(xk[2 * cc + 1], a1, a3);
 #pragma unroll
@@ -1129,7 +1142,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = kbase + tile * 16 + g + 8 * (e >> 1);
+              const int key = kbase + tile * 16 + (C::kBlk && (e >> 1) ? 8 + (g ^ 4) : g + 8 * (e >> 1));
               const int qi = (PV ? (2 * t + (e & 1)) & 3 : rbase + 8 * nt + 2 * t + (e & 1)) % N;
               const bool vis = key < vis_base + qi && (win == 0 || key >= vis_base + qi - win);
               x[tile][nt][e] = vis ? x[tile][nt][e] : -INFINITY;
@@ -1259,27 +1272,27 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
               for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
 #pragma unroll
           for (int tile = 0; tile < C::kTiles; ++tile) {
+            // y: dim g of m-tile 2 i, dim g + 8, and the same of m-tile 2 i + 1, each of four keys in
+            // the order of the rows' addresses (lrow_v)
             uint32_t y[4];
-            ldsm_x4_t(swizzled<C::kRBV>(vpl + (32 * i / C::kRBV) * C::kBoxBytesV, tile * 16 + lrow_t,
-                                        (2 * i) % (C::kRBV / 16) + lch_t),
-                      y);
+            ldsm_bytes_x2_t(((vpl + ofs_v) ^ ((2 * i) % (C::kRBV / 16) * 16)) + (32 * i / C::kRBV) * C::kBoxBytesV +
+                                tile * 16 * C::kRBV,
+                            y);
             if (stale) {  // codes at or past len may be NaN
-              const int k0 = kbase + tile * 16 + 2 * t;
-              const uint32_t m01 = (k0 < len ? 0x0000ffffu : 0u) | (k0 + 1 < len ? 0xffff0000u : 0u);
-              const uint32_t m23 = (k0 + 8 < len ? 0x0000ffffu : 0u) | (k0 + 9 < len ? 0xffff0000u : 0u);
-              y[0] &= m01;
-              y[1] &= m01;
-              y[2] &= m23;
-              y[3] &= m23;
+              const int k0 = kbase + tile * 16 + 2 * t, k2 = kbase + tile * 16 + 8 + ((2 * t) ^ 4);
+              const uint32_t m = (k0 < len ? 0x000000ffu : 0u) | (k0 + 1 < len ? 0x0000ff00u : 0u) |
+                                 (k2 < len ? 0x00ff0000u : 0u) | (k2 + 1 < len ? 0xff000000u : 0u);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[r] &= m;
             }
-            // y: dims 2g, 2g + 1 of key 2t (low half) and of key 2t + 1; a pair of keys per register
-            uint32_t a[4], b[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) e4m3x4_to_f16x2(__byte_perm(y[r], 0u, 0x3120), a[r], b[r]);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t a[4];
+              e4m3x4_to_f16x2(y[2 * j], a[0], a[2]);
+              e4m3x4_to_f16x2(y[2 * j + 1], a[1], a[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[0][nt], a[0], a[1], a[2], a[3], pb2[tile][nt][0], pb2[tile][nt][1]);
-              mma_f16(acc[1][nt], b[0], b[1], b[2], b[3], pb2[tile][nt][0], pb2[tile][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(acc[j][nt], a[0], a[1], a[2], a[3], pb2[tile][nt][0], pb2[tile][nt][1]);
             }
           }
 #pragma unroll
@@ -1541,9 +1554,9 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
         }
         break;
       }
-      // o: four (4-bit pages) or two (8-bit, e4m3) consecutive head dims per store where the
+      // o: four (4-bit pages) or two (8-bit) consecutive head dims per store where the
       // accumulator layout puts them in one thread, as in the combine below
-      constexpr int kRun = BITS == 4 ? 4 : BITS == 16 ? 1 : 2;
+      constexpr int kRun = BITS == 4 ? 4 : BITS == 8 ? 2 : 1;
 #pragma unroll
       for (int mt = 0; mt < C::kMt; mt += kRun)
 #pragma unroll
@@ -1616,10 +1629,10 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
           cl[rbase + r] = l_run[nt][e2];
         }
     }
-    // o values, four (4-bit pages) or two (8-bit, e4m3) consecutive head dims per store where
+    // o values, four (4-bit pages) or two (8-bit) consecutive head dims per store where
     // the accumulator layout puts them in one thread; padding rows of the last n-tile
     // are never read
-    constexpr int kRun = BITS == 4 ? 4 : BITS == 16 ? 1 : 2;
+    constexpr int kRun = BITS == 4 ? 4 : BITS == 8 ? 2 : 1;
 #pragma unroll
     for (int mt = 0; mt < C::kMt; mt += kRun)
 #pragma unroll
