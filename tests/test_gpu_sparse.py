@@ -503,3 +503,62 @@ def test_two_threads_on_the_default_stream_and_on_one_side_stream():
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_scores_read_again_from_memory_and_marks_in_two_segments():
+    # more blocks than the choice keeps scores of in shared memory (24576) and marks at once (32768)
+    rng = np.random.default_rng(47)
+    n, d, bs = 33001, 64, 16
+    bounds = random_bounds(rng, n, 1, d)
+    bounds[5000:5040] = bounds[0]
+    bounds[32990] = bounds[0]
+    q = bf16(rng.normal(size=(1, 2, 1, d)))
+    tables = [[int(x) for x in rng.permutation(n)]]
+    for top_k in (2, 300, 25000):
+        check_choice(rng, bounds, q, tables, [n * bs - 7], bs, top_k, 1, 1)
+    same = bounds[:1].expand(n, 1, 2, d).contiguous()  # ties everywhere: every block is ambiguous
+    check_choice(rng, same, q, tables, [n * bs - 7], bs, 40, 1, 2)
+
+
+@pytest.mark.parametrize("n", [400, 1800, 9000])
+def test_more_ambiguous_blocks_than_are_ranked_in_shared_memory(n):
+    # 300 blocks within an f32 sum's error of one another, in no order, and equal ones among them
+    rng = np.random.default_rng(n)
+    d, bs = 128, 16
+    base = rng.normal(size=d) * 4
+    lo = rng.normal(size=(n, d)) * 0.1
+    near = rng.permutation(np.arange(1, n - 1))[:300]
+    lo[near] = base
+    lo[near, 0] = 0.5 + (np.arange(300) // 3) * 2.0 ** -8
+    q = np.tile(base, (1, 2, 1, 1))
+    q[..., 0] = 2.0 ** -14
+    bounds, q = bf16(np.stack([lo, lo], 1)[:, None]), bf16(q)
+    tables = [[int(x) for x in rng.permutation(n)]]
+    for top_k in (20, 152, 301):
+        check_choice(rng, bounds, q, tables, [n * bs - 3], bs, top_k, 1, 1)
+
+
+@pytest.mark.parametrize("fmt", [16, "e4m3"])
+def test_bounds_after_a_sequence_gave_up_rows(fmt):
+    # four proposed tokens, three given up, two others appended in their place: the bounds still hold every key
+    rng = np.random.default_rng(53)
+    hk, bs, d = 2, 32, 128
+    tables = i32([[2, 0, 1]])
+    kw = {} if fmt == 16 else dict(bits=8, group_size=B.PKV_GROUP_BLOCK)
+    pools = [torch.zeros((3, hk, bs, d), dtype=torch.bfloat16 if fmt == 16 else torch.uint8, device=DEV) for _ in range(2)]
+    sc = {} if fmt == 16 else {s: torch.zeros((3, hk), device=DEV) for s in ("k_scales", "v_scales")}
+    bounds = torch.full((3, hk, 2, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for at, n, size in ((0, 40, 1.0), (40, 4, 9.0), (41, 2, 1.0), (43, 30, 1.0)):
+        new = [bf16(rng.normal(size=(1, hk, n, d)) * size).to(DEV) for _ in range(2)]
+        B.paged_append(*new, tables, i32([at]), *pools, **sc, **kw)
+        B.update_block_bounds(pools[0], tables, i32([at + n]), bounds, n_new=n, k_scales=sc.get("k_scales"), **kw)
+        keys = pools[0].double() if fmt == 16 else torch.from_numpy(
+            O.block_values(pools[0].cpu().numpy(), sc["k_scales"].cpu().numpy())).to(DEV)
+        rows = keys[tables[0].long()].transpose(0, 1).reshape(hk, 3 * bs, d)[:, :at + n]
+        for j in range(-(-(at + n) // bs)):
+            lo, hi = bounds[int(tables[0, j])].double().unbind(1)
+            held = rows[:, j * bs:(j + 1) * bs]
+            assert (lo <= held.amin(1)).all() and (hi >= held.amax(1)).all()
+            if fmt == "e4m3":  # read whole: no looser than the rounding
+                assert (lo >= held.amin(1) - held.amin(1).abs() * 2.0 ** -7).all()
+                assert (hi <= held.amax(1) + held.amax(1).abs() * 2.0 ** -7).all()
