@@ -281,7 +281,8 @@ _workspaces = _Workspaces()
 class _Call:
     """What a call's shapes settle: the argument structures and the plan."""
 
-    __slots__ = ("layout", "params", "layout_ref", "params_ref", "sparse", "sparse_ref", "workspace_bytes", "out_shape")
+    __slots__ = ("layout", "params", "layout_ref", "params_ref", "sparse", "sparse_ref", "workspace_bytes", "out_shape",
+                 "like_q")
 
     def __init__(self, layout, params, q, sparse=None):
         if q.get_device() < 0:
@@ -291,8 +292,11 @@ class _Call:
         self.sparse_ref = None if sparse is None else ctypes.byref(sparse)
         dv = layout.v_head_dim or layout.head_dim
         self.out_shape = tuple(q.shape[:-1]) + (dv,)
+        self.like_q = self.out_shape == tuple(q.shape)
 
     def new_out(self, q):
+        if self.like_q:
+            return torch.empty_like(q, memory_format=torch.contiguous_format)
         return torch.empty(self.out_shape, dtype=q.dtype, device=q.device)
 
 
@@ -497,26 +501,45 @@ class HostDecodeStep:
             self._handle = None
 
 
-class _on_device:
-    """Makes `device` current for the call (a no-op when it already is)."""
+class _Stay:
+    """The call's device is current already."""
 
-    __slots__ = ("index", "prev")
-
-    def __init__(self, device: torch.device):
-        self.index = device.index
-        self.prev = None
+    __slots__ = ()
 
     def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.index is not None and cur != self.index:
-            self.prev = cur
-            torch.cuda.set_device(self.index)
         return self
 
     def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
         return False
+
+
+class _Switch:
+    """Makes another device current for the call."""
+
+    __slots__ = ("index", "prev")
+
+    def __init__(self, index: int, prev: int):
+        self.index, self.prev = index, prev
+
+    def __enter__(self):
+        torch.cuda.set_device(self.index)
+        return self
+
+    def __exit__(self, *exc):
+        torch.cuda.set_device(self.prev)
+        return False
+
+
+_stay = _Stay()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_device(device: torch.device):
+    index = device.index
+    if index is None:
+        return _stay
+    cur = _current_device()
+    return _stay if cur == index else _Switch(index, cur)
 
 
 def paged_decode_passes(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
