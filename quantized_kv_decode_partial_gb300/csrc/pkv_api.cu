@@ -203,6 +203,28 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
       if (half < rich_rows && ctas >= slots) break;
       part = half;
     }
+    // e4m3 pages: a grid of under two waves (three CTAs per SM, four for 64-dim heads with up to
+    // 8 query rows) loses most to its part-filled last one, so it takes what fills 3, 2 or 1
+    // waves, the most that leaves a CTA 256 KB, or one wave rather than a few CTAs more than
+    // that (4 query rows, D=128: 2 sequences of 8192 rows 13.6 -> 11.5 us, 4 of 60000 101.7 ->
+    // 79.9, 32 of 8000 108.0 -> 82.7, 24 of 1000 to 16000 81.0 -> 70.2; D=64: 32 of 1000 to 16000
+    // 77.1 -> 53.2; 16 query rows, D=128: 4 of 60000 129.5 -> 98.0, 4 of 30000 to 60000 78.5 ->
+    // 93.7; D=64, 8 of 20001 to 40003 57.0 -> 64.5).
+    if (block_scaled(L) && P->window == 0) {
+      const bool small = L->head_dim + v_dim(L) <= 128 && P->num_q_heads / L->num_kv_heads * P->n_query <= 8;
+      const long long wave = (small ? 4ll : 3ll) * (sm_count > 0 ? sm_count : 1);
+      const long long ctas = units * ((span + part - 1) / part);
+      if (2 * ctas > wave && ctas < 2 * wave) {
+        for (int w = 3; w >= 1; --w) {
+          const long long k = w * wave / units;
+          const long long rows = k > 0 ? round_up((span + k - 1) / k, ch) : 0;
+          if (rows * kv_row >= (256ll << 10) || (w == 1 && k > 0 && ctas > wave)) {
+            part = rows;
+            break;
+          }
+        }
+      }
+    }
     // e4m3 pages: a grid of at most one CTA per SM with more partitions than a cluster
     // holds takes 16 of them instead, while a CTA still reads no more than 256 KB: the
     // merge then needs no second launch and no workspace (1 x 8192 rows of 256-dim heads,

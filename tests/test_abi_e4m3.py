@@ -72,3 +72,20 @@ def test_the_fused_call_is_refused(lib):
     rc = lib.pkv_paged_decode_append_attention(ctypes.byref(lay), ctypes.byref(par), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
                                                None, FAKE, None, FAKE, FAKE, 0.1, FAKE, FAKE, 1 << 30, None, None)
     assert rc == B.PKV_ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("seqs,rows,d,rep,parts", [
+    (4, 60000, 128, 4, 42),   # 512 CTAs, a little over one wave of 456: three waves
+    (32, 8000, 128, 4, 5),
+    (32, 16000, 64, 4, 7),    # four CTAs per SM
+    (2, 8192, 128, 4, 26),    # CTAs of 256 KB would not fill a wave: one wave of shorter ones
+    (8, 40003, 128, 4, 16),   # over two waves: as it was
+    (1, 8192, 256, 4, 16),    # half a wave or less: one cluster per KV head
+])
+def test_partitions_fill_whole_waves(lib, seqs, rows, d, rep, parts):
+    hk = 4 if seqs == 1 else 8
+    blocks = -(-rows // 32)
+    plan = B.make_plan(B.PoolLayout(seqs * blocks, hk, 32, d, 8, B.PKV_GROUP_BLOCK),
+                       B.DecodeParams(seqs, hk * rep, 1, blocks, 0, 0, 0, B.PKV_SCHEDULE_PARTITIONS), 152)
+    assert plan.max_partitions == parts
+    assert plan.partition_tokens * plan.max_partitions >= rows
