@@ -58,7 +58,7 @@
 //    chunk's scale, 4 FMAs per 4 MMAs of a 32-row chunk. Up to 8 query rows the kernel is
 //    bound by HBM (64 sequences of 1024 to 32768 rows, D=128: 330 us, 1.03 of a copy's rate);
 //    above, by dependent instructions: 8 sequences of 20001 to 40003 rows, 16 query rows,
-//    95 us (0.79; in blocks of 16 rows 104). Scores by e4m3 MMAs on unconverted keys against q
+//    95 us (0.79; in blocks of 16 rows 110). Scores by e4m3 MMAs on unconverted keys against q
 //    in two e4m3 parts were slower throughout (330 -> 373 us, 126 -> 166 us).
 //  * Rows at or past seq_len in the last page are masked before they can reach
 //    an accumulator (scores set to -inf by select; their V operand or V scale
@@ -186,7 +186,8 @@ struct PartialCfg {
   static constexpr bool kThird = kBlk && !SOLO && kWarps == 4 && NT <= 2 &&
                                  3 * ((8 * kStageBytes > kCombineBytes ? 8 * kStageBytes : kCombineBytes) + kBarrierBytes +
                                       kBalBytes + 8 * kSlotBytes + 2048) <= 228 * 1024;
-  static constexpr int kRegs = kThird ? 168 : 255;  // 3 x 128 threads share an SM's 65536
+  static constexpr bool kFourth = kThird && NT == 1 && D + DV <= 128;
+  static constexpr int kRegs = kFourth ? 128 : kThird ? 168 : 255;  // 4 or 3 x 128 threads share an SM's 65536
   // (a query group of 8 warps shares one ring of 8 or 16 stages, within 144 KB)
   static constexpr int kStagesPerWarp = WQ == 8 ? (8 * 2 * kStageBytes <= 144 * 1024 ? 2 : 1)
                                         : kEightLone ? 1
@@ -709,13 +710,14 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
       }
       if constexpr (C::kBlk) {
         // The blocks' scales: a 4-byte copy per piece and plane. A piece past the length has
-        // none; its slot is zeroed, since its (masked) keys still meet it.
+        // none; its slot is zeroed, since its (masked) keys still meet it, and so are the slots
+        // of a chunk of fewer than four pieces, which are compared with the others.
         if (row >= 0) {
           const int j = lane & 3;
           const int prow = j == 0 ? pr[0] : j == 1 ? pr[1] : j == 2 ? pr[2] : pr[3];
-          if (lane < 8 && j < nb) {
+          if (lane < 8 && (PC || j == 0)) {
             const uint32_t dst = my_slots + is * C::kSlotBytes + (lane < 4 ? 0 : 16) + 4 * j;
-            if (prow >= 0) {
+            if (j < nb && prow >= 0) {
               cp_async_4(dst, bs_src + static_cast<unsigned>(prow) / static_cast<unsigned>(p.block_size));
             } else {
               st_shared_u32(dst, 0u);
@@ -988,7 +990,26 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
       a = PC && two ? v[2 * tile] : v[PC ? tile : 0];
       b = PC && two ? v[2 * tile + 1] : a;
     };
-    auto score_chunk = [&](uint32_t kpl, uint32_t sbq, int kbase, bool full_vis, float (&pr)[C::kTiles][NT][4],
+    // Value scales of small blocks. The weights of a chunk of several blocks meet V's codes as
+    // one fp16 product: each times its block's scale over the chunk's largest (at most 1) times
+    // 2^9, and O^T takes the rest (unit), that largest scale over 2^9. Weights reach 2^kSlack, so
+    // fp16 holds them up to 2^15, and a scale down to 2^-9 of the largest leaves a weight no
+    // smaller than it is, so no less exact than in a chunk of one block. Scales further apart (or a
+    // largest one that leaves no normal number here) send the chunk through the loop once per
+    // block, the other blocks' keys masked: a scale that no query's weight meets may be any.
+    // Returns how often: 1, or the chunk's blocks. Scale 0 adds nothing, whatever the others are.
+    // The comparison costs 5% where instructions bound the kernel (8 sequences of 20001 to 40003
+    // rows in blocks of 16, D=128, 16 query rows: 104.4 -> 109.8 us; 4 rows: 95.4 -> 97.4).
+    auto chunk_passes = [&](uint32_t addr, float& unit) {
+      if constexpr (!(C::kBlk && PC)) return 1;
+      const uint32_t bits = ld_shared_u32(addr + 4 * (lane & 3));  // order as the scales do, which are >= 0
+      const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
+      const uint32_t least = __reduce_min_sync(0xffffffffu, bits - 1);  // but 0
+      unit = __uint_as_float(most) * (1.f / 512.f);
+      // the second: 2^-116 <= most < 2^127
+      return least + (9u << 23) >= most - 1 && most - (11u << 23) < (243u << 23) ? 1 : nb;
+    };
+    auto score_chunk = [&](uint32_t kpl, uint32_t sbq, int kbase, bool full_vis, int block, float (&pr)[C::kTiles][NT][4],
                            float (&corr)[NT][2]) -> bool {
       float kscale[4];
       if constexpr (C::kBlk) load_scales(sbq, kscale);
@@ -1144,7 +1165,8 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
             for (int e = 0; e < 4; ++e) {
               const int key = kbase + tile * 16 + (C::kBlk && (e >> 1) ? 8 + (g ^ 4) : g + 8 * (e >> 1));
               const int qi = (PV ? (2 * t + (e & 1)) & 3 : rbase + 8 * nt + 2 * t + (e & 1)) % N;
-              const bool vis = key < vis_base + qi && (win == 0 || key >= vis_base + qi - win);
+              bool vis = key < vis_base + qi && (win == 0 || key >= vis_base + qi - win);
+              if constexpr (C::kBlk && PC) vis &= block < 0 || (two ? 2 * tile + (e >> 1) : tile) == block;
               x[tile][nt][e] = vis ? x[tile][nt][e] : -INFINITY;
             }
       }
@@ -1229,31 +1251,23 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
             for (int e2 = 0; e2 < 2; ++e2) corr_v[grp][nt][e2] *= corr[nt][e2];
       }
     };
-    auto value_chunk = [&](uint32_t kpl, uint32_t vpl, uint32_t sbq, int kbase, bool stale, const float (&pr)[C::kTiles][NT][4]) {
+    auto value_chunk = [&](uint32_t kpl, uint32_t vpl, uint32_t sbq, int kbase, bool stale, int block, float unit,
+                           const float (&pr)[C::kTiles][NT][4]) {
       // ---- O^T += V^T P^T
       if constexpr (C::kBlk) {
-        // Weights of the whole chunk as B fragments; with several blocks in the chunk, each
-        // key's weight times its block's scale over the chunk's largest (at most 1). The
-        // chunk's product then takes that largest scale on its way into O^T. A weight below
-        // fp16's normal range is off by at most 2^-25, so a key by 2^-25 of what the chunk's
-        // largest scale can hold: more than 2^-11 of its own value only where that scale is
-        // far above both the key's scale and the values stored under it.
+        // Weights of the whole chunk as B fragments, times their blocks' scales where those share one.
         uint32_t pb2[C::kTiles][NT][2];
         float vs[4];
         load_scales(sbq + 16, vs);
-        float vmax = vs[0];
-        if constexpr (PC) {
-          vmax = fmaxf(vmax, vs[1]);
-          if (nb == 4) vmax = fmaxf(vmax, fmaxf(vs[2], vs[3]));
-        }
-        const float vinv = PC && vmax >= 1.1754944e-38f ? fast_rcp(vmax) : 0.f;  // normal numbers
+        if constexpr (!PC) unit = vs[0];
+        const float vinv = PC ? fast_rcp(unit) : 1.f;
 #pragma unroll
         for (int tile = 0; tile < C::kTiles; ++tile) {
           float ra = 1.f, rb = 1.f;
           if constexpr (PC) {
             pick_scales(vs, tile, ra, rb);
-            ra *= vinv;
-            rb *= vinv;
+            ra = block < 0 ? ra * vinv : 1.f;
+            rb = block < 0 ? rb * vinv : 1.f;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -1300,7 +1314,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[2 * i + j][nt][e] = fmaf(vmax, acc[j][nt][e], o[2 * i + j][nt][e]);
+              for (int e = 0; e < 4; ++e) o[2 * i + j][nt][e] = fmaf(unit, acc[j][nt][e], o[2 * i + j][nt][e]);
         }
       } else {
 #pragma unroll
@@ -1430,8 +1444,10 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
       }  // bf16 and affine pages
     };
 
-    for (; done < seg_end; ++done, cs_parity ^= (cs == C::kStagesPerGroup - 1), cs = cs == C::kStagesPerGroup - 1 ? 0 : cs + 1) {
+    int pass = 0;  // of the chunk's passes (one, but for small blocks whose value scales lie far apart)
+    while (done < seg_end) {
       const bool landed = mbar_wait_warp(smem_addr(&my_full[cs]), cs_parity, abort_flag, p.error_flag, p.wait_limit_ns);
+      int passes = 1;
       if (landed && my_ok[cs]) {
         uint8_t* stage = my_ring + cs * C::kStageBytes;
         const uint32_t kpl = smem_addr(stage);
@@ -1448,9 +1464,17 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
         } else {
         float pr[C::kTiles][NT][4];
         float corr[NT][2];
-        if (score_chunk(kpl, sbq, kbase, full_vis, pr, corr)) rescale(corr);
-        value_chunk(kpl, vpl, sbq, kbase, stale, pr);
+        float unit = 0.f;
+        passes = chunk_passes(sbq + 16, unit);
+        const int block = passes > 1 ? pass : -1;  // the pass's block, or all together
+        if (C::kBlk && PC && block >= 0) unit = ld_shared_f32(sbq + 16 + 4 * block);
+        if (score_chunk(kpl, sbq, kbase, full_vis && block < 0, block, pr, corr)) rescale(corr);
+        value_chunk(kpl, vpl, sbq, kbase, stale, block, unit, pr);
         }  // tensor-core contraction
+      }
+      if constexpr (C::kBlk && PC) {
+        pass = pass + 1 < passes ? pass + 1 : 0;
+        if (pass > 0) continue;  // the same chunk again
       }
       if constexpr (WQ == 1) {
         if (!landed) break;
@@ -1461,6 +1485,9 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
         if (group_barrier_any(1 + pg, WQ * 32, !landed)) break;
         if (leader) issue_next(cs);
       }
+      ++done;
+      cs_parity ^= cs == C::kStagesPerGroup - 1;
+      cs = cs == C::kStagesPerGroup - 1 ? 0 : cs + 1;
     }
     if (leader && done < seg_end && done < issued && lane == 0) {
       // Aborted: let this group's copies still in flight land before the ring is reused.
