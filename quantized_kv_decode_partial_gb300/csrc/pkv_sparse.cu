@@ -417,10 +417,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pkv_score_kernel(const __gri
 //
 // With T the k-th largest of the candidates' f32 scores and |f32 - exact| <= E: a score
 // above T + 2E is in (at most k - 1 scores lie above T, and a block below T cannot overtake
-// it), one below T - 2E is out, the rest is ambiguous. E = D 2^-25 |q|_1 max|bound|: D / 8
-// MMA steps and a final sum per score, each off by at most 2^-22 of the products' magnitudes
-// summed (16 exact products join an f32 accumulator per step; the largest error seen, over
-// sums with and without cancellation, is under a tenth of E).
+// it), one below T - 2E is out, the rest is ambiguous. E = 1.5 D 2^-25 |q|_1 max|bound|: an MMA
+// adds 16 exact products and the f32 accumulator, each cut toward 0 below 2^-25 of the power of
+// two that the largest addend reaches, and cuts the sum to 24 bits (2^-23), as sums made to show
+// it do on this GPU. With A the magnitudes summed in an accumulator, an MMA is thus off by at most
+// (17 + 4) 2^-25 A, the D / 16 MMAs of both accumulators by 21/16 D 2^-25 (A + A'), A + A' at most
+// |q|_1 max|bound|, and their sum by 2^-24 of it: 1.35 D 2^-25 in all. Spread scores stay under a
+// tenth of E.
 //
 // T comes from histograms of 2048 equal bins over [lowest, highest] key, narrowed to the bin
 // that holds the k-th until that holds at most 32 keys, which every warp then ranks (one round
@@ -718,7 +721,7 @@ __device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   mu = __reduce_max_sync(0xffffffffu, mu);
   qu = __reduce_max_sync(0xffffffffu, qu);
-  float err = static_cast<float>(p.head_dim) * 2.98023224e-8f * __uint_as_float(qu) * __uint_as_float(mu);  // E
+  float err = static_cast<float>(p.head_dim) * 4.47034836e-8f * __uint_as_float(qu) * __uint_as_float(mu);  // E
   // Where E leaves the normal range so may the products, whose roundings E does not count: exact sums decide.
   if (qu != 0u && mu != 0u && err < 1.17549435e-38f) err = INFINITY;
 
