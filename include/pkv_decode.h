@@ -421,7 +421,9 @@ int pkv_paged_decode_append_attention(const pkv_pool_layout* layout, const pkv_d
  * the first_blocks first, the last_blocks last and, of those between, the best-scored, in
  * all top_k. Blocks are compared as by exact sums, ties going to the lower block: f32 sums
  * decide where their error cannot matter, sums of 48 bits of exact products elsewhere, so the
- * choice does not depend on the order of a sum. A NaN score counts as the lowest.
+ * choice does not depend on the order of a sum (while |q|_1 * max|bound| is within f32's
+ * range). A query row whose sum is NaN counts as the lowest, like a sum of -infinity: the
+ * other rows score the block.
  *
  * The softmax then runs over the chosen rows alone, the causal rule among the n_query newest
  * rows included. window must be 0 and num_seqs * num_kv_heads at most 65535; the layouts and

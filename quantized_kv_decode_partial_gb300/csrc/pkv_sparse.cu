@@ -52,6 +52,15 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {  //
   const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// max(a, 0) and min(a, 0), NaN for NaN
+__device__ __forceinline__ uint32_t positive_bf16x2(uint32_t a) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), __float2bfloat162_rn(0.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t negative_bf16x2(uint32_t a) {
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), __float2bfloat162_rn(0.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -307,15 +316,16 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, size_t unit, 
   pick(ids, ph0, ph1);
   load(ph0, ph1, 1, hi0, hi1);
   load(ph0, ph1, 0, lo0, lo1);
-  {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight
+  {  // the query rows, max(q, 0) then min(q, 0), staged while the first bounds are in flight; a
+     // NaN stays one, so that its row's sums are NaN and no score of a block
     const uint4* q = reinterpret_cast<const uint4*>(p.q + unit * p.nq * D);
     for (int i = threadIdx.x; i < ntiles * 8 * (D / 8); i += WARPS * 32) {
       const int r = i / (D / 8), c = i - r * (D / 8);
       const uint4 v = r < p.nq ? q[i] : make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(sq + r * kStride + c * 16) =
-          make_uint4(max_bf16x2(v.x, 0u), max_bf16x2(v.y, 0u), max_bf16x2(v.z, 0u), max_bf16x2(v.w, 0u));
+          make_uint4(positive_bf16x2(v.x), positive_bf16x2(v.y), positive_bf16x2(v.z), positive_bf16x2(v.w));
       *reinterpret_cast<uint4*>(sq + r * kStride + D * 2 + c * 16) =
-          make_uint4(min_bf16x2(v.x, 0u), min_bf16x2(v.y, 0u), min_bf16x2(v.z, 0u), min_bf16x2(v.w, 0u));
+          make_uint4(negative_bf16x2(v.x), negative_bf16x2(v.y), negative_bf16x2(v.z), negative_bf16x2(v.w));
     }
     __syncthreads();
     ready();

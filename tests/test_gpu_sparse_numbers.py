@@ -43,3 +43,26 @@ def test_addends_that_a_matrix_instruction_cuts(d, n, seqs):
     assert ref[0][0] == [0, high, n - 1]
     sel = B.select_blocks(qt.to(DEV), bounds.to(DEV), i32(tables), i32([n * bs] * seqs), block_size=bs, top_k=3)
     assert sel.blocks.tolist() == ref
+
+
+@pytest.mark.parametrize("n,seqs", [(300, 1), (300, 40), (1500, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan")])
+def test_a_query_row_with_a_nan_scores_lowest(n, seqs, bad):
+    # one launch and two; a row with a NaN has no score, the block's is that of the other rows
+    rng = np.random.default_rng(n + seqs)
+    hk, rep, d, bs, top_k = 2, 4, 128, 16, 20
+    mid = rng.normal(size=(n, hk, d))
+    bounds = torch.from_numpy(np.stack([mid - 0.3, mid + 0.3], 2)).to(torch.bfloat16)
+    q = torch.from_numpy(rng.normal(size=(seqs, hk * rep, 1, d))).to(torch.bfloat16)
+    q[:, 1] *= 4  # a row that would decide the choice
+    clean = q.clone()
+    q[:, 1, 0, 5] = bad      # KV head 0: one of its rows
+    q[:, rep:, 0, 77] = bad  # KV head 1: all of them
+    tables = [[int(x) for x in rng.permutation(n)] for _ in range(seqs)]
+    sel = B.select_blocks(q.to(DEV), bounds.to(DEV), i32(tables), i32([n * bs] * seqs), block_size=bs, top_k=top_k)
+    rows = [0, 2, 3]
+    want = S.choose_blocks(clean[:, rows].double().numpy(), bounds[:, :1].double().numpy(), tables, [n * bs] * seqs, bs,
+                           top_k, 1, 1)
+    for b in range(seqs):
+        assert sel.blocks[b, 0].tolist() == want[b][0], b
+        assert sel.blocks[b, 1].tolist() == list(range(top_k - 1)) + [n - 1], b
