@@ -147,11 +147,11 @@ __global__ void __launch_bounds__(128) pkv_bounds_kernel(const __grid_constant__
           constexpr int kPer = 32 / FMT;  // codes per word
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            // scale * code is exact in f32 (8 by 8 bits), so this rounds once
-            const float x = fmaf(sc[u], static_cast<float>((w[k] >> (FMT * j)) & ((1u << FMT) - 1u)), bi[u]);
+            // each bound's roundings all go outward: to the nearest f32 a key could end inside
+            const float c = static_cast<float>((w[k] >> (FMT * j)) & ((1u << FMT) - 1u));
             const int i = k * kPer + j;
-            lo[i] = __float_as_uint(fminf(__uint_as_float(lo[i]), x));
-            hi[i] = __float_as_uint(fmaxf(__uint_as_float(hi[i]), x));
+            lo[i] = __float_as_uint(fminf(__uint_as_float(lo[i]), __fmaf_rd(sc[u], c, bi[u])));
+            hi[i] = __float_as_uint(fmaxf(__uint_as_float(hi[i]), __fmaf_ru(sc[u], c, bi[u])));
           }
         }
       }
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(128) pkv_bounds_kernel(const __grid_constant__
         if constexpr (FMT == kFmtE4m3) {
           a = __half22float2(*reinterpret_cast<__half2*>(&lo[4 * q + i]));
           c = __half22float2(*reinterpret_cast<__half2*>(&hi[4 * q + i]));
-          a = make_float2(a.x * scale, a.y * scale);
-          c = make_float2(c.x * scale, c.y * scale);
+          a = make_float2(__fmul_rd(a.x, scale), __fmul_rd(a.y, scale));
+          c = make_float2(__fmul_ru(c.x, scale), __fmul_ru(c.y, scale));
         } else {
           a = make_float2(__uint_as_float(lo[8 * q + 2 * i]), __uint_as_float(lo[8 * q + 2 * i + 1]));
           c = make_float2(__uint_as_float(hi[8 * q + 2 * i]), __uint_as_float(hi[8 * q + 2 * i + 1]));

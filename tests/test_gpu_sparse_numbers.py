@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import block_scaled as O
 from oracle import sparse as S
 from quantized_kv_decode_partial_gb300 import binding as B
 
@@ -66,3 +67,55 @@ def test_a_query_row_with_a_nan_scores_lowest(n, seqs, bad):
     for b in range(seqs):
         assert sel.blocks[b, 0].tolist() == want[b][0], b
         assert sel.blocks[b, 1].tolist() == list(range(top_k - 1)) + [n - 1], b
+
+
+def test_bounds_of_e4m3_keys_next_to_a_bf16_value():
+    # scale * code lies within 2^-25 of a bf16 value (on either side), and rounds to it in f32
+    hk, bs, d = 2, 32, 64
+    ks = []
+    for c in (1.125, 1.25, 1.375, 1.625, 1.75, 1.875):
+        for f in range(128, 256):
+            target = f * 2.0 ** -8
+            for step in (-1, 0, 1):
+                s = np.nextafter(np.float32(target / c), np.float32(np.inf if step > 0 else -np.inf)) if step else \
+                    np.float32(target / c)
+                exact = float(s) * c
+                if exact != target and float(np.float32(exact)) == target:
+                    ks.append((s, c))
+    assert len(ks) > 100
+    nb = -(-len(ks) // hk)
+    scales = np.ones((nb, hk), np.float32)
+    vals = np.zeros((nb, hk, bs, d))
+    for i, (s, c) in enumerate(ks):
+        scales[i // hk, i % hk] = s
+        vals[i // hk, i % hk] = np.where(np.arange(d) % 2 == 0, c, -c)
+    pool = O.e4m3_codes(vals)
+    keys = O.block_values(pool, scales)
+    tables = [list(range(nb))]
+    ref = S.update_bounds(np.zeros((nb, hk, 2, d)), keys, tables, [nb * bs], nb * bs, True)
+    got = torch.zeros((nb, hk, 2, d), dtype=torch.bfloat16, device=DEV)
+    B.update_block_bounds(torch.from_numpy(pool).to(DEV), i32(tables), i32([nb * bs]), got, n_new=nb * bs,
+                          k_scales=torch.from_numpy(scales).to(DEV), bits=8, group_size=B.PKV_GROUP_BLOCK)
+    assert np.array_equal(got.double().cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [128, 256])
+def test_bounds_of_affine_keys_next_to_a_bf16_value(bits, d):
+    # a bias of 1 and codes times scales far below half an f32 step of it, above and below
+    rng = np.random.default_rng(bits + d)
+    nb, hk, bs = 6, 2, 32
+    words = rng.integers(-2 ** 31, 2 ** 31, size=(nb, hk, bs, d * bits // 32)).astype(np.int32)
+    scale = rng.choice([-1.0, 1.0], size=(nb, hk, 1, d // 64)) * 2.0 ** -38 * np.ones((1, 1, bs, 1))
+    bias = rng.choice([-1.0, 1.0, 1.5], size=(nb, hk, 1, d // 64)) * np.ones((1, 1, bs, 1))
+    per = 32 // bits
+    codes = (words.view(np.uint32)[..., None] >> (bits * np.arange(per, dtype=np.uint32))) & np.uint32(2 ** bits - 1)
+    codes = codes.reshape(nb, hk, bs, d).astype(np.float64)
+    keys = codes * np.repeat(scale, 64, -1) + np.repeat(bias, 64, -1)  # 53 bits hold them exactly
+    tables = [[3, 0, 5, 1, 4, 2]]
+    ref = S.update_bounds(np.zeros((nb, hk, 2, d)), keys, tables, [nb * bs - 7], nb * bs, False)
+    dev = [torch.from_numpy(x).to(torch.bfloat16).to(DEV) for x in (scale, bias)]
+    got = torch.zeros((nb, hk, 2, d), dtype=torch.bfloat16, device=DEV)
+    B.update_block_bounds(torch.from_numpy(words).to(DEV), i32(tables), i32([nb * bs - 7]), got, n_new=nb * bs,
+                          k_scales=dev[0], k_biases=dev[1], bits=bits)
+    assert np.array_equal(got.double().cpu().numpy(), ref)
