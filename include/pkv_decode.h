@@ -436,11 +436,12 @@ typedef struct pkv_sparse_params {
 } pkv_sparse_params;
 
 typedef struct pkv_sparse_plan {
-  pkv_plan attention;     /* of the decode over chosen blocks: num_seqs * num_kv_heads sequences of
-                             one KV head; its workspace_bytes are what
+  pkv_plan attention;     /* of the decode over a choice of top_k blocks: num_seqs * num_kv_heads
+                             sequences of one KV head; its workspace_bytes are what
                              pkv_selected_decode_attention needs */
   size_t select_bytes;    /* workspace of pkv_select_blocks (0 when the table holds no more than top_k blocks) */
-  size_t workspace_bytes; /* workspace of pkv_sparse_decode_attention */
+  size_t workspace_bytes; /* workspace of pkv_sparse_decode_attention, which plans for no more
+                             blocks than the table holds */
 } pkv_sparse_plan;
 
 /* Plans as pkv_make_plan and pkv_plan_for_current_device do. */

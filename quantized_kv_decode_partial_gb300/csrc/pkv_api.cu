@@ -1088,20 +1088,24 @@ int chosen_partition(const pkv_pool_layout* vl, const pkv_decode_params* vp, int
   return static_cast<int>(round_up((rows + parts - 1) / parts, chunk_rows_of(vl->bits)));
 }
 
+// Most blocks that the choice gives a unit: no more than its table holds.
+int most_chosen(const pkv_decode_params* P, const pkv_sparse_params* S) {
+  return std::min(S->top_k, P->max_blocks_per_seq);
+}
+
 // The decode over chosen blocks: the pool as NB * HK blocks of one KV head, every (sequence,
-// KV head) a sequence of at most top_k of them.
-void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S, int sm_count,
-                 pkv_pool_layout* vl, pkv_decode_params* vp) {
+// KV head) a sequence of at most `blocks` of them, in a table of that width.
+void chosen_view(const pkv_pool_layout* L, const pkv_decode_params* P, int blocks, int sm_count, pkv_pool_layout* vl,
+                 pkv_decode_params* vp) {
   *vl = *L;
   vl->num_blocks = L->num_blocks * L->num_kv_heads;
   vl->num_kv_heads = 1;
   *vp = *P;
   vp->num_seqs = P->num_seqs * L->num_kv_heads;
   vp->num_q_heads = P->num_q_heads / L->num_kv_heads;
-  vp->max_blocks_per_seq = S->top_k;
+  vp->max_blocks_per_seq = blocks;
   if (vp->partition_tokens == 0 && vp->schedule != PKV_SCHEDULE_BALANCED)
-    vp->partition_tokens = chosen_partition(vl, vp, std::min(S->top_k, P->max_blocks_per_seq), P->max_blocks_per_seq,
-                                            sm_count);
+    vp->partition_tokens = chosen_partition(vl, vp, blocks, P->max_blocks_per_seq, sm_count);
 }
 
 // Scores of a unit in the workspace: rows of 16-byte groups.
@@ -1122,31 +1126,36 @@ SparseWorkspace sparse_workspace(const pkv_pool_layout* L, const pkv_decode_para
   w.keys64 = w.tile_abs + (cells ? round256(units * pkv::select_tiles(P->max_blocks_per_seq) * sizeof(float)) : 0);
   w.select_bytes = w.keys64 + round256(cells * sizeof(unsigned long long));
   w.tables = w.select_bytes;
-  w.lens = w.tables + round256(units * S->top_k * sizeof(int32_t));
+  w.lens = w.tables + round256(units * most_chosen(P, S) * sizeof(int32_t));
   w.attention = w.lens + round256(units * sizeof(int32_t));
   return w;
 }
 
 int sparse_plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S, int sm_count,
                      pkv_sparse_plan* out) {
-  pkv_pool_layout vl;
-  pkv_decode_params vp;
-  chosen_view(L, P, S, sm_count, &vl, &vp);
-  int rc = check_params(&vl, &vp);
-  if (rc) return rc;
-  rc = plan_impl(&vl, &vp, sm_count, &out->attention);
-  if (rc) return rc;
+  // a choice of the caller's own may name top_k blocks whatever the table holds
+  pkv_plan step;
+  for (pkv_plan* plan : {&step, &out->attention}) {
+    pkv_pool_layout vl;
+    pkv_decode_params vp;
+    chosen_view(L, P, plan == &step ? most_chosen(P, S) : S->top_k, sm_count, &vl, &vp);
+    int rc = check_params(&vl, &vp);
+    if (rc) return rc;
+    rc = plan_impl(&vl, &vp, sm_count, plan);
+    if (rc) return rc;
+  }
   const SparseWorkspace w = sparse_workspace(L, P, S);
   out->select_bytes = w.select_bytes;
-  out->workspace_bytes = w.attention + out->attention.workspace_bytes;
+  out->workspace_bytes = w.attention + step.workspace_bytes;
   return PKV_OK;
 }
 
-// Fills the parameters of the choice; its workspace is `workspace` (select_bytes).
+// Fills the parameters of the choice; its workspace is `workspace` (select_bytes), its tables
+// are `table_width` wide.
 pkv::SelectParams select_params(const pkv_pool_layout* L, const pkv_decode_params* P, const pkv_sparse_params* S,
                                 const void* q, const void* k_bounds, const int32_t* block_tables,
-                                const int32_t* seq_lens, int32_t* blocks, int32_t* tables, int32_t* lens,
-                                void* workspace, int32_t* error_flag) {
+                                const int32_t* seq_lens, int32_t* blocks, int32_t* tables, int table_width,
+                                int32_t* lens, void* workspace, int32_t* error_flag) {
   const SparseWorkspace w = sparse_workspace(L, P, S);
   char* const ws = static_cast<char*>(workspace);
   pkv::SelectParams p{};
@@ -1160,6 +1169,7 @@ pkv::SelectParams select_params(const pkv_pool_layout* L, const pkv_decode_param
   p.keys64 = reinterpret_cast<unsigned long long*>(ws + w.keys64);
   p.out_blocks = blocks;
   p.out_tables = tables;
+  p.table_width = table_width;
   p.out_lens = lens;
   p.error_flag = error_flag;
   p.num_blocks = L->num_blocks;
@@ -1259,7 +1269,7 @@ int pkv_select_blocks(const pkv_pool_layout* layout, const pkv_decode_params* pa
   if (rc) return rc;
   (void)cudaGetLastError();
   cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
-                                                   chosen_tables, chosen_lens, workspace, error_flag),
+                                                   chosen_tables, sparse->top_k, chosen_lens, workspace, error_flag),
                                      params->num_seqs, sms, dev, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("block choice launch", e);
   return PKV_OK;
@@ -1281,7 +1291,7 @@ int pkv_selected_decode_attention(const pkv_pool_layout* layout, const pkv_decod
   if (rc) return rc;
   pkv_pool_layout vl;
   pkv_decode_params vp;
-  chosen_view(layout, params, sparse, sms, &vl, &vp);
+  chosen_view(layout, params, sparse->top_k, sms, &vl, &vp);
   return enqueue_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, chosen_tables,
                         chosen_lens, scale, out, workspace, workspace_bytes, error_flag, stream,
                         kPassPartial | kPassMerge);
@@ -1310,7 +1320,8 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
   if (rc) return rc;
   pkv_pool_layout vl;
   pkv_decode_params vp;
-  chosen_view(layout, params, sparse, sms, &vl, &vp);
+  const int blocks_wide = most_chosen(params, sparse);
+  chosen_view(layout, params, blocks_wide, sms, &vl, &vp);
   PreparedDecode pd;  // every argument is checked before the first launch
   rc = prepare_decode(&vl, &vp, q, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases, tables, lens, scale, out,
                       ws + w.attention, workspace_bytes - w.attention, error_flag, kPassPartial | kPassMerge, nullptr,
@@ -1319,7 +1330,7 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();
   cudaError_t e = pkv::launch_select(select_params(layout, params, sparse, q, k_bounds, block_tables, seq_lens, blocks,
-                                                   tables, lens, workspace, error_flag),
+                                                   tables, blocks_wide, lens, workspace, error_flag),
                                      params->num_seqs, sms, dev, st);
   if (e != cudaSuccess) return cuda_fail("block choice launch", e);
   return launch_prepared(pd, st);

@@ -150,12 +150,13 @@ struct SelectParams {
   float* tile_abs;                // [units, tiles]: largest magnitude of 16 blocks' bounds
   unsigned long long* keys64;     // [units, max_blocks]: exact scores of many ambiguous blocks, as ordered integers
   int32_t* out_blocks;            // [units, top_k], optional
-  int32_t* out_tables;            // [units, top_k]
+  int32_t* out_tables;            // [units, table_width]
   int32_t* out_lens;              // [units]
   int32_t* error_flag;
   int num_blocks, num_kv_heads, block_size, max_blocks;
   int score_stride;               // max_blocks rounded up to 4
   int n_query, nq, head_dim, top_k, first, last;
+  int table_width;                // entries per unit of out_tables: top_k, or fewer where no unit has as many blocks
   int tiles, tiles_per_warp, key_space, after_scores;  // set by launch_select
 };
 

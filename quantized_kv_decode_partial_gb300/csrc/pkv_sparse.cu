@@ -643,7 +643,7 @@ __device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const __nv_bfloat16* q = p.q + static_cast<size_t>(unit) * p.nq * p.head_dim;
   int32_t* const out_blocks = p.out_blocks ? p.out_blocks + static_cast<size_t>(unit) * p.top_k : nullptr;
-  int32_t* const out_table = p.out_tables + static_cast<size_t>(unit) * p.top_k;
+  int32_t* const out_table = p.out_tables + static_cast<size_t>(unit) * p.table_width;
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   const bool bad = len < p.n_query || len > p.max_blocks * p.block_size;
   const int n = bad ? 0 : (len + p.block_size - 1) / p.block_size;
@@ -656,7 +656,7 @@ __device__ __forceinline__ void select_unit(const SelectParams& p, SelectShared<
     const int ph = j < 0 ? -1 : table[j];
     const bool ok = static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks);
     if (out_blocks) out_blocks[pos] = j;
-    out_table[pos] = ok ? ph * p.num_kv_heads + h : -1;
+    if (pos < p.table_width) out_table[pos] = ok ? ph * p.num_kv_heads + h : -1;
     if (j >= 0 && !ok && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
   };
   for (int i = taken + threadIdx.x; i < p.top_k; i += T) put(i, -1);

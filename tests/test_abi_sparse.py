@@ -48,6 +48,21 @@ def test_plan_sizes(lib):
     assert B.make_sparse_plan(layout(), par, B.SparseParams(200, 1, 2), sm_count=152).select_bytes == 0
 
 
+@pytest.mark.parametrize("width,seqs,fmt", [(4, 8, 16), (4, 8, 8), (64, 64, 8), (3, 1, 4), (300, 2, 16)])
+@pytest.mark.parametrize("top_k", [300, 1000, 16384, 1 << 20])
+def test_a_budget_beyond_the_table_is_planned_as_the_table(lib, width, seqs, fmt, top_k):
+    # no unit has more blocks than its table: neither grid nor workspace grow with the budget
+    lay = layout(bits=fmt, num_kv_heads=8, group_size=B.PKV_GROUP_BLOCK if fmt == 8 else 64)
+    par = B.DecodeParams(seqs, 32, 1, width)
+    plan = lambda k: B.make_sparse_plan(lay, par, B.SparseParams(k, 1, 1), sm_count=152)
+    assert plan(top_k).workspace_bytes == plan(width).workspace_bytes
+    # a choice of the caller's own may name top_k blocks: partitions in proportion, not as many as
+    # the table's few rows would take
+    own = plan(top_k).attention
+    assert own.max_partitions * own.partition_tokens >= top_k * 32
+    assert own.partition_tokens >= 256 or own.max_partitions <= 16
+
+
 @pytest.mark.parametrize("par,sparse,code", [
     ((1, 16, 1, 50, 0, 0), (8, 1, 1), B.PKV_OK),
     ((1, 16, 1, 50, 0, 0), (1, 0, 1), B.PKV_OK),

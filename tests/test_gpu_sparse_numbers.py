@@ -119,3 +119,40 @@ def test_bounds_of_affine_keys_next_to_a_bf16_value(bits, d):
     B.update_block_bounds(torch.from_numpy(words).to(DEV), i32(tables), i32([nb * bs - 7]), got, n_new=nb * bs,
                           k_scales=dev[0], k_biases=dev[1], bits=bits)
     assert np.array_equal(got.double().cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("bits", [16, "e4m3"])
+@pytest.mark.parametrize("width,top_k", [(4, 64), (10, 11), (10, 2000)])
+def test_a_budget_beyond_the_table(bits, width, top_k):
+    # every block is taken: the dense decode's sums in another order, and places past the table's -1
+    g = torch.Generator(device=DEV).manual_seed(width + top_k)
+    seqs, hk, hq, d, bs = 3, 2, 8, 128, 32
+    nb = seqs * width
+    lens = i32([width * bs, 1, width * bs - 37])
+    tables = torch.randperm(nb, generator=g, device=DEV, dtype=torch.int32).view(seqs, width)
+    rows = torch.randn((2, nb, hk, bs, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    q = torch.randn((seqs, hq, 1, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    kw = {}
+    if bits == "e4m3":
+        rows = rows.to(torch.float8_e4m3fn)
+        kw = dict(bits=8, group_size=B.PKV_GROUP_BLOCK, k_scales=torch.ones((nb, hk), device=DEV),
+                  v_scales=torch.ones((nb, hk), device=DEV))
+    bounds = torch.zeros((nb, hk, 2, d), dtype=torch.bfloat16, device=DEV)
+    blocks = torch.full((seqs, hk, top_k), 7, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = B.sparse_decode_attention(q, rows[0], rows[1], bounds, tables, lens, 0.1, top_k=top_k, blocks=blocks,
+                                    error_flag=err, **kw)
+    sel = B.select_blocks(q, bounds, tables, lens, block_size=bs, top_k=top_k, error_flag=err)
+    apart = B.selected_decode_attention(q, rows[0], rows[1], sel, 0.1, error_flag=err, **kw)
+    dense = B.paged_decode_attention(q, rows[0], rows[1], tables, lens, 0.1, error_flag=err, **kw)
+    assert int(err) == 0
+    held = [width, 1, -(-(width * bs - 37) // bs)]
+    for b in range(seqs):
+        for h in range(hk):
+            pad = [-1] * (top_k - held[b])
+            assert blocks[b, h].tolist() == sel.blocks[b, h].tolist() == list(range(held[b])) + pad
+            assert sel.tables[b, h].tolist() == [int(t) * hk + h for t in tables[b, :held[b]]] + pad
+    # bf16 weights round by 2^-8 of each on both sides, outputs by 2^-8 of the value
+    vmax = float(rows[1].float().abs().max())
+    for o in (out, apart):
+        assert ((o.float() - dense.float()).abs() <= 2.0 ** -7 * dense.float().abs() + 2.0 ** -7 * vmax).all()
