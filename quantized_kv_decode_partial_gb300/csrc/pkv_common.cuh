@@ -506,6 +506,14 @@ __device__ __forceinline__ uint32_t ld_nc_keep_u32(const void* ptr) {
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(ptr));
   return v;
 }
+// The same for memory that a kernel overlapping this one may have written before the wait on
+// it (block tables, which the choice of blocks writes after it has let the attention start):
+// not read-only for as long as this kernel runs, so not through the read-only path.
+__device__ __forceinline__ uint32_t ld_keep_u32(const void* ptr) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(ptr));
+  return v;
+}
 
 // Alignment of the first partition of a windowed sequence: a multiple of every
 // chunk size (16 or 32 rows), so partition starts stay on chunk boundaries.

@@ -449,7 +449,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
     const long long r =
         static_cast<long long>(slot) * p.partition_tokens + (pg + lq * C::kWP) * C::kCh + lj * (C::kCh >> pl);
     const long long blk = r / p.block_size < p.max_blocks ? r / p.block_size : p.max_blocks - 1;
-    tbl_pre = static_cast<int>(ld_nc_keep_u32(p.block_tables + static_cast<size_t>(b) * p.max_blocks + blk));
+    tbl_pre = static_cast<int>(ld_keep_u32(p.block_tables + static_cast<size_t>(b) * p.max_blocks + blk));
   }
   if constexpr (HOSTIN) wait_for_prerequisite_grids();  // the host inputs are in flight; the rest may depend on it
   // Fused append: the step's new K/V rows of this (sequence, KV head) are read by the
@@ -581,7 +581,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
         return 0;
       }
       *pk = h * p.block_size + row % p.block_size;
-      return static_cast<int>(__ldg(p.block_tables + static_cast<size_t>(bb) * p.max_blocks + row / p.block_size));
+      return p.block_tables[static_cast<size_t>(bb) * p.max_blocks + row / p.block_size];
     };
     auto bal_coord = [&](int ph, int pk) {
       return pk < 0 ? -2
@@ -598,9 +598,9 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
         crd_cur = bal_coord(ph0, pk0);
       } else {
         const int ph0 = p.window == 0 ? tbl_pre
-                        : lane < my_pieces && stored(lane) ? __ldg(table + piece_row(lane) / p.block_size)
+                        : lane < my_pieces && stored(lane) ? table[piece_row(lane) / p.block_size]
                                                            : 0;
-        tbl_next = 32 + lane < my_pieces && stored(32 + lane) ? __ldg(table + piece_row(32 + lane) / p.block_size) : 0;
+        tbl_next = 32 + lane < my_pieces && stored(32 + lane) ? table[piece_row(32 + lane) / p.block_size] : 0;
         crd_cur = coord_of(ph0, lane);
       }
     }
@@ -649,7 +649,7 @@ __global__ void __maxnreg__((PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>::kR
           tbl_next = k < my_pieces ? bal_entry(k, &pk_next) : 0;
         } else {
           crd_cur = coord_of(tbl_next, ip + lane);
-          tbl_next = k < my_pieces && stored(k) ? __ldg(table + piece_row(k) / p.block_size) : 0;
+          tbl_next = k < my_pieces && stored(k) ? table[piece_row(k) / p.block_size] : 0;
         }
       }
       // row: the first piece's coordinate, -1 when a stored piece has a bad block id

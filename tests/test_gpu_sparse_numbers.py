@@ -156,3 +156,36 @@ def test_a_budget_beyond_the_table(bits, width, top_k):
     vmax = float(rows[1].float().abs().max())
     for o in (out, apart):
         assert ((o.float() - dense.float()).abs() <= 2.0 ** -7 * dense.float().abs() + 2.0 ** -7 * vmax).all()
+
+
+@pytest.mark.parametrize("hk,pages", [(2, 60), (8, 1200)])  # one launch of the choice, and two
+def test_choices_that_change_from_step_to_step_in_one_workspace(hk, pages):
+    # the attention starts beside the choice whose tables it reads, in the memory of the last step's
+    g = torch.Generator(device=DEV).manual_seed(pages)
+    seqs, hq, d, bs, top_k, steps = 3, 2 * hk, 128, 16, 24, 60
+    rows = torch.randn((2, seqs * pages, hk, bs, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    tables = torch.randperm(seqs * pages, generator=g, device=DEV, dtype=torch.int32).view(seqs, pages)
+    lens = i32([pages * bs, pages * bs - 5, (pages - 7) * bs])
+    bounds = torch.empty((seqs * pages, hk, 2, d), dtype=torch.bfloat16, device=DEV)
+    B.update_block_bounds(rows[0], tables, lens, bounds, n_new=pages * bs)
+    q = torch.randn((steps, seqs, hq, 1, d), generator=g, device=DEV, dtype=torch.bfloat16)
+    call = lambda i, **kw: B.sparse_decode_attention(q[i], rows[0], rows[1], bounds, tables, lens, 0.3, top_k=top_k, **kw)
+    want = []
+    for i in range(steps):
+        want.append(call(i))
+        torch.cuda.synchronize()
+    got = torch.empty_like(q)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    for i in range(steps):
+        call(i, out=got[i], workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i], want[i]) for i in range(steps))
+    got.zero_()
+    with torch.cuda.graph(graph):
+        for i in range(steps):
+            call(i, out=got[i], workspace=ws)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i], want[i]) for i in range(steps))
