@@ -431,6 +431,7 @@ class HostDecodeStep:
                  workspace: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None, stream=None,
                  copy_tables: bool = True, contraction: int = 0, schedule: int = 0):
         self.lib = lib = load_library()
+        _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
         dev = k_pool.device
         B, HQ, N, D = q.shape
         self.layout = layout_for(k_pool, D, bits, group_size, v_pool)
@@ -554,6 +555,7 @@ def paged_decode_passes(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     ``"merge"`` (pkv_merge_partitions). ``out`` and, with more than one
     partition, ``workspace`` must be given so the two calls share them."""
     lib = load_library()
+    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
     B, HQ, N, D = q.shape
     layout = layout_for(k_pool, D, bits, group_size, v_pool)
     params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule)

@@ -70,6 +70,16 @@ def test_scales_of_e4m3_pages(call, args, scale, error):
             call(**args(**{name: scale}))
 
 
+@pytest.mark.parametrize("scale,error", [(torch.ones(NB, HK, dtype=torch.bfloat16), TypeError),
+                                         (scales(NB, HK, BS, 2), ValueError), (scales(NB - 1, HK), ValueError)])
+@pytest.mark.parametrize("call,more", [(B.HostDecodeStep, {}), (B.paged_decode_passes, dict(passes="partial"))])
+def test_scales_of_e4m3_pages_in_prepared_steps_and_single_passes(call, more, scale, error):
+    # 16-bit planes, such as affine pages have, would be read as f32 past their end
+    for name in ("k_scales", "v_scales"):
+        with pytest.raises(error, match="e4m3"):
+            call(**decode(**{name: scale}, **more))
+
+
 def test_pools_of_another_format():
     # a pool whose rows hold fewer bytes than the format's would be read past its end
     with pytest.raises(ValueError, match="k_pool"):
