@@ -310,8 +310,14 @@ def _remember(key, call):
     return call
 
 
-def _check_block_scales(k_pool, bits: int, group_size: int, *scales) -> None:
+_E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _check_block_scales(k_pool, v_pool, bits: int, group_size: int, *scales) -> None:
     if bits == 8 and group_size == PKV_GROUP_BLOCK:
+        for pool in (k_pool, v_pool):
+            if pool is not None and pool.dtype not in _E4M3_DTYPES:
+                raise TypeError(f"e4m3 pages are float8_e4m3fn (or uint8) codes, not {pool.dtype}")
         cells = k_pool.shape[:2]
         for s in scales:
             if s is None:
@@ -356,7 +362,7 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     CUDA stream of q's device and returns bf16 [B, HQ, N, D].
     """
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
         call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
@@ -431,7 +437,7 @@ class HostDecodeStep:
                  workspace: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None, stream=None,
                  copy_tables: bool = True, contraction: int = 0, schedule: int = 0):
         self.lib = lib = load_library()
-        _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+        _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
         dev = k_pool.device
         B, HQ, N, D = q.shape
         self.layout = layout_for(k_pool, D, bits, group_size, v_pool)
@@ -555,7 +561,7 @@ def paged_decode_passes(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     ``"merge"`` (pkv_merge_partitions). ``out`` and, with more than one
     partition, ``workspace`` must be given so the two calls share them."""
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     B, HQ, N, D = q.shape
     layout = layout_for(k_pool, D, bits, group_size, v_pool)
     params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule)
@@ -583,7 +589,7 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
     """Writes k_new/v_new bf16 [B, HK, n_new, D] at positions seq_lens[b].. of each
     sequence (quantising affine and e4m3 pages); see include/pkv_decode.h."""
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     B, HK, n_new, D = k_new.shape
     key = ("append", k_new.get_device(), k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, D, bits, group_size)
     call = _calls.get(key)
@@ -655,7 +661,7 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
     up to date after the last n_new rows of every sequence were appended (seq_lens counts
     them); see include/pkv_decode.h. Returns k_bounds."""
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales)
+    _check_block_scales(k_pool, None, bits, group_size, k_scales)
     key = ("bounds", k_bounds.get_device(), k_pool.shape, k_pool.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
            block_tables.dtype, seq_lens.shape, seq_lens.dtype, bits, group_size)
     call = _calls.get(key)
@@ -747,7 +753,7 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     """Decode attention over chosen blocks (pkv_selected_decode_attention); otherwise as
     ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     tables, lens = selection.tables, selection.lens
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
@@ -801,7 +807,7 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     last always among them (pkv_sparse_decode_attention). ``blocks`` int32 [B, HK, top_k]
     receives the choice. Otherwise as ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(k_pool, bits, group_size, k_scales, v_scales)
+    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
         stream = _raw_stream(q.get_device())
         key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, k_bounds.shape,

@@ -80,6 +80,19 @@ def test_scales_of_e4m3_pages_in_prepared_steps_and_single_passes(call, more, sc
             call(**decode(**{name: scale}, **more))
 
 
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int32])
+@pytest.mark.parametrize("call,args,more", [
+    (B.paged_decode_attention, decode, {}), (B.paged_append, append, {}), (B.HostDecodeStep, decode, {}),
+    (B.paged_decode_passes, decode, dict(passes="partial")), (B.sparse_decode_attention, sparse, {}),
+    (B.selected_decode_attention, selected, {}), (B.update_block_bounds, bounds, dict(k_scales=scales(NB, HK), **E4M3))])
+def test_codes_of_another_float8_type(call, args, more, dtype):
+    # their bytes would be read as e4m3fn codes
+    for name in ("k_pool", "v_pool")[:1 if call is B.update_block_bounds else 2]:
+        pool = torch.zeros(NB, HK, BS, D // (4 if dtype is torch.int32 else 1), dtype=dtype)
+        with pytest.raises(TypeError, match="e4m3"):
+            call(**{**args(**more), name: pool})
+
+
 def test_pools_of_another_format():
     # a pool whose rows hold fewer bytes than the format's would be read past its end
     with pytest.raises(ValueError, match="k_pool"):
