@@ -310,6 +310,29 @@ def _remember(key, call):
     return call
 
 
+def _require(dtype: torch.dtype, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _check_tensors(index: int, *tensors) -> None:
+    """All contiguous and on device `index`."""
+    for t in tensors:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on one device")
+
+
+def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)}, not {list(t.shape)}")
+
+
+def _types(tensors) -> tuple:
+    """Shapes and types, for a key."""
+    return tuple([(t.shape, t.dtype) for t in tensors if t is not None])
+
+
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -328,13 +351,28 @@ def _check_block_scales(k_pool, v_pool, bits: int, group_size: int, *scales) -> 
                 raise ValueError("scales of e4m3 pages are contiguous [num_blocks, num_kv_heads] planes")
 
 
-def _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
-                 schedule) -> _Call:
-    """Cached by what settles the call; runs with q's device current."""
+def _require_decode_shapes(q, k_pool, v_pool, block_tables, seq_lens) -> None:
+    """Types and shapes of a decode call over e4m3 pages (k_pool's rows are checked by layout_for)."""
+    _require(torch.bfloat16, q=q)
+    _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+    _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
+    _require_shape("block_tables", block_tables, q.shape[0], block_tables.shape[-1])
+    _require_shape("seq_lens", seq_lens, q.shape[0])
+
+
+def _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction, schedule,
+                 e4m3=None) -> _Call:
+    """Cached by what settles the call; runs with q's device current. e4m3: of such pages, what
+    else is checked (seq_lens, k_scales, v_scales)."""
     key = (q.get_device(), q.shape, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, block_tables.shape, bits, group_size,
            partition_tokens, window, contraction, schedule)
+    if e4m3 is not None:
+        key += (q.dtype, block_tables.dtype) + _types(e4m3)
     call = _calls.get(key)
     if call is None:
+        if e4m3 is not None:
+            _check_block_scales(k_pool, v_pool, bits, group_size, *e4m3[1:])
+            _require_decode_shapes(q, k_pool, v_pool, block_tables, e4m3[0])
         B, HQ, N, D = q.shape
         call = _Call(layout_for(k_pool, D, bits, group_size, v_pool),
                      DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule), q)
@@ -362,15 +400,22 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     CUDA stream of q's device and returns bf16 [B, HQ, N, D].
     """
     lib = load_library()
-    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
+    e4m3 = (seq_lens, k_scales, v_scales) if group_size == PKV_GROUP_BLOCK and bits == 8 else None
     with _on_device(q.device):
-        stream = _raw_stream(q.get_device())
         call = _decode_call(q, k_pool, v_pool, block_tables, bits, group_size, partition_tokens, window, contraction,
-                            schedule)
+                            schedule, e4m3)
+        index = q.get_device()
+        if e4m3 is not None:
+            _check_tensors(index, q, k_pool, v_pool, block_tables, seq_lens, k_scales, v_scales, out, workspace,
+                           error_flag)
+            if out is not None:
+                _require(torch.bfloat16, out=out)
+                _require_shape("out", out, *call.out_shape)
+        stream = _raw_stream(index)
         if out is None:
             out = call.new_out(q)
         if workspace is None and call.workspace_bytes:
-            workspace = _workspaces.get(q.device, q.get_device(), stream, call.workspace_bytes)
+            workspace = _workspaces.get(q.device, index, stream, call.workspace_bytes)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.pkv_paged_decode_attention(
             call.layout_ref, call.params_ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
@@ -439,6 +484,9 @@ class HostDecodeStep:
         self.lib = lib = load_library()
         _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
         dev = k_pool.device
+        if group_size == PKV_GROUP_BLOCK and bits == 8:
+            _require_decode_shapes(q, k_pool, v_pool, block_tables, seq_lens)
+            _check_tensors(k_pool.get_device(), k_pool, v_pool, k_scales, v_scales, workspace, error_flag)
         B, HQ, N, D = q.shape
         self.layout = layout_for(k_pool, D, bits, group_size, v_pool)
         self.params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction,
@@ -541,12 +589,13 @@ _stay = _Stay()
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_device(device: torch.device):
-    index = device.index
-    if index is None:
-        return _stay
+def _on_index(index: int):
     cur = _current_device()
     return _stay if cur == index else _Switch(index, cur)
+
+
+def _on_device(device: torch.device):
+    return _stay if device.index is None else _on_index(device.index)
 
 
 def paged_decode_passes(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -562,6 +611,13 @@ def paged_decode_passes(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     partition, ``workspace`` must be given so the two calls share them."""
     lib = load_library()
     _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
+    if group_size == PKV_GROUP_BLOCK and bits == 8:
+        _require_decode_shapes(q, k_pool, v_pool, block_tables, seq_lens)
+        _check_tensors(q.get_device(), q, k_pool, v_pool, block_tables, seq_lens, k_scales, v_scales, out, workspace,
+                       error_flag)
+        if out is not None:
+            _require(torch.bfloat16, out=out)
+            _require_shape("out", out, *q.shape[:-1], v_head_dim_of(v_pool, bits))
     B, HQ, N, D = q.shape
     layout = layout_for(k_pool, D, bits, group_size, v_pool)
     params = DecodeParams(B, HQ, N, block_tables.shape[1], partition_tokens, window, contraction, schedule)
@@ -589,17 +645,32 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
     """Writes k_new/v_new bf16 [B, HK, n_new, D] at positions seq_lens[b].. of each
     sequence (quantising affine and e4m3 pages); see include/pkv_decode.h."""
     lib = load_library()
-    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
+    index, tables = k_new.get_device(), block_tables.shape
     B, HK, n_new, D = k_new.shape
-    key = ("append", k_new.get_device(), k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, D, bits, group_size)
+    key = ("append", index, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, D, bits, group_size)
+    e4m3 = group_size == PKV_GROUP_BLOCK and bits == 8
+    if e4m3:
+        key += _types((k_new, v_new, block_tables, seq_lens, k_scales, v_scales))
     call = _calls.get(key)
     if call is None:
+        if e4m3:
+            _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
+            _require(torch.bfloat16, k_new=k_new, v_new=v_new)
+            _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+            _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
+            _require_shape("k_new", k_new, B, k_pool.shape[1], n_new, D)
+            _require_shape("v_new", v_new, B, k_pool.shape[1], n_new, v_head_dim_of(v_pool, bits))
+            _require_shape("block_tables", block_tables, B, tables[-1])
+            _require_shape("seq_lens", seq_lens, B)
+            _check_tensors(index, k_new, v_new, block_tables, seq_lens, k_pool, v_pool)
         call = _remember(key, _Call(layout_for(k_pool, D, bits, group_size, v_pool), DecodeParams(), k_new))
-    with _on_device(k_new.device):
-        rc = lib.pkv_paged_append(call.layout_ref, B, block_tables.shape[1], n_new, k_new.data_ptr(), v_new.data_ptr(),
+    if e4m3:
+        _check_tensors(index, k_new, v_new, block_tables, seq_lens, k_pool, v_pool, k_scales, v_scales, error_flag)
+    with _on_index(index):
+        rc = lib.pkv_paged_append(call.layout_ref, B, tables[1], n_new, k_new.data_ptr(), v_new.data_ptr(),
                                   block_tables.data_ptr(), seq_lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                   _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), _ptr(error_flag),
-                                  _raw_stream(k_new.get_device()))
+                                  _raw_stream(index))
     if rc != PKV_OK:
         _check(rc, lib)
 
@@ -633,24 +704,6 @@ def make_sparse_plan(layout: PoolLayout, params: DecodeParams, sparse: SparsePar
         rc = lib.pkv_make_sparse_plan(*args, sm_count, ctypes.byref(plan))
     _check(rc, lib)
     return plan
-
-
-def _require(dtype: torch.dtype, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-
-
-def _check_tensors(index: int, *tensors) -> None:
-    """All contiguous and on device `index`."""
-    for t in tensors:
-        if t is not None and not (t.is_contiguous() and t.get_device() == index):
-            raise ValueError("tensors must be contiguous and on one device")
-
-
-def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be of shape {list(shape)}, not {list(t.shape)}")
 
 
 def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,

@@ -93,6 +93,71 @@ def test_codes_of_another_float8_type(call, args, more, dtype):
             call(**{**args(**more), name: pool})
 
 
+V_POOLS = [codes(NB - 1, HK, BS, D), codes(NB, HK, BS // 2, D), codes(NB, 1, BS, D), codes(NB + 1, HK, BS, D)]
+
+
+@pytest.mark.parametrize("wrong,error", [(dict(v_pool=p), ValueError) for p in V_POOLS] + [
+    (dict(q=torch.zeros(3, 4, 1, D)), TypeError), (dict(seq_lens=torch.zeros(3, dtype=torch.int64)), TypeError),
+    (dict(block_tables=torch.zeros(3, 2, dtype=torch.int64)), TypeError), (dict(block_tables=i32(2, 2)), ValueError),
+    (dict(seq_lens=i32(2)), ValueError)])
+@pytest.mark.parametrize("call,more", [(B.paged_decode_attention, {}), (B.HostDecodeStep, {}),
+                                       (B.paged_decode_passes, dict(passes="partial"))])
+def test_shapes_and_types_of_decode_calls_over_e4m3_pages(call, more, wrong, error):
+    with pytest.raises(error, match=next(iter(wrong))):
+        call(**decode(**wrong, **more))
+
+
+@pytest.mark.parametrize("wrong,error", [(dict(v_pool=p), ValueError) for p in V_POOLS] + [
+    (dict(k_new=torch.zeros(3, HK, 1, D)), TypeError), (dict(v_new=torch.zeros(3, HK, 1, D)), TypeError),
+    (dict(v_new=bf16(3, HK, 1, D // 2)), ValueError), (dict(v_new=bf16(3, HK, 2, D)), ValueError),
+    (dict(v_new=bf16(2, HK, 1, D)), ValueError), (dict(k_new=bf16(3, 1, 1, D), v_new=bf16(3, 1, 1, D)), ValueError),
+    (dict(seq_lens=torch.zeros(3, dtype=torch.int64)), TypeError), (dict(seq_lens=i32(4)), ValueError),
+    (dict(block_tables=torch.zeros(3, 2, dtype=torch.int64)), TypeError), (dict(block_tables=i32(4, 2)), ValueError)])
+def test_shapes_and_types_of_appends_into_e4m3_pages(wrong, error):
+    with pytest.raises(error, match=next(iter(wrong))):
+        B.paged_append(**append(**wrong))
+
+
+@pytest.mark.parametrize("call,args,name,like", [
+    (B.paged_append, append, "k_new", bf16(1, HK, 1, D).expand(3, HK, 1, D)),
+    (B.paged_append, append, "v_new", bf16(3, HK, 1, 2 * D)[..., ::2]),
+    (B.paged_append, append, "v_pool", codes(1, HK, BS, D).expand(NB, HK, BS, D)),
+    (B.paged_append, append, "seq_lens", i32(1).expand(3)),
+    (B.paged_decode_passes, decode, "q", bf16(1, 4, 1, D).expand(3, 4, 1, D)),
+    (B.paged_decode_passes, decode, "block_tables", i32(3, 4)[:, ::2]),
+    (B.HostDecodeStep, decode, "k_pool", codes(NB, HK, BS, 2 * D)[..., ::2])])
+def test_strided_tensors_of_calls_over_e4m3_pages(call, args, name, like):
+    # an expanded tensor holds fewer values than the kernel would read
+    more = dict(passes="partial") if call is B.paged_decode_passes else {}
+    with pytest.raises(ValueError, match="contiguous"):
+        call(**args(**{name: like}, **more))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call,args,name", [(B.paged_append, append, n) for n in ("v_new", "seq_lens", "k_scales", "v_pool")] +
+                         [(B.paged_decode_attention, decode, n) for n in ("seq_lens", "v_scales", "v_pool", "block_tables")])
+def test_e4m3_calls_with_a_tensor_on_the_host_or_strided(call, args, name):
+    right = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in args().items()}
+    call(**right)  # its shapes are remembered
+    with pytest.raises(ValueError, match="one device"):
+        call(**{**right, name: right[name].cpu()})
+    if name != "seq_lens":
+        wide = torch.stack([right[name], right[name]], -1)[..., 0]
+        with pytest.raises(ValueError, match="contiguous"):
+            call(**{**right, name: wide})
+    with pytest.raises((TypeError, ValueError)):
+        call(**{**right, "seq_lens": right["seq_lens"].long()})
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wrong,error", [(dict(out=bf16(3, 4, 1, D // 2)), ValueError), (dict(out=torch.zeros(3, 4, 1, D)), TypeError)])
+def test_outputs_of_e4m3_decode_calls(wrong, error):
+    right = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in decode().items()}
+    with pytest.raises(error, match="out"):
+        B.paged_decode_attention(**right, **{k: v.cuda() for k, v in wrong.items()})
+
+
 def test_pools_of_another_format():
     # a pool whose rows hold fewer bytes than the format's would be read past its end
     with pytest.raises(ValueError, match="k_pool"):
