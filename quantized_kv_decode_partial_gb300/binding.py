@@ -330,7 +330,7 @@ def _require_shape(name: str, t: Optional[torch.Tensor], *shape: int) -> None:
 
 def _types(tensors) -> tuple:
     """Shapes and types, for a key."""
-    return tuple([(t.shape, t.dtype) for t in tensors if t is not None])
+    return tuple([None if t is None else (t.shape, t.dtype) for t in tensors])
 
 
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
@@ -349,6 +349,17 @@ def _check_block_scales(k_pool, v_pool, bits: int, group_size: int, *scales) -> 
                 raise TypeError(f"scales of e4m3 pages are float32 [num_blocks, num_kv_heads], not {s.dtype}")
             if s.shape != cells or not s.is_contiguous():
                 raise ValueError("scales of e4m3 pages are contiguous [num_blocks, num_kv_heads] planes")
+
+
+def _check_planes(k_pool, v_pool, bits: int, group_size: int, k_dim: int, **planes) -> None:
+    """The scale and bias planes of pages of codes; affine ones are bf16 [NB, HK, BS, D / 64]."""
+    if bits == 8 and group_size == PKV_GROUP_BLOCK:
+        _check_block_scales(k_pool, v_pool, bits, group_size, planes.get("k_scales"), planes.get("v_scales"))
+    elif bits != 16:
+        _require(torch.bfloat16, **planes)
+        for name, t in planes.items():
+            d = k_dim if name[0] == "k" else v_head_dim_of(v_pool, bits)
+            _require_shape(name, t, *k_pool.shape[:3], d // 64)
 
 
 def _require_decode_shapes(q, k_pool, v_pool, block_tables, seq_lens) -> None:
@@ -714,14 +725,16 @@ def update_block_bounds(k_pool: torch.Tensor, block_tables: torch.Tensor, seq_le
     up to date after the last n_new rows of every sequence were appended (seq_lens counts
     them); see include/pkv_decode.h. Returns k_bounds."""
     lib = load_library()
-    _check_block_scales(k_pool, None, bits, group_size, k_scales)
     key = ("bounds", k_bounds.get_device(), k_pool.shape, k_pool.dtype, k_bounds.shape, k_bounds.dtype, block_tables.shape,
            block_tables.dtype, seq_lens.shape, seq_lens.dtype, bits, group_size)
+    if bits != 16:
+        key += _types((k_scales, k_biases))
     call = _calls.get(key)
     if call is None:
+        D = k_pool.shape[-1] * k_pool.element_size() * 8 // bits
+        _check_planes(k_pool, None, bits, group_size, D, k_scales=k_scales, k_biases=k_biases)
         _require(torch.bfloat16, k_bounds=k_bounds)
         _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
-        D = k_pool.shape[-1] * k_pool.element_size() * 8 // bits
         _require_shape("k_bounds", k_bounds, k_pool.shape[0], k_pool.shape[1], 2, D)
         _require_shape("seq_lens", seq_lens, block_tables.shape[0])
         layout = layout_for(k_pool, D, bits, group_size)
@@ -806,15 +819,17 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     """Decode attention over chosen blocks (pkv_selected_decode_attention); otherwise as
     ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     tables, lens = selection.tables, selection.lens
     with _on_device(q.device):
-        stream = _raw_stream(q.get_device())
         key = ("selected", q.get_device(), q.shape, q.dtype, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, tables.shape,
                tables.dtype, lens.shape, lens.dtype, bits, group_size, partition_tokens, contraction, schedule)
+        if bits != 16:
+            key += _types((k_scales, k_biases, v_scales, v_biases))
         call = _calls.get(key)
         if call is None:
             B, HQ, N, D = q.shape
+            _check_planes(k_pool, v_pool, bits, group_size, D, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
+                          v_biases=v_biases)
             layout = layout_for(k_pool, D, bits, group_size, v_pool)
             top_k = tables.shape[-1]
             _require(torch.bfloat16, q=q)
@@ -829,6 +844,7 @@ def selected_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
             _remember(key, call)
         _check_tensors(q.get_device(), q, k_pool, v_pool, tables, lens, k_scales, k_biases, v_scales, v_biases, out,
                        workspace, error_flag)
+        stream = _raw_stream(q.get_device())
         if out is None:
             out = call.new_out(q)
         else:
@@ -860,16 +876,18 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     last always among them (pkv_sparse_decode_attention). ``blocks`` int32 [B, HK, top_k]
     receives the choice. Otherwise as ``paged_decode_attention``."""
     lib = load_library()
-    _check_block_scales(k_pool, v_pool, bits, group_size, k_scales, v_scales)
     with _on_device(q.device):
-        stream = _raw_stream(q.get_device())
         key = ("sparse", q.get_device(), q.shape, q.dtype, k_pool.shape, k_pool.dtype, v_pool.shape, v_pool.dtype, k_bounds.shape,
                k_bounds.dtype, block_tables.shape, block_tables.dtype, seq_lens.shape, seq_lens.dtype,
                None if blocks is None else (blocks.shape, blocks.dtype), bits, group_size, partition_tokens,
                contraction, schedule, top_k, first_blocks, last_blocks)
+        if bits != 16:
+            key += _types((k_scales, k_biases, v_scales, v_biases))
         call = _calls.get(key)
         if call is None:
             B, HQ, N, D = q.shape
+            _check_planes(k_pool, v_pool, bits, group_size, D, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
+                          v_biases=v_biases)
             layout = layout_for(k_pool, D, bits, group_size, v_pool)
             _require(torch.bfloat16, q=q, k_bounds=k_bounds)
             _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens, blocks=blocks)
@@ -884,6 +902,7 @@ def sparse_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
             _remember(key, call)
         _check_tensors(q.get_device(), q, k_pool, v_pool, k_bounds, block_tables, seq_lens, blocks, out, k_scales, k_biases,
                        v_scales, v_biases, workspace, error_flag)
+        stream = _raw_stream(q.get_device())
         if out is None:
             out = call.new_out(q)
         else:

@@ -158,6 +158,38 @@ def test_outputs_of_e4m3_decode_calls(wrong, error):
         B.paged_decode_attention(**right, **{k: v.cuda() for k, v in wrong.items()})
 
 
+def affine(args, bits, **kw):
+    words, d = lambda: i32(NB, HK, BS, D * bits // 32), D // 64
+    a = args(k_pool=words(), bits=bits, group_size=64, k_scales=bf16(NB, HK, BS, d), k_biases=bf16(NB, HK, BS, d))
+    if args is not bounds:
+        a.update(v_pool=words(), v_scales=bf16(NB, HK, BS, d), v_biases=bf16(NB, HK, BS, d))
+    return {**a, **kw}
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("plane,error", [(torch.zeros(NB, HK, BS, D // 64), TypeError), (bf16(NB, HK, BS, 1), ValueError),
+                                         (bf16(NB, HK), ValueError), (bf16(NB - 1, HK, BS, D // 64), ValueError)])
+@pytest.mark.parametrize("call,args", [(B.sparse_decode_attention, sparse), (B.selected_decode_attention, selected),
+                                       (B.update_block_bounds, bounds)])
+def test_planes_of_affine_pages_in_sparse_calls(call, args, plane, error, bits):
+    for name in ("k_scales", "k_biases", "v_scales", "v_biases")[:2 if args is bounds else 4]:
+        with pytest.raises(error, match=name):
+            call(**affine(args, bits, **{name: plane}))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call,args", [(B.sparse_decode_attention, sparse), (B.selected_decode_attention, selected),
+                                       (B.update_block_bounds, bounds)])
+def test_sparse_calls_over_affine_pages_with_remembered_shapes(call, args):
+    right = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in affine(args, 4).items()}
+    if "selection" in right:
+        right["selection"] = B.BlockSelection(*(t.cuda() for t in right["selection"]))
+    call(**right)
+    with pytest.raises(ValueError, match="k_scales"):
+        call(**{**right, "k_scales": bf16(NB, HK, BS, 1).cuda()})
+    torch.cuda.synchronize()
+
+
 def test_pools_of_another_format():
     # a pool whose rows hold fewer bytes than the format's would be read past its end
     with pytest.raises(ValueError, match="k_pool"):
