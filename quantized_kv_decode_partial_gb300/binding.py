@@ -3,7 +3,7 @@
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, and PyTorch allocates the output and
 the workspace (held between calls on the default stream, one per host thread
-and device). Every step of the computation runs in the library's kernels;
+and device, up to 32 MB). Every step of the computation runs in the library's kernels;
 there is no fallback, and a missing library raises ``LibraryNotBuilt``.
 """
 
@@ -261,13 +261,16 @@ class _Workspaces(threading.local):
     """The default stream's workspaces of one host thread, a growing one per device. Calls on
     that stream run one after the other, and the launches of one thread's call are not mixed
     with another call's, so they may share it; a call on any other stream (a captured one
-    among them) gets a workspace of its own."""
+    among them) gets a workspace of its own. So does one that needs more than MOST_HELD: a step
+    that large hides what the allocator takes, and its memory goes back when it returns."""
+
+    MOST_HELD = 32 << 20
 
     def __init__(self):
         self.held = {}
 
     def get(self, device: torch.device, index: int, stream: int, nbytes: int) -> torch.Tensor:
-        if stream != 0:
+        if stream != 0 or nbytes > self.MOST_HELD:
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws = self.held.get(index)
         if ws is None or ws.numel() < nbytes:

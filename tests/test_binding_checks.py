@@ -190,6 +190,29 @@ def test_sparse_calls_over_affine_pages_with_remembered_shapes(call, args):
     torch.cuda.synchronize()
 
 
+def test_workspaces_are_held_up_to_a_bound():
+    ws, cpu = B._Workspaces(), torch.device("cpu")
+    small = ws.get(cpu, 0, 0, 1000)
+    assert ws.get(cpu, 0, 0, 10) is small and ws.get(cpu, 0, 7, 10) is not small
+    grown = ws.get(cpu, 0, 0, ws.MOST_HELD)
+    assert grown.numel() == ws.MOST_HELD and ws.get(cpu, 0, 0, 1000) is grown
+    large = ws.get(cpu, 0, 0, ws.MOST_HELD + 1)
+    assert large.numel() == ws.MOST_HELD + 1 and ws.held == {0: grown}
+
+
+@pytest.mark.gpu
+def test_a_large_step_gives_its_workspace_back():
+    # 64 sequences whose tables could hold 262144 blocks of scores: about 200 MB for this one call
+    call = lambda width: B.select_blocks(bf16(64, 4, 1, 64).cuda(), bf16(4, 1, 2, 64).cuda(), i32(64, width).cuda(),
+                                         torch.ones(64, dtype=torch.int32, device="cuda"), block_size=32, top_k=4)
+    call(8)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    call(1 << 18)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() <= before + B._Workspaces.MOST_HELD
+
+
 def test_pools_of_another_format():
     # a pool whose rows hold fewer bytes than the format's would be read past its end
     with pytest.raises(ValueError, match="k_pool"):
