@@ -1242,7 +1242,8 @@ int pkv_update_block_bounds(const pkv_pool_layout* layout, int32_t num_seqs, int
   p.block_size = layout->block_size;
   p.max_blocks = max_blocks_per_seq;
   p.n_new = static_cast<int>(std::min<long long>(n_new, max_len));
-  p.blocks = std::min((layout->block_size - 2 + p.n_new) / layout->block_size + 1, max_blocks_per_seq);
+  const long long touched = (layout->block_size - 2ll + p.n_new) / layout->block_size + 1;
+  p.blocks = static_cast<int>(std::min<long long>(touched, max_blocks_per_seq));
   if (static_cast<long long>(p.blocks) * layout->num_kv_heads >= (1ll << 31) - 4) return PKV_ERR_BAD_PARAMS;
   (void)cudaGetLastError();
   cudaError_t e = pkv::launch_bounds(p, format_of(layout), layout->head_dim, num_seqs,

@@ -1,5 +1,7 @@
 """The choice of blocks and the block bounds at the edges of their numbers."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -189,3 +191,18 @@ def test_choices_that_change_from_step_to_step_in_one_workspace(hk, pages):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(got[i], want[i]) for i in range(steps))
+
+
+def test_bounds_rebuilt_in_tables_of_nearly_2_31_rows():
+    # "at least every length" said with the largest number there is; the rows past the length are not there
+    d, bs, length = 128, 2 ** 30 - 32, 40
+    k = torch.randn((1, 1, 64, d), device=DEV).to(torch.bfloat16)
+    bounds = torch.zeros((1, 1, 2, d), dtype=torch.bfloat16, device=DEV)
+    tables, lens, lib = i32([[0, 0]]), i32([length]), B.load_library()
+    layout = B.PoolLayout(1, 1, bs, d, 16, 64, 0)
+    rc = lib.pkv_update_block_bounds(ctypes.byref(layout), 1, 2, 2 ** 31 - 1, k.data_ptr(), None, None, tables.data_ptr(),
+                                     lens.data_ptr(), bounds.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    rows = k[0, 0, :length].float()
+    assert torch.equal(bounds[0, 0].float(), torch.stack([rows.amin(0), rows.amax(0)]))
