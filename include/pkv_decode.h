@@ -157,8 +157,9 @@ typedef struct pkv_decode_params {
   int32_t schedule;           /* how the rows are split over the CTAs, when partition_tokens = 0:
                                  PKV_SCHEDULE_AUTO (0): balanced for 4-bit pages, and for e4m3
                                  pages with more than 8 query rows per KV head, rows *
-                                 (head_dim + v_head_dim) > 2048 and a table of more than
-                                 8192 cache rows, where the plan
+                                 (head_dim + v_head_dim) > 2048, a table of more than
+                                 8192 cache rows and enough sequences and heads that
+                                 each has few of the GPU's runs, where the plan
                                  would otherwise write partition states to the workspace, else
                                  partitions;
                                  PKV_SCHEDULE_PARTITIONS (1): fixed-size partitions of every

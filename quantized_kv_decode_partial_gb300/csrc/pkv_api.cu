@@ -336,9 +336,24 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
   // 63.4, 32 rows 131.1 -> 96.9; D=256: 8 rows 165.3 -> 176.8, 16 rows 252.6 -> 239.6; 64
   // sequences of up to 32768 rows, D=128, 16 rows: 383.0 -> 355.3). Tables of up to 8192 rows
   // hold too few chunks per run (160 sequences of up to 8192 rows, D=128, 16 rows: 261.4 ->
-  // 268.4; 64 of up to 2000: 44.2 -> 52.1; 100 of up to 16384: 305.0 -> 293.7).
-  const bool bal_format = L->bits == 4 || (block_scaled(L) && nq > 8 && nq * (L->head_dim + v_dim(L)) > 8 * 256 &&
-                                           P->max_blocks_per_seq * static_cast<long long>(L->block_size) > 8192);
+  // 268.4; 64 of up to 2000: 44.2 -> 52.1; 100 of up to 16384: 305.0 -> 293.7). The merge reads a
+  // unit's runs in turn, so a few units are not spread over all of the GPU's: balanced needs 3 M
+  // products (rows * query rows * head dims) per warp, and 128 K for each run of a unit. Units of
+  // equal length, partitions -> balanced: D=128, 16 query rows, 1 unit of 16416 rows 10 -> 285 us,
+  // 8 of 32768 20 -> 66, 64 of 16416 53.2 -> 57.5, 64 of 32768 103.2 -> 98.4; 32 rows, 8 units of 131072 86 ->
+  // 102, 16 178 -> 161, 64 of 16416 88.5 -> 87.0; D=256, 16 rows, 32 units of 16416 67.0 -> 70.7, of 32768
+  // 128.7 -> 122.8; D=64, 32 rows, 64 units of 16416 64.7 -> 53.1, 16 of 131072 94.9 -> 103.0.
+  bool bal_format = L->bits == 4;
+  if (block_scaled(L) && nq > 8 && nq * (L->head_dim + v_dim(L)) > 8 * 256 && max_len > 8192) {
+    const PartialInfo bi = partial_info(format_of(L), L->head_dim, v_dim(L), static_cast<int>(nq), false, false, true);
+    if (bi.exists) {
+      const long long per_sm = std::max(1ll, std::min<long long>(bal_ctas_per_sm_bound(bi), 65536 / (bi.threads * bi.regs)));
+      const long long units = static_cast<long long>(P->num_seqs) * L->num_kv_heads;
+      const long long runs = sms * per_sm * bi.page_groups, warps = sms * per_sm * (bi.threads / 32);
+      const double per_warp = static_cast<double>(units) * window_rows(P, max_len) * nq * (L->head_dim + v_dim(L)) / warps;
+      bal_format = per_warp >= 3 << 20 && per_warp >= static_cast<double>(runs) / units * (128 << 10);
+    }
+  }
   out->balanced = 0;
   if (P->partition_tokens == 0 && P->schedule != PKV_SCHEDULE_PARTITIONS && !cc && !pieces &&
       P->num_seqs <= pkv::kMaxBalancedSeqs &&

@@ -19,6 +19,7 @@ struct PartialInfo {
   int box_row_bytes_v;  // ... of the V plane
   int tensor_elem_bytes;  // element size of the pool tensor maps (2 bf16, 1 affine codes)
   int page_groups;        // page groups per CTA (rings of stages, each read by its query-group warps)
+  int regs;               // most registers per thread it is compiled for
 };
 
 // Partial-kernel instantiation for key head dim dk, value head dim dv and `nq` query

@@ -13,7 +13,8 @@ namespace {
 template <int BITS, int D, int DV, int NT, int WQ, bool SOLO, int CCQ = 0, bool BAL = false>
 PartialInfo info_of() {
   using C = PartialCfg<BITS, D, DV, NT, WQ, SOLO, CCQ, BAL>;
-  return PartialInfo{true, C::kThreads, C::kSmemBytes, C::kCh, C::kRB, C::kRBV, C::kElemBytes, C::kWP};
+  return PartialInfo{true, C::kThreads, C::kSmemBytes, C::kCh, C::kRB, C::kRBV, C::kElemBytes, C::kWP,
+                     C::kRegs};
 }
 
 // Devices on which an instantiation's function attributes are set (bit per device < 64).

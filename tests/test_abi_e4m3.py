@@ -89,3 +89,20 @@ def test_partitions_fill_whole_waves(lib, seqs, rows, d, rep, parts):
                        B.DecodeParams(seqs, hk * rep, 1, blocks, 0, 0, 0, B.PKV_SCHEDULE_PARTITIONS), 152)
     assert plan.max_partitions == parts
     assert plan.partition_tokens * plan.max_partitions >= rows
+
+
+@pytest.mark.parametrize("d,nq,units,rows,balanced", [
+    # runs of a unit that the merge would read one after the other: 1824 runs over few units
+    (128, 16, 1, 16416, 0), (128, 16, 1, 131072, 0), (128, 16, 4, 32768, 0), (128, 32, 8, 131072, 0),
+    (256, 16, 1, 8224, 0), (256, 16, 16, 32768, 0), (64, 32, 2, 131072, 0), (64, 32, 16, 131072, 0),
+    # runs too short
+    (128, 16, 64, 16416, 0), (256, 16, 32, 16416, 0), (128, 32, 64, 8224, 0),
+    # many units of many rows
+    (128, 16, 64, 32768, 1), (128, 32, 64, 16416, 1), (128, 32, 16, 131072, 1), (256, 16, 32, 32768, 1),
+    (64, 32, 64, 16416, 1), (128, 16, 512, 32768, 1),
+])
+def test_balanced_schedule_where_units_have_few_runs(lib, d, nq, units, rows, balanced):
+    hk = 8 if units % 8 == 0 else 1
+    lay = B.PoolLayout(units // hk * rows // 32, hk, 32, d, 8, B.PKV_GROUP_BLOCK)
+    plan = B.make_plan(lay, B.DecodeParams(units // hk, hk * nq, 1, rows // 32), sm_count=152)
+    assert plan.balanced == balanced
