@@ -225,14 +225,18 @@ int plan_impl(const pkv_pool_layout* L, const pkv_decode_params* P, int sm_count
         }
       }
     }
-    // e4m3 pages: a grid of at most one CTA per SM with more partitions than a cluster
-    // holds takes 16 of them instead, while a CTA still reads no more than 256 KB: the
-    // merge then needs no second launch and no workspace (1 x 8192 rows of 256-dim heads,
-    // 32 -> 16 partitions: 9.1 -> 9.7 us on the GPU, 17.9 -> 13.0 us per call from the host).
-    if (block_scaled(L) && P->window == 0) {
+    // e4m3 pages, up to 8 query rows: a grid of at most one CTA per SM with more partitions
+    // than a cluster holds takes 16 of them instead, while a CTA's rows * (bytes + 256) are at most
+    // 400 K: the merge then needs no second launch and no workspace, which saves a call 3 to 4 us of
+    // host time and costs the GPU up to 0.7. From lengths on both sides (1 to 4 units, rows of a
+    // CTA, as planned else -> 16 partitions, in a graph; calls from the host 19.7 -> 16.4 throughout):
+    // D=256, 384 rows 9.1 -> 8.6 us, 512 9.1 -> 9.7, 768 10.0 -> 12.0; D=128, 384 rows 6.9 -> 6.3, 512
+    // 7.0 -> 6.7, 768 7.6 -> 7.9, 1024 7.8 -> 9.1; D=64, 768 rows 6.7 -> 6.6, 1024 6.8 -> 7.5; 16 query
+    // rows, D=128, 384 rows 8.2 -> 9.5, 512 8.4 -> 10.8.
+    if (block_scaled(L) && P->window == 0 && P->num_q_heads / L->num_kv_heads * P->n_query <= 8) {
       const long long parts = (span + part - 1) / part;
       const long long wide = round_up((span + pkv::kMaxClusterParts - 1) / pkv::kMaxClusterParts, ch);
-      if (parts > pkv::kMaxClusterParts && units * parts <= sm_count && wide * kv_row <= (256ll << 10)) part = wide;
+      if (parts > pkv::kMaxClusterParts && units * parts <= sm_count && wide * (kv_row + 256) <= 400ll << 10) part = wide;
     }
     // With a window, every sequence longer than it reads the same span, so the
     // (sequence, KV head) units carry even work. When the grid above is at most two

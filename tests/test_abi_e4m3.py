@@ -106,3 +106,13 @@ def test_balanced_schedule_where_units_have_few_runs(lib, d, nq, units, rows, ba
     lay = B.PoolLayout(units // hk * rows // 32, hk, 32, d, 8, B.PKV_GROUP_BLOCK)
     plan = B.make_plan(lay, B.DecodeParams(units // hk, hk * nq, 1, rows // 32), sm_count=152)
     assert plan.balanced == balanced
+
+
+@pytest.mark.parametrize("d,nq,hk,rows,cluster", [
+    (256, 4, 4, 6144, True), (256, 8, 1, 8192, True), (256, 4, 4, 8704, False), (256, 4, 2, 12288, False),
+    (128, 4, 2, 8192, True), (128, 8, 2, 12288, True), (128, 4, 2, 16384, False), (64, 4, 2, 16384, True),
+    (64, 4, 2, 24576, False), (128, 16, 1, 6144, False), (64, 9, 1, 12288, False)])
+def test_sixteen_partitions_in_a_cluster(lib, d, nq, hk, rows, cluster):
+    lay = B.PoolLayout(rows // 32, hk, 32, d, 8, B.PKV_GROUP_BLOCK)
+    plan = B.make_plan(lay, B.DecodeParams(1, hk * nq, 1, rows // 32), sm_count=152)
+    assert (plan.merge_in_cluster, plan.max_partitions == 16, plan.workspace_bytes == 0) == (cluster,) * 3
