@@ -397,7 +397,7 @@ int pkv_paged_append(const pkv_pool_layout* layout, int32_t num_seqs, int32_t ma
  * caller copies them first). A row whose block id is bad is neither written nor
  * read and sets PKV_DEVERR_BAD_BLOCK.
  * e4m3 pages are refused (PKV_ERR_UNSUPPORTED_SHAPE): a new row may rescale its whole
- * block, which other CTAs read. Call pkv_paged_append, then the decode. */
+ * block, which may span chunks that other CTAs read. Call pkv_paged_append, then the decode. */
 int pkv_paged_decode_append_attention(const pkv_pool_layout* layout, const pkv_decode_params* params,
                                       const void* q, const void* k_new, const void* v_new, void* k_pool,
                                       void* v_pool, void* k_scales, void* k_biases, void* v_scales,

@@ -928,7 +928,8 @@ __global__ void __launch_bounds__(T, 1024 / T) pkv_select_kernel(const __grid_co
 // Scores and choice of one unit by a cluster of 1 to 8 CTAs: each scores its share of the
 // tiles, one per warp, into the first CTA's shared memory, and that one chooses. One launch
 // less, and no trip of the scores through L2: 8 units of 1024 blocks (D=128, 4 query rows)
-// 11.4 -> 10.9 us on the GPU and 2.7 us less per call from the host. With several tiles per
+// 11.4 -> 10.9 us on the GPU (7.9 where no unit has blocks to sum exactly) and 2.7 us less per call
+// from the host. With several tiles per
 // warp or more than one wave of clusters the two kernels were faster (fused -> two: 64 units
 // of 626 blocks, D=256, 17.4 -> 15.7 us; 512 of up to 1024, 43.2 -> 39.8; 64 of 8192,
 // 64.6 -> 61.6).
