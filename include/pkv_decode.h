@@ -505,6 +505,88 @@ int pkv_sparse_decode_attention(const pkv_pool_layout* layout, const pkv_decode_
                                 const int32_t* seq_lens, float scale, int32_t* blocks, void* out, void* workspace,
                                 size_t workspace_bytes, int32_t* error_flag, void* stream);
 
+/* Norm and rotation: what turns a projection's query and key heads into the ones that
+ * attention takes, in one pass over them. The reference's attention takes finished heads;
+ * it has no counterpart of these calls. For each row x of D = head_dim values, in f32 with one rounding to
+ * bf16 at the end:
+ *     y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)    where the weight is given
+ *     (y_a, y_b) -> amplitude * (y_a cos w - y_b sin w, y_b cos w + y_a sin w)
+ * for the pairs (a, b) of the first rot_dims dims, w = position * inv_freq[i] for pair i.
+ * Dims from rot_dims on do not turn. Angles are reduced exactly: any int32 position, with an
+ * error below 2^-21 for |inv_freq| < 2 (finite frequencies; larger ones lose as many bits).
+ * The squares of a row must sum within f32's range. */
+#define PKV_PAIRS_HALVES 0    /* pair i is (i, i + rot_dims/2) */
+#define PKV_PAIRS_ADJACENT 1  /* pair i is (2i, 2i + 1) */
+
+/* Which axis of a position with several (time, height, width, ...) turns which frequency. */
+#define PKV_SECTIONS_BLOCKS 0 /* the first sections[0] by axis 0, the next sections[1] by axis 1, ... */
+#define PKV_SECTIONS_CYCLE 1  /* frequency i by axis a = i % num_axes while i < num_axes * sections[a],
+                                 else by axis 0 */
+
+#define PKV_MAX_AXES 4
+
+typedef struct pkv_rotation {
+  int32_t head_dim;      /* D: 64, 128, 192 or 256 */
+  int32_t rot_dims;      /* dims that turn: a multiple of 8, 8 .. head_dim */
+  int32_t pairing;       /* PKV_PAIRS_* */
+  int32_t num_axes;      /* 1 .. PKV_MAX_AXES */
+  int32_t section_order; /* PKV_SECTIONS_* (num_axes > 1) */
+  int32_t sections[PKV_MAX_AXES]; /* frequencies of each axis, >= 0, rot_dims/2 in all (num_axes > 1); with
+                                     PKV_SECTIONS_CYCLE each axis must find its count below rot_dims/2 */
+  int32_t weight_f32;    /* norm weights are f32, else bf16 */
+  float eps;             /* >= 0 */
+  float weight_offset;   /* 1 for weights stored less one, else 0 */
+  float amplitude;       /* factor on cos and sin, usually 1 */
+} pkv_rotation;
+
+/* Head h of token j of sequence b begins at element b*seq + j*token + h*head; a row's values are
+ * contiguous. Multiples of 8, >= 0; an output's rows must not overlap. Packed tokens
+ * (tokens_per_seq = 0) are counted through by `token` alone. */
+typedef struct pkv_row_strides {
+  int64_t seq, token, head;
+} pkv_row_strides;
+
+/* Norm and rotation alone.
+ *   q, k              bf16 rows of num_q_heads and num_kv_heads heads of num_seqs * tokens_per_seq
+ *                     tokens, 16-byte aligned (num_kv_heads = 0: no keys, k and k_out NULL)
+ *   q_weight, k_weight [head_dim], NULL: no norm of the queries or the keys
+ *   positions         int32 [num_axes][num_seqs * tokens_per_seq]
+ *   inv_freq          f32 [rot_dims/2]
+ *   q_out, k_out      bf16; may be q and k with the same strides
+ * Asynchronous on `stream`. No tokens: nothing is launched. */
+int pkv_norm_rotate(const pkv_rotation* rotation, int32_t num_seqs, int32_t tokens_per_seq, int32_t num_q_heads,
+                    int32_t num_kv_heads, const void* q, const pkv_row_strides* q_strides, const void* k,
+                    const pkv_row_strides* k_strides, const void* q_weight, const void* k_weight,
+                    const int32_t* positions, const float* inv_freq, void* q_out,
+                    const pkv_row_strides* q_out_strides, void* k_out, const pkv_row_strides* k_out_strides,
+                    void* stream);
+
+/* The same with the write: queries go to q_out, keys and values into their pages. What the
+ * pages then hold is bit for bit what pkv_norm_rotate followed by pkv_paged_append writes.
+ *   num_tokens        new tokens of all sequences
+ *   tokens_per_seq    tokens of each (num_tokens = num_seqs * tokens_per_seq), or 0: packed, and
+ *                     sequence b's are query_starts[b] .. query_starts[b+1] - 1
+ *   query_starts      int32 [num_seqs + 1], not falling, within 0 .. num_tokens (packed; else unused).
+ *                     Tokens outside [query_starts[0], query_starts[num_seqs]) are left alone, their
+ *                     q_out rows too. A sequence may have none.
+ *   v                 bf16 rows of v_head_dim values
+ *   positions         as above ([num_axes][num_tokens]), or NULL with one axis: the rows'
+ *                     places in the cache, seq_lens[b] + 0, 1, ...
+ *   seq_lens          rows held BEFORE the write
+ * Layouts, pools, planes, bad block ids and bad lengths (no row of that sequence is
+ * written) as pkv_paged_append; starts that fall or leave 0 .. num_tokens set
+ * PKV_DEVERR_BAD_SEQ_LEN. Queries are normed and rotated whatever becomes of their sequence's
+ * rows, except where their starts are bad. A block that receives rows must belong to one sequence only. */
+int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* rotation, int32_t num_seqs,
+                           int32_t num_tokens, int32_t tokens_per_seq, int32_t num_q_heads,
+                           int32_t max_blocks_per_seq, const void* q, const pkv_row_strides* q_strides, const void* k,
+                           const pkv_row_strides* k_strides, const void* v, const pkv_row_strides* v_strides,
+                           const void* q_weight, const void* k_weight, const int32_t* positions,
+                           const float* inv_freq, const int32_t* query_starts, const int32_t* block_tables,
+                           const int32_t* seq_lens, void* k_pool, void* v_pool, void* k_scales, void* k_biases,
+                           void* v_scales, void* v_biases, void* q_out, const pkv_row_strides* q_out_strides,
+                           int32_t* error_flag, void* stream);
+
 /* Bit-exact gather of one pool plane into contiguous per-sequence rows, the
  * fetch copy of the pages' BlockPool.gather / pickBlocks (state/paged/cache.ts):
  *   out[b][h][t][:] = pool[block_tables[b][t / block_size]][h][t % block_size][:]

@@ -37,6 +37,8 @@ EXPORTS = (
     "pkv_select_blocks",
     "pkv_selected_decode_attention",
     "pkv_sparse_decode_attention",
+    "pkv_norm_rotate",
+    "pkv_norm_rotate_append",
     "pkv_paged_gather",
     "pkv_strerror",
     "pkv_last_cuda_error",
@@ -64,6 +66,14 @@ PKV_CONTRACTION_CUDA_CORE = 2
 PKV_SCHEDULE_AUTO = 0
 PKV_SCHEDULE_PARTITIONS = 1
 PKV_SCHEDULE_BALANCED = 2
+
+PKV_PAIRS_HALVES = 0
+PKV_PAIRS_ADJACENT = 1
+
+PKV_SECTIONS_BLOCKS = 0
+PKV_SECTIONS_CYCLE = 1
+
+PKV_MAX_AXES = 4
 
 PKV_DEVERR_BAD_BLOCK = 1
 PKV_DEVERR_BAD_SEQ_LEN = 2
@@ -104,6 +114,16 @@ class SparseParams(ctypes.Structure):
 
 class SparsePlan(ctypes.Structure):
     _fields_ = [("attention", Plan), ("select_bytes", ctypes.c_size_t), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "rot_dims", "pairing", "num_axes", "section_order")] + \
+        [("sections", ctypes.c_int32 * PKV_MAX_AXES), ("weight_f32", ctypes.c_int32)] + \
+        [(n, ctypes.c_float) for n in ("eps", "weight_offset", "amplitude")]
+
+
+class RowStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("seq", "token", "head")]
 
 
 _lib = None
@@ -167,6 +187,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pkv_selected_decode_attention.restype = ctypes.c_int
     lib.pkv_sparse_decode_attention.argtypes = LPS + [P, P, P, P, P, P, P, P, P, P, F, P, P, P, SZ, P, P]
     lib.pkv_sparse_decode_attention.restype = ctypes.c_int
+    R, S = ctypes.POINTER(Rotation), ctypes.POINTER(RowStrides)
+    lib.pkv_norm_rotate.argtypes = [R, I32, I32, I32, I32, P, S, P, S, P, P, P, P, P, S, P, S, P]
+    lib.pkv_norm_rotate.restype = ctypes.c_int
+    lib.pkv_norm_rotate_append.argtypes = [ctypes.POINTER(PoolLayout), R, I32, I32, I32, I32, I32, P, S, P, S, P, S,
+                                           P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P, P]
+    lib.pkv_norm_rotate_append.restype = ctypes.c_int
     lib.pkv_strerror.argtypes = [ctypes.c_int]
     lib.pkv_strerror.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error.argtypes = []
@@ -687,6 +713,220 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.T
                                   _raw_stream(index))
     if rc != PKV_OK:
         _check(rc, lib)
+
+
+def _row_strides(t: torch.Tensor) -> RowStrides:
+    """Strides of heads [T, H, D] (packed) or [B, N, H, D]; those of dims of one element are never stepped."""
+    st = [0 if n == 1 else x for n, x in zip(t.shape, t.stride())]
+    return RowStrides(0 if t.dim() == 3 else st[0], st[-3], st[-2])
+
+
+def _require_rows(name: str, t: torch.Tensor, lead: tuple, heads: Optional[int], dim: Optional[int] = None) -> None:
+    """Heads of the tokens `lead`: bf16 [*lead, heads, dim], each row's values contiguous."""
+    _require(torch.bfloat16, **{name: t})
+    if tuple(t.shape[:-2]) != lead or (heads is not None and t.shape[-2] != heads) or \
+            (dim is not None and t.shape[-1] != dim):
+        raise ValueError(f"{name} must be of shape {list(lead) + [heads or 'heads', dim or 'dim']}, not {list(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+
+
+def _rotation(head_dim: int, inv_freq: torch.Tensor, num_axes: int, q_weight, k_weight, eps: float, weight_offset: float,
+              sections, section_order: int, pairing: int, amplitude: float) -> Rotation:
+    _require(torch.float32, inv_freq=inv_freq)
+    _require_shape("inv_freq", inv_freq, inv_freq.numel())
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w in weights:
+        if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype is not weights[0].dtype:
+            raise TypeError("norm weights are bfloat16 or float32, both of one type")
+        _require_shape("norm weights", w, head_dim)
+    if num_axes > 1 and sections is None or sections is not None and len(sections) != num_axes:
+        raise ValueError(f"positions of {num_axes} axes need sections of as many")
+    if num_axes > PKV_MAX_AXES:
+        raise ValueError(f"positions of {num_axes} axes (at most {PKV_MAX_AXES})")
+    r = Rotation(head_dim, 2 * inv_freq.numel(), pairing, num_axes, section_order)
+    r.sections[:num_axes] = list(sections) if sections is not None else [inv_freq.numel()]
+    if sections is not None and num_axes == 1 and list(sections) != [inv_freq.numel()]:
+        raise ValueError("sections must add up to the frequencies")
+    r.weight_f32 = bool(weights) and weights[0].dtype is torch.float32
+    r.eps, r.weight_offset, r.amplitude = eps, weight_offset, amplitude
+    return r
+
+
+class _RotateCall:
+    """What the shapes and strides of a rotating call settle."""
+
+    __slots__ = ("rotation", "layout", "num_seqs", "tokens_per_seq", "tokens", "strides", "refs", "out_shapes")
+
+    def __init__(self, rotation, layout, lead, *rows):
+        self.rotation, self.layout = ctypes.byref(rotation), layout and ctypes.byref(layout)
+        packed = len(lead) == 1
+        self.num_seqs, self.tokens_per_seq = (1, lead[0]) if packed else lead
+        self.tokens = self.num_seqs * self.tokens_per_seq
+        self.strides = [None if t is None else _row_strides(t) for t in rows]
+        self.refs = [None if s is None else ctypes.byref(s) for s in self.strides]
+
+
+def _layout_key(t: Optional[torch.Tensor]):
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+def _on_one_device(index: int, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be on one device")
+
+
+def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, *,
+                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                weight_offset: float = 0.0, sections=None, section_order: int = PKV_SECTIONS_BLOCKS,
+                pairing: int = PKV_PAIRS_HALVES, amplitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                k_out: Optional[torch.Tensor] = None):
+    """RMS norm of each query and key head (where its weight [D], bf16 or f32, is given) and the
+    rotation of its first 2 * len(inv_freq) dims by its position, in one pass
+    (pkv_norm_rotate; see include/pkv_decode.h).
+
+    q bf16 [T, HQ, D] or [B, N, HQ, D], k alike with HK heads (or None); any strides of whole 16
+    bytes, such as slices of one projection's output. positions int32 [T] or [B, N], or with a
+    leading dim of up to 4 axes, whose ``sections`` then say how many frequencies each axis turns.
+    inv_freq f32 [rotated dims / 2]. q_out and k_out may be q and k, or any strides: the decode's
+    [B, HQ, N, D] queries are ``q_out=out.transpose(1, 2)``. Returns (q_out, k_out), contiguous when not given.
+    """
+    lib = load_library()
+    index = q.get_device()
+    key = ("rotate", index, _layout_key(q), _layout_key(k), positions.shape, positions.dtype, inv_freq.shape, inv_freq.dtype,
+           _layout_key(q_weight), _layout_key(k_weight), _layout_key(q_out), _layout_key(k_out), eps, weight_offset,
+           None if sections is None else tuple(sections), section_order, pairing, amplitude)
+    call = _calls.get(key)
+    if call is None:
+        if index < 0:
+            raise ValueError("expected CUDA tensors")
+        if q.dim() not in (3, 4):
+            raise ValueError("q must be [T, HQ, D] or [B, N, HQ, D]")
+        lead, D = tuple(q.shape[:-2]), q.shape[-1]
+        _require_rows("q", q, lead, None)
+        if k is not None:
+            _require_rows("k", k, lead, None, D)
+        if k is None and (k_out is not None or k_weight is not None):
+            raise ValueError("k_out and k_weight need k")
+        for name, out, of in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if out is not None:
+                _require_rows(name, out, lead, of.shape[-2], D)
+        _require(torch.int32, positions=positions)
+        axes = positions.shape[0] if positions.dim() == len(lead) + 1 else 1
+        _require_shape("positions", positions, *(() if positions.dim() == len(lead) else (axes,)), *lead)
+        rot = _rotation(D, inv_freq, axes, q_weight, k_weight, eps, weight_offset, sections, section_order, pairing, amplitude)
+        call = _RotateCall(rot, None, lead, q, k, q if q_out is None else q_out, k if k_out is None else k_out)
+        call.out_shapes = [None if out is not None or t is None else tuple(t.shape) for t, out in ((q, q_out), (k, k_out))]
+        for i, shape in enumerate(call.out_shapes):
+            if shape is not None:
+                call.strides[2 + i] = _row_strides(torch.empty(shape, device="meta"))
+                call.refs[2 + i] = ctypes.byref(call.strides[2 + i])
+        _remember(key, call)
+    _check_tensors(index, positions, inv_freq, q_weight, k_weight)
+    _on_one_device(index, k, q_out, k_out)
+    with _on_index(index):
+        if q_out is None:
+            q_out = torch.empty(call.out_shapes[0], dtype=q.dtype, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(call.out_shapes[1], dtype=k.dtype, device=k.device)
+        refs = call.refs
+        rc = lib.pkv_norm_rotate(call.rotation, call.num_seqs, call.tokens_per_seq, q.shape[-2],
+                                 0 if k is None else k.shape[-2], q.data_ptr(), refs[0], _ptr(k), refs[1], _ptr(q_weight),
+                                 _ptr(k_weight), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(), refs[2],
+                                 _ptr(k_out), refs[3], _raw_stream(index))
+    if rc != PKV_OK:
+        _check(rc, lib)
+    return q_out, k_out
+
+
+def norm_rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                       inv_freq: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, k_pool: torch.Tensor,
+                       v_pool: torch.Tensor, *, query_starts: Optional[torch.Tensor] = None, bits: int = 16,
+                       group_size: int = 64, k_scales: Optional[torch.Tensor] = None,
+                       k_biases: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                       v_biases: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                       sections=None, section_order: int = PKV_SECTIONS_BLOCKS, pairing: int = PKV_PAIRS_HALVES,
+                       amplitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                       error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``norm_rotate`` with the write (pkv_norm_rotate_append): the keys and v's rows go into their
+    pages behind the seq_lens int32 [B] rows that each sequence holds, as ``paged_append`` would
+    write them; returns the queries.
+
+    q, k, v are [B, N, heads, D] (N new tokens of each sequence), or packed [T, heads, D] with
+    query_starts int32 [B + 1]: sequence b's tokens are query_starts[b] .. query_starts[b + 1] - 1
+    (without query_starts, one token each). positions as for ``norm_rotate``, or None for the rows'
+    places in the cache. Pages, planes and block tables as for ``paged_append``."""
+    lib = load_library()
+    index = q.get_device()
+    key = ("rotate_append", index, _layout_key(q), _layout_key(k), _layout_key(v),
+           None if positions is None else (positions.shape, positions.dtype), inv_freq.shape, inv_freq.dtype,
+           _types((block_tables, seq_lens, k_pool, v_pool, query_starts, k_scales, k_biases, v_scales, v_biases)),
+           bits, group_size, _layout_key(q_weight), _layout_key(k_weight), _layout_key(q_out), eps, weight_offset,
+           None if sections is None else tuple(sections), section_order, pairing, amplitude)
+    call = _calls.get(key)
+    if call is None:
+        if index < 0:
+            raise ValueError("expected CUDA tensors")
+        if q.dim() not in (3, 4):
+            raise ValueError("q must be [T, HQ, D] or [B, N, HQ, D]")
+        lead, D, hk = tuple(q.shape[:-2]), q.shape[-1], k_pool.shape[1]
+        packed = len(lead) == 1 and query_starts is not None
+        if len(lead) == 2 and query_starts is not None:
+            raise ValueError("query_starts are those of packed tokens [T, heads, D]")
+        B = block_tables.shape[0]
+        if not packed and lead[0] != B:
+            raise ValueError(f"{lead[0]} sequences of new tokens and {B} block tables")
+        layout = layout_for(k_pool, D, bits, group_size, v_pool)
+        _require_rows("q", q, lead, None)
+        _require_rows("k", k, lead, hk, D)
+        _require_rows("v", v, lead, hk, v_head_dim_of(v_pool, bits))
+        if q_out is not None:
+            _require_rows("q_out", q_out, lead, q.shape[-2], D)
+        _require(torch.int32, positions=positions, block_tables=block_tables, seq_lens=seq_lens, query_starts=query_starts)
+        if bits == 16:
+            _require(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
+        _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
+        _require_shape("block_tables", block_tables, B, block_tables.shape[-1])
+        _require_shape("seq_lens", seq_lens, B)
+        _require_shape("query_starts", query_starts, B + 1)
+        _check_planes(k_pool, v_pool, bits, group_size, D, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
+                      v_biases=v_biases)
+        axes = 1
+        if positions is not None:
+            axes = positions.shape[0] if positions.dim() == len(lead) + 1 else 1
+            _require_shape("positions", positions, *(() if positions.dim() == len(lead) else (axes,)), *lead)
+        rot = _rotation(D, inv_freq, axes, q_weight, k_weight, eps, weight_offset, sections, section_order, pairing, amplitude)
+        call = _RotateCall(rot, layout, lead, q, k, v, q if q_out is None else q_out)
+        if len(lead) == 1:
+            call.num_seqs, call.tokens_per_seq = B, 0 if packed else 1
+            if not packed:  # one token of each sequence: the strides between tokens are those between sequences
+                for st in call.strides:
+                    st.seq = st.token
+        if q_out is None:
+            call.out_shapes = tuple(q.shape)
+            st = call.strides[3] = _row_strides(torch.empty(call.out_shapes, device="meta"))
+            if len(lead) == 1 and not packed:
+                st.seq = st.token
+            call.refs[3] = ctypes.byref(st)
+        _remember(key, call)
+    _check_tensors(index, positions, inv_freq, q_weight, k_weight, block_tables, seq_lens, query_starts, k_pool, v_pool,
+                   k_scales, k_biases, v_scales, v_biases, error_flag)
+    _on_one_device(index, k, v, q_out)
+    with _on_index(index):
+        if q_out is None:
+            q_out = torch.empty(call.out_shapes, dtype=q.dtype, device=q.device)
+        refs = call.refs
+        rc = lib.pkv_norm_rotate_append(
+            call.layout, call.rotation, call.num_seqs, call.tokens, call.tokens_per_seq, q.shape[-2], block_tables.shape[1],
+            q.data_ptr(), refs[0], k.data_ptr(), refs[1], v.data_ptr(), refs[2], _ptr(q_weight), _ptr(k_weight),
+            _ptr(positions), inv_freq.data_ptr(), _ptr(query_starts), block_tables.data_ptr(), seq_lens.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), _ptr(k_scales), _ptr(k_biases), _ptr(v_scales), _ptr(v_biases),
+            q_out.data_ptr(), refs[3], _ptr(error_flag), _raw_stream(index))
+    if rc != PKV_OK:
+        _check(rc, lib)
+    return q_out
 
 
 def paged_gather(pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_len: int,

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -1039,6 +1040,212 @@ int pkv_paged_gather(const void* pool, int32_t num_blocks, int32_t num_kv_heads,
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Norm and rotation, alone or with the write into pages (pkv_rotate.cu)
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_rotation(const pkv_rotation* r) {
+  if (!r) return PKV_ERR_NULL_POINTER;
+  if (r->head_dim != 64 && r->head_dim != 128 && r->head_dim != 192 && r->head_dim != 256) return PKV_ERR_BAD_LAYOUT;
+  if (r->rot_dims < 8 || r->rot_dims > r->head_dim || r->rot_dims % 8) return PKV_ERR_BAD_PARAMS;
+  if (r->pairing != PKV_PAIRS_HALVES && r->pairing != PKV_PAIRS_ADJACENT) return PKV_ERR_BAD_PARAMS;
+  if (r->num_axes < 1 || r->num_axes > PKV_MAX_AXES) return PKV_ERR_BAD_PARAMS;
+  if (r->section_order != PKV_SECTIONS_BLOCKS && r->section_order != PKV_SECTIONS_CYCLE) return PKV_ERR_BAD_PARAMS;
+  if (r->num_axes > 1) {
+    const long long half = r->rot_dims / 2;
+    long long sum = 0;
+    for (int a = 0; a < r->num_axes; ++a) {
+      const long long s = r->sections[a];
+      if (s < 0 || s > half) return PKV_ERR_BAD_PARAMS;
+      // the last frequency that the cycle gives to axis a
+      if (r->section_order == PKV_SECTIONS_CYCLE && a > 0 && s > 0 && r->num_axes * (s - 1) + a >= half)
+        return PKV_ERR_BAD_PARAMS;
+      sum += s;
+    }
+    if (sum != half) return PKV_ERR_BAD_PARAMS;
+  }
+  if (!(r->eps >= 0.f) || !std::isfinite(r->eps) || !std::isfinite(r->weight_offset) || !std::isfinite(r->amplitude))
+    return PKV_ERR_BAD_PARAMS;
+  return PKV_OK;
+}
+
+// Rows that 16-byte vectors reach: strides of whole vectors, base aligned.
+int check_rows(const void* data, const pkv_row_strides* s) {
+  if (!data || !s) return PKV_ERR_NULL_POINTER;
+  if (s->seq < 0 || s->token < 0 || s->head < 0) return PKV_ERR_BAD_PARAMS;
+  if (!aligned(data, 16) || s->seq % 8 || s->token % 8 || s->head % 8) return PKV_ERR_MISALIGNED;
+  return PKV_OK;
+}
+
+// Output rows: the same, and no two of them share a value. Dims in order of their strides must each step
+// over all that the smaller ones span.
+int check_out_rows(const void* data, const pkv_row_strides* s, long long seqs, long long tokens, long long heads,
+                   long long dim) {
+  const int rc = check_rows(data, s);
+  if (rc) return rc;
+  struct Dim {
+    long long size, stride;
+  } d[3] = {{seqs, s->seq}, {tokens, s->token}, {heads, s->head}};
+  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  long long span = dim;
+  for (const Dim& x : d) {
+    if (x.size <= 1) continue;
+    if (x.stride < span) return PKV_ERR_BAD_PARAMS;
+    span += (x.size - 1) * x.stride;
+  }
+  return PKV_OK;
+}
+
+pkv::HeadRows head_rows(const void* data, const pkv_row_strides* s) {
+  return pkv::HeadRows{static_cast<__nv_bfloat16*>(const_cast<void*>(data)), s->seq, s->token, s->head};
+}
+
+int fill_rotation(const pkv_rotation* r, const void* q_weight, const void* k_weight, const int32_t* positions,
+                  const float* inv_freq, pkv::RotateParams* p) {
+  if (!inv_freq) return PKV_ERR_NULL_POINTER;
+  const uintptr_t wa = r->weight_f32 ? 4 : 2;
+  if (!aligned(inv_freq, 4) || !aligned(positions, 4) || !aligned(q_weight, wa) || !aligned(k_weight, wa))
+    return PKV_ERR_MISALIGNED;
+  p->q_weight = q_weight;
+  p->k_weight = k_weight;
+  p->weight_f32 = r->weight_f32 != 0;
+  p->eps = r->eps;
+  p->weight_offset = r->weight_offset;
+  p->turn.rot = r->rot_dims;
+  p->turn.adjacent = r->pairing == PKV_PAIRS_ADJACENT;
+  p->turn.num_axes = r->num_axes;
+  p->turn.cycle = r->section_order == PKV_SECTIONS_CYCLE;
+  for (int a = 0; a < PKV_MAX_AXES; ++a) p->turn.sections[a] = a < r->num_axes ? r->sections[a] : 0;
+  p->turn.amplitude = r->amplitude;
+  p->positions = positions;
+  p->inv_freq = inv_freq;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_norm_rotate(const pkv_rotation* rotation, int32_t num_seqs, int32_t tokens_per_seq, int32_t num_q_heads,
+                    int32_t num_kv_heads, const void* q, const pkv_row_strides* q_strides, const void* k,
+                    const pkv_row_strides* k_strides, const void* q_weight, const void* k_weight,
+                    const int32_t* positions, const float* inv_freq, void* q_out,
+                    const pkv_row_strides* q_out_strides, void* k_out, const pkv_row_strides* k_out_strides,
+                    void* stream) {
+  int rc = check_rotation(rotation);
+  if (rc) return rc;
+  if (num_seqs < 0 || tokens_per_seq < 0 || num_q_heads <= 0 || num_q_heads > 65535 || num_kv_heads < 0 ||
+      num_kv_heads > 65535)
+    return PKV_ERR_BAD_PARAMS;
+  const long long tokens = static_cast<long long>(num_seqs) * tokens_per_seq;
+  if (tokens >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  if (tokens == 0) return PKV_OK;
+  if (!positions) return PKV_ERR_NULL_POINTER;
+  pkv::RotateParams p{};
+  rc = check_rows(q, q_strides);
+  if (!rc) rc = check_out_rows(q_out, q_out_strides, num_seqs, tokens_per_seq, num_q_heads, rotation->head_dim);
+  if (!rc && num_kv_heads > 0) {
+    rc = check_rows(k, k_strides);
+    if (!rc) rc = check_out_rows(k_out, k_out_strides, num_seqs, tokens_per_seq, num_kv_heads, rotation->head_dim);
+  }
+  if (!rc) rc = fill_rotation(rotation, q_weight, num_kv_heads > 0 ? k_weight : nullptr, positions, inv_freq, &p);
+  if (rc) return rc;
+  p.q = head_rows(q, q_strides);
+  p.q_out = head_rows(q_out, q_out_strides);
+  if (num_kv_heads > 0) {
+    p.k = head_rows(k, k_strides);
+    p.k_out = head_rows(k_out, k_out_strides);
+  }
+  p.tokens = static_cast<int>(tokens);
+  p.tokens_per_seq = tokens_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  (void)cudaGetLastError();
+  cudaError_t e = pkv::launch_rotate(p, rotation->head_dim, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("rotation kernel launch", e);
+  return PKV_OK;
+}
+
+int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* rotation, int32_t num_seqs,
+                           int32_t num_tokens, int32_t tokens_per_seq, int32_t num_q_heads,
+                           int32_t max_blocks_per_seq, const void* q, const pkv_row_strides* q_strides, const void* k,
+                           const pkv_row_strides* k_strides, const void* v, const pkv_row_strides* v_strides,
+                           const void* q_weight, const void* k_weight, const int32_t* positions,
+                           const float* inv_freq, const int32_t* query_starts, const int32_t* block_tables,
+                           const int32_t* seq_lens, void* k_pool, void* v_pool, void* k_scales, void* k_biases,
+                           void* v_scales, void* v_biases, void* q_out, const pkv_row_strides* q_out_strides,
+                           int32_t* error_flag, void* stream) {
+  int rc = check_layout(layout);
+  if (rc) return rc;
+  if (!pkv::append_supported(format_of(layout), layout->head_dim, v_dim(layout))) return PKV_ERR_BAD_LAYOUT;
+  rc = check_rotation(rotation);
+  if (rc) return rc;
+  if (rotation->head_dim != layout->head_dim) return PKV_ERR_BAD_LAYOUT;
+  if (num_seqs <= 0 || num_seqs > 65535 || num_tokens < 0 || tokens_per_seq < 0 || num_q_heads <= 0 ||
+      num_q_heads > 65535 || max_blocks_per_seq <= 0)
+    return PKV_ERR_BAD_PARAMS;
+  if (static_cast<long long>(max_blocks_per_seq) * layout->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  if (tokens_per_seq > 0 && static_cast<long long>(num_seqs) * tokens_per_seq != num_tokens) return PKV_ERR_BAD_PARAMS;
+  if (num_tokens == 0) return PKV_OK;
+  if (!positions && rotation->num_axes != 1) return PKV_ERR_BAD_PARAMS;
+  if (!block_tables || !seq_lens || !k_pool || !v_pool || (tokens_per_seq == 0 && !query_starts))
+    return PKV_ERR_NULL_POINTER;
+  if (!scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(query_starts, 4) || !aligned(error_flag, 4))
+    return PKV_ERR_MISALIGNED;
+  if (!scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 4)) return PKV_ERR_MISALIGNED;
+  const bool packed = tokens_per_seq == 0;
+  pkv::RotateParams p{};
+  rc = check_rows(q, q_strides);
+  if (!rc) rc = check_rows(k, k_strides);
+  if (!rc) rc = check_rows(v, v_strides);
+  if (!rc)
+    rc = check_out_rows(q_out, q_out_strides, packed ? 1 : num_seqs, packed ? num_tokens : tokens_per_seq, num_q_heads,
+                        layout->head_dim);
+  if (!rc) rc = fill_rotation(rotation, q_weight, k_weight, positions, inv_freq, &p);
+  if (rc) return rc;
+  p.q = head_rows(q, q_strides);
+  p.k = head_rows(k, k_strides);
+  p.v = head_rows(v, v_strides);
+  p.q_out = head_rows(q_out, q_out_strides);
+  p.tokens = num_tokens;
+  p.tokens_per_seq = tokens_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = layout->num_kv_heads;
+  p.query_starts = query_starts;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  if (block_scaled(layout)) {
+    p.block_pool[0] = static_cast<uint8_t*>(k_pool);
+    p.block_pool[1] = static_cast<uint8_t*>(v_pool);
+    p.block_scales[0] = static_cast<float*>(k_scales);
+    p.block_scales[1] = static_cast<float*>(v_scales);
+  } else {
+    p.dst = append_target(layout->bits != 16, k_pool, v_pool, k_scales, k_biases, v_scales, v_biases);
+  }
+  p.error_flag = error_flag;
+  p.num_blocks = layout->num_blocks;
+  p.block_size = layout->block_size;
+  p.max_blocks = max_blocks_per_seq;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  (void)cudaGetLastError();
+  cudaError_t e = pkv::launch_rotate_append(p, format_of(layout), layout->head_dim, v_dim(layout), sms,
+                                            static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("rotation and append kernel launch", e);
+  return PKV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Sparse decode attention over chosen blocks (pkv_sparse.cu)
 // ---------------------------------------------------------------------------
 namespace {
@@ -1479,7 +1686,7 @@ const char* pkv_strerror(int code) {
     case PKV_ERR_NULL_POINTER: return "a required pointer is NULL";
     case PKV_ERR_MISALIGNED: return "a pointer is not aligned (16 bytes for data planes, 4 for int32 arrays)";
     case PKV_ERR_BAD_LAYOUT: return "unsupported pool layout (bits, group_size, head dims or block_size)";
-    case PKV_ERR_BAD_PARAMS: return "bad decode parameters (sequences, heads, n_query, table width or partition)";
+    case PKV_ERR_BAD_PARAMS: return "bad parameters (sequences, heads, tokens, n_query, table width, partition, strides or rotation)";
     case PKV_ERR_UNSUPPORTED_SHAPE:
       return "no kernel for this pair of key/value head dims with this many query rows per KV head";
     case PKV_ERR_WORKSPACE_TOO_SMALL: return "workspace missing or smaller than the plan needs";

@@ -126,6 +126,49 @@ struct AppendBlockParams {
   int num_blocks, num_kv_heads, block_size, max_blocks, n_new;
 };
 
+// Heads of a run of tokens: head h of token j of sequence b begins at
+// data + b * seq + j * token + h * head (strides in elements; packed tokens have one sequence).
+struct HeadRows {
+  __nv_bfloat16* data;
+  long long seq, token, head;
+};
+
+// How positions turn the first `rot` dims of a head (pkv_rotate.cuh).
+struct RotationShape {
+  int rot;       // rotated dims, a multiple of 8
+  int adjacent;  // pairs (2i, 2i+1), else (i, i + rot/2)
+  int num_axes;
+  int cycle;     // frequencies go to the axes in turn, else in blocks
+  int sections[4];
+  float amplitude;
+};
+
+// Norm and rotation of queries and keys, and their write into pages (pkv_rotate.cu).
+struct RotateParams {
+  HeadRows q, k, v;        // inputs (v: of the write alone)
+  HeadRows q_out, k_out;   // k_out: without the write
+  const void* q_weight;    // NULL: no norm
+  const void* k_weight;
+  int weight_f32;
+  float eps, weight_offset;
+  RotationShape turn;
+  const int32_t* positions;  // [num_axes, tokens]; NULL (with the write): the rows' places in the cache
+  const float* inv_freq;     // [rot / 2]
+  int tokens, tokens_per_seq;  // tokens_per_seq 0: packed, found by query_starts
+  int num_seqs, num_q_heads, num_kv_heads;
+  int groups;              // warps that share a token's heads
+  // the write
+  const int32_t* query_starts;  // [num_seqs + 1] (packed)
+  const int32_t* block_tables;
+  const int32_t* seq_lens;      // rows before the write
+  AppendTarget dst;             // bf16 and affine pages
+  uint8_t* block_pool[2];       // e4m3 pages: K, V
+  float* block_scales[2];
+  int32_t* error_flag;
+  int num_blocks, block_size, max_blocks;
+  int q_ctas, head_warps, table_rows;  // e4m3 pages: CTAs of query rows, warps per KV head, rows whose angles are tabled
+};
+
 // Upkeep of the block bounds (pkv_sparse.cu).
 struct BoundsParams {
   const void* k_pool;

@@ -82,6 +82,12 @@ cudaError_t launch_append(const AppendParams& p, int bits, int head_dim, int v_h
                           cudaStream_t stream);
 cudaError_t launch_append_blocks(const AppendBlockParams& p, int num_seqs, cudaStream_t stream);
 
+// Norm and rotation of queries and keys (head_dim 64, 128, 192 or 256), alone or with the write
+// into pages (the layouts of append_supported); p's launch fields are set by the call.
+cudaError_t launch_rotate(const RotateParams& p, int head_dim, int sm_count, cudaStream_t stream);
+cudaError_t launch_rotate_append(const RotateParams& p, int fmt, int head_dim, int v_head_dim, int sm_count,
+                                 cudaStream_t stream);
+
 cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_seqs, cudaStream_t stream);
 int select_tiles(int max_blocks);  // tiles of SelectParams for a table of this width
 cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device, cudaStream_t stream);
