@@ -587,6 +587,55 @@ int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* ro
                            void* v_scales, void* v_biases, void* q_out, const pkv_row_strides* q_out_strides,
                            int32_t* error_flag, void* stream);
 
+/* Prompt attention: many new tokens of each sequence over the pages that hold them and the
+ * rows before them, as many query rows as there are (the decode calls stop at 64 per KV head).
+ * The queries of all sequences are packed: sequence b's n = query_starts[b+1] - query_starts[b]
+ * tokens are its newest, and its token i sees
+ *     keys t <= seq_lens[b] - n + i   and, with a window W, t > seq_lens[b] - n + i - W.
+ * Everything else is as for pkv_paged_decode_attention. The reference leaves prompts to its
+ * framework's own attention over gathered rows; it has no counterpart of this call. */
+typedef struct pkv_prefill_params {
+  int32_t num_seqs;           /* B, 1 .. 65535 */
+  int32_t num_tokens;         /* tokens in q, >= 0 */
+  int32_t num_q_heads;        /* HQ, a multiple of num_kv_heads, at most 64 per KV head */
+  int32_t max_blocks_per_seq; /* row stride of block_tables, > 0 */
+  int32_t window;             /* sliding window in rows, 0 = none */
+  int32_t splits;             /* CTAs that share the keys of one tile of queries: 0 = chosen from the
+                                 tokens, the table's width and the SM count, 1 .. 64 */
+} pkv_prefill_params;
+
+typedef struct pkv_prefill_plan {
+  int32_t unit_tokens;    /* tokens of one CTA */
+  int32_t key_tile;       /* key rows per step */
+  int32_t units;          /* CTAs per KV head and split, those of short last tiles included */
+  int32_t splits;
+  int32_t smem_bytes;     /* dynamic shared memory of a CTA */
+  size_t workspace_bytes; /* f32 states of split key ranges (0 with splits = 1) */
+} pkv_prefill_plan;
+
+int pkv_make_prefill_plan(const pkv_pool_layout* layout, const pkv_prefill_params* params, int32_t sm_count,
+                          pkv_prefill_plan* plan);
+int pkv_prefill_plan_for_current_device(const pkv_pool_layout* layout, const pkv_prefill_params* params,
+                                        pkv_prefill_plan* plan);
+
+/*   q             bf16 rows of num_q_heads heads, 16-byte aligned; q_strides as for
+ *                 pkv_norm_rotate, packed; not zero for a dim of more than one
+ *   query_starts  int32 [num_seqs + 1], not falling, within 0 .. num_tokens. Rows of tokens outside
+ *                 [query_starts[0], query_starts[num_seqs]) are neither read nor written.
+ *   seq_lens      rows held, the new ones included
+ *   out           bf16 [num_tokens, num_q_heads, v_head_dim]
+ *   workspace     plan.workspace_bytes; calls that overlap on the GPU need one each
+ * A seq_len below the sequence's tokens or above the table's rows writes zeros for the sequence and sets
+ * PKV_DEVERR_BAD_SEQ_LEN, as do starts that fall or leave 0 .. num_tokens (their sequences' outputs are
+ * then unspecified). Rows of bad blocks are skipped and flagged; a query that sees no row gets zeros.
+ * Cached rows below seq_len must be finite; blocks wholly outside the window are not read. */
+int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill_params* params, const void* q,
+                                const pkv_row_strides* q_strides, const void* k_pool, const void* v_pool,
+                                const void* k_scales, const void* k_biases, const void* v_scales,
+                                const void* v_biases, const int32_t* block_tables, const int32_t* seq_lens,
+                                const int32_t* query_starts, float scale, void* out, void* workspace,
+                                size_t workspace_bytes, int32_t* error_flag, void* stream);
+
 /* Bit-exact gather of one pool plane into contiguous per-sequence rows, the
  * fetch copy of the pages' BlockPool.gather / pickBlocks (state/paged/cache.ts):
  *   out[b][h][t][:] = pool[block_tables[b][t / block_size]][h][t % block_size][:]

@@ -39,6 +39,9 @@ EXPORTS = (
     "pkv_sparse_decode_attention",
     "pkv_norm_rotate",
     "pkv_norm_rotate_append",
+    "pkv_make_prefill_plan",
+    "pkv_prefill_plan_for_current_device",
+    "pkv_paged_prefill_attention",
     "pkv_paged_gather",
     "pkv_strerror",
     "pkv_last_cuda_error",
@@ -126,6 +129,16 @@ class RowStrides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("seq", "token", "head")]
 
 
+class PrefillParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_seqs", "num_tokens", "num_q_heads", "max_blocks_per_seq", "window", "splits")]
+
+
+class PrefillPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("unit_tokens", "key_tile", "units", "splits", "smem_bytes")] + \
+        [("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -193,6 +206,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pkv_norm_rotate_append.argtypes = [ctypes.POINTER(PoolLayout), R, I32, I32, I32, I32, I32, P, S, P, S, P, S,
                                            P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P, P]
     lib.pkv_norm_rotate_append.restype = ctypes.c_int
+    LP = [ctypes.POINTER(PoolLayout), ctypes.POINTER(PrefillParams)]
+    lib.pkv_make_prefill_plan.argtypes = LP + [I32, ctypes.POINTER(PrefillPlan)]
+    lib.pkv_make_prefill_plan.restype = ctypes.c_int
+    lib.pkv_prefill_plan_for_current_device.argtypes = LP + [ctypes.POINTER(PrefillPlan)]
+    lib.pkv_prefill_plan_for_current_device.restype = ctypes.c_int
+    lib.pkv_paged_prefill_attention.argtypes = LP + [P, S, P, P, P, P, P, P, P, P, P, F, P, P, SZ, P, P]
+    lib.pkv_paged_prefill_attention.restype = ctypes.c_int
     lib.pkv_strerror.argtypes = [ctypes.c_int]
     lib.pkv_strerror.restype = ctypes.c_char_p
     lib.pkv_last_cuda_error.argtypes = []
@@ -927,6 +947,94 @@ def norm_rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     if rc != PKV_OK:
         _check(rc, lib)
     return q_out
+
+
+def make_prefill_plan(layout: PoolLayout, params: PrefillParams, sm_count: Optional[int] = None) -> PrefillPlan:
+    """The library's plan of a prompt attention call (splits, workspace bytes)."""
+    lib = load_library()
+    plan = PrefillPlan()
+    args = (ctypes.byref(layout), ctypes.byref(params))
+    if sm_count is None:
+        rc = lib.pkv_prefill_plan_for_current_device(*args, ctypes.byref(plan))
+    else:
+        rc = lib.pkv_make_prefill_plan(*args, sm_count, ctypes.byref(plan))
+    _check(rc, lib)
+    return plan
+
+
+class _PrefillCall:
+    """What the shapes of a prompt attention call settle."""
+
+    __slots__ = ("refs", "keep", "workspace_bytes", "out_shape")
+
+
+def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Tensor,
+                            seq_lens: torch.Tensor, query_starts: torch.Tensor, scale: float, *, bits: int = 16,
+                            group_size: int = 64, k_scales: Optional[torch.Tensor] = None,
+                            k_biases: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                            v_biases: Optional[torch.Tensor] = None, window: int = 0, splits: int = 0,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of many new tokens of each sequence over the pages (pkv_paged_prefill_attention; see
+    include/pkv_decode.h).
+
+    q bf16 [T, HQ, D], packed, with strides of whole 16 bytes: sequence b's tokens are
+    query_starts[b] .. query_starts[b + 1] - 1 (int32 [B + 1]), the newest of the seq_lens[b] rows that its
+    pages hold. Pages and planes as for ``paged_decode_attention``. Returns bf16 [T, HQ, Dv]; rows of
+    tokens of no sequence are left as they were (in ``out``) or unspecified.
+    """
+    lib = load_library()
+    index = q.get_device()
+    key = ("prefill", index, _layout_key(q), None if out is None else (out.shape, out.dtype),
+           _types((k_pool, v_pool, block_tables, seq_lens, query_starts, k_scales, k_biases, v_scales, v_biases)), bits,
+           group_size, window, splits)
+    with _on_index(index) if index >= 0 else _stay:
+        call = _calls.get(key)
+        if call is None:
+            if index < 0:
+                raise ValueError("expected CUDA tensors")
+            if q.dim() != 3:
+                raise ValueError("q must be [T, HQ, D]")
+            T, HQ, D = q.shape
+            B = block_tables.shape[0]
+            layout = layout_for(k_pool, D, bits, group_size, v_pool)
+            _require_rows("q", q, (T,), None)
+            _require(torch.int32, block_tables=block_tables, seq_lens=seq_lens, query_starts=query_starts)
+            if bits == 16:
+                _require(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
+            _require_shape("v_pool", v_pool, *k_pool.shape[:3], v_pool.shape[-1])
+            _require_shape("block_tables", block_tables, B, block_tables.shape[-1])
+            _require_shape("seq_lens", seq_lens, B)
+            _require_shape("query_starts", query_starts, B + 1)
+            _check_planes(k_pool, v_pool, bits, group_size, D, k_scales=k_scales, k_biases=k_biases, v_scales=v_scales,
+                          v_biases=v_biases)
+            call = _PrefillCall()
+            call.out_shape = (T, HQ, layout.v_head_dim or D)
+            if out is not None:
+                _require(torch.bfloat16, out=out)
+                _require_shape("out", out, *call.out_shape)
+            params = PrefillParams(B, T, HQ, block_tables.shape[1], window, splits)
+            strides = _row_strides(q)
+            call.keep = (layout, params, strides)
+            call.refs = tuple(ctypes.byref(x) for x in call.keep)
+            call.workspace_bytes = make_prefill_plan(layout, params).workspace_bytes
+            _remember(key, call)
+        _check_tensors(index, k_pool, v_pool, block_tables, seq_lens, query_starts, k_scales, k_biases, v_scales, v_biases,
+                       out, workspace, error_flag)
+        stream = _raw_stream(index)
+        if out is None:
+            out = torch.empty(call.out_shape, dtype=q.dtype, device=q.device)
+        if workspace is None and call.workspace_bytes:
+            workspace = _workspaces.get(q.device, index, stream, call.workspace_bytes)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        layout_ref, params_ref, strides_ref = call.refs
+        rc = lib.pkv_paged_prefill_attention(
+            layout_ref, params_ref, q.data_ptr(), strides_ref, k_pool.data_ptr(), v_pool.data_ptr(), _ptr(k_scales),
+            _ptr(k_biases), _ptr(v_scales), _ptr(v_biases), block_tables.data_ptr(), seq_lens.data_ptr(),
+            query_starts.data_ptr(), float(scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(error_flag), stream)
+    if rc != PKV_OK:
+        _check(rc, lib)
+    return out
 
 
 def paged_gather(pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_len: int,

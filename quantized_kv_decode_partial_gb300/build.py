@@ -27,6 +27,7 @@ SOURCES = [
     "pkv_append.cu",
     "pkv_append_blocks.cu",
     "pkv_rotate.cu",
+    "pkv_prefill_bf16.cu",
     "pkv_sparse.cu",
     "pkv_partial_bf16.cu",
     "pkv_partial_bf16_cc.cu",

@@ -1246,6 +1246,193 @@ int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* ro
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Prompt attention (pkv_prefill.cuh)
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
+  const int rc = check_layout(L);
+  if (rc) return rc;
+  if (!P) return PKV_ERR_NULL_POINTER;
+  if (P->num_seqs <= 0 || P->num_seqs > 65535 || P->num_tokens < 0 || P->max_blocks_per_seq <= 0 || P->window < 0 ||
+      P->splits < 0 || P->splits > 64)
+    return PKV_ERR_BAD_PARAMS;
+  if (P->num_q_heads <= 0 || P->num_q_heads % L->num_kv_heads) return PKV_ERR_BAD_PARAMS;
+  if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  if (static_cast<long long>(P->num_tokens) * P->num_q_heads >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  if (P->num_q_heads / L->num_kv_heads > 64) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (format_of(L) != 16 || !pkv::prefill_info(L->head_dim, v_dim(L)).exists) return PKV_ERR_UNSUPPORTED_SHAPE;
+  return PKV_OK;
+}
+
+// Splits of every unit's keys. One wave of CTAs of a single split leaves SMs idle when there are
+// few units or just over a whole number of waves; a split costs its CTAs a start and its rows a
+// trip through the workspace. Counted in key tiles of the longest possible sequence:
+//     waves(S) * (tiles / S + start) + S * join
+// for the S that makes it least.
+int prefill_splits(const pkv_pool_layout* L, const pkv_prefill_params* P, long long ctas, int key_tile, int unit_tokens,
+                   int sm_count) {
+  const long long table = static_cast<long long>(P->max_blocks_per_seq) * L->block_size;
+  const long long rows = P->window > 0 ? std::min<long long>(table, static_cast<long long>(P->window) + unit_tokens) : table;
+  const double tiles = static_cast<double>((rows + key_tile - 1) / key_tile);
+  // a tile takes about 1 us; a split's state is written and read at about 5 TB/s
+  const double join = static_cast<double>(P->num_tokens) * P->num_q_heads * v_dim(L) * 8.0 / 5e6;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 64 && s * 2 <= tiles + 1; ++s) {
+    const double waves = static_cast<double>((ctas * s + sm_count - 1) / sm_count);
+    const double cost = waves * (tiles / s + 3.0) + (s > 1 ? s * join + 3.0 : 0.0);
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_count, pkv_prefill_plan* plan) {
+  const pkv::PrefillInfo info = pkv::prefill_info(L->head_dim, v_dim(L));
+  const int rep = P->num_q_heads / L->num_kv_heads;
+  pkv_prefill_plan r{};
+  r.unit_tokens = info.query_tiles * (128 / rep);
+  r.key_tile = info.key_tile;
+  r.units = P->num_tokens / r.unit_tokens + P->num_seqs;
+  const long long ctas = static_cast<long long>(r.units) * L->num_kv_heads;
+  r.splits = P->splits > 0 ? P->splits : prefill_splits(L, P, ctas, info.key_tile, r.unit_tokens, sm_count);
+  if (ctas * r.splits >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  r.smem_bytes = info.smem_bytes;
+  if (r.splits > 1)
+    r.workspace_bytes = static_cast<size_t>(r.splits) * P->num_tokens * P->num_q_heads * (v_dim(L) + 2) * sizeof(float);
+  *plan = r;
+  return PKV_OK;
+}
+
+// The queries as [64 dims][head][token][run of 64 dims]; a box holds the heads of one KV head at
+// `tokens` tokens.
+int encode_query_map(CUtensorMap* map, const void* q, int head_dim, int heads, long long tokens, const pkv_row_strides* s,
+                     int rep, int box_tokens) {
+  auto encode = tensor_map_encoder();
+  if (!encode) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled entry point unavailable");
+    return PKV_ERR_CUDA;
+  }
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens),
+                        static_cast<cuuint64_t>(head_dim / 64)};
+  cuuint64_t strides[3] = {heads > 1 ? static_cast<cuuint64_t>(s->head) * 2 : row,
+                           tokens > 1 ? static_cast<cuuint64_t>(s->token) * 2 : row, 128};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rep), static_cast<cuuint32_t>(box_tokens), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_make_prefill_plan(const pkv_pool_layout* layout, const pkv_prefill_params* params, int32_t sm_count,
+                          pkv_prefill_plan* plan) {
+  if (!plan) return PKV_ERR_NULL_POINTER;
+  const int rc = check_prefill(layout, params);
+  if (rc) return rc;
+  if (sm_count <= 0) return PKV_ERR_BAD_PARAMS;
+  return prefill_plan(layout, params, sm_count, plan);
+}
+
+int pkv_prefill_plan_for_current_device(const pkv_pool_layout* layout, const pkv_prefill_params* params,
+                                        pkv_prefill_plan* plan) {
+  if (!plan) return PKV_ERR_NULL_POINTER;
+  int rc = check_prefill(layout, params);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc) return rc;
+  return prefill_plan(layout, params, sms, plan);
+}
+
+int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill_params* params, const void* q,
+                                const pkv_row_strides* q_strides, const void* k_pool, const void* v_pool,
+                                const void* k_scales, const void* k_biases, const void* v_scales,
+                                const void* v_biases, const int32_t* block_tables, const int32_t* seq_lens,
+                                const int32_t* query_starts, float scale, void* out, void* workspace,
+                                size_t workspace_bytes, int32_t* error_flag, void* stream) {
+  int rc = check_prefill(layout, params);
+  if (rc) return rc;
+  if (!std::isfinite(scale)) return PKV_ERR_BAD_PARAMS;
+  if (params->num_tokens == 0) return PKV_OK;
+  rc = check_rows(q, q_strides);
+  if (rc) return rc;
+  if ((params->num_q_heads > 1 && q_strides->head == 0) || (params->num_tokens > 1 && q_strides->token == 0) ||
+      q_strides->head >= (1ll << 38) || q_strides->token >= (1ll << 38))
+    return PKV_ERR_BAD_PARAMS;
+  if (!k_pool || !v_pool || !block_tables || !seq_lens || !query_starts || !out) return PKV_ERR_NULL_POINTER;
+  if (!scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_starts, 4) || !aligned(error_flag, 4) ||
+      !scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 4))
+    return PKV_ERR_MISALIGNED;
+  int sms = 0, device = 0;
+  rc = device_sm_count(&sms, &device);
+  if (rc) return rc;
+  pkv_prefill_plan plan{};
+  rc = prefill_plan(layout, params, sms, &plan);
+  if (rc) return rc;
+  if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
+    return PKV_ERR_WORKSPACE_TOO_SMALL;
+
+  const int D = layout->head_dim, DV = v_dim(layout), rep = params->num_q_heads / layout->num_kv_heads;
+  pkv::PrefillParams p{};
+  p.query_starts = query_starts;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = p.ws_o ? p.ws_o + static_cast<size_t>(plan.splits) * params->num_tokens * params->num_q_heads * DV : nullptr;
+  p.error_flag = error_flag;
+  p.num_seqs = params->num_seqs;
+  p.tokens = params->num_tokens;
+  p.num_q_heads = params->num_q_heads;
+  p.num_kv_heads = layout->num_kv_heads;
+  p.rep = rep;
+  p.tile_tokens = 128 / rep;
+  p.num_blocks = layout->num_blocks;
+  p.block_size = layout->block_size;
+  p.max_blocks = params->max_blocks_per_seq;
+  // rows of one copy: the largest power of two that divides blocks and key tiles
+  while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= plan.key_tile) ++p.piece_log2;
+  p.window = params->window;
+  p.splits = plan.splits;
+  p.score_scale = std::fabs(scale) * 1.4426950408889634f;
+  p.negate = scale < 0.f;
+  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  const int piece = 1 << p.piece_log2;
+  const long long pool_rows = static_cast<long long>(layout->num_blocks) * layout->num_kv_heads * layout->block_size;
+  CUtensorMap tq, tk, tv;
+  rc = encode_query_map(&tq, q, D, params->num_q_heads, params->num_tokens, q_strides, rep, p.tile_tokens);
+  if (!rc) rc = pool_tensor_map(&tk, k_pool, 2, D, pool_rows, 128, piece, true);
+  if (!rc) rc = pool_tensor_map(&tv, v_pool, 2, DV, pool_rows, 128, piece, true);
+  if (rc) return rc;
+  (void)cudaGetLastError();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device);
+  if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
+  if (plan.splits > 1) {
+    e = pkv::launch_prefill_join(p, DV, st);
+    if (e != cudaSuccess) return cuda_fail("prompt attention join launch", e);
+  }
+  return PKV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Sparse decode attention over chosen blocks (pkv_sparse.cu)
 // ---------------------------------------------------------------------------
 namespace {

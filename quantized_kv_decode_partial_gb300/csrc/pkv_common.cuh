@@ -169,6 +169,25 @@ struct RotateParams {
   int q_ctas, head_warps, table_rows;  // e4m3 pages: CTAs of query rows, warps per KV head, rows whose angles are tabled
 };
 
+// Attention of many new tokens over the pages (pkv_prefill.cuh).
+struct PrefillParams {
+  const int32_t* query_starts;  // [num_seqs + 1]
+  const int32_t* block_tables;  // [num_seqs, max_blocks]
+  const int32_t* seq_lens;      // rows held, the new ones included
+  __nv_bfloat16* out;           // [tokens, HQ, DV]
+  float* ws_o;                  // [splits][tokens * HQ][DV]
+  float* ws_ml;                 // [splits][tokens * HQ][2]
+  int32_t* error_flag;
+  int num_seqs, tokens, num_q_heads, num_kv_heads, rep;
+  int tile_tokens;              // tokens of one query tile: 128 / rep
+  int num_blocks, block_size, max_blocks;
+  int piece_log2;               // rows of one copy: a power of two that divides block_size and KT
+  int window, splits;
+  float score_scale;            // |softmax scale| * log2(e)
+  int negate;                   // the softmax scale is negative
+  unsigned long long wait_limit_ns;
+};
+
 // Upkeep of the block bounds (pkv_sparse.cu).
 struct BoundsParams {
   const void* k_pool;

@@ -88,6 +88,17 @@ cudaError_t launch_rotate(const RotateParams& p, int head_dim, int sm_count, cud
 cudaError_t launch_rotate_append(const RotateParams& p, int fmt, int head_dim, int v_head_dim, int sm_count,
                                  cudaStream_t stream);
 
+// Prompt attention (pkv_prefill.cuh): query tiles per CTA, key rows per tile, shared memory of a
+// pair of head dims. units: CTAs per KV head and split.
+struct PrefillInfo {
+  bool exists;
+  int query_tiles, key_tile, smem_bytes;
+};
+PrefillInfo prefill_info(int dk, int dv);
+cudaError_t launch_prefill_bf16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream);
+
 cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_seqs, cudaStream_t stream);
 int select_tiles(int max_blocks);  // tiles of SelectParams for a table of this width
 cudaError_t launch_select(SelectParams p, int num_seqs, int sm_count, int device, cudaStream_t stream);

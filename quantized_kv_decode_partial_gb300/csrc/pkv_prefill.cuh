@@ -1,0 +1,448 @@
+// Attention of many new tokens of each sequence over its paged cache: tcgen05 products with
+// scores, weights and outputs in tensor memory.
+//
+// A CTA takes one KV head and up to NQ tiles of 128 query rows; a tile's rows are
+// floor(128 / REP) consecutive tokens times the KV head's REP query heads, so that short
+// chunks fill tiles and every key tile serves all of them. Keys pass in tiles of KT rows.
+// One warp copies K and V tiles (TMA, one box per run of rows that lie in one block and 64
+// dims), one warp issues the products, and a warpgroup per query tile (thread = query row) turns
+// scores into weights:
+//     S = Q K^T (tensor memory) -> p = 2^(c s - c m), written over S as bf16 -> O += P V
+// with P read by the product from tensor memory and O never leaving it. The maximum m follows
+// the scores only when they exceed it by more than 2^8 in weight, so O is rescaled rarely; f32
+// sums and bf16 weights lose nothing by the factor. With two query tiles one tile's softmax runs
+// beside the other's products; with one (dims of 256), its next scores are computed meanwhile.
+//
+// Few query rows over long caches: the key tiles of each CTA's rows are split over `splits`
+// CTAs whose f32 states (O, m, l) are joined by a second kernel.
+#pragma once
+
+#include "pkv_rotate.cuh"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+// Tiles of one instantiation.
+template <int D, int DV>
+struct PrefillShape {
+  static constexpr int kQ = DV == 256 ? 1 : 2;                        // query tiles per CTA
+  static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;         // key rows per tile
+  static constexpr int kStages = D == 64 ? 4 : 2;                     // of K, and of V
+  static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
+  static constexpr int kSmem = kQ * kQBytes + kStages * (kKBytes + kVBytes) + 1024;
+  static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
+  static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+constexpr int kPrefillThreads = 384;  // two softmax warpgroups, then the product and copy warps
+constexpr int kPrefillStates = 512;   // tensor memory columns
+
+// A work unit's place: computed by every warp from the same words.
+struct PrefillUnit {
+  int head, split;
+  int first;           // first token of the unit (packed), and its tokens
+  int tokens;
+  int position;        // cache place of the first token
+  const int32_t* table;
+  bool live, valid;    // live: has tokens; valid: its sequence's lengths are
+};
+
+__device__ __forceinline__ PrefillUnit prefill_unit(const PrefillParams& p, int unit_tokens) {
+  PrefillUnit u;
+  int x = blockIdx.x;
+  u.split = x % p.splits;
+  x /= p.splits;
+  u.head = x % p.num_kv_heads;
+  // Later tiles of a sequence see more keys: they start first.
+  const int slots = gridDim.x / (p.splits * p.num_kv_heads);
+  const int slot = slots - 1 - x / p.num_kv_heads;
+  // Sequence b's units have the slots from floor(start_b / unit) + b on, as many as it can need.
+  const int b = find_last(p.num_seqs, slot,
+                          [&](int i) { return static_cast<long long>(p.query_starts[i] / unit_tokens) + i; });
+  const int start = p.query_starts[b];
+  const long long n = static_cast<long long>(p.query_starts[b + 1]) - start;
+  const long long first = (slot - (static_cast<long long>(start / unit_tokens) + b)) * unit_tokens;
+  const int len = p.seq_lens[b];
+  const bool starts_ok = start >= 0 && n >= 0 && start + n <= p.tokens;
+  u.live = starts_ok && first >= 0 && first < n;
+  u.valid = u.live && len >= n && len <= static_cast<long long>(p.max_blocks) * p.block_size;
+  u.first = u.live ? static_cast<int>(start + first) : 0;
+  u.tokens = u.live ? static_cast<int>(min(n - first, static_cast<long long>(unit_tokens))) : 0;
+  u.position = u.valid ? static_cast<int>(len - n + first) : 0;
+  u.table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  if ((!starts_ok || (u.live && !u.valid)) && threadIdx.x == 0 && p.error_flag)
+    atomicOr(p.error_flag, kDevErrBadSeqLen);
+  return u;
+}
+
+// A query row's results: bf16 outputs, or with splits its f32 state.
+struct PrefillRow {
+  bool live;
+  size_t row;  // token * HQ + head
+};
+
+// tq, tk, tv: TMA descriptors of the queries ([64 dims][head][token][run of dims]) and of the pools'
+// planes ([64 dims][row][run of dims]).
+template <int D, int DV>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+    pkv_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tq,
+                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  using T = PrefillShape<D, DV>;
+  constexpr int KT = T::KT, NS = T::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[4 * NS + 8];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, bad_blocks;
+  __shared__ uint32_t piece_bits[NS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  wait_for_prerequisite_grids();
+  const int unit_tokens = T::kQ * p.tile_tokens;
+  const PrefillUnit u = prefill_unit(p, unit_tokens);
+  if (!u.live) return;
+  const size_t all_rows = static_cast<size_t>(p.tokens) * p.num_q_heads;
+  // The unit's row i: token i / rep, query head i % rep of the KV head.
+  auto row_of = [&](int tile, int r) {
+    const int token = r / p.rep, t = tile * p.tile_tokens + token;
+    PrefillRow q;
+    q.live = token < p.tile_tokens && t < u.tokens;
+    q.row = (static_cast<size_t>(u.first) + t) * p.num_q_heads + u.head * p.rep + (r - token * p.rep);
+    return q;
+  };
+  const int tiles_q = (u.tokens + p.tile_tokens - 1) / p.tile_tokens;  // 1 .. kQ
+  // Keys that any row of the unit sees: [lo, hi).
+  const int hi = u.position + u.tokens;
+  const int lo = p.window > 0 ? max(0, u.position - p.window + 1) : 0;
+  const int tile_lo = lo / KT, tile_n = (hi + KT - 1) / KT - tile_lo;
+  const int t0 = tile_lo + static_cast<int>(static_cast<long long>(tile_n) * u.split / p.splits);
+  const int nt = u.valid ? tile_lo + static_cast<int>(static_cast<long long>(tile_n) * (u.split + 1) / p.splits) - t0 : 0;
+
+  if (nt == 0) {  // nothing to see, or a bad length: zeros
+    for (int i = threadIdx.x; i < tiles_q * 128; i += blockDim.x) {
+      const PrefillRow q = row_of(i >> 7, i & 127);
+      if (!q.live) continue;
+      if (p.splits > 1) {
+        float* ml = p.ws_ml + (u.split * all_rows + q.row) * 2;
+        ml[0] = -INFINITY;
+        ml[1] = 0.f;
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(p.out + q.row * DV);
+        for (int d = 0; d < DV / 8; ++d) o[d] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    return;
+  }
+
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t smem_k = smem + T::kQ * T::kQBytes, smem_v = smem_k + NS * T::kKBytes;
+  const uint32_t bar0 = smem_addr(bars);
+  auto k_full = [&](int s) { return bar0 + 8 * s; };
+  auto k_empty = [&](int s) { return bar0 + 8 * (NS + s); };
+  auto v_full = [&](int s) { return bar0 + 8 * (2 * NS + s); };
+  auto v_empty = [&](int s) { return bar0 + 8 * (3 * NS + s); };
+  auto s_full = [&](int s) { return bar0 + 8 * (4 * NS + s); };
+  auto p_full = [&](int s) { return bar0 + 8 * (4 * NS + 2 + s); };
+  auto o_done = [&](int s) { return bar0 + 8 * (4 * NS + 4 + s); };
+  const uint32_t q_full = bar0 + 8 * (4 * NS + 6), drained = bar0 + 8 * (4 * NS + 7);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4 * NS + 8; ++i) {
+      const bool by_threads = i == 4 * NS + 2 || i == 4 * NS + 3;  // p_full
+      mbar_init(bar0 + 8 * i, by_threads ? 128 : 1);
+    }
+    fence_barrier_init();
+    abort_flag = 0;
+    bad_blocks = 0;
+  }
+  if (warp == 8) tmem_alloc(smem_addr(&tmem_slot), kPrefillStates);
+  __syncthreads();
+  // Are all blocks of this CTA's keys in the pool? Almost always; then no tile asks again.
+  {
+    const int b0 = max(lo, t0 * KT) / p.block_size, b1 = (min(hi, (t0 + nt) * KT) - 1) / p.block_size;
+    for (int i = b0 + static_cast<int>(threadIdx.x); i <= b1; i += blockDim.x) {
+      if (static_cast<unsigned>(u.table[i]) >= static_cast<unsigned>(p.num_blocks)) {
+        bad_blocks = 1;
+        if (p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+      }
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  const bool any_bad = bad_blocks != 0;
+  const int piece = 1 << p.piece_log2, pieces = KT >> p.piece_log2;
+  const int items = nt * tiles_q;  // item i: query tile i % tiles_q, key tile t0 + i / tiles_q, score tile i & 1
+  // The pieces of key tile t that are copied, and (lane l) the pool row of piece l.
+  auto tile_pieces = [&](int t, int& row) {
+    const int key = t * KT + lane * piece;
+    bool ok = lane < pieces && key < hi && key + piece > lo;
+    row = 0;
+    if (ok) {
+      const int blk = key / p.block_size;
+      const int phys = static_cast<int>(ld_keep_u32(u.table + blk));
+      ok = static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_blocks);
+      row = ok ? (phys * p.num_kv_heads + u.head) * p.block_size + (key - blk * p.block_size) : 0;
+    }
+    return __ballot_sync(0xffffffffu, ok);
+  };
+
+  if (warp == 9) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, tiles_q * (D / 64) * p.tile_tokens * p.rep * 128);
+      for (int t = 0; t < tiles_q; ++t)
+        for (int c = 0; c < D / 64; ++c)
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+              "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem + t * T::kQBytes + c * 128 * 128),
+              "l"(reinterpret_cast<uint64_t>(&tq)), "r"(0), "r"(u.head * p.rep), "r"(u.first + t * p.tile_tokens), "r"(c),
+              "r"(q_full)
+              : "memory");
+    }
+    int row, k_tiles = 0, v_tiles = 0;  // tiles asked for
+    uint32_t bits = tile_pieces(t0, row);
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % NS;
+      int next_row = 0;
+      uint32_t next_bits = 0;
+      if (j + 1 < nt) next_bits = tile_pieces(t0 + j + 1, next_row);  // its table words arrive meanwhile
+      auto fill = [&](uint32_t full, uint32_t base, const CUtensorMap* map, int runs) {
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(bits) * runs * piece * 128);
+        __syncwarp();
+        for (int i0 = 0; i0 < pieces * runs; i0 += 32) {
+          const int i = i0 + lane;
+          const int pc = i % pieces, c = i / pieces;
+          const int y = __shfl_sync(0xffffffffu, row, pc);
+          if (i < pieces * runs && (bits >> pc & 1))
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + c * (KT * 128) + pc * piece * 128),
+                "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(c), "r"(full)
+                : "memory");
+        }
+        __syncwarp();
+      };
+      const int round = (j / NS - 1) & 1;
+      if (j >= NS && !mbar_wait_warp(k_empty(s), round, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
+      fill(k_full(s), smem_k + s * T::kKBytes, &tk, D / 64);
+      ++k_tiles;
+      if (j >= NS && !mbar_wait_warp(v_empty(s), round, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
+      if (lane == 0) piece_bits[s] = bits;
+      fill(v_full(s), smem_v + s * T::kVBytes, &tv, DV / 64);
+      ++v_tiles;
+      row = next_row;
+      bits = next_bits;
+    }
+    // Every copy lands before the CTA ends, whatever the other warps did.
+    int none = 0;
+    mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+    for (int i = max(0, k_tiles - NS); i < k_tiles; ++i)
+      mbar_wait_warp(k_full(i % NS), (i / NS) & 1, &none, p.error_flag, kWaitLimitNs);
+    for (int i = max(0, v_tiles - NS); i < v_tiles; ++i)
+      mbar_wait_warp(v_full(i % NS), (i / NS) & 1, &none, p.error_flag, kWaitLimitNs);
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ products
+    const uint32_t instr_s = umma_instr(KT, false, p.negate != 0), instr_o = umma_instr(DV, true, false);
+    bool ok = mbar_wait_warp(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
+    auto scores = [&](int i) {
+      const int q = i % tiles_q, j = i / tiles_q, s = j % NS;
+      if (q == 0) ok = ok && mbar_wait_warp(k_full(s), (j / NS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (!ok) return;
+      tmem_fence_after_sync();
+      if (lane == 0) {
+        const uint32_t a0 = smem + q * T::kQBytes, b0 = smem_k + s * T::kKBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          umma_ss(tmem + (i & 1) * KT, umma_desc(a0 + (k / 4) * (128 * 128) + (k % 4) * 32, 0),
+                  umma_desc(b0 + (k / 4) * (KT * 128) + (k % 4) * 32, 0), instr_s, k > 0);
+        umma_commit(s_full(i & 1));
+        if (q == tiles_q - 1) umma_commit(k_empty(s));
+      }
+      __syncwarp();
+    };
+    if (ok) scores(0);
+    if (ok && items > 1) scores(1);
+    for (int i = 0; ok && i < items; ++i) {
+      const int q = i % tiles_q, j = i / tiles_q, s = j % NS;
+      ok = mbar_wait_warp(p_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (ok && q == 0) {
+        ok = mbar_wait_warp(v_full(s), (j / NS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        // Rows that nobody sees have weight zero, which must meet zeros, whatever is there.
+        const int key = (t0 + j) * KT;
+        const uint32_t bits = piece_bits[s];
+        if (ok && (key < lo || key + KT > hi || any_bad)) {
+          for (int r = lane; r < KT; r += 32) {
+            if (key + r >= lo && key + r < hi && (bits >> (r >> p.piece_log2) & 1)) continue;
+            for (int c = 0; c < DV / 64; ++c)
+              for (int w = 0; w < 8; ++w)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem_v + s * T::kVBytes + c * (KT * 128) +
+                                                                             r * 128 + w * 16),
+                             "r"(0u)
+                             : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      tmem_fence_after_sync();
+      if (lane == 0) {
+        const uint32_t b0 = smem_v + s * T::kVBytes;
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          umma_ts(tmem + T::kTmemO + q * DV, tmem + (i & 1) * KT + k * 8, umma_desc(b0 + k * 2048, KT * 128), instr_o,
+                  j > 0 || k > 0);
+        umma_commit(o_done(q));
+        if (q == tiles_q - 1) umma_commit(v_empty(s));
+      }
+      __syncwarp();
+      if (i + 2 < items) scores(i + 2);
+    }
+  } else if (warp < 8 && (warp >> 2) < tiles_q) {
+    // ------------------------------------------------------------------ softmax of one query tile
+    const int q = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes
+    const PrefillRow out = row_of(q, r);
+    const int first = q * p.tile_tokens;  // the tile's first token, and its last
+    const int last = min(first + p.tile_tokens, u.tokens) - 1;
+    const int pos = u.position + min(first + r / p.rep, last);  // rows without a token go along with the last one
+    const int below = p.window > 0 ? pos - p.window : -1;       // keys at or below it are out of the window
+    const float c = p.score_scale;
+    float m = -INFINITY, l = 0.f;  // running maximum (of unscaled scores) and sum of weights
+    const uint32_t o_at = tmem + lanes + T::kTmemO + q * DV;
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      const int i = j * tiles_q + q;
+      const int key = (t0 + j) * KT;
+      ok = mbar_wait_warp(s_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (!ok) break;
+      tmem_fence_after_sync();
+      const uint32_t s_at = tmem + lanes + (i & 1) * KT;
+      // Which of the tile's keys this row sees: [v0, v1), less the pieces that were not copied.
+      const bool masked = any_bad || key + KT > u.position + first + 1 ||
+                          (p.window > 0 && key <= u.position + last - p.window);
+      const int v0 = below + 1 - key, v1 = pos + 1 - key;
+      uint32_t bits = 0xFFFFFFFFu;
+      if (any_bad) {
+        int row;
+        bits = tile_pieces(t0 + j, row);
+      }
+      auto seen = [&](int col) { return col >= v0 && col < v1 && (bits >> (col >> p.piece_log2) & 1); };
+      float mx = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < KT / 32; ++h) {
+        uint32_t s[32];
+        tmem_ld_32(s_at + h * 32, s);
+        tmem_wait_ld(s);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, seen(h * 32 + e) ? __uint_as_float(s[e]) : -INFINITY);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
+        }
+      }
+      if (j == 0) {
+        m = mx;
+      } else {
+        const float up = fmaxf(m, mx);
+        const bool rise = (up - m) * c > 8.f || (m == -INFINITY && up > m);
+        if (__any_sync(0xffffffffu, rise)) {
+          const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
+          m = up;
+          l *= by;
+          ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+          if (!ok) break;
+          tmem_fence_after_sync();
+#pragma unroll 1
+          for (int d = 0; d < DV; d += 32) {
+            uint32_t o[32];
+            tmem_ld_32(o_at + d, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+            tmem_st_32(o_at + d, o);
+          }
+        }
+      }
+      const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+      for (int h = 0; h < KT / 32; ++h) {
+        uint32_t s[32], w[16];
+        tmem_ld_32(s_at + h * 32, s);
+        tmem_wait_ld(s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x = fast_exp2(fmaf(__uint_as_float(s[e]), c, -mc)), y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), c, -mc));
+          if (masked) {
+            x = seen(h * 32 + e) ? x : 0.f;
+            y = seen(h * 32 + e + 1) ? y : 0.f;
+          }
+          l += x + y;
+          w[e / 2] = pack_bf16x2(x, y);
+        }
+        tmem_st_16(s_at + h * 16, w);  // over scores that have been read
+      }
+      tmem_wait_st();
+      // Every phase of o_done is seen before the next one's product can be issued, so that a parity
+      // stands for one phase (the last product is long done: scores two tiles on wait for it).
+      if (j > 0) ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (!ok) break;
+      tmem_fence_before_sync();
+      mbar_arrive(p_full(i & 1));
+    }
+    if (ok) ok = mbar_wait_warp(o_done(q), (nt - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+    if (ok) {
+      tmem_fence_after_sync();
+      const bool split = p.splits > 1;
+      const float inv = split ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      if (split && out.live) {
+        float* ml = p.ws_ml + (u.split * all_rows + out.row) * 2;
+        ml[0] = m * c;
+        ml[1] = l;
+      }
+#pragma unroll 1
+      for (int d = 0; d < DV; d += 32) {
+        uint32_t o[32];
+        tmem_ld_32(o_at + d, o);
+        tmem_wait_ld(o);
+        if (out.live && split) {
+          float4* to = reinterpret_cast<float4*>(p.ws_o + (u.split * all_rows + out.row) * DV + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                __uint_as_float(o[4 * e + 3]));
+        } else if (out.live) {
+          uint4* to = reinterpret_cast<uint4*>(p.out + out.row * DV + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            to[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  __syncwarp();
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    tmem_fence_after_sync();
+    if (abort_flag) {  // a wait gave up: products may still run, and tensor memory is theirs until they are done
+      int none = 0;
+      if (lane == 0) umma_commit(drained);
+      __syncwarp();
+      mbar_wait_warp(drained, 0, &none, p.error_flag, kWaitLimitNs);
+    }
+    tmem_free(tmem, kPrefillStates);
+  }
+}
+
+}  // namespace pkv

@@ -1,0 +1,146 @@
+// Prompt attention over bf16 pages, and the join of split key ranges.
+#include <atomic>
+
+#include "pkv_launch.h"
+#include "pkv_prefill.cuh"
+
+namespace pkv {
+
+namespace {
+
+struct PrefillJoinParams {
+  const float* ws_o;
+  const float* ws_ml;
+  const int32_t* query_starts;
+  __nv_bfloat16* out;
+  int num_seqs, tokens, num_q_heads, splits;
+};
+
+// One warp per output row: the states of its splits, weighted by 2^(m - max m).
+template <int DV>
+__global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_constant__ PrefillJoinParams p) {
+  wait_for_prerequisite_grids();
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const long long rows = static_cast<long long>(p.tokens) * p.num_q_heads;
+  if (row >= rows) return;
+  const int t = static_cast<int>(row / p.num_q_heads);
+  const int b = find_last(p.num_seqs, t, [&](int i) { return p.query_starts[i]; });
+  if (p.query_starts[b] > t || p.query_starts[b + 1] <= t) return;  // a row of no sequence stays as it was
+  constexpr int V = DV / 32 >= 4 ? 4 : 2;  // values a lane takes at once
+  constexpr int N = DV / (32 * V);
+  float acc[N][V] = {}, total = 0.f, top = -INFINITY;
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    const float* ml = p.ws_ml + (static_cast<size_t>(s0 + lane) * rows + row) * 2;
+    const bool have = s0 + lane < p.splits;
+    const float m = have ? ml[0] : -INFINITY, l = have ? ml[1] : 0.f;
+    float mx = m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    const float up = fmaxf(top, mx);
+    if (up == -INFINITY) continue;
+    const float by = top == -INFINITY ? 0.f : fast_exp2(top - up);
+    top = up;
+    total *= by;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[n][v] *= by;
+    const float w = l != 0.f ? fast_exp2(m - up) : 0.f;  // a split without keys has no outputs
+    float sum = w * l;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    total += sum;
+    for (int s = 0; s < min(32, p.splits - s0); ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      if (__shfl_sync(0xffffffffu, l, s) == 0.f) continue;
+      const float* o = p.ws_o + (static_cast<size_t>(s0 + s) * rows + row) * DV + lane * V;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o + n * 32 * V);
+          acc[n][0] = fmaf(ws, x.x, acc[n][0]);
+          acc[n][1] = fmaf(ws, x.y, acc[n][1]);
+          acc[n][2] = fmaf(ws, x.z, acc[n][2]);
+          acc[n][3] = fmaf(ws, x.w, acc[n][3]);
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o + n * 32 * V);
+          acc[n][0] = fmaf(ws, x.x, acc[n][0]);
+          acc[n][1] = fmaf(ws, x.y, acc[n][1]);
+        }
+      }
+    }
+  }
+  const float inv = total != 0.f ? 1.f / total : 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    __nv_bfloat16* to = p.out + row * DV + n * 32 * V + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<uint32_t*>(to + v) = pack_bf16x2(acc[n][v] * inv, acc[n][v + 1] * inv);
+  }
+}
+
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernels wait before they touch memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int DV>
+cudaError_t launch_of(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int units,
+                      cudaStream_t stream, int device) {
+  constexpr int smem = PrefillShape<D, DV>::kSmem;
+  static std::atomic<bool> ready[256];  // per device; a second thread's call sets the same attribute again
+  if (device < 0 || device >= 256 || !ready[device].load(std::memory_order_relaxed)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(pkv_prefill_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (device >= 0 && device < 256) ready[device].store(true, std::memory_order_relaxed);
+  }
+  return launch_dependent(pkv_prefill_kernel<D, DV>, dim3(units * p.num_kv_heads * p.splits), kPrefillThreads, smem, stream,
+                          p, tq, tk, tv);
+}
+
+#define PKV_PREFILL_SHAPES(X) X(64, 64) X(128, 128) X(256, 256) X(192, 128) X(256, 128) X(128, 256)
+
+}  // namespace
+
+PrefillInfo prefill_info(int dk, int dv) {
+#define X(DK_, DV_)               \
+  if (dk == DK_ && dv == DV_)     \
+    return PrefillInfo{true, PrefillShape<DK_, DV_>::kQ, PrefillShape<DK_, DV_>::KT, PrefillShape<DK_, DV_>::kSmem};
+  PKV_PREFILL_SHAPES(X)
+#undef X
+  return PrefillInfo{};
+}
+
+cudaError_t launch_prefill_bf16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, int units, cudaStream_t stream, int device) {
+#define X(DK_, DV_) \
+  if (dk == DK_ && dv == DV_) return launch_of<DK_, DV_>(p, tq, tk, tv, units, stream, device);
+  PKV_PREFILL_SHAPES(X)
+#undef X
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream) {
+  PrefillJoinParams j{p.ws_o, p.ws_ml, p.query_starts, p.out, p.num_seqs, p.tokens, p.num_q_heads, p.splits};
+  const long long rows = static_cast<long long>(p.tokens) * p.num_q_heads;
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  if (dv == 64) return launch_dependent(pkv_prefill_join_kernel<64>, grid, 128, 0, stream, j);
+  if (dv == 128) return launch_dependent(pkv_prefill_join_kernel<128>, grid, 128, 0, stream, j);
+  return launch_dependent(pkv_prefill_join_kernel<256>, grid, 128, 0, stream, j);
+}
+
+}  // namespace pkv
