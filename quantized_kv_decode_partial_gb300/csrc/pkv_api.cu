@@ -1409,7 +1409,8 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= plan.key_tile) ++p.piece_log2;
   p.window = params->window;
   p.splits = plan.splits;
-  p.score_scale = std::fabs(scale) * 1.4426950408889634f;
+  // not zero, so that a score of -infinity (a masked one) has no weight whatever the scale
+  p.score_scale = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-37f);
   p.negate = scale < 0.f;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   const int piece = 1 << p.piece_log2;

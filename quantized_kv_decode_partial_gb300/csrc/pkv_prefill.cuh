@@ -27,15 +27,23 @@ template <int D, int DV>
 struct PrefillShape {
   static constexpr int kQ = DV == 256 ? 1 : 2;                        // query tiles per CTA
   static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;         // key rows per tile
-  static constexpr int kStages = D == 64 ? 4 : 2;                     // of K, and of V
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
-  static constexpr int kSmem = kQ * kQBytes + kStages * (kKBytes + kVBytes) + 1024;
+  // Stages of K and of V: as many as fit (up to 4), K first. A K tile is asked for when the last product that
+  // read its stage is done; with two stages that is five products ahead, a copy's latency at best.
+  static constexpr int kRoom = 226 * 1024 - kQ * kQBytes;
+  static constexpr int kVS = kRoom / (kKBytes + kVBytes) > 4 ? 4 : kRoom / (kKBytes + kVBytes);
+  static constexpr int kKS = (kRoom - kVS * kVBytes) / kKBytes > 4 ? 4 : (kRoom - kVS * kVBytes) / kKBytes;
+  static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + 1024;
   static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
   static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kVS >= 2 && kKS >= 2 && kSmem <= 227 * 1024, "shared memory");
 };
 
-constexpr int kPrefillThreads = 384;  // two softmax warpgroups, then the product and copy warps
+constexpr int kPrefillThreads = 384;  // two softmax warpgroups, then one with the product and the copy warp
+// Registers: softmax threads hold a row's scores. 2 * 128 * 208 + 128 * 88 is what the block is launched
+// with, 384 * 168. (The change stands inside the branches: before them it bounds both sides' registers.)
+#define PKV_PREFILL_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 208;")
+#define PKV_PREFILL_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 88;")
 constexpr int kPrefillStates = 512;   // tensor memory columns
 
 // A work unit's place: computed by every warp from the same words.
@@ -76,6 +84,82 @@ __device__ __forceinline__ PrefillUnit prefill_unit(const PrefillParams& p, int 
   return u;
 }
 
+// Pairs of f32 values in one register pair: packed arithmetic, each lane of it rounded as the scalar one.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// A row's KT scores.
+template <int KT>
+__device__ __forceinline__ void tmem_ld_tile(uint32_t addr, float (&s)[KT]) {
+  uint32_t v[KT / 32][32];
+#pragma unroll
+  for (int h = 0; h < KT / 32; ++h) tmem_ld_32(addr + 32 * h, v[h]);
+#pragma unroll
+  for (int h = 0; h < KT / 32; ++h) {
+    tmem_wait_ld(v[h]);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[32 * h + e] = __uint_as_float(v[h][e]);
+  }
+}
+
+template <int KT>
+__device__ __forceinline__ float row_max(const float (&s)[KT]) {
+  float top[8];
+#pragma unroll
+  for (int n = 0; n < 8; ++n) top[n] = fmaxf(s[n], s[8 + n]);
+#pragma unroll
+  for (int e = 16; e < KT; e += 16)
+#pragma unroll
+    for (int n = 0; n < 8; ++n) top[n] = max3(top[n], s[e + n], s[e + 8 + n]);
+  return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+}
+
+// A row's weights 2^(c s - c m) as bf16 pairs, their f32 sums added to `sums`; returns the largest score.
+template <int KT>
+__device__ __forceinline__ float weights(const float (&s)[KT], float c, float m, uint64_t (&sums)[2], uint32_t (&w)[KT / 2]) {
+  const float mc = m == -INFINITY ? 0.f : m * c;
+  const uint64_t cc = pair(c, c), mm = pair(-mc, -mc);
+#pragma unroll
+  for (int e = 0; e < KT / 2; ++e) {
+    float x, y;
+    unpair(fma2(pair(s[2 * e], s[2 * e + 1]), cc, mm), x, y);
+    x = fast_exp2(x);
+    y = fast_exp2(y);
+    sums[e & 1] = add2(sums[e & 1], pair(x, y));
+    w[e] = pack_bf16x2(x, y);
+  }
+  return row_max<KT>(s);
+}
+
 // A query row's results: bf16 outputs, or with splits its f32 state.
 struct PrefillRow {
   bool live;
@@ -89,12 +173,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     pkv_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using T = PrefillShape<D, DV>;
-  constexpr int KT = T::KT, NS = T::kStages;
+  constexpr int KT = T::KT, KS = T::kKS, VS = T::kVS;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * NS + 8];
+  __shared__ __align__(8) uint64_t bars[2 * KS + 2 * VS + 8];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, bad_blocks;
-  __shared__ uint32_t piece_bits[NS];
+  __shared__ uint32_t piece_bits[VS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   wait_for_prerequisite_grids();
@@ -135,21 +219,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   }
 
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t smem_k = smem + T::kQ * T::kQBytes, smem_v = smem_k + NS * T::kKBytes;
+  const uint32_t smem_k = smem + T::kQ * T::kQBytes, smem_v = smem_k + KS * T::kKBytes;
   const uint32_t bar0 = smem_addr(bars);
   auto k_full = [&](int s) { return bar0 + 8 * s; };
-  auto k_empty = [&](int s) { return bar0 + 8 * (NS + s); };
-  auto v_full = [&](int s) { return bar0 + 8 * (2 * NS + s); };
-  auto v_empty = [&](int s) { return bar0 + 8 * (3 * NS + s); };
-  auto s_full = [&](int s) { return bar0 + 8 * (4 * NS + s); };
-  auto p_full = [&](int s) { return bar0 + 8 * (4 * NS + 2 + s); };
-  auto o_done = [&](int s) { return bar0 + 8 * (4 * NS + 4 + s); };
-  const uint32_t q_full = bar0 + 8 * (4 * NS + 6), drained = bar0 + 8 * (4 * NS + 7);
+  auto k_empty = [&](int s) { return bar0 + 8 * (KS + s); };
+  auto v_full = [&](int s) { return bar0 + 8 * (2 * KS + s); };
+  auto v_empty = [&](int s) { return bar0 + 8 * (2 * KS + VS + s); };
+  constexpr int kRest = 2 * KS + 2 * VS;
+  auto s_full = [&](int s) { return bar0 + 8 * (kRest + s); };
+  auto p_full = [&](int s) { return bar0 + 8 * (kRest + 2 + s); };
+  auto o_done = [&](int s) { return bar0 + 8 * (kRest + 4 + s); };
+  const uint32_t q_full = bar0 + 8 * (kRest + 6), drained = bar0 + 8 * (kRest + 7);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * NS + 8; ++i) {
-      const bool by_threads = i == 4 * NS + 2 || i == 4 * NS + 3;  // p_full
-      mbar_init(bar0 + 8 * i, by_threads ? 128 : 1);
+    for (int i = 0; i < kRest + 8; ++i) {
+      const bool by_warps = i == kRest + 2 || i == kRest + 3;  // p_full: the four warps of a query tile
+      mbar_init(bar0 + 8 * i, by_warps ? 4 : 1);
     }
     fence_barrier_init();
     abort_flag = 0;
@@ -188,9 +273,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     return __ballot_sync(0xffffffffu, ok);
   };
 
-  if (warp == 9) {
-    // ------------------------------------------------------------------ copies
-    if (lane == 0) {
+  if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------------ copies: Q and K, and V
+    PKV_PREFILL_FEWER_REGISTERS();
+    const bool is_k = warp == 9;
+    if (is_k && lane == 0) {
       mbar_arrive_expect_tx(q_full, tiles_q * (D / 64) * p.tile_tokens * p.rep * 128);
       for (int t = 0; t < tiles_q; ++t)
         for (int c = 0; c < D / 64; ++c)
@@ -201,78 +288,87 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               "r"(q_full)
               : "memory");
     }
-    int row, k_tiles = 0, v_tiles = 0;  // tiles asked for
+    const int stages = is_k ? KS : VS, runs = is_k ? D / 64 : DV / 64, bytes = is_k ? T::kKBytes : T::kVBytes;
+    const uint32_t base = is_k ? smem_k : smem_v, full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
+    const uint64_t map = reinterpret_cast<uint64_t>(is_k ? &tk : &tv);
+    int row, asked = 0;
     uint32_t bits = tile_pieces(t0, row);
     for (int j = 0; j < nt; ++j) {
-      const int s = j % NS;
+      const int s = j % stages;
       int next_row = 0;
       uint32_t next_bits = 0;
-      if (j + 1 < nt) next_bits = tile_pieces(t0 + j + 1, next_row);  // its table words arrive meanwhile
-      auto fill = [&](uint32_t full, uint32_t base, const CUtensorMap* map, int runs) {
-        if (lane == 0) mbar_arrive_expect_tx(full, __popc(bits) * runs * piece * 128);
-        __syncwarp();
-        for (int i0 = 0; i0 < pieces * runs; i0 += 32) {
-          const int i = i0 + lane;
-          const int pc = i % pieces, c = i / pieces;
-          const int y = __shfl_sync(0xffffffffu, row, pc);
-          if (i < pieces * runs && (bits >> pc & 1))
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + c * (KT * 128) + pc * piece * 128),
-                "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(c), "r"(full)
-                : "memory");
-        }
-        __syncwarp();
-      };
-      const int round = (j / NS - 1) & 1;
-      if (j >= NS && !mbar_wait_warp(k_empty(s), round, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
-      fill(k_full(s), smem_k + s * T::kKBytes, &tk, D / 64);
-      ++k_tiles;
-      if (j >= NS && !mbar_wait_warp(v_empty(s), round, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
-      if (lane == 0) piece_bits[s] = bits;
-      fill(v_full(s), smem_v + s * T::kVBytes, &tv, DV / 64);
-      ++v_tiles;
+      if (j + 1 < nt) next_bits = tile_pieces(t0 + j + 1, next_row);  // before the wait: its table words take a while
+      if (j >= stages && !mbar_wait_warp(empty0 + 8 * s, (j / stages - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns))
+        break;
+      if (lane == 0) {
+        if (!is_k) piece_bits[s] = bits;
+        mbar_arrive_expect_tx(full0 + 8 * s, __popc(bits) * runs * piece * 128);
+      }
+      __syncwarp();
+      for (int i0 = 0; i0 < pieces * runs; i0 += 32) {
+        const int i = i0 + lane;
+        const int pc = i % pieces, c = i / pieces;
+        const int y = __shfl_sync(0xffffffffu, row, pc);
+        if (i < pieces * runs && (bits >> pc & 1))
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+              "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + s * bytes + c * (KT * 128) + pc * piece * 128),
+              "l"(map), "r"(0), "r"(y), "r"(c), "r"(full0 + 8 * s)
+              : "memory");
+      }
+      __syncwarp();
+      ++asked;
       row = next_row;
       bits = next_bits;
     }
     // Every copy lands before the CTA ends, whatever the other warps did.
     int none = 0;
-    mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
-    for (int i = max(0, k_tiles - NS); i < k_tiles; ++i)
-      mbar_wait_warp(k_full(i % NS), (i / NS) & 1, &none, p.error_flag, kWaitLimitNs);
-    for (int i = max(0, v_tiles - NS); i < v_tiles; ++i)
-      mbar_wait_warp(v_full(i % NS), (i / NS) & 1, &none, p.error_flag, kWaitLimitNs);
+    if (is_k) mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+    for (int i = max(0, asked - stages); i < asked; ++i)
+      mbar_wait_warp(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
   } else if (warp == 8) {
     // ------------------------------------------------------------------ products
+    PKV_PREFILL_FEWER_REGISTERS();
+    const uint32_t leader = elect_lane(), base = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t instr_s = umma_instr(KT, false, p.negate != 0), instr_o = umma_instr(DV, true, false);
     bool ok = mbar_wait_warp(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
-    auto scores = [&](int i) {
-      const int q = i % tiles_q, j = i / tiles_q, s = j % NS;
-      if (q == 0) ok = ok && mbar_wait_warp(k_full(s), (j / NS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+    // Item i's query tile and key tile are counted along; a stage's index and parity follow its ring.
+    struct Place {
+      int q, tile, stage, parity;
+    } sp{0, 0, 0, 0}, op{0, 0, 0, 0};  // of the scores and of the outputs that come next
+    auto next = [&](Place& x, int stages) {
+      if (++x.q < tiles_q) return;
+      x.q = 0;
+      ++x.tile;
+      if (++x.stage == stages) {
+        x.stage = 0;
+        x.parity ^= 1;
+      }
+    };
+    auto scores = [&](int slot) {
+      const int s = sp.stage;
+      if (sp.q == 0) ok = mbar_wait_warp(k_full(s), sp.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) return;
       tmem_fence_after_sync();
-      if (lane == 0) {
-        const uint32_t a0 = smem + q * T::kQBytes, b0 = smem_k + s * T::kKBytes;
+      const uint64_t a0 = umma_desc(smem + sp.q * T::kQBytes, 0), b0 = umma_desc(smem_k + s * T::kKBytes, 0);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_ss(tmem + (i & 1) * KT, umma_desc(a0 + (k / 4) * (128 * 128) + (k % 4) * 32, 0),
-                  umma_desc(b0 + (k / 4) * (KT * 128) + (k % 4) * 32, 0), instr_s, k > 0);
-        umma_commit(s_full(i & 1));
-        if (q == tiles_q - 1) umma_commit(k_empty(s));
-      }
-      __syncwarp();
+      for (int k = 0; k < D / 16; ++k)
+        umma_ss(leader, base + slot * KT, a0 + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                b0 + ((k / 4) * (KT * 128) + (k % 4) * 32) / 16, instr_s, k > 0);
+      umma_commit(leader, s_full(slot));
+      if (sp.q == tiles_q - 1) umma_commit(leader, k_empty(s));
+      next(sp, KS);
     };
     if (ok) scores(0);
     if (ok && items > 1) scores(1);
     for (int i = 0; ok && i < items; ++i) {
-      const int q = i % tiles_q, j = i / tiles_q, s = j % NS;
-      ok = mbar_wait_warp(p_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
-      if (ok && q == 0) {
-        ok = mbar_wait_warp(v_full(s), (j / NS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      const int s = op.stage, slot = i & 1;
+      if (op.q == 0) {
+        ok = mbar_wait_warp(v_full(s), op.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
         // Rows that nobody sees have weight zero, which must meet zeros, whatever is there.
-        const int key = (t0 + j) * KT;
-        const uint32_t bits = piece_bits[s];
+        const int key = (t0 + op.tile) * KT;
         if (ok && (key < lo || key + KT > hi || any_bad)) {
+          const uint32_t bits = piece_bits[s];
           for (int r = lane; r < KT; r += 32) {
             if (key + r >= lo && key + r < hi && (bits >> (r >> p.piece_log2) & 1)) continue;
             for (int c = 0; c < DV / 64; ++c)
@@ -286,22 +382,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           __syncwarp();
         }
       }
+      ok = ok && mbar_wait_warp(p_full(slot), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) break;
       tmem_fence_after_sync();
-      if (lane == 0) {
-        const uint32_t b0 = smem_v + s * T::kVBytes;
+      const uint64_t b0 = umma_desc(smem_v + s * T::kVBytes, KT * 128);
+      const uint32_t o = base + T::kTmemO + op.q * DV, w = base + slot * KT;
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          umma_ts(tmem + T::kTmemO + q * DV, tmem + (i & 1) * KT + k * 8, umma_desc(b0 + k * 2048, KT * 128), instr_o,
-                  j > 0 || k > 0);
-        umma_commit(o_done(q));
-        if (q == tiles_q - 1) umma_commit(v_empty(s));
-      }
-      __syncwarp();
-      if (i + 2 < items) scores(i + 2);
+      for (int k = 0; k < KT / 16; ++k) umma_ts(leader, o, w + k * 8, b0 + k * 2048 / 16, instr_o, op.tile > 0 || k > 0);
+      umma_commit(leader, o_done(op.q));
+      if (op.q == tiles_q - 1) umma_commit(leader, v_empty(s));
+      next(op, VS);
+      // Into the weights' columns, which the product before reads: one thread's products run in order.
+      if (i + 2 < items) scores(slot);
     }
   } else if (warp < 8 && (warp >> 2) < tiles_q) {
     // ------------------------------------------------------------------ softmax of one query tile
+    PKV_PREFILL_MORE_REGISTERS();
     const int q = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes
     const PrefillRow out = row_of(q, r);
@@ -310,7 +406,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     const int pos = u.position + min(first + r / p.rep, last);  // rows without a token go along with the last one
     const int below = p.window > 0 ? pos - p.window : -1;       // keys at or below it are out of the window
     const float c = p.score_scale;
-    float m = -INFINITY, l = 0.f;  // running maximum (of unscaled scores) and sum of weights
+    float m = -INFINITY;          // running maximum of the unscaled scores
+    uint64_t l[2] = {0ull, 0ull};  // sums of weights, two pairs
     const uint32_t o_at = tmem + lanes + T::kTmemO + q * DV;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -320,88 +417,81 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if (!ok) break;
       tmem_fence_after_sync();
       const uint32_t s_at = tmem + lanes + (i & 1) * KT;
+      float s[KT];
+      tmem_ld_tile<KT>(s_at, s);
       // Which of the tile's keys this row sees: [v0, v1), less the pieces that were not copied.
       const bool masked = any_bad || key + KT > u.position + first + 1 ||
                           (p.window > 0 && key <= u.position + last - p.window);
-      const int v0 = below + 1 - key, v1 = pos + 1 - key;
-      uint32_t bits = 0xFFFFFFFFu;
-      if (any_bad) {
-        int row;
-        bits = tile_pieces(t0 + j, row);
-      }
-      auto seen = [&](int col) { return col >= v0 && col < v1 && (bits >> (col >> p.piece_log2) & 1); };
-      float mx = -INFINITY;
+      if (masked) {
+        const int v0 = below + 1 - key, v1 = pos + 1 - key;
+        uint32_t bits = 0xFFFFFFFFu;
+        if (any_bad) {
+          int row;
+          bits = tile_pieces(t0 + j, row);
+        }
 #pragma unroll
-      for (int h = 0; h < KT / 32; ++h) {
-        uint32_t s[32];
-        tmem_ld_32(s_at + h * 32, s);
-        tmem_wait_ld(s);
-        if (masked) {
+        for (int h = 0; h < KT / 32; ++h) {
+          uint32_t seen = low_bits(v1 - 32 * h) & ~low_bits(v0 - 32 * h);
+          if (any_bad)
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> ((32 * h + e) >> p.piece_log2) & 1)) seen &= ~(1u << e);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, seen(h * 32 + e) ? __uint_as_float(s[e]) : -INFINITY);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
+          for (int e = 0; e < 32; ++e) s[32 * h + e] = (seen >> e & 1) ? s[32 * h + e] : -INFINITY;
         }
       }
-      if (j == 0) {
-        m = mx;
-      } else {
-        const float up = fmaxf(m, mx);
-        const bool rise = (up - m) * c > 8.f || (m == -INFINITY && up > m);
-        if (__any_sync(0xffffffffu, rise)) {
-          const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
-          m = up;
-          l *= by;
-          ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
-          if (!ok) break;
-          tmem_fence_after_sync();
+      // Weights by the maximum so far, while the tile's own is found beside them; where that one is more
+      // than 2^8 above, the outputs are rescaled and the weights computed again. The first tile waits for its
+      // maximum.
+      if (j == 0) m = row_max<KT>(s);
+      uint64_t sums[2] = {l[0], l[1]};
+      uint32_t w[KT / 2];
+      float mx = weights<KT>(s, c, m, sums, w);
+      const float up = fmaxf(m, mx);
+      if (j > 0 && __any_sync(0xffffffffu, (up - m) * c > 8.f || (m == -INFINITY && up > m))) {
+        const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
+        m = up;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) sums[n] = mul2(l[n], pair(by, by));
+        weights<KT>(s, c, m, sums, w);
+        ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        if (!ok) break;
+        tmem_fence_after_sync();
 #pragma unroll 1
-          for (int d = 0; d < DV; d += 32) {
-            uint32_t o[32];
-            tmem_ld_32(o_at + d, o);
-            tmem_wait_ld(o);
+        for (int d = 0; d < DV; d += 32) {
+          uint32_t o[32];
+          tmem_ld_32(o_at + d, o);
+          tmem_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-            tmem_st_32(o_at + d, o);
-          }
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+          tmem_st_32(o_at + d, o);
         }
       }
-      const float mc = m == -INFINITY ? 0.f : m * c;
+      l[0] = sums[0];
+      l[1] = sums[1];
 #pragma unroll
-      for (int h = 0; h < KT / 32; ++h) {
-        uint32_t s[32], w[16];
-        tmem_ld_32(s_at + h * 32, s);
-        tmem_wait_ld(s);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x = fast_exp2(fmaf(__uint_as_float(s[e]), c, -mc)), y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), c, -mc));
-          if (masked) {
-            x = seen(h * 32 + e) ? x : 0.f;
-            y = seen(h * 32 + e + 1) ? y : 0.f;
-          }
-          l += x + y;
-          w[e / 2] = pack_bf16x2(x, y);
-        }
-        tmem_st_16(s_at + h * 16, w);  // over scores that have been read
-      }
+      for (int h = 0; h < KT / 64; ++h) tmem_st_32(s_at + h * 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32 * h));  // over the scores
       tmem_wait_st();
-      // Every phase of o_done is seen before the next one's product can be issued, so that a parity
-      // stands for one phase (the last product is long done: scores two tiles on wait for it).
-      if (j > 0) ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      // Every phase of o_done is over before the next one's product can be issued, so that a parity
+      // stands for one phase. With two query tiles this tile's scores came after that product.
+      if (j > 0 && tiles_q == 1) ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) break;
       tmem_fence_before_sync();
-      mbar_arrive(p_full(i & 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(i & 1));
     }
     if (ok) ok = mbar_wait_warp(o_done(q), (nt - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
     if (ok) {
       tmem_fence_after_sync();
       const bool split = p.splits > 1;
-      const float inv = split ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      float l0, l1, l2, l3;
+      unpair(l[0], l0, l1);
+      unpair(l[1], l2, l3);
+      const float sum = (l0 + l1) + (l2 + l3);
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
       if (split && out.live) {
         float* ml = p.ws_ml + (u.split * all_rows + out.row) * 2;
         ml[0] = m * c;
-        ml[1] = l;
+        ml[1] = sum;
       }
 #pragma unroll 1
       for (int d = 0; d < DV; d += 32) {
@@ -428,6 +518,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         __syncwarp();
       }
     }
+  } else if (warp >= 8) {
+    PKV_PREFILL_FEWER_REGISTERS();  // the rest of that warpgroup
   }
 
   __syncwarp();
@@ -437,8 +529,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     tmem_fence_after_sync();
     if (abort_flag) {  // a wait gave up: products may still run, and tensor memory is theirs until they are done
       int none = 0;
-      if (lane == 0) umma_commit(drained);
-      __syncwarp();
+      umma_commit(elect_lane(), drained);  // the lane that issued the products
       mbar_wait_warp(drained, 0, &none, p.error_flag, kWaitLimitNs);
     }
     tmem_free(tmem, kPrefillStates);

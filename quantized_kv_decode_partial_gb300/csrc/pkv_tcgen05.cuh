@@ -89,27 +89,49 @@ __device__ __forceinline__ constexpr uint32_t umma_instr(int n, bool b_columns, 
          static_cast<uint32_t>(n >> 3) << 17 | 8u << 24;
 }
 
-// D (TMEM) = A B^T + (accumulate ? D : 0) over 16 contracted values; issued by one thread.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
+// Whether this lane issues for its warp, which is converged.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t is;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
+// D (TMEM) = A B^T + (accumulate ? D : 0) over 16 contracted values. Called by a whole converged warp and
+// issued by the lane with `leader`: operands that the compiler sees to be the same in all lanes stay in uniform
+// registers, where the instruction wants them (behind a branch on the lane each would be moved there first).
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(accumulate))
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
       : "memory");
 }
 // The same with A in tensor memory: two 16-bit values per column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t instr,
+                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(accumulate))
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
       : "memory");
 }
 // The mbarrier gets one arrival once every product this thread has issued is done.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void umma_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
 }
 
 }  // namespace pkv
