@@ -28,6 +28,9 @@ SOURCES = [
     "pkv_append_blocks.cu",
     "pkv_rotate.cu",
     "pkv_prefill_bf16.cu",
+    "pkv_prefill_u4.cu",
+    "pkv_prefill_u8.cu",
+    "pkv_prefill_e4m3.cu",
     "pkv_sparse.cu",
     "pkv_partial_bf16.cu",
     "pkv_partial_bf16_cc.cu",

@@ -417,7 +417,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // of a plane is one TMA copy whatever its width.
 // The box is box_rows rows of every segment of a row (one copy per chunk), or with
 // one_segment, of a single segment (blocks smaller than a chunk: one copy per block piece
-// and segment).
+// and segment). box_row_bytes = kWholeRows: a 2-D view, boxes of box_rows whole rows (of at most
+// 256 bytes), as they lie.
+constexpr int kWholeRows = 0;
+
 int encode_pool_tensor_map(CUtensorMap* map, const void* base, int elem_bytes, long long row_elems, long long rows,
                            int box_row_bytes, int box_rows, bool one_segment) {
   auto encode = tensor_map_encoder();
@@ -427,6 +430,18 @@ int encode_pool_tensor_map(CUtensorMap* map, const void* base, int elem_bytes, l
   }
   const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const long long row_bytes = row_elems * elem_bytes;
+  if (box_row_bytes == kWholeRows) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_elems), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(row_elems), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = encode(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return PKV_OK;
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return PKV_ERR_CUDA;
+  }
   const long long segments = row_bytes / box_row_bytes;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(box_row_bytes / elem_bytes), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(segments)};
@@ -1250,6 +1265,17 @@ int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* ro
 // ---------------------------------------------------------------------------
 namespace {
 
+pkv::PrefillInfo prefill_info(const pkv_pool_layout* L) {
+  const int dk = L->head_dim, dv = v_dim(L);
+  switch (format_of(L)) {
+    case 16: return pkv::prefill_info_bf16(dk, dv);
+    case 4: return pkv::prefill_info_u4(dk, dv);
+    case 8: return pkv::prefill_info_u8(dk, dv);
+    case pkv::kFmtE4m3: return pkv::prefill_info_e4m3(dk, dv);
+    default: return pkv::PrefillInfo{};
+  }
+}
+
 int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
   const int rc = check_layout(L);
   if (rc) return rc;
@@ -1261,7 +1287,7 @@ int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
   if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   if (static_cast<long long>(P->num_tokens) * P->num_q_heads >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   if (P->num_q_heads / L->num_kv_heads > 64) return PKV_ERR_UNSUPPORTED_SHAPE;
-  if (format_of(L) != 16 || !pkv::prefill_info(L->head_dim, v_dim(L)).exists) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (!prefill_info(L).exists) return PKV_ERR_UNSUPPORTED_SHAPE;
   return PKV_OK;
 }
 
@@ -1291,7 +1317,7 @@ int prefill_splits(const pkv_pool_layout* L, const pkv_prefill_params* P, long l
 }
 
 int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_count, pkv_prefill_plan* plan) {
-  const pkv::PrefillInfo info = pkv::prefill_info(L->head_dim, v_dim(L));
+  const pkv::PrefillInfo info = prefill_info(L);
   const int rep = P->num_q_heads / L->num_kv_heads;
   pkv_prefill_plan r{};
   r.unit_tokens = info.query_tiles * (128 / rep);
@@ -1405,8 +1431,9 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   p.num_blocks = layout->num_blocks;
   p.block_size = layout->block_size;
   p.max_blocks = params->max_blocks_per_seq;
-  // rows of one copy: the largest power of two that divides blocks and key tiles
-  while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= plan.key_tile) ++p.piece_log2;
+  // rows of one copy: the largest power of two that divides blocks and key tiles (codes come in half tiles)
+  const int most = layout->bits == 16 ? plan.key_tile : plan.key_tile / 2;
+  while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= most) ++p.piece_log2;
   p.window = params->window;
   p.splits = plan.splits;
   // not zero, so that a score of -infinity (a masked one) has no weight whatever the scale
@@ -1417,12 +1444,34 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   const long long pool_rows = static_cast<long long>(layout->num_blocks) * layout->num_kv_heads * layout->block_size;
   CUtensorMap tq, tk, tv;
   rc = encode_query_map(&tq, q, D, params->num_q_heads, params->num_tokens, q_strides, rep, p.tile_tokens);
-  if (!rc) rc = pool_tensor_map(&tk, k_pool, 2, D, pool_rows, 128, piece, true);
-  if (!rc) rc = pool_tensor_map(&tv, v_pool, 2, DV, pool_rows, 128, piece, true);
+  if (layout->bits == 16) {
+    if (!rc) rc = pool_tensor_map(&tk, k_pool, 2, D, pool_rows, 128, piece, true);
+    if (!rc) rc = pool_tensor_map(&tv, v_pool, 2, DV, pool_rows, 128, piece, true);
+  } else {
+    if (!rc) rc = pool_tensor_map(&tk, k_pool, 1, D * layout->bits / 8, pool_rows, kWholeRows, piece, false);
+    if (!rc) rc = pool_tensor_map(&tv, v_pool, 1, DV * layout->bits / 8, pool_rows, kWholeRows, piece, false);
+  }
   if (rc) return rc;
+  const bool block = block_scaled(layout);
+  auto planes = [&](const void* scales, const void* biases) {
+    pkv::PrefillPlanes x{};
+    if (block) {
+      x.block_scales = static_cast<const float*>(scales);
+    } else {
+      x.scales = static_cast<const __nv_bfloat16*>(scales);
+      x.biases = static_cast<const __nv_bfloat16*>(biases);
+    }
+    return x;
+  };
+  p.k_planes = planes(k_scales, k_biases);
+  p.v_planes = planes(v_scales, v_biases);
   (void)cudaGetLastError();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device);
+  const int fmt = format_of(layout);
+  cudaError_t e = fmt == 16  ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
+                  : fmt == 4 ? pkv::launch_prefill_u4(D, DV, p, tq, tk, tv, plan.units, st, device)
+                  : fmt == 8 ? pkv::launch_prefill_u8(D, DV, p, tq, tk, tv, plan.units, st, device)
+                             : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
   if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
   if (plan.splits > 1) {
     e = pkv::launch_prefill_join(p, DV, st);

@@ -170,7 +170,14 @@ struct RotateParams {
 };
 
 // Attention of many new tokens over the pages (pkv_prefill.cuh).
+struct PrefillPlanes {
+  const __nv_bfloat16* scales;  // [NB, HK, BS, width/64]   (affine pages)
+  const __nv_bfloat16* biases;
+  const float* block_scales;    // [NB, HK]   (e4m3 pages)
+};
+
 struct PrefillParams {
+  PrefillPlanes k_planes, v_planes;
   const int32_t* query_starts;  // [num_seqs + 1]
   const int32_t* block_tables;  // [num_seqs, max_blocks]
   const int32_t* seq_lens;      // rows held, the new ones included

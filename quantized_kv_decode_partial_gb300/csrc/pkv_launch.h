@@ -94,8 +94,17 @@ struct PrefillInfo {
   bool exists;
   int query_tiles, key_tile, smem_bytes;
 };
-PrefillInfo prefill_info(int dk, int dv);
+PrefillInfo prefill_info_bf16(int dk, int dv);
+PrefillInfo prefill_info_u4(int dk, int dv);
+PrefillInfo prefill_info_u8(int dk, int dv);
+PrefillInfo prefill_info_e4m3(int dk, int dv);
 cudaError_t launch_prefill_bf16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_u4(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_u8(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_e4m3(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int units, cudaStream_t stream, int device);
 cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream);
 

@@ -22,18 +22,24 @@
 
 namespace pkv {
 
-// Tiles of one instantiation.
-template <int D, int DV>
+// Tiles of one instantiation. FMT: the page format (16, 4, 8 or kFmtE4m3).
+template <int D, int DV, int FMT>
 struct PrefillShape {
-  static constexpr int kQ = DV == 256 ? 1 : 2;                        // query tiles per CTA
-  static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;         // key rows per tile
+  static constexpr bool kCodes = FMT != 16;
+  // Query tiles per CTA: two where tensor and shared memory hold both.
+  static constexpr int kQ = DV == 256 || (kCodes && D == 256) ? 1 : 2;
+  static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;  // key rows per tile
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
+  // Pages of codes come in through a ring of half tiles, which three warps turn into bf16.
+  static constexpr int kRawSlots = kCodes ? 4 : 0;
+  static constexpr int kKRow = FMT == 4 ? D / 2 : D, kVRow = FMT == 4 ? DV / 2 : DV;  // bytes of a row of codes
+  static constexpr int kRawBytes = KT / 2 * (kKRow > kVRow ? kKRow : kVRow);
   // Stages of K and of V: as many as fit (up to 4), K first. A K tile is asked for when the last product that
   // read its stage is done; with two stages that is five products ahead, a copy's latency at best.
-  static constexpr int kRoom = 226 * 1024 - kQ * kQBytes;
+  static constexpr int kRoom = 226 * 1024 - kQ * kQBytes - kRawSlots * kRawBytes;
   static constexpr int kVS = kRoom / (kKBytes + kVBytes) > 4 ? 4 : kRoom / (kKBytes + kVBytes);
   static constexpr int kKS = (kRoom - kVS * kVBytes) / kKBytes > 4 ? 4 : (kRoom - kVS * kVBytes) / kKBytes;
-  static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + 1024;
+  static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + kRawSlots * kRawBytes + 1024;
   static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
   static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
   static_assert(kVS >= 2 && kKS >= 2 && kSmem <= 227 * 1024, "shared memory");
@@ -160,6 +166,118 @@ __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m,
   return row_max<KT>(s);
 }
 
+// Sixteen codes of a row as bf16 pairs: scale * code (+ bias), in f32, rounded once.
+template <int FMT>
+__device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float bias, uint32_t (&out)[8]) {
+  if constexpr (FMT == kFmtE4m3) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16x2(w[i], lo, hi);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      out[2 * i] = pack_bf16x2(a.x * scale, a.y * scale);
+      out[2 * i + 1] = pack_bf16x2(b.x * scale, b.y * scale);
+    }
+  } else {
+    // codes as halves: 1024 + code has the code in its last bits
+    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f);
+    auto floats = [&](uint32_t bits) {
+      return __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&bits), k1024));
+    };
+    if constexpr (FMT == 8) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = floats(__byte_perm(w[i], 0x64646464u, 0x4140)), b = floats(__byte_perm(w[i], 0x64646464u, 0x4342));
+        out[2 * i] = pack_bf16x2(fmaf(a.x, scale, bias), fmaf(a.y, scale, bias));
+        out[2 * i + 1] = pack_bf16x2(fmaf(b.x, scale, bias), fmaf(b.y, scale, bias));
+      }
+    } else {
+      const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 n[4];  // codes k and k + 4
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n[k] = floats((w[i] >> (4 * k) & 0x000F000Fu) | 0x64006400u);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          out[4 * i + k] = pack_bf16x2(fmaf(n[2 * k].x, scale, bias), fmaf(n[2 * k + 1].x, scale, bias));
+          out[4 * i + 2 + k] = pack_bf16x2(fmaf(n[2 * k].y, scale, bias), fmaf(n[2 * k + 1].y, scale, bias));
+        }
+      }
+    }
+  }
+}
+
+// One warp's third of half a tile of codes: rows [half, half + KT/2) of the tile, 16 values a lane at a time. Rows
+// outside [lo, hi) and those of pieces without their bit become zeros. row: lane l's, the pool row of piece l.
+// ready(): waits for the codes and for the place they go to.
+template <int D, int FMT, int KT, typename Ready>
+__device__ __forceinline__ bool convert_half(uint32_t to, uint32_t from, const PrefillPlanes& planes, int part, int key, int half,
+                                             int lo, int hi, uint32_t bits, int row, const PrefillParams& p,
+                                             const Ready& ready) {
+  constexpr int kPerRow = D / 16, kChunks = KT / 2 * kPerRow, kRounds = (kChunks + 95) / 96;
+  const int lane = threadIdx.x & 31;
+  float scale[kRounds], bias[kRounds];
+  if constexpr (FMT == kFmtE4m3) {
+    const float mine = bits >> lane & 1 ? planes.block_scales[row / p.block_size] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int r = half + (i * 96 + part * 32 + lane) / kPerRow;
+      scale[i] = __shfl_sync(0xffffffffu, mine, (r >> p.piece_log2) & 31);
+      bias[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int c = i * 96 + part * 32 + lane, r = half + c / kPerRow, pc = r >> p.piece_log2;
+      const int first = __shfl_sync(0xffffffffu, row, pc & 31);
+      scale[i] = bias[i] = 0.f;
+      if (c < kChunks && (bits >> (pc & 31) & 1)) {
+        const size_t at = (static_cast<size_t>(first) + (r - (pc << p.piece_log2))) * (D / 64) + c % kPerRow / 4;
+        scale[i] = __bfloat162float(planes.scales[at]);
+        bias[i] = __bfloat162float(planes.biases[at]);
+      }
+    }
+  }
+  if (!ready()) return false;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int c = i * 96 + part * 32 + lane;
+    if (c >= kChunks) break;
+    const int r = half + c / kPerRow, col = c % kPerRow;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (FMT == 4) {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from + c * 8) : "memory");
+    } else {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(from + c * 16)
+                   : "memory");
+    }
+    uint32_t w[8];
+    codes_to_bf16<FMT>(v, scale[i], bias[i], w);
+    if (!(key + r >= lo && key + r < hi && (bits >> ((r >> p.piece_log2) & 31) & 1))) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = 0u;
+    }
+    // 16-byte places of the swizzled row; odd runs of 64 dims write their second one first, so that eight
+    // lanes meet eight different banks' groups
+    const uint32_t at = to + col / 4 * (KT * 128) + r * 128;
+    const int k0 = col % 4 * 2, odd = col / 4 & 1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int y = x ^ odd;
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((k0 + y) ^ (r & 7)) << 4)),
+                   "r"(y ? w[4] : w[0]), "r"(y ? w[5] : w[1]), "r"(y ? w[6] : w[2]), "r"(y ? w[7] : w[3])
+                   : "memory");
+    }
+  }
+  return true;
+}
+
 // A query row's results: bf16 outputs, or with splits its f32 state.
 struct PrefillRow {
   bool live;
@@ -168,14 +286,14 @@ struct PrefillRow {
 
 // tq, tk, tv: TMA descriptors of the queries ([64 dims][head][token][run of dims]) and of the pools'
 // planes ([64 dims][row][run of dims]).
-template <int D, int DV>
+template <int D, int DV, int FMT>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     pkv_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  using T = PrefillShape<D, DV>;
-  constexpr int KT = T::KT, KS = T::kKS, VS = T::kVS;
+  using T = PrefillShape<D, DV, FMT>;
+  constexpr int KT = T::KT, KS = T::kKS, VS = T::kVS, RS = T::kCodes ? T::kRawSlots : 1;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * KS + 2 * VS + 8];
+  __shared__ __align__(8) uint64_t bars[2 * KS + 2 * VS + 2 * RS + 8];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, bad_blocks;
   __shared__ uint32_t piece_bits[VS];
@@ -220,12 +338,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t smem_k = smem + T::kQ * T::kQBytes, smem_v = smem_k + KS * T::kKBytes;
+  const uint32_t smem_raw_codes = smem_v + VS * T::kVBytes;
   const uint32_t bar0 = smem_addr(bars);
   auto k_full = [&](int s) { return bar0 + 8 * s; };
   auto k_empty = [&](int s) { return bar0 + 8 * (KS + s); };
   auto v_full = [&](int s) { return bar0 + 8 * (2 * KS + s); };
   auto v_empty = [&](int s) { return bar0 + 8 * (2 * KS + VS + s); };
-  constexpr int kRest = 2 * KS + 2 * VS;
+  auto raw_full = [&](int s) { return bar0 + 8 * (2 * KS + 2 * VS + s); };
+  auto raw_empty = [&](int s) { return bar0 + 8 * (2 * KS + 2 * VS + RS + s); };
+  constexpr int kRest = 2 * (KS + VS + RS);
   auto s_full = [&](int s) { return bar0 + 8 * (kRest + s); };
   auto p_full = [&](int s) { return bar0 + 8 * (kRest + 2 + s); };
   auto o_done = [&](int s) { return bar0 + 8 * (kRest + 4 + s); };
@@ -233,8 +354,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRest + 8; ++i) {
-      const bool by_warps = i == kRest + 2 || i == kRest + 3;  // p_full: the four warps of a query tile
-      mbar_init(bar0 + 8 * i, by_warps ? 4 : 1);
+      int arrivals = 1;
+      if (i == kRest + 2 || i == kRest + 3) arrivals = 4;  // p_full: the four warps of a query tile
+      if (T::kCodes) {                                     // three warps, half a tile at a time
+        if (i < KS || (i >= 2 * KS && i < 2 * KS + VS)) arrivals = 6;
+        if (i >= 2 * (KS + VS) + RS && i < kRest) arrivals = 3;
+      }
+      mbar_init(bar0 + 8 * i, arrivals);
     }
     fence_barrier_init();
     abort_flag = 0;
@@ -273,21 +399,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     return __ballot_sync(0xffffffffu, ok);
   };
 
-  if (warp == 9 || warp == 10) {
+  // Asks for the query tiles (one lane).
+  auto ask_queries = [&] {
+    mbar_arrive_expect_tx(q_full, tiles_q * (D / 64) * p.tile_tokens * p.rep * 128);
+    for (int t = 0; t < tiles_q; ++t)
+      for (int c = 0; c < D / 64; ++c)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem + t * T::kQBytes + c * 128 * 128),
+            "l"(reinterpret_cast<uint64_t>(&tq)), "r"(0), "r"(u.head * p.rep), "r"(u.first + t * p.tile_tokens), "r"(c),
+            "r"(q_full)
+            : "memory");
+  };
+  if (!T::kCodes && (warp == 9 || warp == 10)) {
     // ------------------------------------------------------------------ copies: Q and K, and V
     PKV_PREFILL_FEWER_REGISTERS();
     const bool is_k = warp == 9;
-    if (is_k && lane == 0) {
-      mbar_arrive_expect_tx(q_full, tiles_q * (D / 64) * p.tile_tokens * p.rep * 128);
-      for (int t = 0; t < tiles_q; ++t)
-        for (int c = 0; c < D / 64; ++c)
-          asm volatile(
-              "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-              "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem + t * T::kQBytes + c * 128 * 128),
-              "l"(reinterpret_cast<uint64_t>(&tq)), "r"(0), "r"(u.head * p.rep), "r"(u.first + t * p.tile_tokens), "r"(c),
-              "r"(q_full)
-              : "memory");
-    }
+    if (is_k && lane == 0) ask_queries();
     const int stages = is_k ? KS : VS, runs = is_k ? D / 64 : DV / 64, bytes = is_k ? T::kKBytes : T::kVBytes;
     const uint32_t base = is_k ? smem_k : smem_v, full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
     const uint64_t map = reinterpret_cast<uint64_t>(is_k ? &tk : &tv);
@@ -326,6 +454,90 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (is_k) mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
     for (int i = max(0, asked - stages); i < asked; ++i)
       mbar_wait_warp(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
+  } else if (T::kCodes && warp >= 9 && warp <= 11) {
+    // ------------------------------------------------------------------ pages of codes, to bf16 tiles
+    // Half tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is half n & 1 of plane tile n / 2. Warp 9
+    // copies their codes, RS units ahead; warps 9 to 11 turn a third of each into bf16.
+    PKV_PREFILL_FEWER_REGISTERS();
+    if constexpr (T::kCodes) {
+    constexpr int kHalf = KT / 2;
+    const int part = warp - 9;
+    if (part == 0 && lane == 0) ask_queries();
+    // plane tile x: K(0), K(1), V(0), K(2), V(1), ..., V(nt - 1)
+    auto plane_tile = [&](int x, bool& is_k, int& j) {
+      if (x <= 1 && x < nt) {
+        is_k = true;
+        j = x;
+      } else if (nt == 1) {
+        is_k = false;
+        j = 0;
+      } else {
+        is_k = (x & 1) && (x + 1) / 2 < nt;
+        j = is_k ? (x + 1) / 2 : (x & 1) ? nt - 1 : x / 2 - 1;
+      }
+    };
+    const int units = 4 * nt;
+    int asked = 0;
+    auto ask = [&](int n) {  // warp 9: the codes of unit n
+      bool is_k;
+      int j, row;
+      plane_tile(n >> 1, is_k, j);
+      const uint32_t bits = tile_pieces(t0 + j, row);
+      const int per = pieces / 2, first = (n & 1) * per;  // pieces of the half
+      const int row_bytes = is_k ? T::kKRow : T::kVRow, s = n % RS;
+      const uint32_t mine = bits >> first & ((1u << per) - 1u);
+      if (lane == 0) mbar_arrive_expect_tx(raw_full(s), __popc(mine) * piece * row_bytes);
+      __syncwarp();
+      if (lane >= first && lane < first + per && (bits >> lane & 1))
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_raw_codes + s * T::kRawBytes + (lane - first) * piece * row_bytes),
+            "l"(reinterpret_cast<uint64_t>(is_k ? &tk : &tv)), "r"(0), "r"(row), "r"(raw_full(s))
+            : "memory");
+      __syncwarp();
+      ++asked;
+    };
+    if (part == 0)
+      for (int n = 0; n < RS && n < units; ++n) ask(n);
+    bool ok = true;
+    for (int n = 0; ok && n < units; ++n) {
+      bool is_k;
+      int j, row;
+      plane_tile(n >> 1, is_k, j);
+      const uint32_t bits = tile_pieces(t0 + j, row);
+      const int key = (t0 + j) * KT, half = (n & 1) * kHalf;
+      if (is_k) {
+        ok = convert_half<D, FMT, KT>(smem_k + (j % KS) * T::kKBytes, smem_raw_codes + (n % RS) * T::kRawBytes, p.k_planes, part,
+                                      key, half, lo, hi, bits, row, p, [&] {
+          return (j < KS || mbar_wait_warp(k_empty(j % KS), (j / KS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) &&
+                 mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        });
+      } else {
+        ok = convert_half<DV, FMT, KT>(smem_v + (j % VS) * T::kVBytes, smem_raw_codes + (n % RS) * T::kRawBytes, p.v_planes, part,
+                                       key, half, lo, hi, bits, row, p, [&] {
+          return (j < VS || mbar_wait_warp(v_empty(j % VS), (j / VS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) &&
+                 mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        });
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();  // the tile's rows are there for the products
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(is_k ? k_full(j % KS) : v_full(j % VS));
+        mbar_arrive(raw_empty(n % RS));
+      }
+      if (part == 0 && n + RS < units) {
+        ok = mbar_wait_warp(raw_empty(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        if (ok) ask(n + RS);
+      }
+    }
+    if (part == 0) {  // every copy lands before the CTA ends
+      int none = 0;
+      mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+      for (int n = max(0, asked - RS); n < asked; ++n)
+        mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
+    }
+    }
   } else if (warp == 8) {
     // ------------------------------------------------------------------ products
     PKV_PREFILL_FEWER_REGISTERS();
@@ -367,7 +579,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         ok = mbar_wait_warp(v_full(s), op.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
         // Rows that nobody sees have weight zero, which must meet zeros, whatever is there.
         const int key = (t0 + op.tile) * KT;
-        if (ok && (key < lo || key + KT > hi || any_bad)) {
+        if (!T::kCodes && ok && (key < lo || key + KT > hi || any_bad)) {
           const uint32_t bits = piece_bits[s];
           for (int r = lane; r < KT; r += 32) {
             if (key + r >= lo && key + r < hi && (bits >> (r >> p.piece_log2) & 1)) continue;

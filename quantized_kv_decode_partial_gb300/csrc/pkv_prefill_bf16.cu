@@ -1,8 +1,5 @@
 // Prompt attention over bf16 pages, and the join of split key ranges.
-#include <atomic>
-
-#include "pkv_launch.h"
-#include "pkv_prefill.cuh"
+#include "pkv_prefill_instances.cuh"
 
 namespace pkv {
 
@@ -81,58 +78,9 @@ __global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_cons
   }
 }
 
-template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                             const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernels wait before they touch memory
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <int D, int DV>
-cudaError_t launch_of(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int units,
-                      cudaStream_t stream, int device) {
-  constexpr int smem = PrefillShape<D, DV>::kSmem;
-  static std::atomic<bool> ready[256];  // per device; a second thread's call sets the same attribute again
-  if (device < 0 || device >= 256 || !ready[device].load(std::memory_order_relaxed)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(pkv_prefill_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (device >= 0 && device < 256) ready[device].store(true, std::memory_order_relaxed);
-  }
-  return launch_dependent(pkv_prefill_kernel<D, DV>, dim3(units * p.num_kv_heads * p.splits), kPrefillThreads, smem, stream,
-                          p, tq, tk, tv);
-}
-
-#define PKV_PREFILL_SHAPES(X) X(64, 64) X(128, 128) X(256, 256) X(192, 128) X(256, 128) X(128, 256)
-
 }  // namespace
 
-PrefillInfo prefill_info(int dk, int dv) {
-#define X(DK_, DV_)               \
-  if (dk == DK_ && dv == DV_)     \
-    return PrefillInfo{true, PrefillShape<DK_, DV_>::kQ, PrefillShape<DK_, DV_>::KT, PrefillShape<DK_, DV_>::kSmem};
-  PKV_PREFILL_SHAPES(X)
-#undef X
-  return PrefillInfo{};
-}
-
-cudaError_t launch_prefill_bf16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                                const CUtensorMap& tv, int units, cudaStream_t stream, int device) {
-#define X(DK_, DV_) \
-  if (dk == DK_ && dv == DV_) return launch_of<DK_, DV_>(p, tq, tk, tv, units, stream, device);
-  PKV_PREFILL_SHAPES(X)
-#undef X
-  return cudaErrorInvalidValue;
-}
+PKV_PREFILL_FORMAT(bf16, 16, PKV_PREFILL_WIDE)
 
 cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream) {
   PrefillJoinParams j{p.ws_o, p.ws_ml, p.query_starts, p.out, p.num_seqs, p.tokens, p.num_q_heads, p.splits};

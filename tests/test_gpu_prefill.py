@@ -49,6 +49,11 @@ class Cache:
                     s = torch.exp2(torch.floor(torch.log2(s)))
                 self.planes[name + "_scales"] = s.to(DEV)
                 self.values.append((pool.double() * s.double()[..., None, None]).to(DEV))
+                used = torch.zeros(nb, bs, dtype=torch.bool)
+                for b, l in enumerate(lens):
+                    for t in range(l):
+                        used[self.tables[b, t // bs], t % bs] = True
+                pool.view(torch.uint8)[~used[:, None, :, None].expand_as(pool)] = 0x7F  # not a number
             else:
                 codes = torch.randint(0, 2 ** bits, (nb, hk, bs, d), generator=g)
                 s = ((torch.rand(nb, hk, bs, d // 64, generator=g) + 0.5) * 4 / 2 ** bits).to(torch.bfloat16)
@@ -170,6 +175,60 @@ def test_windows(window, dk, dv, splits):
 def test_scales(scale):
     lens, news = [300, 200], [300, 7]
     check(randn(sum(news), 4, 128, seed=6), Cache(lens, 2, 128, 128, 32, dict()), news, scale)
+
+
+AFFINE = [(128, 128), (256, 256), (256, 128), (128, 256)]
+CODES = [(E4M3, d) for d in DIMS] + [(dict(bits=b), d) for b in (4, 8) for d in AFFINE]
+
+
+@pytest.mark.parametrize("fmt,dims", CODES)
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_pages_of_codes(fmt, dims, splits):
+    lens, news = [1, 700, 33, 129, 1000, 64, 130], [1, 200, 0, 129, 3, 64, 2]
+    cache = Cache(lens, 2, *dims, 32, fmt, seed=splits)
+    check(randn(sum(news), 6, dims[0], seed=2), cache, news, 1 / math.sqrt(dims[0]), splits=splits)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
+@pytest.mark.parametrize("bs", [8, 16, 32, 64, 96, 128, 256])
+def test_block_sizes_of_codes(fmt, bs):
+    lens, news = [517, 130], [300, 130]
+    for dims in ((128, 128), (256, 256)):
+        check(randn(sum(news), 4, dims[0], seed=3), Cache(lens, 2, *dims, bs, fmt, seed=bs + 1), news, 0.09, splits=1)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
+@pytest.mark.parametrize("window", [1, 100, 500])
+def test_windows_of_codes(fmt, window):
+    lens, news = [900, 260, 5], [300, 260, 5]
+    for dims in ((128, 128), (256, 256)):
+        check(randn(sum(news), 4, dims[0], seed=5), Cache(lens, 2, *dims, 32, fmt), news, 0.09, window=window)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
+@pytest.mark.parametrize("dims", [(128, 128), (256, 256)])
+def test_bad_blocks_of_codes_are_skipped(fmt, dims):
+    lens, news = [300, 200], [150, 200]
+    cache = Cache(lens, 2, *dims, 32, fmt)
+    q = randn(350, 4, dims[0], seed=10)
+    tables = cache.tables.clone()
+    tables[0, 3], tables[1, 0], tables[1, 5] = -1, 10 ** 6, cache.pools[0].shape[0]
+    got, err = run(q, cache, news, 0.09, tables=tables)
+    assert err == 1
+    gone = {0: [3], 1: [0, 5]}
+    ref, tol = reference(q, cache, news, 0.09, hidden=lambda b: torch.tensor([t // 32 in gone[b] for t in range(512)], device=DEV))
+    assert bool(((got.double() - ref).abs() <= tol).all())
+
+
+def test_block_scales_of_zero_and_far_apart():
+    cache = Cache([300], 2, 128, 128, 32, E4M3)
+    for name, scale, row in (("k_scales", 0.0, 2), ("v_scales", 0.0, 3), ("v_scales", 2.0 ** 30, 4), ("v_scales", 2.0 ** -40, 5),
+                             ("k_scales", 2.0 ** -40, 6)):
+        at = cache.tables[0, row].long()
+        which = 0 if name[0] == "k" else 1
+        cache.values[which][at] *= scale / cache.planes[name][at].double()[:, None, None]
+        cache.planes[name][at] = scale
+    check(randn(300, 4, 128, seed=14), cache, [300], 0.09)
 
 
 def test_rising_maxima_are_followed():
