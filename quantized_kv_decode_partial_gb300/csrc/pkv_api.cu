@@ -1402,7 +1402,7 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   if (!scale_planes_given(layout, k_scales, k_biases, v_scales, v_biases)) return PKV_ERR_NULL_POINTER;
   if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_starts, 4) || !aligned(error_flag, 4) ||
-      !scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 4))
+      !scale_planes_aligned(layout, k_scales, k_biases, v_scales, v_biases, 16))
     return PKV_ERR_MISALIGNED;
   int sms = 0, device = 0;
   rc = device_sm_count(&sms, &device);
@@ -1431,8 +1431,8 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   p.num_blocks = layout->num_blocks;
   p.block_size = layout->block_size;
   p.max_blocks = params->max_blocks_per_seq;
-  // rows of one copy: the largest power of two that divides blocks and key tiles (codes come in half tiles)
-  const int most = layout->bits == 16 ? plan.key_tile : plan.key_tile / 2;
+  // rows of one copy: the largest power of two that divides blocks and key tiles (codes come in quarter tiles)
+  const int most = layout->bits == 16 ? plan.key_tile : plan.key_tile / 4;
   while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= most) ++p.piece_log2;
   p.window = params->window;
   p.splits = plan.splits;

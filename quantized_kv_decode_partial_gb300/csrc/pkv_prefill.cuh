@@ -30,10 +30,14 @@ struct PrefillShape {
   static constexpr int kQ = DV == 256 || (kCodes && D == 256) ? 1 : 2;
   static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;  // key rows per tile
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
-  // Pages of codes come in through a ring of half tiles, which three warps turn into bf16.
-  static constexpr int kRawSlots = kCodes ? 4 : 0;
+  // Pages of codes come in through a ring of quarter tiles, which six warps turn into bf16.
+  static constexpr int kRawSlots = kCodes ? 6 : 0;
   static constexpr int kKRow = FMT == 4 ? D / 2 : D, kVRow = FMT == 4 ? DV / 2 : DV;  // bytes of a row of codes
-  static constexpr int kRawBytes = KT / 2 * (kKRow > kVRow ? kKRow : kVRow);
+  static constexpr int kWide = D > DV ? D : DV;
+  static constexpr int kRawCodes = KT / 4 * (kKRow > kVRow ? kKRow : kVRow);
+  static constexpr int kRawPlane = FMT == 4 || FMT == 8 ? KT / 4 * (kWide / 64) * 2 : 0;  // scales, then biases
+  static constexpr int kRawBytes = kRawCodes + 2 * kRawPlane;
+  static constexpr int kThreads = kCodes ? 512 : 384;
   // Stages of K and of V: as many as fit (up to 4), K first. A K tile is asked for when the last product that
   // read its stage is done; with two stages that is five products ahead, a copy's latency at best.
   static constexpr int kRoom = 226 * 1024 - kQ * kQBytes - kRawSlots * kRawBytes;
@@ -42,14 +46,29 @@ struct PrefillShape {
   static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + kRawSlots * kRawBytes + 1024;
   static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
   static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
-  static_assert(kVS >= 2 && kKS >= 2 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kVS >= 2 && kKS >= 2 && kSmem <= 227 * 1024 && kRawBytes % 128 == 0, "shared memory");
 };
 
-constexpr int kPrefillThreads = 384;  // two softmax warpgroups, then one with the product and the copy warp
-// Registers: softmax threads hold a row's scores. 2 * 128 * 208 + 128 * 88 is what the block is launched
-// with, 384 * 168. (The change stands inside the branches: before them it bounds both sides' registers.)
-#define PKV_PREFILL_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 208;")
-#define PKV_PREFILL_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 88;")
+// Registers: softmax threads hold a row's scores. With 384 threads (two softmax warpgroups, one with the product
+// and copy warps) 2 * 128 * 208 + 128 * 88 is what the block was launched with, 384 * 168; with 512 (a fourth of
+// warps that convert codes) 2 * 128 * 192 + 2 * 128 * 64 = 512 * 128. The change stands inside the branches: before
+// them it bounds both sides' registers.
+template <bool CODES>
+__device__ __forceinline__ void more_registers() {
+  if constexpr (CODES) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  }
+}
+template <bool CODES>
+__device__ __forceinline__ void fewer_registers() {
+  if constexpr (CODES) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
+}
 constexpr int kPrefillStates = 512;   // tensor memory columns
 
 // A work unit's place: computed by every warp from the same words.
@@ -175,10 +194,12 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float
     for (int i = 0; i < 4; ++i) {
       uint32_t lo, hi;
       e4m3x4_to_f16x2(w[i], lo, hi);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      out[2 * i] = pack_bf16x2(a.x * scale, a.y * scale);
-      out[2 * i + 1] = pack_bf16x2(b.x * scale, b.y * scale);
+      float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      unpair(mul2(pair(a.x, a.y), pair(scale, scale)), a.x, a.y);
+      unpair(mul2(pair(b.x, b.y), pair(scale, scale)), b.x, b.y);
+      out[2 * i] = pack_bf16x2(a.x, a.y);
+      out[2 * i + 1] = pack_bf16x2(b.x, b.y);
     }
   } else {
     // codes as halves: 1024 + code has the code in its last bits
@@ -211,44 +232,22 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float
   }
 }
 
-// One warp's third of half a tile of codes: rows [half, half + KT/2) of the tile, 16 values a lane at a time. Rows
-// outside [lo, hi) and those of pieces without their bit become zeros. row: lane l's, the pool row of piece l.
-// ready(): waits for the codes and for the place they go to.
-template <int D, int FMT, int KT, typename Ready>
-__device__ __forceinline__ bool convert_half(uint32_t to, uint32_t from, const PrefillPlanes& planes, int part, int key, int half,
-                                             int lo, int hi, uint32_t bits, int row, const PrefillParams& p,
-                                             const Ready& ready) {
-  constexpr int kPerRow = D / 16, kChunks = KT / 2 * kPerRow, kRounds = (kChunks + 95) / 96;
+// Half of a quarter tile of codes (a warp's part of two): rows [first, first + KT/4) of the tile, 16 values a lane
+// at a time. Rows that nobody sees and those of pieces without their bit become zeros.
+template <int D, int FMT, int KT>
+__device__ __forceinline__ void convert_quarter(uint32_t to, uint32_t from, uint32_t from_scales, uint32_t from_biases, int part,
+                                                int first, int seen_lo, int seen_hi, uint32_t bits, const float* scales,
+                                                int piece_log2) {
+  constexpr int kPerRow = D / 16, kChunks = KT / 4 * kPerRow;
   const int lane = threadIdx.x & 31;
-  float scale[kRounds], bias[kRounds];
-  if constexpr (FMT == kFmtE4m3) {
-    const float mine = bits >> lane & 1 ? planes.block_scales[row / p.block_size] : 0.f;
+  const bool whole = seen_lo <= first && seen_hi >= first + KT / 4 && bits == (1u << ((KT / 4) >> piece_log2)) - 1u;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int r = half + (i * 96 + part * 32 + lane) / kPerRow;
-      scale[i] = __shfl_sync(0xffffffffu, mine, (r >> p.piece_log2) & 31);
-      bias[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int c = i * 96 + part * 32 + lane, r = half + c / kPerRow, pc = r >> p.piece_log2;
-      const int first = __shfl_sync(0xffffffffu, row, pc & 31);
-      scale[i] = bias[i] = 0.f;
-      if (c < kChunks && (bits >> (pc & 31) & 1)) {
-        const size_t at = (static_cast<size_t>(first) + (r - (pc << p.piece_log2))) * (D / 64) + c % kPerRow / 4;
-        scale[i] = __bfloat162float(planes.scales[at]);
-        bias[i] = __bfloat162float(planes.biases[at]);
-      }
-    }
-  }
-  if (!ready()) return false;
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int c = i * 96 + part * 32 + lane;
-    if (c >= kChunks) break;
-    const int r = half + c / kPerRow, col = c % kPerRow;
+  for (int i = 0; i < (kChunks + 63) / 64; ++i) {
+    const int c = i * 64 + part * 32 + lane;
+    if (kChunks % 64 && c >= kChunks) break;
+    const int r = c / kPerRow, col = c % kPerRow;  // row of the quarter
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    float scale, bias = 0.f;
     if constexpr (FMT == 4) {
       asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from + c * 8) : "memory");
     } else {
@@ -257,25 +256,35 @@ __device__ __forceinline__ bool convert_half(uint32_t to, uint32_t from, const P
                    : "r"(from + c * 16)
                    : "memory");
     }
+    if constexpr (FMT == kFmtE4m3) {
+      scale = scales[r >> piece_log2];
+    } else {
+      uint16_t s16, b16;
+      const int at = (r * (D / 64) + col / 4) * 2;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(from_scales + at) : "memory");
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b16) : "r"(from_biases + at) : "memory");
+      scale = __uint_as_float(static_cast<uint32_t>(s16) << 16);
+      bias = __uint_as_float(static_cast<uint32_t>(b16) << 16);
+    }
     uint32_t w[8];
-    codes_to_bf16<FMT>(v, scale[i], bias[i], w);
-    if (!(key + r >= lo && key + r < hi && (bits >> ((r >> p.piece_log2) & 31) & 1))) {
+    codes_to_bf16<FMT>(v, scale, bias, w);
+    if (!whole && !(first + r >= seen_lo && first + r < seen_hi && (bits >> (r >> piece_log2) & 1))) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 0u;
     }
     // 16-byte places of the swizzled row; odd runs of 64 dims write their second one first, so that eight
-    // lanes meet eight different banks' groups
-    const uint32_t at = to + col / 4 * (KT * 128) + r * 128;
+    // lanes meet eight different groups of banks
+    const int row = first + r;
+    const uint32_t at = to + col / 4 * (KT * 128) + row * 128;
     const int k0 = col % 4 * 2, odd = col / 4 & 1;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int y = x ^ odd;
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((k0 + y) ^ (r & 7)) << 4)),
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((k0 + y) ^ (row & 7)) << 4)),
                    "r"(y ? w[4] : w[0]), "r"(y ? w[5] : w[1]), "r"(y ? w[6] : w[2]), "r"(y ? w[7] : w[3])
                    : "memory");
     }
   }
-  return true;
 }
 
 // A query row's results: bf16 outputs, or with splits its f32 state.
@@ -287,7 +296,7 @@ struct PrefillRow {
 // tq, tk, tv: TMA descriptors of the queries ([64 dims][head][token][run of dims]) and of the pools'
 // planes ([64 dims][row][run of dims]).
 template <int D, int DV, int FMT>
-__global__ void __launch_bounds__(kPrefillThreads, 1)
+__global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     pkv_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using T = PrefillShape<D, DV, FMT>;
@@ -297,6 +306,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, bad_blocks;
   __shared__ uint32_t piece_bits[VS];
+  __shared__ uint32_t unit_bits[RS];  // pages of codes: a quarter tile's pieces, and their scales (e4m3)
+  __shared__ float unit_scales[RS][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   wait_for_prerequisite_grids();
@@ -356,9 +367,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     for (int i = 0; i < kRest + 8; ++i) {
       int arrivals = 1;
       if (i == kRest + 2 || i == kRest + 3) arrivals = 4;  // p_full: the four warps of a query tile
-      if (T::kCodes) {                                     // three warps, half a tile at a time
-        if (i < KS || (i >= 2 * KS && i < 2 * KS + VS)) arrivals = 6;
-        if (i >= 2 * (KS + VS) + RS && i < kRest) arrivals = 3;
+      if (T::kCodes) {                                     // two warps for each quarter of a tile
+        if (i < KS || (i >= 2 * KS && i < 2 * KS + VS)) arrivals = 8;
+        if (i >= 2 * (KS + VS) + RS && i < kRest) arrivals = 2;
       }
       mbar_init(bar0 + 8 * i, arrivals);
     }
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   };
   if (!T::kCodes && (warp == 9 || warp == 10)) {
     // ------------------------------------------------------------------ copies: Q and K, and V
-    PKV_PREFILL_FEWER_REGISTERS();
+    fewer_registers<T::kCodes>();
     const bool is_k = warp == 9;
     if (is_k && lane == 0) ask_queries();
     const int stages = is_k ? KS : VS, runs = is_k ? D / 64 : DV / 64, bytes = is_k ? T::kKBytes : T::kVBytes;
@@ -454,93 +465,121 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (is_k) mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
     for (int i = max(0, asked - stages); i < asked; ++i)
       mbar_wait_warp(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
-  } else if (T::kCodes && warp >= 9 && warp <= 11) {
+  } else if (T::kCodes && warp >= 9) {
     // ------------------------------------------------------------------ pages of codes, to bf16 tiles
-    // Half tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is half n & 1 of plane tile n / 2. Warp 9
-    // copies their codes, RS units ahead; warps 9 to 11 turn a third of each into bf16.
-    PKV_PREFILL_FEWER_REGISTERS();
+    // Quarter tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is quarter n & 3 of plane tile n / 4. Warp 9
+    // copies their codes (and affine scales), RS units ahead; three pairs of warps turn them into bf16 in turn.
+    fewer_registers<T::kCodes>();
     if constexpr (T::kCodes) {
-    constexpr int kHalf = KT / 2;
-    const int part = warp - 9;
-    if (part == 0 && lane == 0) ask_queries();
-    // plane tile x: K(0), K(1), V(0), K(2), V(1), ..., V(nt - 1)
-    auto plane_tile = [&](int x, bool& is_k, int& j) {
-      if (x <= 1 && x < nt) {
-        is_k = true;
-        j = x;
-      } else if (nt == 1) {
-        is_k = false;
-        j = 0;
+      constexpr int kQuarter = KT / 4;
+      auto plane_tile = [&](int x, bool& is_k, int& j) {
+        if (nt == 1) {
+          is_k = x == 0;
+          j = 0;
+        } else if (x <= 1) {
+          is_k = true;
+          j = x;
+        } else {
+          is_k = (x & 1) && (x + 1) / 2 < nt;
+          j = is_k ? (x + 1) / 2 : (x & 1) ? nt - 1 : x / 2 - 1;
+        }
+      };
+      if (warp == 9) {
+        if (lane == 0) ask_queries();
+        const int per = kQuarter >> p.piece_log2;  // pieces of a quarter
+        bool is_k, ok = true;
+        int j, row, asked = 0;
+        plane_tile(0, is_k, j);
+        uint32_t bits = tile_pieces(t0 + j, row);
+        for (int x = 0; ok && x < 2 * nt; ++x) {
+          float scale = 0.f;
+          if (FMT == kFmtE4m3 && (bits >> lane & 1))
+            scale = (is_k ? p.k_planes : p.v_planes).block_scales[row / p.block_size];
+          bool next_k = false;
+          int next_j = 0, next_row = 0;
+          uint32_t next_bits = 0;
+          if (x + 1 < 2 * nt) {  // its table words arrive before this one's copies wait
+            plane_tile(x + 1, next_k, next_j);
+            next_bits = tile_pieces(t0 + next_j, next_row);
+          }
+          const int row_bytes = is_k ? T::kKRow : T::kVRow, groups = (is_k ? D : DV) / 64;
+          const int plane_bytes = FMT == kFmtE4m3 ? 0 : piece * groups * 2;
+          for (int h = 0; h < 4; ++h) {
+            const int n = 4 * x + h, s = n % RS, first = h * per;
+            if (n >= RS) ok = mbar_wait_warp(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+            if (!ok) break;
+            const uint32_t mine = bits >> first & ((1u << per) - 1u);
+            const bool copies = lane >= first && lane < first + per;
+            if (FMT == kFmtE4m3 && copies) unit_scales[s][lane - first] = scale;
+            __syncwarp();
+            if (lane == 0) {
+              unit_bits[s] = mine;
+              mbar_arrive_expect_tx(raw_full(s), __popc(mine) * (piece * row_bytes + 2 * plane_bytes));
+            }
+            __syncwarp();
+            if (copies && (bits >> lane & 1)) {
+              const uint32_t slot = smem_raw_codes + s * T::kRawBytes;
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                  "[%0], [%1, {%2, %3}], [%4];" ::"r"(slot + (lane - first) * piece * row_bytes),
+                  "l"(reinterpret_cast<uint64_t>(is_k ? &tk : &tv)), "r"(0), "r"(row), "r"(raw_full(s))
+                  : "memory");
+              if constexpr (FMT != kFmtE4m3) {
+                const PrefillPlanes& planes = is_k ? p.k_planes : p.v_planes;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  asm volatile(
+                      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                          slot + T::kRawCodes + b * T::kRawPlane + (lane - first) * plane_bytes),
+                      "l"((b ? planes.biases : planes.scales) + static_cast<size_t>(row) * groups), "r"(plane_bytes),
+                      "r"(raw_full(s))
+                      : "memory");
+              }
+            }
+            __syncwarp();
+            ++asked;
+          }
+          is_k = next_k;
+          j = next_j;
+          row = next_row;
+          bits = next_bits;
+        }
+        int none = 0;  // every copy lands before the CTA ends
+        mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+        for (int n = max(0, asked - RS); n < asked; ++n)
+          mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
       } else {
-        is_k = (x & 1) && (x + 1) / 2 < nt;
-        j = is_k ? (x + 1) / 2 : (x & 1) ? nt - 1 : x / 2 - 1;
+        const int group = (warp - 10) >> 1, part = (warp - 10) & 1;
+        for (int n = group; n < 8 * nt; n += 3) {
+          bool is_k;
+          int j;
+          plane_tile(n >> 2, is_k, j);
+          const int s = n % RS, stage = is_k ? j % KS : j % VS, round = is_k ? j / KS : j / VS;
+          if (round > 0 && !mbar_wait_warp(is_k ? k_empty(stage) : v_empty(stage), (round - 1) & 1, &abort_flag, p.error_flag,
+                                           p.wait_limit_ns))
+            break;
+          if (!mbar_wait_warp(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
+          const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = from + T::kRawCodes;
+          const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;
+          if (is_k) {
+            convert_quarter<D, FMT, KT>(smem_k + stage * T::kKBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
+                                        hi - key, unit_bits[s], unit_scales[s], p.piece_log2);
+          } else {
+            convert_quarter<DV, FMT, KT>(smem_v + stage * T::kVBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
+                                         hi - key, unit_bits[s], unit_scales[s], p.piece_log2);
+          }
+          fence_proxy_async_smem();  // the tile's rows are there for the products
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(is_k ? k_full(stage) : v_full(stage));
+            mbar_arrive(raw_empty(s));
+          }
+        }
       }
-    };
-    const int units = 4 * nt;
-    int asked = 0;
-    auto ask = [&](int n) {  // warp 9: the codes of unit n
-      bool is_k;
-      int j, row;
-      plane_tile(n >> 1, is_k, j);
-      const uint32_t bits = tile_pieces(t0 + j, row);
-      const int per = pieces / 2, first = (n & 1) * per;  // pieces of the half
-      const int row_bytes = is_k ? T::kKRow : T::kVRow, s = n % RS;
-      const uint32_t mine = bits >> first & ((1u << per) - 1u);
-      if (lane == 0) mbar_arrive_expect_tx(raw_full(s), __popc(mine) * piece * row_bytes);
-      __syncwarp();
-      if (lane >= first && lane < first + per && (bits >> lane & 1))
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_raw_codes + s * T::kRawBytes + (lane - first) * piece * row_bytes),
-            "l"(reinterpret_cast<uint64_t>(is_k ? &tk : &tv)), "r"(0), "r"(row), "r"(raw_full(s))
-            : "memory");
-      __syncwarp();
-      ++asked;
-    };
-    if (part == 0)
-      for (int n = 0; n < RS && n < units; ++n) ask(n);
-    bool ok = true;
-    for (int n = 0; ok && n < units; ++n) {
-      bool is_k;
-      int j, row;
-      plane_tile(n >> 1, is_k, j);
-      const uint32_t bits = tile_pieces(t0 + j, row);
-      const int key = (t0 + j) * KT, half = (n & 1) * kHalf;
-      if (is_k) {
-        ok = convert_half<D, FMT, KT>(smem_k + (j % KS) * T::kKBytes, smem_raw_codes + (n % RS) * T::kRawBytes, p.k_planes, part,
-                                      key, half, lo, hi, bits, row, p, [&] {
-          return (j < KS || mbar_wait_warp(k_empty(j % KS), (j / KS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) &&
-                 mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
-        });
-      } else {
-        ok = convert_half<DV, FMT, KT>(smem_v + (j % VS) * T::kVBytes, smem_raw_codes + (n % RS) * T::kRawBytes, p.v_planes, part,
-                                       key, half, lo, hi, bits, row, p, [&] {
-          return (j < VS || mbar_wait_warp(v_empty(j % VS), (j / VS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) &&
-                 mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
-        });
-      }
-      if (!ok) break;
-      fence_proxy_async_smem();  // the tile's rows are there for the products
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(is_k ? k_full(j % KS) : v_full(j % VS));
-        mbar_arrive(raw_empty(n % RS));
-      }
-      if (part == 0 && n + RS < units) {
-        ok = mbar_wait_warp(raw_empty(n % RS), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
-        if (ok) ask(n + RS);
-      }
-    }
-    if (part == 0) {  // every copy lands before the CTA ends
-      int none = 0;
-      mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
-      for (int n = max(0, asked - RS); n < asked; ++n)
-        mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
-    }
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------------ products
-    PKV_PREFILL_FEWER_REGISTERS();
+    fewer_registers<T::kCodes>();
     const uint32_t leader = elect_lane(), base = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t instr_s = umma_instr(KT, false, p.negate != 0), instr_o = umma_instr(DV, true, false);
     bool ok = mbar_wait_warp(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
@@ -609,7 +648,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
   } else if (warp < 8 && (warp >> 2) < tiles_q) {
     // ------------------------------------------------------------------ softmax of one query tile
-    PKV_PREFILL_MORE_REGISTERS();
+    more_registers<T::kCodes>();
     const int q = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes
     const PrefillRow out = row_of(q, r);
@@ -629,42 +668,46 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if (!ok) break;
       tmem_fence_after_sync();
       const uint32_t s_at = tmem + lanes + (i & 1) * KT;
-      float s[KT];
-      tmem_ld_tile<KT>(s_at, s);
       // Which of the tile's keys this row sees: [v0, v1), less the pieces that were not copied.
       const bool masked = any_bad || key + KT > u.position + first + 1 ||
                           (p.window > 0 && key <= u.position + last - p.window);
-      if (masked) {
-        const int v0 = below + 1 - key, v1 = pos + 1 - key;
-        uint32_t bits = 0xFFFFFFFFu;
-        if (any_bad) {
-          int row;
-          bits = tile_pieces(t0 + j, row);
-        }
-#pragma unroll
-        for (int h = 0; h < KT / 32; ++h) {
-          uint32_t seen = low_bits(v1 - 32 * h) & ~low_bits(v0 - 32 * h);
-          if (any_bad)
-            for (int e = 0; e < 32; ++e)
-              if (!(bits >> ((32 * h + e) >> p.piece_log2) & 1)) seen &= ~(1u << e);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[32 * h + e] = (seen >> e & 1) ? s[32 * h + e] : -INFINITY;
-        }
-      }
-      // Weights by the maximum so far, while the tile's own is found beside them; where that one is more
-      // than 2^8 above, the outputs are rescaled and the weights computed again. The first tile waits for its
-      // maximum.
-      if (j == 0) m = row_max<KT>(s);
-      uint64_t sums[2] = {l[0], l[1]};
+      // Weights by the maximum so far, while the tile's own is found beside them. Where that one is more than
+      // 2^8 above, the outputs are rescaled and the weights computed again, from scores that are still there.
+      // The first tile waits for its maximum.
       uint32_t w[KT / 2];
-      float mx = weights<KT>(s, c, m, sums, w);
-      const float up = fmaxf(m, mx);
-      if (j > 0 && __any_sync(0xffffffffu, (up - m) * c > 8.f || (m == -INFINITY && up > m))) {
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        float s[KT];
+        tmem_ld_tile<KT>(s_at, s);
+        if (masked) {
+          const int v0 = below + 1 - key, v1 = pos + 1 - key;
+          uint32_t bits = 0xFFFFFFFFu;
+          if (any_bad) {
+            int row;
+            bits = tile_pieces(t0 + j, row);
+          }
+#pragma unroll
+          for (int h = 0; h < KT / 32; ++h) {
+            uint32_t seen = low_bits(v1 - 32 * h) & ~low_bits(v0 - 32 * h);
+            if (any_bad)
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> ((32 * h + e) >> p.piece_log2) & 1)) seen &= ~(1u << e);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * h + e] = (seen >> e & 1) ? s[32 * h + e] : -INFINITY;
+          }
+        }
+        if (j == 0) m = row_max<KT>(s);
+        uint64_t sums[2] = {l[0], l[1]};
+        const float up = fmaxf(m, weights<KT>(s, c, m, sums, w));
+        if (again || j == 0 || !__any_sync(0xffffffffu, (up - m) * c > 8.f || (m == -INFINITY && up > m))) {
+          l[0] = sums[0];
+          l[1] = sums[1];
+          break;
+        }
         const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
         m = up;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) sums[n] = mul2(l[n], pair(by, by));
-        weights<KT>(s, c, m, sums, w);
+        for (int n = 0; n < 2; ++n) l[n] = mul2(l[n], pair(by, by));
         ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
         if (!ok) break;
         tmem_fence_after_sync();
@@ -678,8 +721,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           tmem_st_32(o_at + d, o);
         }
       }
-      l[0] = sums[0];
-      l[1] = sums[1];
+      if (!ok) break;
 #pragma unroll
       for (int h = 0; h < KT / 64; ++h) tmem_st_32(s_at + h * 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32 * h));  // over the scores
       tmem_wait_st();
@@ -731,7 +773,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
     }
   } else if (warp >= 8) {
-    PKV_PREFILL_FEWER_REGISTERS();  // the rest of that warpgroup
+    fewer_registers<T::kCodes>();  // the rest of that warpgroup
   }
 
   __syncwarp();

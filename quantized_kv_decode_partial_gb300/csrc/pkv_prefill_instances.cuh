@@ -35,7 +35,7 @@ cudaError_t launch_prefill_of(const PrefillParams& p, const CUtensorMap& tq, con
     if (e != cudaSuccess) return e;
     if (device >= 0 && device < 256) ready[device].store(true, std::memory_order_relaxed);
   }
-  return launch_dependent(pkv_prefill_kernel<D, DV, FMT>, dim3(units * p.num_kv_heads * p.splits), kPrefillThreads, smem, stream,
+  return launch_dependent(pkv_prefill_kernel<D, DV, FMT>, dim3(units * p.num_kv_heads * p.splits), PrefillShape<D, DV, FMT>::kThreads, smem, stream,
                           p, tq, tk, tv);
 }
 
