@@ -22,6 +22,8 @@
 
 namespace pkv {
 
+constexpr int kPrefillRoom = 225 * 1024;  // for tiles: 227 KB less barriers and the alignment of the first tile
+
 // Tiles of one instantiation. FMT: the page format (16, 4, 8 or kFmtE4m3).
 template <int D, int DV, int FMT>
 struct PrefillShape {
@@ -31,22 +33,24 @@ struct PrefillShape {
   static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;  // key rows per tile
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
   // Pages of codes come in through a ring of quarter tiles, which six warps turn into bf16.
-  static constexpr int kRawSlots = kCodes ? 6 : 0;
   static constexpr int kKRow = FMT == 4 ? D / 2 : D, kVRow = FMT == 4 ? DV / 2 : DV;  // bytes of a row of codes
   static constexpr int kWide = D > DV ? D : DV;
   static constexpr int kRawCodes = KT / 4 * (kKRow > kVRow ? kKRow : kVRow);
   static constexpr int kRawPlane = FMT == 4 || FMT == 8 ? KT / 4 * (kWide / 64) * 2 : 0;  // scales, then biases
   static constexpr int kRawBytes = kRawCodes + 2 * kRawPlane;
+  // As many as fit beside two stages of K and V (up to 8): each of the three pairs has one or two in the works.
+  static constexpr int kRawFit = (kPrefillRoom - kQ * kQBytes - 2 * (kKBytes + kVBytes)) / kRawBytes;
+  static constexpr int kRawSlots = !kCodes ? 0 : kRawFit > 8 ? 8 : kRawFit;
   static constexpr int kThreads = kCodes ? 512 : 384;
   // Stages of K and of V: as many as fit (up to 4), K first. A K tile is asked for when the last product that
   // read its stage is done; with two stages that is five products ahead, a copy's latency at best.
-  static constexpr int kRoom = 226 * 1024 - kQ * kQBytes - kRawSlots * kRawBytes;
+  static constexpr int kRoom = kPrefillRoom - kQ * kQBytes - kRawSlots * kRawBytes;
   static constexpr int kVS = kRoom / (kKBytes + kVBytes) > 4 ? 4 : kRoom / (kKBytes + kVBytes);
   static constexpr int kKS = (kRoom - kVS * kVBytes) / kKBytes > 4 ? 4 : (kRoom - kVS * kVBytes) / kKBytes;
   static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + kRawSlots * kRawBytes + 1024;
   static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
   static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
-  static_assert(kVS >= 2 && kKS >= 2 && kSmem <= 227 * 1024 && kRawBytes % 128 == 0, "shared memory");
+  static_assert(kVS >= 2 && kKS >= 2 && (!kCodes || kRawSlots >= 6) && kSmem <= kPrefillRoom + 1024 && kRawBytes % 128 == 0, "shared memory");
 };
 
 // Registers: softmax threads hold a row's scores. With 384 threads (two softmax warpgroups, one with the product
@@ -236,38 +240,47 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float
 // at a time. Rows that nobody sees and those of pieces without their bit become zeros.
 template <int D, int FMT, int KT>
 __device__ __forceinline__ void convert_quarter(uint32_t to, uint32_t from, uint32_t from_scales, uint32_t from_biases, int part,
-                                                int first, int seen_lo, int seen_hi, uint32_t bits, const float* scales,
+                                                int first, int seen_lo, int seen_hi, uint32_t bits, uint32_t scales,
                                                 int piece_log2) {
   constexpr int kPerRow = D / 16, kChunks = KT / 4 * kPerRow;
   const int lane = threadIdx.x & 31;
   const bool whole = seen_lo <= first && seen_hi >= first + KT / 4 && bits == (1u << ((KT / 4) >> piece_log2)) - 1u;
+  constexpr int kRounds = (kChunks + 63) / 64;
+  uint4 v[kRounds];  // all loads first: one round's latency instead of every round's
+  float scale[kRounds], bias[kRounds];
 #pragma unroll
-  for (int i = 0; i < (kChunks + 63) / 64; ++i) {
+  for (int i = 0; i < kRounds; ++i) {
     const int c = i * 64 + part * 32 + lane;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    scale[i] = bias[i] = 0.f;
     if (kChunks % 64 && c >= kChunks) break;
     const int r = c / kPerRow, col = c % kPerRow;  // row of the quarter
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    float scale, bias = 0.f;
     if constexpr (FMT == 4) {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from + c * 8) : "memory");
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[i].x), "=r"(v[i].y) : "r"(from + c * 8) : "memory");
     } else {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
                    : "r"(from + c * 16)
                    : "memory");
     }
     if constexpr (FMT == kFmtE4m3) {
-      scale = scales[r >> piece_log2];
+      scale[i] = ld_shared_f32(scales + 4 * (r >> piece_log2));
     } else {
       uint16_t s16, b16;
       const int at = (r * (D / 64) + col / 4) * 2;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(from_scales + at) : "memory");
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b16) : "r"(from_biases + at) : "memory");
-      scale = __uint_as_float(static_cast<uint32_t>(s16) << 16);
-      bias = __uint_as_float(static_cast<uint32_t>(b16) << 16);
+      scale[i] = __uint_as_float(static_cast<uint32_t>(s16) << 16);
+      bias[i] = __uint_as_float(static_cast<uint32_t>(b16) << 16);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int c = i * 64 + part * 32 + lane;
+    if (kChunks % 64 && c >= kChunks) break;
+    const int r = c / kPerRow, col = c % kPerRow;
     uint32_t w[8];
-    codes_to_bf16<FMT>(v, scale, bias, w);
+    codes_to_bf16<FMT>(v[i], scale[i], bias[i], w);
     if (!whole && !(first + r >= seen_lo && first + r < seen_hi && (bits >> (r >> piece_log2) & 1))) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 0u;
@@ -563,10 +576,10 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;
           if (is_k) {
             convert_quarter<D, FMT, KT>(smem_k + stage * T::kKBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
-                                        hi - key, unit_bits[s], unit_scales[s], p.piece_log2);
+                                        hi - key, unit_bits[s], smem_addr(unit_scales[s]), p.piece_log2);
           } else {
             convert_quarter<DV, FMT, KT>(smem_v + stage * T::kVBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
-                                         hi - key, unit_bits[s], unit_scales[s], p.piece_log2);
+                                         hi - key, unit_bits[s], smem_addr(unit_scales[s]), p.piece_log2);
           }
           fence_proxy_async_smem();  // the tile's rows are there for the products
           __syncwarp();
