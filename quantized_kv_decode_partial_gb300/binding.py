@@ -78,6 +78,10 @@ PKV_SECTIONS_CYCLE = 1
 
 PKV_MAX_AXES = 4
 
+PKV_READING_AUTO = 0
+PKV_READING_DIRECT = 1
+PKV_READING_VALUES = 2
+
 PKV_DEVERR_BAD_BLOCK = 1
 PKV_DEVERR_BAD_SEQ_LEN = 2
 PKV_DEVERR_TIMEOUT = 4
@@ -131,11 +135,11 @@ class RowStrides(ctypes.Structure):
 
 class PrefillParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
-                ("num_seqs", "num_tokens", "num_q_heads", "max_blocks_per_seq", "window", "splits")]
+                ("num_seqs", "num_tokens", "num_q_heads", "max_blocks_per_seq", "window", "splits", "reading")]
 
 
 class PrefillPlan(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("unit_tokens", "key_tile", "units", "splits", "smem_bytes")] + \
+    _fields_ = [(n, ctypes.c_int32) for n in ("unit_tokens", "key_tile", "units", "splits", "smem_bytes", "value_blocks")] + \
         [("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -972,7 +976,7 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
                             seq_lens: torch.Tensor, query_starts: torch.Tensor, scale: float, *, bits: int = 16,
                             group_size: int = 64, k_scales: Optional[torch.Tensor] = None,
                             k_biases: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
-                            v_biases: Optional[torch.Tensor] = None, window: int = 0, splits: int = 0,
+                            v_biases: Optional[torch.Tensor] = None, window: int = 0, splits: int = 0, reading: int = 0,
                             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                             error_flag: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of many new tokens of each sequence over the pages (pkv_paged_prefill_attention; see
@@ -987,7 +991,7 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     index = q.get_device()
     key = ("prefill", index, _layout_key(q), None if out is None else (out.shape, out.dtype),
            _types((k_pool, v_pool, block_tables, seq_lens, query_starts, k_scales, k_biases, v_scales, v_biases)), bits,
-           group_size, window, splits)
+           group_size, window, splits, reading)
     with _on_index(index) if index >= 0 else _stay:
         call = _calls.get(key)
         if call is None:
@@ -1013,7 +1017,7 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
             if out is not None:
                 _require(torch.bfloat16, out=out)
                 _require_shape("out", out, *call.out_shape)
-            params = PrefillParams(B, T, HQ, block_tables.shape[1], window, splits)
+            params = PrefillParams(B, T, HQ, block_tables.shape[1], window, splits, reading)
             strides = _row_strides(q)
             call.keep = (layout, params, strides)
             call.refs = tuple(ctypes.byref(x) for x in call.keep)

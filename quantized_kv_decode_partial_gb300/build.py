@@ -28,6 +28,7 @@ SOURCES = [
     "pkv_append_blocks.cu",
     "pkv_rotate.cu",
     "pkv_prefill_bf16.cu",
+    "pkv_prefill_values.cu",
     "pkv_prefill_u4.cu",
     "pkv_prefill_u8.cu",
     "pkv_prefill_e4m3.cu",

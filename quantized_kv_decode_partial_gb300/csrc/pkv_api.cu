@@ -1281,7 +1281,7 @@ int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
   if (rc) return rc;
   if (!P) return PKV_ERR_NULL_POINTER;
   if (P->num_seqs <= 0 || P->num_seqs > 65535 || P->num_tokens < 0 || P->max_blocks_per_seq <= 0 || P->window < 0 ||
-      P->splits < 0 || P->splits > 64)
+      P->splits < 0 || P->splits > 64 || P->reading < PKV_READING_AUTO || P->reading > PKV_READING_VALUES)
     return PKV_ERR_BAD_PARAMS;
   if (P->num_q_heads <= 0 || P->num_q_heads % L->num_kv_heads) return PKV_ERR_BAD_PARAMS;
   if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
@@ -1316,10 +1316,45 @@ int prefill_splits(const pkv_pool_layout* L, const pkv_prefill_params* P, long l
   return best;
 }
 
+// Where the values of each sequence go, and how many blocks of them there can be.
+pkv::PrefillValues prefill_values(const pkv_pool_layout* L, const pkv_prefill_params* P, long long* blocks) {
+  const long long table = static_cast<long long>(P->max_blocks_per_seq) * L->block_size;
+  const long long whole = (table + pkv::kValueRows - 1) / pkv::kValueRows;
+  const long long all = whole * P->num_seqs;
+  // under a window a sequence of n tokens sees n + window - 1 rows: floor((n + window) / 128) + 2 blocks at most
+  const long long part = P->window / pkv::kValueRows + 3;
+  const long long windowed = P->num_tokens / pkv::kValueRows + 1 + part * P->num_seqs;
+  pkv::PrefillValues v{};
+  v.used = 1;
+  v.by_tokens = P->window > 0 && windowed < all;
+  v.per_seq = static_cast<int>(v.by_tokens ? part : whole);
+  *blocks = v.by_tokens ? windowed : all;
+  return v;
+}
+
+// The values pay for themselves from the second CTA on that reads the same keys: turning a tile of 128 keys of 8-bit
+// codes costs a CTA about 1.5 us, writing and reading it as bf16 as much as 15 ns of the GPU's bandwidth. (Batch of
+// 16 chunks of 1 to 512 tokens over e4m3 pages: 1229 us directly; 64 sequences of 16 tokens each are slower that way.)
+constexpr long long kMostValueBytes = 8ll << 30;
+
+long long prefill_value_blocks(const pkv_pool_layout* L, const pkv_prefill_params* P, int unit_tokens) {
+  if (L->bits == 16 || P->reading == PKV_READING_DIRECT) return 0;
+  long long blocks = 0;
+  prefill_values(L, P, &blocks);
+  const long long bytes = blocks * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
+  const bool wanted = P->reading == PKV_READING_VALUES ||
+                      (P->num_tokens >= static_cast<long long>(unit_tokens) * P->num_seqs && bytes <= kMostValueBytes);
+  // rows are counted in int by the copies
+  return wanted && blocks * L->num_kv_heads * pkv::kValueRows < (1ll << 31) ? blocks : 0;
+}
+
 int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_count, pkv_prefill_plan* plan) {
-  const pkv::PrefillInfo info = prefill_info(L);
   const int rep = P->num_q_heads / L->num_kv_heads;
+  pkv::PrefillInfo info = prefill_info(L);
   pkv_prefill_plan r{};
+  r.value_blocks = static_cast<int32_t>(prefill_value_blocks(L, P, info.query_tiles * (128 / rep)));
+  if (P->reading == PKV_READING_VALUES && L->bits != 16 && r.value_blocks == 0) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (r.value_blocks > 0) info = pkv::prefill_info_bf16(L->head_dim, v_dim(L));
   r.unit_tokens = info.query_tiles * (128 / rep);
   r.key_tile = info.key_tile;
   r.units = P->num_tokens / r.unit_tokens + P->num_seqs;
@@ -1329,6 +1364,9 @@ int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_c
   r.smem_bytes = info.smem_bytes;
   if (r.splits > 1)
     r.workspace_bytes = static_cast<size_t>(r.splits) * P->num_tokens * P->num_q_heads * (v_dim(L) + 2) * sizeof(float);
+  if (r.value_blocks > 0)
+    r.workspace_bytes = static_cast<size_t>(round_up(static_cast<long long>(r.workspace_bytes), 256)) +
+                        static_cast<size_t>(r.value_blocks) * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
   *plan = r;
   return PKV_OK;
 }
@@ -1431,9 +1469,12 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   p.num_blocks = layout->num_blocks;
   p.block_size = layout->block_size;
   p.max_blocks = params->max_blocks_per_seq;
+  const int fmt = format_of(layout);
+  const bool block = block_scaled(layout), values = plan.value_blocks > 0;
   // rows of one copy: the largest power of two that divides blocks and key tiles (codes come in quarter tiles)
-  const int most = layout->bits == 16 ? plan.key_tile : plan.key_tile / 4;
-  while (layout->block_size % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= most) ++p.piece_log2;
+  const int most = layout->bits == 16 || values ? plan.key_tile : plan.key_tile / 4;
+  const int block_rows = values ? pkv::kValueRows : layout->block_size;
+  while (block_rows % (2 << p.piece_log2) == 0 && (2 << p.piece_log2) <= most) ++p.piece_log2;
   p.window = params->window;
   p.splits = plan.splits;
   // not zero, so that a score of -infinity (a masked one) has no weight whatever the scale
@@ -1441,18 +1482,6 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   p.negate = scale < 0.f;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   const int piece = 1 << p.piece_log2;
-  const long long pool_rows = static_cast<long long>(layout->num_blocks) * layout->num_kv_heads * layout->block_size;
-  CUtensorMap tq, tk, tv;
-  rc = encode_query_map(&tq, q, D, params->num_q_heads, params->num_tokens, q_strides, rep, p.tile_tokens);
-  if (layout->bits == 16) {
-    if (!rc) rc = pool_tensor_map(&tk, k_pool, 2, D, pool_rows, 128, piece, true);
-    if (!rc) rc = pool_tensor_map(&tv, v_pool, 2, DV, pool_rows, 128, piece, true);
-  } else {
-    if (!rc) rc = pool_tensor_map(&tk, k_pool, 1, D * layout->bits / 8, pool_rows, kWholeRows, piece, false);
-    if (!rc) rc = pool_tensor_map(&tv, v_pool, 1, DV * layout->bits / 8, pool_rows, kWholeRows, piece, false);
-  }
-  if (rc) return rc;
-  const bool block = block_scaled(layout);
   auto planes = [&](const void* scales, const void* biases) {
     pkv::PrefillPlanes x{};
     if (block) {
@@ -1465,13 +1494,55 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   };
   p.k_planes = planes(k_scales, k_biases);
   p.v_planes = planes(v_scales, v_biases);
+  pkv::PrefillValuesParams w{};
+  if (values) {
+    long long blocks = 0;
+    p.values = prefill_values(layout, params, &blocks);
+    const size_t rows = static_cast<size_t>(plan.value_blocks) * layout->num_kv_heads * pkv::kValueRows;
+    w.pool[0] = static_cast<const uint8_t*>(k_pool);
+    w.pool[1] = static_cast<const uint8_t*>(v_pool);
+    w.planes[0] = p.k_planes;
+    w.planes[1] = p.v_planes;
+    // behind the states
+    w.out[0] = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + plan.workspace_bytes - rows * (D + DV) * 2);
+    w.out[1] = w.out[0] + rows * D;
+    w.dim[0] = D;
+    w.dim[1] = DV;
+    w.values = p.values;
+    w.query_starts = query_starts;
+    w.block_tables = block_tables;
+    w.seq_lens = seq_lens;
+    w.num_seqs = p.num_seqs;
+    w.tokens = p.tokens;
+    w.num_kv_heads = p.num_kv_heads;
+    w.num_blocks = p.num_blocks;
+    w.block_size = p.block_size;
+    w.max_blocks = p.max_blocks;
+    w.window = p.window;
+    w.blocks = plan.value_blocks;
+  }
+  const long long pool_rows = static_cast<long long>(values ? plan.value_blocks : layout->num_blocks) * layout->num_kv_heads * block_rows;
+  CUtensorMap tq, tk, tv;
+  rc = encode_query_map(&tq, q, D, params->num_q_heads, params->num_tokens, q_strides, rep, p.tile_tokens);
+  if (layout->bits == 16 || values) {
+    if (!rc) rc = pool_tensor_map(&tk, values ? w.out[0] : k_pool, 2, D, pool_rows, 128, piece, true);
+    if (!rc) rc = pool_tensor_map(&tv, values ? w.out[1] : v_pool, 2, DV, pool_rows, 128, piece, true);
+  } else {
+    if (!rc) rc = pool_tensor_map(&tk, k_pool, 1, D * layout->bits / 8, pool_rows, kWholeRows, piece, false);
+    if (!rc) rc = pool_tensor_map(&tv, v_pool, 1, DV * layout->bits / 8, pool_rows, kWholeRows, piece, false);
+  }
+  if (rc) return rc;
   (void)cudaGetLastError();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int fmt = format_of(layout);
-  cudaError_t e = fmt == 16  ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
-                  : fmt == 4 ? pkv::launch_prefill_u4(D, DV, p, tq, tk, tv, plan.units, st, device)
-                  : fmt == 8 ? pkv::launch_prefill_u8(D, DV, p, tq, tk, tv, plan.units, st, device)
-                             : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
+  cudaError_t e = cudaSuccess;
+  if (values) {
+    e = pkv::launch_prefill_values(w, fmt, st);
+    if (e != cudaSuccess) return cuda_fail("values kernel launch", e);
+  }
+  e = fmt == 16 || values ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
+      : fmt == 4          ? pkv::launch_prefill_u4(D, DV, p, tq, tk, tv, plan.units, st, device)
+      : fmt == 8          ? pkv::launch_prefill_u8(D, DV, p, tq, tk, tv, plan.units, st, device)
+                          : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
   if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
   if (plan.splits > 1) {
     e = pkv::launch_prefill_join(p, DV, st);

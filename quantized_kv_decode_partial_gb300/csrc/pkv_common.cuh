@@ -170,6 +170,23 @@ struct RotateParams {
 };
 
 // Attention of many new tokens over the pages (pkv_prefill.cuh).
+constexpr int kValueRows = 128;  // rows of a block of values
+
+// Pages of codes that many query tiles read are turned into bf16 values once, before the attention: blocks
+// [num_kv_heads][kValueRows][width] of each sequence one after the other.
+struct PrefillValues {
+  int used;
+  int by_tokens, per_seq;  // sequence b's blocks begin at (by_tokens ? its first token / kValueRows : 0) + b * per_seq
+  __host__ __device__ __forceinline__ int base(int b, int start) const {
+    return (by_tokens ? start / kValueRows : 0) + b * per_seq;
+  }
+  // The first row that a sequence's queries can see, rounded down to a block's.
+  static __host__ __device__ __forceinline__ int first_row(int len, int n, int window) {
+    const int lo = window > 0 ? len - n - window + 1 : 0;
+    return lo > 0 ? lo / kValueRows * kValueRows : 0;
+  }
+};
+
 struct PrefillPlanes {
   const __nv_bfloat16* scales;  // [NB, HK, BS, width/64]   (affine pages)
   const __nv_bfloat16* biases;
@@ -178,6 +195,7 @@ struct PrefillPlanes {
 
 struct PrefillParams {
   PrefillPlanes k_planes, v_planes;
+  PrefillValues values;
   const int32_t* query_starts;  // [num_seqs + 1]
   const int32_t* block_tables;  // [num_seqs, max_blocks]
   const int32_t* seq_lens;      // rows held, the new ones included
@@ -188,11 +206,24 @@ struct PrefillParams {
   int num_seqs, tokens, num_q_heads, num_kv_heads, rep;
   int tile_tokens;              // tokens of one query tile: 128 / rep
   int num_blocks, block_size, max_blocks;
-  int piece_log2;               // rows of one copy: a power of two that divides block_size and KT
+  int piece_log2;               // rows of one copy: a power of two that divides block_size (or kValueRows) and KT
   int window, splits;
   float score_scale;            // |softmax scale| * log2(e)
   int negate;                   // the softmax scale is negative
   unsigned long long wait_limit_ns;
+};
+
+// The pass that writes the values (pkv_prefill_values.cu).
+struct PrefillValuesParams {
+  const uint8_t* pool[2];  // K, V
+  PrefillPlanes planes[2];
+  __nv_bfloat16* out[2];   // [blocks][num_kv_heads][kValueRows][dim]
+  int dim[2];
+  PrefillValues values;
+  const int32_t* query_starts;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  int num_seqs, tokens, num_kv_heads, num_blocks, block_size, max_blocks, window, blocks;
 };
 
 // Upkeep of the block bounds (pkv_sparse.cu).

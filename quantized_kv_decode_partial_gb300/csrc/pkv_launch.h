@@ -106,6 +106,7 @@ cudaError_t launch_prefill_u8(int dk, int dv, const PrefillParams& p, const CUte
                               const CUtensorMap& tv, int units, cudaStream_t stream, int device);
 cudaError_t launch_prefill_e4m3(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_values(const PrefillValuesParams& p, int fmt, cudaStream_t stream);
 cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream);
 
 cudaError_t launch_bounds(const BoundsParams& p, int fmt, int head_dim, int num_seqs, cudaStream_t stream);

@@ -17,6 +17,7 @@
 // CTAs whose f32 states (O, m, l) are joined by a second kernel.
 #pragma once
 
+#include "pkv_codes.cuh"
 #include "pkv_rotate.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -82,6 +83,7 @@ struct PrefillUnit {
   int tokens;
   int position;        // cache place of the first token
   const int32_t* table;
+  int dense;           // with values written beforehand: key t lies in block dense + t / 128
   bool live, valid;    // live: has tokens; valid: its sequence's lengths are
 };
 
@@ -108,35 +110,12 @@ __device__ __forceinline__ PrefillUnit prefill_unit(const PrefillParams& p, int 
   u.tokens = u.live ? static_cast<int>(min(n - first, static_cast<long long>(unit_tokens))) : 0;
   u.position = u.valid ? static_cast<int>(len - n + first) : 0;
   u.table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  u.dense = u.valid ? p.values.base(b, start) - p.values.first_row(len, static_cast<int>(n), p.window) / kValueRows : 0;
   if ((!starts_ok || (u.live && !u.valid)) && threadIdx.x == 0 && p.error_flag)
     atomicOr(p.error_flag, kDevErrBadSeqLen);
   return u;
 }
 
-// Pairs of f32 values in one register pair: packed arithmetic, each lane of it rounded as the scalar one.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -187,53 +166,6 @@ __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m,
     w[e] = pack_bf16x2(x, y);
   }
   return row_max<KT>(s);
-}
-
-// Sixteen codes of a row as bf16 pairs: scale * code (+ bias), in f32, rounded once.
-template <int FMT>
-__device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float bias, uint32_t (&out)[8]) {
-  if constexpr (FMT == kFmtE4m3) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t lo, hi;
-      e4m3x4_to_f16x2(w[i], lo, hi);
-      float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-      float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      unpair(mul2(pair(a.x, a.y), pair(scale, scale)), a.x, a.y);
-      unpair(mul2(pair(b.x, b.y), pair(scale, scale)), b.x, b.y);
-      out[2 * i] = pack_bf16x2(a.x, a.y);
-      out[2 * i + 1] = pack_bf16x2(b.x, b.y);
-    }
-  } else {
-    // codes as halves: 1024 + code has the code in its last bits
-    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f);
-    auto floats = [&](uint32_t bits) {
-      return __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&bits), k1024));
-    };
-    if constexpr (FMT == 8) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = floats(__byte_perm(w[i], 0x64646464u, 0x4140)), b = floats(__byte_perm(w[i], 0x64646464u, 0x4342));
-        out[2 * i] = pack_bf16x2(fmaf(a.x, scale, bias), fmaf(a.y, scale, bias));
-        out[2 * i + 1] = pack_bf16x2(fmaf(b.x, scale, bias), fmaf(b.y, scale, bias));
-      }
-    } else {
-      const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float2 n[4];  // codes k and k + 4
-#pragma unroll
-        for (int k = 0; k < 4; ++k) n[k] = floats((w[i] >> (4 * k) & 0x000F000Fu) | 0x64006400u);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          out[4 * i + k] = pack_bf16x2(fmaf(n[2 * k].x, scale, bias), fmaf(n[2 * k + 1].x, scale, bias));
-          out[4 * i + 2 + k] = pack_bf16x2(fmaf(n[2 * k].y, scale, bias), fmaf(n[2 * k + 1].y, scale, bias));
-        }
-      }
-    }
-  }
 }
 
 // Half of a quarter tile of codes (a warp's part of two): rows [first, first + KT/4) of the tile, 16 values a lane
@@ -409,17 +341,25 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   const bool any_bad = bad_blocks != 0;
   const int piece = 1 << p.piece_log2, pieces = KT >> p.piece_log2;
   const int items = nt * tiles_q;  // item i: query tile i % tiles_q, key tile t0 + i / tiles_q, score tile i & 1
-  // The pieces of key tile t that are copied, and (lane l) the pool row of piece l.
+  // The pieces of key tile t that are copied, and (lane l) the row of piece l in the pool or among the values.
   auto tile_pieces = [&](int t, int& row) {
     const int key = t * KT + lane * piece;
     bool ok = lane < pieces && key < hi && key + piece > lo;
     row = 0;
-    if (ok) {
+    if (ok && p.values.used) {
+      row = ((u.dense + key / kValueRows) * p.num_kv_heads + u.head) * kValueRows + key % kValueRows;
+    } else if (ok) {
       const int blk = key / p.block_size;
       const int phys = static_cast<int>(ld_keep_u32(u.table + blk));
       ok = static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_blocks);
       row = ok ? (phys * p.num_kv_heads + u.head) * p.block_size + (key - blk * p.block_size) : 0;
     }
+    return __ballot_sync(0xffffffffu, ok);
+  };
+  // Of 32 keys from `key` on, those whose block is in the pool (asked where some block is not).
+  auto good_keys = [&](int key) {
+    const int blk = min(key + lane, hi - 1) / p.block_size;
+    const bool ok = static_cast<unsigned>(u.table[blk]) < static_cast<unsigned>(p.num_blocks);
     return __ballot_sync(0xffffffffu, ok);
   };
 
@@ -694,17 +634,10 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         tmem_ld_tile<KT>(s_at, s);
         if (masked) {
           const int v0 = below + 1 - key, v1 = pos + 1 - key;
-          uint32_t bits = 0xFFFFFFFFu;
-          if (any_bad) {
-            int row;
-            bits = tile_pieces(t0 + j, row);
-          }
 #pragma unroll
           for (int h = 0; h < KT / 32; ++h) {
             uint32_t seen = low_bits(v1 - 32 * h) & ~low_bits(v0 - 32 * h);
-            if (any_bad)
-              for (int e = 0; e < 32; ++e)
-                if (!(bits >> ((32 * h + e) >> p.piece_log2) & 1)) seen &= ~(1u << e);
+            if (any_bad) seen &= good_keys(key + 32 * h);
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[32 * h + e] = (seen >> e & 1) ? s[32 * h + e] : -INFINITY;
           }

@@ -1,0 +1,102 @@
+// Values of the cached rows that a prompt attention call sees, as bf16, from pages of codes: written once, where
+// several query tiles would otherwise turn the same codes each for itself.
+//
+// One CTA per (128 rows, KV head): 16 codes a thread at a time, every load ahead of the first conversion. Bound by HBM:
+// it reads the codes and writes twice (8-bit) or four times (4-bit) their bytes.
+#include "pkv_codes.cuh"
+#include "pkv_launch.h"
+#include "pkv_rotate.cuh"
+
+namespace pkv {
+
+namespace {
+
+template <int D, int FMT>
+__device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int plane, const int32_t* table, int first_row,
+                                             int len, int head, size_t block) {
+  constexpr int kPerRow = D / 16, kRounds = kValueRows * kPerRow / 256;
+  uint4 v[kRounds];
+  float scale[kRounds], bias[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int c = i * 256 + threadIdx.x, r = c / kPerRow, col = c % kPerRow, t = first_row + r;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    scale[i] = bias[i] = 0.f;
+    if (t >= len) continue;
+    const int blk = t / p.block_size;
+    const int phys = table[blk];
+    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;  // flagged by the attention
+    const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + head;
+    const size_t row = cell * p.block_size + (t - blk * p.block_size);
+    if constexpr (FMT == 4) {
+      const uint2 w = ld_nc_keep_v2(p.pool[plane] + row * (D / 2) + col * 8);
+      v[i].x = w.x;
+      v[i].y = w.y;
+    } else {
+      v[i] = ld_nc_keep_v4(p.pool[plane] + row * D + col * 16);
+    }
+    if constexpr (FMT == kFmtE4m3) {
+      scale[i] = p.planes[plane].block_scales[cell];
+    } else {
+      scale[i] = __bfloat162float(p.planes[plane].scales[row * (D / 64) + col / 4]);
+      bias[i] = __bfloat162float(p.planes[plane].biases[row * (D / 64) + col / 4]);
+    }
+  }
+  __nv_bfloat16* out = p.out[plane] + (block * p.num_kv_heads + head) * kValueRows * D;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int c = i * 256 + threadIdx.x, r = c / kPerRow;
+    if (first_row + r >= len) continue;  // nobody's rows are left as they are
+    uint32_t w[8];
+    codes_to_bf16<FMT>(v[i], scale[i], bias[i], w);
+    uint4* to = reinterpret_cast<uint4*>(out) + 2 * c;
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int D, int DV, int FMT>
+__global__ void __launch_bounds__(256) pkv_prefill_values_kernel(const __grid_constant__ PrefillValuesParams p) {
+  wait_for_prerequisite_grids();
+  const int block = blockIdx.x, head = blockIdx.y;
+  const int b = find_last(p.num_seqs, block, [&](int i) { return p.values.base(i, p.query_starts[i]); });
+  const int start = p.query_starts[b], len = p.seq_lens[b];
+  const long long n = static_cast<long long>(p.query_starts[b + 1]) - start;
+  // bad starts and lengths are the attention's to flag
+  if (start < 0 || n <= 0 || start + n > p.tokens || len < n || len > static_cast<long long>(p.max_blocks) * p.block_size)
+    return;
+  const long long row = static_cast<long long>(block - p.values.base(b, start)) * kValueRows +
+                        p.values.first_row(len, static_cast<int>(n), p.window);
+  if (block < p.values.base(b, start) || row >= len) return;
+  const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, head, block);
+  plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, head, block);
+}
+
+template <int D, int DV, int FMT>
+cudaError_t launch_of(const PrefillValuesParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.blocks, p.num_kv_heads);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pkv_prefill_values_kernel<D, DV, FMT>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_values(const PrefillValuesParams& p, int fmt, cudaStream_t stream) {
+#define X(B_, DK_, DV_) \
+  if (fmt == B_ && p.dim[0] == DK_ && p.dim[1] == DV_) return launch_of<DK_, DV_, B_>(p, stream);
+#define AFFINE(B_) X(B_, 128, 128) X(B_, 256, 256) X(B_, 256, 128) X(B_, 128, 256)
+  AFFINE(kFmtE4m3) X(kFmtE4m3, 64, 64) X(kFmtE4m3, 192, 128) AFFINE(4) AFFINE(8)
+#undef AFFINE
+#undef X
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv

@@ -182,45 +182,54 @@ CODES = [(E4M3, d) for d in DIMS] + [(dict(bits=b), d) for b in (4, 8) for d in 
 
 
 @pytest.mark.parametrize("fmt,dims", CODES)
-@pytest.mark.parametrize("splits", [0, 1, 3])
-def test_pages_of_codes(fmt, dims, splits):
+@pytest.mark.parametrize("splits,reading", [(0, 0), (1, 1), (3, 1), (1, 2), (3, 2)])
+def test_pages_of_codes(fmt, dims, splits, reading):
     lens, news = [1, 700, 33, 129, 1000, 64, 130], [1, 200, 0, 129, 3, 64, 2]
     cache = Cache(lens, 2, *dims, 32, fmt, seed=splits)
-    check(randn(sum(news), 6, dims[0], seed=2), cache, news, 1 / math.sqrt(dims[0]), splits=splits)
+    check(randn(sum(news), 6, dims[0], seed=2), cache, news, 1 / math.sqrt(dims[0]), splits=splits, reading=reading)
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
 @pytest.mark.parametrize("bs", [8, 16, 32, 64, 96, 128, 256])
-def test_block_sizes_of_codes(fmt, bs):
+@pytest.mark.parametrize("reading", [1, 2])
+def test_block_sizes_of_codes(fmt, bs, reading):
     lens, news = [517, 130], [300, 130]
     for dims in ((128, 128), (256, 256)):
-        check(randn(sum(news), 4, dims[0], seed=3), Cache(lens, 2, *dims, bs, fmt, seed=bs + 1), news, 0.09, splits=1)
+        check(randn(sum(news), 4, dims[0], seed=3), Cache(lens, 2, *dims, bs, fmt, seed=bs + 1), news, 0.09, splits=1,
+              reading=reading)
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
 @pytest.mark.parametrize("window", [1, 100, 500])
-def test_windows_of_codes(fmt, window):
-    lens, news = [900, 260, 5], [300, 260, 5]
+@pytest.mark.parametrize("reading", [1, 2])
+def test_windows_of_codes(fmt, window, reading):
+    lens, news = [900, 260, 5, 2000, 129], [300, 260, 5, 0, 129]
     for dims in ((128, 128), (256, 256)):
-        check(randn(sum(news), 4, dims[0], seed=5), Cache(lens, 2, *dims, 32, fmt), news, 0.09, window=window)
+        check(randn(sum(news), 4, dims[0], seed=5), Cache(lens, 2, *dims, 32, fmt), news, 0.09, window=window, reading=reading)
+    # tables so wide that the values lie by tokens
+    cache = Cache(lens, 2, 128, 128, 32, fmt)
+    cache.tables = torch.nn.functional.pad(cache.tables, (0, 400), value=-1)
+    check(randn(sum(news), 4, 128, seed=5), cache, news, 0.09, window=window, reading=reading)
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
 @pytest.mark.parametrize("dims", [(128, 128), (256, 256)])
-def test_bad_blocks_of_codes_are_skipped(fmt, dims):
+@pytest.mark.parametrize("reading", [1, 2])
+def test_bad_blocks_of_codes_are_skipped(fmt, dims, reading):
     lens, news = [300, 200], [150, 200]
     cache = Cache(lens, 2, *dims, 32, fmt)
     q = randn(350, 4, dims[0], seed=10)
     tables = cache.tables.clone()
     tables[0, 3], tables[1, 0], tables[1, 5] = -1, 10 ** 6, cache.pools[0].shape[0]
-    got, err = run(q, cache, news, 0.09, tables=tables)
+    got, err = run(q, cache, news, 0.09, tables=tables, reading=reading)
     assert err == 1
     gone = {0: [3], 1: [0, 5]}
     ref, tol = reference(q, cache, news, 0.09, hidden=lambda b: torch.tensor([t // 32 in gone[b] for t in range(512)], device=DEV))
     assert bool(((got.double() - ref).abs() <= tol).all())
 
 
-def test_block_scales_of_zero_and_far_apart():
+@pytest.mark.parametrize("reading", [1, 2])
+def test_block_scales_of_zero_and_far_apart(reading):
     cache = Cache([300], 2, 128, 128, 32, E4M3)
     for name, scale, row in (("k_scales", 0.0, 2), ("v_scales", 0.0, 3), ("v_scales", 2.0 ** 30, 4), ("v_scales", 2.0 ** -40, 5),
                              ("k_scales", 2.0 ** -40, 6)):
@@ -228,7 +237,7 @@ def test_block_scales_of_zero_and_far_apart():
         which = 0 if name[0] == "k" else 1
         cache.values[which][at] *= scale / cache.planes[name][at].double()[:, None, None]
         cache.planes[name][at] = scale
-    check(randn(300, 4, 128, seed=14), cache, [300], 0.09)
+    check(randn(300, 4, 128, seed=14), cache, [300], 0.09, reading=reading)
 
 
 def test_rising_maxima_are_followed():
@@ -297,6 +306,23 @@ def test_bad_blocks_are_skipped(splits, dk, dv):
     ref, tol = reference(q, cache, news, 0.09, hidden=hidden)
     assert bool(((got.double() - ref).abs() <= tol).all())
     assert not got[150:182].any()  # their only block is none
+
+
+@pytest.mark.parametrize("reading", [1, 2])
+def test_bad_lengths_and_starts_over_codes(reading):
+    lens, news = [200, 150, 90], [100, 50, 90]
+    cache = Cache(lens, 2, 128, 128, 32, E4M3)
+    q = randn(240, 4, 128, seed=9)
+    ref, tol = reference(q, cache, news, 0.09)
+    for bad in (49, -1, 10 ** 6, 2 ** 31 - 1):
+        got, err = run(q, cache, news, 0.09, lens=[200, bad, 90], reading=reading, window=1000)
+        assert err == 2 and not got[100:150].any()
+        diff = (got.double() - ref).abs()
+        assert bool((diff <= tol)[:100].all()) and bool((diff <= tol)[150:].all())
+    for starts in ([0, 160, 140, 240], [0, 50, 100, 241], [-3, 50, 100, 240], [0, 2 ** 31 - 1, 100, 240], [240, 50, 0, 0]):
+        out = torch.full((242, 4, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+        _, err = run(q, cache, news, 0.09, starts=starts, out=out[1:241], reading=reading)
+        assert err & 2 and (out[0] == 5.0).all() and (out[241] == 5.0).all()
 
 
 def test_starts_that_fall_or_leave_the_tokens_touch_nothing_else():
