@@ -166,7 +166,8 @@ struct RotateParams {
   float* block_scales[2];
   int32_t* error_flag;
   int num_blocks, block_size, max_blocks;
-  int q_ctas, head_warps, table_rows;  // e4m3 pages: CTAs of query rows, warps per KV head, rows whose angles are tabled
+  int q_ctas;                  // CTAs of whole tokens (e4m3 pages: of their queries)
+  int head_warps, table_rows;  // e4m3 pages: warps per KV head, rows whose angles are tabled
 };
 
 // Attention of many new tokens over the pages (pkv_prefill.cuh).
@@ -404,6 +405,16 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint6
                : "memory");
 }
 
+// The same without a hint; with there = false nothing is read and 16 zero bytes are written.
+__device__ __forceinline__ void cp_async_16_or_zeros(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 4-byte copy global -> shared through the load/store path.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -418,6 +429,12 @@ __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
 

@@ -11,6 +11,7 @@
 // one scale per block, which needs the largest of the block's new values before the first code
 // is written: there CTAs take (touched block, plane, a few KV heads), hold the rows in
 // registers between the two uses and share the block's angles through shared memory.
+#include <algorithm>
 #include <type_traits>
 
 #include "pkv_append.cuh"
@@ -24,9 +25,10 @@ namespace {
 
 constexpr int kPlain = 0;  // FMT of the kernel without the write
 
-constexpr int kTokenBatch = 4;  // rows a lane has in flight
+constexpr int kRing = 8;        // slots (a warp's rows at once) in flight
+constexpr int kSlotBytes = 512;
 constexpr int kBlockHold = 8;   // row batches a lane of the block path keeps in registers
-constexpr int kTableBytes = 40 << 10;  // of the 48 KB that a launch may have unasked
+constexpr int kTableBytes = 36 << 10;  // of the 48 KB that a launch may have unasked
 
 template <int FMT>
 constexpr int kWarps = FMT == kFmtE4m3 ? 8 : 4;
@@ -55,77 +57,97 @@ __device__ __forceinline__ TokenPlace place_of(const RotateParams& p, int t) {
   return at;
 }
 
-__device__ __forceinline__ long long row_base(const HeadRows& r, const RotateParams& p, int t) {
-  if (p.tokens_per_seq == 0) return t * r.token;
+// A token's sequence and place where the rows are not packed: (0, t) else.
+struct RowAt {
+  int seq, token;
+};
+__device__ __forceinline__ RowAt row_at(const RotateParams& p, int t) {
+  if (p.tokens_per_seq == 0 || p.num_seqs == 1) return {0, t};
   const int b = t / p.tokens_per_seq;
-  return b * r.seq + (t - b * p.tokens_per_seq) * r.token;
+  return {b, t - b * p.tokens_per_seq};
+}
+__device__ __forceinline__ __nv_bfloat16* rows_of(const HeadRows& r, const RowAt& at) {
+  return r.data + at.seq * r.seq + at.token * r.token;
 }
 
-// A lane's eight norm weights (ones where the row has no norm).
-__device__ __forceinline__ void lane_weights(const RotateParams& p, const void* weight, bool used, int off0, int off1,
-                                             float (&w)[8]) {
+// A lane's eight norm weights.
+template <int D>
+__device__ __forceinline__ void lane_weights(const RotateTables<D>& tab, bool key, bool used, int off0, int off1, float (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (weight && used) {
-    load_weight4(weight, p.weight_f32, off0, p.weight_offset, w);
-    load_weight4(weight, p.weight_f32, off1, p.weight_offset, w + 4);
+  if (used) {
+    const float4 a = *reinterpret_cast<const float4*>(&tab.weight[key][off0]);
+    const float4 b = *reinterpret_cast<const float4*>(&tab.weight[key][off1]);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
 }
 
 // cos and sin of a lane's four pairs at token t.
-__device__ __forceinline__ void lane_angles(const RotateParams& p, int u, int t, int cache_place, float (&cs)[4],
-                                            float (&sn)[4]) {
+template <int D>
+__device__ __forceinline__ void lane_angles(const RotateParams& p, const RotateTables<D>& tab, int u, int t, int cache_place,
+                                            float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int f = u * 4 + i;
-    const int pos =
-        p.positions ? p.positions[static_cast<long long>(axis_of(p.turn, f)) * p.tokens + t] : cache_place;
-    turn_at(turn_step(p.inv_freq[f]), pos, p.turn.amplitude, cs[i], sn[i]);
+    const int pos = p.positions ? p.positions[static_cast<long long>(tab.axis[f]) * p.tokens + t] : cache_place;
+    turn_at(tab.step[f], pos, p.turn.amplitude, cs[i], sn[i]);
   }
 }
 
 // One warp: share g of token t's rows. With pages, D and DV are theirs.
-template <int D, int DV, int FMT>
-__device__ __forceinline__ void token_rows(const RotateParams& p, int t, int g, __nv_bfloat16* stage) {
+template <int D, int DV, int FMT, bool SIMPLE>
+__device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTables<D>& tab, int t, int g,
+                                           unsigned char* ring_smem, __nv_bfloat16* stage) {
   using L = RowLanes<D>;
   const int lane = threadIdx.x & 31;
   const int sub = lane / L::kLanes, u = lane % L::kLanes;
-  const bool used = u < L::kUsed;
+  const bool used = L::kUsed == L::kLanes || u < L::kUsed;
   int off0, off1;
   run_offsets(p.turn, u, off0, off1);
   const int HQ = p.num_q_heads, HK = p.num_kv_heads;
-  // keys that leave through registers join the queries' rows
+  // Keys that leave through registers follow the queries: slots of kRows rows, this share's every groups-th.
   constexpr bool kKeysHere = FMT == kPlain || FMT == 16;
-  const int rows = HQ + (kKeysHere ? HK : 0);
-  const int slots = (rows + L::kRows - 1) / L::kRows;
-  const __nv_bfloat16* q_src = p.q.data + row_base(p.q, p, t);
-  const __nv_bfloat16* k_src = (FMT == kPlain && HK == 0) ? nullptr : p.k.data + row_base(p.k, p, t);
+  const int q_slots = (HQ + L::kRows - 1) / L::kRows, k_slots = kKeysHere ? (HK + L::kRows - 1) / L::kRows : 0;
+  const int slots = q_slots + k_slots, G = p.groups;
+  const RowAt row = row_at(p, t);
+  const __nv_bfloat16* k_src = (FMT == kPlain && HK == 0) ? nullptr : rows_of(p.k, row);
 
-  uint2 a[kTokenBatch], b[kTokenBatch];
-  auto load = [&](int s0) {
-#pragma unroll
-    for (int j = 0; j < kTokenBatch; ++j) {
-      const int r = (s0 + j * p.groups) * L::kRows + sub;
-      a[j] = b[j] = make_uint2(0u, 0u);
-      if (used && r < rows) {
-        const __nv_bfloat16* src = r < HQ ? q_src + r * p.q.head : k_src + (r - HQ) * p.k.head;
-        a[j] = ld_nc_keep_v2(src + off0);
-        b[j] = ld_nc_keep_v2(src + off1);
-      }
+  // Rows come through a ring in shared memory, kRing slots ahead: loads in flight without registers. Rows that do not
+  // exist are asked for with no bytes, which leaves zeros.
+  const uint32_t ring = smem_addr(ring_smem) + lane * 16;
+  auto key_row = [&](const __nv_bfloat16* base, long long head, int s) { return base + ((s - q_slots) * L::kRows + sub) * head; };
+  int ask_s = g;
+  const __nv_bfloat16* ask_at =
+      (g < q_slots ? rows_of(p.q, row) + (g * L::kRows + sub) * p.q.head : key_row(k_src, p.k.head, g)) + u * 8;
+  long long ask_step = (g < q_slots ? p.q.head : p.k.head) * (G * L::kRows);
+  int ask_left = (g < q_slots ? HQ : q_slots * L::kRows + HK) - (g * L::kRows + sub);
+  auto ask = [&](uint32_t place) {
+    const bool there = used && ask_left > 0 && ask_s < slots;
+    cp_async_16_or_zeros(ring + place, there ? ask_at : p.q.data, there);
+    cp_async_commit();
+    const bool was_query = ask_s < q_slots;
+    ask_s += G;
+    ask_left -= G * L::kRows;
+    ask_at += ask_step;
+    if (kKeysHere && was_query && ask_s >= q_slots) {
+      ask_at = key_row(k_src, p.k.head, ask_s) + u * 8;
+      ask_step = p.k.head * (G * L::kRows);
+      ask_left = HK - ((ask_s - q_slots) * L::kRows + sub);
     }
   };
-  load(g);
-
-  float wq[8], wk[8], cs[4], sn[4];
-  lane_weights(p, p.q_weight, used, off0, off1, wq);
-  lane_weights(p, p.k_weight, used, off0, off1, wk);
+#pragma unroll 1
+  for (int i = 0; i < kRing; ++i) ask(i * kSlotBytes);
 
   // where the keys go
   TokenPlace at{};
   int phys = -1, offset = 0, cache_place = 0;
   if constexpr (FMT != kPlain) {
     at = place_of(p, t);
-    if (!at.in_sequence) return;
+    if (!at.in_sequence) {
+      cp_async_wait<0>();
+      return;
+    }
     const int len = p.seq_lens[at.seq];
     cache_place = static_cast<int>(static_cast<unsigned>(len) + static_cast<unsigned>(at.index));
     if (FMT != kFmtE4m3) {
@@ -143,63 +165,81 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, int t, int g, 
       }
     }
   }
-  const bool turned = u * 8 < p.turn.rot;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) cs[i] = sn[i] = 0.f;
-  if (turned) lane_angles(p, u, t, cache_place, cs, sn);
+  const bool turned = SIMPLE || u * 8 < p.turn.rot, adjacent = p.turn.adjacent != 0;
+  float w[8], cs[4] = {0.f, 0.f, 0.f, 0.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  if (turned && used) lane_angles(p, tab, u, t, cache_place, cs, sn);
+  bool key = g >= q_slots;
+  lane_weights(tab, key, used, off0, off1, w);
+  LaneTurn turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
 
-  const bool any_norm = p.q_weight || p.k_weight;
-  const long long q_to = row_base(p.q_out, p, t);
-  const long long k_to = FMT == kPlain && HK > 0 ? row_base(p.k_out, p, t) : 0;
   auto pool_row = [&](int h) { return (static_cast<size_t>(phys) * HK + h) * p.block_size + offset; };
-  for (int s0 = g; s0 < slots; s0 += kTokenBatch * p.groups) {
-    if (s0 != g) load(s0);
-#pragma unroll
-    for (int j = 0; j < kTokenBatch; ++j) {
-      const int s = s0 + j * p.groups;
-      if (s >= slots) break;
-      const int r = s * L::kRows + sub;
-      const bool key = r >= HQ;
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = key ? wk[i] : wq[i];
-      turn_row<D>(a[j], b[j], any_norm, (key ? p.k_weight : p.q_weight) != nullptr, w, p.eps, turned, p.turn.adjacent,
-                  cs, sn);
-      if (!used || r >= rows) continue;
-      __nv_bfloat16* to;
-      if (!key) {
-        to = p.q_out.data + q_to + r * p.q_out.head;
-      } else if constexpr (FMT == kPlain) {
-        to = p.k_out.data + k_to + (r - HQ) * p.k_out.head;
-      } else {
-        if (phys < 0) continue;
-        to = p.dst.k_pool_bf16 + pool_row(r - HQ) * D;
-      }
-      *reinterpret_cast<uint2*>(to + off0) = a[j];
-      *reinterpret_cast<uint2*>(to + off1) = b[j];
-    }
+  __nv_bfloat16* k_to = nullptr;
+  long long k_head = 0;
+  if constexpr (FMT == kPlain) {
+    if (HK > 0) k_to = rows_of(p.k_out, row);
+    k_head = p.k_out.head;
+  } else if constexpr (FMT == 16) {
+    if (phys >= 0) k_to = p.dst.k_pool_bf16 + pool_row(0) * D;
+    k_head = static_cast<long long>(p.block_size) * D;
   }
+  __nv_bfloat16* to = key ? (k_to ? k_to + ((g - q_slots) * L::kRows + sub) * k_head : nullptr)
+                          : rows_of(p.q_out, row) + (g * L::kRows + sub) * p.q_out.head;
+  long long to_step = (key ? k_head : p.q_out.head) * (G * L::kRows);
+  int left = (key ? q_slots * L::kRows + HK : HQ) - (g * L::kRows + sub);  // rows of this kind from the lane's on
+  bool normed = (key ? p.k_weight : p.q_weight) != nullptr;
+  uint32_t place = 0;
+#pragma unroll 1
+  for (int s = g; s < slots; s += G) {
+    if (kKeysHere && !key && s >= q_slots) {  // from here on keys
+      if (!k_to) break;
+      key = true;
+      lane_weights(tab, true, used, off0, off1, w);
+      turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
+      to = k_to + ((s - q_slots) * L::kRows + sub) * k_head;
+      to_step = k_head * (G * L::kRows);
+      left = HK - ((s - q_slots) * L::kRows + sub);
+      normed = p.k_weight != nullptr;
+    }
+    cp_async_wait<kRing - 1>();
+    __syncwarp();  // every lane's part of the slot is there
+    const uint32_t from = ring + place - u * 16;
+    uint2 a = ld_shared_v2(from + off0 * 2), b = ld_shared_v2(from + off1 * 2);
+    if (!used) a = b = make_uint2(0u, 0u);
+    __syncwarp();  // every lane has read the slot
+    ask(place);
+    place = (place + kSlotBytes) & (kRing * kSlotBytes - 1);
+    turn_row<D, SIMPLE>(a, b, normed, p.eps, turned, adjacent, turn);
+    if (used && left > 0 && to) {
+      *reinterpret_cast<uint2*>(to + off0) = a;
+      *reinterpret_cast<uint2*>(to + off1) = b;
+    }
+    to += to_step;
+    left -= G * L::kRows;
+  }
+  cp_async_wait<0>();
 
   if constexpr (FMT == 16) {
     if (phys < 0) return;
-    const __nv_bfloat16* v_src = p.v.data + row_base(p.v, p, t);
+    const __nv_bfloat16* v_src = rows_of(p.v, row);
     constexpr int kChunks = DV / 8;
-    for (int c = g * 32 + lane; c < HK * kChunks; c += p.groups * 32) {
+    for (int c = g * 32 + lane; c < HK * kChunks; c += G * 32) {
       const int h = c / kChunks, at8 = (c % kChunks) * 8;
       *reinterpret_cast<uint4*>(p.dst.v_pool_bf16 + pool_row(h) * DV + at8) = ld_nc_keep_v4(v_src + h * p.v.head + at8);
     }
   }
   if constexpr (FMT == 4 || FMT == 8) {
     if (phys < 0) return;
-    const __nv_bfloat16* v_src = p.v.data + row_base(p.v, p, t);
-    for (int h0 = g * L::kRows; h0 < HK; h0 += p.groups * L::kRows) {
+    const __nv_bfloat16* v_src = rows_of(p.v, row);
+    lane_weights(tab, true, used, off0, off1, w);
+    turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
+    for (int h0 = g * L::kRows; h0 < HK; h0 += G * L::kRows) {
       const int h = h0 + sub;
       uint2 x = make_uint2(0u, 0u), y = x;
       if (used && h < HK) {
         x = ld_nc_keep_v2(k_src + h * p.k.head + off0);
         y = ld_nc_keep_v2(k_src + h * p.k.head + off1);
       }
-      turn_row<D>(x, y, any_norm, p.k_weight != nullptr, wk, p.eps, turned, p.turn.adjacent, cs, sn);
+      turn_row<D, SIMPLE>(x, y, p.k_weight != nullptr, p.eps, turned, adjacent, turn);
       __syncwarp();  // the rows staged before have been read
       if (used) {
         *reinterpret_cast<uint2*>(stage + sub * D + off0) = x;
@@ -209,19 +249,20 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, int t, int g, 
 #pragma unroll
       for (int i = 0; i < L::kRows; ++i) {
         if (h0 + i >= HK) break;
-        const size_t row = pool_row(h0 + i);
-        append_plane<FMT, D>(stage + i * D, nullptr, p.dst.k_pool_words, p.dst.k_scales, p.dst.k_biases, row, lane);
+        const size_t to_row = pool_row(h0 + i);
+        append_plane<FMT, D>(stage + i * D, nullptr, p.dst.k_pool_words, p.dst.k_scales, p.dst.k_biases, to_row, lane);
         append_plane<FMT, DV>(v_src + (h0 + i) * p.v.head, nullptr, p.dst.v_pool_words, p.dst.v_scales, p.dst.v_biases,
-                              row, lane);
+                              to_row, lane);
       }
     }
+    __syncwarp();  // the stage is the next token's ring
   }
 }
 
 // One CTA: the new rows of one touched block, in one plane of the KV heads from h0 on. TURN: keys
 // (normed and rotated), else values.
-template <int D, bool TURN>
-__device__ __forceinline__ void block_rows(const RotateParams& p, int slot, int h0, float2* table, uint32_t* red) {
+template <int D, bool TURN, bool SIMPLE, typename Tables>
+__device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, int slot, int h0, float2* table, uint32_t* red) {
   using L = RowLanes<D>;
   constexpr int kPlane = TURN ? 0 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -261,7 +302,7 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, int slot, int 
   const bool used = u < L::kUsed;
   int off0 = u * 8, off1 = u * 8 + 4;
   if (TURN) run_offsets(p.turn, u, off0, off1);
-  const bool turned = TURN && u * 8 < p.turn.rot;
+  const bool turned = TURN && (SIMPLE || u * 8 < p.turn.rot) && used;
   const int per_head = p.head_warps;
   const int h = h0 + warp / per_head, part = warp % per_head;
   const bool live = h < p.num_kv_heads;
@@ -285,15 +326,17 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, int slot, int 
   }
   float w[8];
   const int tabled = min(p.table_rows, r1 - r0), half = p.turn.rot / 2;
-  if (TURN) {
-    lane_weights(p, p.k_weight, used, off0, off1, w);
+  if constexpr (TURN) {
+    fill_tables(tab, p);
+    __syncthreads();
+    lane_weights(tab, true, used, off0, off1, w);
     for (int i = threadIdx.x; i < tabled * half; i += blockDim.x) {
       const int r = i / half, f = i - r * half;
       const int token = start + j0 + r;
-      const int pos = p.positions ? p.positions[static_cast<long long>(axis_of(p.turn, f)) * p.tokens + token]
-                                  : len + j0 + r;
+      const int pos =
+          p.positions ? p.positions[static_cast<long long>(tab.axis[f]) * p.tokens + token] : len + j0 + r;
       float c, s;
-      turn_at(turn_step(p.inv_freq[f]), pos, p.turn.amplitude, c, s);
+      turn_at(tab.step[f], pos, p.turn.amplitude, c, s);
       table[i] = make_float2(c, s);
     }
     __syncthreads();
@@ -310,10 +353,11 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, int slot, int 
             sn[i] = v.y;
           }
         } else {
-          lane_angles(p, u, start + j0 + r - r0, len + j0 + r - r0, cs, sn);
+          lane_angles(p, tab, u, start + j0 + r - r0, len + j0 + r - r0, cs, sn);
         }
       }
-      turn_row<D>(x, y, p.k_weight != nullptr, p.k_weight != nullptr, w, p.eps, turned, p.turn.adjacent, cs, sn);
+      turn_row<D, SIMPLE>(x, y, p.k_weight != nullptr, p.eps, turned, p.turn.adjacent,
+                          make_turn<SIMPLE>(w, cs, sn, turned, p.turn.adjacent));
     }
   };
   uint32_t m = 0u;
@@ -382,9 +426,10 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, int slot, int 
   }
 }
 
-template <int D, int DV, int FMT>
-__global__ void __launch_bounds__(kWarps<FMT> * 32) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
+template <int D, int DV, int FMT, bool SIMPLE>
+__global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 8) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ RotateTables<D> tab;
   __shared__ uint32_t red[kWarps<FMT>];
   wait_for_prerequisite_grids();
   if constexpr (FMT == kFmtE4m3) {
@@ -395,28 +440,31 @@ __global__ void __launch_bounds__(kWarps<FMT> * 32) pkv_rotate_kernel(const __gr
       const int slot = unit / (2 * head_groups), rest = unit - slot * 2 * head_groups;
       float2* table = reinterpret_cast<float2*>(smem);
       if (rest & 1) {
-        block_rows<DV, false>(p, slot, (rest >> 1) * heads, table, red);
+        block_rows<DV, false, SIMPLE>(p, tab, slot, (rest >> 1) * heads, table, red);
       } else {
-        block_rows<D, true>(p, slot, (rest >> 1) * heads, table, red);
+        block_rows<D, true, SIMPLE>(p, tab, slot, (rest >> 1) * heads, table, red);
       }
       return;
     }
   }
+  fill_tables(tab, p);
+  __syncthreads();
   const int warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<FMT> + warp;
-  const int t = static_cast<int>(unit / p.groups), g = static_cast<int>(unit - static_cast<long long>(t) * p.groups);
-  if (t >= p.tokens) return;
-  __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem) + warp * RowLanes<D>::kRows * D;
-  token_rows<D, DV, FMT>(p, t, g, stage);
+  unsigned char* mine = smem + warp * kRing * kSlotBytes;  // a staged row of the affine write takes the ring's place
+  const long long units = static_cast<long long>(p.tokens) * p.groups, step = static_cast<long long>(p.q_ctas) * kWarps<FMT>;
+  for (long long unit = static_cast<long long>(blockIdx.x) * kWarps<FMT> + warp; unit < units; unit += step) {
+    const int t = p.groups == 1 ? static_cast<int>(unit) : static_cast<int>(unit / p.groups);
+    const int g = static_cast<int>(unit - static_cast<long long>(t) * p.groups);
+    token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, reinterpret_cast<__nv_bfloat16*>(mine));
+  }
 }
 
-// Warps per token: as many as fill the GPU, each with whole batches of rows where it has several.
+// Warps per token: as many as fill the GPU.
 int token_groups(long long tokens, int slots, int sm_count) {
   const long long want = 32ll * sm_count;
   long long groups = (want + tokens - 1) / tokens;
   groups = groups < 1 ? 1 : groups > slots ? slots : groups;
-  int per = static_cast<int>((slots + groups - 1) / groups);
-  if (per > kTokenBatch) per = (per + kTokenBatch - 1) / kTokenBatch * kTokenBatch;
+  const int per = static_cast<int>((slots + groups - 1) / groups);
   return (slots + per - 1) / per;
 }
 
@@ -424,13 +472,15 @@ template <int D, int DV, int FMT>
 cudaError_t launch_of(RotateParams p, int sm_count, cudaStream_t stream) {
   using L = RowLanes<D>;
   constexpr bool kKeysHere = FMT == kPlain || FMT == 16;
-  const int rows = p.num_q_heads + (kKeysHere ? p.num_kv_heads : 0);
-  p.groups = token_groups(p.tokens, (rows + L::kRows - 1) / L::kRows, sm_count);
+  const int slots = (p.num_q_heads + L::kRows - 1) / L::kRows + (kKeysHere ? (p.num_kv_heads + L::kRows - 1) / L::kRows : 0);
+  p.groups = token_groups(p.tokens, slots, sm_count);
+  // One wave of CTAs, each of which fills its tables once and takes many tokens.
+  const long long most_ctas = (FMT == kFmtE4m3 ? 3ll : 8ll) * sm_count;
   long long ctas = (static_cast<long long>(p.tokens) * p.groups + kWarps<FMT> - 1) / kWarps<FMT>;
-  size_t smem = 0;
-  if (FMT == 4 || FMT == 8) smem = kWarps<FMT> * L::kRows * D * 2;
+  ctas = std::min(ctas, most_ctas);
+  p.q_ctas = static_cast<int>(ctas);
+  size_t smem = kWarps<FMT> * kRing * kSlotBytes;
   if (FMT == kFmtE4m3) {
-    p.q_ctas = static_cast<int>(ctas);
     const int most = p.tokens_per_seq > 0 ? p.tokens_per_seq : p.tokens;
     const int held = most < p.block_size ? most : p.block_size;  // new rows of a block
     // Warps per KV head: enough that the block's rows stay in registers, and that few heads fill a CTA.
@@ -442,7 +492,7 @@ cudaError_t launch_of(RotateParams p, int sm_count, cudaStream_t stream) {
       p.head_warps *= 2;
     const int fit = kTableBytes / (p.turn.rot * 4);
     p.table_rows = held < fit ? held : fit;
-    smem = static_cast<size_t>(p.table_rows) * p.turn.rot * 4;
+    smem = std::max(smem, static_cast<size_t>(p.table_rows) * p.turn.rot * 4);
     const int heads = kWarps<FMT> / p.head_warps;
     const long long head_groups = (p.num_kv_heads + heads - 1) / heads;
     ctas += (p.tokens / p.block_size + 2ll * p.num_seqs) * head_groups * 2;
@@ -458,7 +508,8 @@ cudaError_t launch_of(RotateParams p, int sm_count, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_rotate_kernel<D, DV, FMT>, p);
+  return p.turn.rot == D && !p.turn.adjacent ? cudaLaunchKernelEx(&cfg, pkv_rotate_kernel<D, DV, FMT, true>, p)
+                                             : cudaLaunchKernelEx(&cfg, pkv_rotate_kernel<D, DV, FMT, false>, p);
 }
 
 }  // namespace

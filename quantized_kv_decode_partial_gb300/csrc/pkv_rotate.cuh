@@ -13,6 +13,7 @@
 // turns; nothing of it runs in f64, whose rate here is two FMAs per clock and SM.
 #pragma once
 
+#include "pkv_codes.cuh"
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -36,12 +37,24 @@ __device__ __forceinline__ uint64_t turn_step(float f) {
   return (u >> 31) ? 0ull - c : c;
 }
 
+// cos and sin (times amplitude) of `position` steps. The angle is brought to the nearest quarter turn, f of a turn away
+// (|f| <= 1/8): there their Taylor series in f^2 are off by less than 2^-28.
 __device__ __forceinline__ void turn_at(uint64_t step, int position, float amplitude, float& c, float& s) {
   const uint64_t turns = step * static_cast<uint64_t>(static_cast<int64_t>(position));
-  // the upper 32 bits as half turns in [-1, 1)
-  sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &s, &c);
-  c = __fmul_rn(c, amplitude);
-  s = __fmul_rn(s, amplitude);
+  const uint32_t u = static_cast<uint32_t>(turns >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
+  const float f = static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 0x1p-32f;
+  const float z = __fmul_rn(f, f);
+  // (2 pi)^n / n!
+  float sn = __fmaf_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(42.0586939f, z, -76.7058597f), z, 81.6052492f), z, -41.3417022f), z,
+                       6.28318531f);
+  sn = __fmul_rn(sn, f);
+  float cn = __fmaf_rn(__fmaf_rn(-26.4262567f, z, 60.2446413f), z, -85.4568172f);
+  cn = __fmaf_rn(__fmaf_rn(__fmaf_rn(cn, z, 64.9393940f), z, -19.7392088f), z, 1.f);
+  const bool odd = quarter & 1;
+  const float x = odd ? sn : cn, y = odd ? cn : sn;
+  c = __fmul_rn(__uint_as_float(__float_as_uint(x) ^ ((quarter + 1 & 2) << 30)), amplitude);
+  s = __fmul_rn(__uint_as_float(__float_as_uint(y) ^ ((quarter & 2) << 30)), amplitude);
 }
 
 // The axis whose position turns frequency i.
@@ -63,62 +76,129 @@ __device__ __forceinline__ void run_offsets(const RotationShape& r, int u, int& 
   off1 = halves ? r.rot / 2 + u * 4 : u * 8 + 4;
 }
 
-// A norm weight's four values from index i on (plus the offset), f32 or bf16.
-__device__ __forceinline__ void load_weight4(const void* w, bool f32, int i, float offset, float* out) {
-  if (f32) {
-    const float* p = static_cast<const float*>(w) + i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = __fadd_rn(p[j], offset);
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = __fadd_rn(__bfloat162float(p[j]), offset);
+// What does not change from token to token, in shared memory: each frequency's step and axis, and the norm weights
+// (plus their offset; ones where there is no norm).
+template <int D>
+struct __align__(16) RotateTables {
+  uint64_t step[D / 2];
+  float weight[2][D];  // queries', keys'
+  uint8_t axis[D / 2];
+};
+
+// Filled by the whole block; the caller synchronises.
+template <int D>
+__device__ __forceinline__ void fill_tables(RotateTables<D>& tab, const RotateParams& p) {
+  for (int i = threadIdx.x; i < p.turn.rot / 2; i += blockDim.x) {
+    tab.step[i] = turn_step(p.inv_freq[i]);
+    tab.axis[i] = static_cast<uint8_t>(axis_of(p.turn, i));
+  }
+  for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+    const void* w = i < D ? p.q_weight : p.k_weight;
+    const int d = i < D ? i : i - D;
+    float x = 1.f;
+    if (w)
+      x = __fadd_rn(p.weight_f32 ? static_cast<const float*>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d]),
+                    p.weight_offset);
+    (&tab.weight[0][0])[i] = x;
   }
 }
 
-// Norm and rotation of a lane's eight values (a: the run at off0, b: at off1). Every lane of the
-// warp takes part; lanes without values pass zeros. Fused multiply-adds are spelled out, so
-// that every kernel that includes this gives the same bits.
-//   normed     the row is divided by its root mean square and multiplied by w
-//   turned     the lane's values turn; cs, sn: of its four pairs
-template <int D>
-__device__ __forceinline__ void turn_row(uint2& a, uint2& b, bool any_norm, bool normed, const float (&w)[8], float eps,
-                                         bool turned, bool adjacent, const float (&cs)[4], const float (&sn)[4]) {
-  float x[8];
-  const uint32_t v[4] = {a.x, a.y, b.x, b.y};
+// What a lane's eight values are multiplied by: value v of a pair becomes r * (v * own + partner * other), r
+// the row's norm. own and other hold the norm weight times cos and sin, so a token's heads share them.
+struct LaneTurn {
+  uint64_t own[4], other[4];  // of the values (0, 1), (2, 3) of the first run, then of the second
+};
+
+// w: the eight weights (ones without a norm); cs, sn: of the lane's four pairs. Products are spelled out here and below,
+// so that every kernel that includes this gives the same bits. SIMPLE: whole heads turn, in halves (then `turned` and
+// `adjacent` are not looked at): the usual form, without the branches of the others.
+template <bool SIMPLE>
+__device__ __forceinline__ LaneTurn make_turn(const float (&w)[8], const float (&cs)[4], const float (&sn)[4], bool turned,
+                                              bool adjacent) {
+  LaneTurn t;
+  if (SIMPLE) adjacent = false;
+  if (!SIMPLE && !turned) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.own[i] = pair(w[2 * i], w[2 * i + 1]);
+      t.other[i] = 0ull;
+    }
+    return t;
+  }
+  float p[8], q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // pair i: the values a and b
+    const float wa = adjacent ? w[2 * i] : w[i], wb = adjacent ? w[2 * i + 1] : w[4 + i];
+    const float pa = __fmul_rn(wa, cs[i]), pb = __fmul_rn(wb, cs[i]), qa = -__fmul_rn(wb, sn[i]), qb = __fmul_rn(wa, sn[i]);
+    if (adjacent) {
+      p[2 * i] = pa;
+      p[2 * i + 1] = pb;
+      q[2 * i] = qa;
+      q[2 * i + 1] = qb;
+    } else {
+      p[i] = pa;
+      p[4 + i] = pb;
+      q[i] = qa;
+      q[4 + i] = qb;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(v[i] << 16);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    t.own[i] = pair(p[2 * i], p[2 * i + 1]);
+    t.other[i] = pair(q[2 * i], q[2 * i + 1]);
   }
-  if (any_norm) {
-    float ss = 0.f;
+  return t;
+}
+
+// Norm and rotation of a lane's eight values (a: the run at off0, b: at off1). Every lane of the warp takes part;
+// lanes without values pass zeros.
+template <int D, bool SIMPLE>
+__device__ __forceinline__ void turn_row(uint2& a, uint2& b, bool normed, float eps, bool turned, bool adjacent,
+                                         const LaneTurn& t) {
+  uint64_t x[4];
+  const uint32_t v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[i], x[i], ss);
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+  float r = 1.f;
+  if (normed) {
+    uint64_t s2 = mul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s2 = fma2(x[i], x[i], s2);
+    float s0, s1;
+    unpair(s2, s0, s1);
+    float ss = __fadd_rn(s0, s1);
 #pragma unroll
     for (int off = 1; off < RowLanes<D>::kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float r = __frsqrt_rn(__fmaf_rn(ss, 1.f / D, eps));
-    if (normed) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
-    }
+    r = rsqrtf(__fmaf_rn(ss, 1.f / D, eps));
   }
-  auto turn = [&](float& p, float& q, int i) {
-    const float x0 = p, x1 = q;
-    p = __fmaf_rn(x0, cs[i], -__fmul_rn(x1, sn[i]));
-    q = __fmaf_rn(x1, cs[i], __fmul_rn(x0, sn[i]));
-  };
-  if (turned) {
-    if (adjacent) {
+  uint64_t y[4];
+  if (!SIMPLE && !turned) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], i);
-    } else {
+    for (int i = 0; i < 4; ++i) y[i] = mul2(x[i], t.own[i]);
+  } else if (!SIMPLE && adjacent) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) turn(x[i], x[i + 4], i);
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpair(x[i], lo, hi);
+      y[i] = fma2(x[i], t.own[i], mul2(pair(hi, lo), t.other[i]));
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], t.own[i], mul2(x[i ^ 2], t.other[i]));
   }
-  a = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  b = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  if (normed) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], pair(r, r));
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpair(y[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  a = make_uint2(w[0], w[1]);
+  b = make_uint2(w[2], w[3]);
 }
 
 // The last b in [0, n) with key(b) <= x, for keys that do not fall; 0 when there is none. Asked
