@@ -11,6 +11,8 @@
 // one scale per block, which needs the largest of the block's new values before the first code
 // is written: there CTAs take (touched block, plane, a few KV heads), hold the rows in
 // registers between the two uses and share the block's angles through shared memory.
+#include <limits.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +27,7 @@ namespace {
 
 constexpr int kPlain = 0;  // FMT of the kernel without the write
 
-constexpr int kRing = 8;        // slots (a warp's rows at once) in flight
+constexpr int kRing = 4;        // slots (a warp's rows at once) in flight
 constexpr int kSlotBytes = 512;
 constexpr int kBlockHold = 8;   // row batches a lane of the block path keeps in registers
 constexpr int kTableBytes = 36 << 10;  // of the 48 KB that a launch may have unasked
@@ -37,8 +39,11 @@ constexpr int kWarps = FMT == kFmtE4m3 ? 8 : 4;
 struct TokenPlace {
   int seq, index;    // its sequence, and which of that one's new rows it is
   int count;         // new rows of the sequence
+  int len;           // rows it held before
   bool in_sequence;  // false: a row of no sequence
 };
+
+constexpr int kPlaceRounds = 4;  // up to 32 * 4 sequences are looked through at once
 
 __device__ __forceinline__ TokenPlace place_of(const RotateParams& p, int t) {
   TokenPlace at;
@@ -46,14 +51,47 @@ __device__ __forceinline__ TokenPlace place_of(const RotateParams& p, int t) {
     at.seq = t / p.tokens_per_seq;
     at.index = t - at.seq * p.tokens_per_seq;
     at.count = p.tokens_per_seq;
+    at.len = p.seq_lens[at.seq];
     at.in_sequence = true;
+    return at;
+  }
+  int start, end;
+  if (p.num_seqs <= 32 * kPlaceRounds) {
+    // every start and length in one trip to memory, instead of one after the other
+    const int lane = threadIdx.x & 31;
+    int starts[kPlaceRounds], lens[kPlaceRounds];
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) {
+      const int b = i * 32 + lane;
+      starts[i] = b < p.num_seqs ? p.query_starts[b] : INT_MAX;
+      lens[i] = b < p.num_seqs ? p.seq_lens[b] : 0;
+    }
+    const int last = p.query_starts[p.num_seqs];
+    int count = 0;  // sequences that begin at or before t
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) count += __popc(__ballot_sync(0xffffffffu, starts[i] <= t));
+    at.seq = max(count - 1, 0);
+    start = end = at.len = 0;
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) {
+      const int s = __shfl_sync(0xffffffffu, starts[i], at.seq & 31), l = __shfl_sync(0xffffffffu, lens[i], at.seq & 31);
+      const int e = __shfl_sync(0xffffffffu, starts[i], (at.seq + 1) & 31);
+      if (i == at.seq / 32) {
+        start = s;
+        at.len = l;
+      }
+      if (i == (at.seq + 1) / 32) end = e;
+    }
+    if (at.seq + 1 == p.num_seqs) end = last;
   } else {
     at.seq = find_last(p.num_seqs, t, [&](int b) { return p.query_starts[b]; });
-    const int start = p.query_starts[at.seq], end = p.query_starts[at.seq + 1];
-    at.index = t - start;
-    at.count = end - start;
-    at.in_sequence = start >= 0 && t >= start && t < end && end <= p.tokens;
+    start = p.query_starts[at.seq];
+    end = p.query_starts[at.seq + 1];
+    at.len = p.seq_lens[at.seq];
   }
+  at.index = t - start;
+  at.count = end - start;
+  at.in_sequence = start >= 0 && t >= start && t < end && end <= p.tokens;
   return at;
 }
 
@@ -96,9 +134,10 @@ __device__ __forceinline__ void lane_angles(const RotateParams& p, const RotateT
 }
 
 // One warp: share g of token t's rows. With pages, D and DV are theirs.
-template <int D, int DV, int FMT, bool SIMPLE>
+// prepare(): called once the first rows are asked for.
+template <int D, int DV, int FMT, bool SIMPLE, typename Prepare>
 __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTables<D>& tab, int t, int g,
-                                           unsigned char* ring_smem, __nv_bfloat16* stage) {
+                                           unsigned char* ring_smem, __nv_bfloat16* stage, const Prepare& prepare) {
   using L = RowLanes<D>;
   const int lane = threadIdx.x & 31;
   const int sub = lane / L::kLanes, u = lane % L::kLanes;
@@ -123,7 +162,11 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
   long long ask_step = (g < q_slots ? p.q.head : p.k.head) * (G * L::kRows);
   int ask_left = (g < q_slots ? HQ : q_slots * L::kRows + HK) - (g * L::kRows + sub);
   auto ask = [&](uint32_t place) {
-    const bool there = used && ask_left > 0 && ask_s < slots;
+    if (ask_s >= slots) {
+      cp_async_commit();
+      return;
+    }
+    const bool there = used && ask_left > 0;
     cp_async_16_or_zeros(ring + place, there ? ask_at : p.q.data, there);
     cp_async_commit();
     const bool was_query = ask_s < q_slots;
@@ -138,6 +181,7 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
   };
 #pragma unroll 1
   for (int i = 0; i < kRing; ++i) ask(i * kSlotBytes);
+  prepare();
 
   // where the keys go
   TokenPlace at{};
@@ -148,7 +192,7 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
       cp_async_wait<0>();
       return;
     }
-    const int len = p.seq_lens[at.seq];
+    const int len = at.len;
     cache_place = static_cast<int>(static_cast<unsigned>(len) + static_cast<unsigned>(at.index));
     if (FMT != kFmtE4m3) {
       const long long end = static_cast<long long>(len) + at.count;
@@ -427,7 +471,7 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
 }
 
 template <int D, int DV, int FMT, bool SIMPLE>
-__global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 8) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 6) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ RotateTables<D> tab;
   __shared__ uint32_t red[kWarps<FMT>];
@@ -447,16 +491,22 @@ __global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 8) pkv
       return;
     }
   }
-  fill_tables(tab, p);
-  __syncthreads();
   const int warp = threadIdx.x >> 5;
+  bool ready = false;
+  auto prepare = [&] {  // the tables, beside the first rows' way here
+    if (ready) return;
+    fill_tables(tab, p);
+    __syncthreads();
+    ready = true;
+  };
   unsigned char* mine = smem + warp * kRing * kSlotBytes;  // a staged row of the affine write takes the ring's place
   const long long units = static_cast<long long>(p.tokens) * p.groups, step = static_cast<long long>(p.q_ctas) * kWarps<FMT>;
   for (long long unit = static_cast<long long>(blockIdx.x) * kWarps<FMT> + warp; unit < units; unit += step) {
     const int t = p.groups == 1 ? static_cast<int>(unit) : static_cast<int>(unit / p.groups);
     const int g = static_cast<int>(unit - static_cast<long long>(t) * p.groups);
-    token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, reinterpret_cast<__nv_bfloat16*>(mine));
+    token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, reinterpret_cast<__nv_bfloat16*>(mine), prepare);
   }
+  prepare();  // a warp without a token
 }
 
 // Warps per token: as many as fill the GPU.
@@ -475,7 +525,7 @@ cudaError_t launch_of(RotateParams p, int sm_count, cudaStream_t stream) {
   const int slots = (p.num_q_heads + L::kRows - 1) / L::kRows + (kKeysHere ? (p.num_kv_heads + L::kRows - 1) / L::kRows : 0);
   p.groups = token_groups(p.tokens, slots, sm_count);
   // One wave of CTAs, each of which fills its tables once and takes many tokens.
-  const long long most_ctas = (FMT == kFmtE4m3 ? 3ll : 8ll) * sm_count;
+  const long long most_ctas = (FMT == kFmtE4m3 ? 3ll : 6ll) * sm_count;
   long long ctas = (static_cast<long long>(p.tokens) * p.groups + kWarps<FMT> - 1) / kWarps<FMT>;
   ctas = std::min(ctas, most_ctas);
   p.q_ctas = static_cast<int>(ctas);
