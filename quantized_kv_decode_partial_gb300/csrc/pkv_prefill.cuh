@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * KS + 2 * VS + 2 * RS + 8];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, bad_blocks;
+  __shared__ int abort_flag;
   __shared__ uint32_t piece_bits[VS];
   __shared__ uint32_t unit_bits[RS];  // pages of codes: a quarter tile's pieces, and their scales (e4m3)
   __shared__ float unit_scales[RS][4];
@@ -320,25 +320,12 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     }
     fence_barrier_init();
     abort_flag = 0;
-    bad_blocks = 0;
   }
   if (warp == 8) tmem_alloc(smem_addr(&tmem_slot), kPrefillStates);
-  __syncthreads();
-  // Are all blocks of this CTA's keys in the pool? Almost always; then no tile asks again.
-  {
-    const int b0 = max(lo, t0 * KT) / p.block_size, b1 = (min(hi, (t0 + nt) * KT) - 1) / p.block_size;
-    for (int i = b0 + static_cast<int>(threadIdx.x); i <= b1; i += blockDim.x) {
-      if (static_cast<unsigned>(u.table[i]) >= static_cast<unsigned>(p.num_blocks)) {
-        bad_blocks = 1;
-        if (p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
-      }
-    }
-  }
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  const bool any_bad = bad_blocks != 0;
   const int piece = 1 << p.piece_log2, pieces = KT >> p.piece_log2;
   const int items = nt * tiles_q;  // item i: query tile i % tiles_q, key tile t0 + i / tiles_q, score tile i & 1
   // The pieces of key tile t that are copied, and (lane l) the row of piece l in the pool or among the values.
@@ -390,7 +377,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       int next_row = 0;
       uint32_t next_bits = 0;
       if (j + 1 < nt) next_bits = tile_pieces(t0 + j + 1, next_row);  // before the wait: its table words take a while
-      if (j >= stages && !mbar_wait_warp(empty0 + 8 * s, (j / stages - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns))
+      if (j >= stages && !mbar_wait_close(empty0 + 8 * s, (j / stages - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns))
         break;
       if (lane == 0) {
         if (!is_k) piece_bits[s] = bits;
@@ -415,9 +402,9 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     }
     // Every copy lands before the CTA ends, whatever the other warps did.
     int none = 0;
-    if (is_k) mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+    if (is_k) mbar_wait_close(q_full, 0, &none, p.error_flag, kWaitLimitNs);
     for (int i = max(0, asked - stages); i < asked; ++i)
-      mbar_wait_warp(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
+      mbar_wait_close(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
   } else if (T::kCodes && warp >= 9) {
     // ------------------------------------------------------------------ pages of codes, to bf16 tiles
     // Quarter tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is quarter n & 3 of plane tile n / 4. Warp 9
@@ -459,7 +446,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           const int plane_bytes = FMT == kFmtE4m3 ? 0 : piece * groups * 2;
           for (int h = 0; h < 4; ++h) {
             const int n = 4 * x + h, s = n % RS, first = h * per;
-            if (n >= RS) ok = mbar_wait_warp(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+            if (n >= RS) ok = mbar_wait_close(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
             if (!ok) break;
             const uint32_t mine = bits >> first & ((1u << per) - 1u);
             const bool copies = lane >= first && lane < first + per;
@@ -498,9 +485,9 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           bits = next_bits;
         }
         int none = 0;  // every copy lands before the CTA ends
-        mbar_wait_warp(q_full, 0, &none, p.error_flag, kWaitLimitNs);
+        mbar_wait_close(q_full, 0, &none, p.error_flag, kWaitLimitNs);
         for (int n = max(0, asked - RS); n < asked; ++n)
-          mbar_wait_warp(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
+          mbar_wait_close(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
       } else {
         const int group = (warp - 10) >> 1, part = (warp - 10) & 1;
         for (int n = group; n < 8 * nt; n += 3) {
@@ -508,10 +495,10 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           int j;
           plane_tile(n >> 2, is_k, j);
           const int s = n % RS, stage = is_k ? j % KS : j % VS, round = is_k ? j / KS : j / VS;
-          if (round > 0 && !mbar_wait_warp(is_k ? k_empty(stage) : v_empty(stage), (round - 1) & 1, &abort_flag, p.error_flag,
+          if (round > 0 && !mbar_wait_close(is_k ? k_empty(stage) : v_empty(stage), (round - 1) & 1, &abort_flag, p.error_flag,
                                            p.wait_limit_ns))
             break;
-          if (!mbar_wait_warp(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
+          if (!mbar_wait_close(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
           const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = from + T::kRawCodes;
           const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;
           if (is_k) {
@@ -535,7 +522,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     fewer_registers<T::kCodes>();
     const uint32_t leader = elect_lane(), base = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t instr_s = umma_instr(KT, false, p.negate != 0), instr_o = umma_instr(DV, true, false);
-    bool ok = mbar_wait_warp(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
+    bool ok = mbar_wait_close(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
     // Item i's query tile and key tile are counted along; a stage's index and parity follow its ring.
     struct Place {
       int q, tile, stage, parity;
@@ -551,7 +538,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     };
     auto scores = [&](int slot) {
       const int s = sp.stage;
-      if (sp.q == 0) ok = mbar_wait_warp(k_full(s), sp.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (sp.q == 0) ok = mbar_wait_close(k_full(s), sp.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) return;
       tmem_fence_after_sync();
       const uint64_t a0 = umma_desc(smem + sp.q * T::kQBytes, 0), b0 = umma_desc(smem_k + s * T::kKBytes, 0);
@@ -568,11 +555,11 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     for (int i = 0; ok && i < items; ++i) {
       const int s = op.stage, slot = i & 1;
       if (op.q == 0) {
-        ok = mbar_wait_warp(v_full(s), op.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
+        ok = mbar_wait_close(v_full(s), op.parity, &abort_flag, p.error_flag, p.wait_limit_ns);
         // Rows that nobody sees have weight zero, which must meet zeros, whatever is there.
         const int key = (t0 + op.tile) * KT;
-        if (!T::kCodes && ok && (key < lo || key + KT > hi || any_bad)) {
-          const uint32_t bits = piece_bits[s];
+        const uint32_t bits = piece_bits[s];
+        if (!T::kCodes && ok && (key < lo || key + KT > hi || bits != (1u << pieces) - 1u)) {
           for (int r = lane; r < KT; r += 32) {
             if (key + r >= lo && key + r < hi && (bits >> (r >> p.piece_log2) & 1)) continue;
             for (int c = 0; c < DV / 64; ++c)
@@ -586,7 +573,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           __syncwarp();
         }
       }
-      ok = ok && mbar_wait_warp(p_full(slot), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      ok = ok && mbar_wait_close(p_full(slot), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) break;
       tmem_fence_after_sync();
       const uint64_t b0 = umma_desc(smem_v + s * T::kVBytes, KT * 128);
@@ -613,11 +600,20 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     float m = -INFINITY;          // running maximum of the unscaled scores
     uint64_t l[2] = {0ull, 0ull};  // sums of weights, two pairs
     const uint32_t o_at = tmem + lanes + T::kTmemO + q * DV;
+    // Are all blocks of this CTA's keys in the pool? Almost always; then no tile asks again.
+    bool any_bad = false;
+    {
+      const int b0 = max(lo, t0 * KT) / p.block_size, b1 = (min(hi, (t0 + nt) * KT) - 1) / p.block_size;
+      for (int i = b0 + r; i <= b1; i += 128)
+        if (static_cast<unsigned>(u.table[i]) >= static_cast<unsigned>(p.num_blocks)) any_bad = true;
+      if (any_bad && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+      any_bad = group_barrier_any(1 + q, 128, any_bad);
+    }
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
       const int i = j * tiles_q + q;
       const int key = (t0 + j) * KT;
-      ok = mbar_wait_warp(s_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      ok = mbar_wait_close(s_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) break;
       tmem_fence_after_sync();
       const uint32_t s_at = tmem + lanes + (i & 1) * KT;
@@ -654,7 +650,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         m = up;
 #pragma unroll
         for (int n = 0; n < 2; ++n) l[n] = mul2(l[n], pair(by, by));
-        ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+        ok = mbar_wait_close(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
         if (!ok) break;
         tmem_fence_after_sync();
 #pragma unroll 1
@@ -673,13 +669,13 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       tmem_wait_st();
       // Every phase of o_done is over before the next one's product can be issued, so that a parity
       // stands for one phase. With two query tiles this tile's scores came after that product.
-      if (j > 0 && tiles_q == 1) ok = mbar_wait_warp(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+      if (j > 0 && tiles_q == 1) ok = mbar_wait_close(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
       if (!ok) break;
       tmem_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(i & 1));
     }
-    if (ok) ok = mbar_wait_warp(o_done(q), (nt - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
+    if (ok) ok = mbar_wait_close(o_done(q), (nt - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
     if (ok) {
       tmem_fence_after_sync();
       const bool split = p.splits > 1;
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     if (abort_flag) {  // a wait gave up: products may still run, and tensor memory is theirs until they are done
       int none = 0;
       umma_commit(elect_lane(), drained);  // the lane that issued the products
-      mbar_wait_warp(drained, 0, &none, p.error_flag, kWaitLimitNs);
+      mbar_wait_close(drained, 0, &none, p.error_flag, kWaitLimitNs);
     }
     tmem_free(tmem, kPrefillStates);
   }

@@ -72,6 +72,32 @@ __device__ __forceinline__ void tmem_st_16(uint32_t addr, const uint32_t (&v)[16
       : "memory");
 }
 
+// mbar_wait_warp for waits that a chain of products hangs on: the clock and the abort flag are looked at only every
+// 32 polls, so that a phase that completes is seen at once.
+__device__ __forceinline__ bool mbar_wait_close(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* error_flag,
+                                                unsigned long long limit_ns) {
+  if (limit_ns < kShortWaitLimitNs) return mbar_wait_warp(bar, parity, abort_flag, error_flag, limit_ns);
+  unsigned long long start = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    int stop = 0;
+    if ((threadIdx.x & 31) == 0) {
+      const unsigned long long now = global_timer_ns();
+      if (start == 0) start = now;
+      if (*abort_flag) {
+        stop = 1;
+      } else if (now - start > limit_ns) {
+        *abort_flag = 1;
+        if (error_flag) atomicOr(error_flag, kDevErrTimeout);
+        stop = 1;
+      }
+    }
+    if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+  }
+}
+
 // ---- matrix products
 
 // Shared-memory operand in 128-byte rows with the 128-byte swizzle, tiles 1024-byte aligned.
