@@ -1,8 +1,8 @@
 // Values of the cached rows that a prompt attention call sees, as bf16, from pages of codes: written once, where
 // several query tiles would otherwise turn the same codes each for itself.
 //
-// One CTA per (128 rows, KV head): 16 codes a thread at a time, every load ahead of the first conversion. Bound by HBM:
-// it reads the codes and writes twice (8-bit) or four times (4-bit) their bytes.
+// One CTA per (32 rows, KV head, plane): 16 codes a thread at a time, every load ahead of the first conversion. Bound by
+// HBM: it reads the codes and writes twice (8-bit) or four times (4-bit) their bytes.
 #include "pkv_codes.cuh"
 #include "pkv_launch.h"
 #include "pkv_rotate.cuh"
@@ -11,15 +11,18 @@ namespace pkv {
 
 namespace {
 
+constexpr int kRows = 32;
+constexpr int kThreads = 128;
+
 template <int D, int FMT>
 __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int plane, const int32_t* table, int first_row,
-                                             int len, int head, size_t block) {
-  constexpr int kPerRow = D / 16, kRounds = kValueRows * kPerRow / 256;
+                                             int len, __nv_bfloat16* out, int head) {
+  constexpr int kPerRow = D / 16, kRounds = kRows * kPerRow / kThreads;
   uint4 v[kRounds];
   float scale[kRounds], bias[kRounds];
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int c = i * 256 + threadIdx.x, r = c / kPerRow, col = c % kPerRow, t = first_row + r;
+    const int c = i * kThreads + threadIdx.x, r = c / kPerRow, col = c % kPerRow, t = first_row + r;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
     scale[i] = bias[i] = 0.f;
     if (t >= len) continue;
@@ -42,10 +45,9 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
       bias[i] = __bfloat162float(p.planes[plane].biases[row * (D / 64) + col / 4]);
     }
   }
-  __nv_bfloat16* out = p.out[plane] + (block * p.num_kv_heads + head) * kValueRows * D;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int c = i * 256 + threadIdx.x, r = c / kPerRow;
+    const int c = i * kThreads + threadIdx.x, r = c / kPerRow;
     if (first_row + r >= len) continue;  // nobody's rows are left as they are
     uint32_t w[8];
     codes_to_bf16<FMT>(v[i], scale[i], bias[i], w);
@@ -56,9 +58,10 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
 }
 
 template <int D, int DV, int FMT>
-__global__ void __launch_bounds__(256) pkv_prefill_values_kernel(const __grid_constant__ PrefillValuesParams p) {
+__global__ void __launch_bounds__(kThreads) pkv_prefill_values_kernel(const __grid_constant__ PrefillValuesParams p) {
   wait_for_prerequisite_grids();
-  const int block = blockIdx.x, head = blockIdx.y;
+  constexpr int kPer = kValueRows / kRows;
+  const int block = blockIdx.x / kPer, head = blockIdx.y, plane = blockIdx.z, row0 = blockIdx.x % kPer * kRows;
   const int b = find_last(p.num_seqs, block, [&](int i) { return p.values.base(i, p.query_starts[i]); });
   const int start = p.query_starts[b], len = p.seq_lens[b];
   const long long n = static_cast<long long>(p.query_starts[b + 1]) - start;
@@ -66,18 +69,22 @@ __global__ void __launch_bounds__(256) pkv_prefill_values_kernel(const __grid_co
   if (start < 0 || n <= 0 || start + n > p.tokens || len < n || len > static_cast<long long>(p.max_blocks) * p.block_size)
     return;
   const long long row = static_cast<long long>(block - p.values.base(b, start)) * kValueRows +
-                        p.values.first_row(len, static_cast<int>(n), p.window);
+                        p.values.first_row(len, static_cast<int>(n), p.window) + row0;
   if (block < p.values.base(b, start) || row >= len) return;
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
-  plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, head, block);
-  plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, head, block);
+  const size_t to = (static_cast<size_t>(block) * p.num_kv_heads + head) * kValueRows + row0;
+  if (plane == 0) {
+    plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, p.out[0] + to * D, head);
+  } else {
+    plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, p.out[1] + to * DV, head);
+  }
 }
 
 template <int D, int DV, int FMT>
 cudaError_t launch_of(const PrefillValuesParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.blocks, p.num_kv_heads);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(p.blocks * (kValueRows / kRows), p.num_kv_heads, 2);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory

@@ -11,8 +11,6 @@
 // one scale per block, which needs the largest of the block's new values before the first code
 // is written: there CTAs take (touched block, plane, a few KV heads), hold the rows in
 // registers between the two uses and share the block's angles through shared memory.
-#include <limits.h>
-
 #include <algorithm>
 #include <type_traits>
 
@@ -45,6 +43,36 @@ struct TokenPlace {
 
 constexpr int kPlaceRounds = 4;  // up to 32 * 4 sequences are looked through at once
 
+// Starts and lengths of that many sequences, spread over a warp: one trip to memory instead of one after the other.
+struct StartsAndLengths {
+  int starts[kPlaceRounds], lens[kPlaceRounds], last;
+  __device__ __forceinline__ explicit StartsAndLengths(const RotateParams& p) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) {
+      const int b = i * 32 + lane;
+      starts[i] = b < p.num_seqs ? p.query_starts[b] : 0;
+      lens[i] = b < p.num_seqs ? p.seq_lens[b] : 0;
+    }
+    last = p.query_starts[p.num_seqs];
+  }
+  // Of sequence b: where it begins and ends, and its length.
+  __device__ __forceinline__ void of(const RotateParams& p, int b, int& start, int& end, int& len) const {
+    start = len = end = 0;
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) {
+      const int s = __shfl_sync(0xffffffffu, starts[i], b & 31), l = __shfl_sync(0xffffffffu, lens[i], b & 31);
+      const int e = __shfl_sync(0xffffffffu, starts[i], (b + 1) & 31);
+      if (i == b / 32) {
+        start = s;
+        len = l;
+      }
+      if (i == (b + 1) / 32) end = e;
+    }
+    if (b + 1 == p.num_seqs) end = last;
+  }
+};
+
 __device__ __forceinline__ TokenPlace place_of(const RotateParams& p, int t) {
   TokenPlace at;
   if (p.tokens_per_seq > 0) {
@@ -57,32 +85,13 @@ __device__ __forceinline__ TokenPlace place_of(const RotateParams& p, int t) {
   }
   int start, end;
   if (p.num_seqs <= 32 * kPlaceRounds) {
-    // every start and length in one trip to memory, instead of one after the other
-    const int lane = threadIdx.x & 31;
-    int starts[kPlaceRounds], lens[kPlaceRounds];
-#pragma unroll
-    for (int i = 0; i < kPlaceRounds; ++i) {
-      const int b = i * 32 + lane;
-      starts[i] = b < p.num_seqs ? p.query_starts[b] : INT_MAX;
-      lens[i] = b < p.num_seqs ? p.seq_lens[b] : 0;
-    }
-    const int last = p.query_starts[p.num_seqs];
+    const StartsAndLengths all(p);
     int count = 0;  // sequences that begin at or before t
 #pragma unroll
-    for (int i = 0; i < kPlaceRounds; ++i) count += __popc(__ballot_sync(0xffffffffu, starts[i] <= t));
+    for (int i = 0; i < kPlaceRounds; ++i)
+      count += __popc(__ballot_sync(0xffffffffu, i * 32 + (threadIdx.x & 31) < p.num_seqs && all.starts[i] <= t));
     at.seq = max(count - 1, 0);
-    start = end = at.len = 0;
-#pragma unroll
-    for (int i = 0; i < kPlaceRounds; ++i) {
-      const int s = __shfl_sync(0xffffffffu, starts[i], at.seq & 31), l = __shfl_sync(0xffffffffu, lens[i], at.seq & 31);
-      const int e = __shfl_sync(0xffffffffu, starts[i], (at.seq + 1) & 31);
-      if (i == at.seq / 32) {
-        start = s;
-        at.len = l;
-      }
-      if (i == (at.seq + 1) / 32) end = e;
-    }
-    if (at.seq + 1 == p.num_seqs) end = last;
+    all.of(p, at.seq, start, end, at.len);
   } else {
     at.seq = find_last(p.num_seqs, t, [&](int b) { return p.query_starts[b]; });
     start = p.query_starts[at.seq];
@@ -313,10 +322,28 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
   const int bs = p.block_size;
   // Sequence b's blocks have the slots from floor(start_b / bs) + 2 b on: n rows touch at most
   // floor(n / bs) + 2 blocks, which is what its share holds.
-  auto start_of = [&](int b) { return p.tokens_per_seq > 0 ? b * p.tokens_per_seq : p.query_starts[b]; };
-  const int seq = find_last(p.num_seqs, slot, [&](int b) { return static_cast<long long>(start_of(b) / bs) + 2ll * b; });
-  const int start = start_of(seq);
-  const int n = p.tokens_per_seq > 0 ? p.tokens_per_seq : p.query_starts[seq + 1] - start;
+  TablesAhead<D> ahead;
+  if constexpr (TURN) ahead.load(p);  // on their way while the block is found
+  int seq, start, n, len;
+  if (p.tokens_per_seq > 0 || p.num_seqs > 32 * kPlaceRounds) {
+    auto start_of = [&](int b) { return p.tokens_per_seq > 0 ? b * p.tokens_per_seq : p.query_starts[b]; };
+    seq = find_last(p.num_seqs, slot, [&](int b) { return static_cast<long long>(start_of(b) / bs) + 2ll * b; });
+    start = start_of(seq);
+    n = p.tokens_per_seq > 0 ? p.tokens_per_seq : p.query_starts[seq + 1] - start;
+    len = p.seq_lens[seq];
+  } else {
+    const StartsAndLengths all(p);
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kPlaceRounds; ++i) {
+      const int b = i * 32 + lane;
+      count += __popc(__ballot_sync(0xffffffffu, b < p.num_seqs && static_cast<long long>(all.starts[i] / bs) + 2ll * b <= slot));
+    }
+    seq = max(count - 1, 0);
+    int end;
+    all.of(p, seq, start, end, len);
+    n = end - start;
+  }
   const long long t = slot - (static_cast<long long>(start / bs) + 2ll * seq);
   if (start < 0 || n <= 0 || t < 0 || static_cast<long long>(start) + n > p.tokens) {
     // starts that fall or leave the tokens: nothing is written
@@ -324,7 +351,6 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
       atomicOr(p.error_flag, kDevErrBadSeqLen);
     return;
   }
-  const int len = p.seq_lens[seq];
   const long long end = static_cast<long long>(len) + n;
   if (len < 0 || end > static_cast<long long>(p.max_blocks) * bs) {
     if (threadIdx.x == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadSeqLen);
@@ -337,10 +363,6 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
   const int r1 = static_cast<int>(min(end - first, static_cast<long long>(bs)));
   const int j0 = static_cast<int>(first + r0 - len);  // which of the sequence's new rows that is
   const int phys = p.block_tables[static_cast<size_t>(seq) * p.max_blocks + blk];
-  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-    if (threadIdx.x == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
-    return;
-  }
 
   const int sub = lane / L::kLanes, u = lane % L::kLanes;
   const bool used = u < L::kUsed;
@@ -368,10 +390,17 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
       b[k] = ld_nc_keep_v2(row + off1);
     }
   }
+  // the rows are in flight while the table's answer arrives
+  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+    if (threadIdx.x == 0 && p.error_flag) atomicOr(p.error_flag, kDevErrBadBlock);
+    return;
+  }
+  const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + h;
+  const float old = live && r0 > 0 ? p.block_scales[kPlane][cell] : 0.f;
   float w[8];
   const int tabled = min(p.table_rows, r1 - r0), half = p.turn.rot / 2;
   if constexpr (TURN) {
-    fill_tables(tab, p);
+    ahead.store(tab, p);
     __syncthreads();
     lane_weights(tab, true, used, off0, off1, w);
     for (int i = threadIdx.x; i < tabled * half; i += blockDim.x) {
@@ -426,8 +455,6 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
   };
   later([&](const uint2& x, const uint2& y, int) { m = max_abs(m, make_uint4(x.x, x.y, y.x, y.y)); });
   m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-  const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + h;
-  const float old = live && r0 > 0 ? p.block_scales[kPlane][cell] : 0.f;
   if (lane == 0) red[warp] = m;
   __syncthreads();  // (and every warp has read the old scale)
   for (int i = 0; i < per_head; ++i) m = max(m, red[warp / per_head * per_head + i]);
@@ -493,9 +520,11 @@ __global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 6) pkv
   }
   const int warp = threadIdx.x >> 5;
   bool ready = false;
+  TablesAhead<D> ahead;
+  ahead.load(p);
   auto prepare = [&] {  // the tables, beside the first rows' way here
     if (ready) return;
-    fill_tables(tab, p);
+    ahead.store(tab, p);
     __syncthreads();
     ready = true;
   };

@@ -85,23 +85,38 @@ struct __align__(16) RotateTables {
   uint8_t axis[D / 2];
 };
 
-// Filled by the whole block; the caller synchronises.
+// Filled by the whole block of at least 128 threads, which then synchronises: the words are asked for first and
+// used when something else has had its time.
 template <int D>
-__device__ __forceinline__ void fill_tables(RotateTables<D>& tab, const RotateParams& p) {
-  for (int i = threadIdx.x; i < p.turn.rot / 2; i += blockDim.x) {
-    tab.step[i] = turn_step(p.inv_freq[i]);
-    tab.axis[i] = static_cast<uint8_t>(axis_of(p.turn, i));
+struct TablesAhead {
+  static constexpr int kWeights = 2 * D / 128;  // of a thread, at most
+  float freq, weight[kWeights];
+  __device__ __forceinline__ void load(const RotateParams& p) {
+    const int t = threadIdx.x;
+    freq = t < p.turn.rot / 2 ? p.inv_freq[t] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) {
+      const int i = t + k * blockDim.x;
+      const void* w = i < D ? p.q_weight : p.k_weight;
+      const int d = i < D ? i : i - D;
+      weight[k] = 0.f;
+      if (i < 2 * D && w)
+        weight[k] = p.weight_f32 ? static_cast<const float*>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d]);
+    }
   }
-  for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
-    const void* w = i < D ? p.q_weight : p.k_weight;
-    const int d = i < D ? i : i - D;
-    float x = 1.f;
-    if (w)
-      x = __fadd_rn(p.weight_f32 ? static_cast<const float*>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d]),
-                    p.weight_offset);
-    (&tab.weight[0][0])[i] = x;
+  __device__ __forceinline__ void store(RotateTables<D>& tab, const RotateParams& p) const {
+    const int t = threadIdx.x;
+    if (t < p.turn.rot / 2) {
+      tab.step[t] = turn_step(freq);
+      tab.axis[t] = static_cast<uint8_t>(axis_of(p.turn, t));
+    }
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) {
+      const int i = t + k * blockDim.x;
+      if (i < 2 * D) (&tab.weight[0][0])[i] = (i < D ? p.q_weight : p.k_weight) ? __fadd_rn(weight[k], p.weight_offset) : 1.f;
+    }
   }
-}
+};
 
 // What a lane's eight values are multiplied by: value v of a pair becomes r * (v * own + partner * other), r
 // the row's norm. own and other hold the norm weight times cos and sin, so a token's heads share them.
