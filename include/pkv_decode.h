@@ -603,12 +603,16 @@ typedef struct pkv_prefill_params {
   int32_t splits;             /* CTAs that share the keys of one tile of queries: 0 = chosen from the
                                  tokens, the table's width and the SM count, 1 .. 64 */
   int32_t reading;            /* how pages of codes are read (bf16 pages: ignored):
-                                 PKV_READING_AUTO (0): as below where sequences have more tokens than one
-                                 CTA on average and the values take no more than 8 GB, else directly;
-                                 PKV_READING_DIRECT (1): every CTA turns the codes it needs into bf16;
-                                 PKV_READING_VALUES (2): a pass before the attention writes the bf16
-                                 values of all rows that any query sees to the workspace. Both
-                                 round each value to bf16 once */
+                                 PKV_READING_VALUES (2): a pass before the attention writes 16-bit
+                                 values of all rows that any query sees to the workspace, bf16 of
+                                 e4m3 pages, fp16 of affine ones (with a power of two for each
+                                 (sequence, KV head) and plane; values below 2^-39 of the
+                                 largest are lost, as are parts of a query row);
+                                 PKV_READING_DIRECT (1): e4m3 pages alone: every CTA turns the codes it
+                                 needs into bf16;
+                                 PKV_READING_AUTO (0): direct for e4m3 pages where sequences have
+                                 fewer tokens than one CTA on average or the values would take more
+                                 than 8 GB, else values */
 } pkv_prefill_params;
 
 #define PKV_READING_AUTO 0
@@ -621,7 +625,7 @@ typedef struct pkv_prefill_plan {
   int32_t units;          /* CTAs per KV head and split, those of short last tiles included */
   int32_t splits;
   int32_t smem_bytes;     /* dynamic shared memory of a CTA */
-  int32_t value_blocks;   /* blocks of 128 rows of bf16 values in the workspace (0: pages are read directly) */
+  int32_t value_blocks;   /* blocks of 128 rows of values in the workspace (0: pages are read directly) */
   size_t workspace_bytes; /* f32 states of split key ranges (none with splits = 1), and the values */
 } pkv_prefill_plan;
 

@@ -29,8 +29,7 @@ SOURCES = [
     "pkv_rotate.cu",
     "pkv_prefill_bf16.cu",
     "pkv_prefill_values.cu",
-    "pkv_prefill_u4.cu",
-    "pkv_prefill_u8.cu",
+    "pkv_prefill_f16.cu",
     "pkv_prefill_e4m3.cu",
     "pkv_sparse.cu",
     "pkv_partial_bf16.cu",

@@ -1265,13 +1265,14 @@ int pkv_norm_rotate_append(const pkv_pool_layout* layout, const pkv_rotation* ro
 // ---------------------------------------------------------------------------
 namespace {
 
-pkv::PrefillInfo prefill_info(const pkv_pool_layout* L) {
+// values: the kernel over values written beforehand.
+pkv::PrefillInfo prefill_info(const pkv_pool_layout* L, bool values) {
   const int dk = L->head_dim, dv = v_dim(L);
   switch (format_of(L)) {
     case 16: return pkv::prefill_info_bf16(dk, dv);
-    case 4: return pkv::prefill_info_u4(dk, dv);
-    case 8: return pkv::prefill_info_u8(dk, dv);
-    case pkv::kFmtE4m3: return pkv::prefill_info_e4m3(dk, dv);
+    case 4:
+    case 8: return values ? pkv::prefill_info_f16(dk, dv) : pkv::PrefillInfo{};
+    case pkv::kFmtE4m3: return values ? pkv::prefill_info_bf16(dk, dv) : pkv::prefill_info_e4m3(dk, dv);
     default: return pkv::PrefillInfo{};
   }
 }
@@ -1287,7 +1288,8 @@ int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
   if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   if (static_cast<long long>(P->num_tokens) * P->num_q_heads >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   if (P->num_q_heads / L->num_kv_heads > 64) return PKV_ERR_UNSUPPORTED_SHAPE;
-  if (!prefill_info(L).exists) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (!prefill_info(L, L->bits != 16).exists) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (P->reading == PKV_READING_DIRECT && L->bits != 16 && !block_scaled(L)) return PKV_ERR_UNSUPPORTED_SHAPE;
   return PKV_OK;
 }
 
@@ -1332,9 +1334,16 @@ pkv::PrefillValues prefill_values(const pkv_pool_layout* L, const pkv_prefill_pa
   return v;
 }
 
-// The values pay for themselves from the second CTA on that reads the same keys: turning a tile of 128 keys of 8-bit
-// codes costs a CTA about 1.5 us, writing and reading it as bf16 as much as 15 ns of the GPU's bandwidth. (Batch of
-// 16 chunks of 1 to 512 tokens over e4m3 pages: 1229 us directly; 64 sequences of 16 tokens each are slower that way.)
+// Factors of fp16 values, behind the states and before the values.
+size_t factor_bytes(const pkv_pool_layout* L, const pkv_prefill_params* P) {
+  if (block_scaled(L)) return 0;
+  return static_cast<size_t>(round_up(2ll * P->num_seqs * L->num_kv_heads * sizeof(float), 256));
+}
+
+// e4m3 pages: the values pay for themselves from the second CTA on that reads the same keys: turning a tile of 128 keys
+// costs a CTA about 1.5 us, writing and reading it as bf16 as much as 15 ns of the GPU's bandwidth (16 chunks of 1
+// to 512 tokens over up to 16000 rows: 1229 us directly, 742 by values). Affine values need more bits than the direct
+// form's bf16 has.
 constexpr long long kMostValueBytes = 8ll << 30;
 
 long long prefill_value_blocks(const pkv_pool_layout* L, const pkv_prefill_params* P, int unit_tokens) {
@@ -1342,19 +1351,19 @@ long long prefill_value_blocks(const pkv_pool_layout* L, const pkv_prefill_param
   long long blocks = 0;
   prefill_values(L, P, &blocks);
   const long long bytes = blocks * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
-  const bool wanted = P->reading == PKV_READING_VALUES ||
+  const bool wanted = P->reading == PKV_READING_VALUES || !block_scaled(L) ||
                       (P->num_tokens >= static_cast<long long>(unit_tokens) * P->num_seqs && bytes <= kMostValueBytes);
-  // rows are counted in int by the copies
-  return wanted && blocks * L->num_kv_heads * pkv::kValueRows < (1ll << 31) ? blocks : 0;
+  return wanted ? blocks : 0;
 }
 
 int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_count, pkv_prefill_plan* plan) {
   const int rep = P->num_q_heads / L->num_kv_heads;
-  pkv::PrefillInfo info = prefill_info(L);
+  const long long blocks = prefill_value_blocks(L, P, prefill_info(L, L->bits != 16).query_tiles * (128 / rep));
+  // rows are counted in int by the copies
+  if (blocks * L->num_kv_heads * pkv::kValueRows >= (1ll << 31)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  const pkv::PrefillInfo info = prefill_info(L, blocks > 0);
   pkv_prefill_plan r{};
-  r.value_blocks = static_cast<int32_t>(prefill_value_blocks(L, P, info.query_tiles * (128 / rep)));
-  if (P->reading == PKV_READING_VALUES && L->bits != 16 && r.value_blocks == 0) return PKV_ERR_UNSUPPORTED_SHAPE;
-  if (r.value_blocks > 0) info = pkv::prefill_info_bf16(L->head_dim, v_dim(L));
+  r.value_blocks = static_cast<int32_t>(blocks);
   r.unit_tokens = info.query_tiles * (128 / rep);
   r.key_tile = info.key_tile;
   r.units = P->num_tokens / r.unit_tokens + P->num_seqs;
@@ -1366,7 +1375,8 @@ int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_c
     r.workspace_bytes = static_cast<size_t>(r.splits) * P->num_tokens * P->num_q_heads * (v_dim(L) + 2) * sizeof(float);
   if (r.value_blocks > 0)
     r.workspace_bytes = static_cast<size_t>(round_up(static_cast<long long>(r.workspace_bytes), 256)) +
-                        static_cast<size_t>(r.value_blocks) * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
+                        static_cast<size_t>(r.value_blocks) * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2 +
+                        factor_bytes(L, P);
   *plan = r;
   return PKV_OK;
 }
@@ -1492,8 +1502,10 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
     }
     return x;
   };
-  p.k_planes = planes(k_scales, k_biases);
-  p.v_planes = planes(v_scales, v_biases);
+  if (block) {
+    p.k_scales = static_cast<const float*>(k_scales);
+    p.v_scales = static_cast<const float*>(v_scales);
+  }
   pkv::PrefillValuesParams w{};
   if (values) {
     long long blocks = 0;
@@ -1501,11 +1513,14 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
     const size_t rows = static_cast<size_t>(plan.value_blocks) * layout->num_kv_heads * pkv::kValueRows;
     w.pool[0] = static_cast<const uint8_t*>(k_pool);
     w.pool[1] = static_cast<const uint8_t*>(v_pool);
-    w.planes[0] = p.k_planes;
-    w.planes[1] = p.v_planes;
+    w.planes[0] = planes(k_scales, k_biases);
+    w.planes[1] = planes(v_scales, v_biases);
     // behind the states
-    w.out[0] = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + plan.workspace_bytes - rows * (D + DV) * 2);
-    w.out[1] = w.out[0] + rows * D;
+    char* base = static_cast<char*>(workspace) + plan.workspace_bytes - rows * (D + DV) * 2;
+    w.out[0] = base;
+    w.out[1] = base + rows * D * 2;
+    w.factors = block ? nullptr : reinterpret_cast<float*>(base - factor_bytes(layout, params));
+    p.factors = w.factors;
     w.dim[0] = D;
     w.dim[1] = DV;
     w.values = p.values;
@@ -1528,8 +1543,8 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
     if (!rc) rc = pool_tensor_map(&tk, values ? w.out[0] : k_pool, 2, D, pool_rows, 128, piece, true);
     if (!rc) rc = pool_tensor_map(&tv, values ? w.out[1] : v_pool, 2, DV, pool_rows, 128, piece, true);
   } else {
-    if (!rc) rc = pool_tensor_map(&tk, k_pool, 1, D * layout->bits / 8, pool_rows, kWholeRows, piece, false);
-    if (!rc) rc = pool_tensor_map(&tv, v_pool, 1, DV * layout->bits / 8, pool_rows, kWholeRows, piece, false);
+    if (!rc) rc = pool_tensor_map(&tk, k_pool, 1, D, pool_rows, kWholeRows, piece, false);
+    if (!rc) rc = pool_tensor_map(&tv, v_pool, 1, DV, pool_rows, kWholeRows, piece, false);
   }
   if (rc) return rc;
   (void)cudaGetLastError();
@@ -1539,10 +1554,9 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
     e = pkv::launch_prefill_values(w, fmt, st);
     if (e != cudaSuccess) return cuda_fail("values kernel launch", e);
   }
-  e = fmt == 16 || values ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
-      : fmt == 4          ? pkv::launch_prefill_u4(D, DV, p, tq, tk, tv, plan.units, st, device)
-      : fmt == 8          ? pkv::launch_prefill_u8(D, DV, p, tq, tk, tv, plan.units, st, device)
-                          : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
+  e = fmt == 4 || fmt == 8    ? pkv::launch_prefill_f16(D, DV, p, tq, tk, tv, plan.units, st, device)
+      : fmt == 16 || values ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
+                            : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
   if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
   if (plan.splits > 1) {
     e = pkv::launch_prefill_join(p, DV, st);

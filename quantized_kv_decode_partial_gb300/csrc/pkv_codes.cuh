@@ -1,4 +1,4 @@
-// Codes of quantised pages to bf16 values, sixteen at a time, and packed f32 arithmetic.
+// Codes of quantised pages to 16-bit values, sixteen at a time, and packed f32 arithmetic.
 #pragma once
 
 #include "pkv_common.cuh"
@@ -29,9 +29,10 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// Sixteen codes of a row as bf16 pairs: scale * code (+ bias), in f32, rounded once.
+// Sixteen codes of a row as pairs of 16-bit values: e4m3 times their scale, in bf16; affine scale * code + bias, in
+// fp16. In f32, rounded once.
 template <int FMT>
-__device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float bias, uint32_t (&out)[8]) {
+__device__ __forceinline__ void codes_to_values(const uint4& v, float scale, float bias, uint32_t (&out)[8]) {
   if constexpr (FMT == kFmtE4m3) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -56,8 +57,8 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 a = floats(__byte_perm(w[i], 0x64646464u, 0x4140)), b = floats(__byte_perm(w[i], 0x64646464u, 0x4342));
-        out[2 * i] = pack_bf16x2(fmaf(a.x, scale, bias), fmaf(a.y, scale, bias));
-        out[2 * i + 1] = pack_bf16x2(fmaf(b.x, scale, bias), fmaf(b.y, scale, bias));
+        out[2 * i] = pack_f16x2(fmaf(a.x, scale, bias), fmaf(a.y, scale, bias));
+        out[2 * i + 1] = pack_f16x2(fmaf(b.x, scale, bias), fmaf(b.y, scale, bias));
       }
     } else {
       const uint32_t w[2] = {v.x, v.y};
@@ -68,8 +69,8 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& v, float scale, float
         for (int k = 0; k < 4; ++k) n[k] = floats((w[i] >> (4 * k) & 0x000F000Fu) | 0x64006400u);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          out[4 * i + k] = pack_bf16x2(fmaf(n[2 * k].x, scale, bias), fmaf(n[2 * k + 1].x, scale, bias));
-          out[4 * i + 2 + k] = pack_bf16x2(fmaf(n[2 * k].y, scale, bias), fmaf(n[2 * k + 1].y, scale, bias));
+          out[4 * i + k] = pack_f16x2(fmaf(n[2 * k].x, scale, bias), fmaf(n[2 * k + 1].x, scale, bias));
+          out[4 * i + 2 + k] = pack_f16x2(fmaf(n[2 * k].y, scale, bias), fmaf(n[2 * k + 1].y, scale, bias));
         }
       }
     }

@@ -195,8 +195,10 @@ struct PrefillPlanes {
 };
 
 struct PrefillParams {
-  PrefillPlanes k_planes, v_planes;
+  const float* k_scales;        // [NB, HK]   (e4m3 pages read directly)
+  const float* v_scales;
   PrefillValues values;
+  const float* factors;         // fp16 values: what K and V were multiplied by, [2][num_seqs][num_kv_heads]
   const int32_t* query_starts;  // [num_seqs + 1]
   const int32_t* block_tables;  // [num_seqs, max_blocks]
   const int32_t* seq_lens;      // rows held, the new ones included
@@ -218,7 +220,8 @@ struct PrefillParams {
 struct PrefillValuesParams {
   const uint8_t* pool[2];  // K, V
   PrefillPlanes planes[2];
-  __nv_bfloat16* out[2];   // [blocks][num_kv_heads][kValueRows][dim]
+  void* out[2];            // [blocks][num_kv_heads][kValueRows][dim]: bf16 (e4m3 pages) or fp16 (affine)
+  float* factors;          // fp16 values: powers of two that bring each (sequence, KV head) into range
   int dim[2];
   PrefillValues values;
   const int32_t* query_starts;

@@ -95,15 +95,12 @@ struct PrefillInfo {
   int query_tiles, key_tile, smem_bytes;
 };
 PrefillInfo prefill_info_bf16(int dk, int dv);
-PrefillInfo prefill_info_u4(int dk, int dv);
-PrefillInfo prefill_info_u8(int dk, int dv);
+PrefillInfo prefill_info_f16(int dk, int dv);
 PrefillInfo prefill_info_e4m3(int dk, int dv);
 cudaError_t launch_prefill_bf16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int units, cudaStream_t stream, int device);
-cudaError_t launch_prefill_u4(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                              const CUtensorMap& tv, int units, cudaStream_t stream, int device);
-cudaError_t launch_prefill_u8(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                              const CUtensorMap& tv, int units, cudaStream_t stream, int device);
+cudaError_t launch_prefill_f16(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, int units, cudaStream_t stream, int device);
 cudaError_t launch_prefill_e4m3(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int units, cudaStream_t stream, int device);
 cudaError_t launch_prefill_values(const PrefillValuesParams& p, int fmt, cudaStream_t stream);

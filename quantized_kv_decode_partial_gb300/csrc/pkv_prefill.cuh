@@ -25,7 +25,7 @@ namespace pkv {
 
 constexpr int kPrefillRoom = 225 * 1024;  // for tiles: 227 KB less barriers and the alignment of the first tile
 
-// Tiles of one instantiation. FMT: the page format (16, 4, 8 or kFmtE4m3).
+// Tiles of one instantiation. FMT: 16 (rows of 16-bit values) or kFmtE4m3.
 template <int D, int DV, int FMT>
 struct PrefillShape {
   static constexpr bool kCodes = FMT != 16;
@@ -33,12 +33,8 @@ struct PrefillShape {
   static constexpr int kQ = DV == 256 || (kCodes && D == 256) ? 1 : 2;
   static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;  // key rows per tile
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
-  // Pages of codes come in through a ring of quarter tiles, which six warps turn into bf16.
-  static constexpr int kKRow = FMT == 4 ? D / 2 : D, kVRow = FMT == 4 ? DV / 2 : DV;  // bytes of a row of codes
-  static constexpr int kWide = D > DV ? D : DV;
-  static constexpr int kRawCodes = KT / 4 * (kKRow > kVRow ? kKRow : kVRow);
-  static constexpr int kRawPlane = FMT == 4 || FMT == 8 ? KT / 4 * (kWide / 64) * 2 : 0;  // scales, then biases
-  static constexpr int kRawBytes = kRawCodes + 2 * kRawPlane;
+  // e4m3 codes come in through a ring of quarter tiles, which six warps turn into bf16.
+  static constexpr int kRawBytes = KT / 4 * (D > DV ? D : DV);
   // As many as fit beside two stages of K and V (up to 8): each of the three pairs has one or two in the works.
   static constexpr int kRawFit = (kPrefillRoom - kQ * kQBytes - 2 * (kKBytes + kVBytes)) / kRawBytes;
   static constexpr int kRawSlots = !kCodes ? 0 : kRawFit > 8 ? 8 : kRawFit;
@@ -78,7 +74,7 @@ constexpr int kPrefillStates = 512;   // tensor memory columns
 
 // A work unit's place: computed by every warp from the same words.
 struct PrefillUnit {
-  int head, split;
+  int seq, head, split;
   int first;           // first token of the unit (packed), and its tokens
   int tokens;
   int position;        // cache place of the first token
@@ -104,6 +100,7 @@ __device__ __forceinline__ PrefillUnit prefill_unit(const PrefillParams& p, int 
   const long long first = (slot - (static_cast<long long>(start / unit_tokens) + b)) * unit_tokens;
   const int len = p.seq_lens[b];
   const bool starts_ok = start >= 0 && n >= 0 && start + n <= p.tokens;
+  u.seq = b;
   u.live = starts_ok && first >= 0 && first < n;
   u.valid = u.live && len >= n && len <= static_cast<long long>(p.max_blocks) * p.block_size;
   u.first = u.live ? static_cast<int>(start + first) : 0;
@@ -151,10 +148,18 @@ __device__ __forceinline__ float row_max(const float (&s)[KT]) {
   return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
 }
 
-// A row's weights 2^(c s - c m) as bf16 pairs, their f32 sums added to `sums`; returns the largest score.
+// s - m, where there is an m.
 template <int KT>
+__device__ __forceinline__ void subtract(float (&s)[KT], float m) {
+  if (m == -INFINITY) return;
+#pragma unroll
+  for (int e = 0; e < KT; ++e) s[e] -= m;
+}
+
+// A row's weights 2^(c s - c m) as pairs of bf16 (or fp16), their f32 sums added to `sums`; returns the largest score.
+template <int KT, bool HALF>
 __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m, uint64_t (&sums)[2], uint32_t (&w)[KT / 2]) {
-  const float mc = m == -INFINITY ? 0.f : m * c;
+  const float mc = fabsf(m) < INFINITY ? m * c : 0.f;
   const uint64_t cc = pair(c, c), mm = pair(-mc, -mc);
 #pragma unroll
   for (int e = 0; e < KT / 2; ++e) {
@@ -163,7 +168,7 @@ __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m,
     x = fast_exp2(x);
     y = fast_exp2(y);
     sums[e & 1] = add2(sums[e & 1], pair(x, y));
-    w[e] = pack_bf16x2(x, y);
+    w[e] = HALF ? pack_f16x2(x, y) : pack_bf16x2(x, y);
   }
   return row_max<KT>(s);
 }
@@ -171,40 +176,25 @@ __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m,
 // Half of a quarter tile of codes (a warp's part of two): rows [first, first + KT/4) of the tile, 16 values a lane
 // at a time. Rows that nobody sees and those of pieces without their bit become zeros.
 template <int D, int FMT, int KT>
-__device__ __forceinline__ void convert_quarter(uint32_t to, uint32_t from, uint32_t from_scales, uint32_t from_biases, int part,
-                                                int first, int seen_lo, int seen_hi, uint32_t bits, uint32_t scales,
-                                                int piece_log2) {
+__device__ __forceinline__ void convert_quarter(uint32_t to, uint32_t from, int part, int first, int seen_lo, int seen_hi,
+                                                uint32_t bits, uint32_t scales, int piece_log2) {
   constexpr int kPerRow = D / 16, kChunks = KT / 4 * kPerRow;
   const int lane = threadIdx.x & 31;
   const bool whole = seen_lo <= first && seen_hi >= first + KT / 4 && bits == (1u << ((KT / 4) >> piece_log2)) - 1u;
   constexpr int kRounds = (kChunks + 63) / 64;
   uint4 v[kRounds];  // all loads first: one round's latency instead of every round's
-  float scale[kRounds], bias[kRounds];
+  float scale[kRounds];
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const int c = i * 64 + part * 32 + lane;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    scale[i] = bias[i] = 0.f;
+    scale[i] = 0.f;
     if (kChunks % 64 && c >= kChunks) break;
-    const int r = c / kPerRow, col = c % kPerRow;  // row of the quarter
-    if constexpr (FMT == 4) {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[i].x), "=r"(v[i].y) : "r"(from + c * 8) : "memory");
-    } else {
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                   : "r"(from + c * 16)
-                   : "memory");
-    }
-    if constexpr (FMT == kFmtE4m3) {
-      scale[i] = ld_shared_f32(scales + 4 * (r >> piece_log2));
-    } else {
-      uint16_t s16, b16;
-      const int at = (r * (D / 64) + col / 4) * 2;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(from_scales + at) : "memory");
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b16) : "r"(from_biases + at) : "memory");
-      scale[i] = __uint_as_float(static_cast<uint32_t>(s16) << 16);
-      bias[i] = __uint_as_float(static_cast<uint32_t>(b16) << 16);
-    }
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                 : "r"(from + c * 16)
+                 : "memory");
+    scale[i] = ld_shared_f32(scales + 4 * (c / kPerRow >> piece_log2));
   }
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
@@ -212,7 +202,7 @@ __device__ __forceinline__ void convert_quarter(uint32_t to, uint32_t from, uint
     if (kChunks % 64 && c >= kChunks) break;
     const int r = c / kPerRow, col = c % kPerRow;
     uint32_t w[8];
-    codes_to_bf16<FMT>(v[i], scale[i], bias[i], w);
+    codes_to_values<FMT>(v[i], scale[i], 0.f, w);
     if (!whole && !(first + r >= seen_lo && first + r < seen_hi && (bits >> (r >> piece_log2) & 1))) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 0u;
@@ -240,18 +230,20 @@ struct PrefillRow {
 
 // tq, tk, tv: TMA descriptors of the queries ([64 dims][head][token][run of dims]) and of the pools'
 // planes ([64 dims][row][run of dims]).
-template <int D, int DV, int FMT>
+// HALF: K and V are fp16 values (PrefillParams.factors); queries become fp16 in shared memory, each row under a power of
+// two of its own, and weights are fp16.
+template <int D, int DV, int FMT, bool HALF>
 __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     pkv_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using T = PrefillShape<D, DV, FMT>;
   constexpr int KT = T::KT, KS = T::kKS, VS = T::kVS, RS = T::kCodes ? T::kRawSlots : 1;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * KS + 2 * VS + 2 * RS + 8];
+  __shared__ __align__(8) uint64_t bars[2 * (KS + VS + RS) + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ uint32_t piece_bits[VS];
-  __shared__ uint32_t unit_bits[RS];  // pages of codes: a quarter tile's pieces, and their scales (e4m3)
+  __shared__ uint32_t unit_bits[RS];  // codes: a quarter tile's pieces, and their scales
   __shared__ float unit_scales[RS][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -306,12 +298,13 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   auto s_full = [&](int s) { return bar0 + 8 * (kRest + s); };
   auto p_full = [&](int s) { return bar0 + 8 * (kRest + 2 + s); };
   auto o_done = [&](int s) { return bar0 + 8 * (kRest + 4 + s); };
-  const uint32_t q_full = bar0 + 8 * (kRest + 6), drained = bar0 + 8 * (kRest + 7);
+  const uint32_t q_full = bar0 + 8 * (kRest + 6), drained = bar0 + 8 * (kRest + 7), q_half = bar0 + 8 * (kRest + 8);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRest + 8; ++i) {
+    for (int i = 0; i < kRest + 9; ++i) {
       int arrivals = 1;
       if (i == kRest + 2 || i == kRest + 3) arrivals = 4;  // p_full: the four warps of a query tile
+      if (i == kRest + 8) arrivals = 4 * tiles_q;           // q_half
       if (T::kCodes) {                                     // two warps for each quarter of a tile
         if (i < KS || (i >= 2 * KS && i < 2 * KS + VS)) arrivals = 8;
         if (i >= 2 * (KS + VS) + RS && i < kRest) arrivals = 2;
@@ -406,9 +399,9 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     for (int i = max(0, asked - stages); i < asked; ++i)
       mbar_wait_close(full0 + 8 * (i % stages), (i / stages) & 1, &none, p.error_flag, kWaitLimitNs);
   } else if (T::kCodes && warp >= 9) {
-    // ------------------------------------------------------------------ pages of codes, to bf16 tiles
+    // ------------------------------------------------------------------ e4m3 codes, to bf16 tiles
     // Quarter tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is quarter n & 3 of plane tile n / 4. Warp 9
-    // copies their codes (and affine scales), RS units ahead; three pairs of warps turn them into bf16 in turn.
+    // copies their codes, RS units ahead; three pairs of warps turn them into bf16 in turn.
     fewer_registers<T::kCodes>();
     if constexpr (T::kCodes) {
       constexpr int kQuarter = KT / 4;
@@ -433,8 +426,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         uint32_t bits = tile_pieces(t0 + j, row);
         for (int x = 0; ok && x < 2 * nt; ++x) {
           float scale = 0.f;
-          if (FMT == kFmtE4m3 && (bits >> lane & 1))
-            scale = (is_k ? p.k_planes : p.v_planes).block_scales[row / p.block_size];
+          if (bits >> lane & 1) scale = (is_k ? p.k_scales : p.v_scales)[row / p.block_size];
           bool next_k = false;
           int next_j = 0, next_row = 0;
           uint32_t next_bits = 0;
@@ -442,40 +434,26 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
             plane_tile(x + 1, next_k, next_j);
             next_bits = tile_pieces(t0 + next_j, next_row);
           }
-          const int row_bytes = is_k ? T::kKRow : T::kVRow, groups = (is_k ? D : DV) / 64;
-          const int plane_bytes = FMT == kFmtE4m3 ? 0 : piece * groups * 2;
+          const int row_bytes = is_k ? D : DV;
           for (int h = 0; h < 4; ++h) {
             const int n = 4 * x + h, s = n % RS, first = h * per;
             if (n >= RS) ok = mbar_wait_close(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
             if (!ok) break;
             const uint32_t mine = bits >> first & ((1u << per) - 1u);
             const bool copies = lane >= first && lane < first + per;
-            if (FMT == kFmtE4m3 && copies) unit_scales[s][lane - first] = scale;
+            if (copies) unit_scales[s][lane - first] = scale;
             __syncwarp();
             if (lane == 0) {
               unit_bits[s] = mine;
-              mbar_arrive_expect_tx(raw_full(s), __popc(mine) * (piece * row_bytes + 2 * plane_bytes));
+              mbar_arrive_expect_tx(raw_full(s), __popc(mine) * piece * row_bytes);
             }
             __syncwarp();
-            if (copies && (bits >> lane & 1)) {
-              const uint32_t slot = smem_raw_codes + s * T::kRawBytes;
+            if (copies && (bits >> lane & 1))
               asm volatile(
                   "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                  "[%0], [%1, {%2, %3}], [%4];" ::"r"(slot + (lane - first) * piece * row_bytes),
+                  "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_raw_codes + s * T::kRawBytes + (lane - first) * piece * row_bytes),
                   "l"(reinterpret_cast<uint64_t>(is_k ? &tk : &tv)), "r"(0), "r"(row), "r"(raw_full(s))
                   : "memory");
-              if constexpr (FMT != kFmtE4m3) {
-                const PrefillPlanes& planes = is_k ? p.k_planes : p.v_planes;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                  asm volatile(
-                      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                          slot + T::kRawCodes + b * T::kRawPlane + (lane - first) * plane_bytes),
-                      "l"((b ? planes.biases : planes.scales) + static_cast<size_t>(row) * groups), "r"(plane_bytes),
-                      "r"(raw_full(s))
-                      : "memory");
-              }
-            }
             __syncwarp();
             ++asked;
           }
@@ -499,14 +477,14 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
                                            p.wait_limit_ns))
             break;
           if (!mbar_wait_close(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
-          const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = from + T::kRawCodes;
+          const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = smem_addr(unit_scales[s]);
           const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;
           if (is_k) {
-            convert_quarter<D, FMT, KT>(smem_k + stage * T::kKBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
-                                        hi - key, unit_bits[s], smem_addr(unit_scales[s]), p.piece_log2);
+            convert_quarter<D, FMT, KT>(smem_k + stage * T::kKBytes, from, part, first, lo - key, hi - key, unit_bits[s], scales,
+                                        p.piece_log2);
           } else {
-            convert_quarter<DV, FMT, KT>(smem_v + stage * T::kVBytes, from, scales, scales + T::kRawPlane, part, first, lo - key,
-                                         hi - key, unit_bits[s], smem_addr(unit_scales[s]), p.piece_log2);
+            convert_quarter<DV, FMT, KT>(smem_v + stage * T::kVBytes, from, part, first, lo - key, hi - key, unit_bits[s], scales,
+                                         p.piece_log2);
           }
           fence_proxy_async_smem();  // the tile's rows are there for the products
           __syncwarp();
@@ -521,8 +499,8 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     // ------------------------------------------------------------------ products
     fewer_registers<T::kCodes>();
     const uint32_t leader = elect_lane(), base = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t instr_s = umma_instr(KT, false, p.negate != 0), instr_o = umma_instr(DV, true, false);
-    bool ok = mbar_wait_close(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
+    const uint32_t instr_s = umma_instr(KT, false, p.negate != 0, HALF), instr_o = umma_instr(DV, true, false, HALF);
+    bool ok = mbar_wait_close(HALF ? q_half : q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
     // Item i's query tile and key tile are counted along; a stage's index and parity follow its ring.
     struct Place {
       int q, tile, stage, parity;
@@ -596,8 +574,12 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     const int last = min(first + p.tile_tokens, u.tokens) - 1;
     const int pos = u.position + min(first + r / p.rep, last);  // rows without a token go along with the last one
     const int below = p.window > 0 ? pos - p.window : -1;       // keys at or below it are out of the window
-    const float c = p.score_scale;
+    float c = p.score_scale;
+    float out_factor = 1.f;
     float m = -INFINITY;          // running maximum of the unscaled scores
+    // c s - c m is rounded once, but c m before it: where that could be off by more than 2^-4 in a row of the warp,
+    // s - m comes first.
+    bool far = false;
     uint64_t l[2] = {0ull, 0ull};  // sums of weights, two pairs
     const uint32_t o_at = tmem + lanes + T::kTmemO + q * DV;
     // Are all blocks of this CTA's keys in the pool? Almost always; then no tile asks again.
@@ -610,7 +592,40 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       any_bad = group_barrier_any(1 + q, 128, any_bad);
     }
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
+    if constexpr (HALF) {
+      // This thread's query row to fp16, its largest value brought to [2^13, 2^14): what is below 2^-39 of that is lost.
+      ok = mbar_wait_close(q_full, 0, &abort_flag, p.error_flag, p.wait_limit_ns);
+      const uint32_t row = smem + q * T::kQBytes + r * 128;
+      auto at = [&](int i) { return row + i / 8 * (128 * 128) + ((i % 8 ^ (r & 7)) << 4); };
+      uint32_t most = 0u;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at(i)) : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = max(most, max(x[k] & 0x7FFFu, x[k] >> 16 & 0x7FFFu));
+      }
+      // 2^e with e = 13 - exponent; zeros and values that are not finite stay as they are
+      const int e = most == 0u || most >= 0x7F80u ? 0 : min(13 - (static_cast<int>(most >> 7) - 127), 120);
+      const float by = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at(i)) : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = pack_f16x2(__uint_as_float(x[k] << 16) * by, __uint_as_float(x[k] & 0xFFFF0000u) * by);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at(i)), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(q_half);
+      const float* factors = p.factors + static_cast<size_t>(u.seq) * p.num_kv_heads + u.head;
+      c = fmaxf(c / by / factors[0], 1e-37f);  // not zero, as ever
+      out_factor = 1.f / factors[static_cast<size_t>(p.num_seqs) * p.num_kv_heads];
+    }
+    const int tiles = HALF && !ok ? 0 : nt;
+    for (int j = 0; j < tiles; ++j) {
       const int i = j * tiles_q + q;
       const int key = (t0 + j) * KT;
       ok = mbar_wait_close(s_full(i & 1), (i >> 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
@@ -640,7 +655,9 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         }
         if (j == 0) m = row_max<KT>(s);
         uint64_t sums[2] = {l[0], l[1]};
-        const float up = fmaxf(m, weights<KT>(s, c, m, sums, w));
+        if (j == 0) far = __any_sync(0xffffffffu, fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
+        if (far) subtract<KT>(s, m);
+        const float up = fmaxf(m, weights<KT, HALF>(s, c, far ? 0.f : m, sums, w) + (far && m > -INFINITY ? m : 0.f));
         if (again || j == 0 || !__any_sync(0xffffffffu, (up - m) * c > 8.f || (m == -INFINITY && up > m))) {
           l[0] = sums[0];
           l[1] = sums[1];
@@ -648,6 +665,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         }
         const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
         m = up;
+        far = __any_sync(0xffffffffu, fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
 #pragma unroll
         for (int n = 0; n < 2; ++n) l[n] = mul2(l[n], pair(by, by));
         ok = mbar_wait_close(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
@@ -683,7 +701,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       unpair(l[0], l0, l1);
       unpair(l[1], l2, l3);
       const float sum = (l0 + l1) + (l2 + l3);
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const float inv = (sum != 0.f ? 1.f / sum : 0.f) * out_factor;
       if (split && out.live) {
         float* ml = p.ws_ml + (u.split * all_rows + out.row) * 2;
         ml[0] = m * c;
@@ -698,8 +716,8 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           float4* to = reinterpret_cast<float4*>(p.ws_o + (u.split * all_rows + out.row) * DV + d);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            to[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                __uint_as_float(o[4 * e + 3]));
+            to[e] = make_float4(__uint_as_float(o[4 * e]) * out_factor, __uint_as_float(o[4 * e + 1]) * out_factor,
+                                __uint_as_float(o[4 * e + 2]) * out_factor, __uint_as_float(o[4 * e + 3]) * out_factor);
         } else if (out.live) {
           uint4* to = reinterpret_cast<uint4*>(p.out + out.row * DV + d);
 #pragma unroll

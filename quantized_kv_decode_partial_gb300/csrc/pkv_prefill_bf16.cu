@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_cons
 
 }  // namespace
 
-PKV_PREFILL_FORMAT(bf16, 16, PKV_PREFILL_WIDE)
+PKV_PREFILL_FORMAT(bf16, 16, false, PKV_PREFILL_WIDE)
 
 cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream) {
   PrefillJoinParams j{p.ws_o, p.ws_ml, p.query_starts, p.out, p.num_seqs, p.tokens, p.num_q_heads, p.splits};

@@ -3,6 +3,6 @@
 
 namespace pkv {
 
-PKV_PREFILL_FORMAT(e4m3, kFmtE4m3, PKV_PREFILL_WIDE)
+PKV_PREFILL_FORMAT(e4m3, kFmtE4m3, false, PKV_PREFILL_WIDE)
 
 }  // namespace pkv

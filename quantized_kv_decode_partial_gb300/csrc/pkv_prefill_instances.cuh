@@ -24,18 +24,18 @@ inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int thre
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int DV, int FMT>
+template <int D, int DV, int FMT, bool HALF>
 cudaError_t launch_prefill_of(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int units,
                       cudaStream_t stream, int device) {
   constexpr int smem = PrefillShape<D, DV, FMT>::kSmem;
   static std::atomic<bool> ready[256];  // per device; a second thread's call sets the same attribute again
   if (device < 0 || device >= 256 || !ready[device].load(std::memory_order_relaxed)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(pkv_prefill_kernel<D, DV, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(pkv_prefill_kernel<D, DV, FMT, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (device >= 0 && device < 256) ready[device].store(true, std::memory_order_relaxed);
   }
-  return launch_dependent(pkv_prefill_kernel<D, DV, FMT>, dim3(units * p.num_kv_heads * p.splits), PrefillShape<D, DV, FMT>::kThreads, smem, stream,
+  return launch_dependent(pkv_prefill_kernel<D, DV, FMT, HALF>, dim3(units * p.num_kv_heads * p.splits), PrefillShape<D, DV, FMT>::kThreads, smem, stream,
                           p, tq, tk, tv);
 }
 
@@ -52,8 +52,8 @@ PrefillInfo prefill_info_of() {
 #define PKV_PREFILL_INFO_OF(DK_, DV_) \
   if (dk == DK_ && dv == DV_) return prefill_info_of<DK_, DV_, kFmt>();
 #define PKV_PREFILL_LAUNCH_OF(DK_, DV_) \
-  if (dk == DK_ && dv == DV_) return launch_prefill_of<DK_, DV_, kFmt>(p, tq, tk, tv, units, stream, device);
-#define PKV_PREFILL_FORMAT(NAME, FMT, SHAPES)                                                                          \
+  if (dk == DK_ && dv == DV_) return launch_prefill_of<DK_, DV_, kFmt, kHalf>(p, tq, tk, tv, units, stream, device);
+#define PKV_PREFILL_FORMAT(NAME, FMT, HALF, SHAPES)                                                                    \
   PrefillInfo prefill_info_##NAME(int dk, int dv) {                                                                    \
     constexpr int kFmt = FMT;                                                                                          \
     SHAPES(PKV_PREFILL_INFO_OF)                                                                                        \
@@ -62,6 +62,7 @@ PrefillInfo prefill_info_of() {
   cudaError_t launch_prefill_##NAME(int dk, int dv, const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, \
                                     const CUtensorMap& tv, int units, cudaStream_t stream, int device) {               \
     constexpr int kFmt = FMT;                                                                                          \
+    constexpr bool kHalf = HALF;                                                                                       \
     SHAPES(PKV_PREFILL_LAUNCH_OF)                                                                                      \
     return cudaErrorInvalidValue;                                                                                      \
   }

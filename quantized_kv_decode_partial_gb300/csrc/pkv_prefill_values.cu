@@ -1,5 +1,11 @@
-// Values of the cached rows that a prompt attention call sees, as bf16, from pages of codes: written once, where
-// several query tiles would otherwise turn the same codes each for itself.
+// Values of the cached rows that a prompt attention call sees, from pages of codes: written once, where several query
+// tiles would otherwise turn the same codes each for itself.
+//
+// e4m3 codes become bf16, which holds a code times a power of two exactly. Affine values need more bits than bf16 has:
+// rounded to it, keys and values together cost the output as much again as its own rounding and that of bf16 weights
+// do (root mean square 2.5e-3 of the output against 1.7e-3). They become fp16, each (sequence, KV head) and plane
+// brought into fp16's range by a power of two that a pass over the scales and biases alone finds first; what is below
+// 2^-39 of the largest is lost. Weights and queries are fp16 then as well.
 //
 // One CTA per (32 rows, KV head, plane): 16 codes a thread at a time, every load ahead of the first conversion. Bound by
 // HBM: it reads the codes and writes twice (8-bit) or four times (4-bit) their bytes.
@@ -16,7 +22,7 @@ constexpr int kThreads = 128;
 
 template <int D, int FMT>
 __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int plane, const int32_t* table, int first_row,
-                                             int len, __nv_bfloat16* out, int head) {
+                                             int len, uint16_t* out, int head, float factor) {
   constexpr int kPerRow = D / 16, kRounds = kRows * kPerRow / kThreads;
   uint4 v[kRounds];
   float scale[kRounds], bias[kRounds];
@@ -41,8 +47,8 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
     if constexpr (FMT == kFmtE4m3) {
       scale[i] = p.planes[plane].block_scales[cell];
     } else {
-      scale[i] = __bfloat162float(p.planes[plane].scales[row * (D / 64) + col / 4]);
-      bias[i] = __bfloat162float(p.planes[plane].biases[row * (D / 64) + col / 4]);
+      scale[i] = __bfloat162float(p.planes[plane].scales[row * (D / 64) + col / 4]) * factor;
+      bias[i] = __bfloat162float(p.planes[plane].biases[row * (D / 64) + col / 4]) * factor;
     }
   }
 #pragma unroll
@@ -50,7 +56,7 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
     const int c = i * kThreads + threadIdx.x, r = c / kPerRow;
     if (first_row + r >= len) continue;  // nobody's rows are left as they are
     uint32_t w[8];
-    codes_to_bf16<FMT>(v[i], scale[i], bias[i], w);
+    codes_to_values<FMT>(v[i], scale[i], bias[i], w);
     uint4* to = reinterpret_cast<uint4*>(out) + 2 * c;
     to[0] = make_uint4(w[0], w[1], w[2], w[3]);
     to[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -73,25 +79,81 @@ __global__ void __launch_bounds__(kThreads) pkv_prefill_values_kernel(const __gr
   if (block < p.values.base(b, start) || row >= len) return;
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   const size_t to = (static_cast<size_t>(block) * p.num_kv_heads + head) * kValueRows + row0;
+  uint16_t* out = static_cast<uint16_t*>(p.out[plane]);
+  const float factor = FMT == kFmtE4m3 ? 1.f : p.factors[(plane * p.num_seqs + b) * p.num_kv_heads + head];
   if (plane == 0) {
-    plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, p.out[0] + to * D, head);
+    plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, out + to * D, head, factor);
   } else {
-    plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, p.out[1] + to * DV, head);
+    plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, out + to * DV, head, factor);
   }
+}
+
+// One CTA per (KV head, sequence, plane): the largest |scale * code + bias| that any code could have in the rows that
+// are seen, and the power of two that brings it to [2^13, 2^14).
+template <int FMT>
+__global__ void __launch_bounds__(1024) pkv_prefill_range_kernel(const __grid_constant__ PrefillValuesParams p) {
+  __shared__ float most[32];
+  wait_for_prerequisite_grids();
+  const int head = blockIdx.x, b = blockIdx.y, plane = blockIdx.z;
+  const int start = p.query_starts[b], len = p.seq_lens[b];
+  const long long n = static_cast<long long>(p.query_starts[b + 1]) - start;
+  const bool seen = start >= 0 && n > 0 && start + n <= p.tokens && len >= n &&
+                    len <= static_cast<long long>(p.max_blocks) * p.block_size;
+  const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  const int pairs = p.dim[plane] / 128;  // of groups in a row, one 32-bit word of scales each
+  constexpr float kLevels = static_cast<float>((1 << FMT) - 1);
+  float m = 0.f;
+  if (seen) {
+#pragma unroll 4
+    for (int t = p.values.first_row(len, static_cast<int>(n), p.window) + threadIdx.x; t < len; t += 1024) {
+      const int blk = t / p.block_size;
+      const int phys = table[blk];
+      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;
+      const size_t row = (static_cast<size_t>(phys) * p.num_kv_heads + head) * p.block_size + (t - blk * p.block_size);
+      for (int i = 0; i < pairs; ++i) {
+        const __nv_bfloat162 s2 = reinterpret_cast<const __nv_bfloat162*>(p.planes[plane].scales)[row * pairs + i];
+        const __nv_bfloat162 b2 = reinterpret_cast<const __nv_bfloat162*>(p.planes[plane].biases)[row * pairs + i];
+        const float2 sc = __bfloat1622float2(s2), bi = __bfloat1622float2(b2);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(bi.x), fabsf(fmaf(sc.x, kLevels, bi.x))),
+                           fmaxf(fabsf(bi.y), fabsf(fmaf(sc.y, kLevels, bi.y)))));
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 32; ++i) m = fmaxf(m, most[i]);
+    // 2^(13 - exponent of m), within what f32 and its reciprocal hold
+    const int e = 13 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
+    p.factors[(plane * p.num_seqs + b) * p.num_kv_heads + head] =
+        m > 0.f && m < INFINITY ? __uint_as_float(static_cast<uint32_t>(min(max(e, -120), 120) + 127) << 23) : 1.f;
+  }
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, dim3 grid, int threads, const PrefillValuesParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernels wait before they touch memory
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D, int DV, int FMT>
 cudaError_t launch_of(const PrefillValuesParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.blocks * (kValueRows / kRows), p.num_kv_heads, 2);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits before it touches memory
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_prefill_values_kernel<D, DV, FMT>, p);
+  if constexpr (FMT != kFmtE4m3) {
+    const cudaError_t e = launch(pkv_prefill_range_kernel<FMT>, dim3(p.num_kv_heads, p.num_seqs, 2), 1024, p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch(pkv_prefill_values_kernel<D, DV, FMT>, dim3(p.blocks * (kValueRows / kRows), p.num_kv_heads, 2), kThreads, p,
+                stream);
 }
 
 }  // namespace

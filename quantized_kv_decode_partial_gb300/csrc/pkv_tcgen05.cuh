@@ -108,10 +108,10 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t smem, uint32_t lead) {
          static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// kind::f16 with bf16 operands and f32 sums, M = 128. b_columns: B's rows run along the
+// kind::f16 with f32 sums, M = 128; operands bf16, or fp16 with `half`. b_columns: B's rows run along the
 // contracted dim. negate: -A.
-__device__ __forceinline__ constexpr uint32_t umma_instr(int n, bool b_columns, bool negate) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (negate ? 1u << 13 : 0u) | (b_columns ? 1u << 16 : 0u) |
+__device__ __forceinline__ constexpr uint32_t umma_instr(int n, bool b_columns, bool negate, bool half) {
+  return 1u << 4 | (half ? 0u : 1u << 7 | 1u << 10) | (negate ? 1u << 13 : 0u) | (b_columns ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n >> 3) << 17 | 8u << 24;
 }
 

@@ -54,24 +54,31 @@ def test_plans(lib, dk, dv, rep):
 
 def test_values_are_written_where_many_tokens_share_keys(lib):
     e4m3 = dict(bits=8, group_size=B.PKV_GROUP_BLOCK)
-    for fmt in (e4m3, dict(bits=8), dict(bits=4)):
-        lay = layout(num_kv_heads=8, **fmt)
-        few, many = params(num_tokens=30, num_q_heads=32, splits=1), params(num_tokens=1000, num_q_heads=32, splits=1)
-        assert plan(lib, lay, few)[1].value_blocks == 0 and plan(lib, lay, few)[1].workspace_bytes == 0
-        p = plan(lib, lay, many)[1]
-        assert p.value_blocks == 2 * 3 and p.workspace_bytes == 6 * 8 * 128 * 256 * 2  # tables of 320 rows
-        for reading, blocks in ((1, 0), (2, 6)):
-            few.reading = many.reading = reading
-            assert plan(lib, lay, few)[1].value_blocks == plan(lib, lay, many)[1].value_blocks == blocks
+    few, many = params(num_tokens=30, num_q_heads=32, splits=1), params(num_tokens=1000, num_q_heads=32, splits=1)
+    lay = layout(num_kv_heads=8, **e4m3)
+    assert plan(lib, lay, few)[1].value_blocks == 0 and plan(lib, lay, few)[1].workspace_bytes == 0
+    p = plan(lib, lay, many)[1]
+    assert p.value_blocks == 2 * 3 and p.workspace_bytes == 6 * 8 * 128 * 256 * 2  # tables of 320 rows
+    for reading, blocks in ((1, 0), (2, 6)):
+        few.reading = many.reading = reading
+        assert plan(lib, lay, few)[1].value_blocks == plan(lib, lay, many)[1].value_blocks == blocks
     # a window bounds them by the tokens; more than 8 GB are written for the asking alone
     lay, wide = layout(num_kv_heads=8, num_blocks=70000, **e4m3), dict(num_tokens=1000, num_q_heads=32, max_blocks_per_seq=33000)
     assert plan(lib, lay, params(window=300, **wide))[1].value_blocks == 1000 // 128 + 1 + 2 * (300 // 128 + 3)
     assert plan(lib, lay, params(**wide))[1].value_blocks == 0
     assert plan(lib, lay, params(reading=2, **wide))[1].value_blocks == 2 * 8250
     # rows beyond 31 bits are never written
-    huge = params(num_seqs=300, reading=2, **wide)  # 300 * 8250 * 8 * 128
-    assert plan(lib, lay, huge)[0] == B.PKV_ERR_UNSUPPORTED_SHAPE
+    assert plan(lib, lay, params(num_seqs=300, reading=2, **wide))[0] == B.PKV_ERR_UNSUPPORTED_SHAPE  # 300 * 8250 * 8 * 128
     assert plan(lib, layout(), params(reading=2))[1].value_blocks == 0  # bf16 pages are read as they are
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_affine_pages_are_read_by_values(lib, bits):
+    lay = layout(num_kv_heads=8, bits=bits)
+    for n in (30, 1000):
+        p = plan(lib, lay, params(num_tokens=n, num_q_heads=32, splits=1))[1]
+        assert p.value_blocks == 6 and p.workspace_bytes == 6 * 8 * 128 * 256 * 2 + 256  # and the factors
+    assert plan(lib, lay, params(num_q_heads=32, reading=1))[0] == B.PKV_ERR_UNSUPPORTED_SHAPE
 
 
 def test_splits_fill_the_gpu_and_can_be_set(lib):

@@ -102,7 +102,7 @@ def reference(q, cache, news, scale, window=0, hidden=None):
         # weights: rounded to bf16 (2^-8); scores: d products of 16 at a time into f32, each step off by
         # 17 * 2^-24 of the sum of magnitudes; the exponential and its argument 2^-20; sums over L keys in f32
         rel = 2.0 ** -8 + 2 * (1.1 * d * 2.0 ** -24 * size + 2.0 ** -20) + L * 2.0 ** -24
-        if cache.fmt.get("bits", 16) != 16:  # keys and values rounded to bf16 on their way in, unless they fit
+        if cache.fmt.get("bits", 16) != 16:  # keys and values rounded to bf16 (affine: fp16) on their way in, unless they fit
             rel = rel + 2.0 ** -8 + 2 * 2.0 ** -8 * size
         out[first:first + n] = o.permute(2, 0, 1, 3).reshape(n, hq, dv)
         tol[first:first + n] = (2.0 ** -8 * o.abs() + rel * a).permute(2, 0, 1, 3).reshape(n, hq, dv)
@@ -181,12 +181,17 @@ AFFINE = [(128, 128), (256, 256), (256, 128), (128, 256)]
 CODES = [(E4M3, d) for d in DIMS] + [(dict(bits=b), d) for b in (4, 8) for d in AFFINE]
 
 
+def allowed(fmt, reading):
+    """Affine pages have one way of being read."""
+    return reading if fmt is E4M3 else 0
+
+
 @pytest.mark.parametrize("fmt,dims", CODES)
 @pytest.mark.parametrize("splits,reading", [(0, 0), (1, 1), (3, 1), (1, 2), (3, 2)])
 def test_pages_of_codes(fmt, dims, splits, reading):
     lens, news = [1, 700, 33, 129, 1000, 64, 130], [1, 200, 0, 129, 3, 64, 2]
     cache = Cache(lens, 2, *dims, 32, fmt, seed=splits)
-    check(randn(sum(news), 6, dims[0], seed=2), cache, news, 1 / math.sqrt(dims[0]), splits=splits, reading=reading)
+    check(randn(sum(news), 6, dims[0], seed=2), cache, news, 1 / math.sqrt(dims[0]), splits=splits, reading=allowed(fmt, reading))
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
@@ -196,7 +201,7 @@ def test_block_sizes_of_codes(fmt, bs, reading):
     lens, news = [517, 130], [300, 130]
     for dims in ((128, 128), (256, 256)):
         check(randn(sum(news), 4, dims[0], seed=3), Cache(lens, 2, *dims, bs, fmt, seed=bs + 1), news, 0.09, splits=1,
-              reading=reading)
+              reading=allowed(fmt, reading))
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
@@ -205,11 +210,11 @@ def test_block_sizes_of_codes(fmt, bs, reading):
 def test_windows_of_codes(fmt, window, reading):
     lens, news = [900, 260, 5, 2000, 129], [300, 260, 5, 0, 129]
     for dims in ((128, 128), (256, 256)):
-        check(randn(sum(news), 4, dims[0], seed=5), Cache(lens, 2, *dims, 32, fmt), news, 0.09, window=window, reading=reading)
+        check(randn(sum(news), 4, dims[0], seed=5), Cache(lens, 2, *dims, 32, fmt), news, 0.09, window=window, reading=allowed(fmt, reading))
     # tables so wide that the values lie by tokens
     cache = Cache(lens, 2, 128, 128, 32, fmt)
     cache.tables = torch.nn.functional.pad(cache.tables, (0, 400), value=-1)
-    check(randn(sum(news), 4, 128, seed=5), cache, news, 0.09, window=window, reading=reading)
+    check(randn(sum(news), 4, 128, seed=5), cache, news, 0.09, window=window, reading=allowed(fmt, reading))
 
 
 @pytest.mark.parametrize("fmt", [E4M3, dict(bits=8), dict(bits=4)])
@@ -221,7 +226,7 @@ def test_bad_blocks_of_codes_are_skipped(fmt, dims, reading):
     q = randn(350, 4, dims[0], seed=10)
     tables = cache.tables.clone()
     tables[0, 3], tables[1, 0], tables[1, 5] = -1, 10 ** 6, cache.pools[0].shape[0]
-    got, err = run(q, cache, news, 0.09, tables=tables, reading=reading)
+    got, err = run(q, cache, news, 0.09, tables=tables, reading=allowed(fmt, reading))
     assert err == 1
     gone = {0: [3], 1: [0, 5]}
     ref, tol = reference(q, cache, news, 0.09, hidden=lambda b: torch.tensor([t // 32 in gone[b] for t in range(512)], device=DEV))
@@ -238,6 +243,40 @@ def test_block_scales_of_zero_and_far_apart(reading):
         cache.values[which][at] *= scale / cache.planes[name][at].double()[:, None, None]
         cache.planes[name][at] = scale
     check(randn(300, 4, 128, seed=14), cache, [300], 0.09, reading=reading)
+
+
+@pytest.mark.parametrize("fmt", [dict(), E4M3, dict(bits=8), dict(bits=4)])
+@pytest.mark.parametrize("D", [128, 256])
+def test_error_beside_the_outputs_own_rounding(fmt, D):
+    """Root mean square over the output: bf16 weights cost as much as the output's rounding to bf16 does (independent, so
+    sqrt(2) of it, with a tenth for the sample); affine pages, whose values have more bits, get fp16 and next to nothing."""
+    lens, news = [2000, 700], [300, 200]
+    cache = Cache(lens, 2, D, D, 32, fmt, seed=2)
+    q = randn(500, 8, D, seed=15)
+    got, _ = run(q, cache, news, 1 / math.sqrt(D))
+    ref, _ = reference(q, cache, news, 1 / math.sqrt(D))
+    own = (ref.to(torch.bfloat16).double() - ref).norm()
+    assert (got.double() - ref).norm() <= (1.1 if fmt.get("bits") in (4, 8) and fmt is not E4M3 else 1.1 * math.sqrt(2)) * own
+
+
+@pytest.mark.parametrize("key,value,query", [(1e-6, 1e-6, 1.0), (1e5, 1e5, 1e-5), (1e-20, 1e20, 1e20), (1.0, 0.0, 1.0),
+                                             (0.0, 1.0, 1.0), (1.0, 1.0, 0.0)])
+def test_affine_pages_of_any_size(key, value, query):
+    """Values far beyond and below fp16's range, per sequence and head: powers of two bring them in."""
+    lens, news = [300, 50], [120, 50]
+    cache = Cache(lens, 2, 128, 128, 32, dict(bits=8))
+    for name, by in (("k", key), ("v", value)):
+        for plane in ("_scales", "_biases"):
+            t = cache.planes[name + plane]
+            ratio = (t.float() * by).to(torch.bfloat16)
+            blocks = cache.tables[0, :10].long()  # the first sequence's alone
+            t[blocks] = ratio[blocks]
+        which = 0 if name == "k" else 1
+        pool = cache.pools[which].view(torch.uint8).double().unflatten(-1, (-1, 64))
+        s, z = cache.planes[name + "_scales"].double(), cache.planes[name + "_biases"].double()
+        cache.values[which] = (pool * s[..., None] + z[..., None]).flatten(-2)
+    q = (randn(170, 4, 128, seed=16).float() * query).to(torch.bfloat16)
+    check(q, cache, news, 0.09)
 
 
 def test_rising_maxima_are_followed():
@@ -387,6 +426,6 @@ def test_refusals():
                 dict(v_pool=cache.pools[1][:2]), dict(block_tables=cache.tables.long()), dict(window=-1), dict(splits=-1),
                 dict(splits=65), dict(scale=math.nan), dict(scale=math.inf), dict(out=q[:49]), dict(out=q.float()),
                 dict(q=q[:, :1].expand(50, 4, 128)), dict(splits=2, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
-                dict(bits=8), dict(q=q.transpose(1, 2)), dict(q=randn(50, 130 * 2, 128))):
+                dict(bits=8), dict(reading=3), dict(q=q.transpose(1, 2)), dict(q=randn(50, 130 * 2, 128))):
         with pytest.raises((TypeError, ValueError, pkv.PkvError)):
             pkv.paged_prefill_attention(**{**good, **bad})
