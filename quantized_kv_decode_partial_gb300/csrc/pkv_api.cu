@@ -1285,7 +1285,8 @@ int check_prefill(const pkv_pool_layout* L, const pkv_prefill_params* P) {
       P->splits < 0 || P->splits > 64 || P->reading < PKV_READING_AUTO || P->reading > PKV_READING_VALUES)
     return PKV_ERR_BAD_PARAMS;
   if (P->num_q_heads <= 0 || P->num_q_heads % L->num_kv_heads) return PKV_ERR_BAD_PARAMS;
-  if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
+  // rows of a last tile are counted in int too
+  if (static_cast<long long>(P->max_blocks_per_seq) * L->block_size >= (1ll << 31) - 256) return PKV_ERR_BAD_PARAMS;
   if (static_cast<long long>(P->num_tokens) * P->num_q_heads >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   if (P->num_q_heads / L->num_kv_heads > 64) return PKV_ERR_UNSUPPORTED_SHAPE;
   if (!prefill_info(L, L->bits != 16).exists) return PKV_ERR_UNSUPPORTED_SHAPE;

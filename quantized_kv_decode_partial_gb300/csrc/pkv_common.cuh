@@ -181,10 +181,13 @@ struct PrefillValues {
   __host__ __device__ __forceinline__ int base(int b, int start) const {
     return (by_tokens ? start / kValueRows : 0) + b * per_seq;
   }
-  // The first row that a sequence's queries can see, rounded down to a block's.
-  static __host__ __device__ __forceinline__ int first_row(int len, int n, int window) {
+  // The first row that a sequence's queries can see, and that rounded down to a block's.
+  static __host__ __device__ __forceinline__ int lowest(int len, int n, int window) {
     const int lo = window > 0 ? len - n - window + 1 : 0;
-    return lo > 0 ? lo / kValueRows * kValueRows : 0;
+    return lo > 0 ? lo : 0;
+  }
+  static __host__ __device__ __forceinline__ int first_row(int len, int n, int window) {
+    return lowest(len, n, window) / kValueRows * kValueRows;
   }
 };
 

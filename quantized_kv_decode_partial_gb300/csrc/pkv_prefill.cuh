@@ -108,7 +108,7 @@ __device__ __forceinline__ PrefillUnit prefill_unit(const PrefillParams& p, int 
   u.position = u.valid ? static_cast<int>(len - n + first) : 0;
   u.table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   u.dense = u.valid ? p.values.base(b, start) - p.values.first_row(len, static_cast<int>(n), p.window) / kValueRows : 0;
-  if ((!starts_ok || (u.live && !u.valid)) && threadIdx.x == 0 && p.error_flag)
+  if (u.live && !u.valid && threadIdx.x == 0 && p.error_flag)
     atomicOr(p.error_flag, kDevErrBadSeqLen);
   return u;
 }
@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   wait_for_prerequisite_grids();
+  if (blockIdx.x == 0 && warp == 0) check_starts(p.query_starts, p.num_seqs, p.tokens, p.error_flag);
   const int unit_tokens = T::kQ * p.tile_tokens;
   const PrefillUnit u = prefill_unit(p, unit_tokens);
   if (!u.live) return;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   // Keys that any row of the unit sees: [lo, hi).
   const int hi = u.position + u.tokens;
   const int lo = p.window > 0 ? max(0, u.position - p.window + 1) : 0;
-  const int tile_lo = lo / KT, tile_n = (hi + KT - 1) / KT - tile_lo;
+  const int tile_lo = lo / KT, tile_n = (hi - 1) / KT + 1 - tile_lo;
   const int t0 = tile_lo + static_cast<int>(static_cast<long long>(tile_n) * u.split / p.splits);
   const int nt = u.valid ? tile_lo + static_cast<int>(static_cast<long long>(tile_n) * (u.split + 1) / p.splits) - t0 : 0;
 

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(1024) pkv_prefill_range_kernel(const __grid_co
   float m = 0.f;
   if (seen) {
 #pragma unroll 4
-    for (int t = p.values.first_row(len, static_cast<int>(n), p.window) + threadIdx.x; t < len; t += 1024) {
+    for (int t = p.values.lowest(len, static_cast<int>(n), p.window) + threadIdx.x; t < len; t += 1024) {
       const int blk = t / p.block_size;
       const int phys = table[blk];
       if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;

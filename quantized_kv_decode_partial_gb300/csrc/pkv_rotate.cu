@@ -346,10 +346,7 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
   }
   const long long t = slot - (static_cast<long long>(start / bs) + 2ll * seq);
   if (start < 0 || n <= 0 || t < 0 || static_cast<long long>(start) + n > p.tokens) {
-    // starts that fall or leave the tokens: nothing is written
-    if (threadIdx.x == 0 && p.error_flag && (n < 0 || start < 0 || static_cast<long long>(start) + n > p.tokens))
-      atomicOr(p.error_flag, kDevErrBadSeqLen);
-    return;
+    return;  // (starts that fall or leave the tokens are flagged elsewhere)
   }
   const long long end = static_cast<long long>(len) + n;
   if (len < 0 || end > static_cast<long long>(p.max_blocks) * bs) {
@@ -536,6 +533,8 @@ __global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 6) pkv
     token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, reinterpret_cast<__nv_bfloat16*>(mine), prepare);
   }
   prepare();  // a warp without a token
+  if (FMT != kPlain && p.tokens_per_seq == 0 && blockIdx.x == 0 && warp == 0)
+    check_starts(p.query_starts, p.num_seqs, p.tokens, p.error_flag);
 }
 
 // Warps per token: as many as fill the GPU.

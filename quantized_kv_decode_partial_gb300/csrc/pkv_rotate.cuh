@@ -233,4 +233,14 @@ __device__ __forceinline__ int find_last(int n, long long x, const Key& key) {
   return lo;
 }
 
+// Packed tokens' starts, looked through by one warp: flags those that fall or leave [0, tokens].
+__device__ __forceinline__ void check_starts(const int32_t* starts, int num_seqs, int tokens, int32_t* error_flag) {
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i <= num_seqs; i += 32) {
+    const int s = starts[i];
+    bad = bad || s < 0 || s > tokens || (i > 0 && s < starts[i - 1]);
+  }
+  if (bad && error_flag) atomicOr(error_flag, kDevErrBadSeqLen);
+}
+
 }  // namespace pkv

@@ -96,6 +96,7 @@ def test_splits_fill_the_gpu_and_can_be_set(lib):
     (dict(), dict(num_tokens=-1), B.PKV_ERR_BAD_PARAMS), (dict(), dict(num_q_heads=3), B.PKV_ERR_BAD_PARAMS),
     (dict(), dict(num_q_heads=0), B.PKV_ERR_BAD_PARAMS), (dict(), dict(num_q_heads=130), B.PKV_ERR_UNSUPPORTED_SHAPE),
     (dict(), dict(max_blocks_per_seq=0), B.PKV_ERR_BAD_PARAMS), (dict(), dict(max_blocks_per_seq=1 << 26), B.PKV_ERR_BAD_PARAMS),
+    (dict(), dict(max_blocks_per_seq=(1 << 26) - 8), B.PKV_ERR_BAD_PARAMS),
     (dict(), dict(window=-1), B.PKV_ERR_BAD_PARAMS), (dict(), dict(splits=-1), B.PKV_ERR_BAD_PARAMS),
     (dict(), dict(splits=65), B.PKV_ERR_BAD_PARAMS), (dict(), dict(reading=3), B.PKV_ERR_BAD_PARAMS), (dict(), dict(reading=-1), B.PKV_ERR_BAD_PARAMS), (dict(), dict(num_tokens=1 << 28), B.PKV_ERR_BAD_PARAMS),
 ])

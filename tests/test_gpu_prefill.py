@@ -171,6 +171,24 @@ def test_windows(window, dk, dv, splits):
     check(randn(sum(news), 4, dk, seed=5), Cache(lens, 2, dk, dv, 32, dict()), news, 0.09, window=window, splits=splits)
 
 
+@pytest.mark.parametrize("fmt", [dict(), E4M3, dict(bits=8)])
+def test_blocks_below_the_window_may_be_gone(fmt):
+    """Their table entries are none, or those of blocks whose scales are not numbers."""
+    lens, news, window = [900, 300], [20, 140], 100
+    cache = Cache(lens, 2, 128, 128, 32, fmt)
+    q = randn(160, 4, 128, seed=17)
+    ref, tol = reference(q, cache, news, 0.09, window)
+    spare = (set(range(cache.pools[0].shape[0])) - set(cache.tables.flatten().tolist())).pop()
+    for t in cache.planes.values():
+        t[spare] = math.nan
+    tables = cache.tables.clone()
+    tables[0, :(900 - 20 - window + 1) // 32 - 1] = -1
+    tables[0, (900 - 20 - window + 1) // 32 - 1] = spare
+    tables[1, :(300 - 140 - window + 1) // 32] = spare
+    got, err = run(q, cache, news, 0.09, tables=tables, window=window)
+    assert err == 0 and bool(((got.double() - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.09, 1.0, 3.0, 1e-8])
 def test_scales(scale):
     lens, news = [300, 200], [300, 7]
@@ -365,9 +383,9 @@ def test_bad_lengths_and_starts_over_codes(reading):
 
 
 def test_starts_that_fall_or_leave_the_tokens_touch_nothing_else():
-    cache = Cache([200, 150], 2, 128, 128, 32, dict())
     q = randn(100, 4, 128, seed=11)
-    for starts in ([0, 60, 40], [0, 50, 101], [-3, 50, 100], [0, 2 ** 31 - 1, 100], [100, 50, 0]):
+    for starts in ([0, 60, 40], [0, 50, 101], [-3, 50, 100], [0, 2 ** 31 - 1, 100], [100, 50, 0], [0, 100, 50, 100]):
+        cache = Cache([200, 150, 90][:len(starts) - 1], 2, 128, 128, 32, dict())
         for splits in (1, 2):
             out = torch.full((102, 4, 128), 5.0, dtype=torch.bfloat16, device=DEV)
             _, err = run(q, cache, [0, 0], 0.09, starts=starts, out=out[1:101], splits=splits)

@@ -269,7 +269,7 @@ def test_bad_blocks_lengths_and_starts(fmt):
         assert all(torch.equal(raw(m[[1, 2, 3, 5]]), raw(b[[1, 2, 3, 5]])) for m, b in zip(mine, before))
         assert (out[9:] == 7.0).all() and not (out[:9] == 7.0).all(-1).any()
     for starts in ([0, 5, 3, 9, 12], [0, 3, 6, 9, 13], [-2, 3, 6, 9, 12], [0, 0, 0, 0, 2 ** 31 - 1]):
-        call([0, 0, 0, 0], starts)  # whatever they say, nothing outside the tokens is touched
+        assert call([0, 0, 0, 0], starts)[0] & 2  # and whatever they say, nothing outside the tokens is touched
     err, out, mine = call([0, 0, 0, 0], [12, 12, 12, 12, 12])
     assert err == 0 and (out == 7.0).all() and all(torch.equal(raw(m), raw(b)) for m, b in zip(mine, before))
 
