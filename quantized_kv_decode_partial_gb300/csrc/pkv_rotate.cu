@@ -26,7 +26,8 @@ namespace {
 constexpr int kPlain = 0;  // FMT of the kernel without the write
 
 constexpr int kRing = 4;        // slots (a warp's rows at once) in flight
-constexpr int kSlotBytes = 512;
+constexpr int kSlotBytes = 1024;
+constexpr int kWarpBytes = kRing * kSlotBytes + 128 * 8;  // ring and a token's angles
 constexpr int kBlockHold = 8;   // row batches a lane of the block path keeps in registers
 constexpr int kTableBytes = 36 << 10;  // of the 48 KB that a launch may have unasked
 
@@ -143,49 +144,68 @@ __device__ __forceinline__ void lane_angles(const RotateParams& p, const RotateT
 }
 
 // One warp: share g of token t's rows. With pages, D and DV are theirs.
+// One warp: cos and sin of every pair at token t, in shared memory.
+template <int D>
+__device__ __forceinline__ void token_angles(const RotateParams& p, const RotateTables<D>& tab, int t, int cache_place,
+                                             float2* angles) {
+  const int half = p.turn.rot / 2;
+  for (int f = threadIdx.x & 31; f < half; f += 32) {
+    const int pos = p.positions ? p.positions[static_cast<long long>(tab.axis[f]) * p.tokens + t] : cache_place;
+    float2 v;
+    turn_at(tab.step[f], pos, p.turn.amplitude, v.x, v.y);
+    angles[f] = v;
+  }
+  __syncwarp();
+}
+
 // prepare(): called once the first rows are asked for.
 template <int D, int DV, int FMT, bool SIMPLE, typename Prepare>
 __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTables<D>& tab, int t, int g,
-                                           unsigned char* ring_smem, __nv_bfloat16* stage, const Prepare& prepare) {
+                                           unsigned char* ring_smem, float2* angles, __nv_bfloat16* stage, const Prepare& prepare) {
   using L = RowLanes<D>;
+  constexpr int kRows = L::kRows2;
   const int lane = threadIdx.x & 31;
-  const int sub = lane / L::kLanes, u = lane % L::kLanes;
-  const bool used = L::kUsed == L::kLanes || u < L::kUsed;
-  int off0, off1;
-  run_offsets(p.turn, u, off0, off1);
+  const int sub = lane / L::kHalf, u = lane % L::kHalf;
+  // the lane's units u and u + kHalf: whether they hold values, and where their runs are
+  const bool used[2] = {true, L::kUsed == L::kLanes || u + L::kHalf < L::kUsed};
+  int off0[2], off1[2];
+  run_offsets(p.turn, u, off0[0], off1[0]);
+  run_offsets(p.turn, u + L::kHalf, off0[1], off1[1]);
   const int HQ = p.num_q_heads, HK = p.num_kv_heads;
   // Keys that leave through registers follow the queries: slots of kRows rows, this share's every groups-th.
   constexpr bool kKeysHere = FMT == kPlain || FMT == 16;
-  const int q_slots = (HQ + L::kRows - 1) / L::kRows, k_slots = kKeysHere ? (HK + L::kRows - 1) / L::kRows : 0;
+  const int q_slots = (HQ + kRows - 1) / kRows, k_slots = kKeysHere ? (HK + kRows - 1) / kRows : 0;
   const int slots = q_slots + k_slots, G = p.groups;
   const RowAt row = row_at(p, t);
   const __nv_bfloat16* k_src = (FMT == kPlain && HK == 0) ? nullptr : rows_of(p.k, row);
 
   // Rows come through a ring in shared memory, kRing slots ahead: loads in flight without registers. Rows that do not
   // exist are asked for with no bytes, which leaves zeros.
-  const uint32_t ring = smem_addr(ring_smem) + lane * 16;
-  auto key_row = [&](const __nv_bfloat16* base, long long head, int s) { return base + ((s - q_slots) * L::kRows + sub) * head; };
+  const uint32_t ring = smem_addr(ring_smem) + sub * (L::kLanes * 16);
+  auto key_row = [&](const __nv_bfloat16* base, long long head, int s) { return base + ((s - q_slots) * kRows + sub) * head; };
   int ask_s = g;
   const __nv_bfloat16* ask_at =
-      (g < q_slots ? rows_of(p.q, row) + (g * L::kRows + sub) * p.q.head : key_row(k_src, p.k.head, g)) + u * 8;
-  long long ask_step = (g < q_slots ? p.q.head : p.k.head) * (G * L::kRows);
-  int ask_left = (g < q_slots ? HQ : q_slots * L::kRows + HK) - (g * L::kRows + sub);
+      (g < q_slots ? rows_of(p.q, row) + (g * kRows + sub) * p.q.head : key_row(k_src, p.k.head, g)) + u * 8;
+  long long ask_step = (g < q_slots ? p.q.head : p.k.head) * (G * kRows);
+  int ask_left = (g < q_slots ? HQ : q_slots * kRows + HK) - (g * kRows + sub);
   auto ask = [&](uint32_t place) {
     if (ask_s >= slots) {
       cp_async_commit();
       return;
     }
-    const bool there = used && ask_left > 0;
-    cp_async_16_or_zeros(ring + place, there ? ask_at : p.q.data, there);
+    const bool there = ask_left > 0;
+    const uint32_t to = ring + place + u * 16;
+    cp_async_16_or_zeros(to, there ? ask_at : p.q.data, there);
+    cp_async_16_or_zeros(to + L::kHalf * 16, there && used[1] ? ask_at + L::kHalf * 8 : p.q.data, there && used[1]);
     cp_async_commit();
     const bool was_query = ask_s < q_slots;
     ask_s += G;
-    ask_left -= G * L::kRows;
+    ask_left -= G * kRows;
     ask_at += ask_step;
     if (kKeysHere && was_query && ask_s >= q_slots) {
       ask_at = key_row(k_src, p.k.head, ask_s) + u * 8;
-      ask_step = p.k.head * (G * L::kRows);
-      ask_left = HK - ((ask_s - q_slots) * L::kRows + sub);
+      ask_step = p.k.head * (G * kRows);
+      ask_left = HK - ((ask_s - q_slots) * kRows + sub);
     }
   };
 #pragma unroll 1
@@ -218,12 +238,26 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
       }
     }
   }
-  const bool turned = SIMPLE || u * 8 < p.turn.rot, adjacent = p.turn.adjacent != 0;
-  float w[8], cs[4] = {0.f, 0.f, 0.f, 0.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-  if (turned && used) lane_angles(p, tab, u, t, cache_place, cs, sn);
+  const bool adjacent = p.turn.adjacent != 0;
+  const bool turned[2] = {SIMPLE || u * 8 < p.turn.rot, SIMPLE || (u + L::kHalf) * 8 < p.turn.rot};
+  token_angles(p, tab, t, cache_place, angles);
   bool key = g >= q_slots;
-  lane_weights(tab, key, used, off0, off1, w);
-  LaneTurn turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
+  LaneTurn turn[2];
+  auto make_turns = [&] {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float w[8], cs[4] = {0.f, 0.f, 0.f, 0.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+      lane_weights(tab, key, used[i], off0[i], off1[i], w);
+      if (turned[i] && used[i]) {
+        const float4* at4 = reinterpret_cast<const float4*>(angles + (u + i * L::kHalf) * 4);
+        const float4 x = at4[0], y = at4[1];
+        cs[0] = x.x, sn[0] = x.y, cs[1] = x.z, sn[1] = x.w;
+        cs[2] = y.x, sn[2] = y.y, cs[3] = y.z, sn[3] = y.w;
+      }
+      turn[i] = make_turn<SIMPLE>(w, cs, sn, turned[i], adjacent);
+    }
+  };
+  make_turns();
 
   auto pool_row = [&](int h) { return (static_cast<size_t>(phys) * HK + h) * p.block_size + offset; };
   __nv_bfloat16* k_to = nullptr;
@@ -235,10 +269,10 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
     if (phys >= 0) k_to = p.dst.k_pool_bf16 + pool_row(0) * D;
     k_head = static_cast<long long>(p.block_size) * D;
   }
-  __nv_bfloat16* to = key ? (k_to ? k_to + ((g - q_slots) * L::kRows + sub) * k_head : nullptr)
-                          : rows_of(p.q_out, row) + (g * L::kRows + sub) * p.q_out.head;
-  long long to_step = (key ? k_head : p.q_out.head) * (G * L::kRows);
-  int left = (key ? q_slots * L::kRows + HK : HQ) - (g * L::kRows + sub);  // rows of this kind from the lane's on
+  __nv_bfloat16* to = key ? (k_to ? k_to + ((g - q_slots) * kRows + sub) * k_head : nullptr)
+                          : rows_of(p.q_out, row) + (g * kRows + sub) * p.q_out.head;
+  long long to_step = (key ? k_head : p.q_out.head) * (G * kRows);
+  int left = (key ? q_slots * kRows + HK : HQ) - (g * kRows + sub);  // rows of this kind from the lane's on
   bool normed = (key ? p.k_weight : p.q_weight) != nullptr;
   uint32_t place = 0;
 #pragma unroll 1
@@ -246,30 +280,38 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
     if (kKeysHere && !key && s >= q_slots) {  // from here on keys
       if (!k_to) break;
       key = true;
-      lane_weights(tab, true, used, off0, off1, w);
-      turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
-      to = k_to + ((s - q_slots) * L::kRows + sub) * k_head;
-      to_step = k_head * (G * L::kRows);
-      left = HK - ((s - q_slots) * L::kRows + sub);
+      make_turns();
+      to = k_to + ((s - q_slots) * kRows + sub) * k_head;
+      to_step = k_head * (G * kRows);
+      left = HK - ((s - q_slots) * kRows + sub);
       normed = p.k_weight != nullptr;
     }
     cp_async_wait<kRing - 1>();
     __syncwarp();  // every lane's part of the slot is there
-    const uint32_t from = ring + place - u * 16;
-    uint2 a = ld_shared_v2(from + off0 * 2), b = ld_shared_v2(from + off1 * 2);
-    if (!used) a = b = make_uint2(0u, 0u);
+    uint2 a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = ld_shared_v2(ring + place + off0[i] * 2);
+      b[i] = ld_shared_v2(ring + place + off1[i] * 2);
+      if (!used[i]) a[i] = b[i] = make_uint2(0u, 0u);
+    }
     __syncwarp();  // every lane has read the slot
     ask(place);
     place = (place + kSlotBytes) & (kRing * kSlotBytes - 1);
-    turn_row<D, SIMPLE>(a, b, normed, p.eps, turned, adjacent, turn);
-    if (used && left > 0 && to) {
-      *reinterpret_cast<uint2*>(to + off0) = a;
-      *reinterpret_cast<uint2*>(to + off1) = b;
+    turn_row2<D, SIMPLE>(a, b, normed, p.eps, turned, adjacent, turn);
+    if (left > 0 && to) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!used[i]) continue;
+        *reinterpret_cast<uint2*>(to + off0[i]) = a[i];
+        *reinterpret_cast<uint2*>(to + off1[i]) = b[i];
+      }
     }
     to += to_step;
-    left -= G * L::kRows;
+    left -= G * kRows;
   }
   cp_async_wait<0>();
+  __syncwarp();  // the angles are the next token's
 
   if constexpr (FMT == 16) {
     if (phys < 0) return;
@@ -283,24 +325,30 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
   if constexpr (FMT == 4 || FMT == 8) {
     if (phys < 0) return;
     const __nv_bfloat16* v_src = rows_of(p.v, row);
-    lane_weights(tab, true, used, off0, off1, w);
-    turn = make_turn<SIMPLE>(w, cs, sn, turned, adjacent);
-    for (int h0 = g * L::kRows; h0 < HK; h0 += G * L::kRows) {
+    key = true;
+    make_turns();
+    for (int h0 = g * kRows; h0 < HK; h0 += G * kRows) {
       const int h = h0 + sub;
-      uint2 x = make_uint2(0u, 0u), y = x;
-      if (used && h < HK) {
-        x = ld_nc_keep_v2(k_src + h * p.k.head + off0);
-        y = ld_nc_keep_v2(k_src + h * p.k.head + off1);
+      uint2 a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = b[i] = make_uint2(0u, 0u);
+        if (used[i] && h < HK) {
+          a[i] = ld_nc_keep_v2(k_src + h * p.k.head + off0[i]);
+          b[i] = ld_nc_keep_v2(k_src + h * p.k.head + off1[i]);
+        }
       }
-      turn_row<D, SIMPLE>(x, y, p.k_weight != nullptr, p.eps, turned, adjacent, turn);
+      turn_row2<D, SIMPLE>(a, b, p.k_weight != nullptr, p.eps, turned, adjacent, turn);
       __syncwarp();  // the rows staged before have been read
-      if (used) {
-        *reinterpret_cast<uint2*>(stage + sub * D + off0) = x;
-        *reinterpret_cast<uint2*>(stage + sub * D + off1) = y;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!used[i]) continue;
+        *reinterpret_cast<uint2*>(stage + sub * D + off0[i]) = a[i];
+        *reinterpret_cast<uint2*>(stage + sub * D + off1[i]) = b[i];
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < L::kRows; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         if (h0 + i >= HK) break;
         const size_t to_row = pool_row(h0 + i);
         append_plane<FMT, D>(stage + i * D, nullptr, p.dst.k_pool_words, p.dst.k_scales, p.dst.k_biases, to_row, lane);
@@ -308,7 +356,7 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
                               to_row, lane);
       }
     }
-    __syncwarp();  // the stage is the next token's ring
+    __syncwarp();  // the stage is the next token's ring, the angles its angles
   }
 }
 
@@ -495,7 +543,7 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
 }
 
 template <int D, int DV, int FMT, bool SIMPLE>
-__global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 6) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 5) pkv_rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ RotateTables<D> tab;
   __shared__ uint32_t red[kWarps<FMT>];
@@ -525,12 +573,13 @@ __global__ void __launch_bounds__(kWarps<FMT> * 32, FMT == kFmtE4m3 ? 3 : 6) pkv
     __syncthreads();
     ready = true;
   };
-  unsigned char* mine = smem + warp * kRing * kSlotBytes;  // a staged row of the affine write takes the ring's place
+  unsigned char* mine = smem + warp * kWarpBytes;  // staged rows of the affine write take the ring's place
+  float2* angles = reinterpret_cast<float2*>(mine + kRing * kSlotBytes);
   const long long units = static_cast<long long>(p.tokens) * p.groups, step = static_cast<long long>(p.q_ctas) * kWarps<FMT>;
   for (long long unit = static_cast<long long>(blockIdx.x) * kWarps<FMT> + warp; unit < units; unit += step) {
     const int t = p.groups == 1 ? static_cast<int>(unit) : static_cast<int>(unit / p.groups);
     const int g = static_cast<int>(unit - static_cast<long long>(t) * p.groups);
-    token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, reinterpret_cast<__nv_bfloat16*>(mine), prepare);
+    token_rows<D, DV, FMT, SIMPLE>(p, tab, t, g, mine, angles, reinterpret_cast<__nv_bfloat16*>(mine), prepare);
   }
   prepare();  // a warp without a token
   if (FMT != kPlain && p.tokens_per_seq == 0 && blockIdx.x == 0 && warp == 0)
@@ -550,14 +599,14 @@ template <int D, int DV, int FMT>
 cudaError_t launch_of(RotateParams p, int sm_count, cudaStream_t stream) {
   using L = RowLanes<D>;
   constexpr bool kKeysHere = FMT == kPlain || FMT == 16;
-  const int slots = (p.num_q_heads + L::kRows - 1) / L::kRows + (kKeysHere ? (p.num_kv_heads + L::kRows - 1) / L::kRows : 0);
+  const int slots = (p.num_q_heads + L::kRows2 - 1) / L::kRows2 + (kKeysHere ? (p.num_kv_heads + L::kRows2 - 1) / L::kRows2 : 0);
   p.groups = token_groups(p.tokens, slots, sm_count);
   // One wave of CTAs, each of which fills its tables once and takes many tokens.
-  const long long most_ctas = (FMT == kFmtE4m3 ? 3ll : 6ll) * sm_count;
+  const long long most_ctas = (FMT == kFmtE4m3 ? 3ll : 5ll) * sm_count;
   long long ctas = (static_cast<long long>(p.tokens) * p.groups + kWarps<FMT> - 1) / kWarps<FMT>;
   ctas = std::min(ctas, most_ctas);
   p.q_ctas = static_cast<int>(ctas);
-  size_t smem = kWarps<FMT> * kRing * kSlotBytes;
+  size_t smem = kWarps<FMT> * kWarpBytes;
   if (FMT == kFmtE4m3) {
     const int most = p.tokens_per_seq > 0 ? p.tokens_per_seq : p.tokens;
     const int held = most < p.block_size ? most : p.block_size;  // new rows of a block

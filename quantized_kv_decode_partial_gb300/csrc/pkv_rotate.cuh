@@ -1,11 +1,10 @@
 // One head's row on its way to attention: RMS norm over the head dim, weight, rotation of
 // pairs of values by the row's position, one rounding to bf16.
 //
-// Lanes. DPL = 8 values per lane, so a row takes D / 8 lanes (8 at D = 64, 16 at 128, 32 at
-// 256, 24 of 32 at 192) and a warp 32 / lanes rows at once. A lane holds both members of its
-// pairs, whatever the pairing, so rotating needs no exchange: two runs of four values, at u*4
-// and R/2 + u*4 of the rotated part (halves), or at u*8 and u*8 + 4 (adjacent pairs and the
-// part that does not turn). Each run is one 8-byte load; a row's runs fill whole sectors.
+// Lanes. A unit is eight values of a row, D / 8 of them in all, which hold both members of their pairs, whatever the
+// pairing, so that rotating needs no exchange: two runs of four values, at u*4 and R/2 + u*4 of the rotated part
+// (halves), or at u*8 and u*8 + 4 (adjacent pairs and the part that does not turn). Each run is one 8-byte access; a row's
+// runs fill whole sectors. A lane has one unit of its row, or two, kHalf apart.
 //
 // Angles. position * frequency is reduced in fixed point: a frequency becomes the fraction of
 // a turn it makes per position, times 2^64, and the product with the position wraps at whole
@@ -23,6 +22,7 @@ struct RowLanes {
   static constexpr int kLanes = D == 64 ? 8 : D == 128 ? 16 : 32;  // lanes a row takes, a power of two
   static constexpr int kUsed = D / 8;                              // of which hold values
   static constexpr int kRows = 32 / kLanes;                        // rows a warp takes at once
+  static constexpr int kHalf = kLanes / 2, kRows2 = 2 * kRows;     // with two units per lane
 };
 
 // 2^64 times the fraction of a turn that an angle of f makes (f mod 2 pi).
@@ -165,55 +165,95 @@ __device__ __forceinline__ LaneTurn make_turn(const float (&w)[8], const float (
   return t;
 }
 
-// Norm and rotation of a lane's eight values (a: the run at off0, b: at off1). Every lane of the warp takes part;
-// lanes without values pass zeros.
-template <int D, bool SIMPLE>
-__device__ __forceinline__ void turn_row(uint2& a, uint2& b, bool normed, float eps, bool turned, bool adjacent,
-                                         const LaneTurn& t) {
-  uint64_t x[4];
-  const uint32_t v[4] = {a.x, a.y, b.x, b.y};
+// Eight values of a row: a is the run at off0, b the run at off1.
+struct Unit {
+  uint64_t x[4];  // as f32 pairs
+  __device__ __forceinline__ Unit(const uint2& a, const uint2& b) {
+    const uint32_t v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
-  float r = 1.f;
-  if (normed) {
+    for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ float squares() const {
     uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) s2 = fma2(x[i], x[i], s2);
     float s0, s1;
     unpair(s2, s0, s1);
-    float ss = __fadd_rn(s0, s1);
-#pragma unroll
-    for (int off = 1; off < RowLanes<D>::kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    r = rsqrtf(__fmaf_rn(ss, 1.f / D, eps));
+    return __fadd_rn(s0, s1);
   }
-  uint64_t y[4];
-  if (!SIMPLE && !turned) {
+  // Rotation and weights, times r where there is a norm; back to bf16.
+  template <bool SIMPLE>
+  __device__ __forceinline__ void turn(bool normed, float r, bool turned, bool adjacent, const LaneTurn& t, uint2& a,
+                                       uint2& b) const {
+    uint64_t y[4];
+    if (!SIMPLE && !turned) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2(x[i], t.own[i]);
-  } else if (!SIMPLE && adjacent) {
+      for (int i = 0; i < 4; ++i) y[i] = mul2(x[i], t.own[i]);
+    } else if (!SIMPLE && adjacent) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpair(x[i], lo, hi);
+        y[i] = fma2(x[i], t.own[i], mul2(pair(hi, lo), t.other[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], t.own[i], mul2(x[i ^ 2], t.other[i]));
+    }
+    if (normed) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], pair(r, r));
+    }
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float lo, hi;
-      unpair(x[i], lo, hi);
-      y[i] = fma2(x[i], t.own[i], mul2(pair(hi, lo), t.other[i]));
+      unpair(y[i], lo, hi);
+      w[i] = pack_bf16x2(lo, hi);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], t.own[i], mul2(x[i ^ 2], t.other[i]));
+    a = make_uint2(w[0], w[1]);
+    b = make_uint2(w[2], w[3]);
   }
+};
+
+__device__ __forceinline__ float inverse_rms(float squares, int dim, float eps) {
+  return rsqrtf(__fmaf_rn(squares, 1.f / dim, eps));
+}
+
+// Norm and rotation of a row that has one unit in each of RowLanes<D>::kLanes lanes. Every lane of the warp takes
+// part; lanes without values pass zeros.
+template <int D, bool SIMPLE>
+__device__ __forceinline__ void turn_row(uint2& a, uint2& b, bool normed, float eps, bool turned, bool adjacent,
+                                         const LaneTurn& t) {
+  const Unit v(a, b);
+  float r = 1.f;
   if (normed) {
+    float ss = v.squares();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], pair(r, r));
+    for (int off = 1; off < RowLanes<D>::kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    r = inverse_rms(ss, D, eps);
   }
-  uint32_t w[4];
+  v.turn<SIMPLE>(normed, r, turned, adjacent, t, a, b);
+}
+
+// The same with two units per lane, u and u + kHalf, for half as many lanes and as much of everything that is done once
+// per row and lane. The squares are added up in the same order.
+template <int D, bool SIMPLE>
+__device__ __forceinline__ void turn_row2(uint2 (&a)[2], uint2 (&b)[2], bool normed, float eps, const bool (&turned)[2],
+                                          bool adjacent, const LaneTurn (&t)[2]) {
+  const Unit v0(a[0], b[0]), v1(a[1], b[1]);
+  float r = 1.f;
+  if (normed) {
+    float s0 = v0.squares(), s1 = v1.squares();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    unpair(y[i], lo, hi);
-    w[i] = pack_bf16x2(lo, hi);
+    for (int off = 1; off < RowLanes<D>::kLanes / 2; off <<= 1) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, off);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+    }
+    r = inverse_rms(s0 + s1, D, eps);
   }
-  a = make_uint2(w[0], w[1]);
-  b = make_uint2(w[2], w[3]);
+  v0.turn<SIMPLE>(normed, r, turned[0], adjacent, t[0], a[0], b[0]);
+  v1.turn<SIMPLE>(normed, r, turned[1], adjacent, t[1], a[1], b[1]);
 }
 
 // The last b in [0, n) with key(b) <= x, for keys that do not fall; 0 when there is none. Asked
