@@ -15,6 +15,12 @@
 //
 // Few query rows over long caches: the key tiles of each CTA's rows are split over `splits`
 // CTAs whose f32 states (O, m, l) are joined by a second kernel.
+//
+// Measured on a GB300: 8 prompts of 1025-8192 tokens, 8 KV heads of 4, 128 dims: 1.42 ms, 1305 TFLOP/s of products, 0.69 of what a
+// large library matrix product reaches alone; 2 chunks of 500-1024 tokens over 30011-60000 rows: 1394 TFLOP/s. The step is
+// bound by hand-overs between products and softmax (without any exponential, sum or maximum it takes 0.91 of its time)
+// and by the power limit, under which the SM clock settles near 1.5 of 2.07 GHz. Two threads per row with a barrier
+// between them took 1.14 times as long, weights handed over by halves 1.19 times. 37 tokens alone: 8.4 us.
 #pragma once
 
 #include "pkv_codes.cuh"
@@ -579,7 +585,8 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     float out_factor = 1.f;
     float m = -INFINITY;          // running maximum of the unscaled scores
     // c s - c m is rounded once, but c m before it: where that could be off by more than 2^-4 in a row of the warp,
-    // s - m comes first.
+    // s - m comes first. Only rows of the unit's tokens have a say in what their warp does: the others hold the next sequence's
+    // queries, or whatever was in shared memory, and no output may depend on them.
     bool far = false;
     uint64_t l[2] = {0ull, 0ull};  // sums of weights, two pairs
     const uint32_t o_at = tmem + lanes + T::kTmemO + q * DV;
@@ -656,17 +663,18 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
         }
         if (j == 0) m = row_max<KT>(s);
         uint64_t sums[2] = {l[0], l[1]};
-        if (j == 0) far = __any_sync(0xffffffffu, fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
+        if (j == 0) far = __any_sync(0xffffffffu, out.live && fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
         if (far) subtract<KT>(s, m);
         const float up = fmaxf(m, weights<KT, HALF>(s, c, far ? 0.f : m, sums, w) + (far && m > -INFINITY ? m : 0.f));
-        if (again || j == 0 || !__any_sync(0xffffffffu, (up - m) * c > 8.f || (m == -INFINITY && up > m))) {
+        if (again || j == 0 ||
+            !__any_sync(0xffffffffu, out.live && ((up - m) * c > 8.f || (m == -INFINITY && up > m)))) {
           l[0] = sums[0];
           l[1] = sums[1];
           break;
         }
         const float by = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
         m = up;
-        far = __any_sync(0xffffffffu, fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
+        far = __any_sync(0xffffffffu, out.live && fabsf(m) * c > 0x1p20f && fabsf(m) < INFINITY);
 #pragma unroll
         for (int n = 0; n < 2; ++n) l[n] = mul2(l[n], pair(by, by));
         ok = mbar_wait_close(o_done(q), (j - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns);
