@@ -11,6 +11,12 @@
 // one scale per block, which needs the largest of the block's new values before the first code
 // is written: there CTAs take (touched block, plane, a few KV heads), hold the rows in
 // registers between the two uses and share the block's angles through shared memory.
+//
+// Measured on a GB300, replayed graphs, against the bytes at the rate of a plain copy: 4 x 3001-5003 tokens, 28 + 4 heads
+// of 128 dims, three axes: 52 us, 0.82 (with one unit of eight values per lane and trip instead of two: 56; the first form, a
+// lane's values loaded when they were needed: 73). 2 x 4097-8191 tokens, 16 + 4 heads of 256 dims of which 64 turn: 57 us,
+// 0.80. bf16 pages, 8 x 1025-4099 tokens: 96 us, 0.82; e4m3 pages, 8 x 2001-8192 tokens: 203 us, 0.71, with the queries' and
+// the blocks' CTAs in one launch (in one each: 218). One token: 2.9 us; one of each of 64 sequences with its write: 4.3.
 #include <algorithm>
 #include <type_traits>
 
@@ -143,7 +149,6 @@ __device__ __forceinline__ void lane_angles(const RotateParams& p, const RotateT
   }
 }
 
-// One warp: share g of token t's rows. With pages, D and DV are theirs.
 // One warp: cos and sin of every pair at token t, in shared memory.
 template <int D>
 __device__ __forceinline__ void token_angles(const RotateParams& p, const RotateTables<D>& tab, int t, int cache_place,
@@ -158,7 +163,7 @@ __device__ __forceinline__ void token_angles(const RotateParams& p, const Rotate
   __syncwarp();
 }
 
-// prepare(): called once the first rows are asked for.
+// One warp: share g of token t's rows. With pages, D and DV are theirs. prepare(): called once the first rows are asked for.
 template <int D, int DV, int FMT, bool SIMPLE, typename Prepare>
 __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTables<D>& tab, int t, int g,
                                            unsigned char* ring_smem, float2* angles, __nv_bfloat16* stage, const Prepare& prepare) {
