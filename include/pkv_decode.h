@@ -626,7 +626,9 @@ typedef struct pkv_prefill_plan {
   int32_t splits;
   int32_t smem_bytes;     /* dynamic shared memory of a CTA */
   int32_t value_blocks;   /* blocks of 128 rows of values in the workspace (0: pages are read directly) */
-  size_t workspace_bytes; /* f32 states of split key ranges (none with splits = 1), and the values */
+  size_t workspace_bytes; /* f32 states of split key ranges (none with splits = 1), and the values: as many as
+                             the tables have rows, or the tokens and the window need; tables cut to the
+                             longest sequence keep it, and the pass over it, small */
 } pkv_prefill_plan;
 
 int pkv_make_prefill_plan(const pkv_pool_layout* layout, const pkv_prefill_params* params, int32_t sm_count,
