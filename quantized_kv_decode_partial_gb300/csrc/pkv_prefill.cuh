@@ -484,6 +484,10 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           if (round > 0 && !mbar_wait_close(is_k ? k_empty(stage) : v_empty(stage), (round - 1) & 1, &abort_flag, p.error_flag,
                                            p.wait_limit_ns))
             break;
+          // The slot's codes before these were another pair's (3 need not divide RS), so nothing yet says that their copy has
+          // landed, and while it has not, raw_full is two phases behind, where the parity below passes at once. The slot's release
+          // says so. Its own parity is sure: this pair's unit n - 3 was asked for, so all up to n - 3 - RS are released.
+          if (n >= RS && !mbar_wait_close(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
           if (!mbar_wait_close(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
           const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = smem_addr(unit_scales[s]);
           const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;
