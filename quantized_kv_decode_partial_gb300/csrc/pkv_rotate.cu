@@ -280,10 +280,10 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
   int left = (key ? q_slots * kRows + HK : HQ) - (g * kRows + sub);  // rows of this kind from the lane's on
   bool normed = (key ? p.k_weight : p.q_weight) != nullptr;
   uint32_t place = 0;
+  const int end = k_to ? slots : q_slots;  // keys without a place go nowhere
 #pragma unroll 1
-  for (int s = g; s < slots; s += G) {
+  for (int s = g; s < end; s += G) {
     if (kKeysHere && !key && s >= q_slots) {  // from here on keys
-      if (!k_to) break;
       key = true;
       make_turns();
       to = k_to + ((s - q_slots) * kRows + sub) * k_head;
@@ -304,7 +304,7 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
     ask(place);
     place = (place + kSlotBytes) & (kRing * kSlotBytes - 1);
     turn_row2<D, SIMPLE>(a, b, normed, p.eps, turned, adjacent, turn);
-    if (left > 0 && to) {
+    if (left > 0) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (!used[i]) continue;
