@@ -607,7 +607,8 @@ typedef struct pkv_prefill_params {
                                  values of all rows that any query sees to the workspace, bf16 of
                                  e4m3 pages, fp16 of affine ones (with a power of two for each
                                  (sequence, KV head) and plane; values below 2^-39 of the
-                                 largest are lost, as are parts of a query row);
+                                 largest are lost, as are parts of a query row, and weights
+                                 below 2^-32 of a row's largest);
                                  PKV_READING_DIRECT (1): e4m3 pages alone: every CTA turns the codes it
                                  needs into bf16;
                                  PKV_READING_AUTO (0): direct for e4m3 pages where sequences have

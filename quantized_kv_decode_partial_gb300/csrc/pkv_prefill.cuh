@@ -164,10 +164,14 @@ __device__ __forceinline__ void subtract(float (&s)[KT], float m) {
 }
 
 // A row's weights 2^(c s - c m) as pairs of bf16 (or fp16), their f32 sums added to `sums`; returns the largest score.
+// fp16 ends at 2^-24 (what is at most half of it is lost) and its steps are even below 2^-14, where a few keys can stand
+// against a million small ones. There all weights, and so their sums, are 2^7 times as large: at most 2^15 with what
+// the maximum may lag behind, and lost only below 2^-32 of the maximum's.
 template <int KT, bool HALF>
 __device__ __forceinline__ float weights(const float (&s)[KT], float c, float m, uint64_t (&sums)[2], uint32_t (&w)[KT / 2]) {
+  constexpr float kUp = HALF ? 7.f : 0.f;
   const float mc = fabsf(m) < INFINITY ? m * c : 0.f;
-  const uint64_t cc = pair(c, c), mm = pair(-mc, -mc);
+  const uint64_t cc = pair(c, c), mm = pair(kUp - mc, kUp - mc);
 #pragma unroll
   for (int e = 0; e < KT / 2; ++e) {
     float x, y;
