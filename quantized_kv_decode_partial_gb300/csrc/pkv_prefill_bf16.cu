@@ -11,9 +11,11 @@ struct PrefillJoinParams {
   const int32_t* query_starts;
   __nv_bfloat16* out;
   int num_seqs, tokens, num_q_heads, splits;
+  float score_scale;
 };
 
-// One warp per output row: the states of its splits, weighted by 2^(m - max m).
+// One warp per output row: the states of its splits, weighted by 2^(c (m - max m)). Differences of maxima come before
+// the scale: rounded products c m would lose them far from zero.
 template <int DV>
 __global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_constant__ PrefillJoinParams p) {
   wait_for_prerequisite_grids();
@@ -36,14 +38,14 @@ __global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_cons
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     const float up = fmaxf(top, mx);
     if (up == -INFINITY) continue;
-    const float by = top == -INFINITY ? 0.f : fast_exp2(top - up);
+    const float by = top == -INFINITY ? 0.f : fast_exp2((top - up) * p.score_scale);
     top = up;
     total *= by;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[n][v] *= by;
-    const float w = l != 0.f ? fast_exp2(m - up) : 0.f;  // a split without keys has no outputs
+    const float w = l != 0.f ? fast_exp2((m - up) * p.score_scale) : 0.f;  // a split without keys has no outputs
     float sum = w * l;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(128) pkv_prefill_join_kernel(const __grid_cons
 PKV_PREFILL_FORMAT(bf16, 16, false, PKV_PREFILL_WIDE)
 
 cudaError_t launch_prefill_join(const PrefillParams& p, int dv, cudaStream_t stream) {
-  PrefillJoinParams j{p.ws_o, p.ws_ml, p.query_starts, p.out, p.num_seqs, p.tokens, p.num_q_heads, p.splits};
+  PrefillJoinParams j{p.ws_o, p.ws_ml, p.query_starts, p.out, p.num_seqs, p.tokens, p.num_q_heads, p.splits, p.score_scale};
   const long long rows = static_cast<long long>(p.tokens) * p.num_q_heads;
   const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
   if (dv == 64) return launch_dependent(pkv_prefill_join_kernel<64>, grid, 128, 0, stream, j);

@@ -66,3 +66,26 @@ def test_one_key_against_a_million_small_ones(fmt, below):
     rel = 2.0 ** -8 + 2.0 ** -18 + rows / 4 * 2.0 ** -24 + 2.0 ** -8
     tol = rel * want + (rows * 2.0 ** -32 if fmt.get("bits") and fmt is not E4M3 else 0.0)
     assert bool(((got - want).abs() <= tol).all()), (got[0, 0, 0].item(), want[0, 0, 0].item())
+
+
+@pytest.mark.parametrize("fmt", FORMATS[:3])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7])
+@pytest.mark.parametrize("scale", [0.2, 0.24, 0.28, 0.31])
+def test_splits_far_from_zero_keep_their_differences(fmt, splits, scale):
+    """Scores of 2^24 and, in the first half of the keys, 8 more, all exact in f32; the scale makes steps of about two of the 8.
+    The second half's share of the weights is what the output says: parts of the keys join by the difference of their maxima."""
+    rows, T, bs = 1792, 4, 256
+    k = torch.zeros(rows, D, dtype=torch.int32, device=DEV)
+    v = torch.zeros_like(k)
+    k[:, 0] = 64
+    k[:rows // 2, 1], v[rows // 2:] = 1, 8
+    q = torch.zeros(T, 2, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0], q[..., 1] = 2.0 ** 18, 8.0
+    got = attend(fmt, q, k, v, bs, 1.0, 0.125, scale, splits=splits).double()
+    seen = rows // 2 - T + 1 + torch.arange(T, device=DEV, dtype=torch.float64)  # of the second half
+    less = seen * math.exp(-8 * float(torch.tensor(scale, dtype=torch.float32)))
+    want = (less / (less + rows // 2))[:, None, None].expand_as(got)
+    # weights and outputs half a step of bf16 each (2^-8); of arguments up to 2^2, after the difference, c and the product are
+    # rounded (2^2 * 2^-23) and the exponential is off by 2^-20; sums of 1792 terms
+    tol = (2 * 2.0 ** -8 + 2.0 ** -18 + rows * 2.0 ** -24) * want
+    assert bool(((got - want).abs() <= tol).all()), ((got - want).abs() / want).max().item()
