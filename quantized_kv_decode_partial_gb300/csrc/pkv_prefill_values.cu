@@ -20,9 +20,10 @@ namespace {
 constexpr int kRows = 32;
 constexpr int kThreads = 128;
 
+// Rows below `lowest` are nobody's: their blocks may have been given to others, so nothing of them is read.
 template <int D, int FMT>
 __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int plane, const int32_t* table, int first_row,
-                                             int len, uint16_t* out, int head, float factor) {
+                                             int lowest, int len, uint16_t* out, int head, float factor) {
   constexpr int kPerRow = D / 16, kRounds = kRows * kPerRow / kThreads;
   uint4 v[kRounds];
   float scale[kRounds], bias[kRounds];
@@ -31,7 +32,7 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
     const int c = i * kThreads + threadIdx.x, r = c / kPerRow, col = c % kPerRow, t = first_row + r;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
     scale[i] = bias[i] = 0.f;
-    if (t >= len) continue;
+    if (t < lowest || t >= len) continue;
     const int blk = t / p.block_size;
     const int phys = table[blk];
     if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;  // flagged by the attention
@@ -54,7 +55,7 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const int c = i * kThreads + threadIdx.x, r = c / kPerRow;
-    if (first_row + r >= len) continue;  // nobody's rows are left as they are
+    if (first_row + r < lowest || first_row + r >= len) continue;  // nobody's rows are left as they are
     uint32_t w[8];
     codes_to_values<FMT>(v[i], scale[i], bias[i], w);
     uint4* to = reinterpret_cast<uint4*>(out) + 2 * c;
@@ -77,14 +78,15 @@ __global__ void __launch_bounds__(kThreads) pkv_prefill_values_kernel(const __gr
   const long long row = static_cast<long long>(block - p.values.base(b, start)) * kValueRows +
                         p.values.first_row(len, static_cast<int>(n), p.window) + row0;
   if (block < p.values.base(b, start) || row >= len) return;
+  const int lowest = p.values.lowest(len, static_cast<int>(n), p.window);
   const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   const size_t to = (static_cast<size_t>(block) * p.num_kv_heads + head) * kValueRows + row0;
   uint16_t* out = static_cast<uint16_t*>(p.out[plane]);
   const float factor = FMT == kFmtE4m3 ? 1.f : p.factors[(plane * p.num_seqs + b) * p.num_kv_heads + head];
   if (plane == 0) {
-    plane_values<D, FMT>(p, 0, table, static_cast<int>(row), len, out + to * D, head, factor);
+    plane_values<D, FMT>(p, 0, table, static_cast<int>(row), lowest, len, out + to * D, head, factor);
   } else {
-    plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), len, out + to * DV, head, factor);
+    plane_values<DV, FMT>(p, 1, table, static_cast<int>(row), lowest, len, out + to * DV, head, factor);
   }
 }
 
