@@ -630,8 +630,21 @@ __device__ __forceinline__ uint32_t ld_nc_keep_u32(const void* ptr) {
   return v;
 }
 // The same for memory that a kernel overlapping this one may have written before the wait on
-// it (block tables, which the choice of blocks writes after it has let the attention start):
+// it (block tables, which the choice of blocks writes after it has let the attention start;
+// pages and new rows, behind a decode step whose epilogue lets the next kernel start):
 // not read-only for as long as this kernel runs, so not through the read-only path.
+__device__ __forceinline__ uint4 ld_keep_v4(const void* ptr) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(ptr));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_keep_v2(const void* ptr) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(ptr));
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_keep_u32(const void* ptr) {
   uint32_t v;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(ptr));

@@ -39,11 +39,11 @@ __device__ __forceinline__ void plane_values(const PrefillValuesParams& p, int p
     const size_t cell = static_cast<size_t>(phys) * p.num_kv_heads + head;
     const size_t row = cell * p.block_size + (t - blk * p.block_size);
     if constexpr (FMT == 4) {
-      const uint2 w = ld_nc_keep_v2(p.pool[plane] + row * (D / 2) + col * 8);
+      const uint2 w = ld_keep_v2(p.pool[plane] + row * (D / 2) + col * 8);
       v[i].x = w.x;
       v[i].y = w.y;
     } else {
-      v[i] = ld_nc_keep_v4(p.pool[plane] + row * D + col * 16);
+      v[i] = ld_keep_v4(p.pool[plane] + row * D + col * 16);
     }
     if constexpr (FMT == kFmtE4m3) {
       scale[i] = p.planes[plane].block_scales[cell];

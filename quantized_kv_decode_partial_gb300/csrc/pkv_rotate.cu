@@ -324,7 +324,7 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
     constexpr int kChunks = DV / 8;
     for (int c = g * 32 + lane; c < HK * kChunks; c += G * 32) {
       const int h = c / kChunks, at8 = (c % kChunks) * 8;
-      *reinterpret_cast<uint4*>(p.dst.v_pool_bf16 + pool_row(h) * DV + at8) = ld_nc_keep_v4(v_src + h * p.v.head + at8);
+      *reinterpret_cast<uint4*>(p.dst.v_pool_bf16 + pool_row(h) * DV + at8) = ld_keep_v4(v_src + h * p.v.head + at8);
     }
   }
   if constexpr (FMT == 4 || FMT == 8) {
@@ -339,8 +339,8 @@ __device__ __forceinline__ void token_rows(const RotateParams& p, const RotateTa
       for (int i = 0; i < 2; ++i) {
         a[i] = b[i] = make_uint2(0u, 0u);
         if (used[i] && h < HK) {
-          a[i] = ld_nc_keep_v2(k_src + h * p.k.head + off0[i]);
-          b[i] = ld_nc_keep_v2(k_src + h * p.k.head + off1[i]);
+          a[i] = ld_keep_v2(k_src + h * p.k.head + off0[i]);
+          b[i] = ld_keep_v2(k_src + h * p.k.head + off1[i]);
         }
       }
       turn_row2<D, SIMPLE>(a, b, p.k_weight != nullptr, p.eps, turned, adjacent, turn);
@@ -436,8 +436,8 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
     a[k] = b[k] = make_uint2(0u, 0u);
     if (live && used && r < r1) {
       const __nv_bfloat16* row = src + (r - r0) * in.token;
-      a[k] = ld_nc_keep_v2(row + off0);
-      b[k] = ld_nc_keep_v2(row + off1);
+      a[k] = ld_keep_v2(row + off0);
+      b[k] = ld_keep_v2(row + off1);
     }
   }
   // the rows are in flight while the table's answer arrives
@@ -496,8 +496,8 @@ __device__ __forceinline__ void block_rows(const RotateParams& p, Tables& tab, i
       const int r = row0 + k * row_step;
       uint2 x = make_uint2(0u, 0u), y = x;
       if (live && used && r < r1) {
-        x = ld_nc_keep_v2(src + (r - r0) * in.token + off0);
-        y = ld_nc_keep_v2(src + (r - r0) * in.token + off1);
+        x = ld_keep_v2(src + (r - r0) * in.token + off0);
+        y = ld_keep_v2(src + (r - r0) * in.token + off1);
       }
       finish(x, y, r);
       use(x, y, r);
