@@ -623,13 +623,18 @@ typedef struct pkv_prefill_params {
 typedef struct pkv_prefill_plan {
   int32_t unit_tokens;    /* tokens of one CTA */
   int32_t key_tile;       /* key rows per step */
-  int32_t units;          /* CTAs per KV head and split, those of short last tiles included */
+  int32_t units;          /* CTAs per KV head and split, those of short last tiles included (of a group of
+                             sequences, see workspace_bytes) */
   int32_t splits;
   int32_t smem_bytes;     /* dynamic shared memory of a CTA */
   int32_t value_blocks;   /* blocks of 128 rows of values in the workspace (0: pages are read directly) */
   size_t workspace_bytes; /* f32 states of split key ranges (none with splits = 1), and the values: as many as
                              the tables have rows, or the tokens and the window need; tables cut to the
-                             longest sequence keep it, and the pass over it, small */
+                             longest sequence keep it, and the pass over it, small. Affine pages, which have no
+                             other reading: where all values would take more than 8 GB, those of a group of
+                             sequences, as many as 8 GB hold (at least one), and the groups go through the
+                             workspace one after the other. 2^31 rows of values at once (KV heads counted) are
+                             refused: PKV_ERR_UNSUPPORTED_SHAPE */
 } pkv_prefill_plan;
 
 int pkv_make_prefill_plan(const pkv_pool_layout* layout, const pkv_prefill_params* params, int32_t sm_count,

@@ -1319,14 +1319,14 @@ int prefill_splits(const pkv_pool_layout* L, const pkv_prefill_params* P, long l
   return best;
 }
 
-// Where the values of each sequence go, and how many blocks of them there can be.
-pkv::PrefillValues prefill_values(const pkv_pool_layout* L, const pkv_prefill_params* P, long long* blocks) {
+// Where the values of each of `seqs` sequences go, and how many blocks of them there can be.
+pkv::PrefillValues prefill_values(const pkv_pool_layout* L, const pkv_prefill_params* P, int seqs, long long* blocks) {
   const long long table = static_cast<long long>(P->max_blocks_per_seq) * L->block_size;
   const long long whole = (table + pkv::kValueRows - 1) / pkv::kValueRows;
-  const long long all = whole * P->num_seqs;
+  const long long all = whole * seqs;
   // under a window a sequence of n tokens sees n + window - 1 rows: floor((n + window) / 128) + 2 blocks at most
   const long long part = P->window / pkv::kValueRows + 3;
-  const long long windowed = P->num_tokens / pkv::kValueRows + 1 + part * P->num_seqs;
+  const long long windowed = P->num_tokens / pkv::kValueRows + 1 + part * seqs;
   pkv::PrefillValues v{};
   v.used = 1;
   v.by_tokens = P->window > 0 && windowed < all;
@@ -1335,25 +1335,44 @@ pkv::PrefillValues prefill_values(const pkv_pool_layout* L, const pkv_prefill_pa
   return v;
 }
 
+constexpr long long kMostValueBytes = 8ll << 30;
+
+long long value_bytes(const pkv_pool_layout* L, long long blocks) {
+  return blocks * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
+}
+
+// Sequences whose values the workspace holds at a time. Affine pages have no other reading, so where the values of all would
+// take more than 8 GB, the call goes through the sequences in groups of this many (one at least), each one's values
+// written over the last one's. A group reads as much as it would together with the others.
+int prefill_group(const pkv_pool_layout* L, const pkv_prefill_params* P) {
+  if (L->bits == 16 || block_scaled(L)) return P->num_seqs;
+  int fit = 1;
+  for (int step = 1 << 16; step > 0; step >>= 1) {
+    long long blocks = 0;
+    if (fit + step > P->num_seqs) continue;
+    prefill_values(L, P, fit + step, &blocks);
+    if (value_bytes(L, blocks) <= kMostValueBytes) fit += step;
+  }
+  return fit;
+}
+
 // Factors of fp16 values, behind the states and before the values.
-size_t factor_bytes(const pkv_pool_layout* L, const pkv_prefill_params* P) {
+size_t factor_bytes(const pkv_pool_layout* L, int seqs) {
   if (block_scaled(L)) return 0;
-  return static_cast<size_t>(round_up(2ll * P->num_seqs * L->num_kv_heads * sizeof(float), 256));
+  return static_cast<size_t>(round_up(2ll * seqs * L->num_kv_heads * sizeof(float), 256));
 }
 
 // e4m3 pages: the values pay for themselves from the second CTA on that reads the same keys: turning a tile of 128 keys
 // costs a CTA about 1.5 us, writing and reading it as bf16 as much as 15 ns of the GPU's bandwidth (16 chunks of 1
 // to 512 tokens over up to 16000 rows: 1229 us directly, 742 by values). Affine values need more bits than the direct
 // form's bf16 has.
-constexpr long long kMostValueBytes = 8ll << 30;
-
 long long prefill_value_blocks(const pkv_pool_layout* L, const pkv_prefill_params* P, int unit_tokens) {
   if (L->bits == 16 || P->reading == PKV_READING_DIRECT) return 0;
   long long blocks = 0;
-  prefill_values(L, P, &blocks);
-  const long long bytes = blocks * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2;
+  prefill_values(L, P, prefill_group(L, P), &blocks);
   const bool wanted = P->reading == PKV_READING_VALUES || !block_scaled(L) ||
-                      (P->num_tokens >= static_cast<long long>(unit_tokens) * P->num_seqs && bytes <= kMostValueBytes);
+                      (P->num_tokens >= static_cast<long long>(unit_tokens) * P->num_seqs &&
+                       value_bytes(L, blocks) <= kMostValueBytes);
   return wanted ? blocks : 0;
 }
 
@@ -1367,17 +1386,19 @@ int prefill_plan(const pkv_pool_layout* L, const pkv_prefill_params* P, int sm_c
   r.value_blocks = static_cast<int32_t>(blocks);
   r.unit_tokens = info.query_tiles * (128 / rep);
   r.key_tile = info.key_tile;
-  r.units = P->num_tokens / r.unit_tokens + P->num_seqs;
+  const int group = prefill_group(L, P);
+  r.units = P->num_tokens / r.unit_tokens + group;
   const long long ctas = static_cast<long long>(r.units) * L->num_kv_heads;
-  r.splits = P->splits > 0 ? P->splits : prefill_splits(L, P, ctas, info.key_tile, r.unit_tokens, sm_count);
+  // of a group, which has its share of the tokens
+  const long long own = static_cast<long long>(P->num_tokens) * group / P->num_seqs / r.unit_tokens + group;
+  r.splits = P->splits > 0 ? P->splits : prefill_splits(L, P, own * L->num_kv_heads, info.key_tile, r.unit_tokens, sm_count);
   if (ctas * r.splits >= (1ll << 31)) return PKV_ERR_BAD_PARAMS;
   r.smem_bytes = info.smem_bytes;
   if (r.splits > 1)
     r.workspace_bytes = static_cast<size_t>(r.splits) * P->num_tokens * P->num_q_heads * (v_dim(L) + 2) * sizeof(float);
   if (r.value_blocks > 0)
     r.workspace_bytes = static_cast<size_t>(round_up(static_cast<long long>(r.workspace_bytes), 256)) +
-                        static_cast<size_t>(r.value_blocks) * L->num_kv_heads * pkv::kValueRows * (L->head_dim + v_dim(L)) * 2 +
-                        factor_bytes(L, P);
+                        static_cast<size_t>(value_bytes(L, blocks)) + factor_bytes(L, group);
   *plan = r;
   return PKV_OK;
 }
@@ -1464,14 +1485,10 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
 
   const int D = layout->head_dim, DV = v_dim(layout), rep = params->num_q_heads / layout->num_kv_heads;
   pkv::PrefillParams p{};
-  p.query_starts = query_starts;
-  p.block_tables = block_tables;
-  p.seq_lens = seq_lens;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o ? p.ws_o + static_cast<size_t>(plan.splits) * params->num_tokens * params->num_q_heads * DV : nullptr;
   p.error_flag = error_flag;
-  p.num_seqs = params->num_seqs;
   p.tokens = params->num_tokens;
   p.num_q_heads = params->num_q_heads;
   p.num_kv_heads = layout->num_kv_heads;
@@ -1482,6 +1499,7 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   p.max_blocks = params->max_blocks_per_seq;
   const int fmt = format_of(layout);
   const bool block = block_scaled(layout), values = plan.value_blocks > 0;
+  const int group = prefill_group(layout, params);
   // rows of one copy: the largest power of two that divides blocks and key tiles (codes come in quarter tiles)
   const int most = layout->bits == 16 || values ? plan.key_tile : plan.key_tile / 4;
   const int block_rows = values ? pkv::kValueRows : layout->block_size;
@@ -1510,7 +1528,7 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   pkv::PrefillValuesParams w{};
   if (values) {
     long long blocks = 0;
-    p.values = prefill_values(layout, params, &blocks);
+    p.values = prefill_values(layout, params, group, &blocks);
     const size_t rows = static_cast<size_t>(plan.value_blocks) * layout->num_kv_heads * pkv::kValueRows;
     w.pool[0] = static_cast<const uint8_t*>(k_pool);
     w.pool[1] = static_cast<const uint8_t*>(v_pool);
@@ -1520,22 +1538,17 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
     char* base = static_cast<char*>(workspace) + plan.workspace_bytes - rows * (D + DV) * 2;
     w.out[0] = base;
     w.out[1] = base + rows * D * 2;
-    w.factors = block ? nullptr : reinterpret_cast<float*>(base - factor_bytes(layout, params));
+    w.factors = block ? nullptr : reinterpret_cast<float*>(base - factor_bytes(layout, group));
     p.factors = w.factors;
     w.dim[0] = D;
     w.dim[1] = DV;
     w.values = p.values;
-    w.query_starts = query_starts;
-    w.block_tables = block_tables;
-    w.seq_lens = seq_lens;
-    w.num_seqs = p.num_seqs;
     w.tokens = p.tokens;
     w.num_kv_heads = p.num_kv_heads;
     w.num_blocks = p.num_blocks;
     w.block_size = p.block_size;
     w.max_blocks = p.max_blocks;
     w.window = p.window;
-    w.blocks = plan.value_blocks;
   }
   const long long pool_rows = static_cast<long long>(values ? plan.value_blocks : layout->num_blocks) * layout->num_kv_heads * block_rows;
   CUtensorMap tq, tk, tv;
@@ -1551,14 +1564,28 @@ int pkv_paged_prefill_attention(const pkv_pool_layout* layout, const pkv_prefill
   (void)cudaGetLastError();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (values) {
-    e = pkv::launch_prefill_values(w, fmt, st);
-    if (e != cudaSuccess) return cuda_fail("values kernel launch", e);
+  for (int b0 = 0; b0 < params->num_seqs; b0 += group) {
+    p.num_seqs = std::min(group, params->num_seqs - b0);
+    p.query_starts = query_starts + b0;
+    p.block_tables = block_tables + static_cast<size_t>(b0) * p.max_blocks;
+    p.seq_lens = seq_lens + b0;
+    if (values) {
+      w.num_seqs = p.num_seqs;
+      w.query_starts = p.query_starts;
+      w.block_tables = p.block_tables;
+      w.seq_lens = p.seq_lens;
+      w.blocks = w.values.by_tokens ? plan.value_blocks : w.values.per_seq * p.num_seqs;
+      e = pkv::launch_prefill_values(w, fmt, st);
+      if (e != cudaSuccess) return cuda_fail("values kernel launch", e);
+    }
+    const int units = params->num_tokens / plan.unit_tokens + p.num_seqs;
+    e = fmt == 4 || fmt == 8    ? pkv::launch_prefill_f16(D, DV, p, tq, tk, tv, units, st, device)
+        : fmt == 16 || values ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, units, st, device)
+                              : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, units, st, device);
+    if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
   }
-  e = fmt == 4 || fmt == 8    ? pkv::launch_prefill_f16(D, DV, p, tq, tk, tv, plan.units, st, device)
-      : fmt == 16 || values ? pkv::launch_prefill_bf16(D, DV, p, tq, tk, tv, plan.units, st, device)
-                            : pkv::launch_prefill_e4m3(D, DV, p, tq, tk, tv, plan.units, st, device);
-  if (e != cudaSuccess) return cuda_fail("prompt attention kernel launch", e);
+  p.num_seqs = params->num_seqs;
+  p.query_starts = query_starts;
   if (plan.splits > 1) {
     e = pkv::launch_prefill_join(p, DV, st);
     if (e != cudaSuccess) return cuda_fail("prompt attention join launch", e);
