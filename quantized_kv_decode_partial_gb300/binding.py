@@ -354,12 +354,13 @@ class _Call:
 
 
 _calls = {}
+_prompt_calls = {}  # of calls whose keys hold a step's token count: as many as there are counts, so they stay among themselves
 
 
-def _remember(key, call):
-    if len(_calls) > 1024:
-        _calls.clear()
-    _calls[key] = call
+def _remember(key, call, calls=_calls):
+    if len(calls) > 1024:
+        calls.clear()
+    calls[key] = call
     return call
 
 
@@ -821,7 +822,7 @@ def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Ten
     key = ("rotate", index, _layout_key(q), _layout_key(k), positions.shape, positions.dtype, inv_freq.shape, inv_freq.dtype,
            _layout_key(q_weight), _layout_key(k_weight), _layout_key(q_out), _layout_key(k_out), eps, weight_offset,
            None if sections is None else tuple(sections), section_order, pairing, amplitude)
-    call = _calls.get(key)
+    call = _prompt_calls.get(key)
     if call is None:
         if index < 0:
             raise ValueError("expected CUDA tensors")
@@ -846,7 +847,7 @@ def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Ten
             if shape is not None:
                 call.strides[2 + i] = _row_strides(torch.empty(shape, device="meta"))
                 call.refs[2 + i] = ctypes.byref(call.strides[2 + i])
-        _remember(key, call)
+        _remember(key, call, _prompt_calls)
     _check_tensors(index, positions, inv_freq, q_weight, k_weight)
     _on_one_device(index, k, q_out, k_out)
     with _on_index(index):
@@ -889,7 +890,7 @@ def norm_rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
            _types((block_tables, seq_lens, k_pool, v_pool, query_starts, k_scales, k_biases, v_scales, v_biases)),
            bits, group_size, _layout_key(q_weight), _layout_key(k_weight), _layout_key(q_out), eps, weight_offset,
            None if sections is None else tuple(sections), section_order, pairing, amplitude)
-    call = _calls.get(key)
+    call = _prompt_calls.get(key)
     if call is None:
         if index < 0:
             raise ValueError("expected CUDA tensors")
@@ -934,7 +935,7 @@ def norm_rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
             if len(lead) == 1 and not packed:
                 st.seq = st.token
             call.refs[3] = ctypes.byref(st)
-        _remember(key, call)
+        _remember(key, call, _prompt_calls)
     _check_tensors(index, positions, inv_freq, q_weight, k_weight, block_tables, seq_lens, query_starts, k_pool, v_pool,
                    k_scales, k_biases, v_scales, v_biases, error_flag)
     _on_one_device(index, k, v, q_out)
@@ -993,7 +994,7 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
            _types((k_pool, v_pool, block_tables, seq_lens, query_starts, k_scales, k_biases, v_scales, v_biases)), bits,
            group_size, window, splits, reading)
     with _on_index(index) if index >= 0 else _stay:
-        call = _calls.get(key)
+        call = _prompt_calls.get(key)
         if call is None:
             if index < 0:
                 raise ValueError("expected CUDA tensors")
@@ -1022,7 +1023,7 @@ def paged_prefill_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
             call.keep = (layout, params, strides)
             call.refs = tuple(ctypes.byref(x) for x in call.keep)
             call.workspace_bytes = make_prefill_plan(layout, params).workspace_bytes
-            _remember(key, call)
+            _remember(key, call, _prompt_calls)
         _check_tensors(index, k_pool, v_pool, block_tables, seq_lens, query_starts, k_scales, k_biases, v_scales, v_biases,
                        out, workspace, error_flag)
         stream = _raw_stream(index)
