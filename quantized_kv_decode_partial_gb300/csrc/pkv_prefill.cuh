@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
     const int pos = u.position + min(first + r / p.rep, last);  // rows without a token go along with the last one
     const int below = p.window > 0 ? pos - p.window : -1;       // keys at or below it are out of the window
     float c = p.score_scale;
-    float out_factor = 1.f, true_score = 1.f;  // (powers of two)
+    float out_factor = 1.f;
     float m = -INFINITY;          // running maximum of the unscaled scores
     // c s - c m is rounded once, but c m before it: where that could be off by more than 2^-4 in a row of the warp,
     // s - m comes first. Only rows of the unit's tokens have a say in what their warp does: the others hold the next sequence's
@@ -638,7 +638,6 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(q_half);
       const float* factors = p.factors + static_cast<size_t>(u.seq) * p.num_kv_heads + u.head;
-      true_score = 1.f / by / factors[0];
       c = fmaxf(c / by / factors[0], 1e-37f);  // not zero, as ever
       out_factor = 1.f / factors[static_cast<size_t>(p.num_seqs) * p.num_kv_heads];
     }
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
       const float inv = (sum != 0.f ? 1.f / sum : 0.f) * out_factor;
       if (split && out.live) {
         float* ml = p.ws_ml + (u.split * all_rows + out.row) * 2;
-        ml[0] = m * true_score;  // unscaled, so that the join can take differences first
+        ml[0] = m * (c / p.score_scale);  // unscaled (the factor is a power of two), so that the join can take differences first
         ml[1] = sum;
       }
 #pragma unroll 1
