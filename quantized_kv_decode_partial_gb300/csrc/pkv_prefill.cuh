@@ -40,11 +40,14 @@ struct PrefillShape {
   static constexpr int kQ = DV == 256 || (kCodes && D == 256) ? 1 : 2;
   static constexpr int KT = D <= 128 && DV <= 128 ? 128 : 64;  // key rows per tile
   static constexpr int kQBytes = 128 * D * 2, kKBytes = KT * D * 2, kVBytes = KT * DV * 2;
-  // e4m3 codes come in through a ring of quarter tiles, which six warps turn into bf16.
+  // e4m3 codes come in through a ring of quarter tiles, which six warps, in pairs, turn into bf16.
+  static constexpr int kPairs = 3;
   static constexpr int kRawBytes = KT / 4 * (D > DV ? D : DV);
-  // As many as fit beside two stages of K and V (up to 8): each of the three pairs has one or two in the works.
+  // As many as fit beside two stages of K and V (up to 9), and of each of the three pairs as many as of the others: a slot is one
+  // pair's alone. A pair that came upon another's slot could be two phases ahead of its barrier, whose parity then passes
+  // although the codes are still on their way. (Eight slots and one more wait, for the release of the codes before: the same time.)
   static constexpr int kRawFit = (kPrefillRoom - kQ * kQBytes - 2 * (kKBytes + kVBytes)) / kRawBytes;
-  static constexpr int kRawSlots = !kCodes ? 0 : kRawFit > 8 ? 8 : kRawFit;
+  static constexpr int kRawSlots = !kCodes ? 0 : (kRawFit > 9 ? 9 : kRawFit) / kPairs * kPairs;
   static constexpr int kThreads = kCodes ? 512 : 384;
   // Stages of K and of V: as many as fit (up to 4), K first. A K tile is asked for when the last product that
   // read its stage is done; with two stages that is five products ahead, a copy's latency at best.
@@ -54,7 +57,9 @@ struct PrefillShape {
   static constexpr int kSmem = kQ * kQBytes + kKS * kKBytes + kVS * kVBytes + kRawSlots * kRawBytes + 1024;
   static constexpr int kTmemO = 2 * KT;  // columns: two score tiles, then the outputs
   static_assert(kTmemO + kQ * DV <= 512, "tensor memory");
-  static_assert(kVS >= 2 && kKS >= 2 && (!kCodes || kRawSlots >= 6) && kSmem <= kPrefillRoom + 1024 && kRawBytes % 128 == 0, "shared memory");
+  static_assert(kVS >= 2 && kKS >= 2 && (!kCodes || (kRawSlots >= 2 * kPairs && kRawSlots % kPairs == 0)) &&
+                    kSmem <= kPrefillRoom + 1024 && kRawBytes % 128 == 0,
+                "shared memory");
 };
 
 // Registers: softmax threads hold a row's scores. With 384 threads (two softmax warpgroups, one with the product
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
   } else if (T::kCodes && warp >= 9) {
     // ------------------------------------------------------------------ e4m3 codes, to bf16 tiles
     // Quarter tiles in the order K(0), K(1), V(0), K(2), V(1), ...: unit n is quarter n & 3 of plane tile n / 4. Warp 9
-    // copies their codes, RS units ahead; three pairs of warps turn them into bf16 in turn.
+    // copies their codes, RS units ahead; pairs of warps turn them into bf16 in turn.
     fewer_registers<T::kCodes>();
     if constexpr (T::kCodes) {
       constexpr int kQuarter = KT / 4;
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           mbar_wait_close(raw_full(n % RS), (n / RS) & 1, &none, p.error_flag, kWaitLimitNs);
       } else {
         const int group = (warp - 10) >> 1, part = (warp - 10) & 1;
-        for (int n = group; n < 8 * nt; n += 3) {
+        for (int n = group; n < 8 * nt; n += T::kPairs) {
           bool is_k;
           int j;
           plane_tile(n >> 2, is_k, j);
@@ -488,10 +493,6 @@ __global__ void __launch_bounds__(PrefillShape<D, DV, FMT>::kThreads, 1)
           if (round > 0 && !mbar_wait_close(is_k ? k_empty(stage) : v_empty(stage), (round - 1) & 1, &abort_flag, p.error_flag,
                                            p.wait_limit_ns))
             break;
-          // The slot's codes before these were another pair's (3 need not divide RS), so nothing yet says that their copy has
-          // landed, and while it has not, raw_full is two phases behind, where the parity below passes at once. The slot's release
-          // says so. Its own parity is sure: this pair's unit n - 3 was asked for, so all up to n - 3 - RS are released.
-          if (n >= RS && !mbar_wait_close(raw_empty(s), (n / RS - 1) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
           if (!mbar_wait_close(raw_full(s), (n / RS) & 1, &abort_flag, p.error_flag, p.wait_limit_ns)) break;
           const uint32_t from = smem_raw_codes + s * T::kRawBytes, scales = smem_addr(unit_scales[s]);
           const int key = (t0 + j) * KT, first = (n & 3) * kQuarter;

@@ -13,11 +13,17 @@ import pytest
 CSRC = Path(__file__).resolve().parents[1] / "quantized_kv_decode_partial_gb300" / "csrc"
 
 
-def waits_of_the_kernel():
-    """Barriers that a converting warp waits for before it reads unit n's codes, in order."""
+def the_kernel():
+    """Barriers that a converting warp waits for before it reads unit n's codes, in order; and the numbers of slots that shapes of
+    heads can get."""
     text = (CSRC / "pkv_prefill.cuh").read_text()
-    part = text[text.index("for (int n = group; n < 8 * nt; n += 3)"):text.index("convert_quarter<D, FMT, KT>(smem_k")]
-    return re.findall(r"mbar_wait_close\((?:is_k \? )?(\w+)\(", part)
+    part = text[text.index("for (int n = group; n < 8 * nt; n += "):text.index("convert_quarter<D, FMT, KT>(smem_k")]
+    rule = re.search(r"kRawSlots = !kCodes \? 0 : (.*);", text).group(1)
+    most = int(re.search(r"kRawFit > (\d+) \? \1 : kRawFit", rule).group(1))
+    by = int(re.search(r"kPairs = (\d+);", text).group(1)) if rule.endswith("/ kPairs * kPairs") else 1
+    assert by in (1, 3)  # the model's pairs
+    return (re.findall(r"mbar_wait_close\((?:is_k \? )?(\w+)\(", part),
+            sorted({min(fit, most) // by * by for fit in range(6, 30)}))
 
 
 class Barrier:
@@ -137,19 +143,20 @@ def runs(slots, waits):
                 yield Ring(slots, stages, nt, waits, late, random.Random(1000 * slots + 100 * stages + nt))
 
 
-@pytest.mark.parametrize("slots", [6, 7, 8])
-def test_no_unit_is_read_before_its_copy_landed(slots):
-    waits = waits_of_the_kernel()
-    assert waits[-1] == "raw_full"
-    for ring in runs(slots, waits):
-        ring.run()
+def test_no_unit_is_read_before_its_copy_landed():
+    waits, counts = the_kernel()
+    assert waits[-1] == "raw_full" and min(counts) >= 6
+    for slots in counts:
+        for ring in runs(slots, waits):
+            ring.run()
 
 
 def test_the_model_sees_a_parity_that_is_a_phase_behind():
-    """Without the wait for a slot's release, with slots that several pairs take in turn: each mistake that one copy's
-    delay can make is one of these two."""
-    with pytest.raises(AssertionError, match="read while slot|not its own"):
-        for ring in runs(8, ["k_empty", "raw_full"]):
+    """Slots that several pairs take in turn, and no other wait: each mistake that one copy's delay can make is one of these two. A
+    wait for the slot's release before rules them out, as do slots that are one pair's alone."""
+    for slots in (7, 8):
+        with pytest.raises(AssertionError, match="read while slot|not its own"):
+            for ring in runs(slots, ["k_empty", "raw_full"]):
+                ring.run()
+        for ring in runs(slots, ["k_empty", "raw_empty", "raw_full"]):
             ring.run()
-    for ring in runs(6, ["k_empty", "raw_full"]):  # here a slot is one pair's alone
-        ring.run()
