@@ -1362,10 +1362,12 @@ size_t factor_bytes(const pkv_pool_layout* L, int seqs) {
   return static_cast<size_t>(round_up(2ll * seqs * L->num_kv_heads * sizeof(float), 256));
 }
 
-// e4m3 pages: the values pay for themselves from the second CTA on that reads the same keys: turning a tile of 128 keys
-// costs a CTA about 1.5 us, writing and reading it as bf16 as much as 15 ns of the GPU's bandwidth (16 chunks of 1
-// to 512 tokens over up to 16000 rows: 1229 us directly, 742 by values). Affine values need more bits than the direct
-// form's bf16 has.
+// e4m3 pages: the values pay for themselves from the second CTA on that reads the same keys (16 chunks of 1 to 512 tokens over
+// up to 16000 rows, 8 KV heads of 128 dims: 1480 us directly, 704 by values). With fewer tokens the direct form needs no
+// workspace and no pass over the tables' whole width, which the lengths need not fill: 16 x 1 to 4 tokens over up to 16000 rows
+// take 502 us directly and 270 by values with tables as wide as that, 273 and 646 with tables of 131072 rows, which are split
+// more; 64 x 1 to 4 over up to 1000 rows 97 and 85, with tables of 8192 rows 109 and 233. Affine values need more bits than the
+// direct form's bf16 has.
 long long prefill_value_blocks(const pkv_pool_layout* L, const pkv_prefill_params* P, int unit_tokens) {
   if (L->bits == 16 || P->reading == PKV_READING_DIRECT) return 0;
   long long blocks = 0;

@@ -16,10 +16,12 @@
 // Few query rows over long caches: the key tiles of each CTA's rows are split over `splits`
 // CTAs whose f32 states (O, m, l) are joined by a second kernel.
 //
-// Measured on a GB300: 8 prompts of 1025-8192 tokens, 8 KV heads of 4, 128 dims: 1.42-1.47 ms, 1260-1305 TFLOP/s of
+// Measured on a GB300: 8 prompts of 1025-8192 tokens, 8 KV heads of 4, 128 dims: 1.42-1.48 ms, 1255-1305 TFLOP/s of
 // products, 0.66-0.69 of what a large library matrix product reaches alone; 2 chunks of 500-1024 tokens over 30011-60000 rows:
-// 1320-1394 TFLOP/s. The step is
-// bound by hand-overs between products and softmax (without any exponential, sum or maximum it takes 0.91 of its time)
+// 1310-1394 TFLOP/s. The prompts with heads of 64 dims, whose softmax is the same beside half the products: 720-726 TFLOP/s;
+// 192 for keys, 128 for values: 954-989; 4 KV heads of 256: 1106-1116, 256 and 128: 1131-1146, 128 and 256: 897. e4m3 codes
+// read directly, 16 x 1-16 tokens over 700-16000 rows: 500 us, 12 times the bytes' floor; a tile of keys takes a CTA 4 us. The
+// step is bound by hand-overs between products and softmax (without any exponential, sum or maximum it takes 0.91 of its time)
 // and by the power limit, under which the SM clock settles near 1.5 of 2.07 GHz. Two threads per row with a barrier
 // between them took 1.14 times as long, weights handed over by halves 1.19 times. 37 tokens alone: 8.4 us.
 #pragma once

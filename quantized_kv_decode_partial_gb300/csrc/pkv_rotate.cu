@@ -13,10 +13,12 @@
 // registers between the two uses and share the block's angles through shared memory.
 //
 // Measured on a GB300, replayed graphs, against the bytes at the rate of a plain copy: 4 x 3001-5003 tokens, 28 + 4 heads
-// of 128 dims, three axes: 52 us, 0.82 (with one unit of eight values per lane and trip instead of two: 56; the first form, a
-// lane's values loaded when they were needed: 73). 2 x 4097-8191 tokens, 16 + 4 heads of 256 dims of which 64 turn: 57 us,
-// 0.80. bf16 pages, 8 x 1025-4099 tokens: 96 us, 0.82; e4m3 pages, 8 x 2001-8192 tokens: 203 us, 0.71, with the queries' and
-// the blocks' CTAs in one launch (in one each: 218). One token: 2.9 us; one of each of 64 sequences with its write: 4.3.
+// of 128 dims, three axes: 50-52 us, 0.82-0.85 (with one unit of eight values per lane and trip instead of two: 56; the first form, a
+// lane's values loaded when they were needed: 73). 2 x 4097-8191 tokens, 16 + 4 heads of 256 dims of which 64 turn: 55-57 us,
+// 0.80-0.82. bf16 pages, 8 x 1025-4099 tokens: 96-97 us, 0.82; e4m3 pages, 8 x 2001-8192 tokens: 201-203 us, 0.71, with the
+// queries' and the blocks' CTAs in one launch (in one each: 218). Affine pages, the prompts of the bf16 ones: 191 us with heads of
+// 128 dims, 153 with half as many of 256, 0.36-0.48: rows go through the quantiser one after the other. One token: 2.9 us;
+// one of each of 64 sequences with its write: 4.3, and 7.8 with cold caches, into affine pages 12.3.
 #include <algorithm>
 #include <type_traits>
 
